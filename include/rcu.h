@@ -57,6 +57,8 @@ typedef struct rcu_rssm_s *rcu_rssm_t;
  * CuDNN API for LSTMs with projections", pytorch/pytorch issue 46213). */
 #define RCU_F32 0
 #define RCU_BF16 1
+/* 8-bit activation checkpoints (rcu_act8_pack), as a backward's saved input. */
+#define RCU_I8 2
 
 /* Status codes. */
 #define RCU_OK 0
@@ -66,6 +68,7 @@ typedef struct rcu_rssm_s *rcu_rssm_t;
 #define RCU_ERR_TIMEOUT (-4)     /* a device-side step barrier gave up waiting */
 #define RCU_ERR_LENGTHS (-5)     /* device found a length outside [1, T] */
 #define RCU_ERR_STATE (-6)       /* weights not set for every layer/direction */
+#define RCU_ERR_SLOTS (-7)       /* device found a state slot outside [-1, slots) */
 
 /* Attributes for rnn_set_attr / rssm_set_attr. */
 #define RCU_ATTR_BARRIER_TIMEOUT_NS 1 /* bound on any device wait (default 2e9 ns) */
@@ -532,6 +535,168 @@ RCU_API int rssm_profile_reset(rcu_rssm_t h);
 RCU_API int rssm_get_trace(rcu_rssm_t h, int64_t *host_out, int n_steps, void *stream);
 RCU_API int rssm_last_launch_count(rcu_rssm_t h);
 RCU_API int rssm_destroy(rcu_rssm_t h);
+
+/* ------------------------------------------------------------------------ */
+/* Sequence operators: gated linear recurrence, layer norm, 8-bit activation  */
+/* checkpoints                                                                */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * A handle holds what the calls below keep between launches: the device error
+ * word and a workspace for partial sums that grows on demand.  It owns no
+ * weights: parameters that an optimiser updates every step are passed to each
+ * call.  As with the other handles, one stream at a time uses it.
+ *
+ * Matrices are given by a pointer and a row stride ld in elements (>= the row
+ * width; rows are dense), so that a slice of a wider matrix, for example one
+ * gate of a fused projection's output, is passed as it is.  dtype is RCU_F32
+ * or RCU_BF16; sums, statistics and states are fp32 throughout.  Any alignment
+ * that the type itself has is taken; 16-byte aligned rows run fastest.
+ */
+typedef struct rcu_seq_s rcu_seq;
+
+RCU_API int rcu_seq_create(rcu_seq **out);
+RCU_API int rcu_seq_destroy(rcu_seq *h);
+
+/* Synchronise `stream` and return the device status of the calls so far
+ * (RCU_OK, RCU_ERR_LENGTHS, RCU_ERR_SLOTS), then clear it. */
+RCU_API int rcu_seq_get_status(rcu_seq *h, void *stream);
+
+/* RCU_ATTR_PROFILE as for the other handles; RCU_ATTR_FORCE_PATH: 0 =
+ * automatic, 1 = the kernels' plain loads where aligned rows would move by
+ * wider or asynchronous copies (rcu_linrec_forward/_backward: no TMA;
+ * layer norm and act8: no vector accesses). */
+RCU_API int rcu_seq_set_attr(rcu_seq *h, int attr, int64_t value);
+RCU_API int rcu_seq_profile_entry(rcu_seq *h, int i, const char **name, double *total_ms,
+                                  int64_t *count);
+RCU_API int rcu_seq_profile_reset(rcu_seq *h);
+
+/* Number of kernel launches the last call on `h` enqueued. */
+RCU_API int rcu_seq_last_launch_count(rcu_seq *h);
+
+/* Steps between the states rcu_linrec_forward keeps for the backward pass. */
+#define RCU_LINREC_CHUNK 64
+
+/* Row order of a [T, B, H] tensor: row t*B + b, or (batch first) b*T + t. */
+#define RCU_TIME_FIRST 0
+#define RCU_BATCH_FIRST 1
+
+/*
+ * Gated linear recurrence: an elementwise recurrent cell whose gates do not
+ * see the state, so that all steps can run in parallel over time.  Per channel
+ * with parameter lambda and a constant c > 0, for t < lengths[b]:
+ *   s = sigmoid(r_t), g = sigmoid(i_t)
+ *   a = exp(-c softplus(lambda) s)
+ *   h_t = a h_{t-1} + sqrt(1 - a^2) g x_t,   y_t = h_t
+ *   x, r, i  [T, B, H] in `layout`, of type dtype (r, i before the sigmoid).
+ *   lambda   [H] fp32.
+ *   lengths  NULL (all T) or device int32 [B], 0 <= lengths[b] <= T; a value
+ *            outside is clamped and reported by rcu_seq_get_status.  y is 0 at
+ *            t >= lengths[b]; the inputs there are not used.
+ *   h0       [B, H] fp32 or NULL (zeros).
+ *   y        [T, B, H] in `layout`, type dtype (rounded; the state is not).
+ *   h_n      [B, H] fp32 or NULL: the state after each row's last step (h0 for
+ *            a row of length 0).
+ *   states   [ceil(T / RCU_LINREC_CHUNK), B, H] fp32 or NULL: the state before
+ *            steps 0, 64, 128, ..., which rcu_linrec_backward needs (of a
+ *            chunk past a row's end: its last state).
+ * T or B may be 0.  Long sequences of few channels are split over time;
+ * results do not depend on anything but the inputs.
+ */
+RCU_API int rcu_linrec_forward(rcu_seq *h, int dtype, int layout, int T, int B, int H,
+                               const void *x, int64_t ldx, const void *r, int64_t ldr,
+                               const void *i, int64_t ldi, const float *lambda, double c,
+                               const int32_t *lengths, const float *h0, void *y, int64_t ldy,
+                               float *h_n, float *states, void *stream);
+
+/*
+ * Backward pass of rcu_linrec_forward.  Takes its inputs and its states, and
+ * the gradients of a loss with respect to y (dy) and h_n (dh_n, NULL = 0).
+ *   saved    the type of x, r, i: dtype, or RCU_I8: 8-bit checkpoints made by
+ *            rcu_act8_pack (x, r, i then hold int8 codes and xe, re, ie their
+ *            exponents [T*B, ceil(H / 64)], rows in `layout`; else NULL).  The
+ *            gradients are then those at the values the checkpoints stand
+ *            for, with the states of the exact forward.
+ *   dx, dr, di  [T, B, H] of type dtype, each may be NULL; 0 past a row's end.
+ *   dlambda  [H] fp32 or NULL: summed over steps and rows, in a fixed order.
+ *   dh0      [B, H] fp32 or NULL.
+ */
+RCU_API int rcu_linrec_backward(rcu_seq *h, int dtype, int saved, int layout, int T, int B, int H,
+                                const void *x, int64_t ldx, const void *r, int64_t ldr,
+                                const void *i, int64_t ldi, const int8_t *xe, const int8_t *re,
+                                const int8_t *ie, const float *lambda, double c,
+                                const int32_t *lengths, const float *states, const void *dy,
+                                int64_t lddy, const float *dh_n, void *dx, int64_t lddx,
+                                void *dr, int64_t lddr, void *di, int64_t lddi, float *dlambda,
+                                float *dh0, void *stream);
+
+/*
+ * One step of the recurrence for B requests, states updated in place:
+ *   x, r, i, y [B, H] of type dtype; state [slots, H] fp32.
+ *   slot  NULL (row b uses state row b; then slots >= B) or device int32 [B]:
+ *         the state row of request b, or -1 for a row that takes no part (its
+ *         y is 0).  The slots of rows that take part must differ.  A slot
+ *         outside [-1, slots) is treated as -1 and reported by
+ *         rcu_seq_get_status.
+ */
+RCU_API int rcu_linrec_step(rcu_seq *h, int dtype, int B, int H, const void *x, int64_t ldx,
+                            const void *r, int64_t ldr, const void *i, int64_t ldi,
+                            const float *lambda, double c, float *state, int slots,
+                            const int32_t *slot, void *y, int64_t ldy, void *stream);
+
+/*
+ * Layer norm over rows of n values, with the residual addition that stands
+ * before it in a stack of layers:
+ *   u = x, or x + residual rounded to dtype;
+ *   y = (u - mean) * rstd * weight + bias, mean over the row,
+ *   rstd = 1 / sqrt(mean((u - mean)^2) + eps).
+ *   x [rows, n], residual [rows, n] or NULL; weight, bias [n] fp32 or NULL (1, 0);
+ *   y [rows, n]; sum [rows, n] receives u (required with a residual, else
+ *   NULL); mean, rstd [rows] fp32, each may be NULL.  eps >= 0.
+ */
+RCU_API int rcu_layernorm_forward(rcu_seq *h, int dtype, int64_t rows, int n, const void *x,
+                                  int64_t ldx, const void *residual, int64_t ldres,
+                                  const float *weight, const float *bias, double eps, void *y,
+                                  int64_t ldy, void *sum, int64_t ldsum, float *mean, float *rstd,
+                                  void *stream);
+
+/*
+ * Backward pass of rcu_layernorm_forward with respect to u, weight and bias:
+ *   xhat = (u - mean) * rstd, q = dy * weight,
+ *   du = rstd * (q - mean(q) - xhat * mean(q * xhat)) + dsum,
+ *   dweight = sum over rows of dy * xhat, dbias = sum over rows of dy.
+ *   u [rows, n]: the normalised values' input (x, or the forward's sum), of
+ *   type `saved`: dtype, or RCU_I8 with its exponents ue [rows, ceil(n / 64)]
+ *   (else NULL); dsum [rows, n] or NULL: the gradient reaching u another way
+ *   (the residual stream); du [rows, n]; dweight, dbias [n] fp32, each may be
+ *   NULL, summed in a fixed order.
+ */
+RCU_API int rcu_layernorm_backward(rcu_seq *h, int dtype, int saved, int64_t rows, int n,
+                                   const void *dy, int64_t lddy, const void *u, int64_t ldu,
+                                   const int8_t *ue, const float *weight, const float *mean,
+                                   const float *rstd, const void *dsum, int64_t ldds, void *du,
+                                   int64_t lddu, float *dweight, float *dbias, void *stream);
+
+/* Values along a row that share an exponent in an 8-bit checkpoint. */
+#define RCU_ACT8_BLOCK 64
+
+/*
+ * 8-bit activation checkpoints: each row in blocks of 64 values (the last one
+ * shorter), a block held as int8 codes and one power of two: value = code *
+ * 2^exp with exp the smallest integer in [-126, 121] for which every |v| <=
+ * 127 * 2^exp, code = v / 2^exp rounded to the nearest even.  Scaling by a
+ * power of two is exact, so an error is at most half a step of the block,
+ * 2^(exp-1) (below 1/126 of the block's largest magnitude).  Magnitudes above
+ * 127 * 2^121, the last 1/128 of the range of fp32, are held as that value,
+ * the largest one that comes back finite.  A NaN or infinity is held
+ * as code -128 and comes back as NaN; it takes no part in the exponent.
+ *   x [rows, n] of type dtype; codes [rows, n] int8 (row stride ldc); exps
+ *   [rows, ceil(n / 64)] int8, dense.
+ */
+RCU_API int rcu_act8_pack(rcu_seq *h, int dtype, int64_t rows, int n, const void *x, int64_t ldx,
+                          int8_t *codes, int64_t ldc, int8_t *exps, void *stream);
+RCU_API int rcu_act8_unpack(rcu_seq *h, int dtype, int64_t rows, int n, const int8_t *codes,
+                            int64_t ldc, const int8_t *exps, void *y, int64_t ldy, void *stream);
 
 #ifdef __cplusplus
 }

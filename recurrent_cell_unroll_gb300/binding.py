@@ -23,14 +23,16 @@ import torch
 from . import _build
 
 RCU_LSTM, RCU_GRU, RCU_BIDIR = 0, 1, 0x100
-RCU_F32, RCU_BF16 = 0, 1
+RCU_F32, RCU_BF16, RCU_I8 = 0, 1, 2
 RCU_OK, RCU_ERR_INVALID, RCU_ERR_UNSUPPORTED, RCU_ERR_CUDA = 0, -1, -2, -3
-RCU_ERR_TIMEOUT, RCU_ERR_LENGTHS, RCU_ERR_STATE = -4, -5, -6
+RCU_ERR_TIMEOUT, RCU_ERR_LENGTHS, RCU_ERR_STATE, RCU_ERR_SLOTS = -4, -5, -6, -7
 RCU_ATTR_BARRIER_TIMEOUT_NS, RCU_ATTR_TEST_DROP_ARRIVAL, RCU_ATTR_FORCE_PATH = 1, 2, 3
 RCU_ATTR_PROFILE, RCU_ATTR_TRACE, RCU_ATTR_TC_KSPLIT = 4, 5, 7
 RCU_ATTR_LAYER_PIPELINE = 10
 RCU_CLIP_CELL, RCU_CLIP_PROJ = 0, 1
 RCU_ATTR_HOST_CHUNKS, RCU_MAX_HOST_CHUNKS = 8, 16
+RCU_TIME_FIRST, RCU_BATCH_FIRST = 0, 1
+RCU_LINREC_CHUNK, RCU_ACT8_BLOCK = 64, 64
 
 EXPORTED = (
     "rcu_last_error", "rcu_version", "rnn_create", "rnn_set_weights", "rnn_forward",
@@ -43,6 +45,10 @@ EXPORTED = (
     "rssm_unroll_actor_host", "rnn_backward", "rnn_get_weight_grads", "rssm_backward",
     "rssm_get_weight_grads", "rssm_profile_entry", "rssm_profile_reset", "rssm_backward_actor",
     "rssm_get_actor_grads", "rnn_host_plan",
+    "rcu_seq_create", "rcu_seq_destroy", "rcu_seq_get_status", "rcu_seq_set_attr",
+    "rcu_seq_profile_entry", "rcu_seq_profile_reset", "rcu_seq_last_launch_count",
+    "rcu_linrec_forward", "rcu_linrec_backward", "rcu_linrec_step", "rcu_layernorm_forward",
+    "rcu_layernorm_backward", "rcu_act8_pack", "rcu_act8_unpack",
 )
 
 _lib = None
@@ -61,7 +67,7 @@ def lib_path() -> str:
 
 def signatures() -> dict:
     """ctypes (restype, argtypes) of every entry point of include/rcu.h."""
-    P, I, I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+    P, I, I64, D = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_double
     return {
         "rcu_last_error": (ctypes.c_char_p, []),
         "rcu_version": (ctypes.c_char_p, []),
@@ -102,6 +108,25 @@ def signatures() -> dict:
         "rssm_profile_entry": (I, [P, I, ctypes.POINTER(ctypes.c_char_p),
                                    ctypes.POINTER(ctypes.c_double), ctypes.POINTER(I64)]),
         "rssm_profile_reset": (I, [P]),
+        "rcu_seq_create": (I, [ctypes.POINTER(P)]),
+        "rcu_seq_destroy": (I, [P]),
+        "rcu_seq_get_status": (I, [P, P]),
+        "rcu_seq_set_attr": (I, [P, I, I64]),
+        "rcu_seq_profile_entry": (I, [P, I, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(D),
+                                      ctypes.POINTER(I64)]),
+        "rcu_seq_profile_reset": (I, [P]),
+        "rcu_seq_last_launch_count": (I, [P]),
+        "rcu_linrec_forward": (I, [P, I, I, I, I, I] + [P, I64] * 3 + [P, D, P, P, P, I64, P, P,
+                                                                       P]),
+        "rcu_linrec_backward": (I, [P, I, I, I, I, I, I] + [P, I64] * 3 + [P, P, P, P, D, P, P]
+                                + [P, I64, P] + [P, I64] * 3 + [P, P, P]),
+        "rcu_linrec_step": (I, [P, I, I, I] + [P, I64] * 3 + [P, D, P, I, P, P, I64, P]),
+        "rcu_layernorm_forward": (I, [P, I, I64, I, P, I64, P, I64, P, P, D, P, I64, P, I64, P, P,
+                                      P]),
+        "rcu_layernorm_backward": (I, [P, I, I, I64, I, P, I64, P, I64, P, P, P, P, P, I64, P, I64,
+                                       P, P, P]),
+        "rcu_act8_pack": (I, [P, I, I64, I, P, I64, P, I64, P, P]),
+        "rcu_act8_unpack": (I, [P, I, I64, I, P, I64, P, P, I64, P]),
     }
 
 
@@ -655,6 +680,300 @@ class RSSM:
     def close(self):
         if self.h:
             rssm_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SeqOps:
+    """The sequence operators (gated linear recurrence, layer norm, 8-bit
+    activation checkpoints; see rcu.h) on torch tensors of the device that was
+    current when it was made.
+
+    Matrices are float32 or bfloat16.  A tensor whose rows are dense and evenly
+    spaced (a slice of a wider tensor's last dimension) is used in place, one
+    of any other layout as a contiguous copy.  Parameters, states and
+    statistics are float32.  With ``stream`` the outputs are allocated for
+    that stream, and work on it follows what it held before: a caller that
+    made an input on another stream orders the two.
+    """
+
+    _DTYPES = {torch.float32: RCU_F32, torch.bfloat16: RCU_BF16}
+
+    def __init__(self):
+        self.h = None
+        h = ctypes.c_void_p()
+        self.lib = load()
+        self.device = torch.cuda.current_device()
+        _check(self.lib.rcu_seq_create(ctypes.byref(h)))
+        self.h = h
+
+    # ---- arguments
+
+    def _on(self, t, name):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a tensor on a CUDA device")
+        if t.get_device() != self.device:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the handle on "
+                             f"cuda:{self.device}")
+
+    def _data(self, t, name):
+        """The RCU_* type of a matrix operand."""
+        self._on(t, name)
+        dtype = self._DTYPES.get(t.dtype)
+        if dtype is None:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        return dtype
+
+    def _rows(self, t, name, dtype, shape):
+        """A matrix operand as (kept tensor, pointer, row stride)."""
+        self._on(t, name)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.is_contiguous():
+            return t, t.data_ptr(), shape[-1]
+        st = t.stride()
+        if len(st) > 1 and st[-1] == 1 and st[-2] >= shape[-1] and all(
+                st[k] == st[k + 1] * shape[k + 1] for k in range(len(st) - 2)):
+            return t, t.data_ptr(), st[-2]
+        t = t.clone(memory_format=torch.contiguous_format)
+        return t, t.data_ptr(), shape[-1]
+
+    def _dense(self, t, name, shape, dtype=torch.float32):
+        """A dense operand as (kept tensor, pointer); None stays NULL."""
+        if t is None:
+            return None, None
+        self._on(t, name)
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if not t.is_contiguous():
+            t = t.clone(memory_format=torch.contiguous_format)
+        return t, t.data_ptr()
+
+    def _saved(self, t, name, dtype, shape):
+        """A backward's saved input, a tensor or an 8-bit checkpoint: (kept,
+        pointer, row stride, exponents' pointer)."""
+        if isinstance(t, torch.Tensor):
+            return (*self._rows(t, name, dtype, shape), None)
+        codes, exps = t
+        c = self._rows(codes, name + "'s codes", torch.int8, shape)
+        e = self._dense(exps, name + "'s exponents", (*shape[:-1], -(-shape[-1] // RCU_ACT8_BLOCK)),
+                        torch.int8)
+        return (c[0], e[0]), c[1], c[2], e[1]
+
+    def _run(self, stream, call):
+        """call(raw stream) with `stream` (None: the current one) as the
+        current stream, so that its allocations belong to it."""
+        if stream is None:
+            return call(torch._C._cuda_getCurrentRawStream(self.device))
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+    @staticmethod
+    def _tbh(shape, batch_first):
+        if len(shape) != 3:
+            raise ValueError(f"x must have three dimensions, got {list(shape)}")
+        return (shape[1], shape[0], shape[2]) if batch_first else tuple(shape)
+
+    # ---- gated linear recurrence
+
+    def linrec_forward(self, x, r, i, lam, c=8.0, lengths=None, h0=None, batch_first=False,
+                       states=False, stream=None):
+        """y, h_n and, with states=True, what linrec_backward needs (else
+        None).  x, r, i: [T, B, H] (batch_first: [B, T, H]); lam [H]; lengths
+        int32 [B]; h0 [B, H]."""
+        dt = self._data(x, "x")
+        T, B, H = self._tbh(x.shape, batch_first)
+
+        def call(s):
+            xs, rs, is_ = (self._rows(t, k, x.dtype, x.shape)
+                           for k, t in (("x", x), ("r", r), ("i", i)))
+            lm = self._dense(lam, "lam", (H,))
+            ln = self._dense(lengths, "lengths", (B,), torch.int32)
+            hs = self._dense(h0, "h0", (B, H))
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            h_n = torch.empty((B, H), device=x.device)
+            st = torch.empty((-(-T // RCU_LINREC_CHUNK), B, H), device=x.device) if states else None
+            _check(self.lib.rcu_linrec_forward(
+                self.h, dt, RCU_BATCH_FIRST if batch_first else RCU_TIME_FIRST, T, B, H, xs[1],
+                xs[2], rs[1], rs[2], is_[1], is_[2], lm[1], c, ln[1], hs[1], y.data_ptr(), H,
+                h_n.data_ptr(), st.data_ptr() if states else None, s))
+            return y, h_n, st
+        return self._run(stream, call)
+
+    def linrec_backward(self, dy, x, r, i, lam, states, c=8.0, lengths=None, dh_n=None,
+                        batch_first=False, stream=None):
+        """dx, dr, di (of dy's type), dlam [H] and dh0 [B, H].  x, r, i: the
+        forward's inputs, or all three as act8_pack's (codes, exponents)."""
+        dt = self._data(dy, "dy")
+        T, B, H = self._tbh(dy.shape, batch_first)
+        q8 = not isinstance(x, torch.Tensor)
+        if any(isinstance(t, torch.Tensor) == q8 for t in (r, i)):
+            raise ValueError("x, r, i are all tensors or all 8-bit checkpoints")
+
+        def call(s):
+            xs, rs, is_ = (self._saved(t, k, dy.dtype, dy.shape)
+                           for k, t in (("x", x), ("r", r), ("i", i)))
+            dys = self._rows(dy, "dy", dy.dtype, dy.shape)
+            lm = self._dense(lam, "lam", (H,))
+            ln = self._dense(lengths, "lengths", (B,), torch.int32)
+            st = self._dense(states, "states", (-(-T // RCU_LINREC_CHUNK), B, H))
+            hs = self._dense(dh_n, "dh_n", (B, H))
+            dx, dr, di = (torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+                          for _ in range(3))
+            dlam = torch.empty((H,), device=dy.device)
+            dh0 = torch.empty((B, H), device=dy.device)
+            _check(self.lib.rcu_linrec_backward(
+                self.h, dt, RCU_I8 if q8 else dt,
+                RCU_BATCH_FIRST if batch_first else RCU_TIME_FIRST, T, B, H, xs[1], xs[2], rs[1],
+                rs[2], is_[1], is_[2], xs[3], rs[3], is_[3], lm[1], c, ln[1], st[1], dys[1],
+                dys[2], hs[1], dx.data_ptr(), H, dr.data_ptr(), H, di.data_ptr(), H,
+                dlam.data_ptr(), dh0.data_ptr(), s))
+            return dx, dr, di, dlam, dh0
+        return self._run(stream, call)
+
+    def linrec_step(self, x, r, i, lam, state, c=8.0, slot=None, stream=None):
+        """y [B, H] of one step of B requests; state [slots, H] is updated in
+        place, at slot[b] (int32 [B], -1: takes no part; None: row b)."""
+        dt = self._data(x, "x")
+        if x.dim() != 2:
+            raise ValueError(f"x must have two dimensions, got {list(x.shape)}")
+        B, H = x.shape
+        if not state.is_contiguous() or state.dim() != 2:
+            raise ValueError("state must be a contiguous [slots, H] tensor")
+
+        def call(s):
+            xs, rs, is_ = (self._rows(t, k, x.dtype, x.shape)
+                           for k, t in (("x", x), ("r", r), ("i", i)))
+            lm = self._dense(lam, "lam", (H,))
+            st = self._dense(state, "state", (state.shape[0], H))
+            sl = self._dense(slot, "slot", (B,), torch.int32)
+            y = torch.empty((B, H), dtype=x.dtype, device=x.device)
+            _check(self.lib.rcu_linrec_step(self.h, dt, B, H, xs[1], xs[2], rs[1], rs[2], is_[1],
+                                            is_[2], lm[1], c, st[1], state.shape[0], sl[1],
+                                            y.data_ptr(), H, s))
+            return y
+        return self._run(stream, call)
+
+    # ---- layer norm
+
+    def layernorm_forward(self, x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
+        """(y, mean, rstd) of x [..., n]; with a residual (y, sum, mean, rstd),
+        sum = x + residual being what is normalised."""
+        dt = self._data(x, "x")
+        n = x.shape[-1]
+        rows = x.numel() // n if n else 0
+
+        def call(s):
+            xs = self._rows(x, "x", x.dtype, x.shape)
+            rs = self._rows(residual, "residual", x.dtype, x.shape) if residual is not None \
+                else (None, None, 0)
+            w, b = self._dense(weight, "weight", (n,)), self._dense(bias, "bias", (n,))
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            u = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None \
+                else None
+            mean = torch.empty(x.shape[:-1], device=x.device)
+            rstd = torch.empty(x.shape[:-1], device=x.device)
+            _check(self.lib.rcu_layernorm_forward(
+                self.h, dt, rows, n, xs[1], xs[2], rs[1], rs[2], w[1], b[1], eps, y.data_ptr(), n,
+                None if u is None else u.data_ptr(), n, mean.data_ptr(), rstd.data_ptr(), s))
+            return (y, mean, rstd) if u is None else (y, u, mean, rstd)
+        return self._run(stream, call)
+
+    def layernorm_backward(self, dy, u, mean, rstd, weight=None, dsum=None, stream=None):
+        """(du, dweight, dbias).  u: what the forward normalised (x, or its
+        sum), or act8_pack's (codes, exponents) of it; dsum: the gradient that
+        reaches u another way."""
+        dt = self._data(dy, "dy")
+        n = dy.shape[-1]
+        rows = dy.numel() // n if n else 0
+
+        def call(s):
+            us = self._saved(u, "u", dy.dtype, dy.shape)
+            dys = self._rows(dy, "dy", dy.dtype, dy.shape)
+            ds = self._rows(dsum, "dsum", dy.dtype, dy.shape) if dsum is not None \
+                else (None, None, 0)
+            w = self._dense(weight, "weight", (n,))
+            m = self._dense(mean, "mean", dy.shape[:-1])
+            rs = self._dense(rstd, "rstd", dy.shape[:-1])
+            du = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
+            dw, db = (torch.empty((n,), device=dy.device) for _ in range(2))
+            _check(self.lib.rcu_layernorm_backward(
+                self.h, dt, dt if us[3] is None else RCU_I8, rows, n, dys[1], dys[2], us[1], us[2],
+                us[3], w[1], m[1], rs[1], ds[1], ds[2], du.data_ptr(), n, dw.data_ptr(),
+                db.data_ptr(), s))
+            return du, dw, db
+        return self._run(stream, call)
+
+    # ---- 8-bit activation checkpoints
+
+    def act8_pack(self, x, stream=None):
+        """(codes int8 [..., n], exponents int8 [..., ceil(n / 64)]) of x."""
+        dt = self._data(x, "x")
+        n = x.shape[-1]
+        rows = x.numel() // n if n else 0
+
+        def call(s):
+            xs = self._rows(x, "x", x.dtype, x.shape)
+            codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+            exps = torch.empty((*x.shape[:-1], -(-n // RCU_ACT8_BLOCK)), dtype=torch.int8,
+                               device=x.device)
+            _check(self.lib.rcu_act8_pack(self.h, dt, rows, n, xs[1], xs[2], codes.data_ptr(), n,
+                                          exps.data_ptr(), s))
+            return codes, exps
+        return self._run(stream, call)
+
+    def act8_unpack(self, codes, exps, dtype=torch.float32, stream=None):
+        """The values an 8-bit checkpoint stands for."""
+        dt = self._DTYPES.get(dtype)
+        if dt is None:
+            raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+        n = codes.shape[-1]
+        rows = codes.numel() // n if n else 0
+
+        def call(s):
+            cs = self._saved((codes, exps), "x", None, codes.shape)
+            y = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+            _check(self.lib.rcu_act8_unpack(self.h, dt, rows, n, cs[1], cs[2], cs[3],
+                                            y.data_ptr(), n, s))
+            return y
+        return self._run(stream, call)
+
+    # ---- handle
+
+    def status(self, stream=None) -> int:
+        """Synchronise and return the device status code (0 = ok); does not raise."""
+        return self.lib.rcu_seq_get_status(self.h, _stream(stream))
+
+    def set_attr(self, attr, value):
+        _check(self.lib.rcu_seq_set_attr(self.h, attr, value))
+
+    def launch_count(self) -> int:
+        return self.lib.rcu_seq_last_launch_count(self.h)
+
+    def profile(self) -> dict:
+        """{call: (total_ms, calls)} recorded while RCU_ATTR_PROFILE is on."""
+        out, i = {}, 0
+        name, ms, n = ctypes.c_char_p(), ctypes.c_double(), ctypes.c_int64()
+        while self.lib.rcu_seq_profile_entry(self.h, i, ctypes.byref(name), ctypes.byref(ms),
+                                             ctypes.byref(n)) == RCU_OK:
+            out[name.value.decode()] = (ms.value, n.value)
+            i += 1
+        return out
+
+    def close(self):
+        if self.h:
+            self.lib.rcu_seq_destroy(self.h)
             self.h = None
 
     def __del__(self):

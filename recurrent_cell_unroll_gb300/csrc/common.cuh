@@ -13,7 +13,10 @@ namespace rcu {
 // before touching any peer's shared memory.
 // DEV_BOUNDS: a device bounds check of the RCU_DEBUG build failed (the
 // access was skipped).
-enum DevErr : int { DEV_OK = 0, DEV_TIMEOUT = 1, DEV_LENGTHS = 2, DEV_CONFIG = 3, DEV_BOUNDS = 4 };
+// DEV_SLOTS: a request named a state row outside the table (it was left out).
+enum DevErr : int {
+  DEV_OK = 0, DEV_TIMEOUT = 1, DEV_LENGTHS = 2, DEV_CONFIG = 3, DEV_BOUNDS = 4, DEV_SLOTS = 5
+};
 
 // Device bounds checks, compiled only into the debug build of the library
 // (-DRCU_DEBUG: recurrent_cell_unroll_gb300._build.build(debug=True)), the

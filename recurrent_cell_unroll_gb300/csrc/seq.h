@@ -1,0 +1,100 @@
+// Launchers of the sequence operators (gated linear recurrence, layer norm,
+// 8-bit activation checkpoints), shared by their kernel files and api_seq.cu.
+// Arguments have been checked: dtype is RCU_F32 or RCU_BF16, sizes are >= 1,
+// row strides >= the row width.  `vec` false forbids the wide and asynchronous
+// accesses that aligned rows otherwise use.  *launches counts kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace rcu {
+
+// A [T, B, H] tensor: element (t, b, h) at p + t*st + b*sb + h (elements).
+struct SeqIn {
+  const void *p;
+  int64_t st, sb;
+  const int8_t *e;  // 8-bit checkpoint: exponents [rows][ceil(H/64)]; else NULL
+};
+struct SeqOut {
+  void *p;
+  int64_t st, sb;
+};
+
+struct LinrecFwd {
+  int dtype, T, B, H;
+  SeqIn x, r, i;
+  const float *lambda;
+  float c;
+  const int32_t *lengths;
+  const float *h0;
+  SeqOut y;
+  float *h_n, *states;
+};
+
+struct LinrecBwd {
+  int dtype, saved, T, B, H;
+  SeqIn x, r, i;
+  int64_t et, eb;  // rows of the exponents: row (t, b) = t*et + b*eb
+  const float *lambda;
+  float c;
+  const int32_t *lengths;
+  const float *states;
+  SeqIn dy;
+  const float *dh_n;
+  SeqOut dx, dr, di;
+  float *dlambda, *dh0;
+};
+
+// Device memory the call may use: bytes needed, then the launch with it.
+size_t linrec_fwd_workspace(const LinrecFwd &p, int nsm);
+cudaError_t launch_linrec_fwd(const LinrecFwd &p, void *ws, int *err, int nsm, bool vec,
+                              cudaStream_t s, int *launches);
+size_t linrec_bwd_workspace(const LinrecBwd &p, int nsm);
+cudaError_t launch_linrec_bwd(const LinrecBwd &p, void *ws, int *err, int nsm, bool vec,
+                              cudaStream_t s, int *launches);
+cudaError_t launch_linrec_step(int dtype, int B, int H, const void *x, int64_t ldx, const void *r,
+                               int64_t ldr, const void *i, int64_t ldi, const float *lambda,
+                               float c, float *state, int slots, const int32_t *slot, void *y,
+                               int64_t ldy, int *err, bool vec, cudaStream_t s, int *launches);
+
+struct LnFwd {
+  int dtype;
+  int64_t rows;
+  int n;
+  const void *x, *res;
+  int64_t ldx, ldres;
+  const float *weight, *bias;
+  float eps;
+  void *y, *sum;
+  int64_t ldy, ldsum;
+  float *mean, *rstd;
+};
+struct LnBwd {
+  int dtype, saved;
+  int64_t rows;
+  int n;
+  const void *dy, *u;
+  int64_t lddy, ldu;
+  const int8_t *ue;
+  const float *weight, *mean, *rstd;
+  const void *dsum;
+  int64_t ldds;
+  void *du;
+  int64_t lddu;
+  float *dweight, *dbias;
+};
+cudaError_t launch_ln_fwd(const LnFwd &p, int nsm, bool vec, cudaStream_t s, int *launches);
+size_t ln_bwd_workspace(const LnBwd &p, int nsm);
+cudaError_t launch_ln_bwd(const LnBwd &p, void *ws, int nsm, bool vec, cudaStream_t s,
+                          int *launches);
+
+cudaError_t launch_act8_pack(int dtype, int64_t rows, int n, const void *x, int64_t ldx,
+                             int8_t *codes, int64_t ldc, int8_t *exps, int nsm, bool vec,
+                             cudaStream_t s, int *launches);
+cudaError_t launch_act8_unpack(int dtype, int64_t rows, int n, const int8_t *codes, int64_t ldc,
+                               const int8_t *exps, void *y, int64_t ldy, int nsm, bool vec,
+                               cudaStream_t s, int *launches);
+
+}  // namespace rcu
