@@ -787,6 +787,24 @@ bool tc_map_2d(CUtensorMap *map, const void *base, long long rows, int cols, int
   return make_map(map, base, rows, cols, ld, box_rows);
 }
 
+bool tc_map_3d(CUtensorMap *map, const void *base, int bytes, long long nx, long long ny,
+               long long nz, long long sy, long long sz, int bx, int by, int bz) {
+  auto fn = encode_fn();
+  if (!fn || reinterpret_cast<uintptr_t>(base) % 16 || sy * bytes % 16 || sz * bytes % 16)
+    return false;
+  const CUtensorMapDataType type = bytes == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  cuuint64_t dims[3] = {(cuuint64_t)nx, (cuuint64_t)ny, (cuuint64_t)nz};
+  cuuint64_t strides[2] = {(cuuint64_t)sy * bytes, (cuuint64_t)sz * bytes};
+  cuuint32_t box[3] = {(cuuint32_t)bx, (cuuint32_t)by, (cuuint32_t)bz};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, type, 3, const_cast<void *>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int tc_rec_units() { return UNITS; }
 
 bool tc_rec_packable(int cell, int H, int Hout, int P) {

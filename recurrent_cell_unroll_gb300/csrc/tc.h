@@ -78,6 +78,11 @@ cudaError_t launch_tc_recurrent(const TcRecParams &p, int nsm, cudaStream_t s);
 // declares its own cluster shape of `cs` CTAs (false, nothing launched, when
 // that cluster grid cannot be resident at once).
 bool tc_map_2d(CUtensorMap *map, const void *base, long long rows, int cols, int ld, int box_rows);
+// A tensor of nz x ny x nx elements of 1, 2 or 4 bytes (rows dense; sy, sz:
+// elements from one y, z to the next) in boxes of bz x by x bx, not swizzled;
+// false where its base or a stride is not a multiple of 16 bytes.
+bool tc_map_3d(CUtensorMap *map, const void *base, int bytes, long long nx, long long ny,
+               long long nz, long long sy, long long sz, int bx, int by, int bz);
 bool tc_launch_clustered(const void *fn, int grid, int nthreads, int cs, size_t smem, void **args,
                          cudaStream_t s, cudaError_t *err);
 
