@@ -1,0 +1,449 @@
+// Gated linear recurrence, backward: the gradients of x, r, i, lambda and h0.
+//
+// The gradient that reaches a state follows the same recurrence backwards in
+// time, e_t = dy_t + a_{t+1} e_{t+1}, so the tiles run from the last to the
+// first and each warp publishes two maps of its steps: h -> P h + E forwards
+// and c -> P c + R backwards (c = a e; the factor is the same).  The state
+// that enters a tile comes from the forward's states, so only the backward
+// carry crosses tiles.  Per element: four values read and three written, once;
+// em1, b and both sigmoids stay in registers between the two runs.
+#include "linrec_tile.cuh"
+
+namespace rcu {
+namespace {
+
+using namespace linrec;
+
+constexpr int S = CHUNK / NW, STEPS = CHUNK, STAGES = 3, PER_SM = 2;
+
+template <typename V>
+struct Smem {
+  typename Slot<V>::type part[2][NW][32];     // the warps' P and R, by parity of the tile
+  V fwd[2][NW][32];                           // and their E
+  typename Slot<V>::type peer[2][MAXCS][32];  // the blocks' P and R, by parity of the round
+  V sum[NW][32];                              // the warps' shares of dlambda
+  uint64_t full[STAGES];
+  int abort;
+};
+
+// Bytes of a tile of the saved inputs (IT) and of dy.
+template <typename IT, typename T>
+constexpr int in_bytes() { return STEPS * Shape<T>::CW * (int)sizeof(IT); }
+template <typename IT, typename T>
+constexpr int stage_bytes() { return 3 * in_bytes<IT, T>() + STEPS * 128; }
+
+// A lane's saved values of one step (CPT channels), raw, from shared or global memory
+template <typename IT, int CPT>
+__device__ __forceinline__ uint32_t raw_smem(const uint8_t *at, int lane) {
+  constexpr int N = CPT * (int)sizeof(IT);
+  at += lane * N;
+  if (N == 4) return *reinterpret_cast<const uint32_t *>(at);
+  if (N == 2) return *reinterpret_cast<const unsigned short *>(at);
+  return *at;
+}
+template <typename IT, int CPT>
+struct Global {
+  __device__ __forceinline__ static uint32_t load(const IT *p, int live, bool word) {
+    return load_raw(p, live, word);
+  }
+};
+template <int CPT>
+struct Global<int8_t, CPT> {
+  __device__ __forceinline__ static uint32_t load(const int8_t *p, int live, bool) {
+    const uint8_t *q = reinterpret_cast<const uint8_t *>(p);
+    uint32_t v = live > 0 ? __ldg(q) : 0u;
+    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 8;
+    return v;
+  }
+};
+
+// 8-bit codes: c + 128 in the low bits of 2^23 is exact in fp32; code -128 is NaN
+__device__ __forceinline__ float code_value(uint32_t biased, float scale) {
+  const float v = __uint_as_float(0x4b000000u | biased) - 8388736.f;
+  return v == -128.f ? __int_as_float(0x7fc00000) : v * scale;
+}
+template <typename IT, typename V>
+struct Decode;
+template <>
+struct Decode<bf16, F2> {
+  __device__ __forceinline__ static F2 logit(uint32_t v, float) { return bf16_pair(logit_floor(v)); }
+  __device__ __forceinline__ static F2 value(uint32_t v, float) { return bf16_pair(v); }
+};
+template <>
+struct Decode<int8_t, F2> {
+  __device__ __forceinline__ static F2 value(uint32_t v, float scale) {
+    v ^= 0x8080u;
+    return f2(code_value(v & 0xffu, scale), code_value(v >> 8, scale));
+  }
+  __device__ __forceinline__ static F2 logit(uint32_t v, float scale) {
+    const F2 f = value(v, scale);
+    return f2(logit_floor(lo(f)), logit_floor(hi(f)));
+  }
+};
+template <>
+struct Decode<float, float> {
+  __device__ __forceinline__ static float logit(uint32_t v, float) {
+    return logit_floor(__uint_as_float(v));
+  }
+  __device__ __forceinline__ static float value(uint32_t v, float) { return __uint_as_float(v); }
+};
+template <>
+struct Decode<int8_t, float> {
+  __device__ __forceinline__ static float value(uint32_t v, float scale) {
+    return code_value(v ^ 0x80u, scale);
+  }
+  __device__ __forceinline__ static float logit(uint32_t v, float scale) {
+    return logit_floor(value(v, scale));
+  }
+};
+
+// One step's gates: em1 = a - 1, nb = -beta g x, ns = -sigmoid(r), ng = -sigmoid(i).
+__device__ __forceinline__ void gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &nb, F2 &ns, F2 &ng) {
+  const Sig v = sigmoids(r, i);
+  ns = v.ns, ng = v.ng;
+  em1 = ex2m1(mul2(k2, ns));
+  const F2 w = one_minus_a2(em1);
+  nb = mul2(mul2(w, inv_beta(w)), mul2(ng, x));
+}
+template <typename IT>
+__device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (&scale)[3][S], F2 k2,
+                                      F2 (&em1)[S], F2 (&nb)[S], F2 (&ns)[S], F2 (&ng)[S]) {
+  typedef Decode<IT, F2> D;
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    gate(D::value(raw[0][s], scale[0][s]), D::logit(raw[1][s], scale[1][s]),
+         D::logit(raw[2][s], scale[2][s]), k2, em1[s], nb[s], ns[s], ng[s]);
+}
+// fp32 has one channel a lane: there the arithmetic pairs two steps
+template <typename IT>
+__device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (&scale)[3][S],
+                                      float k2, float (&em1)[S], float (&nb)[S], float (&ns)[S],
+                                      float (&ng)[S]) {
+  typedef Decode<IT, float> D;
+#pragma unroll
+  for (int s = 0; s < S; s += 2) {
+    F2 v[4];
+    gate(f2(D::value(raw[0][s], scale[0][s]), D::value(raw[0][s + 1], scale[0][s + 1])),
+         f2(D::logit(raw[1][s], scale[1][s]), D::logit(raw[1][s + 1], scale[1][s + 1])),
+         f2(D::logit(raw[2][s], scale[2][s]), D::logit(raw[2][s + 1], scale[2][s + 1])), f2(k2),
+         v[0], v[1], v[2], v[3]);
+    em1[s] = lo(v[0]), nb[s] = lo(v[1]), ns[s] = lo(v[2]), ng[s] = lo(v[3]);
+    em1[s + 1] = hi(v[0]), nb[s + 1] = hi(v[1]), ns[s + 1] = hi(v[2]), ng[s + 1] = hi(v[3]);
+  }
+}
+
+// Local gradients of one step from ne = -dL/dh_t and the state before it, which
+// moves on by one step:
+//   dx = e beta g,  di = e b (1 - g),  dlog_s = dL/dlog(a) s = e s (a h - a^2 b / w),
+//   dr = -K dlog_s (1 - s)
+template <typename V>
+__device__ __forceinline__ void grads(V em1, V nb, V ns, V ng, V nk, V ne, V &h, V &dx, V &dr, V &di,
+                                      V &dlog_s) {
+  V one, minus;
+  set(one, 1.f);
+  set(minus, -1.f);
+  const V w = one_minus_a2(em1), rb = inv_beta(w), arb = mul_v(add_v(em1, one), rb);
+  const V ah = fma_v(em1, h, h);
+  dx = mul_v(ne, mul_v(mul_v(w, rb), ng));
+  di = mul_v(mul_v(ne, nb), add_v(ng, one));
+  dlog_s = mul_v(mul_v(ne, ns), fma_v(mul_v(arb, arb), nb, ah));
+  dr = mul_v(mul_v(nk, dlog_s), add_v(ns, one));
+  h = fma_v(nb, minus, ah);
+}
+
+template <typename IT, typename T, bool TMA>
+__global__ void __launch_bounds__(NT, PER_SM)
+    linrec_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
+                      const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap mdy,
+                      const LinrecBwd p, const Cut cut, float *__restrict__ partial, const int words,
+                      int *err) {
+  constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
+  constexpr int IN = in_bytes<IT, T>(), STAGE = stage_bytes<IT, T>();
+  constexpr bool Q8 = sizeof(IT) == 1;
+  typedef typename Lane<T>::V V;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t *ring = smem;
+  Smem<V> &sh = *reinterpret_cast<Smem<V> *>(smem + (TMA ? STAGES * STAGE : 0));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int cs = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
+  const int stride = gridDim.x / cs, u0 = blockIdx.x / cs;
+
+  // the next tile to copy: live tiles of this block, the last steps first
+  int pu = u0, pk = 0, issued = 0;
+  auto issue = [&] {  // thread 0
+    for (; pu < cut.units; pu += stride, pk = 0) {
+      const Unit v = unit_of(cut, p.B, pu, CW);
+      const int len = row_length(p.lengths, v.b, p.T, err);
+      int tile;
+      do tile = v.last - 1 - (pk++ * cs + rank);
+      while (tile >= v.first && tile * STEPS >= len);
+      if (tile < v.first) continue;
+      const int st = issued++ % STAGES;
+      uint8_t *dst = ring + st * STAGE;
+      tc::mbar_arrive_expect_tx(&sh.full[st], STAGE);
+      tma_load_3d(dst, &mx, &sh.full[st], v.c0, v.b, tile * STEPS);
+      tma_load_3d(dst + IN, &mr, &sh.full[st], v.c0, v.b, tile * STEPS);
+      tma_load_3d(dst + 2 * IN, &mi, &sh.full[st], v.c0, v.b, tile * STEPS);
+      tma_load_3d(dst + 3 * IN, &mdy, &sh.full[st], v.c0, v.b, tile * STEPS);
+      return;
+    }
+  };
+  if (TMA) {
+    if (threadIdx.x == 0) {
+      for (int st = 0; st < STAGES; ++st) tc::mbar_init(&sh.full[st], 1);
+      sh.abort = 0;
+      tc::fence_mbar_init();
+      for (int st = 0; st < STAGES; ++st) issue();
+    }
+    __syncthreads();
+  }
+  if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
+
+  int used = 0, parity = 0, round = 0;
+  for (int u = u0; u < cut.units; u += stride) {
+    const Unit v = unit_of(cut, p.B, u, CW);
+    const int len = row_length(p.lengths, v.b, p.T, err);
+    const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
+    const int64_t row = (int64_t)v.b * p.H + ch;
+    V k2, nk, nc, sum, zero, minus;
+    set(zero, 0.f);
+    set(minus, -1.f);
+    load_v(p.lambda + ch, live, k2);
+    k2 = decay_rate2(k2, p.c);
+    set(nk, -1.f / LOG2E);
+    nk = mul_v(nk, k2);  // -K
+    if (p.dh_n) load_v(p.dh_n + row, live, nc);
+    else nc = zero;
+    nc = mul_v(nc, minus);  // the carry, negated: -dL/dh after the steps so far
+    sum = zero;
+    for (int base = v.last - 1; base >= v.first; base -= cs) {
+      const int tile = base - rank, tw = tile * STEPS + warp * S;
+      const bool on = tile >= v.first && tile * STEPS < len;  // the same for the whole block
+      V em1[S], nb[S], ns[S], ng[S], dy[S], h = zero, fe = zero;
+      Aff<V> mine = identity<V>();
+      if (on) {
+        load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
+        float scale[3][S];
+        if (Q8) {  // lane 8 k + s has the exponent of tensor k at step s
+          const int k = lane / S, t = tw + lane % S;
+          const int8_t *e = k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e;
+          int ex = 0;
+          if (k < 3 && t < len)
+            ex = __ldg(e + (t * p.et + v.b * p.eb) * ceil_div(p.H, BLOCK8) + v.c0 / BLOCK8);
+          const float f = __int_as_float((ex + 127) << 23);
+#pragma unroll
+          for (int k2i = 0; k2i < 3; ++k2i)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+              scale[k2i][s] = __shfl_sync(0xffffffffu, f, k2i * S + s);
+        }
+        uint32_t raw[3][S], rawd[S];
+        if (TMA) {
+          const int st = used % STAGES;
+          tc::mbar_wait(&sh.full[st], (used / STAGES) & 1, err, &sh.abort, WAIT_NS);
+          ++used;
+          const uint8_t *src = ring + st * STAGE;
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+              raw[k][s] = raw_smem<IT, CPT>(src + k * IN + (warp * S + s) * (IN / STEPS), lane);
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+            rawd[s] = raw_smem<T, CPT>(src + 3 * IN + (warp * S + s) * 128, lane);
+        } else {
+          const SeqIn *src[3] = {&p.x, &p.r, &p.i};
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const IT *q = static_cast<const IT *>(src[k]->p) + tw * src[k]->st + v.b * src[k]->sb + ch;
+#pragma unroll
+            for (int s = 0; s < S; ++s)
+              raw[k][s] = Global<IT, CPT>::load(q + s * src[k]->st, tw + s < len ? live : 0,
+                                                words >> k & 1);
+          }
+          const T *q = static_cast<const T *>(p.dy.p) + tw * p.dy.st + v.b * p.dy.sb + ch;
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+            rawd[s] = load_raw(q + s * p.dy.st, tw + s < len ? live : 0, words >> 3 & 1);
+        }
+        gates<IT>(raw, scale, k2, em1, nb, ns, ng);
+#pragma unroll
+        for (int s = 0; s < S; ++s) dy[s] = Decode<T, V>::value(rawd[s], 0.f);
+        if (tw + S > len) {
+#pragma unroll
+          for (int s = 0; s < S; ++s)
+            if (tw + s >= len) em1[s] = nb[s] = ns[s] = ng[s] = dy[s] = 0;
+        }
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          fe = fma_v(nb[s], minus, fma_v(em1[s], fe, fe));
+          mine.p = fma_v(em1[s], mine.p, mine.p);
+        }
+#pragma unroll
+        for (int s = S - 1; s >= 0; --s) {
+          const V ne = fma_v(dy[s], minus, mine.e);
+          mine.e = fma_v(em1[s], ne, ne);
+        }
+      }
+      V c = nc;
+      if (on || cs > 1) {
+        put(&sh.part[parity][warp][lane], mine);
+        sh.fwd[parity][warp][lane] = fe;
+        __syncthreads();
+        // the tile's values are in registers: its buffer takes the next copy
+        if (TMA && on && threadIdx.x == 0) issue();
+        if (cs > 1) {
+          Aff<V> all = identity<V>(), after = identity<V>();  // after: of the warps after this one
+#pragma unroll
+          for (int w = NW - 1; w >= 0; --w) {
+            if (w == warp) after = all;
+            all = then(all, get(&sh.part[parity][w][lane]));
+          }
+          if (warp < cs) put_peer(&sh.peer[round & 1][rank][lane], warp, all);
+          tc::cluster_sync();
+#pragma unroll
+          for (int q = 0; q < MAXCS; ++q)
+            if (q < cs) {
+              if (q == rank) c = nc;
+              nc = apply(get(&sh.peer[round & 1][q][lane]), nc);
+            }
+          c = apply(after, c);
+          ++round;
+        } else {
+#pragma unroll
+          for (int w = NW - 1; w >= 0; --w) {
+            if (w == warp) c = nc;
+            nc = apply(get(&sh.part[parity][w][lane]), nc);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < NW - 1; ++w)
+          if (w < warp)
+            h = fma_v(get(&sh.part[parity][w][lane]).p, h, sh.fwd[parity][w][lane]);
+        parity ^= 1;
+      }
+      if (tile >= v.first) {
+        if (on) {
+#pragma unroll
+          for (int s = S - 1; s >= 0; --s) {  // dy becomes -dL/dh
+            dy[s] = fma_v(dy[s], minus, c);
+            c = fma_v(em1[s], dy[s], dy[s]);
+          }
+        }
+        V part = zero;
+        const int64_t tb = tw, b = v.b;
+        T *dx = p.dx.p ? static_cast<T *>(p.dx.p) + tb * p.dx.st + b * p.dx.sb + ch : nullptr;
+        T *dr = p.dr.p ? static_cast<T *>(p.dr.p) + tb * p.dr.st + b * p.dr.sb + ch : nullptr;
+        T *di = p.di.p ? static_cast<T *>(p.di.p) + tb * p.di.st + b * p.di.sb + ch : nullptr;
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          V gx = zero, gr = zero, gi = zero, gl = zero;
+          if (on) grads(em1[s], nb[s], ns[s], ng[s], nk, dy[s], h, gx, gr, gi, gl);
+          part = add_v(part, gl);
+          if (tw + s < p.T) {
+            if (dx) store_raw(dx + s * p.dx.st, gx, live, words >> 4 & 1);
+            if (dr) store_raw(dr + s * p.dr.st, gr, live, words >> 5 & 1);
+            if (di) store_raw(di + s * p.di.st, gi, live, words >> 6 & 1);
+          }
+        }
+        sum = add_v(sum, part);
+      }
+    }
+    if (rank == 0 && warp == 0 && p.dh0) store_v(p.dh0 + row, mul_v(nc, minus), live);
+    if (p.dlambda) {
+      __syncthreads();
+      sh.sum[warp][lane] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        sum = zero;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) sum = add_v(sum, sh.sum[w][lane]);
+        store_v(partial + ((int64_t)(v.seg * p.B + v.b) * cs + rank) * p.H + ch, sum, live);
+      }
+    }
+  }
+  if (cs > 1) tc::cluster_sync();  // no block leaves while a peer may still write to it
+}
+
+// dlambda[h] = -c sigmoid(lambda) * the sum of `rows` partial sums.  A warp has
+// 32 channels; its block's warps share the rows, and the shares join in order.
+constexpr int SUM_WARPS = 16;
+__global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int rows, int H,
+                                      const float *__restrict__ lambda, float c,
+                                      float *__restrict__ dlambda) {
+  __shared__ float part[SUM_WARPS][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (h < H)
+#pragma unroll 4
+    for (int b = warp; b < rows; b += SUM_WARPS) s += partial[(int64_t)b * H + h];
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && h < H) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < SUM_WARPS; ++w) s += part[w][lane];
+    dlambda[h] = -c * s / (1.f + expf(-lambda[h]));
+  }
+}
+
+template <typename T>
+Plan plan_bwd(const LinrecBwd &p, int nsm) {
+  return plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), nsm, PER_SM);
+}
+Plan plan_of(const LinrecBwd &p, int nsm) {
+  return p.dtype == RCU_BF16 ? plan_bwd<bf16>(p, nsm) : plan_bwd<float>(p, nsm);
+}
+
+template <typename IT, typename T>
+cudaError_t bwd(const LinrecBwd &p, float *partial, int *err, int nsm, bool vec, cudaStream_t s,
+                int *launches) {
+  constexpr int CW = Shape<T>::CW;
+  const Plan pl = plan_of(p, nsm);
+  CUtensorMap m[4];
+  const SeqIn *in[4] = {&p.x, &p.r, &p.i, &p.dy};
+  const SeqOut *out[3] = {&p.dx, &p.dr, &p.di};
+  bool tma = vec;
+  int words = 0;
+  for (int k = 0; k < 4; ++k) {
+    const int bytes = k < 3 ? (int)sizeof(IT) : (int)sizeof(T);
+    tma = tma &&
+          tc_map_3d(&m[k], in[k]->p, bytes, p.H, p.B, p.T, in[k]->sb, in[k]->st, CW, 1, STEPS);
+    words |= word_aligned(in[k]->p, in[k]->st, in[k]->sb, bytes) << k;
+  }
+  for (int k = 0; k < 3; ++k)
+    words |= word_aligned(out[k]->p, out[k]->st, out[k]->sb, sizeof(T)) << (4 + k);
+  const size_t smem =
+      sizeof(Smem<typename Lane<T>::V>) + (tma ? STAGES * stage_bytes<IT, T>() : 0);
+  cudaError_t e =
+      tma ? launch_cut(linrec_bwd_kernel<IT, T, true>, pl, smem, s, m[0], m[1], m[2], m[3], p,
+                       pl.cut, partial, words, err)
+          : launch_cut(linrec_bwd_kernel<IT, T, false>, pl, smem, s, m[0], m[1], m[2], m[3], p,
+                       pl.cut, partial, words, err);
+  ++*launches;
+  if (e != cudaSuccess || !p.dlambda) return e;
+  linrec_dlambda_kernel<<<ceil_div(p.H, 32), 32 * SUM_WARPS, 0, s>>>(
+      partial, p.B * pl.cut.nseg * pl.cs, p.H, p.lambda, p.c, p.dlambda);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t linrec_bwd_workspace(const LinrecBwd &p, int nsm) {
+  const Plan pl = plan_of(p, nsm);
+  return (size_t)p.B * pl.cut.nseg * pl.cs * p.H * 4;
+}
+
+cudaError_t launch_linrec_bwd(const LinrecBwd &p, void *ws, int *err, int nsm, bool vec,
+                              cudaStream_t s, int *launches) {
+  float *partial = static_cast<float *>(ws);
+  const bool q8 = p.saved == RCU_I8;
+  if (p.dtype == RCU_BF16)
+    return q8 ? bwd<int8_t, bf16>(p, partial, err, nsm, vec, s, launches)
+              : bwd<bf16, bf16>(p, partial, err, nsm, vec, s, launches);
+  return q8 ? bwd<int8_t, float>(p, partial, err, nsm, vec, s, launches)
+            : bwd<float, float>(p, partial, err, nsm, vec, s, launches);
+}
+
+}  // namespace rcu

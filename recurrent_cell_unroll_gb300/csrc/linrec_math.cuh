@@ -42,91 +42,115 @@ __device__ __forceinline__ float rsq(float v) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// minimum / maximum that keep a NaN
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
+// maximum that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
-// -c softplus(lambda) log2(e): the exponent of a per unit of s, base 2.
+// Two fp32 values in one 64-bit register pair: on sm_100 and later one packed
+// instruction adds, multiplies or fuses both, which halves what the arithmetic
+// takes of the issue slots (the forward's other limit beside the memory).
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float v) { return f2(v, v); }
+__device__ __forceinline__ float lo(F2 v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi(F2 v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// c softplus(lambda) log2(e): -log2(a) per unit of s.
 __device__ __forceinline__ float decay_rate2(float lambda, float c) {
   const float sp = lambda > 0.f ? lambda + log1pf(expf(-lambda)) : log1pf(expf(lambda));
-  return -c * sp * LOG2E;
+  return c * sp * LOG2E;
+}
+
+__device__ __forceinline__ F2 decay_rate2(F2 lambda, float c) {
+  return f2(decay_rate2(lo(lambda), c), decay_rate2(hi(lambda), c));
 }
 
 // 2^t - 1 for t <= 0, relative error 2e-7.  t = n + f, n whole, |f| <= 1/2:
 // 2^n (2^f - 1) + (2^n - 1), with (2^f - 1) / f a polynomial of degree 5
 // fitted to the least relative error (1.1e-8 before rounding); n = 0 leaves
 // the polynomial alone, so that small t keep their precision.
-__device__ __forceinline__ float ex2m1(float t) {
-  t = max_nan(t, -126.f);
-  const float m = t + 12582912.f;  // 1.5 * 2^23: rounds t to a whole number in the low bits
-  const float f = t - (m - 12582912.f);
-  float p = 1.5403512e-4f;
-  p = fmaf(p, f, 1.3390735e-3f);
-  p = fmaf(p, f, 9.6182376e-3f);
-  p = fmaf(p, f, 5.5503573e-2f);
-  p = fmaf(p, f, 2.4022649e-1f);
-  p = fmaf(p, f, 6.9314718e-1f);
-  const float s = __int_as_float((__float_as_int(m) << 23) + 0x3f800000);  // 2^n
-  return fmaf(s, p * f, s - 1.f);
+__device__ __forceinline__ F2 ex2m1(F2 t) {
+  t = f2(max_nan(lo(t), -126.f), max_nan(hi(t), -126.f));
+  const F2 m = add2(t, f2(12582912.f));  // 1.5 * 2^23: rounds t to a whole number in the low bits
+  const F2 f = fma2(add2(m, f2(-12582912.f)), f2(-1.f), t);
+  F2 p = f2(1.5403512e-4f);
+  p = fma2(p, f, f2(1.3390735e-3f));
+  p = fma2(p, f, f2(9.6182376e-3f));
+  p = fma2(p, f, f2(5.5503573e-2f));
+  p = fma2(p, f, f2(2.4022649e-1f));
+  p = fma2(p, f, f2(6.9314718e-1f));
+  const F2 s = f2(__int_as_float((__float_as_int(lo(m)) << 23) + 0x3f800000),  // 2^n
+                  __int_as_float((__float_as_int(hi(m)) << 23) + 0x3f800000));
+  return fma2(s, mul2(p, f), add2(s, f2(-1.f)));
 }
 
-// The two sigmoids: er = e^-r, ei = e^-i, s = 1 / (1 + er), g = 1 / (1 + ei).
-// The exponents stop at 62, where the product of the denominators is still a
-// normal number: a sigmoid below 2^-62 is held there.  A NaN stays one.
+// The two sigmoids of a pair of elements, negated: ns = -1 / (1 + e^-r) makes
+// the decay's exponent k2 ns, and the signs of the others cancel in products.
+// Logits stop at -42 (logit_floor), where e^-r is 2^60.6 and the product of the
+// denominators still a normal number: a sigmoid below 6e-19 is held there.  A
+// NaN stays one.
 struct Sig {
-  float er, ei, s, g;
+  F2 ns, ng;
 };
-__device__ __forceinline__ Sig sigmoids(float r, float i) {
-  Sig v;
-  v.er = ex2(min_nan(r * -LOG2E, 62.f));
-  v.ei = ex2(min_nan(i * -LOG2E, 62.f));
-  const float pr = 1.f + v.er, pi = 1.f + v.ei;
-  const float inv = rcp(pr * pi);
-  v.s = inv * pi;
-  v.g = inv * pr;
-  return v;
+__device__ __forceinline__ float logit_floor(float v) { return max_nan(v, -42.f); }
+__device__ __forceinline__ uint32_t logit_floor(uint32_t bf16x2) {  // two bf16: -42 = 0xc228
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bf16x2), "r"(0xc228c228u));
+  return r;
+}
+__device__ __forceinline__ Sig sigmoids(F2 r, F2 i) {
+  const F2 tr = mul2(r, f2(-LOG2E)), ti = mul2(i, f2(-LOG2E));
+  const F2 pr = add2(f2(ex2(lo(tr)), ex2(hi(tr))), f2(1.f));
+  const F2 pi = add2(f2(ex2(lo(ti)), ex2(hi(ti))), f2(1.f));
+  const F2 d = mul2(pr, pi), ninv = f2(rcp(-lo(d)), rcp(-hi(d)));
+  return {mul2(ninv, pi), mul2(ninv, pr)};
 }
 
-// w = 1 - a^2 from em1 = a - 1, and 1 / sqrt(w).  w = 0 (a decay rate of 0)
-// gives a large finite root: every use multiplies it by something that is 0.
-__device__ __forceinline__ float one_minus_a2(float em1) { return -em1 * (2.f + em1); }
-__device__ __forceinline__ float inv_beta(float w) { return rsq(max_nan(w, 1e-37f)); }
+// w = 1 - a^2 = em1 (-2 - em1) from em1 = a - 1.  A decay rate of 0 would make
+// it 0: the tiny addend leaves a finite 1 / sqrt(w), which every use multiplies
+// by something that is 0 then.
+__device__ __forceinline__ F2 one_minus_a2(F2 em1) {
+  return fma2(em1, fma2(em1, f2(-1.f), f2(-2.f)), f2(1e-37f));
+}
+__device__ __forceinline__ float one_minus_a2(float em1) {
+  return fmaf(em1, -2.f - em1, 1e-37f);
+}
+__device__ __forceinline__ F2 inv_beta(F2 w) { return f2(rsq(lo(w)), rsq(hi(w))); }
+__device__ __forceinline__ float inv_beta(float w) { return rsq(w); }
 
-// em1 and b = beta g x of one element.
-__device__ __forceinline__ void gate(float x, float r, float i, float k2, float &em1, float &b) {
+// em1 and b = beta g x of a pair of elements (logits already floored).
+__device__ __forceinline__ void gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &b) {
   const Sig v = sigmoids(r, i);
-  em1 = ex2m1(k2 * v.s);
-  const float w = one_minus_a2(em1);
-  b = w * inv_beta(w) * (v.g * x);
+  em1 = ex2m1(mul2(k2, v.ns));
+  const F2 w = one_minus_a2(em1);
+  b = mul2(mul2(w, inv_beta(w)), mul2(mul2(v.ng, f2(-1.f)), x));
 }
 
 // One step: a h + b.
+__device__ __forceinline__ F2 step(F2 em1, F2 h, F2 b) { return add2(h, fma2(em1, h, b)); }
 __device__ __forceinline__ float step(float em1, float h, float b) { return h + fmaf(em1, h, b); }
-
-// Local gradients of one element given e = dL/dh_t and the state before it.
-struct Grad {
-  float dx, dr, di, dlog_s;  // dlog_s: dL/da a s, summed over elements into dlambda
-};
-__device__ __forceinline__ Grad grads(float x, const Sig &v, float em1, float k, float hp,
-                                      float e) {
-  const float w = one_minus_a2(em1), rb = inv_beta(w), beta = w * rb;
-  const float gx = v.g * x, a = 1.f + em1;
-  Grad d;
-  d.dx = e * (beta * v.g);
-  d.di = e * (beta * gx) * (v.ei * v.g);
-  // s / beta stays finite as s goes to 0 (like sqrt(s)), so s comes in before 1 / beta's product
-  d.dlog_s = e * (fmaf(em1, hp, hp) * v.s - a * a * gx * (v.s * rb));
-  d.dr = k * d.dlog_s * (v.er * v.s);
-  return d;
-}
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }

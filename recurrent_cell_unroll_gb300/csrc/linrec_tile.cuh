@@ -1,0 +1,249 @@
+// What the gated linear recurrence's forward (linrec_fwd.cu) and backward
+// (linrec_bwd.cu) kernels share: how the work is cut into tiles, units and
+// clusters, and how a tile's values and the affine maps of its steps move.
+//
+// A block of NW warps takes a tile of NW * S steps x CW channels of one batch
+// row; CW values of the tensors' type are 128 bytes, so that a step of a tile
+// is one full line.  Warp w has the steps [w * S, w * S + S), lane l the CPT
+// channels from l * CPT.  A step is h -> a h + b, and steps compose to affine
+// maps h -> P h + E: each warp reduces its steps to a map, the maps are chained
+// in order, and the warp then runs its steps from the state that reaches it.
+#pragma once
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "linrec_math.cuh"
+#include "rcu.h"
+#include "seq.h"
+#include "tc.h"
+#include "tc_common.cuh"
+
+namespace rcu {
+namespace linrec {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int CHUNK = RCU_LINREC_CHUNK;
+constexpr int BLOCK8 = RCU_ACT8_BLOCK;
+constexpr int NW = 8, NT = 32 * NW;
+constexpr int MAXCS = 8;                     // blocks of a cluster (the portable limit)
+constexpr uint64_t WAIT_NS = 2000000000ull;  // bound on any wait for a copy
+
+template <typename T>
+struct Shape {
+  static constexpr int CPT = 4 / (int)sizeof(T), CW = 32 * CPT;
+};
+
+// The length of row b, clamped to [0, T]; an outside value is reported.
+__device__ __forceinline__ int row_length(const int32_t *lengths, int b, int T, int *err) {
+  if (!lengths) return T;
+  const int len = lengths[b];
+  if (len < 0 || len > T) atomicCAS(err, (int)DEV_OK, (int)DEV_LENGTHS);
+  return min(max(len, 0), T);
+}
+
+// Unit u = (segment of time, batch row, group of CW channels), the groups
+// fastest: blocks that run together then read neighbouring channels of the same
+// steps.  A cluster takes a unit, its blocks consecutive tiles of it.
+struct Cut {
+  int groups, units, tiles, tps, nseg;  // tps: tiles of a segment
+};
+struct Unit {
+  int seg, b, c0, first, last;  // tiles [first, last)
+};
+__device__ __forceinline__ Unit unit_of(const Cut &cut, int B, int u, int cw) {
+  Unit v;
+  v.c0 = u % cut.groups * cw;
+  const int q = u / cut.groups;
+  v.b = q % B;
+  v.seg = q / B;
+  v.first = v.seg * cut.tps;
+  v.last = min(cut.tiles, v.first + cut.tps);
+  return v;
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                            int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// ---- one lane's values of a step, as they lie in memory (CPT of them)
+
+// fp32: one channel; bf16: two, as one word where the address allows
+__device__ __forceinline__ uint32_t load_raw(const float *p, int live, bool) {
+  return live > 0 ? __float_as_uint(__ldg(p)) : 0u;
+}
+__device__ __forceinline__ uint32_t load_raw(const bf16 *p, int live, bool word) {
+  if (live > 1 && word) return __ldg(reinterpret_cast<const uint32_t *>(p));
+  const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+  uint32_t v = live > 0 ? __ldg(q) : 0u;
+  if (live > 1) v |= (uint32_t)__ldg(q + 1) << 16;
+  return v;
+}
+__device__ __forceinline__ void store_raw(float *p, float v, int live, bool) {
+  if (live > 0) *p = v;
+}
+__device__ __forceinline__ void store_raw(bf16 *p, F2 v, int live, bool word) {
+  const __nv_bfloat162 o = __floats2bfloat162_rn(lo(v), hi(v));
+  if (live > 1 && word) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = o;
+  } else {
+    if (live > 0) p[0] = o.x;
+    if (live > 1) p[1] = o.y;
+  }
+}
+__device__ __forceinline__ F2 bf16_pair(uint32_t v) {
+  return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// ---- a lane's channels: two in a pair (bf16), or one (fp32)
+
+template <typename T>
+struct Lane;
+template <>
+struct Lane<float> {
+  typedef float V;
+};
+template <>
+struct Lane<bf16> {
+  typedef F2 V;
+};
+__device__ __forceinline__ float fma_v(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ F2 fma_v(F2 a, F2 b, F2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float add_v(float a, float b) { return a + b; }
+__device__ __forceinline__ F2 add_v(F2 a, F2 b) { return add2(a, b); }
+__device__ __forceinline__ float mul_v(float a, float b) { return a * b; }
+__device__ __forceinline__ F2 mul_v(F2 a, F2 b) { return mul2(a, b); }
+__device__ __forceinline__ void set(float &v, float c) { v = c; }
+__device__ __forceinline__ void set(F2 &v, float c) { v = f2(c); }
+
+// from and to fp32 rows [.., H]
+__device__ __forceinline__ void load_v(const float *p, int live, float &v) {
+  v = live > 0 ? p[0] : 0.f;
+}
+__device__ __forceinline__ void load_v(const float *p, int live, F2 &v) {
+  v = f2(live > 0 ? p[0] : 0.f, live > 1 ? p[1] : 0.f);
+}
+__device__ __forceinline__ void store_v(float *p, float v, int live) {
+  if (live > 0) p[0] = v;
+}
+__device__ __forceinline__ void store_v(float *p, F2 v, int live) {
+  if (live > 0) p[0] = lo(v);
+  if (live > 1) p[1] = hi(v);
+}
+
+// ---- affine maps h -> P h + E
+
+template <typename V>
+struct Aff {
+  V p, e;
+};
+template <typename V>
+__device__ __forceinline__ Aff<V> identity() {
+  Aff<V> a;
+  set(a.p, 1.f);
+  set(a.e, 0.f);
+  return a;
+}
+template <typename V>
+__device__ __forceinline__ V apply(const Aff<V> &a, V h) {
+  return fma_v(a.p, h, a.e);
+}
+// first a, then b
+template <typename V>
+__device__ __forceinline__ Aff<V> then(const Aff<V> &a, const Aff<V> &b) {
+  return {mul_v(a.p, b.p), fma_v(b.p, a.e, b.e)};
+}
+// as a lane's 8 or 16 bytes of shared memory
+template <typename V>
+struct Slot;
+template <>
+struct Slot<float> {
+  typedef float2 type;
+};
+template <>
+struct Slot<F2> {
+  typedef float4 type;
+};
+__device__ __forceinline__ void put(float2 *at, const Aff<float> &a) {
+  *at = make_float2(a.p, a.e);
+}
+__device__ __forceinline__ void put(float4 *at, const Aff<F2> &a) {
+  *at = make_float4(lo(a.p), hi(a.p), lo(a.e), hi(a.e));
+}
+__device__ __forceinline__ Aff<float> get(const float2 *at) {
+  const float2 v = *at;
+  return {v.x, v.y};
+}
+__device__ __forceinline__ Aff<F2> get(const float4 *at) {
+  const float4 v = *at;
+  return {f2(v.x, v.y), f2(v.z, v.w)};
+}
+// the same into block `rank` of the cluster (its copy of the variable at `at`)
+__device__ __forceinline__ void put_peer(float2 *at, int rank, const Aff<float> &a) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
+                   tc::mapa_shared(tc::smem_u32(at), rank)),
+               "f"(a.p), "f"(a.e)
+               : "memory");
+}
+__device__ __forceinline__ void put_peer(float4 *at, int rank, const Aff<F2> &a) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                   tc::mapa_shared(tc::smem_u32(at), rank)),
+               "f"(lo(a.p)), "f"(hi(a.p)), "f"(lo(a.e)), "f"(hi(a.e))
+               : "memory");
+}
+
+// ---- host side
+
+inline bool word_aligned(const void *p, int64_t st, int64_t sb, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % 4 == 0 && st * bytes % 4 == 0 && sb * bytes % 4 == 0;
+}
+
+struct Plan {
+  Cut cut;
+  int cs, grid;
+};
+
+// How the recurrence over `tiles` tiles of B rows x `groups` channel groups is
+// cut for a kernel of which per_sm blocks run on an SM.
+inline Plan plan_cut(int tiles, int B, int groups, int nsm, int per_sm) {
+  Plan pl;
+  const int64_t slots = (int64_t)nsm * per_sm, rows = (int64_t)B * groups;
+  pl.cut.groups = groups;
+  pl.cut.tiles = tiles;
+  pl.cs = 1;
+  pl.cut.nseg = 1;
+  while (pl.cs < MAXCS && rows * pl.cs * 2 <= slots && pl.cs < tiles) pl.cs *= 2;
+  pl.cut.tps = ceil_div(tiles, pl.cut.nseg);
+  pl.cut.units = (int)(rows * pl.cut.nseg);
+  pl.grid = (int)std::min<int64_t>((int64_t)pl.cut.units * pl.cs, slots / pl.cs * pl.cs);
+  return pl;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cut(void (*fn)(KArgs...), const Plan &pl, size_t smem, cudaStream_t s,
+                       Args... args) {
+  cudaError_t e =
+      cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(pl.grid);
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = pl.cs;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = pl.cs > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+}  // namespace linrec
+}  // namespace rcu
