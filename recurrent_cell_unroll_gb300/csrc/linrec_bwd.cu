@@ -14,7 +14,11 @@ namespace {
 
 using namespace linrec;
 
-constexpr int S = CHUNK / NW, STEPS = CHUNK, STAGES = 3, PER_SM = 2;
+#ifndef V_STAGES
+#define V_STAGES 2
+#define V_PER 2
+#endif
+constexpr int S = CHUNK / NW, STEPS = CHUNK, STAGES = V_STAGES, PER_SM = V_PER;
 
 template <typename V>
 struct Smem {
@@ -23,6 +27,7 @@ struct Smem {
   typename Slot<V>::type peer[2][MAXCS][32];  // the blocks' P and R, by parity of the round
   V sum[NW][32];                              // the warps' shares of dlambda
   uint64_t full[STAGES];
+  uint64_t met[2];  // every block's map of a round is here, by parity of the round
   int abort;
 };
 
@@ -62,38 +67,53 @@ __device__ __forceinline__ float code_value(uint32_t biased, float scale) {
   const float v = __uint_as_float(0x4b000000u | biased) - 8388736.f;
   return v == -128.f ? __int_as_float(0x7fc00000) : v * scale;
 }
+// One step's values: x, and the logits within their limits
 template <typename IT, typename V>
 struct Decode;
 template <>
 struct Decode<bf16, F2> {
-  __device__ __forceinline__ static F2 logit(uint32_t v, float) { return bf16_pair(logit_floor(v)); }
-  __device__ __forceinline__ static F2 value(uint32_t v, float) { return bf16_pair(v); }
+  __device__ __forceinline__ static F2 x(uint32_t v, float) { return bf16_pair(v); }
+  __device__ __forceinline__ static F2 r(uint32_t v, float, const Limits &l) {
+    return bf16_pair(limit_r(v, l));
+  }
+  __device__ __forceinline__ static F2 i(uint32_t v, float) { return bf16_pair(floor_logit(v)); }
 };
 template <>
 struct Decode<int8_t, F2> {
-  __device__ __forceinline__ static F2 value(uint32_t v, float scale) {
+  __device__ __forceinline__ static F2 x(uint32_t v, float scale) {
     v ^= 0x8080u;
     return f2(code_value(v & 0xffu, scale), code_value(v >> 8, scale));
   }
-  __device__ __forceinline__ static F2 logit(uint32_t v, float scale) {
-    const F2 f = value(v, scale);
-    return f2(logit_floor(lo(f)), logit_floor(hi(f)));
+  __device__ __forceinline__ static F2 r(uint32_t v, float scale, const Limits &l) {
+    const F2 f = x(v, scale);  // not limited as bf16: the channels' limits, widened
+    const float a = __uint_as_float(l.top2 << 16), b = __uint_as_float(l.top2 & 0xffff0000u);
+    return f2(min_nan(floor_logit(lo(f)), a), min_nan(floor_logit(hi(f)), b));
+  }
+  __device__ __forceinline__ static F2 i(uint32_t v, float scale) {
+    const F2 f = x(v, scale);
+    return f2(floor_logit(lo(f)), floor_logit(hi(f)));
   }
 };
 template <>
 struct Decode<float, float> {
-  __device__ __forceinline__ static float logit(uint32_t v, float) {
-    return logit_floor(__uint_as_float(v));
+  __device__ __forceinline__ static float x(uint32_t v, float) { return __uint_as_float(v); }
+  __device__ __forceinline__ static float r(uint32_t v, float, const Limits &l) {
+    return limit_r(__uint_as_float(v), l);
   }
-  __device__ __forceinline__ static float value(uint32_t v, float) { return __uint_as_float(v); }
+  __device__ __forceinline__ static float i(uint32_t v, float) {
+    return floor_logit(__uint_as_float(v));
+  }
 };
 template <>
 struct Decode<int8_t, float> {
-  __device__ __forceinline__ static float value(uint32_t v, float scale) {
+  __device__ __forceinline__ static float x(uint32_t v, float scale) {
     return code_value(v ^ 0x80u, scale);
   }
-  __device__ __forceinline__ static float logit(uint32_t v, float scale) {
-    return logit_floor(value(v, scale));
+  __device__ __forceinline__ static float r(uint32_t v, float scale, const Limits &l) {
+    return limit_r(x(v, scale), l);
+  }
+  __device__ __forceinline__ static float i(uint32_t v, float scale) {
+    return floor_logit(x(v, scale));
   }
 };
 
@@ -107,26 +127,26 @@ __device__ __forceinline__ void gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &nb, F
 }
 template <typename IT>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (&scale)[3][S], F2 k2,
-                                      F2 (&em1)[S], F2 (&nb)[S], F2 (&ns)[S], F2 (&ng)[S]) {
+                                      const Limits &lim, F2 (&em1)[S], F2 (&nb)[S], F2 (&ns)[S], F2 (&ng)[S]) {
   typedef Decode<IT, F2> D;
 #pragma unroll
   for (int s = 0; s < S; ++s)
-    gate(D::value(raw[0][s], scale[0][s]), D::logit(raw[1][s], scale[1][s]),
-         D::logit(raw[2][s], scale[2][s]), k2, em1[s], nb[s], ns[s], ng[s]);
+    gate(D::x(raw[0][s], scale[0][s]), D::r(raw[1][s], scale[1][s], lim),
+         D::i(raw[2][s], scale[2][s]), k2, em1[s], nb[s], ns[s], ng[s]);
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
 template <typename IT>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (&scale)[3][S],
-                                      float k2, float (&em1)[S], float (&nb)[S], float (&ns)[S],
-                                      float (&ng)[S]) {
+                                      float k2, const Limits &lim, float (&em1)[S], float (&nb)[S],
+                                      float (&ns)[S], float (&ng)[S]) {
   typedef Decode<IT, float> D;
 #pragma unroll
   for (int s = 0; s < S; s += 2) {
     F2 v[4];
-    gate(f2(D::value(raw[0][s], scale[0][s]), D::value(raw[0][s + 1], scale[0][s + 1])),
-         f2(D::logit(raw[1][s], scale[1][s]), D::logit(raw[1][s + 1], scale[1][s + 1])),
-         f2(D::logit(raw[2][s], scale[2][s]), D::logit(raw[2][s + 1], scale[2][s + 1])), f2(k2),
-         v[0], v[1], v[2], v[3]);
+    gate(f2(D::x(raw[0][s], scale[0][s]), D::x(raw[0][s + 1], scale[0][s + 1])),
+         f2(D::r(raw[1][s], scale[1][s], lim), D::r(raw[1][s + 1], scale[1][s + 1], lim)),
+         f2(D::i(raw[2][s], scale[2][s]), D::i(raw[2][s + 1], scale[2][s + 1])), f2(k2), v[0], v[1],
+         v[2], v[3]);
     em1[s] = lo(v[0]), nb[s] = lo(v[1]), ns[s] = lo(v[2]), ng[s] = lo(v[3]);
     em1[s + 1] = hi(v[0]), nb[s + 1] = hi(v[1]), ns[s + 1] = hi(v[2]), ng[s + 1] = hi(v[3]);
   }
@@ -188,15 +208,15 @@ __global__ void __launch_bounds__(NT, PER_SM)
       return;
     }
   };
-  if (TMA) {
-    if (threadIdx.x == 0) {
-      for (int st = 0; st < STAGES; ++st) tc::mbar_init(&sh.full[st], 1);
-      sh.abort = 0;
-      tc::fence_mbar_init();
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < STAGES; ++st) tc::mbar_init(&sh.full[st], 1);
+    for (int q = 0; q < 2; ++q) tc::mbar_init(&sh.met[q], 1);
+    sh.abort = 0;
+    tc::fence_mbar_init();
+    if (TMA)
       for (int st = 0; st < STAGES; ++st) issue();
-    }
-    __syncthreads();
   }
+  __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
   int used = 0, parity = 0, round = 0;
@@ -210,6 +230,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
     set(minus, -1.f);
     load_v(p.lambda + ch, live, k2);
     k2 = decay_rate2(k2, p.c);
+    const Limits lim = limits(k2);
+    // all three outputs move a word a lane
+    const bool whole = v.c0 + CW <= p.H && (words >> 4 & 7) == 7 && p.dx.p && p.dr.p && p.di.p;
     set(nk, -1.f / LOG2E);
     nk = mul_v(nk, k2);  // -K
     if (p.dh_n) load_v(p.dh_n + row, live, nc);
@@ -266,9 +289,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
           for (int s = 0; s < S; ++s)
             rawd[s] = load_raw(q + s * p.dy.st, tw + s < len ? live : 0, words >> 3 & 1);
         }
-        gates<IT>(raw, scale, k2, em1, nb, ns, ng);
+        gates<IT>(raw, scale, k2, lim, em1, nb, ns, ng);
 #pragma unroll
-        for (int s = 0; s < S; ++s) dy[s] = Decode<T, V>::value(rawd[s], 0.f);
+        for (int s = 0; s < S; ++s) dy[s] = Decode<T, V>::x(rawd[s], 0.f);
         if (tw + S > len) {
 #pragma unroll
           for (int s = 0; s < S; ++s)
@@ -290,8 +313,12 @@ __global__ void __launch_bounds__(NT, PER_SM)
         put(&sh.part[parity][warp][lane], mine);
         sh.fwd[parity][warp][lane] = fe;
         __syncthreads();
-        // the tile's values are in registers: its buffer takes the next copy
-        if (TMA && on && threadIdx.x == 0) issue();
+        if (threadIdx.x == 0) {
+          if (cs > 1)
+            tc::mbar_arrive_expect_tx(&sh.met[round & 1], cs * 32 * (uint32_t)sizeof(Aff<V>));
+          // the tile's values are in registers: its buffer takes the next copy
+          if (TMA && on) issue();
+        }
         if (cs > 1) {
           Aff<V> all = identity<V>(), after = identity<V>();  // after: of the warps after this one
 #pragma unroll
@@ -299,8 +326,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
             if (w == warp) after = all;
             all = then(all, get(&sh.part[parity][w][lane]));
           }
-          if (warp < cs) put_peer(&sh.peer[round & 1][rank][lane], warp, all);
-          tc::cluster_sync();
+          if (warp < cs)
+            put_peer(&sh.peer[round & 1][rank][lane], &sh.met[round & 1], warp, all);
+          tc::mbar_wait_cluster(&sh.met[round & 1], round >> 1 & 1, err, &sh.abort, WAIT_NS);
 #pragma unroll
           for (int q = 0; q < MAXCS; ++q)
             if (q < cs) {
@@ -322,31 +350,51 @@ __global__ void __launch_bounds__(NT, PER_SM)
             h = fma_v(get(&sh.part[parity][w][lane]).p, h, sh.fwd[parity][w][lane]);
         parity ^= 1;
       }
-      if (tile >= v.first) {
-        if (on) {
+      if (tile < v.first) continue;
+      const int64_t tb = tw, b = v.b;
+      T *dx = static_cast<T *>(p.dx.p) + tb * p.dx.st + b * p.dx.sb + ch;
+      T *dr = static_cast<T *>(p.dr.p) + tb * p.dr.st + b * p.dr.sb + ch;
+      T *di = static_cast<T *>(p.di.p) + tb * p.di.st + b * p.di.sb + ch;
+      if (on) {
 #pragma unroll
-          for (int s = S - 1; s >= 0; --s) {  // dy becomes -dL/dh
-            dy[s] = fma_v(dy[s], minus, c);
-            c = fma_v(em1[s], dy[s], dy[s]);
-          }
+        for (int s = S - 1; s >= 0; --s) {  // dy becomes -dL/dh
+          dy[s] = fma_v(dy[s], minus, c);
+          c = fma_v(em1[s], dy[s], dy[s]);
         }
         V part = zero;
-        const int64_t tb = tw, b = v.b;
-        T *dx = p.dx.p ? static_cast<T *>(p.dx.p) + tb * p.dx.st + b * p.dx.sb + ch : nullptr;
-        T *dr = p.dr.p ? static_cast<T *>(p.dr.p) + tb * p.dr.st + b * p.dr.sb + ch : nullptr;
-        T *di = p.di.p ? static_cast<T *>(p.di.p) + tb * p.di.st + b * p.di.sb + ch : nullptr;
+        if (whole && tw + S <= p.T) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          V gx = zero, gr = zero, gi = zero, gl = zero;
-          if (on) grads(em1[s], nb[s], ns[s], ng[s], nk, dy[s], h, gx, gr, gi, gl);
-          part = add_v(part, gl);
-          if (tw + s < p.T) {
-            if (dx) store_raw(dx + s * p.dx.st, gx, live, words >> 4 & 1);
-            if (dr) store_raw(dr + s * p.dr.st, gr, live, words >> 5 & 1);
-            if (di) store_raw(di + s * p.di.st, gi, live, words >> 6 & 1);
+          for (int s = 0; s < S; ++s) {
+            V gx, gr, gi, gl;
+            grads(em1[s], nb[s], ns[s], ng[s], nk, dy[s], h, gx, gr, gi, gl);
+            part = add_v(part, gl);
+            store_raw(dx, gx);
+            store_raw(dr, gr);
+            store_raw(di, gi);
+            dx += p.dx.st, dr += p.dr.st, di += p.di.st;
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            V gx, gr, gi, gl;
+            grads(em1[s], nb[s], ns[s], ng[s], nk, dy[s], h, gx, gr, gi, gl);
+            part = add_v(part, gl);
+            if (tw + s < p.T) {
+              if (p.dx.p) store_raw(dx, gx, live);
+              if (p.dr.p) store_raw(dr, gr, live);
+              if (p.di.p) store_raw(di, gi, live);
+            }
+            dx += p.dx.st, dr += p.dr.st, di += p.di.st;
           }
         }
         sum = add_v(sum, part);
+      } else {
+        for (int s = 0; s < S && tw + s < p.T; ++s) {
+          if (p.dx.p) store_raw(dx, zero, live);
+          if (p.dr.p) store_raw(dr, zero, live);
+          if (p.di.p) store_raw(di, zero, live);
+          dx += p.dx.st, dr += p.dr.st, di += p.di.st;
+        }
       }
     }
     if (rank == 0 && warp == 0 && p.dh0) store_v(p.dh0 + row, mul_v(nc, minus), live);

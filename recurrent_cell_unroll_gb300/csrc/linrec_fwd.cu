@@ -14,7 +14,12 @@ namespace {
 
 using namespace linrec;
 
-constexpr int S = 8, STEPS = NW * S, STAGES = 2, PER_SM = 3;
+#ifndef V_S
+#define V_S 16
+#define V_STAGES 2
+#define V_PER 2
+#endif
+constexpr int S = V_S, STEPS = NW * S, STAGES = V_STAGES, PER_SM = V_PER;
 constexpr int TILE_BYTES = STEPS * 128;
 
 template <typename V>
@@ -22,25 +27,27 @@ struct Smem {
   typename Slot<V>::type part[2][NW][32];     // the warps' maps, by parity of the tile
   typename Slot<V>::type peer[2][MAXCS][32];  // the cluster's blocks' maps, by parity of the round
   uint64_t full[STAGES];
+  uint64_t met[2];  // every block's map of a round is here, by parity of the round
   int abort;
 };
 
 // em1 and b of the lane's channels at each of S steps
-__device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], F2 k2, F2 (&em1)[S], F2 (&in)[S]) {
+__device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], F2 k2, const Limits &lim,
+                                      F2 (&em1)[S], F2 (&in)[S]) {
 #pragma unroll
   for (int s = 0; s < S; ++s)
-    gate(bf16_pair(raw[0][s]), bf16_pair(logit_floor(raw[1][s])), bf16_pair(logit_floor(raw[2][s])),
-         k2, em1[s], in[s]);
+    gate(bf16_pair(raw[0][s]), bf16_pair(limit_r(raw[1][s], lim)),
+         bf16_pair(floor_logit(raw[2][s])), k2, em1[s], in[s]);
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
-__device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, float (&em1)[S],
-                                      float (&in)[S]) {
+__device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, const Limits &lim,
+                                      float (&em1)[S], float (&in)[S]) {
   auto at = [&](int k, int s) { return __uint_as_float(raw[k][s]); };
 #pragma unroll
   for (int s = 0; s < S; s += 2) {
     F2 m, b;
-    gate(f2(at(0, s), at(0, s + 1)), f2(logit_floor(at(1, s)), logit_floor(at(1, s + 1))),
-         f2(logit_floor(at(2, s)), logit_floor(at(2, s + 1))), f2(k2), m, b);
+    gate(f2(at(0, s), at(0, s + 1)), f2(limit_r(at(1, s), lim), limit_r(at(1, s + 1), lim)),
+         f2(floor_logit(at(2, s)), floor_logit(at(2, s + 1))), f2(k2), m, b);
     em1[s] = lo(m), em1[s + 1] = hi(m);
     in[s] = lo(b), in[s + 1] = hi(b);
   }
@@ -77,15 +84,15 @@ __global__ void __launch_bounds__(NT, PER_SM)
       return;
     }
   };
-  if (TMA) {
-    if (threadIdx.x == 0) {
-      for (int st = 0; st < STAGES; ++st) tc::mbar_init(&sh.full[st], 1);
-      sh.abort = 0;
-      tc::fence_mbar_init();
+  if (threadIdx.x == 0) {
+    for (int st = 0; st < STAGES; ++st) tc::mbar_init(&sh.full[st], 1);
+    for (int q = 0; q < 2; ++q) tc::mbar_init(&sh.met[q], 1);
+    sh.abort = 0;
+    tc::fence_mbar_init();
+    if (TMA)
       for (int st = 0; st < STAGES; ++st) issue();
-    }
-    __syncthreads();
   }
+  __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
   int used = 0, parity = 0, round = 0;
@@ -97,6 +104,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
     V k2, carry;
     load_v(p.lambda + ch, live, k2);
     k2 = decay_rate2(k2, p.c);
+    const Limits lim = limits(k2);
+    const bool whole = v.c0 + CW <= p.H && (words >> 3 & 1);  // y moves a word a lane
     if (p.h0) load_v(p.h0 + row, live, carry);
     else set(carry, 0.f);
     for (int base = v.first; base < v.last; base += cs) {
@@ -126,7 +135,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
               raw[k][s] = load_raw(q + s * src[k]->st, tw + s < len ? live : 0, words >> k & 1);
           }
         }
-        gates(raw, k2, em1, in);
+        gates(raw, k2, lim, em1, in);
         if (tw + S > len) {
 #pragma unroll
           for (int s = 0; s < S; ++s)
@@ -142,8 +151,12 @@ __global__ void __launch_bounds__(NT, PER_SM)
       if (on || cs > 1) {
         put(&sh.part[parity][warp][lane], mine);
         __syncthreads();
-        // the tile's values are in registers: its buffer takes the next copy
-        if (TMA && on && threadIdx.x == 0) issue();
+        if (threadIdx.x == 0) {
+          if (cs > 1)
+            tc::mbar_arrive_expect_tx(&sh.met[round & 1], cs * 32 * (uint32_t)sizeof(Aff<V>));
+          // the tile's values are in registers: its buffer takes the next copy
+          if (TMA && on) issue();
+        }
         Aff<V> before = identity<V>();  // the maps of the warps before this one
         if (cs > 1) {
           Aff<V> all = identity<V>();
@@ -152,8 +165,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
             if (w == warp) before = all;
             all = then(all, get(&sh.part[parity][w][lane]));
           }
-          if (warp < cs) put_peer(&sh.peer[round & 1][rank][lane], warp, all);
-          tc::cluster_sync();
+          if (warp < cs)
+            put_peer(&sh.peer[round & 1][rank][lane], &sh.met[round & 1], warp, all);
+          tc::mbar_wait_cluster(&sh.met[round & 1], round >> 1 & 1, err, &sh.abort, WAIT_NS);
 #pragma unroll
           for (int q = 0; q < MAXCS; ++q)
             if (q < cs) {
@@ -162,8 +176,6 @@ __global__ void __launch_bounds__(NT, PER_SM)
             }
           ++round;
         }
-        if (warp == 0 && tile < v.last && p.states)
-          store_v(p.states + (int64_t)tile * p.B * p.H + row, h, live);
         if (cs > 1) {
           h = apply(before, h);
         } else {
@@ -174,24 +186,28 @@ __global__ void __launch_bounds__(NT, PER_SM)
           }
         }
         parity ^= 1;
-      } else if (warp == 0 && p.states) {
-        store_v(p.states + (int64_t)tile * p.B * p.H + row, h, live);
       }
-      if (tile < v.last) {
-        T *y = static_cast<T *>(p.y.p) + tw * p.y.st + v.b * p.y.sb + ch;
-        if (on && tw + S <= len) {
+      if (tile >= v.last) continue;
+      if (p.states && warp % (CHUNK / S) == 0 && tw < p.T)
+        store_v(p.states + (int64_t)(tw / CHUNK) * p.B * p.H + row, h, live);
+      T *y = static_cast<T *>(p.y.p) + tw * p.y.st + v.b * p.y.sb + ch;
+      if (whole && on && tw + S <= len) {
 #pragma unroll
-          for (int s = 0; s < S; ++s) {
-            h = step(em1[s], h, in[s]);
-            store_raw(y + s * p.y.st, h, live, words >> 3 & 1);
-          }
-        } else {
+        for (int s = 0; s < S; ++s) {
+          h = step(em1[s], h, in[s]);
+          store_raw(y, h);
+          y += p.y.st;
+        }
+      } else {
 #pragma unroll
-          for (int s = 0; s < S; ++s) {
-            if (on) h = step(em1[s], h, in[s]);
-            if (tw + s < p.T)
-              store_raw(y + s * p.y.st, tw + s < len ? h : V(0), live, words >> 3 & 1);
+        for (int s = 0; s < S; ++s) {
+          if (on) h = step(em1[s], h, in[s]);
+          const V out = tw + s < len ? h : V(0);
+          if (tw + s < p.T) {
+            if (whole) store_raw(y, out);
+            else store_raw(y, out, live);
           }
+          y += p.y.st;
         }
       }
     }

@@ -42,7 +42,12 @@ __device__ __forceinline__ float rsq(float v) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// maximum that keeps a NaN
+// minimum / maximum that keep a NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -77,22 +82,22 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// c softplus(lambda) log2(e): -log2(a) per unit of s.
+// c softplus(lambda) log2(e): -log2(a) per unit of s.  Held at 1e20, where a is
+// 2^-60 at the lowest sigmoid already.
 __device__ __forceinline__ float decay_rate2(float lambda, float c) {
   const float sp = lambda > 0.f ? lambda + log1pf(expf(-lambda)) : log1pf(expf(lambda));
-  return c * sp * LOG2E;
+  return min_nan(c * sp * LOG2E, 1e20f);
 }
 
 __device__ __forceinline__ F2 decay_rate2(F2 lambda, float c) {
   return f2(decay_rate2(lo(lambda), c), decay_rate2(hi(lambda), c));
 }
 
-// 2^t - 1 for t <= 0, relative error 2e-7.  t = n + f, n whole, |f| <= 1/2:
+// 2^t - 1 for -126 <= t <= 0, relative error 2e-7.  t = n + f, n whole, |f| <= 1/2:
 // 2^n (2^f - 1) + (2^n - 1), with (2^f - 1) / f a polynomial of degree 5
 // fitted to the least relative error (1.1e-8 before rounding); n = 0 leaves
 // the polynomial alone, so that small t keep their precision.
 __device__ __forceinline__ F2 ex2m1(F2 t) {
-  t = f2(max_nan(lo(t), -126.f), max_nan(hi(t), -126.f));
   const F2 m = add2(t, f2(12582912.f));  // 1.5 * 2^23: rounds t to a whole number in the low bits
   const F2 f = fma2(add2(m, f2(-12582912.f)), f2(-1.f), t);
   F2 p = f2(1.5403512e-4f);
@@ -108,17 +113,42 @@ __device__ __forceinline__ F2 ex2m1(F2 t) {
 
 // The two sigmoids of a pair of elements, negated: ns = -1 / (1 + e^-r) makes
 // the decay's exponent k2 ns, and the signs of the others cancel in products.
-// Logits stop at -42 (logit_floor), where e^-r is 2^60.6 and the product of the
-// denominators still a normal number: a sigmoid below 6e-19 is held there.  A
-// NaN stays one.
+// Logits stop at -42, where e^-r is 2^60.6 and the product of the denominators
+// still a normal number: a sigmoid below 6e-19 is held there.  r also stops
+// where a reaches 2^-100 (r_ceiling of the channel's rate): the state it would
+// still pass on is below any rounding, and ex2m1 keeps its range.  A NaN stays
+// one.  bf16 logits are limited as packed pairs, two at a time.
 struct Sig {
   F2 ns, ng;
 };
-__device__ __forceinline__ float logit_floor(float v) { return max_nan(v, -42.f); }
-__device__ __forceinline__ uint32_t logit_floor(uint32_t bf16x2) {  // two bf16: -42 = 0xc228
+constexpr float LOGIT_FLOOR = -42.f;
+__device__ __forceinline__ float r_ceiling(float k2) {
+  const float s = 100.f / k2;  // sigmoid(r) at the limit
+  return s < 1.f ? fmaxf(logf(s / (1.f - s)), LOGIT_FLOOR) : __int_as_float(0x7f800000);
+}
+struct Limits {
+  float top;       // fp32: of the lane's channel
+  uint32_t top2;   // bf16: of its two channels
+};
+__device__ __forceinline__ float floor_logit(float v) { return max_nan(v, LOGIT_FLOOR); }
+__device__ __forceinline__ uint32_t floor_logit(uint32_t v) {  // bf16 -42 = 0xc228
   uint32_t r;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bf16x2), "r"(0xc228c228u));
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0xc228c228u));
   return r;
+}
+__device__ __forceinline__ float limit_r(float v, const Limits &l) {
+  return min_nan(floor_logit(v), l.top);
+}
+__device__ __forceinline__ uint32_t limit_r(uint32_t v, const Limits &l) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(floor_logit(v)), "r"(l.top2));
+  return r;
+}
+__device__ __forceinline__ Limits limits(float k2) { return {r_ceiling(k2), 0u}; }
+__device__ __forceinline__ Limits limits(F2 k2) {
+  // rounded towards zero: 2^-100 by a percent or so
+  const float a = r_ceiling(lo(k2)), b = r_ceiling(hi(k2));
+  return {0.f, (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u)};
 }
 __device__ __forceinline__ Sig sigmoids(F2 r, F2 i) {
   const F2 tr = mul2(r, f2(-LOG2E)), ti = mul2(i, f2(-LOG2E));
@@ -140,12 +170,12 @@ __device__ __forceinline__ float one_minus_a2(float em1) {
 __device__ __forceinline__ F2 inv_beta(F2 w) { return f2(rsq(lo(w)), rsq(hi(w))); }
 __device__ __forceinline__ float inv_beta(float w) { return rsq(w); }
 
-// em1 and b = beta g x of a pair of elements (logits already floored).
+// em1 and b = beta g x of a pair of elements (logits already limited).
 __device__ __forceinline__ void gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &b) {
   const Sig v = sigmoids(r, i);
   em1 = ex2m1(mul2(k2, v.ns));
-  const F2 w = one_minus_a2(em1);
-  b = mul2(mul2(w, inv_beta(w)), mul2(mul2(v.ng, f2(-1.f)), x));
+  const F2 nw = fma2(em1, add2(em1, f2(2.f)), f2(-1e-37f));  // -w: its sign meets ng's
+  b = mul2(mul2(nw, f2(rsq(-lo(nw)), rsq(-hi(nw)))), mul2(v.ng, x));
 }
 
 // One step: a h + b.

@@ -85,17 +85,18 @@ __device__ __forceinline__ uint32_t load_raw(const bf16 *p, int live, bool word)
   if (live > 1) v |= (uint32_t)__ldg(q + 1) << 16;
   return v;
 }
-__device__ __forceinline__ void store_raw(float *p, float v, int live, bool) {
+__device__ __forceinline__ void store_raw(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_raw(bf16 *p, F2 v) {
+  *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(lo(v), hi(v));
+}
+// channels past the row's end or a pair that is not one word
+__device__ __forceinline__ void store_raw(float *p, float v, int live) {
   if (live > 0) *p = v;
 }
-__device__ __forceinline__ void store_raw(bf16 *p, F2 v, int live, bool word) {
+__device__ __forceinline__ void store_raw(bf16 *p, F2 v, int live) {
   const __nv_bfloat162 o = __floats2bfloat162_rn(lo(v), hi(v));
-  if (live > 1 && word) {
-    *reinterpret_cast<__nv_bfloat162 *>(p) = o;
-  } else {
-    if (live > 0) p[0] = o.x;
-    if (live > 1) p[1] = o.y;
-  }
+  if (live > 0) p[0] = o.x;
+  if (live > 1) p[1] = o.y;
 }
 __device__ __forceinline__ F2 bf16_pair(uint32_t v) {
   return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -184,18 +185,18 @@ __device__ __forceinline__ Aff<F2> get(const float4 *at) {
   const float4 v = *at;
   return {f2(v.x, v.y), f2(v.z, v.w)};
 }
-// the same into block `rank` of the cluster (its copy of the variable at `at`)
-__device__ __forceinline__ void put_peer(float2 *at, int rank, const Aff<float> &a) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(
-                   tc::mapa_shared(tc::smem_u32(at), rank)),
-               "f"(a.p), "f"(a.e)
-               : "memory");
+// The same into block `rank` of the cluster (its copy of *at), counted there as
+// bytes that its barrier `bar` (its copy) expects: the barrier's phase carries
+// the data's visibility, so that no fence waits for the outputs' plain stores.
+__device__ __forceinline__ void put_peer(float2 *at, uint64_t *bar, int rank, const Aff<float> &a) {
+  const uint32_t to = tc::mapa_shared(tc::smem_u32(at), rank);
+  const uint32_t b = tc::mapa_shared(tc::smem_u32(bar), rank);
+  tc::st_async_f32(to, a.p, b);
+  tc::st_async_f32(to + 4, a.e, b);
 }
-__device__ __forceinline__ void put_peer(float4 *at, int rank, const Aff<F2> &a) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                   tc::mapa_shared(tc::smem_u32(at), rank)),
-               "f"(lo(a.p)), "f"(hi(a.p)), "f"(lo(a.e)), "f"(hi(a.e))
-               : "memory");
+__device__ __forceinline__ void put_peer(float4 *at, uint64_t *bar, int rank, const Aff<F2> &a) {
+  tc::st_async_v4(tc::mapa_shared(tc::smem_u32(at), rank), lo(a.p), hi(a.p), lo(a.e), hi(a.e),
+                  tc::mapa_shared(tc::smem_u32(bar), rank));
 }
 
 // ---- host side
