@@ -117,38 +117,36 @@ struct Decode<int8_t, float> {
   }
 };
 
-// One step's gates: em1 = a - 1, nb = -beta g x, ns = -sigmoid(r), ng = -sigmoid(i).
-__device__ __forceinline__ void gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &nb, F2 &ns, F2 &ng) {
-  const Sig v = sigmoids(r, i);
-  ns = v.ns, ng = v.ng;
-  em1 = ex2m1(mul2(k2, ns));
-  const F2 w = one_minus_a2(em1);
-  nb = mul2(mul2(w, inv_beta(w)), mul2(ng, x));
-}
-template <typename IT>
+// Of each of S steps: em1 = a - 1, nb = -beta g x, ns = -sigmoid(r), ng = -sigmoid(i).
+template <typename IT, bool SMALL>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (&scale)[3][S], F2 k2,
-                                      const Limits &lim, F2 (&em1)[S], F2 (&nb)[S], F2 (&ns)[S], F2 (&ng)[S]) {
+                                      const Limits &lim, F2 (&em1)[S], F2 (&nb)[S], F2 (&ns)[S],
+                                      F2 (&ng)[S]) {
   typedef Decode<IT, F2> D;
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    gate(D::x(raw[0][s], scale[0][s]), D::r(raw[1][s], scale[1][s], lim),
-         D::i(raw[2][s], scale[2][s]), k2, em1[s], nb[s], ns[s], ng[s]);
+  for (int s = 0; s < S; ++s) {
+    const Sig v = gate<SMALL>(
+        D::x(raw[0][s], scale[0][s]),
+        SMALL ? D::i(raw[1][s], scale[1][s]) : D::r(raw[1][s], scale[1][s], lim),
+        D::i(raw[2][s], scale[2][s]), k2, em1[s], nb[s]);
+    ns[s] = v.ns, ng[s] = v.ng;
+  }
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
-template <typename IT>
+template <typename IT, bool SMALL>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (&scale)[3][S],
                                       float k2, const Limits &lim, float (&em1)[S], float (&nb)[S],
                                       float (&ns)[S], float (&ng)[S]) {
   typedef Decode<IT, float> D;
 #pragma unroll
   for (int s = 0; s < S; s += 2) {
-    F2 v[4];
-    gate(f2(D::x(raw[0][s], scale[0][s]), D::x(raw[0][s + 1], scale[0][s + 1])),
-         f2(D::r(raw[1][s], scale[1][s], lim), D::r(raw[1][s + 1], scale[1][s + 1], lim)),
-         f2(D::i(raw[2][s], scale[2][s]), D::i(raw[2][s + 1], scale[2][s + 1])), f2(k2), v[0], v[1],
-         v[2], v[3]);
-    em1[s] = lo(v[0]), nb[s] = lo(v[1]), ns[s] = lo(v[2]), ng[s] = lo(v[3]);
-    em1[s + 1] = hi(v[0]), nb[s + 1] = hi(v[1]), ns[s + 1] = hi(v[2]), ng[s + 1] = hi(v[3]);
+    F2 m, b;
+    const Sig v = gate<SMALL>(
+        f2(D::x(raw[0][s], scale[0][s]), D::x(raw[0][s + 1], scale[0][s + 1])),
+        f2(D::r(raw[1][s], scale[1][s], lim), D::r(raw[1][s + 1], scale[1][s + 1], lim)),
+        f2(D::i(raw[2][s], scale[2][s]), D::i(raw[2][s + 1], scale[2][s + 1])), f2(k2), m, b);
+    em1[s] = lo(m), nb[s] = lo(b), ns[s] = lo(v.ns), ng[s] = lo(v.ng);
+    em1[s + 1] = hi(m), nb[s + 1] = hi(b), ns[s + 1] = hi(v.ns), ng[s + 1] = hi(v.ng);
   }
 }
 
@@ -159,10 +157,11 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (
 template <typename V>
 __device__ __forceinline__ void grads(V em1, V nb, V ns, V ng, V nk, V ne, V &h, V &dx, V &dr, V &di,
                                       V &dlog_s) {
-  V one, minus;
+  V one, minus, tiny;
   set(one, 1.f);
   set(minus, -1.f);
-  const V w = one_minus_a2(em1), rb = inv_beta(w), arb = mul_v(add_v(em1, one), rb);
+  set(tiny, 1e-37f);
+  const V w = one_minus_a2(em1, tiny), rb = inv_beta(w), arb = mul_v(add_v(em1, one), rb);
   const V ah = fma_v(em1, h, h);
   dx = mul_v(ne, mul_v(mul_v(w, rb), ng));
   di = mul_v(mul_v(ne, nb), add_v(ng, one));
@@ -219,18 +218,24 @@ __global__ void __launch_bounds__(NT, PER_SM)
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
-  int used = 0, parity = 0, round = 0;
+  int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
+  V k2;
+  Limits lim;
+  bool small = false;
   for (int u = u0; u < cut.units; u += stride) {
     const Unit v = unit_of(cut, p.B, u, CW);
     const int len = row_length(p.lengths, v.b, p.T, err);
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
-    V k2, nk, nc, sum, zero, minus;
+    V nk, nc, sum, zero, minus;
     set(zero, 0.f);
     set(minus, -1.f);
-    load_v(p.lambda + ch, live, k2);
-    k2 = decay_rate2(k2, p.c);
-    const Limits lim = limits(k2);
+    if (v.c0 != held) {
+      held = v.c0;
+      rate(p.lambda + ch, p.c, live, k2);
+      lim = limits(k2);
+      small = __all_sync(0xffffffffu, small_rate(k2));
+    }
     // all three outputs move a word a lane
     const bool whole = v.c0 + CW <= p.H && (words >> 4 & 7) == 7 && p.dx.p && p.dr.p && p.di.p;
     set(nk, -1.f / LOG2E);
@@ -289,7 +294,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
           for (int s = 0; s < S; ++s)
             rawd[s] = load_raw(q + s * p.dy.st, tw + s < len ? live : 0, words >> 3 & 1);
         }
-        gates<IT>(raw, scale, k2, lim, em1, nb, ns, ng);
+        if (small) gates<IT, true>(raw, scale, k2, lim, em1, nb, ns, ng);
+        else gates<IT, false>(raw, scale, k2, lim, em1, nb, ns, ng);
 #pragma unroll
         for (int s = 0; s < S; ++s) dy[s] = Decode<T, V>::x(rawd[s], 0.f);
         if (tw + S > len) {

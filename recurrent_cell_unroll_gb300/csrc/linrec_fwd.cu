@@ -32,22 +32,26 @@ struct Smem {
 };
 
 // em1 and b of the lane's channels at each of S steps
+template <bool SMALL>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], F2 k2, const Limits &lim,
                                       F2 (&em1)[S], F2 (&in)[S]) {
 #pragma unroll
   for (int s = 0; s < S; ++s)
-    gate(bf16_pair(raw[0][s]), bf16_pair(limit_r(raw[1][s], lim)),
-         bf16_pair(floor_logit(raw[2][s])), k2, em1[s], in[s]);
+    gate_b<SMALL>(bf16_pair(raw[0][s]),
+                  bf16_pair(SMALL ? floor_logit(raw[1][s]) : limit_r(raw[1][s], lim)),
+                  bf16_pair(floor_logit(raw[2][s])), k2, em1[s], in[s]);
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
+template <bool SMALL>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, const Limits &lim,
                                       float (&em1)[S], float (&in)[S]) {
   auto at = [&](int k, int s) { return __uint_as_float(raw[k][s]); };
 #pragma unroll
   for (int s = 0; s < S; s += 2) {
     F2 m, b;
-    gate(f2(at(0, s), at(0, s + 1)), f2(limit_r(at(1, s), lim), limit_r(at(1, s + 1), lim)),
-         f2(floor_logit(at(2, s)), floor_logit(at(2, s + 1))), f2(k2), m, b);
+    gate_b<SMALL>(f2(at(0, s), at(0, s + 1)),
+                  f2(limit_r(at(1, s), lim), limit_r(at(1, s + 1), lim)),
+                  f2(floor_logit(at(2, s)), floor_logit(at(2, s + 1))), f2(k2), m, b);
     em1[s] = lo(m), em1[s + 1] = hi(m);
     in[s] = lo(b), in[s + 1] = hi(b);
   }
@@ -95,16 +99,22 @@ __global__ void __launch_bounds__(NT, PER_SM)
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
-  int used = 0, parity = 0, round = 0;
+  int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
+  V k2;
+  Limits lim;
+  bool small = false;
   for (int u = u0; u < cut.units; u += stride) {
     const Unit v = unit_of(cut, p.B, u, CW);
     const int len = row_length(p.lengths, v.b, p.T, err);
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
-    V k2, carry;
-    load_v(p.lambda + ch, live, k2);
-    k2 = decay_rate2(k2, p.c);
-    const Limits lim = limits(k2);
+    V carry;
+    if (v.c0 != held) {
+      held = v.c0;
+      rate(p.lambda + ch, p.c, live, k2);
+      lim = limits(k2);
+      small = __all_sync(0xffffffffu, small_rate(k2));
+    }
     const bool whole = v.c0 + CW <= p.H && (words >> 3 & 1);  // y moves a word a lane
     if (p.h0) load_v(p.h0 + row, live, carry);
     else set(carry, 0.f);
@@ -135,7 +145,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
               raw[k][s] = load_raw(q + s * src[k]->st, tw + s < len ? live : 0, words >> k & 1);
           }
         }
-        gates(raw, k2, lim, em1, in);
+        if (small) gates<true>(raw, k2, lim, em1, in);
+        else gates<false>(raw, k2, lim, em1, in);
         if (tw + S > len) {
 #pragma unroll
           for (int s = 0; s < S; ++s)

@@ -37,6 +37,11 @@ __device__ __forceinline__ float rcp(float v) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
+__device__ __forceinline__ float root(float v) {
+  float r;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
 __device__ __forceinline__ float rsq(float v) {
   float r;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -89,10 +94,6 @@ __device__ __forceinline__ float decay_rate2(float lambda, float c) {
   return min_nan(c * sp * LOG2E, 1e20f);
 }
 
-__device__ __forceinline__ F2 decay_rate2(F2 lambda, float c) {
-  return f2(decay_rate2(lo(lambda), c), decay_rate2(hi(lambda), c));
-}
-
 // 2^t - 1 for -126 <= t <= 0, relative error 2e-7.  t = n + f, n whole, |f| <= 1/2:
 // 2^n (2^f - 1) + (2^n - 1), with (2^f - 1) / f a polynomial of degree 5
 // fitted to the least relative error (1.1e-8 before rounding); n = 0 leaves
@@ -109,6 +110,25 @@ __device__ __forceinline__ F2 ex2m1(F2 t) {
   const F2 s = f2(__int_as_float((__float_as_int(lo(m)) << 23) + 0x3f800000),  // 2^n
                   __int_as_float((__float_as_int(hi(m)) << 23) + 0x3f800000));
   return fma2(s, mul2(p, f), add2(s, f2(-1.f)));
+}
+
+// The same for -1/2 <= t <= 0, where n is 0 for the half of them and the
+// polynomial alone reaches: a third of the operations.  Decay rates up to
+// SMALL_RATE keep t there whatever the gates do (a state remembers for two
+// steps or more at an open gate, as trained recurrences over long sequences
+// do); a warp whose channels all have such rates takes this form.
+constexpr float SMALL_RATE = 0.5f;
+__device__ __forceinline__ F2 ex2m1_small(F2 t) {
+  F2 p = f2(1.15445221e-3f);
+  p = fma2(p, t, f2(9.5412815e-3f));
+  p = fma2(p, t, f2(5.54904081e-2f));
+  p = fma2(p, t, f2(2.40225643e-1f));
+  p = fma2(p, t, f2(6.93147182e-1f));
+  return mul2(p, t);
+}
+__device__ __forceinline__ bool small_rate(float k2) { return k2 <= SMALL_RATE; }
+__device__ __forceinline__ bool small_rate(F2 k2) {
+  return lo(k2) <= SMALL_RATE && hi(k2) <= SMALL_RATE;
 }
 
 // The two sigmoids of a pair of elements, negated: ns = -1 / (1 + e^-r) makes
@@ -158,24 +178,37 @@ __device__ __forceinline__ Sig sigmoids(F2 r, F2 i) {
   return {mul2(ninv, pi), mul2(ninv, pr)};
 }
 
-// w = 1 - a^2 = em1 (-2 - em1) from em1 = a - 1.  A decay rate of 0 would make
-// it 0: the tiny addend leaves a finite 1 / sqrt(w), which every use multiplies
-// by something that is 0 then.
-__device__ __forceinline__ F2 one_minus_a2(F2 em1) {
-  return fma2(em1, fma2(em1, f2(-1.f), f2(-2.f)), f2(1e-37f));
+// w = 1 - a^2 = em1 (-2 - em1) from em1 = a - 1, and its roots.  A decay rate
+// of 0 makes w 0: where 1 / sqrt(w) is wanted a tiny addend keeps that finite,
+// and every use multiplies it by something that is 0 then.
+__device__ __forceinline__ F2 one_minus_a2(F2 em1, F2 tiny) {
+  return fma2(em1, fma2(em1, f2(-1.f), f2(-2.f)), tiny);
 }
-__device__ __forceinline__ float one_minus_a2(float em1) {
-  return fmaf(em1, -2.f - em1, 1e-37f);
+__device__ __forceinline__ float one_minus_a2(float em1, float tiny) {
+  return fmaf(em1, -2.f - em1, tiny);
 }
 __device__ __forceinline__ F2 inv_beta(F2 w) { return f2(rsq(lo(w)), rsq(hi(w))); }
 __device__ __forceinline__ float inv_beta(float w) { return rsq(w); }
 
-// em1 and b = beta g x of a pair of elements (logits already limited).
-__device__ __forceinline__ void gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &b) {
+// em1 and nb = -b = -beta g x of a pair of elements (logits already limited),
+// and the sigmoids, negated.
+template <bool SMALL>
+__device__ __forceinline__ Sig gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &nb) {
   const Sig v = sigmoids(r, i);
-  em1 = ex2m1(mul2(k2, v.ns));
-  const F2 nw = fma2(em1, add2(em1, f2(2.f)), f2(-1e-37f));  // -w: its sign meets ng's
-  b = mul2(mul2(nw, f2(rsq(-lo(nw)), rsq(-hi(nw)))), mul2(v.ng, x));
+  const F2 t = mul2(k2, v.ns);
+  em1 = SMALL ? ex2m1_small(t) : ex2m1(t);
+  const F2 w = mul2(em1, fma2(em1, f2(-1.f), f2(-2.f)));
+  nb = mul2(f2(root(lo(w)), root(hi(w))), mul2(v.ng, x));
+  return v;
+}
+// em1 and b alone
+template <bool SMALL>
+__device__ __forceinline__ void gate_b(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &b) {
+  const Sig v = sigmoids(r, i);
+  const F2 t = mul2(k2, v.ns);
+  em1 = SMALL ? ex2m1_small(t) : ex2m1(t);
+  const F2 nw = mul2(em1, add2(em1, f2(2.f)));
+  b = mul2(f2(-root(-lo(nw)), -root(-hi(nw))), mul2(v.ng, x));
 }
 
 // One step: a h + b.

@@ -138,6 +138,14 @@ __device__ __forceinline__ void store_v(float *p, F2 v, int live) {
   if (live > 1) p[1] = hi(v);
 }
 
+// the decay rates of the lane's channels (0 for one past the row's end)
+__device__ __forceinline__ void rate(const float *lambda, float c, int live, float &k2) {
+  k2 = live > 0 ? decay_rate2(lambda[0], c) : 0.f;
+}
+__device__ __forceinline__ void rate(const float *lambda, float c, int live, F2 &k2) {
+  k2 = f2(live > 0 ? decay_rate2(lambda[0], c) : 0.f, live > 1 ? decay_rate2(lambda[1], c) : 0.f);
+}
+
 // ---- affine maps h -> P h + E
 
 template <typename V>
