@@ -13,10 +13,15 @@
 using namespace rcu;
 using namespace rcu_api;
 
-struct rcu_seq_s : EventProfiler {
+struct rcu_seq_s : EventProfiler, DevMem {
   int device, nsm;
   DevBuf ctl;  // device error word
   DevBuf ws;   // partial sums of the call in flight
+  cudaError_t grow(size_t bytes, void **p) override {
+    const cudaError_t e = ws.ensure(bytes);
+    *p = ws.p;
+    return e;
+  }
   int force_path = 0;
   int launches = 0;
 };
@@ -184,9 +189,8 @@ extern "C" int rcu_linrec_forward(rcu_seq *h, int dtype, int layout, int T, int 
   const LinrecFwd p{dtype, T, B, H, seq_in(layout, T, B, x, ldx), seq_in(layout, T, B, r, ldr),
                     seq_in(layout, T, B, i, ldi), lambda, (float)c, lengths, h0,
                     seq_out(layout, T, B, y, ldy), h_n, states};
-  CU(h->ws.ensure(linrec_fwd_workspace(p, h->nsm)));
   begin(h, "linrec_forward", s);
-  CU(launch_linrec_fwd(p, h->ws.p, (int *)h->ctl.p, h->nsm, !h->force_path, s, &h->launches));
+  CU(launch_linrec_fwd(p, (int *)h->ctl.p, !h->force_path, s, &h->launches));
   h->prof_end(s);
   return RCU_OK;
 }
@@ -228,9 +232,8 @@ extern "C" int rcu_linrec_backward(rcu_seq *h, int dtype, int saved, int layout,
               seq_out(layout, T, B, dx, lddx), seq_out(layout, T, B, dr, lddr),
               seq_out(layout, T, B, di, lddi), dlambda, dh0};
   strides(layout, T, B, 1, &p.et, &p.eb);
-  CU(h->ws.ensure(linrec_bwd_workspace(p, h->nsm)));
   begin(h, "linrec_backward", s);
-  CU(launch_linrec_bwd(p, h->ws.p, (int *)h->ctl.p, h->nsm, !h->force_path, s, &h->launches));
+  CU(launch_linrec_bwd(p, *h, (int *)h->ctl.p, !h->force_path, s, &h->launches));
   h->prof_end(s);
   return RCU_OK;
 }
@@ -310,9 +313,8 @@ extern "C" int rcu_layernorm_backward(rcu_seq *h, int dtype, int saved, int64_t 
                 "rcu_layernorm_backward: exponents are required with RCU_I8 and NULL without");
   const LnBwd p{dtype, saved, rows, n, dy, u, lddy, ldu, ue, weight, mean, rstd, dsum, ldds, du,
                 lddu, dweight, dbias};
-  CU(h->ws.ensure(ln_bwd_workspace(p, h->nsm)));
   begin(h, "layernorm_backward", s);
-  CU(launch_ln_bwd(p, h->ws.p, h->nsm, !h->force_path, s, &h->launches));
+  CU(launch_ln_bwd(p, *h, h->nsm, !h->force_path, s, &h->launches));
   h->prof_end(s);
   return RCU_OK;
 }

@@ -14,11 +14,11 @@ namespace {
 
 using namespace linrec;
 
-#ifndef V_STAGES
-#define V_STAGES 2
-#define V_PER 2
-#endif
-constexpr int S = CHUNK / NW, STEPS = CHUNK, STAGES = V_STAGES, PER_SM = V_PER;
+// Eight warps of 8 steps: the tile is what one kept state covers, and 16 steps a
+// lane would need more than the 255 registers a thread can have.
+constexpr int NW = 8, NT = 32 * NW, S = CHUNK / NW, STEPS = CHUNK, STAGES = 2, PER_SM = 2;
+constexpr int MAXCS = 8;  // blocks of a cluster
+constexpr int BATCH = 4;  // pairs whose gates are computed together
 
 template <typename V>
 struct Smem {
@@ -85,9 +85,9 @@ struct Decode<int8_t, F2> {
     return f2(code_value(v & 0xffu, scale), code_value(v >> 8, scale));
   }
   __device__ __forceinline__ static F2 r(uint32_t v, float scale, const Limits &l) {
-    const F2 f = x(v, scale);  // not limited as bf16: the channels' limits, widened
+    const F2 f = i(v, scale);  // not limited as bf16: the channels' limits, widened
     const float a = __uint_as_float(l.top2 << 16), b = __uint_as_float(l.top2 & 0xffff0000u);
-    return f2(min_nan(floor_logit(lo(f)), a), min_nan(floor_logit(hi(f)), b));
+    return f2(min_nan(lo(f), a), min_nan(hi(f), b));
   }
   __device__ __forceinline__ static F2 i(uint32_t v, float scale) {
     const F2 f = x(v, scale);
@@ -124,12 +124,16 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (
                                       F2 (&ng)[S]) {
   typedef Decode<IT, F2> D;
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const Sig v = gate<SMALL>(
-        D::x(raw[0][s], scale[0][s]),
-        SMALL ? D::i(raw[1][s], scale[1][s]) : D::r(raw[1][s], scale[1][s], lim),
-        D::i(raw[2][s], scale[2][s]), k2, em1[s], nb[s]);
-    ns[s] = v.ns, ng[s] = v.ng;
+  for (int s = 0; s < S; s += BATCH) {
+    F2 x[BATCH], r[BATCH], i[BATCH];
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) {
+      const int q = s + n;
+      x[n] = D::x(raw[0][q], scale[0][q]);
+      r[n] = SMALL ? D::i(raw[1][q], scale[1][q]) : D::r(raw[1][q], scale[1][q], lim);
+      i[n] = D::i(raw[2][q], scale[2][q]);
+    }
+    gates_n<SMALL, BATCH>(x, r, i, k2, em1 + s, nb + s, ns + s, ng + s);
   }
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
@@ -139,14 +143,22 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (
                                       float (&ns)[S], float (&ng)[S]) {
   typedef Decode<IT, float> D;
 #pragma unroll
-  for (int s = 0; s < S; s += 2) {
-    F2 m, b;
-    const Sig v = gate<SMALL>(
-        f2(D::x(raw[0][s], scale[0][s]), D::x(raw[0][s + 1], scale[0][s + 1])),
-        f2(D::r(raw[1][s], scale[1][s], lim), D::r(raw[1][s + 1], scale[1][s + 1], lim)),
-        f2(D::i(raw[2][s], scale[2][s]), D::i(raw[2][s + 1], scale[2][s + 1])), f2(k2), m, b);
-    em1[s] = lo(m), nb[s] = lo(b), ns[s] = lo(v.ns), ng[s] = lo(v.ng);
-    em1[s + 1] = hi(m), nb[s + 1] = hi(b), ns[s + 1] = hi(v.ns), ng[s + 1] = hi(v.ng);
+  for (int s = 0; s < S; s += 2 * BATCH) {
+    F2 x[BATCH], r[BATCH], i[BATCH], m[BATCH], b[BATCH], vs[BATCH], vg[BATCH];
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) {
+      const int q = s + 2 * n;
+      x[n] = f2(D::x(raw[0][q], scale[0][q]), D::x(raw[0][q + 1], scale[0][q + 1]));
+      r[n] = f2(D::r(raw[1][q], scale[1][q], lim), D::r(raw[1][q + 1], scale[1][q + 1], lim));
+      i[n] = f2(D::i(raw[2][q], scale[2][q]), D::i(raw[2][q + 1], scale[2][q + 1]));
+    }
+    gates_n<SMALL, BATCH>(x, r, i, f2(k2), m, b, vs, vg);
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) {
+      const int q = s + 2 * n;
+      em1[q] = lo(m[n]), nb[q] = lo(b[n]), ns[q] = lo(vs[n]), ng[q] = lo(vg[n]);
+      em1[q + 1] = hi(m[n]), nb[q + 1] = hi(b[n]), ns[q + 1] = hi(vs[n]), ng[q + 1] = hi(vg[n]);
+    }
   }
 }
 
@@ -244,6 +256,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
     else nc = zero;
     nc = mul_v(nc, minus);  // the carry, negated: -dL/dh after the steps so far
     sum = zero;
+    V enter = zero;  // the state that enters the tile, read one tile ahead
     for (int base = v.last - 1; base >= v.first; base -= cs) {
       const int tile = base - rank, tw = tile * STEPS + warp * S;
       const bool on = tile >= v.first && tile * STEPS < len;  // the same for the whole block
@@ -374,9 +387,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
             V gx, gr, gi, gl;
             grads(em1[s], nb[s], ns[s], ng[s], nk, dy[s], h, gx, gr, gi, gl);
             part = add_v(part, gl);
-            store_raw(dx, gx);
-            store_raw(dr, gr);
-            store_raw(di, gi);
+            store_word(dx, gx);
+            store_word(dr, gr);
+            store_word(di, gi);
             dx += p.dx.st, dr += p.dr.st, di += p.di.st;
           }
         } else {
@@ -422,7 +435,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
 // dlambda[h] = -c sigmoid(lambda) * the sum of `rows` partial sums.  A warp has
 // 32 channels; its block's warps share the rows, and the shares join in order.
 constexpr int SUM_WARPS = 16;
-__global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int rows, int H,
+__global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int64_t rows, int H,
                                       const float *__restrict__ lambda, float c,
                                       float *__restrict__ dlambda) {
   __shared__ float part[SUM_WARPS][32];
@@ -430,7 +443,7 @@ __global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int row
   float s = 0.f;
   if (h < H)
 #pragma unroll 4
-    for (int b = warp; b < rows; b += SUM_WARPS) s += partial[(int64_t)b * H + h];
+    for (int64_t b = warp; b < rows; b += SUM_WARPS) s += partial[b * H + h];
   part[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && h < H) {
@@ -441,63 +454,69 @@ __global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int row
   }
 }
 
-template <typename T>
-Plan plan_bwd(const LinrecBwd &p, int nsm) {
-  return plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), nsm, PER_SM);
-}
-Plan plan_of(const LinrecBwd &p, int nsm) {
-  return p.dtype == RCU_BF16 ? plan_bwd<bf16>(p, nsm) : plan_bwd<float>(p, nsm);
-}
-
-template <typename IT, typename T>
-cudaError_t bwd(const LinrecBwd &p, float *partial, int *err, int nsm, bool vec, cudaStream_t s,
-                int *launches) {
-  constexpr int CW = Shape<T>::CW;
-  const Plan pl = plan_of(p, nsm);
+struct Maps {
   CUtensorMap m[4];
+  bool tma;
+  int words;
+};
+template <typename IT, typename T>
+Maps maps(const LinrecBwd &p, bool vec) {
+  Maps v;
   const SeqIn *in[4] = {&p.x, &p.r, &p.i, &p.dy};
   const SeqOut *out[3] = {&p.dx, &p.dr, &p.di};
-  bool tma = vec;
-  int words = 0;
+  v.tma = vec;
+  v.words = 0;
   for (int k = 0; k < 4; ++k) {
     const int bytes = k < 3 ? (int)sizeof(IT) : (int)sizeof(T);
-    tma = tma &&
-          tc_map_3d(&m[k], in[k]->p, bytes, p.H, p.B, p.T, in[k]->sb, in[k]->st, CW, 1, STEPS);
-    words |= word_aligned(in[k]->p, in[k]->st, in[k]->sb, bytes) << k;
+    v.tma = v.tma && tc_map_3d(&v.m[k], in[k]->p, bytes, p.H, p.B, p.T, in[k]->sb, in[k]->st,
+                               Shape<T>::CW, 1, STEPS);
+    v.words |= word_aligned(in[k]->p, in[k]->st, in[k]->sb, bytes) << k;
   }
   for (int k = 0; k < 3; ++k)
-    words |= word_aligned(out[k]->p, out[k]->st, out[k]->sb, sizeof(T)) << (4 + k);
-  const size_t smem =
-      sizeof(Smem<typename Lane<T>::V>) + (tma ? STAGES * stage_bytes<IT, T>() : 0);
-  cudaError_t e =
-      tma ? launch_cut(linrec_bwd_kernel<IT, T, true>, pl, smem, s, m[0], m[1], m[2], m[3], p,
-                       pl.cut, partial, words, err)
-          : launch_cut(linrec_bwd_kernel<IT, T, false>, pl, smem, s, m[0], m[1], m[2], m[3], p,
-                       pl.cut, partial, words, err);
+    v.words |= word_aligned(out[k]->p, out[k]->st, out[k]->sb, sizeof(T)) << (4 + k);
+  return v;
+}
+
+template <typename IT, typename T, bool TMA>
+cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStream_t s,
+                int *launches) {
+  constexpr size_t SMEM =
+      sizeof(Smem<typename Lane<T>::V>) + (TMA ? STAGES * stage_bytes<IT, T>() : 0);
+  static const Resident res = resident(linrec_bwd_kernel<IT, T, TMA>, NT, MAXCS, SMEM, 0);
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res);
+  const int64_t rows = (int64_t)p.B * pl.cut.nseg * pl.cs;
+  float *partial = nullptr;
+  if (p.dlambda) {
+    cudaError_t e = ws.get((size_t)rows * p.H * 4, &partial);
+    if (e != cudaSuccess) return e;
+  }
+  cudaError_t e = launch_cut(linrec_bwd_kernel<IT, T, TMA>, pl, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
+                             v.m[3], p, pl.cut, partial, v.words, err);
   ++*launches;
   if (e != cudaSuccess || !p.dlambda) return e;
-  linrec_dlambda_kernel<<<ceil_div(p.H, 32), 32 * SUM_WARPS, 0, s>>>(
-      partial, p.B * pl.cut.nseg * pl.cs, p.H, p.lambda, p.c, p.dlambda);
+  linrec_dlambda_kernel<<<ceil_div(p.H, 32), 32 * SUM_WARPS, 0, s>>>(partial, rows, p.H, p.lambda,
+                                                                     p.c, p.dlambda);
   ++*launches;
   return cudaGetLastError();
 }
 
-}  // namespace
-
-size_t linrec_bwd_workspace(const LinrecBwd &p, int nsm) {
-  const Plan pl = plan_of(p, nsm);
-  return (size_t)p.B * pl.cut.nseg * pl.cs * p.H * 4;
+template <typename IT, typename T>
+cudaError_t bwd(const LinrecBwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s, int *launches) {
+  const Maps v = maps<IT, T>(p, vec);
+  return v.tma ? run<IT, T, true>(p, v, ws, err, s, launches)
+               : run<IT, T, false>(p, v, ws, err, s, launches);
 }
 
-cudaError_t launch_linrec_bwd(const LinrecBwd &p, void *ws, int *err, int nsm, bool vec,
-                              cudaStream_t s, int *launches) {
-  float *partial = static_cast<float *>(ws);
+}  // namespace
+
+cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
+                              int *launches) {
   const bool q8 = p.saved == RCU_I8;
   if (p.dtype == RCU_BF16)
-    return q8 ? bwd<int8_t, bf16>(p, partial, err, nsm, vec, s, launches)
-              : bwd<bf16, bf16>(p, partial, err, nsm, vec, s, launches);
-  return q8 ? bwd<int8_t, float>(p, partial, err, nsm, vec, s, launches)
-            : bwd<float, float>(p, partial, err, nsm, vec, s, launches);
+    return q8 ? bwd<int8_t, bf16>(p, ws, err, vec, s, launches)
+              : bwd<bf16, bf16>(p, ws, err, vec, s, launches);
+  return q8 ? bwd<int8_t, float>(p, ws, err, vec, s, launches)
+            : bwd<float, float>(p, ws, err, vec, s, launches);
 }
 
 }  // namespace rcu

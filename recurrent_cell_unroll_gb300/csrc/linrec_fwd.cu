@@ -14,59 +14,77 @@ namespace {
 
 using namespace linrec;
 
-#ifndef V_S
-#define V_S 16
-#define V_STAGES 2
-#define V_PER 2
-#endif
-constexpr int S = V_S, STEPS = NW * S, STAGES = V_STAGES, PER_SM = V_PER;
+// Four warps of 16 steps, three blocks on an SM (168 registers a thread): of the
+// shapes tried the fastest (8 warps of 16 steps, two blocks: 207 us at bf16
+// T=512 B=256 H=1024; 8 of 8, three blocks: 224; this: 186).
+constexpr int NW = 4, NT = 32 * NW, S = 16, STEPS = NW * S, STAGES = 2, PER_SM = 3;
+constexpr int MAXCS = 12;  // blocks of a cluster: with more, their maps leave room for two on an SM
+constexpr int BATCH = 4;   // pairs whose gates are computed together
 constexpr int TILE_BYTES = STEPS * 128;
+static_assert(STEPS == CHUNK, "a tile starts from one of the kept states");
 
 template <typename V>
 struct Smem {
   typename Slot<V>::type part[2][NW][32];     // the warps' maps, by parity of the tile
-  typename Slot<V>::type peer[2][MAXCS][32];  // the cluster's blocks' maps, by parity of the round
   uint64_t full[STAGES];
   uint64_t met[2];  // every block's map of a round is here, by parity of the round
   int abort;
+  // then [2][cs][32]: the cluster's blocks' maps, by parity of the round
 };
 
-// em1 and b of the lane's channels at each of S steps
+// em1 and -b of the lane's channels at each of S steps, BATCH pairs at a time
 template <bool SMALL>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], F2 k2, const Limits &lim,
-                                      F2 (&em1)[S], F2 (&in)[S]) {
+                                      F2 (&em1)[S], F2 (&nb)[S]) {
 #pragma unroll
-  for (int s = 0; s < S; ++s)
-    gate_b<SMALL>(bf16_pair(raw[0][s]),
-                  bf16_pair(SMALL ? floor_logit(raw[1][s]) : limit_r(raw[1][s], lim)),
-                  bf16_pair(floor_logit(raw[2][s])), k2, em1[s], in[s]);
+  for (int s = 0; s < S; s += BATCH) {
+    F2 x[BATCH], r[BATCH], i[BATCH], ns[BATCH], ng[BATCH];
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) {
+      x[n] = bf16_pair(raw[0][s + n]);
+      r[n] = bf16_pair(SMALL ? floor_logit(raw[1][s + n]) : limit_r(raw[1][s + n], lim));
+      i[n] = bf16_pair(floor_logit(raw[2][s + n]));
+    }
+    gates_n<SMALL, BATCH>(x, r, i, k2, em1 + s, nb + s, ns, ng);
+  }
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
 template <bool SMALL>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, const Limits &lim,
-                                      float (&em1)[S], float (&in)[S]) {
+                                      float (&em1)[S], float (&nb)[S]) {
   auto at = [&](int k, int s) { return __uint_as_float(raw[k][s]); };
 #pragma unroll
-  for (int s = 0; s < S; s += 2) {
-    F2 m, b;
-    gate_b<SMALL>(f2(at(0, s), at(0, s + 1)),
-                  f2(limit_r(at(1, s), lim), limit_r(at(1, s + 1), lim)),
-                  f2(floor_logit(at(2, s)), floor_logit(at(2, s + 1))), f2(k2), m, b);
-    em1[s] = lo(m), em1[s + 1] = hi(m);
-    in[s] = lo(b), in[s + 1] = hi(b);
+  for (int s = 0; s < S; s += 2 * BATCH) {
+    F2 x[BATCH], r[BATCH], i[BATCH], m[BATCH], b[BATCH], ns[BATCH], ng[BATCH];
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) {
+      const int q = s + 2 * n;
+      x[n] = f2(at(0, q), at(0, q + 1));
+      r[n] = f2(limit_r(at(1, q), lim), limit_r(at(1, q + 1), lim));
+      i[n] = f2(floor_logit(at(2, q)), floor_logit(at(2, q + 1)));
+    }
+    gates_n<SMALL, BATCH>(x, r, i, f2(k2), m, b, ns, ng);
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n) {
+      em1[s + 2 * n] = lo(m[n]), em1[s + 2 * n + 1] = hi(m[n]);
+      nb[s + 2 * n] = lo(b[n]), nb[s + 2 * n + 1] = hi(b[n]);
+    }
   }
 }
 
 template <typename T, bool TMA>
 __global__ void __launch_bounds__(NT, PER_SM)
     linrec_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
-                      const __grid_constant__ CUtensorMap mi, const LinrecFwd p, const Cut cut,
+                      const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap my,
+                      const LinrecFwd p, const Cut cut,
                       const int words, int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   typedef typename Lane<T>::V V;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *ring = smem;
-  Smem<V> &sh = *reinterpret_cast<Smem<V> *>(smem + (TMA ? STAGES * 3 * TILE_BYTES : 0));
+  uint8_t *out = smem + STAGES * 3 * TILE_BYTES;  // the outputs of the tile, on their way
+  Smem<V> &sh = *reinterpret_cast<Smem<V> *>(smem + (TMA ? (STAGES * 3 + 1) * TILE_BYTES : 0));
+  typename Slot<V>::type *peers = reinterpret_cast<typename Slot<V>::type *>(&sh + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cs = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
   const int stride = gridDim.x / cs, u0 = blockIdx.x / cs;
@@ -115,13 +133,13 @@ __global__ void __launch_bounds__(NT, PER_SM)
       lim = limits(k2);
       small = __all_sync(0xffffffffu, small_rate(k2));
     }
-    const bool whole = v.c0 + CW <= p.H && (words >> 3 & 1);  // y moves a word a lane
     if (p.h0) load_v(p.h0 + row, live, carry);
     else set(carry, 0.f);
+    carry = neg_v(carry);  // the kernel has -b at hand, and so works on -h throughout
     for (int base = v.first; base < v.last; base += cs) {
       const int tile = base + rank, tw = tile * STEPS + warp * S;
       const bool on = tile < v.last && tile * STEPS < len;  // the same for the whole block
-      V em1[S], in[S];
+      V em1[S], nb[S];
       Aff<V> mine = identity<V>();
       if (on) {
         uint32_t raw[3][S];
@@ -145,16 +163,16 @@ __global__ void __launch_bounds__(NT, PER_SM)
               raw[k][s] = load_raw(q + s * src[k]->st, tw + s < len ? live : 0, words >> k & 1);
           }
         }
-        if (small) gates<true>(raw, k2, lim, em1, in);
-        else gates<false>(raw, k2, lim, em1, in);
+        if (small) gates<true>(raw, k2, lim, em1, nb);
+        else gates<false>(raw, k2, lim, em1, nb);
         if (tw + S > len) {
 #pragma unroll
           for (int s = 0; s < S; ++s)
-            if (tw + s >= len) em1[s] = in[s] = 0;  // all bits zero: 0.0 in either form
+            if (tw + s >= len) em1[s] = nb[s] = 0;  // all bits zero: 0.0 in either form
         }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          mine.e = step(em1[s], mine.e, in[s]);
+          mine.e = step(em1[s], mine.e, nb[s]);
           mine.p = fma_v(em1[s], mine.p, mine.p);
         }
       }
@@ -176,14 +194,15 @@ __global__ void __launch_bounds__(NT, PER_SM)
             if (w == warp) before = all;
             all = then(all, get(&sh.part[parity][w][lane]));
           }
-          if (warp < cs)
-            put_peer(&sh.peer[round & 1][rank][lane], &sh.met[round & 1], warp, all);
+          typename Slot<V>::type *now = peers + (round & 1) * cs * 32 + lane;
+          for (int q = warp; q < cs; q += NW)
+            put_peer(now + rank * 32, &sh.met[round & 1], q, all);
           tc::mbar_wait_cluster(&sh.met[round & 1], round >> 1 & 1, err, &sh.abort, WAIT_NS);
 #pragma unroll
           for (int q = 0; q < MAXCS; ++q)
             if (q < cs) {
               if (q == rank) h = carry;
-              carry = apply(get(&sh.peer[round & 1][q][lane]), carry);
+              carry = apply(get(now + q * 32), carry);
             }
           ++round;
         }
@@ -199,63 +218,81 @@ __global__ void __launch_bounds__(NT, PER_SM)
         parity ^= 1;
       }
       if (tile >= v.last) continue;
-      if (p.states && warp % (CHUNK / S) == 0 && tw < p.T)
-        store_v(p.states + (int64_t)(tw / CHUNK) * p.B * p.H + row, h, live);
-      T *y = static_cast<T *>(p.y.p) + tw * p.y.st + v.b * p.y.sb + ch;
-      if (whole && on && tw + S <= len) {
+      if (warp == 0 && p.states)
+        store_v(p.states + (int64_t)tile * p.B * p.H + row, neg_v(h), live);
+      if (TMA) {
+        uint32_t *to = reinterpret_cast<uint32_t *>(out + warp * S * 128) + lane;
+        if (lane == 0) store_wait_read();
+        __syncwarp();
+        if (on && tw + S <= len) {
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-          h = step(em1[s], h, in[s]);
-          store_raw(y, h);
-          y += p.y.st;
+          for (int s = 0; s < S; ++s) {
+            h = step(em1[s], h, nb[s]);
+            to[s * 32] = pack(neg_v(h));
+          }
+        } else {
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            if (on) h = step(em1[s], h, nb[s]);
+            to[s * 32] = tw + s < len ? pack(neg_v(h)) : 0u;
+          }
+        }
+        fence_async_proxy();
+        __syncwarp();
+        if (lane == 0 && tw < p.T) {
+          tma_store_3d(&my, to, v.c0, v.b, tw);
+          store_commit();
         }
       } else {
+        T *y = static_cast<T *>(p.y.p) + tw * p.y.st + v.b * p.y.sb + ch;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          if (on) h = step(em1[s], h, in[s]);
-          const V out = tw + s < len ? h : V(0);
-          if (tw + s < p.T) {
-            if (whole) store_raw(y, out);
-            else store_raw(y, out, live);
-          }
+          if (on) h = step(em1[s], h, nb[s]);
+          if (tw + s < p.T)
+            store_raw(y, tw + s < len ? neg_v(h) : V(0), live, words >> 3 & 1);
           y += p.y.st;
         }
       }
     }
-    if (rank == 0 && warp == 0 && p.h_n) store_v(p.h_n + row, carry, live);
+    if (rank == 0 && warp == 0 && p.h_n) store_v(p.h_n + row, neg_v(carry), live);
   }
+  if (TMA && lane == 0) store_wait();
   if (cs > 1) tc::cluster_sync();  // no block leaves while a peer may still write to it
 }
 
+template <typename T, bool TMA>
+cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], int words, int *err,
+                cudaStream_t s) {
+  typedef typename Lane<T>::V V;
+  constexpr size_t SMEM0 = sizeof(Smem<V>) + (TMA ? (STAGES * 3 + 1) * TILE_BYTES : 0);
+  constexpr size_t SMEM_PER_CS = 2 * 32 * sizeof(Aff<V>);
+  static const Resident res =
+      resident(linrec_fwd_kernel<T, TMA>, NT, MAXCS, SMEM0, SMEM_PER_CS);
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res);
+  return launch_cut(linrec_fwd_kernel<T, TMA>, pl, NT, SMEM0 + pl.cs * SMEM_PER_CS, s, m[0], m[1],
+                    m[2], m[3], p, pl.cut, words, err);
+}
+
 template <typename T>
-cudaError_t fwd(const LinrecFwd &p, int *err, int nsm, bool vec, cudaStream_t s, int *launches) {
-  constexpr int CW = Shape<T>::CW;
-  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, CW), nsm, PER_SM);
-  CUtensorMap m[3];
-  const SeqIn *in[3] = {&p.x, &p.r, &p.i};
+cudaError_t fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s) {
+  CUtensorMap m[4];
+  const SeqIn y{p.y.p, p.y.st, p.y.sb, nullptr}, *at[4] = {&p.x, &p.r, &p.i, &y};
   bool tma = vec;
-  int words = word_aligned(p.y.p, p.y.st, p.y.sb, sizeof(T)) << 3;
-  for (int k = 0; k < 3; ++k) {
-    tma = tma && tc_map_3d(&m[k], in[k]->p, sizeof(T), p.H, p.B, p.T, in[k]->sb, in[k]->st, CW, 1,
-                           STEPS);
-    words |= word_aligned(in[k]->p, in[k]->st, in[k]->sb, sizeof(T)) << k;
+  int words = 0;
+  for (int k = 0; k < 4; ++k) {
+    tma = tma && tc_map_3d(&m[k], at[k]->p, sizeof(T), p.H, p.B, p.T, at[k]->sb, at[k]->st,
+                           Shape<T>::CW, 1, k < 3 ? STEPS : S);
+    words |= word_aligned(at[k]->p, at[k]->st, at[k]->sb, sizeof(T)) << k;
   }
-  const size_t smem = sizeof(Smem<typename Lane<T>::V>) + (tma ? STAGES * 3 * TILE_BYTES : 0);
-  ++*launches;
-  return tma ? launch_cut(linrec_fwd_kernel<T, true>, pl, smem, s, m[0], m[1], m[2], p, pl.cut,
-                          words, err)
-             : launch_cut(linrec_fwd_kernel<T, false>, pl, smem, s, m[0], m[1], m[2], p, pl.cut,
-                          words, err);
+  return tma ? run<T, true>(p, m, words, err, s) : run<T, false>(p, m, words, err, s);
 }
 
 }  // namespace
 
-size_t linrec_fwd_workspace(const LinrecFwd &, int) { return 0; }
-
-cudaError_t launch_linrec_fwd(const LinrecFwd &p, void *, int *err, int nsm, bool vec,
-                              cudaStream_t s, int *launches) {
-  return p.dtype == RCU_BF16 ? fwd<bf16>(p, err, nsm, vec, s, launches)
-                             : fwd<float>(p, err, nsm, vec, s, launches);
+cudaError_t launch_linrec_fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s,
+                              int *launches) {
+  ++*launches;
+  return p.dtype == RCU_BF16 ? fwd<bf16>(p, err, vec, s) : fwd<float>(p, err, vec, s);
 }
 
 }  // namespace rcu

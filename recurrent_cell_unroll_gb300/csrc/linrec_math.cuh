@@ -12,10 +12,8 @@
 // measured as an error of 7e-6 in dh0, against 1e-6 in this form.
 //
 // The forward in bf16 moves 8 bytes an element, which leaves an SM about 0.34
-// cycles for it: a direct evaluation's six special-function operations (16 a
-// cycle) alone would take 0.38.  So the two sigmoids share one reciprocal and
-// expm1 is a polynomial on the FMA units; two exponentials, a reciprocal and a
-// reciprocal root remain.
+// cycles for it, or 43 issue slots: every operation counts.  So arithmetic runs
+// as packed pairs, and expm1 is a polynomial on the FMA units.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -118,47 +116,45 @@ __device__ __forceinline__ F2 ex2m1(F2 t) {
 // steps or more at an open gate, as trained recurrences over long sequences
 // do); a warp whose channels all have such rates takes this form.
 constexpr float SMALL_RATE = 0.5f;
-__device__ __forceinline__ F2 ex2m1_small(F2 t) {
-  F2 p = f2(1.15445221e-3f);
-  p = fma2(p, t, f2(9.5412815e-3f));
-  p = fma2(p, t, f2(5.54904081e-2f));
-  p = fma2(p, t, f2(2.40225643e-1f));
-  p = fma2(p, t, f2(6.93147182e-1f));
-  return mul2(p, t);
+template <int N>
+__device__ __forceinline__ void ex2m1_small(const F2 (&t)[N], F2 *v) {
+  const F2 c[4] = {f2(9.5412815e-3f), f2(5.54904081e-2f), f2(2.40225643e-1f), f2(6.93147182e-1f)};
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = f2(1.15445221e-3f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = fma2(v[n], t[n], c[k]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) v[n] = mul2(v[n], t[n]);
 }
 __device__ __forceinline__ bool small_rate(float k2) { return k2 <= SMALL_RATE; }
 __device__ __forceinline__ bool small_rate(F2 k2) {
   return lo(k2) <= SMALL_RATE && hi(k2) <= SMALL_RATE;
 }
 
-// The two sigmoids of a pair of elements, negated: ns = -1 / (1 + e^-r) makes
-// the decay's exponent k2 ns, and the signs of the others cancel in products.
-// Logits stop at -42, where e^-r is 2^60.6 and the product of the denominators
-// still a normal number: a sigmoid below 6e-19 is held there.  r also stops
-// where a reaches 2^-100 (r_ceiling of the channel's rate): the state it would
-// still pass on is below any rounding, and ex2m1 keeps its range.  A NaN stays
-// one.  bf16 logits are limited as packed pairs, two at a time.
-struct Sig {
-  F2 ns, ng;
-};
+// The two sigmoids share one reciprocal, of the product of their denominators:
+// logits stop at -42, where e^42 = 2^60.6 keeps that product a normal number and
+// a sigmoid is 6e-19.  r above r_ceiling of its channel's rate, where a is 2^-100,
+// is taken as that: what the state would still pass on is below any rounding, and
+// ex2m1 keeps its range (SMALL_RATE needs no ceiling).  A NaN stays one.  bf16
+// logits are limited as packed pairs, two at a time.
 constexpr float LOGIT_FLOOR = -42.f;
 __device__ __forceinline__ float r_ceiling(float k2) {
   const float s = 100.f / k2;  // sigmoid(r) at the limit
   return s < 1.f ? fmaxf(logf(s / (1.f - s)), LOGIT_FLOOR) : __int_as_float(0x7f800000);
 }
-struct Limits {
-  float top;       // fp32: of the lane's channel
-  uint32_t top2;   // bf16: of its two channels
-};
 __device__ __forceinline__ float floor_logit(float v) { return max_nan(v, LOGIT_FLOOR); }
 __device__ __forceinline__ uint32_t floor_logit(uint32_t v) {  // bf16 -42 = 0xc228
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0xc228c228u));
   return r;
 }
-__device__ __forceinline__ float limit_r(float v, const Limits &l) {
-  return min_nan(floor_logit(v), l.top);
-}
+struct Limits {
+  float top;       // fp32: of the lane's channel
+  uint32_t top2;   // bf16: of its two channels
+};
+__device__ __forceinline__ float limit_r(float v, const Limits &l) { return min_nan(floor_logit(v), l.top); }
 __device__ __forceinline__ uint32_t limit_r(uint32_t v, const Limits &l) {
   uint32_t r;
   asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(floor_logit(v)), "r"(l.top2));
@@ -166,16 +162,9 @@ __device__ __forceinline__ uint32_t limit_r(uint32_t v, const Limits &l) {
 }
 __device__ __forceinline__ Limits limits(float k2) { return {r_ceiling(k2), 0u}; }
 __device__ __forceinline__ Limits limits(F2 k2) {
-  // rounded towards zero: 2^-100 by a percent or so
+  // rounded towards zero: a's exponent at the limit moves by a percent or so
   const float a = r_ceiling(lo(k2)), b = r_ceiling(hi(k2));
   return {0.f, (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u)};
-}
-__device__ __forceinline__ Sig sigmoids(F2 r, F2 i) {
-  const F2 tr = mul2(r, f2(-LOG2E)), ti = mul2(i, f2(-LOG2E));
-  const F2 pr = add2(f2(ex2(lo(tr)), ex2(hi(tr))), f2(1.f));
-  const F2 pi = add2(f2(ex2(lo(ti)), ex2(hi(ti))), f2(1.f));
-  const F2 d = mul2(pr, pi), ninv = f2(rcp(-lo(d)), rcp(-hi(d)));
-  return {mul2(ninv, pi), mul2(ninv, pr)};
 }
 
 // w = 1 - a^2 = em1 (-2 - em1) from em1 = a - 1, and its roots.  A decay rate
@@ -190,28 +179,55 @@ __device__ __forceinline__ float one_minus_a2(float em1, float tiny) {
 __device__ __forceinline__ F2 inv_beta(F2 w) { return f2(rsq(lo(w)), rsq(hi(w))); }
 __device__ __forceinline__ float inv_beta(float w) { return rsq(w); }
 
-// em1 and nb = -b = -beta g x of a pair of elements (logits already limited),
-// and the sigmoids, negated.
-template <bool SMALL>
-__device__ __forceinline__ Sig gate(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &nb) {
-  const Sig v = sigmoids(r, i);
-  const F2 t = mul2(k2, v.ns);
-  em1 = SMALL ? ex2m1_small(t) : ex2m1(t);
-  const F2 w = mul2(em1, fma2(em1, f2(-1.f), f2(-2.f)));
-  nb = mul2(f2(root(lo(w)), root(hi(w))), mul2(v.ng, x));
-  return v;
-}
-// em1 and b alone
-template <bool SMALL>
-__device__ __forceinline__ void gate_b(F2 x, F2 r, F2 i, F2 k2, F2 &em1, F2 &b) {
-  const Sig v = sigmoids(r, i);
-  const F2 t = mul2(k2, v.ns);
-  em1 = SMALL ? ex2m1_small(t) : ex2m1(t);
-  const F2 nw = mul2(em1, add2(em1, f2(2.f)));
-  b = mul2(f2(-root(-lo(nw)), -root(-hi(nw))), mul2(v.ng, x));
+// Of N pairs of elements (logits already limited): em1 = a - 1, nb = -beta g x,
+// and the sigmoids negated (ns makes the decay's exponent k2 ns; the other signs
+// cancel in products).
+// Written stage by stage over the N pairs: each stage's operations are
+// independent, and a warp has few others to hide the latency of a chain of
+// twenty dependent ones behind.
+template <bool SMALL, int N>
+__device__ __forceinline__ void gates_n(const F2 (&x)[N], const F2 (&r)[N], const F2 (&i)[N],
+                                        F2 k2, F2 *em1, F2 *nb, F2 *ns, F2 *ng) {
+  F2 pr[N], pi[N], t[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    pr[n] = mul2(r[n], f2(-LOG2E));
+    pi[n] = mul2(i[n], f2(-LOG2E));
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    pr[n] = f2(ex2(lo(pr[n])), ex2(hi(pr[n])));
+    pi[n] = f2(ex2(lo(pi[n])), ex2(hi(pi[n])));
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    pr[n] = add2(pr[n], f2(1.f));
+    pi[n] = add2(pi[n], f2(1.f));
+    t[n] = mul2(pr[n], pi[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) t[n] = f2(rcp(-lo(t[n])), rcp(-hi(t[n])));
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    ns[n] = mul2(t[n], pi[n]);
+    ng[n] = mul2(t[n], pr[n]);
+    t[n] = mul2(k2, ns[n]);
+  }
+  if (SMALL) {
+    ex2m1_small<N>(t, em1);
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n) em1[n] = ex2m1(t[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) t[n] = mul2(em1[n], fma2(em1[n], f2(-1.f), f2(-2.f)));
+#pragma unroll
+  for (int n = 0; n < N; ++n) t[n] = f2(root(lo(t[n])), root(hi(t[n])));
+#pragma unroll
+  for (int n = 0; n < N; ++n) nb[n] = mul2(t[n], mul2(ng[n], x[n]));
 }
 
-// One step: a h + b.
+// One step, a h + b, on the negated state and input: -h moves like h.
 __device__ __forceinline__ F2 step(F2 em1, F2 h, F2 b) { return add2(h, fma2(em1, h, b)); }
 __device__ __forceinline__ float step(float em1, float h, float b) { return h + fmaf(em1, h, b); }
 

@@ -24,11 +24,13 @@ __global__ void linrec_step_kernel(int B, int H, const T *x, int64_t ldx, const 
   }
   float out = 0.f;
   if (row >= 0) {
-    F2 em1, in;
     const float k2 = decay_rate2(lambda[h], c);
-    gate_b<false>(f2(to_f(x[b * ldx + h])), f2(limit_r(to_f(r[b * ldr + h]), limits(k2))),
-                  f2(floor_logit(to_f(i[b * ldi + h]))), f2(k2), em1, in);
-    out = state[row * H + h] = step(lo(em1), state[row * H + h], lo(in));
+    const F2 vx[1] = {f2(to_f(x[b * ldx + h]))};
+    const F2 vr[1] = {f2(limit_r(to_f(r[b * ldr + h]), limits(k2)))};
+    const F2 vi[1] = {f2(to_f(i[b * ldi + h]))};
+    F2 em1, nb, ns, ng;
+    gates_n<false, 1>(vx, vr, vi, f2(k2), &em1, &nb, &ns, &ng);
+    out = state[row * H + h] = step(lo(em1), state[row * H + h], -lo(nb));
   }
   y[b * ldy + h] = from_f<T>(out);
 }

@@ -3,7 +3,7 @@
 // clusters, and how a tile's values and the affine maps of its steps move.
 //
 // A block of NW warps takes a tile of NW * S steps x CW channels of one batch
-// row; CW values of the tensors' type are 128 bytes, so that a step of a tile
+// row (NW, S: the kernel's own); CW values of the tensors' type are 128 bytes, so that a step of a tile
 // is one full line.  Warp w has the steps [w * S, w * S + S), lane l the CPT
 // channels from l * CPT.  A step is h -> a h + b, and steps compose to affine
 // maps h -> P h + E: each warp reduces its steps to a map, the maps are chained
@@ -26,8 +26,6 @@ using bf16 = __nv_bfloat16;
 
 constexpr int CHUNK = RCU_LINREC_CHUNK;
 constexpr int BLOCK8 = RCU_ACT8_BLOCK;
-constexpr int NW = 8, NT = 32 * NW;
-constexpr int MAXCS = 8;                     // blocks of a cluster (the portable limit)
 constexpr uint64_t WAIT_NS = 2000000000ull;  // bound on any wait for a copy
 
 template <typename T>
@@ -72,6 +70,30 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
       : "memory");
 }
 
+// A warp's S steps from shared memory (written by all its lanes, a step 128
+// bytes) to the tensor: rows and channels past its ends are left out.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, const void *src, int x, int y,
+                                             int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(tc::smem_u32(src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// every committed store of this thread has read its source / has been written
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void store_wait() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async_proxy() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // ---- one lane's values of a step, as they lie in memory (CPT of them)
 
 // fp32: one channel; bf16: two, as one word where the address allows
@@ -85,11 +107,19 @@ __device__ __forceinline__ uint32_t load_raw(const bf16 *p, int live, bool word)
   if (live > 1) v |= (uint32_t)__ldg(q + 1) << 16;
   return v;
 }
-__device__ __forceinline__ void store_raw(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store_raw(bf16 *p, F2 v) {
-  *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(lo(v), hi(v));
+__device__ __forceinline__ void store_raw(float *p, float v, int live, bool) {
+  if (live > 0) *p = v;
 }
-// channels past the row's end or a pair that is not one word
+__device__ __forceinline__ void store_raw(bf16 *p, F2 v, int live, bool word) {
+  const __nv_bfloat162 o = __floats2bfloat162_rn(lo(v), hi(v));
+  if (live > 1 && word) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = o;
+  } else {
+    if (live > 0) p[0] = o.x;
+    if (live > 1) p[1] = o.y;
+  }
+}
+// channels past the row's end, or a pair that is not one word
 __device__ __forceinline__ void store_raw(float *p, float v, int live) {
   if (live > 0) *p = v;
 }
@@ -97,6 +127,17 @@ __device__ __forceinline__ void store_raw(bf16 *p, F2 v, int live) {
   const __nv_bfloat162 o = __floats2bfloat162_rn(lo(v), hi(v));
   if (live > 0) p[0] = o.x;
   if (live > 1) p[1] = o.y;
+}
+// a whole word
+__device__ __forceinline__ void store_word(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_word(bf16 *p, F2 v) {
+  *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(lo(v), hi(v));
+}
+// a lane's word of a step, for shared memory
+__device__ __forceinline__ uint32_t pack(float v) { return __float_as_uint(v); }
+__device__ __forceinline__ uint32_t pack(F2 v) {
+  const __nv_bfloat162 o = __floats2bfloat162_rn(lo(v), hi(v));
+  return *reinterpret_cast<const uint32_t *>(&o);
 }
 __device__ __forceinline__ F2 bf16_pair(uint32_t v) {
   return f2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -120,6 +161,8 @@ __device__ __forceinline__ float add_v(float a, float b) { return a + b; }
 __device__ __forceinline__ F2 add_v(F2 a, F2 b) { return add2(a, b); }
 __device__ __forceinline__ float mul_v(float a, float b) { return a * b; }
 __device__ __forceinline__ F2 mul_v(F2 a, F2 b) { return mul2(a, b); }
+__device__ __forceinline__ float neg_v(float a) { return -a; }
+__device__ __forceinline__ F2 neg_v(F2 a) { return f2(-lo(a), -hi(a)); }
 __device__ __forceinline__ void set(float &v, float c) { v = c; }
 __device__ __forceinline__ void set(F2 &v, float c) { v = f2(c); }
 
@@ -218,31 +261,75 @@ struct Plan {
   int cs, grid;
 };
 
+// How many clusters of each size a kernel can have resident (size 1: blocks).
+struct Resident {
+  static constexpr int MAX = 16;
+  int clusters[MAX + 1] = {};
+};
+template <typename... KArgs>
+Resident resident(void (*fn)(KArgs...), int threads, int max_cs, size_t smem0, size_t smem_per_cs) {
+  Resident r;
+  int dev = 0, nsm = 0, blocks = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  const size_t most = smem0 + max_cs * smem_per_cs;
+  cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (max_cs > 8)
+    cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, fn, threads, smem0 + smem_per_cs);
+  r.clusters[1] = std::max(1, blocks * nsm);
+  for (int cs = 2; cs <= max_cs; ++cs) {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at;
+    cfg.gridDim = dim3(cs);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem0 + cs * smem_per_cs;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&r.clusters[cs], fn, &cfg) != cudaSuccess)
+      r.clusters[cs] = 0;
+  }
+  cudaGetLastError();  // a size the GPU has no room for is no error of the call
+  return r;
+}
+
 // How the recurrence over `tiles` tiles of B rows x `groups` channel groups is
-// cut for a kernel of which per_sm blocks run on an SM.
-inline Plan plan_cut(int tiles, int B, int groups, int nsm, int per_sm) {
+// cut: the cluster size that needs the fewest turns, a turn being one tile a
+// block.  A larger cluster splits a sequence further, which pays where there
+// are fewer rows than blocks (or a last, thin wave of them), and costs its
+// blocks' exchange and their waiting for one another, some three tenths of a turn
+// (backward from 8 bits, T=1000 B=32 H=1024: 145 us without clusters, 159 in
+// pairs, though 16 turns each; 32 rows of 65536 steps forward: 250 us with 12
+// blocks a row, 290 with 8).
+inline Plan plan_cut(int tiles, int B, int groups, const Resident &res) {
   Plan pl;
-  const int64_t slots = (int64_t)nsm * per_sm, rows = (int64_t)B * groups;
+  const int64_t rows = (int64_t)B * groups;
+  double best = 0;
+  pl.cs = 1;
+  for (int cs = 1; cs <= Resident::MAX && cs <= tiles; ++cs) {
+    if (res.clusters[cs] < 1) continue;
+    const double waves = (double)((rows + res.clusters[cs] - 1) / res.clusters[cs]);
+    const double cost = waves * ceil_div(tiles, cs) * (cs > 1 ? 1.3 : 1.0);
+    if (cs == 1 || cost < best) best = cost, pl.cs = cs;
+  }
   pl.cut.groups = groups;
   pl.cut.tiles = tiles;
-  pl.cs = 1;
   pl.cut.nseg = 1;
-  while (pl.cs < MAXCS && rows * pl.cs * 2 <= slots && pl.cs < tiles) pl.cs *= 2;
   pl.cut.tps = ceil_div(tiles, pl.cut.nseg);
   pl.cut.units = (int)(rows * pl.cut.nseg);
-  pl.grid = (int)std::min<int64_t>((int64_t)pl.cut.units * pl.cs, slots / pl.cs * pl.cs);
+  pl.grid = (int)std::min<int64_t>(pl.cut.units, res.clusters[pl.cs]) * pl.cs;
   return pl;
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cut(void (*fn)(KArgs...), const Plan &pl, size_t smem, cudaStream_t s,
-                       Args... args) {
-  cudaError_t e =
-      cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_cut(void (*fn)(KArgs...), const Plan &pl, int threads, size_t smem,
+                       cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(pl.grid);
-  cfg.blockDim = dim3(NT);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at;

@@ -47,13 +47,23 @@ struct LinrecBwd {
   float *dlambda, *dh0;
 };
 
-// Device memory the call may use: bytes needed, then the launch with it.
-size_t linrec_fwd_workspace(const LinrecFwd &p, int nsm);
-cudaError_t launch_linrec_fwd(const LinrecFwd &p, void *ws, int *err, int nsm, bool vec,
-                              cudaStream_t s, int *launches);
-size_t linrec_bwd_workspace(const LinrecBwd &p, int nsm);
-cudaError_t launch_linrec_bwd(const LinrecBwd &p, void *ws, int *err, int nsm, bool vec,
-                              cudaStream_t s, int *launches);
+// Device memory that a call may use between its launches; it grows on demand
+// and is the handle's.
+struct DevMem {
+  virtual cudaError_t grow(size_t bytes, void **p) = 0;
+  template <typename T>
+  cudaError_t get(size_t bytes, T **p) {
+    void *v = nullptr;
+    const cudaError_t e = grow(bytes, &v);
+    *p = static_cast<T *>(v);
+    return e;
+  }
+};
+
+cudaError_t launch_linrec_fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s,
+                              int *launches);
+cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
+                              int *launches);
 cudaError_t launch_linrec_step(int dtype, int B, int H, const void *x, int64_t ldx, const void *r,
                                int64_t ldr, const void *i, int64_t ldi, const float *lambda,
                                float c, float *state, int slots, const int32_t *slot, void *y,
@@ -86,8 +96,7 @@ struct LnBwd {
   float *dweight, *dbias;
 };
 cudaError_t launch_ln_fwd(const LnFwd &p, int nsm, bool vec, cudaStream_t s, int *launches);
-size_t ln_bwd_workspace(const LnBwd &p, int nsm);
-cudaError_t launch_ln_bwd(const LnBwd &p, void *ws, int nsm, bool vec, cudaStream_t s,
+cudaError_t launch_ln_bwd(const LnBwd &p, DevMem &ws, int nsm, bool vec, cudaStream_t s,
                           int *launches);
 
 cudaError_t launch_act8_pack(int dtype, int64_t rows, int n, const void *x, int64_t ldx,
