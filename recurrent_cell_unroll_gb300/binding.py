@@ -713,77 +713,81 @@ class SeqOps:
         self.h = h
 
     # ---- arguments
+    #
+    # A call on small tensors is bound by this marshalling, so each operand takes
+    # one pass of cheap checks; what does not pass them goes to _refuse_or_copy.
+    # A copy stays alive in `keep` until the call is enqueued (its memory is then
+    # reused in stream order).
 
-    def _on(self, t, name):
+    def _refuse_or_copy(self, t, name, dtype, shape, keep):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a tensor on a CUDA device")
         if t.get_device() != self.device:
             raise ValueError(f"{name} is on cuda:{t.get_device()}, the handle on "
                              f"cuda:{self.device}")
-
-    def _data(self, t, name):
-        """The RCU_* type of a matrix operand."""
-        self._on(t, name)
-        dtype = self._DTYPES.get(t.dtype)
-        if dtype is None:
-            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
-        return dtype
-
-    def _rows(self, t, name, dtype, shape):
-        """A matrix operand as (kept tensor, pointer, row stride)."""
-        self._on(t, name)
         if t.dtype != dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
         if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if t.is_contiguous():
-            return t, t.data_ptr(), shape[-1]
-        st = t.stride()
-        if len(st) > 1 and st[-1] == 1 and st[-2] >= shape[-1] and all(
-                st[k] == st[k + 1] * shape[k + 1] for k in range(len(st) - 2)):
-            return t, t.data_ptr(), st[-2]
         t = t.clone(memory_format=torch.contiguous_format)
-        return t, t.data_ptr(), shape[-1]
+        keep.append(t)
+        return t
 
-    def _dense(self, t, name, shape, dtype=torch.float32):
-        """A dense operand as (kept tensor, pointer); None stays NULL."""
+    def _dense(self, t, name, dtype, shape, keep):
+        """Pointer of a dense operand; None stays NULL."""
         if t is None:
-            return None, None
-        self._on(t, name)
-        if t.dtype != dtype:
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if not t.is_contiguous():
-            t = t.clone(memory_format=torch.contiguous_format)
-        return t, t.data_ptr()
+            return None
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                and t.get_device() == self.device and t.is_contiguous()):
+            t = self._refuse_or_copy(t, name, dtype, shape, keep)
+        return t.data_ptr()
 
-    def _saved(self, t, name, dtype, shape):
-        """A backward's saved input, a tensor or an 8-bit checkpoint: (kept,
-        pointer, row stride, exponents' pointer)."""
+    def _rows(self, t, name, dtype, shape, keep):
+        """(pointer, row stride) of a matrix operand: in place where its rows
+        are dense and evenly spaced."""
+        if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+                and t.get_device() == self.device):
+            if t.is_contiguous():
+                return t.data_ptr(), shape[-1]
+            st = t.stride()
+            if len(st) > 1 and st[-1] == 1 and st[-2] >= shape[-1] and all(
+                    st[k] == st[k + 1] * shape[k + 1] for k in range(len(st) - 2)):
+                return t.data_ptr(), st[-2]
+        return self._refuse_or_copy(t, name, dtype, shape, keep).data_ptr(), shape[-1]
+
+    def _saved(self, t, name, dtype, shape, keep):
+        """(pointer, row stride, exponents' pointer) of a backward's saved
+        input: a tensor, or an 8-bit checkpoint (codes, exponents)."""
         if isinstance(t, torch.Tensor):
-            return (*self._rows(t, name, dtype, shape), None)
+            return (*self._rows(t, name, dtype, shape, keep), None)
         codes, exps = t
-        c = self._rows(codes, name + "'s codes", torch.int8, shape)
-        e = self._dense(exps, name + "'s exponents", (*shape[:-1], -(-shape[-1] // RCU_ACT8_BLOCK)),
-                        torch.int8)
-        return (c[0], e[0]), c[1], c[2], e[1]
+        return (*self._rows(codes, name + "'s codes", torch.int8, shape, keep),
+                self._dense(exps, name + "'s exponents", torch.int8,
+                            (*shape[:-1], -(-shape[-1] // RCU_ACT8_BLOCK)), keep))
 
-    def _run(self, stream, call):
-        """call(raw stream) with `stream` (None: the current one) as the
-        current stream, so that its allocations belong to it."""
-        if stream is None:
-            return call(torch._C._cuda_getCurrentRawStream(self.device))
+    def _type(self, t, name, dims=None):
+        """(torch dtype, RCU_* type, shape) of the operand that sets them."""
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a tensor on a CUDA device")
+        shape = t.shape
+        dt = self._DTYPES.get(t.dtype)
+        if dt is None:
+            raise ValueError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+        if len(shape) != dims if dims else len(shape) < 1:
+            raise ValueError(f"{name} must have {dims or 'at least one'} dimensions, "
+                             f"got {list(shape)}")
+        return t.dtype, dt, shape
+
+    def _on_stream(self, stream, call, *args):
+        """The call with `stream` as the current stream, so that what it
+        allocates belongs to it."""
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=self.device)
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call(*args)
 
-    @staticmethod
-    def _tbh(shape, batch_first):
-        if len(shape) != 3:
-            raise ValueError(f"x must have three dimensions, got {list(shape)}")
-        return (shape[1], shape[0], shape[2]) if batch_first else tuple(shape)
+    def _raw_stream(self):
+        return torch._C._cuda_getCurrentRawStream(self.device)
 
     # ---- gated linear recurrence
 
@@ -792,162 +796,173 @@ class SeqOps:
         """y, h_n and, with states=True, what linrec_backward needs (else
         None).  x, r, i: [T, B, H] (batch_first: [B, T, H]); lam [H]; lengths
         int32 [B]; h0 [B, H]."""
-        dt = self._data(x, "x")
-        T, B, H = self._tbh(x.shape, batch_first)
-
-        def call(s):
-            xs, rs, is_ = (self._rows(t, k, x.dtype, x.shape)
-                           for k, t in (("x", x), ("r", r), ("i", i)))
-            lm = self._dense(lam, "lam", (H,))
-            ln = self._dense(lengths, "lengths", (B,), torch.int32)
-            hs = self._dense(h0, "h0", (B, H))
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            h_n = torch.empty((B, H), device=x.device)
-            st = torch.empty((-(-T // RCU_LINREC_CHUNK), B, H), device=x.device) if states else None
-            _check(self.lib.rcu_linrec_forward(
-                self.h, dt, RCU_BATCH_FIRST if batch_first else RCU_TIME_FIRST, T, B, H, xs[1],
-                xs[2], rs[1], rs[2], is_[1], is_[2], lm[1], c, ln[1], hs[1], y.data_ptr(), H,
-                h_n.data_ptr(), st.data_ptr() if states else None, s))
-            return y, h_n, st
-        return self._run(stream, call)
+        if stream is not None:
+            return self._on_stream(stream, self.linrec_forward, x, r, i, lam, c, lengths, h0,
+                                   batch_first, states)
+        dtype, dt, shape = self._type(x, "x", 3)
+        T, B, H = shape
+        if batch_first:
+            T, B = B, T
+        keep, f32, dev = [], torch.float32, x.device
+        xp, xl = self._rows(x, "x", dtype, shape, keep)
+        rp, rl = self._rows(r, "r", dtype, shape, keep)
+        ip, il = self._rows(i, "i", dtype, shape, keep)
+        lp = self._dense(lam, "lam", f32, (H,), keep)
+        np_ = self._dense(lengths, "lengths", torch.int32, (B,), keep)
+        hp = self._dense(h0, "h0", f32, (B, H), keep)
+        y = torch.empty(shape, dtype=dtype, device=dev)
+        h_n = torch.empty((B, H), dtype=f32, device=dev)
+        st = torch.empty((-(-T // RCU_LINREC_CHUNK), B, H), dtype=f32, device=dev) if states \
+            else None
+        _check(self.lib.rcu_linrec_forward(
+            self.h, dt, 1 if batch_first else 0, T, B, H, xp, xl, rp, rl, ip, il, lp, c, np_, hp,
+            y.data_ptr(), H, h_n.data_ptr(), st.data_ptr() if states else None,
+            self._raw_stream()))
+        return y, h_n, st
 
     def linrec_backward(self, dy, x, r, i, lam, states, c=8.0, lengths=None, dh_n=None,
                         batch_first=False, stream=None):
         """dx, dr, di (of dy's type), dlam [H] and dh0 [B, H].  x, r, i: the
         forward's inputs, or all three as act8_pack's (codes, exponents)."""
-        dt = self._data(dy, "dy")
-        T, B, H = self._tbh(dy.shape, batch_first)
-        q8 = not isinstance(x, torch.Tensor)
-        if any(isinstance(t, torch.Tensor) == q8 for t in (r, i)):
+        if stream is not None:
+            return self._on_stream(stream, self.linrec_backward, dy, x, r, i, lam, states, c,
+                                   lengths, dh_n, batch_first)
+        dtype, dt, shape = self._type(dy, "dy", 3)
+        T, B, H = shape
+        if batch_first:
+            T, B = B, T
+        keep, f32, dev = [], torch.float32, dy.device
+        xp, xl, xe = self._saved(x, "x", dtype, shape, keep)
+        rp, rl, re = self._saved(r, "r", dtype, shape, keep)
+        ip, il, ie = self._saved(i, "i", dtype, shape, keep)
+        if (xe is None) != (re is None) or (xe is None) != (ie is None):
             raise ValueError("x, r, i are all tensors or all 8-bit checkpoints")
-
-        def call(s):
-            xs, rs, is_ = (self._saved(t, k, dy.dtype, dy.shape)
-                           for k, t in (("x", x), ("r", r), ("i", i)))
-            dys = self._rows(dy, "dy", dy.dtype, dy.shape)
-            lm = self._dense(lam, "lam", (H,))
-            ln = self._dense(lengths, "lengths", (B,), torch.int32)
-            st = self._dense(states, "states", (-(-T // RCU_LINREC_CHUNK), B, H))
-            hs = self._dense(dh_n, "dh_n", (B, H))
-            dx, dr, di = (torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-                          for _ in range(3))
-            dlam = torch.empty((H,), device=dy.device)
-            dh0 = torch.empty((B, H), device=dy.device)
-            _check(self.lib.rcu_linrec_backward(
-                self.h, dt, RCU_I8 if q8 else dt,
-                RCU_BATCH_FIRST if batch_first else RCU_TIME_FIRST, T, B, H, xs[1], xs[2], rs[1],
-                rs[2], is_[1], is_[2], xs[3], rs[3], is_[3], lm[1], c, ln[1], st[1], dys[1],
-                dys[2], hs[1], dx.data_ptr(), H, dr.data_ptr(), H, di.data_ptr(), H,
-                dlam.data_ptr(), dh0.data_ptr(), s))
-            return dx, dr, di, dlam, dh0
-        return self._run(stream, call)
+        yp, yl = self._rows(dy, "dy", dtype, shape, keep)
+        lp = self._dense(lam, "lam", f32, (H,), keep)
+        np_ = self._dense(lengths, "lengths", torch.int32, (B,), keep)
+        sp = self._dense(states, "states", f32, (-(-T // RCU_LINREC_CHUNK), B, H), keep)
+        hp = self._dense(dh_n, "dh_n", f32, (B, H), keep)
+        dx = torch.empty(shape, dtype=dtype, device=dev)
+        dr = torch.empty(shape, dtype=dtype, device=dev)
+        di = torch.empty(shape, dtype=dtype, device=dev)
+        dlam = torch.empty((H,), dtype=f32, device=dev)
+        dh0 = torch.empty((B, H), dtype=f32, device=dev)
+        _check(self.lib.rcu_linrec_backward(
+            self.h, dt, dt if xe is None else RCU_I8, 1 if batch_first else 0, T, B, H, xp, xl,
+            rp, rl, ip, il, xe, re, ie, lp, c, np_, sp, yp, yl, hp, dx.data_ptr(), H,
+            dr.data_ptr(), H, di.data_ptr(), H, dlam.data_ptr(), dh0.data_ptr(),
+            self._raw_stream()))
+        return dx, dr, di, dlam, dh0
 
     def linrec_step(self, x, r, i, lam, state, c=8.0, slot=None, stream=None):
         """y [B, H] of one step of B requests; state [slots, H] is updated in
         place, at slot[b] (int32 [B], -1: takes no part; None: row b)."""
-        dt = self._data(x, "x")
-        if x.dim() != 2:
-            raise ValueError(f"x must have two dimensions, got {list(x.shape)}")
-        B, H = x.shape
-        if not state.is_contiguous() or state.dim() != 2:
+        if stream is not None:
+            return self._on_stream(stream, self.linrec_step, x, r, i, lam, state, c, slot)
+        dtype, dt, shape = self._type(x, "x", 2)
+        B, H = shape
+        keep, f32 = [], torch.float32
+        if not isinstance(state, torch.Tensor) or state.dim() != 2 or not state.is_contiguous():
             raise ValueError("state must be a contiguous [slots, H] tensor")
-
-        def call(s):
-            xs, rs, is_ = (self._rows(t, k, x.dtype, x.shape)
-                           for k, t in (("x", x), ("r", r), ("i", i)))
-            lm = self._dense(lam, "lam", (H,))
-            st = self._dense(state, "state", (state.shape[0], H))
-            sl = self._dense(slot, "slot", (B,), torch.int32)
-            y = torch.empty((B, H), dtype=x.dtype, device=x.device)
-            _check(self.lib.rcu_linrec_step(self.h, dt, B, H, xs[1], xs[2], rs[1], rs[2], is_[1],
-                                            is_[2], lm[1], c, st[1], state.shape[0], sl[1],
-                                            y.data_ptr(), H, s))
-            return y
-        return self._run(stream, call)
+        slots = state.shape[0]
+        xp, xl = self._rows(x, "x", dtype, shape, keep)
+        rp, rl = self._rows(r, "r", dtype, shape, keep)
+        ip, il = self._rows(i, "i", dtype, shape, keep)
+        lp = self._dense(lam, "lam", f32, (H,), keep)
+        sp = self._dense(state, "state", f32, (slots, H), keep)
+        tp = self._dense(slot, "slot", torch.int32, (B,), keep)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+        _check(self.lib.rcu_linrec_step(self.h, dt, B, H, xp, xl, rp, rl, ip, il, lp, c, sp, slots,
+                                        tp, y.data_ptr(), H, self._raw_stream()))
+        return y
 
     # ---- layer norm
 
     def layernorm_forward(self, x, weight=None, bias=None, eps=1e-5, residual=None, stream=None):
         """(y, mean, rstd) of x [..., n]; with a residual (y, sum, mean, rstd),
         sum = x + residual being what is normalised."""
-        dt = self._data(x, "x")
-        n = x.shape[-1]
+        if stream is not None:
+            return self._on_stream(stream, self.layernorm_forward, x, weight, bias, eps, residual)
+        dtype, dt, shape = self._type(x, "x")
+        n = shape[-1]
         rows = x.numel() // n if n else 0
-
-        def call(s):
-            xs = self._rows(x, "x", x.dtype, x.shape)
-            rs = self._rows(residual, "residual", x.dtype, x.shape) if residual is not None \
-                else (None, None, 0)
-            w, b = self._dense(weight, "weight", (n,)), self._dense(bias, "bias", (n,))
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            u = torch.empty(x.shape, dtype=x.dtype, device=x.device) if residual is not None \
-                else None
-            mean = torch.empty(x.shape[:-1], device=x.device)
-            rstd = torch.empty(x.shape[:-1], device=x.device)
-            _check(self.lib.rcu_layernorm_forward(
-                self.h, dt, rows, n, xs[1], xs[2], rs[1], rs[2], w[1], b[1], eps, y.data_ptr(), n,
-                None if u is None else u.data_ptr(), n, mean.data_ptr(), rstd.data_ptr(), s))
-            return (y, mean, rstd) if u is None else (y, u, mean, rstd)
-        return self._run(stream, call)
+        keep, f32, dev = [], torch.float32, x.device
+        xp, xl = self._rows(x, "x", dtype, shape, keep)
+        wp = self._dense(weight, "weight", f32, (n,), keep)
+        bp = self._dense(bias, "bias", f32, (n,), keep)
+        u, rp, rl, up = None, None, 0, None
+        if residual is not None:
+            rp, rl = self._rows(residual, "residual", dtype, shape, keep)
+            u = torch.empty(shape, dtype=dtype, device=dev)
+            up = u.data_ptr()
+        y = torch.empty(shape, dtype=dtype, device=dev)
+        lead = shape[:-1]
+        mean = torch.empty(lead, dtype=f32, device=dev)
+        rstd = torch.empty(lead, dtype=f32, device=dev)
+        _check(self.lib.rcu_layernorm_forward(
+            self.h, dt, rows, n, xp, xl, rp, rl, wp, bp, eps, y.data_ptr(), n, up, n,
+            mean.data_ptr(), rstd.data_ptr(), self._raw_stream()))
+        return (y, mean, rstd) if u is None else (y, u, mean, rstd)
 
     def layernorm_backward(self, dy, u, mean, rstd, weight=None, dsum=None, stream=None):
         """(du, dweight, dbias).  u: what the forward normalised (x, or its
         sum), or act8_pack's (codes, exponents) of it; dsum: the gradient that
         reaches u another way."""
-        dt = self._data(dy, "dy")
-        n = dy.shape[-1]
+        if stream is not None:
+            return self._on_stream(stream, self.layernorm_backward, dy, u, mean, rstd, weight, dsum)
+        dtype, dt, shape = self._type(dy, "dy")
+        n = shape[-1]
         rows = dy.numel() // n if n else 0
-
-        def call(s):
-            us = self._saved(u, "u", dy.dtype, dy.shape)
-            dys = self._rows(dy, "dy", dy.dtype, dy.shape)
-            ds = self._rows(dsum, "dsum", dy.dtype, dy.shape) if dsum is not None \
-                else (None, None, 0)
-            w = self._dense(weight, "weight", (n,))
-            m = self._dense(mean, "mean", dy.shape[:-1])
-            rs = self._dense(rstd, "rstd", dy.shape[:-1])
-            du = torch.empty(dy.shape, dtype=dy.dtype, device=dy.device)
-            dw, db = (torch.empty((n,), device=dy.device) for _ in range(2))
-            _check(self.lib.rcu_layernorm_backward(
-                self.h, dt, dt if us[3] is None else RCU_I8, rows, n, dys[1], dys[2], us[1], us[2],
-                us[3], w[1], m[1], rs[1], ds[1], ds[2], du.data_ptr(), n, dw.data_ptr(),
-                db.data_ptr(), s))
-            return du, dw, db
-        return self._run(stream, call)
+        keep, f32, dev, lead = [], torch.float32, dy.device, shape[:-1]
+        up, ul, ue = self._saved(u, "u", dtype, shape, keep)
+        yp, yl = self._rows(dy, "dy", dtype, shape, keep)
+        sp, sl = self._rows(dsum, "dsum", dtype, shape, keep) if dsum is not None else (None, 0)
+        wp = self._dense(weight, "weight", f32, (n,), keep)
+        mp = self._dense(mean, "mean", f32, lead, keep)
+        rp = self._dense(rstd, "rstd", f32, lead, keep)
+        du = torch.empty(shape, dtype=dtype, device=dev)
+        dw = torch.empty((n,), dtype=f32, device=dev)
+        db = torch.empty((n,), dtype=f32, device=dev)
+        _check(self.lib.rcu_layernorm_backward(
+            self.h, dt, dt if ue is None else RCU_I8, rows, n, yp, yl, up, ul, ue, wp, mp, rp, sp,
+            sl, du.data_ptr(), n, dw.data_ptr(), db.data_ptr(), self._raw_stream()))
+        return du, dw, db
 
     # ---- 8-bit activation checkpoints
 
     def act8_pack(self, x, stream=None):
         """(codes int8 [..., n], exponents int8 [..., ceil(n / 64)]) of x."""
-        dt = self._data(x, "x")
-        n = x.shape[-1]
+        if stream is not None:
+            return self._on_stream(stream, self.act8_pack, x)
+        dtype, dt, shape = self._type(x, "x")
+        n = shape[-1]
         rows = x.numel() // n if n else 0
-
-        def call(s):
-            xs = self._rows(x, "x", x.dtype, x.shape)
-            codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-            exps = torch.empty((*x.shape[:-1], -(-n // RCU_ACT8_BLOCK)), dtype=torch.int8,
-                               device=x.device)
-            _check(self.lib.rcu_act8_pack(self.h, dt, rows, n, xs[1], xs[2], codes.data_ptr(), n,
-                                          exps.data_ptr(), s))
-            return codes, exps
-        return self._run(stream, call)
+        keep, dev = [], x.device
+        xp, xl = self._rows(x, "x", dtype, shape, keep)
+        codes = torch.empty(shape, dtype=torch.int8, device=dev)
+        exps = torch.empty((*shape[:-1], -(-n // RCU_ACT8_BLOCK)), dtype=torch.int8, device=dev)
+        _check(self.lib.rcu_act8_pack(self.h, dt, rows, n, xp, xl, codes.data_ptr(), n,
+                                      exps.data_ptr(), self._raw_stream()))
+        return codes, exps
 
     def act8_unpack(self, codes, exps, dtype=torch.float32, stream=None):
         """The values an 8-bit checkpoint stands for."""
+        if stream is not None:
+            return self._on_stream(stream, self.act8_unpack, codes, exps, dtype)
         dt = self._DTYPES.get(dtype)
         if dt is None:
             raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
-        n = codes.shape[-1]
+        if not isinstance(codes, torch.Tensor) or codes.dim() < 1:
+            raise ValueError("codes must be a tensor on a CUDA device")
+        shape = codes.shape
+        n = shape[-1]
         rows = codes.numel() // n if n else 0
-
-        def call(s):
-            cs = self._saved((codes, exps), "x", None, codes.shape)
-            y = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-            _check(self.lib.rcu_act8_unpack(self.h, dt, rows, n, cs[1], cs[2], cs[3],
-                                            y.data_ptr(), n, s))
-            return y
-        return self._run(stream, call)
+        keep = []
+        cp, cl, ep = self._saved((codes, exps), "x", None, shape, keep)
+        y = torch.empty(shape, dtype=dtype, device=codes.device)
+        _check(self.lib.rcu_act8_unpack(self.h, dt, rows, n, cp, cl, ep, y.data_ptr(), n,
+                                        self._raw_stream()))
+        return y
 
     # ---- handle
 

@@ -39,66 +39,160 @@ __device__ __forceinline__ void load_codes(const int8_t *p, uint32_t (&w)[2]) {
   w[0] = v.x, w[1] = v.y;
 }
 
+// Division of a word's index by a row's words.  Where rows lie one behind another
+// and hold whole blocks (FLAT) the matrix is one long row and none is needed; else
+// it is a multiplication by 2^32 / d, rounded up, which is exact as long as the
+// index times d stays below 2^32 (larger products take the division itself).
+struct Divide {
+  uint32_t d, inv;
+  bool quick;
+  __device__ __forceinline__ int64_t operator()(int64_t i) const {
+    return quick ? (int64_t)__umulhi((uint32_t)i, inv) : i / d;
+  }
+};
+inline Divide divide(int64_t total, int d) {
+  Divide v;
+  v.d = (uint32_t)d;
+  v.inv = (uint32_t)(((1ull << 32) + d - 1) / d);
+  v.quick = d > 1 && (double)(total + 64) * d < 4294967296.0;
+  return v;
+}
+
+constexpr int UNROLL = 4;  // words of a thread in flight
+
+// The largest magnitude of a word's values as fp32 bits: as whole numbers the
+// bits order like the magnitudes, with infinity and NaN above all.
+__device__ __forceinline__ uint32_t top_bits(const uint4 &v, const float *) {
+  const uint32_t m = 0x7fffffffu;
+  return max(max(v.x & m, v.y & m), max(v.z & m, v.w & m));
+}
+__device__ __forceinline__ uint32_t top_bits(const uint4 &v, const bf16 *) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+  return max(a << 16, a & 0xffff0000u);
+}
+// Codes of finite values that all fit at the scale inv: adding 1.5 * 2^23 rounds
+// to a whole number, to the nearest even, whose low byte is the code.
+__device__ __forceinline__ uint32_t quick_code(float v, float inv) {
+  return __float_as_uint(fmaf(v, inv, 12582912.f));
+}
+__device__ __forceinline__ uint32_t join4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+__device__ __forceinline__ void quick_codes(const uint4 &v, float inv, uint32_t (&w)[1],
+                                            const float *) {
+  w[0] = join4(quick_code(__uint_as_float(v.x), inv), quick_code(__uint_as_float(v.y), inv),
+               quick_code(__uint_as_float(v.z), inv), quick_code(__uint_as_float(v.w), inv));
+}
+__device__ __forceinline__ void quick_codes(const uint4 &v, float inv, uint32_t (&w)[2],
+                                            const bf16 *) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  uint32_t q[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    q[2 * j] = quick_code(__uint_as_float(u[j] << 16), inv);
+    q[2 * j + 1] = quick_code(__uint_as_float(u[j] & 0xffff0000u), inv);
+  }
+  w[0] = join4(q[0], q[1], q[2], q[3]);
+  w[1] = join4(q[4], q[5], q[6], q[7]);
+}
+
 // Rows of whole words; the last block of a row may be short (whole words too).
-template <typename T>
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(NT)
-    act8_pack_wide_kernel(int64_t rows, int n, const T *__restrict__ x, int64_t ldx,
+    act8_pack_wide_kernel(Divide by_row, int64_t rows, int n, const T *__restrict__ x, int64_t ldx,
                           int8_t *__restrict__ codes, int64_t ldc, int8_t *__restrict__ exps) {
   constexpr int VEC = Wide<T>::VEC, LANES = Wide<T>::LANES;
   const int nb = ceil_div(n, BLOCK8);
   const int64_t total = rows * nb * LANES;  // words, with those a short block lacks
-  for (int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x; id - threadIdx.x % 32 < total;
-       id += (int64_t)gridDim.x * NT) {
-    const int64_t blk = id / LANES, row = blk / nb;
-    const int c = (int)(blk % nb) * BLOCK8 + (int)(id % LANES) * VEC;
-    const bool on = id < total && c < n;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (on) raw = __ldg(reinterpret_cast<const uint4 *>(x + row * ldx + c));
-    const T *v = reinterpret_cast<const T *>(&raw);
-    float top = 0.f;
+  // a warp's lanes stay in step: the maxima below are over lanes of one warp
+  for (int64_t first = ((int64_t)blockIdx.x * UNROLL) * NT + threadIdx.x;
+       first - threadIdx.x % 32 < total; first += (int64_t)gridDim.x * UNROLL * NT) {
+    uint4 raw[UNROLL];
+    int64_t row[UNROLL];
+    int c[UNROLL];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const float a = fabsf(to_f(v[j]));
-      if (a < __int_as_float(0x7f800000)) top = fmaxf(top, a);
+    for (int q = 0; q < UNROLL; ++q) {
+      const int64_t id = first + q * NT, blk = id / LANES;
+      row[q] = FLAT ? 0 : by_row(blk);
+      c[q] = (int)(blk - row[q] * nb) * BLOCK8 + (int)(id % LANES) * VEC;
+      raw[q] = make_uint4(0, 0, 0, 0);
+      if (id < total && (FLAT || c[q] < n))
+        raw[q] = __ldg(reinterpret_cast<const uint4 *>(FLAT ? x + id * VEC : x + row[q] * ldx + c[q]));
     }
 #pragma unroll
-    for (int o = LANES / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = act8_exponent(top);
-    const float inv = power2(-e);
-    if (!on) continue;
-    uint32_t w[VEC / 4];
+    for (int q = 0; q < UNROLL; ++q) {
+      const int64_t id = first + q * NT;
+      uint32_t top = top_bits(raw[q], static_cast<const T *>(nullptr));
 #pragma unroll
-    for (int q = 0; q < VEC / 4; ++q) {
-      w[q] = 0;
+      for (int o = LANES / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // not finite, or above the largest scale: value by value (a block's lanes together)
+      const bool plain = top <= __float_as_uint(127.f * power2(121));
+      if (__any_sync(0xffffffffu, !plain)) {
+        float most = 0.f;
+        const T *v = reinterpret_cast<const T *>(&raw[q]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[q] |= (uint32_t)(act8_code(to_f(v[4 * q + j]), inv) & 0xff) << (8 * j);
+        for (int j = 0; j < VEC; ++j)
+          if (isfinite(to_f(v[j]))) most = fmaxf(most, fabsf(to_f(v[j])));
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1)
+          most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        top = __float_as_uint(most);
+      }
+      const int e = act8_exponent(__uint_as_float(top));
+      if (id >= total || (!FLAT && c[q] >= n)) continue;
+      uint32_t w[VEC / 4];
+      if (plain) {
+        quick_codes(raw[q], power2(-e), w, static_cast<const T *>(nullptr));
+      } else {
+        const T *v = reinterpret_cast<const T *>(&raw[q]);
+#pragma unroll
+        for (int k = 0; k < VEC / 4; ++k) {
+          w[k] = 0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[k] |= (uint32_t)(act8_code(to_f(v[4 * k + j]), power2(-e)) & 0xff) << (8 * j);
+        }
+      }
+      store_codes(FLAT ? codes + id * VEC : codes + row[q] * ldc + c[q], w);
+      if (id % LANES == 0) exps[id / LANES] = (int8_t)e;
     }
-    store_codes(codes + row * ldc + c, w);
-    if (id % LANES == 0) exps[blk] = (int8_t)e;
   }
 }
 
-template <typename T>
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(NT)
-    act8_unpack_wide_kernel(int64_t rows, int n, const int8_t *__restrict__ codes, int64_t ldc,
-                            const int8_t *__restrict__ exps, T *__restrict__ y, int64_t ldy) {
-  constexpr int VEC = Wide<T>::VEC;
+    act8_unpack_wide_kernel(Divide by_row, int64_t rows, int n, const int8_t *__restrict__ codes,
+                            int64_t ldc, const int8_t *__restrict__ exps, T *__restrict__ y,
+                            int64_t ldy) {
+  constexpr int VEC = Wide<T>::VEC, LANES = Wide<T>::LANES;
   const int nw = n / VEC, nb = ceil_div(n, BLOCK8);
   const int64_t total = rows * nw;
-  for (int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x; id < total;
-       id += (int64_t)gridDim.x * NT) {
-    const int64_t row = id / nw;
-    const int c = (int)(id % nw) * VEC;
-    uint32_t w[VEC / 4];
-    load_codes(codes + row * ldc + c, w);
-    const int e = __ldg(exps + row * nb + c / BLOCK8);
-    uint4 raw;
-    T *v = reinterpret_cast<T *>(&raw);
+  for (int64_t first = ((int64_t)blockIdx.x * UNROLL) * NT + threadIdx.x; first < total;
+       first += (int64_t)gridDim.x * UNROLL * NT) {
+    uint32_t w[UNROLL][VEC / 4];
+    int64_t to[UNROLL];
+    int e[UNROLL];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      v[j] = from_f<T>(act8_value((int8_t)(w[j / 4] >> (8 * (j % 4))), e));
-    *reinterpret_cast<uint4 *>(y + row * ldy + c) = raw;
+    for (int q = 0; q < UNROLL; ++q) {
+      const int64_t id = first + q * NT;
+      if (id >= total) break;
+      const int64_t row = FLAT ? 0 : by_row(id);
+      const int c = (int)(id - row * nw) * VEC;
+      to[q] = FLAT ? id * VEC : row * ldy + c;
+      load_codes(codes + (FLAT ? id * VEC : row * ldc + c), w[q]);
+      e[q] = __ldg(exps + (FLAT ? id / LANES : row * nb + c / BLOCK8));
+    }
+#pragma unroll
+    for (int q = 0; q < UNROLL; ++q) {
+      if (first + q * NT >= total) break;
+      uint4 raw;
+      T *v = reinterpret_cast<T *>(&raw);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        v[j] = from_f<T>(act8_value((int8_t)(w[q][j / 4] >> (8 * (j % 4))), e[q]));
+      *reinterpret_cast<uint4 *>(y + to[q]) = raw;
+    }
   }
 }
 
@@ -161,23 +255,32 @@ void pack(int64_t rows, int n, const T *x, int64_t ldx, int8_t *codes, int64_t l
           int nsm, bool vec, cudaStream_t s) {
   constexpr int VEC = Wide<T>::VEC;
   const int nb = ceil_div(n, BLOCK8);
-  if (vec && n % VEC == 0 && aligned(x, ldx, sizeof(T), 16) && aligned(codes, ldc, 1, VEC))
-    act8_pack_wide_kernel<T><<<grid_for(rows * nb * Wide<T>::LANES, nsm), NT, 0, s>>>(
-        rows, n, x, ldx, codes, ldc, exps);
-  else
+  const int64_t words = rows * nb * Wide<T>::LANES;
+  const int grid = grid_for((words + UNROLL - 1) / UNROLL, nsm);
+  if (!vec || n % VEC || !aligned(x, ldx, sizeof(T), 16) || !aligned(codes, ldc, 1, VEC))
     act8_pack_kernel<T><<<grid_for(rows * nb * 32, nsm), NT, 0, s>>>(rows, n, x, ldx, codes, ldc,
                                                                       exps);
+  else if (n % BLOCK8 == 0 && ldx == n && ldc == n)
+    act8_pack_wide_kernel<T, true><<<grid, NT, 0, s>>>(Divide{}, rows, n, x, ldx, codes, ldc, exps);
+  else
+    act8_pack_wide_kernel<T, false><<<grid, NT, 0, s>>>(divide(rows * nb, nb), rows, n, x, ldx,
+                                                        codes, ldc, exps);
 }
 template <typename T>
 void unpack(int64_t rows, int n, const int8_t *codes, int64_t ldc, const int8_t *exps, T *y,
             int64_t ldy, int nsm, bool vec, cudaStream_t s) {
   constexpr int VEC = Wide<T>::VEC;
-  if (vec && n % VEC == 0 && aligned(y, ldy, sizeof(T), 16) && aligned(codes, ldc, 1, VEC))
-    act8_unpack_wide_kernel<T><<<grid_for(rows * (n / VEC), nsm), NT, 0, s>>>(rows, n, codes, ldc,
-                                                                             exps, y, ldy);
-  else
+  const int64_t words = rows * (n / VEC);
+  const int grid = grid_for((words + UNROLL - 1) / UNROLL, nsm);
+  if (!vec || n % VEC || !aligned(y, ldy, sizeof(T), 16) || !aligned(codes, ldc, 1, VEC))
     act8_unpack_kernel<T><<<grid_for(rows * ceil_div(n, BLOCK8) * 32, nsm), NT, 0, s>>>(
         rows, n, codes, ldc, exps, y, ldy);
+  else if (n % BLOCK8 == 0 && ldy == n && ldc == n)
+    act8_unpack_wide_kernel<T, true><<<grid, NT, 0, s>>>(Divide{}, rows, n, codes, ldc, exps, y,
+                                                         ldy);
+  else
+    act8_unpack_wide_kernel<T, false><<<grid, NT, 0, s>>>(divide(words, n / VEC), rows, n, codes,
+                                                          ldc, exps, y, ldy);
 }
 
 }  // namespace

@@ -32,4 +32,15 @@ __device__ __forceinline__ float act8_value(int code, int e) {
   return code == -128 ? __int_as_float(0x7fc00000) : (float)code * power2(e);
 }
 
+// Four codes of one word as fp32 whole numbers: c + 128 in the low byte of 2^23
+// is exact.  Code -128 comes out as -128 here; act8_any_nan tells whether a word
+// holds one (a byte of w ^ 0x80808080 is 0 then).
+__device__ __forceinline__ float act8_whole(uint32_t w, int j) {
+  return __uint_as_float(__byte_perm(w ^ 0x80808080u, 0x4b000000u, 0x7540 + j)) - 8388736.f;
+}
+__device__ __forceinline__ bool act8_any_nan(uint32_t w) {
+  const uint32_t t = w ^ 0x80808080u;
+  return ((t - 0x01010101u) & ~t & 0x80808080u) != 0;
+}
+
 }  // namespace rcu

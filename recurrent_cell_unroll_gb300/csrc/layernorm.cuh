@@ -46,6 +46,10 @@ struct Vals {
   __device__ __forceinline__ void set(int j, float v) {
     reinterpret_cast<T *>(&raw)[j] = from_f<T>(v);
   }
+  __device__ __forceinline__ void decode(float (&f)[VEC]) const {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = (*this)[j];
+  }
 };
 // 8-bit codes with their block's exponent (VEC divides the block)
 template <int VEC>
@@ -57,8 +61,23 @@ struct Vals<int8_t, VEC> {
   }
   __device__ __forceinline__ void zero() { raw = decltype(raw){}, e = 0; }
   __device__ __forceinline__ void block(const int8_t *p) { e = __ldg(p); }
-  __device__ __forceinline__ float operator[](int j) const {
-    return act8_value(reinterpret_cast<const int8_t *>(&raw)[j], e);
+  __device__ __forceinline__ void decode(float (&f)[VEC]) const {
+    const float scale = power2(e);
+    if (VEC == 1) {
+      f[0] = act8_value((int8_t)*reinterpret_cast<const unsigned char *>(&raw), e);
+      return;
+    }
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&raw);
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[4 * q + j] = act8_whole(w[q], j) * scale;
+      if (act8_any_nan(w[q])) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          f[4 * q + j] = act8_value((int8_t)(w[q] >> (8 * j)), e);
+      }
+    }
   }
 };
 
@@ -69,7 +88,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // The sums of a and b over a row's W warps, the same in all of them.  Warp w of
-// the row writes its part; `buf` alternates, so one barrier a sum is enough.
+// the row writes its part; `buf` alternates, so one barrier a sum is enough, and
+// it is the row's own (a block's rows do not wait for one another).
 template <int W>
 __device__ __forceinline__ void row_sum(float &a, float &b, float2 (*part)[32], int &buf) {
   a = warp_sum(a);
@@ -77,7 +97,7 @@ __device__ __forceinline__ void row_sum(float &a, float &b, float2 (*part)[32], 
   if (W > 1) {
     const int warp = threadIdx.x / 32;
     if (threadIdx.x % 32 == 0) part[buf][warp] = make_float2(a, b);
-    __syncthreads();
+    asm volatile("barrier.sync %0, %1;" ::"r"(warp / W + 1), "r"(32 * W) : "memory");
     a = b = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {

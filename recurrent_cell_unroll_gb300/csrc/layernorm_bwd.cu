@@ -1,7 +1,7 @@
 // Layer norm, backward: du, and the weight's and bias's gradients.
 //
 // Bound by memory, and shaped as the forward: a row belongs to W warps of one
-// block, 16 values a lane, the next row's loads in flight.  Each lane has the
+// block, 16 or 32 values a lane, the next row's loads in flight.  Each lane has the
 // same columns of every row its warps take, so the column sums (dweight, dbias)
 // build up in its registers; every block writes one row of partial sums at the
 // end, and a second kernel adds those in a fixed order.
@@ -64,16 +64,24 @@ __global__ void __launch_bounds__(32 * W * R)
     for (int k = 0; k < N; ++k) dy[k] = dy1[k], u[k] = u1[k], ds[k] = ds1[k];
     if (AHEAD) load(row + step);
     float s1 = 0.f, s2 = 0.f;
+    float xh[N][VEC];  // kept to the second pass where making it again costs more (8 bits)
+    auto normalise = [&](int k) {
+      u[k].decode(xh[k]);
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+      for (int j = 0; j < VEC; ++j) xh[k][j] = (xh[k][j] - mean) * rstd;
+    };
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      normalise(k);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float g = dy[k][j], xh = (u[k][j] - mean) * rstd, q = g * w[k][j];
+        const float g = dy[k][j], q = g * w[k][j];
         s1 += q;
-        s2 = fmaf(q, xh, s2);
-        gw[k][j] = fmaf(g, xh, gw[k][j]);
+        s2 = fmaf(q, xh[k][j], s2);
+        gw[k][j] = fmaf(g, xh[k][j], gw[k][j]);
         gb[k][j] += g;
       }
+    }
     row_sum<W>(s1, s2, part, buf);
     s1 /= p.n;
     s2 /= p.n;
@@ -84,10 +92,10 @@ __global__ void __launch_bounds__(32 * W * R)
         const int c = (k * 32 * W + lane) * VEC;
         if (c < p.n) {
           Vals<T, VEC> o;
+          if (sizeof(IT) > 1) normalise(k);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const float xh = (u[k][j] - mean) * rstd;
-            const float d = fmaf(-xh, s2, fmaf(dy[k][j], w[k][j], -s1));
+            const float d = fmaf(-xh[k][j], s2, fmaf(dy[k][j], w[k][j], -s1));
             o.set(j, fmaf(rstd, d, p.dsum ? ds[k][j] : 0.f));
           }
           o.store(du + c);
@@ -131,14 +139,15 @@ __global__ void __launch_bounds__(32 * W * R)
 
 // out[c] = the sum of `rows` partial rows: a block has 32 columns, its warps
 // share the rows, and their sums join in order.
-constexpr int SUM_WARPS = 16;
-__global__ void ln_columns_kernel(const float *__restrict__ part_w, const float *__restrict__ part_b,
+constexpr int SUM_WARPS = 32;
+__global__ void __launch_bounds__(32 * SUM_WARPS) ln_columns_kernel(const float *__restrict__ part_w, const float *__restrict__ part_b,
                                   int rows, int n, float *__restrict__ dw, float *__restrict__ db) {
   __shared__ float2 part[SUM_WARPS][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c = blockIdx.x * 32 + lane;
   float a = 0.f, b = 0.f;
+  wait_for_previous();
   if (c < n)
-#pragma unroll 4
+#pragma unroll 8
     for (int r = warp; r < rows; r += SUM_WARPS) {
       a += part_w[(int64_t)r * n + c];
       b += part_b[(int64_t)r * n + c];
@@ -231,8 +240,9 @@ cudaError_t run(const LnBwd &p, DevMem &ws, int nsm, cudaStream_t s, int *launch
   ln_bwd_kernel<IT, T, VEC, N, W, R><<<grid, NT, SMEM, s>>>(p, part, part_b);
   ++*launches;
   if (columns) {
-    ln_columns_kernel<<<ceil_div(p.n, 32), 32 * SUM_WARPS, 0, s>>>(part, part_b, grid, p.n,
-                                                                   p.dweight, p.dbias);
+    const cudaError_t e = launch_after(ln_columns_kernel, dim3(ceil_div(p.n, 32)), 32 * SUM_WARPS, s,
+                                       part, part_b, grid, p.n, p.dweight, p.dbias);
+    if (e != cudaSuccess) return e;
     ++*launches;
   }
   return cudaGetLastError();
@@ -250,21 +260,24 @@ cudaError_t run_long(const LnBwd &p, DevMem &ws, int nsm, cudaStream_t s, int *l
   float *part_b = part + (int64_t)shares * p.n;
   ln_bwd_long_columns_kernel<IT, T>
       <<<dim3(ceil_div(p.n, 32), shares), 32 * SUM_WARPS, 0, s>>>(p, part, part_b);
-  ln_columns_kernel<<<ceil_div(p.n, 32), 32 * SUM_WARPS, 0, s>>>(part, part_b, shares, p.n,
-                                                                 p.dweight, p.dbias);
   *launches += 2;
-  return cudaGetLastError();
+  return launch_after(ln_columns_kernel, dim3(ceil_div(p.n, 32)), 32 * SUM_WARPS, s, part, part_b,
+                      shares, p.n, p.dweight, p.dbias);
 }
 
-// Values a lane: 8 of a short row, else 16.
+// Values a lane (PER): 32 where they lie packed (bf16 by 16-byte words), so that a
+// row of 1024 needs no barrier (182 us at 131072 rows, 191 with 16 values in two
+// warps); else 16 (fp32 from 8 bits 12501x1000: 29 us, 38 with 32).
 template <typename IT, typename T, int VEC>
 cudaError_t shape(const LnBwd &p, DevMem &ws, int nsm, cudaStream_t s, int *launches) {
+  constexpr bool PACKED = sizeof(IT) == 2 && VEC == VEC_BF16;
+  constexpr int PER = PACKED ? 32 : 16, MORE = PER / 16;
   if (p.n <= 256) return run<IT, T, VEC, 8 / VEC, 1>(p, ws, nsm, s, launches);
   if (p.n <= 512) return run<IT, T, VEC, 16 / VEC, 1>(p, ws, nsm, s, launches);
-  if (p.n <= 1024) return run<IT, T, VEC, 16 / VEC, 2>(p, ws, nsm, s, launches);
-  if (p.n <= 2048) return run<IT, T, VEC, 16 / VEC, 4>(p, ws, nsm, s, launches);
-  if (p.n <= 4096) return run<IT, T, VEC, 16 / VEC, 8>(p, ws, nsm, s, launches);
-  if (p.n <= 8192) return run<IT, T, VEC, 16 / VEC, 16>(p, ws, nsm, s, launches);
+  if (p.n <= 1024) return run<IT, T, VEC, PER / VEC, 2 / MORE>(p, ws, nsm, s, launches);
+  if (p.n <= 2048) return run<IT, T, VEC, PER / VEC, 4 / MORE>(p, ws, nsm, s, launches);
+  if (p.n <= 4096) return run<IT, T, VEC, PER / VEC, 8 / MORE>(p, ws, nsm, s, launches);
+  if (p.n <= 8192) return run<IT, T, VEC, PER / VEC, 16 / MORE>(p, ws, nsm, s, launches);
   return run_long<IT, T>(p, ws, nsm, s, launches);
 }
 

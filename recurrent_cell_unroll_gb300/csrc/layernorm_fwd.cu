@@ -3,9 +3,11 @@
 // Bound by memory: a row is read once, as 16-byte words where the rows allow,
 // kept in registers as it came (bf16 stays packed) and summed twice, the second
 // time about the mean.  A row belongs to W warps of one block, the fewest for
-// which a lane has at most 32 values; short rows share a block.  Blocks take
-// rows until there are none left, and have the next row's loads in flight while
-// they work on one.
+// which a lane has at most 16 values: weight and bias of a lane's columns then
+// fit its registers beside them (with 32 values a lane, read again for every row,
+// bf16 131072x1024 took 284 us).  Short rows share a block.  Blocks take rows
+// until there are none left, and have the next row's loads in flight while they
+// work on one.
 #include "layernorm.cuh"
 
 namespace rcu {
@@ -37,6 +39,15 @@ __global__ void __launch_bounds__(32 * W * R) ln_fwd_kernel(const LnFwd p) {
     }
   };
   load((int64_t)blockIdx.x * R + sub);
+  float w[N][VEC], b[N][VEC];
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = (k * 32 * W + lane) * VEC + j;
+      w[k][j] = p.weight && c < p.n ? __ldg(p.weight + c) : 1.f;
+      b[k][j] = p.bias && c < p.n ? __ldg(p.bias + c) : 0.f;
+    }
   for (int64_t base = (int64_t)blockIdx.x * R; base < p.rows; base += step) {
     const int64_t row = base + sub;
     Word u[N];
@@ -82,8 +93,7 @@ __global__ void __launch_bounds__(32 * W * R) ln_fwd_kernel(const LnFwd p) {
           Word o;
 #pragma unroll
           for (int j = 0; j < VEC; ++j)
-            o.set(j, fmaf((u[k][j] - mean) * rstd, p.weight ? __ldg(p.weight + c + j) : 1.f,
-                          p.bias ? __ldg(p.bias + c + j) : 0.f));
+            o.set(j, fmaf((u[k][j] - mean) * rstd, w[k][j], b[k][j]));
           o.store(y + c);
         }
       }
@@ -157,16 +167,15 @@ void run(const LnFwd &p, int nsm, cudaStream_t s) {
   ln_fwd_kernel<T, VEC, N, W, R, RES><<<grid, 32 * W * R, 0, s>>>(p);
 }
 
-// Values a lane: 8, 16 or 32 of one warp's row, 32 of a longer one's.
+// Values a lane: 8 of a short row, else 16.
 template <typename T, int VEC, bool RES>
 void shape(const LnFwd &p, int nsm, cudaStream_t s) {
   if (p.n <= 256) run<T, VEC, 8 / VEC, 1, RES>(p, nsm, s);
   else if (p.n <= 512) run<T, VEC, 16 / VEC, 1, RES>(p, nsm, s);
-  else if (p.n <= 1024) run<T, VEC, 32 / VEC, 1, RES>(p, nsm, s);
-  else if (p.n <= 2048) run<T, VEC, 32 / VEC, 2, RES>(p, nsm, s);
-  else if (p.n <= 4096) run<T, VEC, 32 / VEC, 4, RES>(p, nsm, s);
-  else if (p.n <= 8192) run<T, VEC, 32 / VEC, 8, RES>(p, nsm, s);
-  else if (p.n <= 16384) run<T, VEC, 32 / VEC, 16, RES>(p, nsm, s);
+  else if (p.n <= 1024) run<T, VEC, 16 / VEC, 2, RES>(p, nsm, s);
+  else if (p.n <= 2048) run<T, VEC, 16 / VEC, 4, RES>(p, nsm, s);
+  else if (p.n <= 4096) run<T, VEC, 16 / VEC, 8, RES>(p, nsm, s);
+  else if (p.n <= 8192) run<T, VEC, 16 / VEC, 16, RES>(p, nsm, s);
   else ln_fwd_long_kernel<T, VEC><<<(int)std::min<int64_t>(p.rows, 4 * nsm), LONG_NT, 0, s>>>(p);
 }
 

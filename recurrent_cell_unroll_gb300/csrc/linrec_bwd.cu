@@ -7,6 +7,7 @@
 // that enters a tile comes from the forward's states, so only the backward
 // carry crosses tiles.  Per element: four values read and three written, once;
 // em1, b and both sigmoids stay in registers between the two runs.
+#include "act8.cuh"
 #include "linrec_tile.cuh"
 
 namespace rcu {
@@ -31,41 +32,34 @@ struct Smem {
   int abort;
 };
 
-// Bytes of a tile of the saved inputs (IT) and of dy.
-template <typename IT, typename T>
-constexpr int in_bytes() { return STEPS * Shape<T>::CW * (int)sizeof(IT); }
-template <typename IT, typename T>
-constexpr int stage_bytes() { return 3 * in_bytes<IT, T>() + STEPS * 128; }
-
-// A lane's saved values of one step (CPT channels), raw, from shared or global memory
-template <typename IT, int CPT>
-__device__ __forceinline__ uint32_t raw_smem(const uint8_t *at, int lane) {
-  constexpr int N = CPT * (int)sizeof(IT);
-  at += lane * N;
-  if (N == 4) return *reinterpret_cast<const uint32_t *>(at);
-  if (N == 2) return *reinterpret_cast<const unsigned short *>(at);
-  return *at;
+// Bytes of a tile of a saved input (IT) and of all four.
+template <typename IT, typename T, bool TMA>
+constexpr int in_bytes() {
+  return STEPS * (TMA ? Shape<T>::CW * (int)sizeof(IT) : Loose<IT, Shape<T>::CPT>::PITCH);
 }
-template <typename IT, int CPT>
-struct Global {
-  __device__ __forceinline__ static uint32_t load(const IT *p, int live, bool word) {
-    return load_raw(p, live, word);
-  }
-};
-template <int CPT>
-struct Global<int8_t, CPT> {
-  __device__ __forceinline__ static uint32_t load(const int8_t *p, int live, bool) {
-    const uint8_t *q = reinterpret_cast<const uint8_t *>(p);
-    uint32_t v = live > 0 ? __ldg(q) : 0u;
-    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 8;
-    return v;
-  }
-};
+template <typename IT, typename T, bool TMA>
+constexpr int stage_bytes() { return 3 * in_bytes<IT, T, TMA>() + in_bytes<T, T, TMA>(); }
 
-// 8-bit codes: c + 128 in the low bits of 2^23 is exact in fp32; code -128 is NaN
-__device__ __forceinline__ float code_value(uint32_t biased, float scale) {
-  const float v = __uint_as_float(0x4b000000u | biased) - 8388736.f;
-  return v == -128.f ? __int_as_float(0x7fc00000) : v * scale;
+// A lane's values of one step (CPT channels) in a tile that TMA brought
+template <typename IT, int CPT>
+__device__ __forceinline__ uint32_t tile_raw(const uint8_t *row, int lane) {
+  constexpr int N = CPT * (int)sizeof(IT);
+  row += lane * N;
+  if (N == 4) return *reinterpret_cast<const uint32_t *>(row);
+  if (N == 2) return *reinterpret_cast<const unsigned short *>(row);
+  return *row;
+}
+
+// 8-bit codes: c + 128 in the low bits of 2^23 is exact in fp32.  A code of -128
+// (not a number) comes out as -128 here; any_nan tells whether a lane has one, and
+// its results are made NaN afterwards.
+__device__ __forceinline__ float code_value(uint32_t biased) {
+  return __uint_as_float(0x4b000000u | biased) - 8388736.f;
+}
+template <int CPT>
+__device__ __forceinline__ uint32_t nan_flags(uint32_t raw) {  // a byte of raw ^ 0x80.. is 0
+  const uint32_t one = CPT == 1 ? 0x01u : 0x0101u, t = raw ^ (one << 7);
+  return (t - one) & ~t & (one << 7);
 }
 // One step's values: x, and the logits within their limits
 template <typename IT, typename V>
@@ -82,7 +76,7 @@ template <>
 struct Decode<int8_t, F2> {
   __device__ __forceinline__ static F2 x(uint32_t v, float scale) {
     v ^= 0x8080u;
-    return f2(code_value(v & 0xffu, scale), code_value(v >> 8, scale));
+    return mul2(f2(code_value(v & 0xffu), code_value(v >> 8)), f2(scale));
   }
   __device__ __forceinline__ static F2 r(uint32_t v, float scale, const Limits &l) {
     const F2 f = i(v, scale);  // not limited as bf16: the channels' limits, widened
@@ -107,7 +101,7 @@ struct Decode<float, float> {
 template <>
 struct Decode<int8_t, float> {
   __device__ __forceinline__ static float x(uint32_t v, float scale) {
-    return code_value(v ^ 0x80u, scale);
+    return code_value(v ^ 0x80u) * scale;
   }
   __device__ __forceinline__ static float r(uint32_t v, float scale, const Limits &l) {
     return limit_r(x(v, scale), l);
@@ -162,6 +156,29 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], const float (
   }
 }
 
+// NaN where a step's code says so: in what x, r or i enter.
+__device__ __forceinline__ bool not_a_number(uint32_t raw, int j) {
+  return (raw >> (8 * j) & 0xffu) == 0x80u;
+}
+template <int CPT>
+__device__ __forceinline__ void spoil(uint32_t x, uint32_t r, uint32_t i, float &em1, float &nb,
+                                      float &ns, float &ng) {
+  const float nan = __int_as_float(0x7fc00000);
+  if (not_a_number(x, 0)) nb = nan;
+  if (not_a_number(r, 0)) em1 = nb = ns = nan;
+  if (not_a_number(i, 0)) nb = ng = nan;
+}
+template <int CPT>
+__device__ __forceinline__ void spoil(uint32_t x, uint32_t r, uint32_t i, F2 &em1, F2 &nb, F2 &ns,
+                                      F2 &ng) {
+  float m[2] = {lo(em1), hi(em1)}, b[2] = {lo(nb), hi(nb)}, s[2] = {lo(ns), hi(ns)},
+        g[2] = {lo(ng), hi(ng)};
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    spoil<1>(x >> (8 * j), r >> (8 * j), i >> (8 * j), m[j], b[j], s[j], g[j]);
+  em1 = f2(m[0], m[1]), nb = f2(b[0], b[1]), ns = f2(s[0], s[1]), ng = f2(g[0], g[1]);
+}
+
 // Local gradients of one step from ne = -dL/dh_t and the state before it, which
 // moves on by one step:
 //   dx = e beta g,  di = e b (1 - g),  dlog_s = dL/dlog(a) s = e s (a h - a^2 b / w),
@@ -186,22 +203,24 @@ template <typename IT, typename T, bool TMA>
 __global__ void __launch_bounds__(NT, PER_SM)
     linrec_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap mdy,
-                      const LinrecBwd p, const Cut cut, float *__restrict__ partial, const int words,
+                      const LinrecBwd p, const Cut cut, float *__restrict__ partial, const bool words,
                       int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
-  constexpr int IN = in_bytes<IT, T>(), STAGE = stage_bytes<IT, T>();
+  constexpr int IN = in_bytes<IT, T, TMA>(), STAGE = stage_bytes<IT, T, TMA>();
+  constexpr int IN_ROW = IN / STEPS, DY_ROW = in_bytes<T, T, TMA>() / STEPS;
   constexpr bool Q8 = sizeof(IT) == 1;
   typedef typename Lane<T>::V V;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *ring = smem;
-  Smem<V> &sh = *reinterpret_cast<Smem<V> *>(smem + (TMA ? STAGES * STAGE : 0));
+  Smem<V> &sh = *reinterpret_cast<Smem<V> *>(smem + STAGES * STAGE);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cs = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
   const int stride = gridDim.x / cs, u0 = blockIdx.x / cs;
 
-  // the next tile to copy: live tiles of this block, the last steps first
+  // Copies of the live tiles of this block, the last steps first: by TMA (thread
+  // 0, the whole tile) or by each warp its own rows.
   int pu = u0, pk = 0, issued = 0;
-  auto issue = [&] {  // thread 0
+  auto issue = [&] {
     for (; pu < cut.units; pu += stride, pk = 0) {
       const Unit v = unit_of(cut, p.B, pu, CW);
       const int len = row_length(p.lengths, v.b, p.T, err);
@@ -209,34 +228,73 @@ __global__ void __launch_bounds__(NT, PER_SM)
       do tile = v.last - 1 - (pk++ * cs + rank);
       while (tile >= v.first && tile * STEPS >= len);
       if (tile < v.first) continue;
-      const int st = issued++ % STAGES;
-      uint8_t *dst = ring + st * STAGE;
-      tc::mbar_arrive_expect_tx(&sh.full[st], STAGE);
-      tma_load_3d(dst, &mx, &sh.full[st], v.c0, v.b, tile * STEPS);
-      tma_load_3d(dst + IN, &mr, &sh.full[st], v.c0, v.b, tile * STEPS);
-      tma_load_3d(dst + 2 * IN, &mi, &sh.full[st], v.c0, v.b, tile * STEPS);
-      tma_load_3d(dst + 3 * IN, &mdy, &sh.full[st], v.c0, v.b, tile * STEPS);
-      return;
+      uint8_t *dst = ring + issued % STAGES * STAGE;
+      if (TMA) {
+        uint64_t *bar = &sh.full[issued % STAGES];
+        tc::mbar_arrive_expect_tx(bar, STAGE);
+        tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
+        tma_load_3d(dst + IN, &mr, bar, v.c0, v.b, tile * STEPS);
+        tma_load_3d(dst + 2 * IN, &mi, bar, v.c0, v.b, tile * STEPS);
+        tma_load_3d(dst + 3 * IN, &mdy, bar, v.c0, v.b, tile * STEPS);
+      } else {
+        const int64_t tw = tile * STEPS + warp * S, b = v.b;
+        const int width = min(CW, p.H - v.c0), rows = (int)min(len - tw, (int64_t)S);
+#pragma unroll 1
+        for (int k = 0; k < 3; ++k) {
+          const SeqIn &in = (&p.x)[k];
+          copy_rows<IT, CPT>(dst + k * IN + warp * S * IN_ROW,
+                             static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
+                             in.st * (int64_t)sizeof(IT), rows, width * (int)sizeof(IT));
+        }
+        copy_rows<T, CPT>(dst + 3 * IN + warp * S * DY_ROW,
+                          static_cast<const T *>(p.dy.p) + tw * p.dy.st + b * p.dy.sb + v.c0,
+                          p.dy.st * (int64_t)sizeof(T), rows, width * (int)sizeof(T));
+      }
+      ++issued;
+      break;
     }
+    if (!TMA) copy_commit();
   };
   if (threadIdx.x == 0) {
     for (int st = 0; st < STAGES; ++st) tc::mbar_init(&sh.full[st], 1);
     for (int q = 0; q < 2; ++q) tc::mbar_init(&sh.met[q], 1);
     sh.abort = 0;
     tc::fence_mbar_init();
-    if (TMA)
-      for (int st = 0; st < STAGES; ++st) issue();
+  }
+  if (!TMA || threadIdx.x == 0) {
+#pragma unroll 1
+    for (int st = 0; st < STAGES; ++st) issue();
   }
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
+  // 8 bits: lane 8 k + s has the exponent of tensor k at the warp's step s of a tile
+  auto exponent = [&](const Unit &v, int len, int tile) {
+    const int k = lane / S;
+    const int64_t t = (int64_t)tile * STEPS + warp * S + lane % S;
+    const int8_t *e = k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e;
+    if (k > 2 || tile < v.first || t >= len) return 0;
+    return (int)__ldg(e + (t * p.et + v.b * p.eb) * ceil_div(p.H, BLOCK8) + v.c0 / BLOCK8);
+  };
   int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
   V k2;
   Limits lim;
   bool small = false;
+  // What a unit starts with is read while the one before it is worked on.
+  V first;
+  int len1 = p.T;
+  auto look = [&](int u) {
+    if (u >= cut.units) return;
+    const Unit v = unit_of(cut, p.B, u, CW);
+    const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
+    set(first, 0.f);
+    if (p.dh_n) load_v(p.dh_n + (int64_t)v.b * p.H + ch, live, first);
+    len1 = row_length(p.lengths, v.b, p.T, err);
+  };
+  look(u0);
   for (int u = u0; u < cut.units; u += stride) {
     const Unit v = unit_of(cut, p.B, u, CW);
-    const int len = row_length(p.lengths, v.b, p.T, err);
+    const int len = len1;
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
     V nk, nc, sum, zero, minus;
@@ -248,15 +306,14 @@ __global__ void __launch_bounds__(NT, PER_SM)
       lim = limits(k2);
       small = __all_sync(0xffffffffu, small_rate(k2));
     }
-    // all three outputs move a word a lane
-    const bool whole = v.c0 + CW <= p.H && (words >> 4 & 7) == 7 && p.dx.p && p.dr.p && p.di.p;
+    const bool whole = v.c0 + CW <= p.H && words;
     set(nk, -1.f / LOG2E);
     nk = mul_v(nk, k2);  // -K
-    if (p.dh_n) load_v(p.dh_n + row, live, nc);
-    else nc = zero;
-    nc = mul_v(nc, minus);  // the carry, negated: -dL/dh after the steps so far
+    nc = neg_v(first);  // the carry, negated: -dL/dh after the steps so far
+    look(u + stride);
     sum = zero;
     V enter = zero;  // the state that enters the tile, read one tile ahead
+    int ex = Q8 ? exponent(v, len, v.last - 1 - rank) : 0;
     for (int base = v.last - 1; base >= v.first; base -= cs) {
       const int tile = base - rank, tw = tile * STEPS + warp * S;
       const bool on = tile >= v.first && tile * STEPS < len;  // the same for the whole block
@@ -265,50 +322,60 @@ __global__ void __launch_bounds__(NT, PER_SM)
       if (on) {
         load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
         float scale[3][S];
-        if (Q8) {  // lane 8 k + s has the exponent of tensor k at step s
-          const int k = lane / S, t = tw + lane % S;
-          const int8_t *e = k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e;
-          int ex = 0;
-          if (k < 3 && t < len)
-            ex = __ldg(e + (t * p.et + v.b * p.eb) * ceil_div(p.H, BLOCK8) + v.c0 / BLOCK8);
-          const float f = __int_as_float((ex + 127) << 23);
+        if (Q8) {
+          const float f = power2(ex);
 #pragma unroll
-          for (int k2i = 0; k2i < 3; ++k2i)
+          for (int k = 0; k < 3; ++k)
 #pragma unroll
-            for (int s = 0; s < S; ++s)
-              scale[k2i][s] = __shfl_sync(0xffffffffu, f, k2i * S + s);
+            for (int s = 0; s < S; ++s) scale[k][s] = __shfl_sync(0xffffffffu, f, k * S + s);
         }
         uint32_t raw[3][S], rawd[S];
+        const uint8_t *src = ring + used % STAGES * STAGE;
         if (TMA) {
-          const int st = used % STAGES;
-          tc::mbar_wait(&sh.full[st], (used / STAGES) & 1, err, &sh.abort, WAIT_NS);
-          ++used;
-          const uint8_t *src = ring + st * STAGE;
+          tc::mbar_wait(&sh.full[used % STAGES], (used / STAGES) & 1, err, &sh.abort, WAIT_NS);
 #pragma unroll
           for (int k = 0; k < 3; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s)
-              raw[k][s] = raw_smem<IT, CPT>(src + k * IN + (warp * S + s) * (IN / STEPS), lane);
+              raw[k][s] = tile_raw<IT, CPT>(src + k * IN + (warp * S + s) * IN_ROW, lane);
 #pragma unroll
           for (int s = 0; s < S; ++s)
-            rawd[s] = raw_smem<T, CPT>(src + 3 * IN + (warp * S + s) * 128, lane);
+            rawd[s] = tile_raw<T, CPT>(src + 3 * IN + (warp * S + s) * DY_ROW, lane);
         } else {
-          const SeqIn *src[3] = {&p.x, &p.r, &p.i};
+          copy_wait<STAGES - 1>();
+          __syncwarp();
+          const int64_t b = v.b;
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
-            const IT *q = static_cast<const IT *>(src[k]->p) + tw * src[k]->st + v.b * src[k]->sb + ch;
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-              raw[k][s] = Global<IT, CPT>::load(q + s * src[k]->st, tw + s < len ? live : 0,
-                                                words >> k & 1);
+            const SeqIn &in = (&p.x)[k];
+            loose_rows<IT, CPT, S>(
+                src + k * IN + warp * S * IN_ROW,
+                static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
+                in.st * (int64_t)sizeof(IT), raw[k]);
           }
-          const T *q = static_cast<const T *>(p.dy.p) + tw * p.dy.st + v.b * p.dy.sb + ch;
-#pragma unroll
-          for (int s = 0; s < S; ++s)
-            rawd[s] = load_raw(q + s * p.dy.st, tw + s < len ? live : 0, words >> 3 & 1);
+          loose_rows<T, CPT, S>(src + 3 * IN + warp * S * DY_ROW,
+                                static_cast<const T *>(p.dy.p) + tw * p.dy.st + b * p.dy.sb + v.c0,
+                                p.dy.st * (int64_t)sizeof(T), rawd);
         }
-        if (small) gates<IT, true>(raw, scale, k2, lim, em1, nb, ns, ng);
-        else gates<IT, false>(raw, scale, k2, lim, em1, nb, ns, ng);
+        if (tw >= len) {  // a warp past the row's end has the identity
+#pragma unroll
+          for (int s = 0; s < S; ++s) em1[s] = nb[s] = ns[s] = ng[s] = 0;
+        } else if (small) {
+          gates<IT, true>(raw, scale, k2, lim, em1, nb, ns, ng);
+        } else {
+          gates<IT, false>(raw, scale, k2, lim, em1, nb, ns, ng);
+        }
+        if (Q8) {
+          uint32_t bad = 0;
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int s = 0; s < S; ++s) bad |= nan_flags<CPT>(raw[k][s]);
+          if (bad) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) spoil<CPT>(raw[0][s], raw[1][s], raw[2][s], em1[s], nb[s], ns[s], ng[s]);
+          }
+        }
 #pragma unroll
         for (int s = 0; s < S; ++s) dy[s] = Decode<T, V>::x(rawd[s], 0.f);
         if (tw + S > len) {
@@ -325,6 +392,14 @@ __global__ void __launch_bounds__(NT, PER_SM)
         for (int s = S - 1; s >= 0; --s) {
           const V ne = fma_v(dy[s], minus, mine.e);
           mine.e = fma_v(em1[s], ne, ne);
+        }
+      }
+      if (Q8) ex = exponent(v, len, tile - cs);  // of this block's next tile
+      if (on) {
+        ++used;
+        if (!TMA) {
+          __syncwarp();  // the warp's values are in registers
+          issue();
         }
       }
       V c = nc;
@@ -434,15 +509,16 @@ __global__ void __launch_bounds__(NT, PER_SM)
 
 // dlambda[h] = -c sigmoid(lambda) * the sum of `rows` partial sums.  A warp has
 // 32 channels; its block's warps share the rows, and the shares join in order.
-constexpr int SUM_WARPS = 16;
+constexpr int SUM_WARPS = 32;
 __global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int64_t rows, int H,
                                       const float *__restrict__ lambda, float c,
                                       float *__restrict__ dlambda) {
   __shared__ float part[SUM_WARPS][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, h = blockIdx.x * 32 + lane;
   float s = 0.f;
+  wait_for_previous();
   if (h < H)
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t b = warp; b < rows; b += SUM_WARPS) s += partial[b * H + h];
   part[warp][lane] = s;
   __syncthreads();
@@ -457,7 +533,7 @@ __global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int64_t
 struct Maps {
   CUtensorMap m[4];
   bool tma;
-  int words;
+  bool words;  // all three outputs, in whole words a lane
 };
 template <typename IT, typename T>
 Maps maps(const LinrecBwd &p, bool vec) {
@@ -465,15 +541,14 @@ Maps maps(const LinrecBwd &p, bool vec) {
   const SeqIn *in[4] = {&p.x, &p.r, &p.i, &p.dy};
   const SeqOut *out[3] = {&p.dx, &p.dr, &p.di};
   v.tma = vec;
-  v.words = 0;
   for (int k = 0; k < 4; ++k) {
     const int bytes = k < 3 ? (int)sizeof(IT) : (int)sizeof(T);
     v.tma = v.tma && tc_map_3d(&v.m[k], in[k]->p, bytes, p.H, p.B, p.T, in[k]->sb, in[k]->st,
                                Shape<T>::CW, 1, STEPS);
-    v.words |= word_aligned(in[k]->p, in[k]->st, in[k]->sb, bytes) << k;
   }
+  v.words = true;
   for (int k = 0; k < 3; ++k)
-    v.words |= word_aligned(out[k]->p, out[k]->st, out[k]->sb, sizeof(T)) << (4 + k);
+    v.words = v.words && out[k]->p && word_aligned(out[k]->p, out[k]->st, out[k]->sb, sizeof(T));
   return v;
 }
 
@@ -481,7 +556,7 @@ template <typename IT, typename T, bool TMA>
 cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStream_t s,
                 int *launches) {
   constexpr size_t SMEM =
-      sizeof(Smem<typename Lane<T>::V>) + (TMA ? STAGES * stage_bytes<IT, T>() : 0);
+      sizeof(Smem<typename Lane<T>::V>) + STAGES * stage_bytes<IT, T, TMA>();
   static const Resident res = resident(linrec_bwd_kernel<IT, T, TMA>, NT, MAXCS, SMEM, 0);
   const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res);
   const int64_t rows = (int64_t)p.B * pl.cut.nseg * pl.cs;
@@ -494,10 +569,9 @@ cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStr
                              v.m[3], p, pl.cut, partial, v.words, err);
   ++*launches;
   if (e != cudaSuccess || !p.dlambda) return e;
-  linrec_dlambda_kernel<<<ceil_div(p.H, 32), 32 * SUM_WARPS, 0, s>>>(partial, rows, p.H, p.lambda,
-                                                                     p.c, p.dlambda);
   ++*launches;
-  return cudaGetLastError();
+  return launch_after(linrec_dlambda_kernel, dim3(ceil_div(p.H, 32)), 32 * SUM_WARPS, s,
+                      (const float *)partial, rows, p.H, p.lambda, p.c, p.dlambda);
 }
 
 template <typename IT, typename T>

@@ -32,6 +32,10 @@ struct Smem {
   // then [2][cs][32]: the cluster's blocks' maps, by parity of the round
 };
 
+// Bytes of the three inputs' tiles
+template <typename T, bool TMA>
+constexpr int stage_bytes() { return 3 * (TMA ? TILE_BYTES : STEPS * Loose<T, Shape<T>::CPT>::PITCH); }
+
 // em1 and -b of the lane's channels at each of S steps, BATCH pairs at a time
 template <bool SMALL>
 __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], F2 k2, const Limits &lim,
@@ -77,42 +81,61 @@ __global__ void __launch_bounds__(NT, PER_SM)
     linrec_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap my,
                       const LinrecFwd p, const Cut cut,
-                      const int words, int *err) {
+                      const bool words, int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   typedef typename Lane<T>::V V;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *ring = smem;
-  uint8_t *out = smem + STAGES * 3 * TILE_BYTES;  // the outputs of the tile, on their way
-  Smem<V> &sh = *reinterpret_cast<Smem<V> *>(smem + (TMA ? (STAGES * 3 + 1) * TILE_BYTES : 0));
+  constexpr int STAGE = stage_bytes<T, TMA>();
+  uint8_t *out = smem + STAGES * STAGE;  // the outputs of the tile, on their way
+  Smem<V> &sh = *reinterpret_cast<Smem<V> *>(out + (TMA ? TILE_BYTES : 0));
   typename Slot<V>::type *peers = reinterpret_cast<typename Slot<V>::type *>(&sh + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int cs = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
   const int stride = gridDim.x / cs, u0 = blockIdx.x / cs;
 
-  // the next tile to copy: live tiles of this block in the order they are used
+  // Copies of the live tiles of this block, in the order they are used: by TMA
+  // (thread 0, the whole tile) or by each warp its own rows.
   int pu = u0, pk = 0, issued = 0;
-  auto issue = [&] {  // thread 0
+  auto issue = [&] {
     for (; pu < cut.units; pu += stride, pk = 0) {
       const Unit v = unit_of(cut, p.B, pu, CW);
-      const int tile = v.first + pk * cs + rank;
-      if (tile >= v.last || tile * STEPS >= row_length(p.lengths, v.b, p.T, err)) continue;
-      const int st = issued++ % STAGES;
-      uint8_t *dst = ring + st * 3 * TILE_BYTES;
-      tc::mbar_arrive_expect_tx(&sh.full[st], 3 * TILE_BYTES);
-      tma_load_3d(dst, &mx, &sh.full[st], v.c0, v.b, tile * STEPS);
-      tma_load_3d(dst + TILE_BYTES, &mr, &sh.full[st], v.c0, v.b, tile * STEPS);
-      tma_load_3d(dst + 2 * TILE_BYTES, &mi, &sh.full[st], v.c0, v.b, tile * STEPS);
+      const int tile = v.first + pk * cs + rank, len = row_length(p.lengths, v.b, p.T, err);
+      if (tile >= v.last || tile * STEPS >= len) continue;
+      uint8_t *dst = ring + issued % STAGES * STAGE;
+      if (TMA) {
+        uint64_t *bar = &sh.full[issued % STAGES];
+        tc::mbar_arrive_expect_tx(bar, STAGE);
+        tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
+        tma_load_3d(dst + STAGE / 3, &mr, bar, v.c0, v.b, tile * STEPS);
+        tma_load_3d(dst + 2 * STAGE / 3, &mi, bar, v.c0, v.b, tile * STEPS);
+      } else {
+        const int64_t tw = tile * STEPS + warp * S;
+        const int bytes = min(CW, p.H - v.c0) * (int)sizeof(T);
+#pragma unroll 1
+        for (int k = 0; k < 3; ++k) {
+          const SeqIn &in = (&p.x)[k];
+          copy_rows<T, CPT>(
+              dst + k * (STAGE / 3) + warp * (STAGE / 3 / NW),
+              static_cast<const T *>(in.p) + tw * in.st + (int64_t)v.b * in.sb + v.c0,
+              in.st * (int64_t)sizeof(T), (int)min(len - tw, (int64_t)S), bytes);
+        }
+      }
+      ++issued;
       ++pk;
-      return;
+      break;
     }
+    if (!TMA) copy_commit();
   };
   if (threadIdx.x == 0) {
     for (int st = 0; st < STAGES; ++st) tc::mbar_init(&sh.full[st], 1);
     for (int q = 0; q < 2; ++q) tc::mbar_init(&sh.met[q], 1);
     sh.abort = 0;
     tc::fence_mbar_init();
-    if (TMA)
-      for (int st = 0; st < STAGES; ++st) issue();
+  }
+  if (!TMA || threadIdx.x == 0) {
+#pragma unroll 1
+    for (int st = 0; st < STAGES; ++st) issue();
   }
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
@@ -121,46 +144,57 @@ __global__ void __launch_bounds__(NT, PER_SM)
   V k2;
   Limits lim;
   bool small = false;
+  // What a unit starts with is read while the one before it is worked on.
+  V first;
+  int len1 = p.T;
+  auto look = [&](int u) {
+    if (u >= cut.units) return;
+    const Unit v = unit_of(cut, p.B, u, CW);
+    const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
+    set(first, 0.f);
+    if (p.h0) load_v(p.h0 + (int64_t)v.b * p.H + ch, live, first);
+    len1 = row_length(p.lengths, v.b, p.T, err);
+  };
+  look(u0);
   for (int u = u0; u < cut.units; u += stride) {
     const Unit v = unit_of(cut, p.B, u, CW);
-    const int len = row_length(p.lengths, v.b, p.T, err);
+    const int len = len1;
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
-    V carry;
     if (v.c0 != held) {
       held = v.c0;
       rate(p.lambda + ch, p.c, live, k2);
       lim = limits(k2);
       small = __all_sync(0xffffffffu, small_rate(k2));
     }
-    if (p.h0) load_v(p.h0 + row, live, carry);
-    else set(carry, 0.f);
-    carry = neg_v(carry);  // the kernel has -b at hand, and so works on -h throughout
+    V carry = neg_v(first);  // the kernel has -b at hand, and so works on -h throughout
+    look(u + stride);
     for (int base = v.first; base < v.last; base += cs) {
       const int tile = base + rank, tw = tile * STEPS + warp * S;
       const bool on = tile < v.last && tile * STEPS < len;  // the same for the whole block
       V em1[S], nb[S];
       Aff<V> mine = identity<V>();
-      if (on) {
+      if (on && tw < len) {  // (a warp past the row's end has the identity)
         uint32_t raw[3][S];
+        const uint8_t *src = ring + used % STAGES * STAGE + warp * (STAGE / 3 / NW);
         if (TMA) {
-          const int st = used % STAGES;
-          tc::mbar_wait(&sh.full[st], (used / STAGES) & 1, err, &sh.abort, WAIT_NS);
-          ++used;
-          const uint8_t *src = ring + st * 3 * TILE_BYTES + warp * S * 128 + lane * 4;
+          tc::mbar_wait(&sh.full[used % STAGES], (used / STAGES) & 1, err, &sh.abort, WAIT_NS);
 #pragma unroll
           for (int k = 0; k < 3; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s)
-              raw[k][s] = *reinterpret_cast<const uint32_t *>(src + k * TILE_BYTES + s * 128);
+              raw[k][s] = *reinterpret_cast<const uint32_t *>(src + k * (STAGE / 3) + s * 128 +
+                                                              lane * 4);
         } else {
-          const SeqIn *src[3] = {&p.x, &p.r, &p.i};
+          copy_wait<STAGES - 1>();
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
-            const T *q = static_cast<const T *>(src[k]->p) + tw * src[k]->st + v.b * src[k]->sb + ch;
-#pragma unroll
-            for (int s = 0; s < S; ++s)
-              raw[k][s] = load_raw(q + s * src[k]->st, tw + s < len ? live : 0, words >> k & 1);
+            const SeqIn &in = (&p.x)[k];
+            loose_rows<T, CPT, S>(src + k * (STAGE / 3),
+                                  static_cast<const T *>(in.p) + (int64_t)tw * in.st +
+                                      (int64_t)v.b * in.sb + v.c0,
+                                  in.st * (int64_t)sizeof(T), raw[k]);
           }
         }
         if (small) gates<true>(raw, k2, lim, em1, nb);
@@ -174,6 +208,13 @@ __global__ void __launch_bounds__(NT, PER_SM)
         for (int s = 0; s < S; ++s) {
           mine.e = step(em1[s], mine.e, nb[s]);
           mine.p = fma_v(em1[s], mine.p, mine.p);
+        }
+      }
+      if (on) {
+        ++used;
+        if (!TMA) {
+          __syncwarp();  // the warp's values are in registers
+          issue();
         }
       }
       V h = carry;
@@ -233,7 +274,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
         } else {
 #pragma unroll
           for (int s = 0; s < S; ++s) {
-            if (on) h = step(em1[s], h, nb[s]);
+            if (on && tw < len) h = step(em1[s], h, nb[s]);
             to[s * 32] = tw + s < len ? pack(neg_v(h)) : 0u;
           }
         }
@@ -244,12 +285,12 @@ __global__ void __launch_bounds__(NT, PER_SM)
           store_commit();
         }
       } else {
-        T *y = static_cast<T *>(p.y.p) + tw * p.y.st + v.b * p.y.sb + ch;
+        T *y = static_cast<T *>(p.y.p) + (int64_t)tw * p.y.st + (int64_t)v.b * p.y.sb + ch;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          if (on) h = step(em1[s], h, nb[s]);
+          if (on && tw < len) h = step(em1[s], h, nb[s]);
           if (tw + s < p.T)
-            store_raw(y, tw + s < len ? neg_v(h) : V(0), live, words >> 3 & 1);
+            store_raw(y, tw + s < len ? neg_v(h) : V(0), live, words);
           y += p.y.st;
         }
       }
@@ -261,16 +302,16 @@ __global__ void __launch_bounds__(NT, PER_SM)
 }
 
 template <typename T, bool TMA>
-cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], int words, int *err,
-                cudaStream_t s) {
+cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], int *err, cudaStream_t s) {
   typedef typename Lane<T>::V V;
-  constexpr size_t SMEM0 = sizeof(Smem<V>) + (TMA ? (STAGES * 3 + 1) * TILE_BYTES : 0);
+  constexpr size_t SMEM0 =
+      sizeof(Smem<V>) + STAGES * stage_bytes<T, TMA>() + (TMA ? TILE_BYTES : 0);
   constexpr size_t SMEM_PER_CS = 2 * 32 * sizeof(Aff<V>);
   static const Resident res =
       resident(linrec_fwd_kernel<T, TMA>, NT, MAXCS, SMEM0, SMEM_PER_CS);
   const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res);
   return launch_cut(linrec_fwd_kernel<T, TMA>, pl, NT, SMEM0 + pl.cs * SMEM_PER_CS, s, m[0], m[1],
-                    m[2], m[3], p, pl.cut, words, err);
+                    m[2], m[3], p, pl.cut, word_aligned(p.y.p, p.y.st, p.y.sb, sizeof(T)), err);
 }
 
 template <typename T>
@@ -278,13 +319,10 @@ cudaError_t fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s) {
   CUtensorMap m[4];
   const SeqIn y{p.y.p, p.y.st, p.y.sb, nullptr}, *at[4] = {&p.x, &p.r, &p.i, &y};
   bool tma = vec;
-  int words = 0;
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 4; ++k)
     tma = tma && tc_map_3d(&m[k], at[k]->p, sizeof(T), p.H, p.B, p.T, at[k]->sb, at[k]->st,
                            Shape<T>::CW, 1, k < 3 ? STEPS : S);
-    words |= word_aligned(at[k]->p, at[k]->st, at[k]->sb, sizeof(T)) << k;
-  }
-  return tma ? run<T, true>(p, m, words, err, s) : run<T, false>(p, m, words, err, s);
+  return tma ? run<T, true>(p, m, err, s) : run<T, false>(p, m, err, s);
 }
 
 }  // namespace

@@ -94,19 +94,70 @@ __device__ __forceinline__ void fence_async_proxy() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// ---- one lane's values of a step, as they lie in memory (CPT of them)
+// ---- tiles that TMA cannot address (rows not 16-byte aligned)
+//
+// Each warp copies the rows of its own steps by 16-byte asynchronous copies: the
+// aligned words that hold a row's bytes, so that a row keeps its offset (0 to 15)
+// in shared memory.  The last word is cut at the row's end; the first one's
+// leading bytes are the tensor's or its allocation's, which starts on a word.
 
-// fp32: one channel; bf16: two, as one word where the address allows
-__device__ __forceinline__ uint32_t load_raw(const float *p, int live, bool) {
-  return live > 0 ? __float_as_uint(__ldg(p)) : 0u;
+template <typename IT, int CPT>
+struct Loose {
+  static constexpr int BYTES = 32 * CPT * (int)sizeof(IT), PITCH = BYTES + 16;
+};
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t load_raw(const bf16 *p, int live, bool word) {
-  if (live > 1 && word) return __ldg(reinterpret_cast<const uint32_t *>(p));
-  const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
-  uint32_t v = live > 0 ? __ldg(q) : 0u;
-  if (live > 1) v |= (uint32_t)__ldg(q + 1) << 16;
-  return v;
+
+// `rows` rows from `src` (`pitch` bytes apart), `bytes` of each.  The loops stay
+// loops: unrolled, the kernel outgrew the instruction cache.
+template <typename IT, int CPT>
+__device__ __forceinline__ void copy_rows(uint8_t *dst, const void *src, int64_t pitch, int rows,
+                                          int bytes) {
+  typedef Loose<IT, CPT> L;
+  constexpr int WORDS = L::PITCH / 16, TOGETHER = 32 / WORDS;  // of a row; rows at once
+  const int lane = threadIdx.x % 32, at = lane % WORDS * 16;
+  const int first = lane / WORDS < TOGETHER ? lane / WORDS : rows;
+  const uint8_t *p = static_cast<const uint8_t *>(src) + first * pitch;
+  uint32_t to = tc::smem_u32(dst) + first * L::PITCH + at;
+#pragma unroll 1
+  for (int s = first; s < rows; s += TOGETHER, p += TOGETHER * pitch, to += TOGETHER * L::PITCH) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15), left = off + bytes - at;
+    if (left > 0)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p - off + at),
+                   "r"(min(left, 16))
+                   : "memory");
+  }
 }
+
+// A lane's CPT values of S rows of such a copy, whose source rows start at `src`.
+template <typename IT, int CPT, int S>
+__device__ __forceinline__ void loose_rows(const uint8_t *tile, const void *src, int64_t pitch,
+                                           uint32_t (&raw)[S]) {
+  typedef Loose<IT, CPT> L;
+  constexpr int N = CPT * (int)sizeof(IT);
+  const uint32_t base = tc::smem_u32(tile) + threadIdx.x % 32 * N;
+  uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 15);
+  const uint32_t more = (uint32_t)pitch;
+#pragma unroll
+  for (int s = 0; s < S; ++s, off = (off + more) & 15) {
+    const uint32_t at = base + s * L::PITCH + off;
+    uint32_t w0, w1;
+    if (sizeof(IT) == 4) {
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw[s]) : "r"(at) : "memory");
+    } else {  // the two words that hold them, shifted together
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at & ~3u) : "memory");
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"((at & ~3u) + 4) : "memory");
+      raw[s] = __funnelshift_r(w0, w1, (at & 3) * 8) & (N == 4 ? ~0u : (1u << (8 * (N & 3))) - 1);
+    }
+  }
+}
+
+// ---- one lane's values of a step, as they go out
+
 __device__ __forceinline__ void store_raw(float *p, float v, int live, bool) {
   if (live > 0) *p = v;
 }
@@ -320,7 +371,11 @@ inline Plan plan_cut(int tiles, int B, int groups, const Resident &res) {
   pl.cut.nseg = 1;
   pl.cut.tps = ceil_div(tiles, pl.cut.nseg);
   pl.cut.units = (int)(rows * pl.cut.nseg);
-  pl.grid = (int)std::min<int64_t>(pl.cut.units, res.clusters[pl.cs]) * pl.cs;
+  // a whole number of times the groups, where that many clusters fit: every
+  // cluster then stays with its channels, whose constants it keeps
+  int64_t clusters = std::min<int64_t>(pl.cut.units, res.clusters[pl.cs]);
+  if (clusters < pl.cut.units && clusters >= 4 * groups) clusters -= clusters % groups;
+  pl.grid = (int)clusters * pl.cs;
   return pl;
 }
 

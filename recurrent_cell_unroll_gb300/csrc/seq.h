@@ -24,7 +24,7 @@ struct SeqOut {
 
 struct LinrecFwd {
   int dtype, T, B, H;
-  SeqIn x, r, i;
+  SeqIn x, r, i;  // one behind another: kernels take them by number
   const float *lambda;
   float c;
   const int32_t *lengths;
@@ -35,7 +35,7 @@ struct LinrecFwd {
 
 struct LinrecBwd {
   int dtype, saved, T, B, H;
-  SeqIn x, r, i;
+  SeqIn x, r, i;  // one behind another: kernels take them by number
   int64_t et, eb;  // rows of the exponents: row (t, b) = t*et + b*eb
   const float *lambda;
   float c;
@@ -59,6 +59,27 @@ struct DevMem {
     return e;
   }
 };
+
+// A launch of a kernel that sums what the one before it on the stream wrote, and
+// starts with wait_for_previous(): its blocks are brought up while that one ends.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(void (*fn)(KArgs...), dim3 grid, int threads, cudaStream_t s,
+                         Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+// Until the kernel before this one on the stream has ended and its writes are seen.
+__device__ __forceinline__ void wait_for_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 cudaError_t launch_linrec_fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s,
                               int *launches);

@@ -1,7 +1,6 @@
 """Host logic of the sequence operators that needs no GPU: refusals before any
 CUDA call, and the wrapper's reading of tensor layouts."""
 import ctypes
-from types import SimpleNamespace
 
 import pytest
 import torch
@@ -37,17 +36,21 @@ def test_null_handles_are_refused(lib):
 
 
 def rows(t, shape=None):
-    """SeqOps._rows without a device."""
-    me = SimpleNamespace(_on=lambda t, name: None)
-    return binding.SeqOps._rows(me, t, "t", t.dtype, shape or t.shape)
+    """SeqOps._rows of a tensor taken to be on the handle's device (that of a
+    host tensor is -1): (pointer, row stride, the copy if one was made)."""
+    me = object.__new__(binding.SeqOps)
+    me.h, me.device = None, -1
+    me._refuse_or_copy = lambda t, name, dtype, shape, keep: \
+        keep.append(t.clone(memory_format=torch.contiguous_format)) or keep[0]
+    keep = []
+    return (*me._rows(t, "t", t.dtype, shape or t.shape, keep), keep[0] if keep else None)
 
 
 def test_evenly_spaced_rows_are_used_in_place():
     wide = torch.arange(4 * 6 * 20, dtype=torch.float32).view(4, 6, 20)
     part = wide[..., 5:13]
-    kept, ptr, ld = rows(part)
-    assert kept is part and ptr == part.data_ptr() and ld == 20
-    assert rows(wide)[2] == 20 and rows(wide)[0] is wide
+    assert rows(part) == (part.data_ptr(), 20, None)
+    assert rows(wide) == (wide.data_ptr(), 20, None)
 
 
 @pytest.mark.parametrize("make", [
@@ -60,16 +63,20 @@ def test_evenly_spaced_rows_are_used_in_place():
 ])
 def test_other_layouts_are_copied(make):
     t = make(torch.randn(4, 6, 20))
-    kept, ptr, ld = rows(t)
-    assert kept is not t and kept.is_contiguous() and torch.equal(kept, t) and ld == t.shape[-1]
+    ptr, ld, copy = rows(t)
+    assert copy.is_contiguous() and torch.equal(copy, t)
+    assert ptr == copy.data_ptr() and ld == t.shape[-1]
 
 
 def test_operands_are_checked_before_the_call():
-    with pytest.raises(ValueError):
-        rows(torch.zeros(3, 4), (3, 5))
-    with pytest.raises(ValueError):  # not on a GPU
-        binding.SeqOps._on(SimpleNamespace(device=0), torch.zeros(3), "x")
-    with pytest.raises(ValueError):
-        binding.SeqOps._tbh((3, 4), False)
-    assert binding.SeqOps._tbh((3, 4, 5), False) == (3, 4, 5)
-    assert binding.SeqOps._tbh((3, 4, 5), True) == (4, 3, 5)
+    me = object.__new__(binding.SeqOps)
+    me.h, me.device = None, 0
+    x = torch.zeros(3, 4)
+    for call in (lambda: me._rows(x, "x", x.dtype, x.shape, []),        # not on a GPU
+                 lambda: me._dense(x, "x", x.dtype, x.shape, []),
+                 lambda: me._dense([1.0], "x", x.dtype, x.shape, []),
+                 lambda: me._type(None, "x"), lambda: me._type(x.half(), "x"),
+                 lambda: me._type(x, "x", 3), lambda: me._type(torch.zeros(()), "x")):
+        with pytest.raises(ValueError):
+            call()
+    assert me._type(x, "x", 2) == (torch.float32, binding.RCU_F32, x.shape)
