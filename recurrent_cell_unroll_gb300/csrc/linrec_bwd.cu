@@ -199,11 +199,13 @@ __device__ __forceinline__ void grads(V em1, V nb, V ns, V ng, V nk, V ne, V &h,
   h = fma_v(nb, minus, ah);
 }
 
-template <typename IT, typename T, bool TMA>
+// MAP: only the backward map (P, R) of each segment but the first, from r and dy
+// alone, into `maps`, which the launch after it starts its segments from.
+template <typename IT, typename T, bool TMA, bool MAP>
 __global__ void __launch_bounds__(NT, PER_SM)
     linrec_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap mdy,
-                      const LinrecBwd p, const Cut cut, float *__restrict__ partial, const bool words,
+                      const LinrecBwd p, const Cut cut, void *maps, float *__restrict__ partial, const bool words,
                       int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   constexpr int IN = in_bytes<IT, T, TMA>(), STAGE = stage_bytes<IT, T, TMA>();
@@ -217,12 +219,13 @@ __global__ void __launch_bounds__(NT, PER_SM)
   const int cs = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
   const int stride = gridDim.x / cs, u0 = blockIdx.x / cs;
 
+  const int skip = MAP ? p.B * cut.groups : 0;  // units of the first segment
   // Copies of the live tiles of this block, the last steps first: by TMA (thread
   // 0, the whole tile) or by each warp its own rows.
   int pu = u0, pk = 0, issued = 0;
   auto issue = [&] {
     for (; pu < cut.units; pu += stride, pk = 0) {
-      const Unit v = unit_of(cut, p.B, pu, CW);
+      const Unit v = unit_of(cut, p.B, pu + skip, CW);
       const int len = row_length(p.lengths, v.b, p.T, err);
       int tile;
       do tile = v.last - 1 - (pk++ * cs + rank);
@@ -231,16 +234,18 @@ __global__ void __launch_bounds__(NT, PER_SM)
       uint8_t *dst = ring + issued % STAGES * STAGE;
       if (TMA) {
         uint64_t *bar = &sh.full[issued % STAGES];
-        tc::mbar_arrive_expect_tx(bar, STAGE);
-        tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
+        tc::mbar_arrive_expect_tx(bar, MAP ? STAGE - 2 * IN : STAGE);
         tma_load_3d(dst + IN, &mr, bar, v.c0, v.b, tile * STEPS);
-        tma_load_3d(dst + 2 * IN, &mi, bar, v.c0, v.b, tile * STEPS);
+        if (!MAP) {
+          tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
+          tma_load_3d(dst + 2 * IN, &mi, bar, v.c0, v.b, tile * STEPS);
+        }
         tma_load_3d(dst + 3 * IN, &mdy, bar, v.c0, v.b, tile * STEPS);
       } else {
         const int64_t tw = tile * STEPS + warp * S, b = v.b;
         const int width = min(CW, p.H - v.c0), rows = (int)min(len - tw, (int64_t)S);
 #pragma unroll 1
-        for (int k = 0; k < 3; ++k) {
+        for (int k = MAP ? 1 : 0; k < (MAP ? 2 : 3); ++k) {
           const SeqIn &in = (&p.x)[k];
           copy_rows<IT, CPT>(dst + k * IN + warp * S * IN_ROW,
                              static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
@@ -280,21 +285,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
   V k2;
   Limits lim;
   bool small = false;
-  // What a unit starts with is read while the one before it is worked on.
-  V first;
-  int len1 = p.T;
-  auto look = [&](int u) {
-    if (u >= cut.units) return;
-    const Unit v = unit_of(cut, p.B, u, CW);
-    const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
-    set(first, 0.f);
-    if (p.dh_n) load_v(p.dh_n + (int64_t)v.b * p.H + ch, live, first);
-    len1 = row_length(p.lengths, v.b, p.T, err);
-  };
-  look(u0);
   for (int u = u0; u < cut.units; u += stride) {
-    const Unit v = unit_of(cut, p.B, u, CW);
-    const int len = len1;
+    const Unit v = unit_of(cut, p.B, u + skip, CW);
+    const int len = row_length(p.lengths, v.b, p.T, err);
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
     V nk, nc, sum, zero, minus;
@@ -309,10 +302,14 @@ __global__ void __launch_bounds__(NT, PER_SM)
     const bool whole = v.c0 + CW <= p.H && words;
     set(nk, -1.f / LOG2E);
     nk = mul_v(nk, k2);  // -K
-    nc = neg_v(first);  // the carry, negated: -dL/dh after the steps so far
-    look(u + stride);
+    set(nc, 0.f);
+    if (p.dh_n) load_v(p.dh_n + row, live, nc);
+    nc = neg_v(nc);  // the carry, negated: -dL/dh after the steps so far
+    if (!MAP && v.seg < cut.nseg - 1)
+      nc = apply(chain_segments<V, NW>(maps, cut, p.B, v, CW, cut.nseg - 1, v.seg, -1, sh.part[0]),
+                 nc);
+    Aff<V> all_map = identity<V>();
     sum = zero;
-    V enter = zero;  // the state that enters the tile, read one tile ahead
     int ex = Q8 ? exponent(v, len, v.last - 1 - rank) : 0;
     for (int base = v.last - 1; base >= v.first; base -= cs) {
       const int tile = base - rank, tw = tile * STEPS + warp * S;
@@ -320,7 +317,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
       V em1[S], nb[S], ns[S], ng[S], dy[S], h = zero, fe = zero;
       Aff<V> mine = identity<V>();
       if (on) {
-        load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
+        if (!MAP) load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
         float scale[3][S];
         if (Q8) {
           const float f = power2(ex);
@@ -337,7 +334,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
           for (int k = 0; k < 3; ++k)
 #pragma unroll
             for (int s = 0; s < S; ++s)
-              raw[k][s] = tile_raw<IT, CPT>(src + k * IN + (warp * S + s) * IN_ROW, lane);
+              raw[k][s] = MAP && k != 1
+                              ? 0u
+                              : tile_raw<IT, CPT>(src + k * IN + (warp * S + s) * IN_ROW, lane);
 #pragma unroll
           for (int s = 0; s < S; ++s)
             rawd[s] = tile_raw<T, CPT>(src + 3 * IN + (warp * S + s) * DY_ROW, lane);
@@ -348,6 +347,11 @@ __global__ void __launch_bounds__(NT, PER_SM)
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const SeqIn &in = (&p.x)[k];
+            if (MAP && k != 1) {
+#pragma unroll
+              for (int s = 0; s < S; ++s) raw[k][s] = 0u;
+              continue;
+            }
             loose_rows<IT, CPT, S>(
                 src + k * IN + warp * S * IN_ROW,
                 static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
@@ -435,7 +439,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
 #pragma unroll
           for (int w = NW - 1; w >= 0; --w) {
             if (w == warp) c = nc;
-            nc = apply(get(&sh.part[parity][w][lane]), nc);
+            const Aff<V> a = get(&sh.part[parity][w][lane]);
+            if (MAP) all_map = then(all_map, a);
+            else nc = apply(a, nc);
           }
         }
 #pragma unroll
@@ -444,7 +450,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
             h = fma_v(get(&sh.part[parity][w][lane]).p, h, sh.fwd[parity][w][lane]);
         parity ^= 1;
       }
-      if (tile < v.first) continue;
+      if (MAP || tile < v.first) continue;
       const int64_t tb = tw, b = v.b;
       T *dx = static_cast<T *>(p.dx.p) + tb * p.dx.st + b * p.dx.sb + ch;
       T *dr = static_cast<T *>(p.dr.p) + tb * p.dr.st + b * p.dr.sb + ch;
@@ -491,7 +497,11 @@ __global__ void __launch_bounds__(NT, PER_SM)
         }
       }
     }
-    if (rank == 0 && warp == 0 && p.dh0) store_v(p.dh0 + row, mul_v(nc, minus), live);
+    if (MAP) {
+      if (warp == 0) put(segment_map<V>(maps, cut, p.B, v.seg, v, CW), all_map);
+      continue;
+    }
+    if (v.seg == 0 && rank == 0 && warp == 0 && p.dh0) store_v(p.dh0 + row, mul_v(nc, minus), live);
     if (p.dlambda) {
       __syncthreads();
       sh.sum[warp][lane] = sum;
@@ -557,16 +567,30 @@ cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStr
                 int *launches) {
   constexpr size_t SMEM =
       sizeof(Smem<typename Lane<T>::V>) + STAGES * stage_bytes<IT, T, TMA>();
-  static const Resident res = resident(linrec_bwd_kernel<IT, T, TMA>, NT, MAXCS, SMEM, 0);
-  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res);
+  typedef typename Lane<T>::V V;
+  static const Resident res = resident(linrec_bwd_kernel<IT, T, TMA, false>, NT, MAXCS, SMEM, 0);
+  static const Resident res_map = resident(linrec_bwd_kernel<IT, T, TMA, true>, NT, 1, SMEM, 0);
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, 0.5);
   const int64_t rows = (int64_t)p.B * pl.cut.nseg * pl.cs;
-  float *partial = nullptr;
-  if (p.dlambda) {
-    cudaError_t e = ws.get((size_t)rows * p.H * 4, &partial);
+  // the workspace: the segments' maps, then dlambda's partial sums
+  const size_t map_bytes = pl.cut.nseg > 1 ? (size_t)pl.cut.units * 32 * sizeof(Aff<V>) : 0;
+  const size_t sum_bytes = p.dlambda ? (size_t)rows * p.H * 4 : 0;
+  uint8_t *mem = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (map_bytes + sum_bytes) e = ws.get(map_bytes + sum_bytes, &mem);
+  if (e != cudaSuccess) return e;
+  float *partial = reinterpret_cast<float *>(mem + map_bytes);
+  if (pl.cut.nseg > 1) {
+    Plan first = pl;
+    first.cut.units = pl.cut.units / pl.cut.nseg * (pl.cut.nseg - 1);
+    first.grid = std::min(first.cut.units, res_map.clusters[1]);
+    e = launch_cut(linrec_bwd_kernel<IT, T, TMA, true>, first, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
+                   v.m[3], p, first.cut, (void *)mem, partial, v.words, err);
     if (e != cudaSuccess) return e;
+    ++*launches;
   }
-  cudaError_t e = launch_cut(linrec_bwd_kernel<IT, T, TMA>, pl, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
-                             v.m[3], p, pl.cut, partial, v.words, err);
+  e = launch_cut(linrec_bwd_kernel<IT, T, TMA, false>, pl, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
+                 v.m[3], p, pl.cut, (void *)mem, partial, v.words, err);
   ++*launches;
   if (e != cudaSuccess || !p.dlambda) return e;
   ++*launches;

@@ -76,12 +76,14 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, con
   }
 }
 
-template <typename T, bool TMA>
+// MAP: only the affine map of each segment but the last, into `maps`, which the
+// launch after it starts its segments from.
+template <typename T, bool TMA, bool MAP>
 __global__ void __launch_bounds__(NT, PER_SM)
     linrec_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap my,
                       const LinrecFwd p, const Cut cut,
-                      const bool words, int *err) {
+                      void *maps, const bool words, int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   typedef typename Lane<T>::V V;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -169,6 +171,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
     }
     V carry = neg_v(first);  // the kernel has -b at hand, and so works on -h throughout
     look(u + stride);
+    Aff<V> whole = identity<V>();
+    if (!MAP && v.seg > 0)
+      carry = apply(chain_segments<V, NW>(maps, cut, p.B, v, CW, 0, v.seg, 1, sh.part[0]), carry);
     for (int base = v.first; base < v.last; base += cs) {
       const int tile = base + rank, tw = tile * STEPS + warp * S;
       const bool on = tile < v.last && tile * STEPS < len;  // the same for the whole block
@@ -253,12 +258,14 @@ __global__ void __launch_bounds__(NT, PER_SM)
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
             if (w == warp) h = carry;
-            carry = apply(get(&sh.part[parity][w][lane]), carry);
+            const Aff<V> a = get(&sh.part[parity][w][lane]);
+            if (MAP) whole = then(whole, a);
+            else carry = apply(a, carry);
           }
         }
         parity ^= 1;
       }
-      if (tile >= v.last) continue;
+      if (MAP || tile >= v.last) continue;
       if (warp == 0 && p.states)
         store_v(p.states + (int64_t)tile * p.B * p.H + row, neg_v(h), live);
       if (TMA) {
@@ -295,42 +302,62 @@ __global__ void __launch_bounds__(NT, PER_SM)
         }
       }
     }
-    if (rank == 0 && warp == 0 && p.h_n) store_v(p.h_n + row, neg_v(carry), live);
+    if (MAP) {
+      if (warp == 0) put(segment_map<V>(maps, cut, p.B, v.seg, v, CW), whole);
+    } else if (rank == 0 && warp == 0 && p.h_n && v.seg == cut.nseg - 1) store_v(p.h_n + row, neg_v(carry), live);
   }
   if (TMA && lane == 0) store_wait();
   if (cs > 1) tc::cluster_sync();  // no block leaves while a peer may still write to it
 }
 
 template <typename T, bool TMA>
-cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], int *err, cudaStream_t s) {
+cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], DevMem &ws, int *err, cudaStream_t s,
+                int *launches) {
   typedef typename Lane<T>::V V;
   constexpr size_t SMEM0 =
       sizeof(Smem<V>) + STAGES * stage_bytes<T, TMA>() + (TMA ? TILE_BYTES : 0);
   constexpr size_t SMEM_PER_CS = 2 * 32 * sizeof(Aff<V>);
   static const Resident res =
-      resident(linrec_fwd_kernel<T, TMA>, NT, MAXCS, SMEM0, SMEM_PER_CS);
-  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res);
-  return launch_cut(linrec_fwd_kernel<T, TMA>, pl, NT, SMEM0 + pl.cs * SMEM_PER_CS, s, m[0], m[1],
-                    m[2], m[3], p, pl.cut, word_aligned(p.y.p, p.y.st, p.y.sb, sizeof(T)), err);
+      resident(linrec_fwd_kernel<T, TMA, false>, NT, MAXCS, SMEM0, SMEM_PER_CS);
+  static const Resident res_map =
+      resident(linrec_fwd_kernel<T, TMA, true>, NT, 1, SMEM0, SMEM_PER_CS);
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, 0.8);
+  const size_t smem = SMEM0 + pl.cs * SMEM_PER_CS;
+  const bool words = word_aligned(p.y.p, p.y.st, p.y.sb, sizeof(T));
+  void *maps = nullptr;
+  if (pl.cut.nseg > 1) {
+    Plan first = pl;
+    first.cut.units = pl.cut.units / pl.cut.nseg * (pl.cut.nseg - 1);
+    first.grid = std::min(first.cut.units, res_map.clusters[1]);
+    cudaError_t e = ws.get((size_t)first.cut.units * 32 * sizeof(Aff<V>), &maps);
+    if (e == cudaSuccess)
+      e = launch_cut(linrec_fwd_kernel<T, TMA, true>, first, NT, smem, s, m[0], m[1], m[2], m[3], p,
+                     first.cut, maps, words, err);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
+  ++*launches;
+  return launch_cut(linrec_fwd_kernel<T, TMA, false>, pl, NT, smem, s, m[0], m[1], m[2], m[3], p,
+                    pl.cut, maps, words, err);
 }
 
 template <typename T>
-cudaError_t fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s) {
+cudaError_t fwd(const LinrecFwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s, int *launches) {
   CUtensorMap m[4];
   const SeqIn y{p.y.p, p.y.st, p.y.sb, nullptr}, *at[4] = {&p.x, &p.r, &p.i, &y};
   bool tma = vec;
   for (int k = 0; k < 4; ++k)
     tma = tma && tc_map_3d(&m[k], at[k]->p, sizeof(T), p.H, p.B, p.T, at[k]->sb, at[k]->st,
                            Shape<T>::CW, 1, k < 3 ? STEPS : S);
-  return tma ? run<T, true>(p, m, err, s) : run<T, false>(p, m, err, s);
+  return tma ? run<T, true>(p, m, ws, err, s, launches) : run<T, false>(p, m, ws, err, s, launches);
 }
 
 }  // namespace
 
-cudaError_t launch_linrec_fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s,
+cudaError_t launch_linrec_fwd(const LinrecFwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
                               int *launches) {
-  ++*launches;
-  return p.dtype == RCU_BF16 ? fwd<bf16>(p, err, vec, s) : fwd<float>(p, err, vec, s);
+  return p.dtype == RCU_BF16 ? fwd<bf16>(p, ws, err, vec, s, launches)
+                             : fwd<float>(p, ws, err, vec, s, launches);
 }
 
 }  // namespace rcu

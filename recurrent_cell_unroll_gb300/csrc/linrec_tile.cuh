@@ -301,6 +301,36 @@ __device__ __forceinline__ void put_peer(float4 *at, uint64_t *bar, int rank, co
                   tc::mapa_shared(tc::smem_u32(bar), rank));
 }
 
+// ---- segments: the maps that a first launch leaves, [segment][row][group][lane]
+
+template <typename V>
+__device__ __forceinline__ typename Slot<V>::type *segment_map(void *maps, const Cut &cut, int B,
+                                                               int seg, const Unit &v, int cw) {
+  return static_cast<typename Slot<V>::type *>(maps) +
+         (((int64_t)seg * B + v.b) * cut.groups + v.c0 / cw) * 32 + threadIdx.x % 32;
+}
+// The map of segments [from, to) in steps of `by` (forwards or backwards), the
+// block's NWARP warps taking a share each: all its threads call this.
+template <typename V, int NWARP>
+__device__ __forceinline__ Aff<V> chain_segments(void *maps, const Cut &cut, int B, const Unit &v,
+                                                 int cw, int from, int to, int by,
+                                                 typename Slot<V>::type (*part)[32]) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int n = (to - from) * by, each = ceil_div(n, NWARP);
+  Aff<V> a = identity<V>();
+#pragma unroll 8
+  for (int q = warp * each; q < min(n, (warp + 1) * each); ++q)
+    a = then(a, get(segment_map<V>(maps, cut, B, from + q * by, v, cw)));
+  __syncthreads();
+  put(&part[warp][lane], a);
+  __syncthreads();
+  a = identity<V>();
+#pragma unroll
+  for (int w = 0; w < NWARP; ++w) a = then(a, get(&part[w][lane]));
+  __syncthreads();
+  return a;
+}
+
 // ---- host side
 
 inline bool word_aligned(const void *p, int64_t st, int64_t sb, int bytes) {
@@ -355,7 +385,13 @@ Resident resident(void (*fn)(KArgs...), int threads, int max_cs, size_t smem0, s
 // (backward from 8 bits, T=1000 B=32 H=1024: 145 us without clusters, 159 in
 // pairs, though 16 turns each; 32 rows of 65536 steps forward: 250 us with 12
 // blocks a row, 290 with 8).
-inline Plan plan_cut(int tiles, int B, int groups, const Resident &res) {
+//
+// With few rows, clusters leave most of the GPU idle: then the sequence is cut into
+// segments that run as rows of their own, after a first launch (costing `share` of
+// the second) has reduced each segment to its affine map.  One row of 65536 steps x
+// 256 channels, bf16: forward 159 us in a cluster of 12, SEGF us in segments;
+// backward 389 and SEGB.
+inline Plan plan_cut(int tiles, int B, int groups, const Resident &res, double share) {
   Plan pl;
   const int64_t rows = (int64_t)B * groups;
   double best = 0;
@@ -366,10 +402,13 @@ inline Plan plan_cut(int tiles, int B, int groups, const Resident &res) {
     const double cost = waves * ceil_div(tiles, cs) * (cs > 1 ? 1.3 : 1.0);
     if (cs == 1 || cost < best) best = cost, pl.cs = cs;
   }
+  pl.cut.nseg = 1;
+  const int nseg = (int)std::min<int64_t>(res.clusters[1] / rows, tiles / 4);
+  if (nseg > 1 && (1 + share) * ceil_div(tiles, nseg) + 6 < best) pl.cut.nseg = nseg, pl.cs = 1;
   pl.cut.groups = groups;
   pl.cut.tiles = tiles;
-  pl.cut.nseg = 1;
   pl.cut.tps = ceil_div(tiles, pl.cut.nseg);
+  pl.cut.nseg = ceil_div(tiles, pl.cut.tps);
   pl.cut.units = (int)(rows * pl.cut.nseg);
   // a whole number of times the groups, where that many clusters fit: every
   // cluster then stays with its channels, whose constants it keeps

@@ -51,6 +51,7 @@ struct LinrecBwd {
 // and is the handle's.
 struct DevMem {
   virtual cudaError_t grow(size_t bytes, void **p) = 0;
+  cudaError_t get(size_t bytes, void **p) { return grow(bytes, p); }
   template <typename T>
   cudaError_t get(size_t bytes, T **p) {
     void *v = nullptr;
@@ -81,7 +82,7 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-cudaError_t launch_linrec_fwd(const LinrecFwd &p, int *err, bool vec, cudaStream_t s,
+cudaError_t launch_linrec_fwd(const LinrecFwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
                               int *launches);
 cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
                               int *launches);
