@@ -543,9 +543,12 @@ RCU_API int rssm_destroy(rcu_rssm_t h);
 
 /*
  * A handle holds what the calls below keep between launches: the device error
- * word and a workspace for partial sums that grows on demand.  It owns no
- * weights: parameters that an optimiser updates every step are passed to each
- * call.  As with the other handles, one stream at a time uses it.
+ * word and a workspace for partial sums that grows on demand (so a call made
+ * while its stream is captured into a CUDA graph has to have run once at that
+ * size before; what a captured graph uses is kept until rcu_seq_destroy).  It
+ * owns no weights: parameters that an optimiser updates every step are passed
+ * to each call.  As with the other handles, one stream at a time uses it, and
+ * the current device has to be the one that it was made on.
  *
  * Matrices are given by a pointer and a row stride ld in elements (>= the row
  * width; rows are dense), so that a slice of a wider matrix, for example one

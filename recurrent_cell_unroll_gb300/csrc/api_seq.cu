@@ -1,9 +1,11 @@
 // Host side of the C ABI's sequence operators (include/rcu.h): the handle,
 // argument checks and the launches of the gated linear recurrence (linrec.cu),
 // layer norm (layernorm.cu) and 8-bit activation checkpoints (act8.cu).
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
+#include <vector>
 
 #include "rcu.h"
 #include "common.cuh"
@@ -17,10 +19,22 @@ struct rcu_seq_s : EventProfiler, DevMem {
   int device, nsm;
   DevBuf ctl;  // device error word
   DevBuf ws;   // partial sums of the call in flight
+  // An outgrown buffer lives as long as the handle: a captured graph may still
+  // use it.  Growing to twice the size at least bounds what they hold together.
+  std::vector<void *> outgrown;
   cudaError_t grow(size_t bytes, void **p) override {
+    if (bytes > ws.n && ws.p) {
+      outgrown.push_back(ws.p);
+      bytes = std::max(bytes, 2 * ws.n);
+      ws.p = nullptr;
+      ws.n = 0;
+    }
     const cudaError_t e = ws.ensure(bytes);
     *p = ws.p;
     return e;
+  }
+  ~rcu_seq_s() {
+    for (void *p : outgrown) cudaFree(p);
   }
   int force_path = 0;
   int launches = 0;
@@ -35,6 +49,17 @@ void begin(rcu_seq *h, const char *name, cudaStream_t s) {
 }
 
 bool dtype_ok(int dtype) { return dtype == RCU_F32 || dtype == RCU_BF16; }
+
+// The handle, and that its device is the current one.
+int check_handle(const char *fn, rcu_seq *h) {
+  if (!h) return fail(RCU_ERR_INVALID, "%s: NULL handle", fn);
+  int dev = -1;
+  CU(cudaGetDevice(&dev));
+  if (dev != h->device)
+    return fail(RCU_ERR_INVALID, "%s: the handle belongs to device %d, the current one is %d", fn,
+                h->device, dev);
+  return RCU_OK;
+}
 
 // A matrix operand: present, and its rows do not overlap.
 int check_mat(const char *fn, const char *name, const void *p, int64_t ld, int width,
@@ -70,7 +95,8 @@ SeqOut seq_out(int layout, int T, int B, void *p, int64_t ld) {
 
 int check_linrec(const char *fn, rcu_seq *h, int dtype, int layout, int T, int B, int H,
                  const float *lambda, double c) {
-  if (!h) return fail(RCU_ERR_INVALID, "%s: NULL handle", fn);
+  const int rc = check_handle(fn, h);
+  if (rc != RCU_OK) return rc;
   if (!dtype_ok(dtype)) return fail(RCU_ERR_INVALID, "%s: dtype must be RCU_F32 or RCU_BF16", fn);
   if (layout != RCU_TIME_FIRST && layout != RCU_BATCH_FIRST)
     return fail(RCU_ERR_INVALID, "%s: unknown layout %d", fn, layout);
@@ -84,7 +110,8 @@ int check_linrec(const char *fn, rcu_seq *h, int dtype, int layout, int T, int B
 }
 
 int check_rows(const char *fn, rcu_seq *h, int dtype, int64_t rows, int n) {
-  if (!h) return fail(RCU_ERR_INVALID, "%s: NULL handle", fn);
+  const int rc = check_handle(fn, h);
+  if (rc != RCU_OK) return rc;
   if (!dtype_ok(dtype)) return fail(RCU_ERR_INVALID, "%s: dtype must be RCU_F32 or RCU_BF16", fn);
   if (rows < 0 || n < 1)
     return fail(RCU_ERR_INVALID, "%s: rows must be >= 0 and n >= 1 (got %lld, %d)", fn,

@@ -53,8 +53,8 @@ __device__ __forceinline__ uint32_t tile_raw(const uint8_t *row, int lane) {
 // 8-bit codes: c + 128 in the low bits of 2^23 is exact in fp32.  A code of -128
 // (not a number) comes out as -128 here; any_nan tells whether a lane has one, and
 // its results are made NaN afterwards.
-__device__ __forceinline__ float code_value(uint32_t biased) {
-  return __uint_as_float(0x4b000000u | biased) - 8388736.f;
+__device__ __forceinline__ float code_bits(uint32_t biased, int j) {  // 2^23 + byte j
+  return __uint_as_float(__byte_perm(biased, 0x4b000000u, 0x7540 + j));
 }
 template <int CPT>
 __device__ __forceinline__ uint32_t nan_flags(uint32_t raw) {  // a byte of raw ^ 0x80.. is 0
@@ -76,7 +76,7 @@ template <>
 struct Decode<int8_t, F2> {
   __device__ __forceinline__ static F2 x(uint32_t v, float scale) {
     v ^= 0x8080u;
-    return mul2(f2(code_value(v & 0xffu), code_value(v >> 8)), f2(scale));
+    return mul2(add2(f2(code_bits(v, 0), code_bits(v, 1)), f2(-8388736.f)), f2(scale));
   }
   __device__ __forceinline__ static F2 r(uint32_t v, float scale, const Limits &l) {
     const F2 f = i(v, scale);  // not limited as bf16: the channels' limits, widened
@@ -101,7 +101,7 @@ struct Decode<float, float> {
 template <>
 struct Decode<int8_t, float> {
   __device__ __forceinline__ static float x(uint32_t v, float scale) {
-    return code_value(v ^ 0x80u) * scale;
+    return (code_bits(v ^ 0x80u, 0) - 8388736.f) * scale;
   }
   __device__ __forceinline__ static float r(uint32_t v, float scale, const Limits &l) {
     return limit_r(x(v, scale), l);

@@ -291,6 +291,42 @@ def test_linrec_long_sequence_of_few_channels(ops, path, dtype):
     check_rec(ops, 4111, 2, 33, dtype, lengths=[4111, 2049])
 
 
+@pytest.mark.parametrize("T,B,H,lengths", [(20000, 1, 33, None), (12345, 2, 40, [12345, 9000]),
+                                           (16000, 1, 16, [0])])
+def test_linrec_segments(ops, path, T, B, H, lengths):
+    """So few channels that the sequence runs in segments (two launches a pass)."""
+    check_rec(ops, T, B, H, "bf16", lengths=lengths)
+    x, r, i, lam, h0 = (t.cuda() for t in rec_inputs(T, B, H, "bf16"))
+    _, _, st = ops.linrec_forward(x, r, i, lam, h0=h0, states=True)
+    assert ops.launch_count() == 2
+    ops.linrec_backward(x, x, r, i, lam, st)
+    assert ops.launch_count() == 3
+
+
+def test_linrec_nan_codes(ops, path):
+    """A code that is not a number reaches what its value enters, and no more."""
+    T, B, H = 70, 1, 64
+    for dtype in ("f32", "bf16"):
+        x, r, i, lam, h0 = (t.cuda() for t in rec_inputs(T, B, H, dtype, 21))
+        _, _, st = ops.linrec_forward(x, r, i, lam, h0=h0, states=True)
+        dy = torch.ones_like(x)
+        saved = [ops.act8_pack(t) for t in (x, r, i)]
+        clean = ops.linrec_backward(dy, *saved, lam, st)
+        for k in range(3):
+            codes = saved[k][0].clone()
+            codes[66, 0, 5] = -128
+            bad = list(saved)
+            bad[k] = (codes, saved[k][1])
+            got = ops.linrec_backward(dy, *bad, lam, st)
+            wide = [act8_values(a.cpu(), b.cpu()) for a, b in bad]
+            ref = rec_backward(dy.cpu().double(), *wide, lam.cpu().double(), st.cpu().double(), 8.0,
+                               torch.tensor([T]), None)
+            for a, b, c in zip(got[:3], ref, clean):
+                assert torch.equal(torch.isnan(a).cpu(), torch.isnan(b))
+                same = ~torch.isnan(a)
+                assert torch.equal(a[same], c[same])
+
+
 def test_linrec_extreme_gates(ops, path):
     """Logits from -90 to 90 and infinite ones, decay parameters from -30 to 30:
     decays of exactly 0 and 1, input scales of 0, no NaN anywhere."""
