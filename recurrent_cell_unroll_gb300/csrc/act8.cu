@@ -3,7 +3,7 @@
 // Bound by memory.  A block of 64 values belongs to as many lanes as hold it in
 // 16-byte words (8 of bf16, 16 of fp32): its largest magnitude is a maximum over
 // those lanes, and the codes go out 8 or 4 bytes a lane.  Rows that are not
-// 16-byte aligned, or end inside a block, go value by value, a warp a block.
+// 16-byte aligned, or not of whole words, go value by value, a warp a block.
 #include <algorithm>
 
 #include "act8.cuh"
@@ -196,48 +196,75 @@ __global__ void __launch_bounds__(NT)
   }
 }
 
+// Value by value: a warp has UNROLL blocks at once, two values of each a lane.
 template <typename T>
 __global__ void __launch_bounds__(NT)
-    act8_pack_kernel(int64_t rows, int n, const T *__restrict__ x, int64_t ldx,
+    act8_pack_kernel(Divide by_row, int64_t rows, int n, const T *__restrict__ x, int64_t ldx,
                      int8_t *__restrict__ codes, int64_t ldc, int8_t *__restrict__ exps) {
   const int nb = ceil_div(n, BLOCK8), lane = threadIdx.x % 32;
-  for (int64_t id = (int64_t)blockIdx.x * (NT / 32) + threadIdx.x / 32; id < rows * nb;
-       id += (int64_t)gridDim.x * (NT / 32)) {  // a warp per block
-    const int64_t row = id / nb;
-    const int c0 = (int)(id % nb) * BLOCK8;
-    float v[2], top = 0.f;
+  const int64_t total = rows * nb;
+  for (int64_t id = ((int64_t)blockIdx.x * (NT / 32) + threadIdx.x / 32) * UNROLL; id < total;
+       id += (int64_t)gridDim.x * (NT / 32) * UNROLL) {
+    float v[UNROLL][2];
+    int64_t row[UNROLL];
+    int c0[UNROLL];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = c0 + 32 * j + lane;
-      v[j] = c < n ? to_f(x[row * ldx + c]) : 0.f;
-      if (isfinite(v[j])) top = fmaxf(top, fabsf(v[j]));
+    for (int q = 0; q < UNROLL; ++q) {
+      row[q] = by_row(id + q);
+      c0[q] = id + q < total ? (int)(id + q - row[q] * nb) * BLOCK8 : n;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = c0[q] + 32 * j + lane;
+        v[q][j] = c < n ? to_f(x[row[q] * ldx + c]) : 0.f;
+      }
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = act8_exponent(top);
+    for (int q = 0; q < UNROLL; ++q) {
+      uint32_t top = 0;  // fp32 bits order like the magnitudes
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = c0 + 32 * j + lane;
-      if (c < n) codes[row * ldc + c] = (int8_t)act8_code(v[j], power2(-e));
+      for (int j = 0; j < 2; ++j)
+        if (isfinite(v[q][j])) top = max(top, __float_as_uint(v[q][j]) & 0x7fffffffu);
+      const int e = act8_exponent(__uint_as_float(__reduce_max_sync(0xffffffffu, top)));
+      const float inv = power2(-e);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = c0[q] + 32 * j + lane;
+        if (c < n) codes[row[q] * ldc + c] = (int8_t)act8_code(v[q][j], inv);
+      }
+      if (lane == 0 && c0[q] < n) exps[id + q] = (int8_t)e;
     }
-    if (lane == 0) exps[id] = (int8_t)e;
   }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(NT)
-    act8_unpack_kernel(int64_t rows, int n, const int8_t *__restrict__ codes, int64_t ldc,
-                       const int8_t *__restrict__ exps, T *__restrict__ y, int64_t ldy) {
+    act8_unpack_kernel(Divide by_row, int64_t rows, int n, const int8_t *__restrict__ codes,
+                       int64_t ldc, const int8_t *__restrict__ exps, T *__restrict__ y,
+                       int64_t ldy) {
   const int nb = ceil_div(n, BLOCK8), lane = threadIdx.x % 32;
-  for (int64_t id = (int64_t)blockIdx.x * (NT / 32) + threadIdx.x / 32; id < rows * nb;
-       id += (int64_t)gridDim.x * (NT / 32)) {
-    const int64_t row = id / nb;
-    const int c0 = (int)(id % nb) * BLOCK8, e = exps[id];
+  const int64_t total = rows * nb;
+  for (int64_t id = ((int64_t)blockIdx.x * (NT / 32) + threadIdx.x / 32) * UNROLL; id < total;
+       id += (int64_t)gridDim.x * (NT / 32) * UNROLL) {
+    int code[UNROLL][2], e[UNROLL], c0[UNROLL];
+    int64_t row[UNROLL];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = c0 + 32 * j + lane;
-      if (c < n) y[row * ldy + c] = from_f<T>(act8_value(codes[row * ldc + c], e));
+    for (int q = 0; q < UNROLL; ++q) {
+      row[q] = by_row(id + q);
+      c0[q] = id + q < total ? (int)(id + q - row[q] * nb) * BLOCK8 : n;
+      e[q] = c0[q] < n ? exps[id + q] : 0;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = c0[q] + 32 * j + lane;
+        code[q][j] = c < n ? codes[row[q] * ldc + c] : 0;
+      }
     }
+#pragma unroll
+    for (int q = 0; q < UNROLL; ++q)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = c0[q] + 32 * j + lane;
+        if (c < n) y[row[q] * ldy + c] = from_f<T>(act8_value(code[q][j], e[q]));
+      }
   }
 }
 
@@ -258,8 +285,8 @@ void pack(int64_t rows, int n, const T *x, int64_t ldx, int8_t *codes, int64_t l
   const int64_t words = rows * nb * Wide<T>::LANES;
   const int grid = grid_for((words + UNROLL - 1) / UNROLL, nsm);
   if (!vec || n % VEC || !aligned(x, ldx, sizeof(T), 16) || !aligned(codes, ldc, 1, VEC))
-    act8_pack_kernel<T><<<grid_for(rows * nb * 32, nsm), NT, 0, s>>>(rows, n, x, ldx, codes, ldc,
-                                                                      exps);
+    act8_pack_kernel<T><<<grid_for((rows * nb + UNROLL - 1) / UNROLL * 32, nsm), NT, 0, s>>>(
+        divide(rows * nb, nb), rows, n, x, ldx, codes, ldc, exps);
   else if (n % BLOCK8 == 0 && ldx == n && ldc == n)
     act8_pack_wide_kernel<T, true><<<grid, NT, 0, s>>>(Divide{}, rows, n, x, ldx, codes, ldc, exps);
   else
@@ -270,11 +297,12 @@ template <typename T>
 void unpack(int64_t rows, int n, const int8_t *codes, int64_t ldc, const int8_t *exps, T *y,
             int64_t ldy, int nsm, bool vec, cudaStream_t s) {
   constexpr int VEC = Wide<T>::VEC;
+  const int nb = ceil_div(n, BLOCK8);
   const int64_t words = rows * (n / VEC);
   const int grid = grid_for((words + UNROLL - 1) / UNROLL, nsm);
   if (!vec || n % VEC || !aligned(y, ldy, sizeof(T), 16) || !aligned(codes, ldc, 1, VEC))
-    act8_unpack_kernel<T><<<grid_for(rows * ceil_div(n, BLOCK8) * 32, nsm), NT, 0, s>>>(
-        rows, n, codes, ldc, exps, y, ldy);
+    act8_unpack_kernel<T><<<grid_for((rows * nb + UNROLL - 1) / UNROLL * 32, nsm), NT, 0, s>>>(
+        divide(rows * nb, nb), rows, n, codes, ldc, exps, y, ldy);
   else if (n % BLOCK8 == 0 && ldy == n && ldc == n)
     act8_unpack_wide_kernel<T, true><<<grid, NT, 0, s>>>(Divide{}, rows, n, codes, ldc, exps, y,
                                                          ldy);

@@ -283,7 +283,7 @@ extern "C" int rcu_linrec_step(rcu_seq *h, int dtype, int B, int H, const void *
     return fail(RCU_ERR_INVALID, "rcu_linrec_step: %d state rows for %d requests", slots, B);
   begin(h, "linrec_step", s);
   CU(launch_linrec_step(dtype, B, H, x, ldx, r, ldr, i, ldi, lambda, (float)c, state, slots, slot,
-                        y, ldy, (int *)h->ctl.p, !h->force_path, s, &h->launches));
+                        y, ldy, (int *)h->ctl.p, h->nsm, !h->force_path, s, &h->launches));
   h->prof_end(s);
   return RCU_OK;
 }

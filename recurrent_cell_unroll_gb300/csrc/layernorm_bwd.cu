@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(32 * W * R)
       w[k][j] = c < p.n ? (p.weight ? __ldg(p.weight + c) : 1.f) : 0.f;
       gw[k][j] = gb[k][j] = 0.f;
     }
-  // 16 warps a row leave no registers for a second row's values
-  constexpr bool AHEAD = W < 16;
+  // 16 warps a row, or a register for every value, leave none for a second row
+  constexpr bool AHEAD = W < 16 && VEC > 1;
   if (AHEAD) load((int64_t)blockIdx.x * R + sub);
   for (int64_t base = (int64_t)blockIdx.x * R; base < p.rows; base += step) {
     const int64_t row = base + sub;

@@ -89,7 +89,8 @@ cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, bool vec
 cudaError_t launch_linrec_step(int dtype, int B, int H, const void *x, int64_t ldx, const void *r,
                                int64_t ldr, const void *i, int64_t ldi, const float *lambda,
                                float c, float *state, int slots, const int32_t *slot, void *y,
-                               int64_t ldy, int *err, bool vec, cudaStream_t s, int *launches);
+                               int64_t ldy, int *err, int nsm, bool vec, cudaStream_t s,
+                               int *launches);
 
 struct LnFwd {
   int dtype;
