@@ -821,12 +821,14 @@ class SeqOps:
         return y, h_n, st
 
     def linrec_backward(self, dy, x, r, i, lam, states, c=8.0, lengths=None, dh_n=None,
-                        batch_first=False, stream=None):
+                        batch_first=False, out=None, stream=None):
         """dx, dr, di (of dy's type), dlam [H] and dh0 [B, H].  x, r, i: the
-        forward's inputs, or all three as act8_pack's (codes, exponents)."""
+        forward's inputs, or all three as act8_pack's (codes, exponents).  out:
+        a contiguous tensor like dy but 3H wide, for the gradient of a fused
+        projection: dx, dr, di are then its three parts."""
         if stream is not None:
             return self._on_stream(stream, self.linrec_backward, dy, x, r, i, lam, states, c,
-                                   lengths, dh_n, batch_first)
+                                   lengths, dh_n, batch_first, out)
         dtype, dt, shape = self._type(dy, "dy", 3)
         T, B, H = shape
         if batch_first:
@@ -842,15 +844,23 @@ class SeqOps:
         np_ = self._dense(lengths, "lengths", torch.int32, (B,), keep)
         sp = self._dense(states, "states", f32, (-(-T // RCU_LINREC_CHUNK), B, H), keep)
         hp = self._dense(dh_n, "dh_n", f32, (B, H), keep)
-        dx = torch.empty(shape, dtype=dtype, device=dev)
-        dr = torch.empty(shape, dtype=dtype, device=dev)
-        di = torch.empty(shape, dtype=dtype, device=dev)
+        if out is None:
+            dx = torch.empty(shape, dtype=dtype, device=dev)
+            dr = torch.empty(shape, dtype=dtype, device=dev)
+            di = torch.empty(shape, dtype=dtype, device=dev)
+            ld = H
+        else:
+            if not isinstance(out, torch.Tensor) or not out.is_contiguous():
+                raise ValueError("out must be a contiguous tensor")
+            self._dense(out, "out", dtype, (*shape[:2], 3 * H), keep)
+            dx, dr, di = out[..., :H], out[..., H:2 * H], out[..., 2 * H:]
+            ld = 3 * H
         dlam = torch.empty((H,), dtype=f32, device=dev)
         dh0 = torch.empty((B, H), dtype=f32, device=dev)
         _check(self.lib.rcu_linrec_backward(
             self.h, dt, dt if xe is None else RCU_I8, 1 if batch_first else 0, T, B, H, xp, xl,
-            rp, rl, ip, il, xe, re, ie, lp, c, np_, sp, yp, yl, hp, dx.data_ptr(), H,
-            dr.data_ptr(), H, di.data_ptr(), H, dlam.data_ptr(), dh0.data_ptr(),
+            rp, rl, ip, il, xe, re, ie, lp, c, np_, sp, yp, yl, hp, dx.data_ptr(),
+            ld, dr.data_ptr(), ld, di.data_ptr(), ld, dlam.data_ptr(), dh0.data_ptr(),
             self._raw_stream()))
         return dx, dr, di, dlam, dh0
 

@@ -823,3 +823,61 @@ def test_c_entry_refusals(ops):
     assert lib.rcu_act8_unpack(h, 0, 8, 8, None, 8, p, p, 8, None) == binding.RCU_ERR_INVALID
     torch.cuda.synchronize()
     assert ops.status() == 0
+
+
+# --------------------------------------------------------------------------- together
+
+def test_backward_into_a_fused_gradient(ops, path):
+    T, B, H = 130, 2, 72
+    x, r, i, lam, h0 = (t.cuda() for t in rec_inputs(T, B, H, "bf16", 18))
+    z = torch.cat([x, r, i], -1)
+    parts = z.chunk(3, -1)
+    y, _, st = ops.linrec_forward(*parts, lam, h0=h0, states=True)
+    dy = torch.randn_like(y)
+    want = ops.linrec_backward(dy, x, r, i, lam, st)
+    dz = torch.full_like(z, 7.0)
+    got = ops.linrec_backward(dy, *parts, lam, st, out=dz)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert torch.equal(dz, torch.cat(want[:3], -1))
+    with pytest.raises(ValueError):
+        ops.linrec_backward(dy, *parts, lam, st, out=dz[..., :-1])
+
+
+@pytest.mark.parametrize("act8", [False, True])
+def test_block_gradients(act8):
+    """The stack's gradients against torch autograd on the same formulas in 64
+    bits (fp32 products); from 8-bit checkpoints within their steps."""
+    from recurrent_cell_unroll_gb300.linrec_block import C, LinRecStack
+    net = LinRecStack(2, 24, 40, dtype=torch.float32)
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(70, 3, 24, generator=g)
+    lengths = torch.tensor([70, 33, 1])
+    y, state = net.forward(x.cuda(), lengths=lengths.int().cuda(), act8=act8)
+    wy, ws = torch.randn(y.shape, generator=g), torch.randn(state.shape, generator=g)
+    ((y * wy.cuda()).sum() + (state * ws.cuda()).sum()).backward()
+    leaves = [{k: t.detach().cpu().double().requires_grad_() for k, t in b.items()} for b in net.blocks]
+    u, v, after = x.double(), torch.zeros_like(x).double(), []
+    for b in leaves:
+        u = u + v
+        n, _, _ = ln_forward(u, b["weight"], b["bias"], 1e-5)
+        out, h, _ = rec_forward(*(n @ b["w_in"]).chunk(3, -1), b["lam"], C, lengths, None)
+        v = out @ b["w_out"]
+        after.append(h)
+    (((u + v) * wy.double()).sum() + (torch.stack(after) * ws.double()).sum()).backward()
+    close(y, (u + v).detach(), "y")
+    for b, ref in zip(net.blocks, leaves):
+        for k, t in b.items():
+            top = float(ref[k].grad.abs().max())
+            off = float((t.grad.cpu().double() - ref[k].grad).abs().max())
+            # products in fp32 (TF32 is off by default) round some 2^-20 of their terms' scale;
+            # 8 bits: half a step of 1/63 of a block's largest value, of either sign
+            assert off <= (0.05 if act8 else 1e-4) * top, (k, off, top)
+
+
+@pytest.mark.parametrize("act8", [False, True])
+def test_example_trains_and_serves(act8):
+    from recurrent_cell_unroll_gb300 import linrec_block
+    losses, off = linrec_block.main(["--steps", "40"] + (["--act8"] if act8 else []))
+    assert losses[-1] < 0.8 * losses[0]
+    assert off <= 2e-2  # two passes of bf16 activations
