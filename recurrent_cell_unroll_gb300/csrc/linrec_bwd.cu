@@ -61,16 +61,21 @@ __device__ __forceinline__ uint32_t nan_flags(uint32_t raw) {  // a byte of raw 
   const uint32_t one = CPT == 1 ? 0x01u : 0x0101u, t = raw ^ (one << 7);
   return (t - one) & ~t & (one << 7);
 }
-// One step's values: x, and the logits within their limits
+// One step's values: x, and the gates' exponents (-logit log2(e), of logits within
+// their limits).  8-bit codes are scaled by `scale`, the gates' by its product
+// with -log2(e): their limits are on the exponents.
+constexpr float EXP_TOP = -LOGIT_FLOOR * LOG2E;
 template <typename IT, typename V>
 struct Decode;
 template <>
 struct Decode<bf16, F2> {
   __device__ __forceinline__ static F2 x(uint32_t v, float) { return bf16_pair(v); }
   __device__ __forceinline__ static F2 r(uint32_t v, float, const Limits &l) {
-    return bf16_pair(limit_r(v, l));
+    return exponent_of(bf16_pair(limit_r(v, l)));
   }
-  __device__ __forceinline__ static F2 i(uint32_t v, float) { return bf16_pair(floor_logit(v)); }
+  __device__ __forceinline__ static F2 i(uint32_t v, float) {
+    return exponent_of(bf16_pair(floor_logit(v)));
+  }
 };
 template <>
 struct Decode<int8_t, F2> {
@@ -79,23 +84,23 @@ struct Decode<int8_t, F2> {
     return mul2(add2(f2(code_bits(v, 0), code_bits(v, 1)), f2(-8388736.f)), f2(scale));
   }
   __device__ __forceinline__ static F2 r(uint32_t v, float scale, const Limits &l) {
-    const F2 f = i(v, scale);  // not limited as bf16: the channels' limits, widened
+    const F2 t = i(v, scale);  // not limited as bf16: the channels' limits, widened
     const float a = __uint_as_float(l.top2 << 16), b = __uint_as_float(l.top2 & 0xffff0000u);
-    return f2(min_nan(lo(f), a), min_nan(hi(f), b));
+    return f2(fmaxf(lo(t), a * -LOG2E), fmaxf(hi(t), b * -LOG2E));
   }
   __device__ __forceinline__ static F2 i(uint32_t v, float scale) {
-    const F2 f = x(v, scale);
-    return f2(floor_logit(lo(f)), floor_logit(hi(f)));
+    const F2 t = x(v, scale);
+    return f2(fminf(lo(t), EXP_TOP), fminf(hi(t), EXP_TOP));
   }
 };
 template <>
 struct Decode<float, float> {
   __device__ __forceinline__ static float x(uint32_t v, float) { return __uint_as_float(v); }
   __device__ __forceinline__ static float r(uint32_t v, float, const Limits &l) {
-    return limit_r(__uint_as_float(v), l);
+    return limit_r(__uint_as_float(v), l) * -LOG2E;
   }
   __device__ __forceinline__ static float i(uint32_t v, float) {
-    return floor_logit(__uint_as_float(v));
+    return floor_logit(__uint_as_float(v)) * -LOG2E;
   }
 };
 template <>
@@ -104,10 +109,10 @@ struct Decode<int8_t, float> {
     return (code_bits(v ^ 0x80u, 0) - 8388736.f) * scale;
   }
   __device__ __forceinline__ static float r(uint32_t v, float scale, const Limits &l) {
-    return limit_r(x(v, scale), l);
+    return fmaxf(i(v, scale), l.top * -LOG2E);
   }
   __device__ __forceinline__ static float i(uint32_t v, float scale) {
-    return floor_logit(x(v, scale));
+    return fminf(x(v, scale), EXP_TOP);
   }
 };
 
@@ -222,15 +227,24 @@ __global__ void __launch_bounds__(NT, PER_SM)
   const int skip = MAP ? p.B * cut.groups : 0;  // units of the first segment
   // Copies of the live tiles of this block, the last steps first: by TMA (thread
   // 0, the whole tile) or by each warp its own rows.
-  int pu = u0, pk = 0, issued = 0;
+  int pu = u0 - stride, issued = 0, tile1 = -1, len1 = 0;
+  Unit v1;  // whose tiles are being copied: the next one is tile1
+  v1.first = 0;
   auto issue = [&] {
-    for (; pu < cut.units; pu += stride, pk = 0) {
-      const Unit v = unit_of(cut, p.B, pu + skip, CW);
-      const int len = row_length(p.lengths, v.b, p.T, err);
-      int tile;
-      do tile = v.last - 1 - (pk++ * cs + rank);
-      while (tile >= v.first && tile * STEPS >= len);
-      if (tile < v.first) continue;
+    while (true) {
+      if (tile1 < v1.first) {
+        if (pu >= cut.units - stride) break;
+        pu += stride;
+        v1 = unit_of(cut, p.B, pu + skip, CW);
+        len1 = row_length(p.lengths, v1.b, p.T, err);
+        tile1 = v1.last - 1 - rank;
+        const int dead = tile1 - (ceil_div(len1, STEPS) - 1);  // tiles past the row's end
+        if (dead > 0) tile1 -= ceil_div(dead, cs) * cs;
+        continue;
+      }
+      const Unit &v = v1;
+      const int tile = tile1, len = len1;
+      tile1 -= cs;
       uint8_t *dst = ring + issued % STAGES * STAGE;
       if (TMA) {
         uint64_t *bar = &sh.full[issued % STAGES];
@@ -273,14 +287,6 @@ __global__ void __launch_bounds__(NT, PER_SM)
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
-  // 8 bits: lane 8 k + s has the exponent of tensor k at the warp's step s of a tile
-  auto exponent = [&](const Unit &v, int len, int tile) {
-    const int k = lane / S;
-    const int64_t t = (int64_t)tile * STEPS + warp * S + lane % S;
-    const int8_t *e = k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e;
-    if (k > 2 || tile < v.first || t >= len) return 0;
-    return (int)__ldg(e + (t * p.et + v.b * p.eb) * ceil_div(p.H, BLOCK8) + v.c0 / BLOCK8);
-  };
   int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
   V k2;
   Limits lim;
@@ -310,7 +316,24 @@ __global__ void __launch_bounds__(NT, PER_SM)
                  nc);
     Aff<V> all_map = identity<V>();
     sum = zero;
-    int ex = Q8 ? exponent(v, len, v.last - 1 - rank) : 0;
+    // 8 bits: lane 8 k + s has the exponent of tensor k at the warp's step s, read a
+    // tile ahead from where `ep` points
+    const int8_t *ep = nullptr;
+    int64_t ep_step = 0;
+    int et = 0, ex = 0;  // et: the lane's step in the tile that ep is at
+    auto next_exponent = [&] {
+      ex = lane < 3 * S && et >= v.first * STEPS && et < len ? (int)__ldg(ep) : 0;
+      ep -= ep_step;
+      et -= cs * STEPS;
+    };
+    if (Q8) {
+      const int nb8 = ceil_div(p.H, BLOCK8), k = lane / S;
+      et = (v.last - 1 - rank) * STEPS + warp * S + lane % S;
+      ep = (k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e) + ((int64_t)et * p.et + v.b * p.eb) * nb8 +
+           v.c0 / BLOCK8;
+      ep_step = (int64_t)cs * STEPS * p.et * nb8;
+      next_exponent();
+    }
     for (int base = v.last - 1; base >= v.first; base -= cs) {
       const int tile = base - rank, tw = tile * STEPS + warp * S;
       const bool on = tile >= v.first && tile * STEPS < len;  // the same for the whole block
@@ -320,7 +343,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
         if (!MAP) load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
         float scale[3][S];
         if (Q8) {
-          const float f = power2(ex);
+          const float f = power2(ex) * (lane < S ? 1.f : -LOG2E);
+          next_exponent();
 #pragma unroll
           for (int k = 0; k < 3; ++k)
 #pragma unroll
@@ -398,7 +422,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
           mine.e = fma_v(em1[s], ne, ne);
         }
       }
-      if (Q8) ex = exponent(v, len, tile - cs);  // of this block's next tile
+      if (Q8 && !on) next_exponent();
       if (on) {
         ++used;
         if (!TMA) {

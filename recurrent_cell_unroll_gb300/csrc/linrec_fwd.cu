@@ -46,8 +46,9 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], F2 k2, const 
 #pragma unroll
     for (int n = 0; n < BATCH; ++n) {
       x[n] = bf16_pair(raw[0][s + n]);
-      r[n] = bf16_pair(SMALL ? floor_logit(raw[1][s + n]) : limit_r(raw[1][s + n], lim));
-      i[n] = bf16_pair(floor_logit(raw[2][s + n]));
+      r[n] = exponent_of(
+          bf16_pair(SMALL ? floor_logit(raw[1][s + n]) : limit_r(raw[1][s + n], lim)));
+      i[n] = exponent_of(bf16_pair(floor_logit(raw[2][s + n])));
     }
     gates_n<SMALL, BATCH>(x, r, i, k2, em1 + s, nb + s, ns, ng);
   }
@@ -64,8 +65,8 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, con
     for (int n = 0; n < BATCH; ++n) {
       const int q = s + 2 * n;
       x[n] = f2(at(0, q), at(0, q + 1));
-      r[n] = f2(limit_r(at(1, q), lim), limit_r(at(1, q + 1), lim));
-      i[n] = f2(floor_logit(at(2, q)), floor_logit(at(2, q + 1)));
+      r[n] = exponent_of(f2(limit_r(at(1, q), lim), limit_r(at(1, q + 1), lim)));
+      i[n] = exponent_of(f2(floor_logit(at(2, q)), floor_logit(at(2, q + 1))));
     }
     gates_n<SMALL, BATCH>(x, r, i, f2(k2), m, b, ns, ng);
 #pragma unroll
@@ -98,12 +99,22 @@ __global__ void __launch_bounds__(NT, PER_SM)
 
   // Copies of the live tiles of this block, in the order they are used: by TMA
   // (thread 0, the whole tile) or by each warp its own rows.
-  int pu = u0, pk = 0, issued = 0;
+  int pu = u0 - stride, issued = 0, tile1 = 0, end1 = 0, len1 = 0;
+  Unit v1;  // whose tiles are being copied: the next one is tile1, and end1 ends them
   auto issue = [&] {
-    for (; pu < cut.units; pu += stride, pk = 0) {
-      const Unit v = unit_of(cut, p.B, pu, CW);
-      const int tile = v.first + pk * cs + rank, len = row_length(p.lengths, v.b, p.T, err);
-      if (tile >= v.last || tile * STEPS >= len) continue;
+    while (true) {
+      if (tile1 >= end1) {
+        if (pu >= cut.units - stride) break;
+        pu += stride;
+        v1 = unit_of(cut, p.B, pu, CW);
+        len1 = row_length(p.lengths, v1.b, p.T, err);
+        tile1 = v1.first + rank;
+        end1 = min(v1.last, ceil_div(len1, STEPS));
+        continue;
+      }
+      const Unit &v = v1;
+      const int tile = tile1, len = len1;
+      tile1 += cs;
       uint8_t *dst = ring + issued % STAGES * STAGE;
       if (TMA) {
         uint64_t *bar = &sh.full[issued % STAGES];
@@ -124,7 +135,6 @@ __global__ void __launch_bounds__(NT, PER_SM)
         }
       }
       ++issued;
-      ++pk;
       break;
     }
     if (!TMA) copy_commit();
@@ -148,19 +158,19 @@ __global__ void __launch_bounds__(NT, PER_SM)
   bool small = false;
   // What a unit starts with is read while the one before it is worked on.
   V first;
-  int len1 = p.T;
+  int len0 = p.T;
   auto look = [&](int u) {
     if (u >= cut.units) return;
     const Unit v = unit_of(cut, p.B, u, CW);
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     set(first, 0.f);
     if (p.h0) load_v(p.h0 + (int64_t)v.b * p.H + ch, live, first);
-    len1 = row_length(p.lengths, v.b, p.T, err);
+    len0 = row_length(p.lengths, v.b, p.T, err);
   };
   look(u0);
   for (int u = u0; u < cut.units; u += stride) {
     const Unit v = unit_of(cut, p.B, u, CW);
-    const int len = len1;
+    const int len = len0;
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
     if (v.c0 != held) {

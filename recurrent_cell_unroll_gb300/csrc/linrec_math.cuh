@@ -160,6 +160,7 @@ __device__ __forceinline__ uint32_t limit_r(uint32_t v, const Limits &l) {
   asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(floor_logit(v)), "r"(l.top2));
   return r;
 }
+__device__ __forceinline__ F2 exponent_of(F2 logit) { return mul2(logit, f2(-LOG2E)); }
 __device__ __forceinline__ Limits limits(float k2) { return {r_ceiling(k2), 0u}; }
 __device__ __forceinline__ Limits limits(F2 k2) {
   // rounded towards zero: a's exponent at the limit moves by a percent or so
@@ -179,25 +180,20 @@ __device__ __forceinline__ float one_minus_a2(float em1, float tiny) {
 __device__ __forceinline__ F2 inv_beta(F2 w) { return f2(rsq(lo(w)), rsq(hi(w))); }
 __device__ __forceinline__ float inv_beta(float w) { return rsq(w); }
 
-// Of N pairs of elements (logits already limited): em1 = a - 1, nb = -beta g x,
-// and the sigmoids negated (ns makes the decay's exponent k2 ns; the other signs
-// cancel in products).
+// Of N pairs of elements: em1 = a - 1, nb = -beta g x, and the sigmoids negated
+// (ns makes the decay's exponent k2 ns; the other signs cancel in products).  The
+// gates come as exponents, tr = -r log2(e) and ti likewise, of limited logits.
 // Written stage by stage over the N pairs: each stage's operations are
 // independent, and a warp has few others to hide the latency of a chain of
 // twenty dependent ones behind.
 template <bool SMALL, int N>
-__device__ __forceinline__ void gates_n(const F2 (&x)[N], const F2 (&r)[N], const F2 (&i)[N],
+__device__ __forceinline__ void gates_n(const F2 (&x)[N], const F2 (&tr)[N], const F2 (&ti)[N],
                                         F2 k2, F2 *em1, F2 *nb, F2 *ns, F2 *ng) {
   F2 pr[N], pi[N], t[N];
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    pr[n] = mul2(r[n], f2(-LOG2E));
-    pi[n] = mul2(i[n], f2(-LOG2E));
-  }
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    pr[n] = f2(ex2(lo(pr[n])), ex2(hi(pr[n])));
-    pi[n] = f2(ex2(lo(pi[n])), ex2(hi(pi[n])));
+    pr[n] = f2(ex2(lo(tr[n])), ex2(hi(tr[n])));
+    pi[n] = f2(ex2(lo(ti[n])), ex2(hi(ti[n])));
   }
 #pragma unroll
   for (int n = 0; n < N; ++n) {
