@@ -260,7 +260,7 @@ extern "C" int rcu_linrec_backward(rcu_seq *h, int dtype, int saved, int layout,
               seq_out(layout, T, B, di, lddi), dlambda, dh0};
   strides(layout, T, B, 1, &p.et, &p.eb);
   begin(h, "linrec_backward", s);
-  CU(launch_linrec_bwd(p, *h, (int *)h->ctl.p, !h->force_path, s, &h->launches));
+  CU(launch_linrec_bwd(p, *h, (int *)h->ctl.p, h->nsm, !h->force_path, s, &h->launches));
   h->prof_end(s);
   return RCU_OK;
 }

@@ -1,0 +1,209 @@
+// Gated linear recurrence, backward, for short sequences of many rows: a warp has a
+// row's channels to itself.
+//
+// The tiled kernel gives each of its warps 8 of a tile's 64 steps, which short
+// sequences leave idle, and joins them with a barrier a tile.  Here a warp runs all
+// steps, first forwards, keeping the states in shared memory, then backwards with
+// the gates made again; nothing is exchanged.  It stays with its channels, whose
+// constants it keeps, from one batch row to the next.  Making the gates twice tells
+// with the length: bf16 B=250 H=2048 takes 91 us here and 118 tiled at 20 steps, 165
+// and 122 at 40; fp32 B=183 H=3312 158 and 202 at 17 steps.
+#include "linrec_bwd.cuh"
+
+namespace rcu {
+namespace {
+
+using namespace linrec;
+
+constexpr int NW = 4, NT = 32 * NW, N = 4;  // N: steps whose reads are in flight together
+constexpr int SHORT_T = 20;
+
+// A lane's values of a step from global memory (`word`: as one access)
+template <typename IT, int CPT>
+__device__ __forceinline__ uint32_t global_raw(const IT *p, int live, bool word) {
+  constexpr int B = CPT * (int)sizeof(IT);
+  if (B == 4 && word && live == CPT) return __ldg(reinterpret_cast<const uint32_t *>(p));
+  if (B == 2 && word && live == CPT) return __ldg(reinterpret_cast<const unsigned short *>(p));
+  uint32_t v = 0;
+  if (sizeof(IT) == 4) {
+    if (live > 0) v = __ldg(reinterpret_cast<const uint32_t *>(p));
+  } else if (sizeof(IT) == 2) {
+    const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+    if (live > 0) v = __ldg(q);
+    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 16;
+  } else {
+    const unsigned char *q = reinterpret_cast<const unsigned char *>(p);
+    if (live > 0) v = __ldg(q);
+    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 8;
+  }
+  return v;
+}
+
+template <typename IT, typename T>
+__global__ void __launch_bounds__(NT, 3)
+    linrec_bwd_short_kernel(const LinrecBwd p, const int groups, float *__restrict__ partial,
+                            const int words, int *err) {
+  constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
+  constexpr bool Q8 = sizeof(IT) == 1;
+  typedef typename Lane<T>::V V;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  V *before = reinterpret_cast<V *>(smem) + (size_t)warp * p.T * 32 + lane;  // the state before t
+  const int w = blockIdx.x * NW + warp, c0 = w % groups * CW, stride = gridDim.x * NW / groups;
+  const int ch = c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
+  const int nb8 = ceil_div(p.H, BLOCK8);
+  V k2, nk, zero, minus;
+  set(zero, 0.f);
+  set(minus, -1.f);
+  rate(p.lambda + ch, p.c, live, k2);
+  const Limits lim = limits(k2);
+  const bool small = __all_sync(0xffffffffu, small_rate(k2));
+  set(nk, -1.f / LOG2E);
+  nk = mul_v(nk, k2);  // -K
+
+  uint32_t raw[3][N], rawd[N];
+  float scale[3][N];
+  auto load = [&](int64_t b, int t0, int len, bool with_dy) {
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+      const int64_t t = t0 + s;
+      const int on = t < len ? live : 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const SeqIn &in = (&p.x)[k];
+        raw[k][s] = global_raw<IT, CPT>(static_cast<const IT *>(in.p) + t * in.st + b * in.sb + ch,
+                                        on, words >> k & 1);
+        if (Q8)
+          scale[k][s] = power2(on ? __ldg(in.e + (t * p.et + b * p.eb) * nb8 + c0 / BLOCK8) : 0) *
+                        (k ? -LOG2E : 1.f);
+      }
+      if (with_dy)
+        rawd[s] = global_raw<T, CPT>(static_cast<const T *>(p.dy.p) + t * p.dy.st + b * p.dy.sb + ch,
+                                     on, words >> 3 & 1);
+    }
+  };
+  V em1[N], nb[N], ns[N], ng[N];
+  auto make_gates = [&](int t0, int len) {
+    if (small) gates<IT, true, 2>(raw, scale, k2, lim, em1, nb, ns, ng);
+    else gates<IT, false, 2>(raw, scale, k2, lim, em1, nb, ns, ng);
+    if (Q8) spoil_codes<CPT>(raw, em1, nb, ns, ng);
+    if (t0 + N > len) {
+#pragma unroll
+      for (int s = 0; s < N; ++s)
+        if (t0 + s >= len) em1[s] = nb[s] = ns[s] = ng[s] = 0;
+    }
+  };
+  for (int64_t b = w / groups; b < p.B; b += stride) {
+    const int64_t row = b * p.H + ch;
+    const int len = row_length(p.lengths, (int)b, p.T, err);
+    V h, nc = zero, sum = zero;
+    load_v(p.states + row, live, h);
+    if (p.dh_n) load_v(p.dh_n + row, live, nc);
+    nc = neg_v(nc);
+    load(b, 0, len, false);
+    for (int t0 = 0; t0 < len; t0 += N) {
+      make_gates(t0, len);
+      if (t0 + N < len) load(b, t0 + N, len, false);
+#pragma unroll
+      for (int s = 0; s < N; ++s) {
+        if (t0 + s < len) before[(t0 + s) * 32] = h;
+        h = fma_v(nb[s], minus, fma_v(em1[s], h, h));
+      }
+    }
+    T *out[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const SeqOut &o = (&p.dx)[k];
+      out[k] = static_cast<T *>(o.p) + b * o.sb + ch;
+    }
+    auto store = [&](int k, int64_t t, V v) {
+      const SeqOut &o = (&p.dx)[k];
+      if (o.p) store_raw(out[k] + t * o.st, v, live, words >> (4 + k) & 1);
+    };
+    for (int t = p.T - 1; t >= len; --t)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) store(k, t, zero);
+    int t0 = len > 0 ? (len - 1) / N * N : -N;
+    if (t0 >= 0) load(b, t0, len, true);
+    for (; t0 >= 0; t0 -= N) {
+      make_gates(t0, len);
+      V dy[N];
+#pragma unroll
+      for (int s = 0; s < N; ++s) dy[s] = Decode<T, V>::x(rawd[s], 0.f);
+      if (t0 > 0) load(b, t0 - N, len, true);
+#pragma unroll
+      for (int s = N - 1; s >= 0; --s) {
+        if (t0 + s >= len) continue;
+        const V ne = fma_v(dy[s], minus, nc);
+        nc = fma_v(em1[s], ne, ne);
+        V hp = before[(t0 + s) * 32], gx, gr, gi, gl;
+        grads(em1[s], nb[s], ns[s], ng[s], nk, ne, hp, gx, gr, gi, gl);
+        sum = add_v(sum, gl);
+        store(0, t0 + s, gx);
+        store(1, t0 + s, gr);
+        store(2, t0 + s, gi);
+      }
+    }
+    if (p.dh0) store_v(p.dh0 + row, neg_v(nc), live);
+    if (p.dlambda) store_v(partial + row, sum, live);
+  }
+}
+
+template <typename IT, typename T>
+cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s, int *launches) {
+  const int groups = ceil_div(p.H, Shape<T>::CW);
+  const size_t smem = (size_t)NW * p.T * 32 * sizeof(typename Lane<T>::V);
+  auto fn = linrec_bwd_short_kernel<IT, T>;
+  cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)smem);
+  if (e != cudaSuccess) return e;
+  // a whole number of warps a group: each warp stays with its channels
+  const int64_t most = (int64_t)3 * nsm * NW;
+  const int64_t each = std::max<int64_t>(1, std::min<int64_t>(p.B, most / groups));
+  const int64_t warps = each * groups;
+  // blocks of NW warps: a multiple of the groups in all
+  int64_t blocks = (warps + NW - 1) / NW;
+  while (blocks * NW % groups) ++blocks;
+  const SeqIn *in[4] = {&p.x, &p.r, &p.i, &p.dy};
+  const SeqOut *out[3] = {&p.dx, &p.dr, &p.di};
+  auto whole = [](const void *q, int64_t st, int64_t sb, int size) {
+    const int bytes = Shape<T>::CPT * size;
+    return reinterpret_cast<uintptr_t>(q) % bytes == 0 && st * size % bytes == 0 &&
+           sb * size % bytes == 0;
+  };
+  int words = 0;
+  for (int k = 0; k < 4; ++k)
+    words |= whole(in[k]->p, in[k]->st, in[k]->sb, k < 3 ? sizeof(IT) : sizeof(T)) << k;
+  for (int k = 0; k < 3; ++k)
+    words |= whole(out[k]->p, out[k]->st, out[k]->sb, sizeof(T)) << (4 + k);
+  float *partial = nullptr;
+  if (p.dlambda) {
+    e = ws.get((size_t)p.B * p.H * 4, &partial);
+    if (e != cudaSuccess) return e;
+  }
+  fn<<<(unsigned)blocks, NT, smem, s>>>(p, groups, partial, words, err);
+  ++*launches;
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !p.dlambda) return e;
+  ++*launches;
+  return launch_dlambda(partial, p.B, p, s);
+}
+
+}  // namespace
+
+bool linrec::short_bwd_pays(const LinrecBwd &p, int resident_blocks) {
+  const int groups = ceil_div(p.H, p.dtype == RCU_BF16 ? Shape<bf16>::CW : Shape<float>::CW);
+  return p.T <= SHORT_T && (int64_t)p.B * groups >= resident_blocks;
+}
+
+cudaError_t linrec::launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm,
+                                     cudaStream_t s, int *launches) {
+  const bool q8 = p.saved == RCU_I8;
+  if (p.dtype == RCU_BF16)
+    return q8 ? run<int8_t, bf16>(p, ws, err, nsm, s, launches)
+              : run<bf16, bf16>(p, ws, err, nsm, s, launches);
+  return q8 ? run<int8_t, float>(p, ws, err, nsm, s, launches)
+            : run<float, float>(p, ws, err, nsm, s, launches);
+}
+
+}  // namespace rcu

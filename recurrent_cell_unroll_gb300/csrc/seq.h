@@ -43,7 +43,7 @@ struct LinrecBwd {
   const float *states;
   SeqIn dy;
   const float *dh_n;
-  SeqOut dx, dr, di;
+  SeqOut dx, dr, di;  // as x, r, i
   float *dlambda, *dh0;
 };
 
@@ -84,8 +84,8 @@ __device__ __forceinline__ void wait_for_previous() {
 
 cudaError_t launch_linrec_fwd(const LinrecFwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
                               int *launches);
-cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
-                              int *launches);
+cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm, bool vec,
+                              cudaStream_t s, int *launches);
 cudaError_t launch_linrec_step(int dtype, int B, int H, const void *x, int64_t ldx, const void *r,
                                int64_t ldr, const void *i, int64_t ldi, const float *lambda,
                                float c, float *state, int slots, const int32_t *slot, void *y,
