@@ -3,8 +3,10 @@
  *
  * The library runs the time-unrolled forward pass of stacked LSTM, GRU and
  * LSTM-with-projection (LSTMP) networks, padded or variable-length, and the
- * RSSM prior unroll, entirely in its own CUDA kernels (sm_103a).  The caller
- * supplies device memory and a CUDA stream; nothing here depends on PyTorch.
+ * RSSM prior unroll, and operators over sequences (a gated linear recurrence,
+ * layer norm, 8-bit activation checkpoints), entirely in its own CUDA kernels
+ * (sm_103a).  The caller supplies device memory and a CUDA stream; nothing here
+ * depends on PyTorch.
  *
  * Conventions shared by every entry point
  *  - Return value: RCU_OK (0) or a negative RCU_ERR_* code.  The message of
@@ -562,13 +564,13 @@ RCU_API int rcu_seq_create(rcu_seq **out);
 RCU_API int rcu_seq_destroy(rcu_seq *h);
 
 /* Synchronise `stream` and return the device status of the calls so far
- * (RCU_OK, RCU_ERR_LENGTHS, RCU_ERR_SLOTS), then clear it. */
+ * (RCU_OK, RCU_ERR_LENGTHS, RCU_ERR_SLOTS; RCU_ERR_TIMEOUT if a device wait
+ * gave up), then clear it. */
 RCU_API int rcu_seq_get_status(rcu_seq *h, void *stream);
 
 /* RCU_ATTR_PROFILE as for the other handles; RCU_ATTR_FORCE_PATH: 0 =
- * automatic, 1 = the kernels' plain loads where aligned rows would move by
- * wider or asynchronous copies (rcu_linrec_forward/_backward: no TMA;
- * layer norm and act8: no vector accesses). */
+ * automatic, 1 = aligned rows move as unaligned ones do
+ * (rcu_linrec_forward/_backward: no TMA; the others: no vector accesses). */
 RCU_API int rcu_seq_set_attr(rcu_seq *h, int attr, int64_t value);
 RCU_API int rcu_seq_profile_entry(rcu_seq *h, int i, const char **name, double *total_ms,
                                   int64_t *count);
@@ -604,7 +606,9 @@ RCU_API int rcu_seq_last_launch_count(rcu_seq *h);
  *            steps 0, 64, 128, ..., which rcu_linrec_backward needs (of a
  *            chunk past a row's end: its last state).
  * T or B may be 0.  Long sequences of few channels are split over time;
- * results do not depend on anything but the inputs.
+ * results do not depend on anything but the inputs.  The decay is applied as
+ * h + (a - 1) h, which keeps slow decays exact; an infinite state is NaN one
+ * step later.
  */
 RCU_API int rcu_linrec_forward(rcu_seq *h, int dtype, int layout, int T, int B, int H,
                                const void *x, int64_t ldx, const void *r, int64_t ldr,

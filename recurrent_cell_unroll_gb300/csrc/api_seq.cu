@@ -102,6 +102,9 @@ int check_linrec(const char *fn, rcu_seq *h, int dtype, int layout, int T, int B
     return fail(RCU_ERR_INVALID, "%s: unknown layout %d", fn, layout);
   if (T < 0 || B < 0 || H < 1)
     return fail(RCU_ERR_INVALID, "%s: T, B must be >= 0 and H >= 1 (got %d, %d, %d)", fn, T, B, H);
+  // tiles and rows are counted in 32 bits
+  if (T > (1 << 30) || (int64_t)B * ((H + 31) / 32) > (1 << 30))
+    return fail(RCU_ERR_UNSUPPORTED, "%s: T or B * H / 32 above 2^30", fn);
   if (!lambda) return fail(RCU_ERR_INVALID, "%s: lambda is NULL", fn);
   // c is used in fp32: it has to be a positive number there too
   if (!((float)c > 0.f) || !std::isfinite((float)c))

@@ -15,7 +15,9 @@ namespace {
 using namespace linrec;
 
 // Eight warps of 8 steps: the tile is what one kept state covers, and 16 steps a
-// lane would need more than the 255 registers a thread can have.
+// lane would need more than the 255 registers a thread can have.  Two blocks an SM
+// (128 registers); bf16 rows that TMA cannot address take more, and one block is
+// faster there (T=15731 B=1 H=2133: 282 us, 308 with two).
 constexpr int NW = 8, NT = 32 * NW, S = CHUNK / NW, STEPS = CHUNK, STAGES = 2, PER_SM = 2;
 constexpr int MAXCS = 8;  // blocks of a cluster
 constexpr int BATCH = 4;  // pairs whose gates are computed together
@@ -52,7 +54,7 @@ __device__ __forceinline__ uint32_t tile_raw(const uint8_t *row, int lane) {
 // MAP: only the backward map (P, R) of each segment but the first, from r and dy
 // alone, into `maps`, which the launch after it starts its segments from.
 template <typename IT, typename T, bool TMA, bool MAP>
-__global__ void __launch_bounds__(NT, PER_SM)
+__global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
     linrec_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap mdy,
                       const LinrecBwd p, const Cut cut, void *maps, float *__restrict__ partial, const bool words,

@@ -15,8 +15,8 @@ namespace {
 using namespace linrec;
 
 // Four warps of 16 steps, three blocks on an SM (168 registers a thread): of the
-// shapes tried the fastest (8 warps of 16 steps, two blocks: 207 us at bf16
-// T=512 B=256 H=1024; 8 of 8, three blocks: 224; this: 186).
+// shapes tried the fastest (at bf16 T=512 B=256 H=1024 8 warps of 16 steps
+// in two blocks took 11 % longer, 8 of 8 in three 20 %).
 constexpr int NW = 4, NT = 32 * NW, S = 16, STEPS = NW * S, STAGES = 2, PER_SM = 3;
 constexpr int MAXCS = 12;  // blocks of a cluster: with more, their maps leave room for two on an SM
 constexpr int BATCH = 4;   // pairs whose gates are computed together

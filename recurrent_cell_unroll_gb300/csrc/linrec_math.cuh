@@ -135,13 +135,14 @@ __device__ __forceinline__ bool small_rate(F2 k2) {
 
 // The two sigmoids share one reciprocal, of the product of their denominators:
 // logits stop at -42, where e^42 = 2^60.6 keeps that product a normal number and
-// a sigmoid is 6e-19.  r above r_ceiling of its channel's rate, where a is 2^-100,
-// is taken as that: what the state would still pass on is below any rounding, and
+// a sigmoid is 6e-19.  r above r_ceiling of its channel's rate, where a is 2^-90, is
+// taken as that: what the state would still pass on is below any rounding, and
 // ex2m1 keeps its range (SMALL_RATE needs no ceiling).  A NaN stays one.  bf16
-// logits are limited as packed pairs, two at a time.
+// logits are limited as packed pairs, two at a time; a ceiling rounded to bf16 moves
+// by at most 1/4, the exponent by a factor of e^(1/4): to 2^-116 at worst.
 constexpr float LOGIT_FLOOR = -42.f;
 __device__ __forceinline__ float r_ceiling(float k2) {
-  const float s = 100.f / k2;  // sigmoid(r) at the limit
+  const float s = 90.f / k2;  // sigmoid(r) at the limit
   return s < 1.f ? fmaxf(logf(s / (1.f - s)), LOGIT_FLOOR) : __int_as_float(0x7f800000);
 }
 __device__ __forceinline__ float floor_logit(float v) { return max_nan(v, LOGIT_FLOOR); }
@@ -163,7 +164,6 @@ __device__ __forceinline__ uint32_t limit_r(uint32_t v, const Limits &l) {
 __device__ __forceinline__ F2 exponent_of(F2 logit) { return mul2(logit, f2(-LOG2E)); }
 __device__ __forceinline__ Limits limits(float k2) { return {r_ceiling(k2), 0u}; }
 __device__ __forceinline__ Limits limits(F2 k2) {
-  // rounded towards zero: a's exponent at the limit moves by a percent or so
   const float a = r_ceiling(lo(k2)), b = r_ceiling(hi(k2));
   return {0.f, (__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xffff0000u)};
 }

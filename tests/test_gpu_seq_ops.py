@@ -53,7 +53,7 @@ def close(got, ref, name, scale=None):
 # --------------------------------------------------------------------------- 64-bit definitions
 
 def rec_gates(x, r, i, lam, c):
-    sp = torch.nn.functional.softplus(lam, threshold=1e9)
+    sp = torch.logaddexp(lam, torch.zeros_like(lam))
     s, g = torch.sigmoid(r), torch.sigmoid(i)
     em1 = torch.expm1(-c * sp * s)
     return s, g, em1, torch.sqrt(-em1 * (2 + em1))
@@ -83,7 +83,7 @@ def rec_backward(dy, x, r, i, lam, states, c, lengths, dh_n):
         before[t] = h
         h = h + em1[t] * h + beta[t] * g[t] * x[t]
     e = torch.zeros(B, H, dtype=torch.float64) if dh_n is None else dh_n
-    sp = torch.nn.functional.softplus(lam, threshold=1e9)
+    sp = torch.logaddexp(lam, torch.zeros_like(lam))
     dx, dr, di = (torch.zeros(T, B, H, dtype=torch.float64) for _ in range(3))
     dsp = torch.zeros(B, H, dtype=torch.float64)
     for t in reversed(range(T)):
@@ -349,6 +349,11 @@ def test_linrec_extreme_gates(ops, path):
     lam = torch.linspace(-30, 30, H)
     h0 = torch.randn(B, H, generator=g)
     check_rec(ops, T, B, H, "f32", inputs=(x, r, i, lam, h0))
+    check_rec(ops, T, B, H, "bf16", inputs=(*(t.bfloat16() for t in (x, r, i)), lam, h0))
+    # decay rates up to where fp32 ends: the gate's ceiling in every binade
+    lam2 = torch.exp2(torch.linspace(-4, 120, H))
+    check_rec(ops, T, B, H, "bf16", inputs=(*(t.bfloat16() for t in (x, r, i)), lam2, h0))
+    check_rec(ops, T, B, H, "f32", inputs=(x, r, i, lam2, h0))
     vals = torch.tensor([-math.inf, -90.0, -50.0, 50.0, 90.0, math.inf])
     r = vals[torch.randint(0, 6, (T, B, H), generator=g)]
     i = vals[torch.randint(0, 6, (T, B, H), generator=g)]
