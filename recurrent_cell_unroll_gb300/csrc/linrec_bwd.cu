@@ -39,7 +39,10 @@ constexpr int in_bytes() {
   return STEPS * (TMA ? Shape<T>::CW * (int)sizeof(IT) : Loose<IT, Shape<T>::CPT>::PITCH);
 }
 template <typename IT, typename T, bool TMA>
-constexpr int stage_bytes() { return 3 * in_bytes<IT, T, TMA>() + in_bytes<T, T, TMA>(); }
+constexpr int tensor_bytes() { return 3 * in_bytes<IT, T, TMA>() + in_bytes<T, T, TMA>(); }
+// and with the states that enter the tile
+template <typename IT, typename T, bool TMA>
+constexpr int stage_bytes() { return tensor_bytes<IT, T, TMA>() + Shape<T>::CW * 4; }
 
 // A lane's values of one step (CPT channels) in a tile that TMA brought
 template <typename IT, int CPT>
@@ -58,9 +61,10 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
     linrec_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap mdy,
                       const LinrecBwd p, const Cut cut, void *maps, float *__restrict__ partial, const bool words,
-                      int *err) {
+                      const bool bulk_states, int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
-  constexpr int IN = in_bytes<IT, T, TMA>(), STAGE = stage_bytes<IT, T, TMA>();
+  constexpr int IN = in_bytes<IT, T, TMA>(), TENSORS = tensor_bytes<IT, T, TMA>();
+  constexpr int STAGE = stage_bytes<IT, T, TMA>();
   constexpr int IN_ROW = IN / STEPS, DY_ROW = in_bytes<T, T, TMA>() / STEPS;
   constexpr bool Q8 = sizeof(IT) == 1;
   typedef typename Lane<T>::V V;
@@ -95,7 +99,11 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
       uint8_t *dst = ring + issued % STAGES * STAGE;
       if (TMA) {
         uint64_t *bar = &sh.full[issued % STAGES];
-        tc::mbar_arrive_expect_tx(bar, MAP ? STAGE - 2 * IN : STAGE);
+        const int states = bulk_states && !MAP ? min(CW, p.H - v.c0) * 4 : 0;
+        tc::mbar_arrive_expect_tx(bar, (MAP ? TENSORS - 2 * IN : TENSORS) + states);
+        if (states)
+          tc::bulk_load(dst + TENSORS, p.states + ((int64_t)tile * p.B + v.b) * p.H + v.c0, states,
+                        bar);
         tma_load_3d(dst + IN, &mr, bar, v.c0, v.b, tile * STEPS);
         if (!MAP) {
           tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
@@ -187,7 +195,8 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
       V em1[S], nb[S], ns[S], ng[S], dy[S], h = zero, fe = zero;
       Aff<V> mine = identity<V>();
       if (on) {
-        if (!MAP) load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
+        if (!MAP && !(TMA && bulk_states))
+          load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
         float scale[3][S];
         if (Q8) {
           const float f = power2(ex) * (lane < S ? 1.f : -LOG2E);
@@ -211,6 +220,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
 #pragma unroll
           for (int s = 0; s < S; ++s)
             rawd[s] = tile_raw<T, CPT>(src + 3 * IN + (warp * S + s) * DY_ROW, lane);
+          if (!MAP && bulk_states) h = reinterpret_cast<const V *>(src + TENSORS)[lane];
         } else {
           copy_wait<STAGES - 1>();
           __syncwarp();
@@ -404,7 +414,8 @@ __global__ void linrec_dlambda_kernel(const float *__restrict__ partial, int64_t
 struct Maps {
   CUtensorMap m[4];
   bool tma;
-  bool words;  // all three outputs, in whole words a lane
+  bool words;   // all three outputs, in whole words a lane
+  bool states;  // rows of the kept states as bulk copies
 };
 template <typename IT, typename T>
 Maps maps(const LinrecBwd &p, bool vec) {
@@ -417,6 +428,7 @@ Maps maps(const LinrecBwd &p, bool vec) {
     v.tma = v.tma && tc_map_3d(&v.m[k], in[k]->p, bytes, p.H, p.B, p.T, in[k]->sb, in[k]->st,
                                Shape<T>::CW, 1, STEPS);
   }
+  v.states = p.H % 4 == 0 && reinterpret_cast<uintptr_t>(p.states) % 16 == 0;
   v.words = true;
   for (int k = 0; k < 3; ++k)
     v.words = v.words && out[k]->p && word_aligned(out[k]->p, out[k]->st, out[k]->sb, sizeof(T));
@@ -446,12 +458,12 @@ cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStr
     first.cut.units = pl.cut.units / pl.cut.nseg * (pl.cut.nseg - 1);
     first.grid = std::min(first.cut.units, res_map.clusters[1]);
     e = launch_cut(linrec_bwd_kernel<IT, T, TMA, true>, first, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
-                   v.m[3], p, first.cut, (void *)mem, partial, v.words, err);
+                   v.m[3], p, first.cut, (void *)mem, partial, v.words, v.states, err);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
   e = launch_cut(linrec_bwd_kernel<IT, T, TMA, false>, pl, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
-                 v.m[3], p, pl.cut, (void *)mem, partial, v.words, err);
+                 v.m[3], p, pl.cut, (void *)mem, partial, v.words, v.states, err);
   ++*launches;
   if (e != cudaSuccess || !p.dlambda) return e;
   ++*launches;
