@@ -4,7 +4,9 @@
 // block, 16 or 32 values a lane, the next row's loads in flight.  Each lane has the
 // same columns of every row its warps take, so the column sums (dweight, dbias)
 // build up in its registers; every block writes one row of partial sums at the
-// end, and a second kernel adds those in a fixed order.
+// end, and a second kernel adds those in a fixed order.  Measured: bf16
+// 131072x1024 with dsum 184 us, 5.9 TB/s; fp32 from 8 bits 12501x1000 29 us (22 and
+// 9 for the two kernels with a cold cache), which L2 holds: latency of its waves.
 #include "layernorm.cuh"
 
 namespace rcu {

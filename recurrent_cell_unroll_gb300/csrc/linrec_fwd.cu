@@ -7,6 +7,13 @@
 // of a cluster, which exchange their tiles' maps through distributed shared
 // memory: no second read, no flags in global memory, and the order of every
 // sum is fixed.
+//
+// Measured, bf16: T=512 B=256 H=1024 174 us, 6.2 TB/s of the 1084 MB it must
+// move: bound by memory (77 % of DRAM's peak), with the FMA pipe half busy.
+// T=65536 B=1 H=2048 242 us, 4.5 TB/s: 32 clusters of 12 blocks fill 384 of the
+// 456 places, and each round of tiles waits for its cluster's slowest block.
+// fp32 T=512 B=128 H=1024 162 us, 6.7 TB/s.  T=80 B=1 H=256 is the call's own
+// cost, 19 us, of which the kernel is 6.
 #include "linrec_tile.cuh"
 
 namespace rcu {

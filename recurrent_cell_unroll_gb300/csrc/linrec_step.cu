@@ -5,6 +5,8 @@
 // state), by memory above: 16 (bf16) or 24 bytes (fp32) an element.  A channel's
 // constants cost more than a step, so a thread keeps VEC channels and takes
 // several requests; their reads are in flight together.
+// Measured, bf16 B=256 H=1024: 6.5 us with a cold cache, 14.6 us from call to call,
+// which is the host's.
 #include "linrec_tile.cuh"
 
 namespace rcu {

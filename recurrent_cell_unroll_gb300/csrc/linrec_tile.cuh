@@ -3,9 +3,9 @@
 // clusters, and how a tile's values and the affine maps of its steps move.
 //
 // A block of NW warps takes a tile of NW * S steps x CW channels of one batch
-// row (NW, S: the kernel's own); CW values of the tensors' type are 128 bytes, so that a step of a tile
-// is one full line.  Warp w has the steps [w * S, w * S + S), lane l the CPT
-// channels from l * CPT.  A step is h -> a h + b, and steps compose to affine
+// row (NW, S: the kernel's own); CW values of the tensors' type are 128 bytes, so
+// that a step of a tile is one full line.  Warp w has the steps [w * S, w * S + S),
+// lane l the CPT channels from l * CPT.  A step is h -> a h + b, and steps compose to affine
 // maps h -> P h + E: each warp reduces its steps to a map, the maps are chained
 // in order, and the warp then runs its steps from the state that reaches it.
 #pragma once
