@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
           }
           if (warp < cs)
             put_peer(&sh.peer[round & 1][rank][lane], &sh.met[round & 1], warp, all);
-          tc::mbar_wait_cluster(&sh.met[round & 1], round >> 1 & 1, err, &sh.abort, WAIT_NS);
+          wait_round(&sh.met[round & 1], round >> 1 & 1, err, &sh.abort);
 #pragma unroll
           for (int q = 0; q < MAXCS; ++q)
             if (q < cs) {

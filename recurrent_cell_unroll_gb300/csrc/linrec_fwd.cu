@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
           typename Slot<V>::type *now = peers + (round & 1) * cs * 32 + lane;
           for (int q = warp; q < cs; q += NW)
             put_peer(now + rank * 32, &sh.met[round & 1], q, all);
-          tc::mbar_wait_cluster(&sh.met[round & 1], round >> 1 & 1, err, &sh.abort, WAIT_NS);
+          wait_round(&sh.met[round & 1], round >> 1 & 1, err, &sh.abort);
 #pragma unroll
           for (int q = 0; q < MAXCS; ++q)
             if (q < cs) {

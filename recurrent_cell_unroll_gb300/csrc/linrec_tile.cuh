@@ -61,6 +61,16 @@ __device__ __forceinline__ Unit unit_of(const Cut &cut, int B, int u, int cw) {
   return v;
 }
 
+// Whether a wait is to end unfinished: past its limit, or as another one ran out.
+__device__ __forceinline__ bool give_up(uint64_t deadline, int *err, volatile int *abort) {
+  if (!*abort && ld_volatile_int(err) != (int)DEV_TIMEOUT) {
+    if (globaltimer_ns() <= deadline) return false;
+    atomicCAS(err, (int)DEV_OK, (int)DEV_TIMEOUT);
+  }
+  *abort = 1;
+  return true;
+}
+
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
                                             int y, int z) {
   asm volatile(
@@ -299,6 +309,16 @@ __device__ __forceinline__ void put_peer(float2 *at, uint64_t *bar, int rank, co
 __device__ __forceinline__ void put_peer(float4 *at, uint64_t *bar, int rank, const Aff<F2> &a) {
   tc::st_async_v4(tc::mapa_shared(tc::smem_u32(at), rank), lo(a.p), hi(a.p), lo(a.e), hi(a.e),
                   tc::mapa_shared(tc::smem_u32(bar), rank));
+}
+
+// Until the cluster's blocks have sent a round's maps.  An error that is reported
+// and stepped over (a length out of range) ends no wait; one that ran out does.
+__device__ __forceinline__ void wait_round(uint64_t *bar, uint32_t parity, int *err,
+                                           volatile int *abort) {
+  if (tc::mbar_try_wait_cluster(bar, parity)) return;
+  const uint64_t deadline = globaltimer_ns() + WAIT_NS;
+  for (uint32_t spins = 1; !tc::mbar_try_wait_cluster(bar, parity); ++spins)
+    if ((spins & 255u) == 0 && give_up(deadline, err, abort)) return;
 }
 
 // ---- segments: the maps that a first launch leaves, [segment][row][group][lane]

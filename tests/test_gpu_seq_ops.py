@@ -394,6 +394,22 @@ def test_linrec_lengths_out_of_range_are_reported(ops):
     assert torch.equal(y, z) and ops.status() == 0
 
 
+def test_linrec_after_an_unread_report(ops):
+    """A length out of range that nobody has asked about yet ends no later call's waits."""
+    T, B, H = 4097, 3, 192
+    x, r, i, lam, h0 = (t.cuda() for t in rec_inputs(T, B, H, "bf16", 7))
+
+    def passes():
+        y, _, st = ops.linrec_forward(x, r, i, lam, h0=h0, states=True)
+        return (y, *ops.linrec_backward(y, x, r, i, lam, st))
+    want = passes()
+    assert ops.status() == 0
+    ops.linrec_forward(x, r, i, lam, lengths=torch.full((B,), T + 1, dtype=torch.int32, device="cuda"))
+    for _ in range(5):
+        assert all(torch.equal(p, q) for p, q in zip(passes(), want))
+    assert ops.status() == binding.RCU_ERR_LENGTHS
+
+
 def test_linrec_empty(ops):
     x = torch.empty(0, 2, 8, device="cuda")
     lam, h0 = torch.zeros(8, device="cuda"), torch.randn(2, 8, device="cuda")
