@@ -34,10 +34,15 @@ struct Smem {
   typename Slot<V>::type part[2][NW][32];     // the warps' P and R, by parity of the tile
   V fwd[2][NW][32];                           // and their E
   typename Slot<V>::type peer[2][MAXCS][32];  // the blocks' P and R, by parity of the round
-  V sum[NW][32];                              // the warps' shares of dlambda
+  V sum[NW][32];  // of dlambda, over the row or, with shares, all the block's rows
   uint64_t full[STAGES];
   uint64_t met[2];  // every block's map of a round is here, by parity of the round
   int abort;
+  Next next;
+  struct {
+    V k2, nk;  // the channel's rate, as rate() has it, and -K
+    Limits lim;
+  } chan[32];
 };
 
 // Bytes of a tile of a saved input (IT) and of all four.
@@ -61,78 +66,90 @@ __device__ __forceinline__ uint32_t tile_raw(const uint8_t *row, int lane) {
   return *row;
 }
 
-// MAP: only the backward map (P, R) of each segment but the first, from r and dy
-// alone, into `maps`, which the launch after it starts its segments from.
-template <typename IT, typename T, bool TMA, bool MAP>
+// MAPS: only the backward map (P, R) of each segment but the first, from r and dy
+// alone, into `mem`, which the launch after it starts its segments from.  (With
+// SHARES, mem has their carries.)
+template <typename IT, typename T, bool TMA, Mode M>
 __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
     linrec_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap mdy,
-                      const LinrecBwd p, const Cut cut, void *maps, float *__restrict__ partial, const bool words,
-                      const bool bulk_states, int *err) {
+                      const LinrecBwd p, const Cut cut, void *mem, float *__restrict__ partial,
+                      const bool words, const bool bulk_states, int *err) {
+  constexpr bool MAP = M == MAPS;
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   constexpr int IN = in_bytes<IT, T, TMA>(), TENSORS = tensor_bytes<IT, T, TMA>();
   constexpr int STAGE = stage_bytes<IT, T, TMA>();
   constexpr int IN_ROW = IN / STEPS, DY_ROW = in_bytes<T, T, TMA>() / STEPS;
   constexpr bool Q8 = sizeof(IT) == 1;
+  // fp32 copies its next tile after a tile's stores, not before them: T=512 B=128 H=1024
+  // 300 us, 325 the other way round (bf16 368 and 353)
+  constexpr bool LATE = TMA && !MAP && sizeof(IT) == 4;
   typedef typename Lane<T>::V V;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *ring = smem;
   Smem<V> &sh = *reinterpret_cast<Smem<V> *>(smem + STAGES * STAGE);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int cs = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
-  const int stride = gridDim.x / cs, u0 = blockIdx.x / cs;
+  const int cs = M == UNITS ? (int)tc::cluster_nctarank() : 1;
+  const int rank = M == UNITS ? (int)tc::cluster_ctarank() : 0;
+  const int stride = M == SHARES ? 1 : gridDim.x / cs, u0 = M == SHARES ? 0 : blockIdx.x / cs;
+  const int units = count_units<M>(cut, p.B);
 
-  const int skip = MAP ? p.B * cut.groups : 0;  // units of the first segment
   // Copies of the live tiles of this block, the last steps first: by TMA (thread
   // 0, the whole tile) or by each warp its own rows.
-  int pu = u0 - stride, issued = 0, tile1 = -1, len1 = 0;
-  Unit v1;  // whose tiles are being copied: the next one is tile1
-  v1.first = 0;
+  // With TMA it is one thread that copies: what it keeps for that is in shared memory,
+  // as its registers would be every thread's (bf16 T=512 B=256 H=1024: 345 us, 353 with
+  // registers).  Clusters, with more to do between two tiles, lose by it (238, 249).
+  constexpr bool ONE = TMA && M != UNITS;
+  Next own;
+  Next &next = ONE ? sh.next : own;
+  if (!ONE || threadIdx.x == 0) {
+    next.u = u0 - stride, next.issued = 0;
+    next.tile = -1, next.v.first = 0;
+  }
   auto issue = [&] {
-    while (true) {
-      if (tile1 < v1.first) {
-        if (pu >= cut.units - stride) break;
-        pu += stride;
-        v1 = unit_of(cut, p.B, pu + skip, CW);
-        len1 = row_length(p.lengths, v1.b, p.T, err);
-        tile1 = v1.last - 1 - rank;
-        const int dead = tile1 - (ceil_div(len1, STEPS) - 1);  // tiles past the row's end
-        if (dead > 0) tile1 -= ceil_div(dead, cs) * cs;
-        continue;
+    Unit v = next.v;
+    int tile = next.tile;
+    while (tile < v.first) {
+      if (next.u >= units - stride) {
+        if (!TMA) copy_commit();
+        return;
       }
-      const Unit &v = v1;
-      const int tile = tile1, len = len1;
-      tile1 -= cs;
-      uint8_t *dst = ring + issued % STAGES * STAGE;
-      if (TMA) {
-        uint64_t *bar = &sh.full[issued % STAGES];
-        const int states = bulk_states && !MAP ? min(CW, p.H - v.c0) * 4 : 0;
-        tc::mbar_arrive_expect_tx(bar, (MAP ? TENSORS - 2 * IN : TENSORS) + states);
-        if (states)
-          tc::bulk_load(dst + TENSORS, p.states + ((int64_t)tile * p.B + v.b) * p.H + v.c0, states,
-                        bar);
-        tma_load_3d(dst + IN, &mr, bar, v.c0, v.b, tile * STEPS);
-        if (!MAP) {
-          tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
-          tma_load_3d(dst + 2 * IN, &mi, bar, v.c0, v.b, tile * STEPS);
-        }
-        tma_load_3d(dst + 3 * IN, &mdy, bar, v.c0, v.b, tile * STEPS);
-      } else {
-        const int64_t tw = tile * STEPS + warp * S, b = v.b;
-        const int width = min(CW, p.H - v.c0), rows = (int)min(len - tw, (int64_t)S);
+      v = next.v = unit_of<M, true>(cut, p.B, next.u += stride, CW);
+      next.len = row_length(p.lengths, v.b, p.T, err);
+      tile = v.last - 1 - rank;
+      const int dead = tile - (ceil_div(next.len, STEPS) - 1);  // tiles past the row's end
+      if (dead > 0) tile -= ceil_div(dead, cs) * cs;
+      next.tile = tile;
+    }
+    next.tile = tile - cs;
+    const int issued = next.issued++;
+    uint8_t *dst = ring + issued % STAGES * STAGE;
+    if (TMA) {
+      uint64_t *bar = &sh.full[issued % STAGES];
+      const int states = bulk_states && !MAP ? min(CW, p.H - v.c0) * 4 : 0;
+      tc::mbar_arrive_expect_tx(bar, (MAP ? TENSORS - 2 * IN : TENSORS) + states);
+      if (states)
+        tc::bulk_load(dst + TENSORS, p.states + ((int64_t)tile * p.B + v.b) * p.H + v.c0, states,
+                      bar);
+      tma_load_3d(dst + IN, &mr, bar, v.c0, v.b, tile * STEPS);
+      if (!MAP) {
+        tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
+        tma_load_3d(dst + 2 * IN, &mi, bar, v.c0, v.b, tile * STEPS);
+      }
+      tma_load_3d(dst + 3 * IN, &mdy, bar, v.c0, v.b, tile * STEPS);
+    } else {
+      const int64_t tw = tile * STEPS + warp * S, b = v.b;
+      const int width = min(CW, p.H - v.c0), rows = (int)min(next.len - tw, (int64_t)S);
 #pragma unroll 1
-        for (int k = MAP ? 1 : 0; k < (MAP ? 2 : 3); ++k) {
-          const SeqIn &in = (&p.x)[k];
-          copy_rows<IT, CPT>(dst + k * IN + warp * S * IN_ROW,
-                             static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
-                             in.st * (int64_t)sizeof(IT), rows, width * (int)sizeof(IT));
-        }
-        copy_rows<T, CPT>(dst + 3 * IN + warp * S * DY_ROW,
-                          static_cast<const T *>(p.dy.p) + tw * p.dy.st + b * p.dy.sb + v.c0,
-                          p.dy.st * (int64_t)sizeof(T), rows, width * (int)sizeof(T));
+      for (int k = MAP ? 1 : 0; k < (MAP ? 2 : 3); ++k) {
+        const SeqIn &in = (&p.x)[k];
+        copy_rows<IT, CPT>(dst + k * IN + warp * S * IN_ROW,
+                           static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
+                           in.st * (int64_t)sizeof(IT), rows, width * (int)sizeof(IT));
       }
-      ++issued;
-      break;
+      copy_rows<T, CPT>(dst + 3 * IN + warp * S * DY_ROW,
+                        static_cast<const T *>(p.dy.p) + tw * p.dy.st + b * p.dy.sb + v.c0,
+                        p.dy.st * (int64_t)sizeof(T), rows, width * (int)sizeof(T));
     }
     if (!TMA) copy_commit();
   };
@@ -149,16 +166,17 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
+  set(sh.sum[warp][lane], 0.f);
   int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
+  bool small = false;
   V k2;
   Limits lim;
-  bool small = false;
-  for (int u = u0; u < cut.units; u += stride) {
-    const Unit v = unit_of(cut, p.B, u + skip, CW);
+  for (int u = u0; u < units; u += stride) {
+    const Unit v = unit_of<M, true>(cut, p.B, u, CW);
     const int len = row_length(p.lengths, v.b, p.T, err);
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
-    V nk, nc, sum, zero, minus;
+    V nc, sum, zero, minus;
     set(zero, 0.f);
     set(minus, -1.f);
     if (v.c0 != held) {
@@ -168,34 +186,27 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
       small = __all_sync(0xffffffffu, small_rate(k2));
     }
     const bool whole = v.c0 + CW <= p.H && words;
-    set(nk, -1.f / LOG2E);
-    nk = mul_v(nk, k2);  // -K
     set(nc, 0.f);
     if (p.dh_n) load_v(p.dh_n + row, live, nc);
     nc = neg_v(nc);  // the carry, negated: -dL/dh after the steps so far
     if (!MAP && v.seg < cut.nseg - 1)
-      nc = apply(chain_segments<V, NW>(maps, cut, p.B, v, CW, cut.nseg - 1, v.seg, -1, sh.part[0]),
+      nc = apply(chain_segments<V, NW>(mem, cut, p.B, v, CW, cut.nseg - 1, v.seg, -1, sh.part[0]),
                  nc);
+    if (M == SHARES && v.last < cut.tiles)
+      nc = take_carry<V>(mem, blockIdx.x - cut.groups, err, &sh.abort);
     Aff<V> all_map = identity<V>();
     sum = zero;
     // 8 bits: lane 8 k + s has the exponent of tensor k at the warp's step s, read a
-    // tile ahead from where `ep` points
-    const int8_t *ep = nullptr;
-    int64_t ep_step = 0;
-    int et = 0, ex = 0;  // et: the lane's step in the tile that ep is at
-    auto next_exponent = [&] {
-      ex = lane < 3 * S && et >= v.first * STEPS && et < len ? (int)__ldg(ep) : 0;
-      ep -= ep_step;
-      et -= cs * STEPS;
+    // tile ahead
+    int ex = 0;
+    auto read_exponent = [&](int tile) {
+      const int t = tile * STEPS + warp * S + lane % S, k = lane / S;
+      ex = 0;
+      if (k < 3 && tile >= v.first && t < len)
+        ex = (int)__ldg((k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e) +
+                        ((int64_t)t * p.et + v.b * p.eb) * ceil_div(p.H, BLOCK8) + v.c0 / BLOCK8);
     };
-    if (Q8) {
-      const int nb8 = ceil_div(p.H, BLOCK8), k = lane / S;
-      et = (v.last - 1 - rank) * STEPS + warp * S + lane % S;
-      ep = (k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e) + ((int64_t)et * p.et + v.b * p.eb) * nb8 +
-           v.c0 / BLOCK8;
-      ep_step = (int64_t)cs * STEPS * p.et * nb8;
-      next_exponent();
-    }
+    if (Q8) read_exponent(v.last - 1 - rank);
     for (int base = v.last - 1; base >= v.first; base -= cs) {
       const int tile = base - rank, tw = tile * STEPS + warp * S;
       const bool on = tile >= v.first && tile * STEPS < len;  // the same for the whole block
@@ -207,7 +218,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
         float scale[3][S];
         if (Q8) {
           const float f = power2(ex) * (lane < S ? 1.f : -LOG2E);
-          next_exponent();
+          read_exponent(tile - cs);
 #pragma unroll
           for (int k = 0; k < 3; ++k)
 #pragma unroll
@@ -276,7 +287,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
           mine.e = fma_v(em1[s], ne, ne);
         }
       }
-      if (Q8 && !on) next_exponent();
+      if (Q8 && !on) read_exponent(tile - cs);
       if (on) {
         ++used;
         if (!TMA) {
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
           if (cs > 1)
             tc::mbar_arrive_expect_tx(&sh.met[round & 1], cs * 32 * (uint32_t)sizeof(Aff<V>));
           // the tile's values are in registers: its buffer takes the next copy
-          if (TMA && on) issue();
+          if (TMA && on && !LATE) issue();
         }
         if (cs > 1) {
           Aff<V> all = identity<V>(), after = identity<V>();  // after: of the warps after this one
@@ -312,7 +323,6 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
               nc = apply(get(&sh.peer[round & 1][q][lane]), nc);
             }
           c = apply(after, c);
-          ++round;
         } else {
 #pragma unroll
           for (int w = NW - 1; w >= 0; --w) {
@@ -326,6 +336,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
         for (int w = 0; w < NW - 1; ++w)
           if (w < warp)
             h = fma_v(get(&sh.part[parity][w][lane]).p, h, sh.fwd[parity][w][lane]);
+        if (M == UNITS) ++round;
         parity ^= 1;
       }
       if (MAP || tile < v.first) continue;
@@ -339,6 +350,9 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
           dy[s] = fma_v(dy[s], minus, c);
           c = fma_v(em1[s], dy[s], dy[s]);
         }
+        V nk;
+        set(nk, -1.f / LOG2E);
+        nk = mul_v(nk, k2);
         V part = zero;
         if (whole && tw + S <= p.T) {
 #pragma unroll
@@ -366,6 +380,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
           }
         }
         sum = add_v(sum, part);
+        if (LATE && threadIdx.x == 0) issue();
       } else {
         for (int s = 0; s < S && tw + s < p.T; ++s) {
           if (p.dx.p) store_raw(dx, zero, live);
@@ -376,20 +391,29 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
       }
     }
     if (MAP) {
-      if (warp == 0) put(segment_map<V>(maps, cut, p.B, v.seg, v, CW), all_map);
+      if (warp == 0) put(segment_map<V>(mem, cut, p.B, v.seg, v, CW), all_map);
       continue;
     }
-    if (v.seg == 0 && rank == 0 && warp == 0 && p.dh0) store_v(p.dh0 + row, mul_v(nc, minus), live);
-    if (p.dlambda) {
+    if (rank == 0 && warp == 0) {
+      if (v.first == 0) {
+        if (p.dh0) store_v(p.dh0 + row, mul_v(nc, minus), live);
+      } else if (M == SHARES) {
+        leave_carry(mem, nc);
+      }
+    }
+    if (p.dlambda) sh.sum[warp][lane] = add_v(sh.sum[warp][lane], sum);
+    if (p.dlambda && !(M == SHARES && u < units - 1)) {
       __syncthreads();
-      sh.sum[warp][lane] = sum;
-      __syncthreads();
+      sum = zero;
       if (warp == 0) {
-        sum = zero;
 #pragma unroll
         for (int w = 0; w < NW; ++w) sum = add_v(sum, sh.sum[w][lane]);
-        store_v(partial + ((int64_t)(v.seg * p.B + v.b) * cs + rank) * p.H + ch, sum, live);
+        const int64_t at = M == SHARES ? blockIdx.x / cut.groups
+                                  : (int64_t)(v.seg * p.B + v.b) * cs + rank;
+        store_v(partial + at * p.H + ch, sum, live);
       }
+      __syncthreads();
+      sh.sum[warp][lane] = zero;
     }
   }
   if (cs > 1) tc::cluster_sync();  // no block leaves while a peer may still write to it
@@ -448,29 +472,38 @@ cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStr
   constexpr size_t SMEM =
       sizeof(Smem<typename Lane<T>::V>) + STAGES * stage_bytes<IT, T, TMA>();
   typedef typename Lane<T>::V V;
-  static const Resident res = resident(linrec_bwd_kernel<IT, T, TMA, false>, NT, MAXCS, SMEM, 0);
-  static const Resident res_map = resident(linrec_bwd_kernel<IT, T, TMA, true>, NT, 1, SMEM, 0);
-  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, 0.5);
-  const int64_t rows = (int64_t)p.B * pl.cut.nseg * pl.cs;
-  // the workspace: the segments' maps, then dlambda's partial sums
-  const size_t map_bytes = pl.cut.nseg > 1 ? (size_t)pl.cut.units * 32 * sizeof(Aff<V>) : 0;
+  static const Resident res = resident(linrec_bwd_kernel<IT, T, TMA, UNITS>, NT, MAXCS, SMEM, 0);
+  static const Resident res_map = resident(linrec_bwd_kernel<IT, T, TMA, MAPS>, NT, 1, SMEM, 0);
+  static const int blocks =
+      resident(linrec_bwd_kernel<IT, T, TMA, SHARES>, NT, 1, SMEM, 0).clusters[1];
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, blocks, 0.5);
+  const int64_t rows = pl.cut.share ? pl.grid / pl.cut.groups : (int64_t)p.B * pl.cut.nseg * pl.cs;
+  // the workspace: the segments' maps or the shares' carries, then dlambda's partial sums
+  const size_t flags = pl.cut.share % pl.cut.tiles ? carry_flags(pl.grid) : 0;
+  const size_t map_bytes = flags             ? flags + (size_t)pl.grid * 32 * sizeof(V)
+                           : pl.cut.nseg > 1 ? (size_t)pl.cut.units * 32 * sizeof(Aff<V>)
+                                             : 0;
   const size_t sum_bytes = p.dlambda ? (size_t)rows * p.H * 4 : 0;
   uint8_t *mem = nullptr;
   cudaError_t e = cudaSuccess;
   if (map_bytes + sum_bytes) e = ws.get(map_bytes + sum_bytes, &mem);
   if (e != cudaSuccess) return e;
   float *partial = reinterpret_cast<float *>(mem + map_bytes);
+  if (flags) e = cudaMemsetAsync(mem, 0, flags, s);
+  if (e != cudaSuccess) return e;
   if (pl.cut.nseg > 1) {
     Plan first = pl;
     first.cut.units = pl.cut.units / pl.cut.nseg * (pl.cut.nseg - 1);
     first.grid = std::min(first.cut.units, res_map.clusters[1]);
-    e = launch_cut(linrec_bwd_kernel<IT, T, TMA, true>, first, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
+    e = launch_cut(linrec_bwd_kernel<IT, T, TMA, MAPS>, first, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
                    v.m[3], p, first.cut, (void *)mem, partial, v.words, v.states, err);
     if (e != cudaSuccess) return e;
     ++*launches;
   }
-  e = launch_cut(linrec_bwd_kernel<IT, T, TMA, false>, pl, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
-                 v.m[3], p, pl.cut, (void *)mem, partial, v.words, v.states, err);
+  e = launch_cut(pl.cut.share ? linrec_bwd_kernel<IT, T, TMA, SHARES>
+                              : linrec_bwd_kernel<IT, T, TMA, UNITS>,
+                 pl, NT, SMEM, s, v.m[0], v.m[1], v.m[2], v.m[3], p, pl.cut, (void *)mem, partial,
+                 v.words, v.states, err);
   ++*launches;
   if (e != cudaSuccess || !p.dlambda) return e;
   ++*launches;

@@ -84,14 +84,15 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, con
   }
 }
 
-// MAP: only the affine map of each segment but the last, into `maps`, which the
-// launch after it starts its segments from.
-template <typename T, bool TMA, bool MAP>
+// MAPS: only the affine map of each segment but the last, into `mem`, which the
+// launch after it starts its segments from.  (With SHARES, mem has their carries.)
+template <typename T, bool TMA, Mode M>
 __global__ void __launch_bounds__(NT, PER_SM)
     linrec_fwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap my,
                       const LinrecFwd p, const Cut cut,
-                      void *maps, const bool words, int *err) {
+                      void *mem, const bool words, int *err) {
+  constexpr bool MAP = M == MAPS;
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   typedef typename Lane<T>::V V;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -101,48 +102,49 @@ __global__ void __launch_bounds__(NT, PER_SM)
   Smem<V> &sh = *reinterpret_cast<Smem<V> *>(out + (TMA ? TILE_BYTES : 0));
   typename Slot<V>::type *peers = reinterpret_cast<typename Slot<V>::type *>(&sh + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int cs = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
-  const int stride = gridDim.x / cs, u0 = blockIdx.x / cs;
+  const int cs = M == UNITS ? (int)tc::cluster_nctarank() : 1;
+  const int rank = M == UNITS ? (int)tc::cluster_ctarank() : 0;
+  const int stride = M == SHARES ? 1 : gridDim.x / cs, u0 = M == SHARES ? 0 : blockIdx.x / cs;
+  const int units = count_units<M>(cut, p.B);
 
   // Copies of the live tiles of this block, in the order they are used: by TMA
   // (thread 0, the whole tile) or by each warp its own rows.
-  int pu = u0 - stride, issued = 0, tile1 = 0, end1 = 0, len1 = 0;
-  Unit v1;  // whose tiles are being copied: the next one is tile1, and end1 ends them
+  Next next;
+  next.u = u0 - stride, next.issued = next.tile = next.end = 0;
   auto issue = [&] {
-    while (true) {
-      if (tile1 >= end1) {
-        if (pu >= cut.units - stride) break;
-        pu += stride;
-        v1 = unit_of(cut, p.B, pu, CW);
-        len1 = row_length(p.lengths, v1.b, p.T, err);
-        tile1 = v1.first + rank;
-        end1 = min(v1.last, ceil_div(len1, STEPS));
-        continue;
+    Unit v = next.v;
+    int tile = next.tile, end = next.end;
+    while (tile >= end) {
+      if (next.u >= units - stride) {
+        if (!TMA) copy_commit();
+        return;
       }
-      const Unit &v = v1;
-      const int tile = tile1, len = len1;
-      tile1 += cs;
-      uint8_t *dst = ring + issued % STAGES * STAGE;
-      if (TMA) {
-        uint64_t *bar = &sh.full[issued % STAGES];
-        tc::mbar_arrive_expect_tx(bar, STAGE);
-        tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
-        tma_load_3d(dst + STAGE / 3, &mr, bar, v.c0, v.b, tile * STEPS);
-        tma_load_3d(dst + 2 * STAGE / 3, &mi, bar, v.c0, v.b, tile * STEPS);
-      } else {
-        const int64_t tw = tile * STEPS + warp * S;
-        const int bytes = min(CW, p.H - v.c0) * (int)sizeof(T);
+      v = next.v = unit_of<M, false>(cut, p.B, next.u += stride, CW);
+      next.len = row_length(p.lengths, v.b, p.T, err);
+      tile = v.first + rank;
+      next.tile = tile;
+      next.end = end = min(v.last, ceil_div(next.len, STEPS));
+    }
+    next.tile = tile + cs;
+    const int issued = next.issued++;
+    uint8_t *dst = ring + issued % STAGES * STAGE;
+    if (TMA) {
+      uint64_t *bar = &sh.full[issued % STAGES];
+      tc::mbar_arrive_expect_tx(bar, STAGE);
+      tma_load_3d(dst, &mx, bar, v.c0, v.b, tile * STEPS);
+      tma_load_3d(dst + STAGE / 3, &mr, bar, v.c0, v.b, tile * STEPS);
+      tma_load_3d(dst + 2 * STAGE / 3, &mi, bar, v.c0, v.b, tile * STEPS);
+    } else {
+      const int64_t tw = tile * STEPS + warp * S;
+      const int bytes = min(CW, p.H - v.c0) * (int)sizeof(T);
 #pragma unroll 1
-        for (int k = 0; k < 3; ++k) {
-          const SeqIn &in = (&p.x)[k];
-          copy_rows<T, CPT>(
-              dst + k * (STAGE / 3) + warp * (STAGE / 3 / NW),
-              static_cast<const T *>(in.p) + tw * in.st + (int64_t)v.b * in.sb + v.c0,
-              in.st * (int64_t)sizeof(T), (int)min(len - tw, (int64_t)S), bytes);
-        }
+      for (int k = 0; k < 3; ++k) {
+        const SeqIn &in = (&p.x)[k];
+        copy_rows<T, CPT>(
+            dst + k * (STAGE / 3) + warp * (STAGE / 3 / NW),
+            static_cast<const T *>(in.p) + tw * in.st + (int64_t)v.b * in.sb + v.c0,
+            in.st * (int64_t)sizeof(T), (int)min(next.len - tw, (int64_t)S), bytes);
       }
-      ++issued;
-      break;
     }
     if (!TMA) copy_commit();
   };
@@ -167,16 +169,16 @@ __global__ void __launch_bounds__(NT, PER_SM)
   V first;
   int len0 = p.T;
   auto look = [&](int u) {
-    if (u >= cut.units) return;
-    const Unit v = unit_of(cut, p.B, u, CW);
+    if (u >= units) return;
+    const Unit v = unit_of<M, false>(cut, p.B, u, CW);
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     set(first, 0.f);
     if (p.h0) load_v(p.h0 + (int64_t)v.b * p.H + ch, live, first);
     len0 = row_length(p.lengths, v.b, p.T, err);
   };
   look(u0);
-  for (int u = u0; u < cut.units; u += stride) {
-    const Unit v = unit_of(cut, p.B, u, CW);
+  for (int u = u0; u < units; u += stride) {
+    const Unit v = unit_of<M, false>(cut, p.B, u, CW);
     const int len = len0;
     const int ch = v.c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
     const int64_t row = (int64_t)v.b * p.H + ch;
@@ -188,9 +190,11 @@ __global__ void __launch_bounds__(NT, PER_SM)
     }
     V carry = neg_v(first);  // the kernel has -b at hand, and so works on -h throughout
     look(u + stride);
+    if (M == SHARES && v.first > 0)
+      carry = take_carry<V>(mem, blockIdx.x - cut.groups, err, &sh.abort);
     Aff<V> whole = identity<V>();
     if (!MAP && v.seg > 0)
-      carry = apply(chain_segments<V, NW>(maps, cut, p.B, v, CW, 0, v.seg, 1, sh.part[0]), carry);
+      carry = apply(chain_segments<V, NW>(mem, cut, p.B, v, CW, 0, v.seg, 1, sh.part[0]), carry);
     for (int base = v.first; base < v.last; base += cs) {
       const int tile = base + rank, tw = tile * STEPS + warp * S;
       const bool on = tile < v.last && tile * STEPS < len;  // the same for the whole block
@@ -320,8 +324,14 @@ __global__ void __launch_bounds__(NT, PER_SM)
       }
     }
     if (MAP) {
-      if (warp == 0) put(segment_map<V>(maps, cut, p.B, v.seg, v, CW), whole);
-    } else if (rank == 0 && warp == 0 && p.h_n && v.seg == cut.nseg - 1) store_v(p.h_n + row, neg_v(carry), live);
+      if (warp == 0) put(segment_map<V>(mem, cut, p.B, v.seg, v, CW), whole);
+    } else if (rank == 0 && warp == 0) {
+      if (v.last == cut.tiles) {
+        if (p.h_n) store_v(p.h_n + row, neg_v(carry), live);
+      } else if (M == SHARES) {
+        leave_carry(mem, carry);
+      }
+    }
   }
   if (TMA && lane == 0) store_wait();
   if (cs > 1) tc::cluster_sync();  // no block leaves while a peer may still write to it
@@ -335,27 +345,34 @@ cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], DevMem &ws, int *
       sizeof(Smem<V>) + STAGES * stage_bytes<T, TMA>() + (TMA ? TILE_BYTES : 0);
   constexpr size_t SMEM_PER_CS = 2 * 32 * sizeof(Aff<V>);
   static const Resident res =
-      resident(linrec_fwd_kernel<T, TMA, false>, NT, MAXCS, SMEM0, SMEM_PER_CS);
+      resident(linrec_fwd_kernel<T, TMA, UNITS>, NT, MAXCS, SMEM0, SMEM_PER_CS);
   static const Resident res_map =
-      resident(linrec_fwd_kernel<T, TMA, true>, NT, 1, SMEM0, SMEM_PER_CS);
-  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, 0.8);
+      resident(linrec_fwd_kernel<T, TMA, MAPS>, NT, 1, SMEM0, SMEM_PER_CS);
+  static const int blocks =
+      resident(linrec_fwd_kernel<T, TMA, SHARES>, NT, 1, SMEM0, SMEM_PER_CS).clusters[1];
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, blocks, 0.8);
   const size_t smem = SMEM0 + pl.cs * SMEM_PER_CS;
   const bool words = word_aligned(p.y.p, p.y.st, p.y.sb, sizeof(T));
-  void *maps = nullptr;
-  if (pl.cut.nseg > 1) {
+  void *mem = nullptr;
+  cudaError_t e = cudaSuccess;
+  if (pl.cut.share % pl.cut.tiles) {
+    const size_t flags = carry_flags(pl.grid);
+    e = ws.get(flags + (size_t)pl.grid * 32 * sizeof(V), &mem);
+    if (e == cudaSuccess) e = cudaMemsetAsync(mem, 0, flags, s);
+  } else if (pl.cut.nseg > 1) {
     Plan first = pl;
     first.cut.units = pl.cut.units / pl.cut.nseg * (pl.cut.nseg - 1);
     first.grid = std::min(first.cut.units, res_map.clusters[1]);
-    cudaError_t e = ws.get((size_t)first.cut.units * 32 * sizeof(Aff<V>), &maps);
+    e = ws.get((size_t)first.cut.units * 32 * sizeof(Aff<V>), &mem);
     if (e == cudaSuccess)
-      e = launch_cut(linrec_fwd_kernel<T, TMA, true>, first, NT, smem, s, m[0], m[1], m[2], m[3], p,
-                     first.cut, maps, words, err);
-    if (e != cudaSuccess) return e;
+      e = launch_cut(linrec_fwd_kernel<T, TMA, MAPS>, first, NT, smem, s, m[0], m[1], m[2], m[3], p,
+                     first.cut, mem, words, err);
     ++*launches;
   }
+  if (e != cudaSuccess) return e;
   ++*launches;
-  return launch_cut(linrec_fwd_kernel<T, TMA, false>, pl, NT, smem, s, m[0], m[1], m[2], m[3], p,
-                    pl.cut, maps, words, err);
+  return launch_cut(pl.cut.share ? linrec_fwd_kernel<T, TMA, SHARES> : linrec_fwd_kernel<T, TMA, UNITS>,
+                    pl, NT, smem, s, m[0], m[1], m[2], m[3], p, pl.cut, mem, words, err);
 }
 
 template <typename T>

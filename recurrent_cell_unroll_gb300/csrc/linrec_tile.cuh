@@ -44,14 +44,56 @@ __device__ __forceinline__ int row_length(const int32_t *lengths, int b, int T, 
 // Unit u = (segment of time, batch row, group of CW channels), the groups
 // fastest: blocks that run together then read neighbouring channels of the same
 // steps.  A cluster takes a unit, its blocks consecutive tiles of it.
+//
+// Or the blocks have equal shares of the tiles: those of a group's rows, one behind
+// another, are cut into pieces of `share`, no fewer than a row has, so that a cut
+// row has two blocks.  A block takes its pieces of rows backwards: the row that its
+// share ends in first, and last the one that the block before it has begun, whose
+// carry is there by then, being the first that block made.
 struct Cut {
-  int groups, units, tiles, tps, nseg;  // tps: tiles of a segment
+  int groups, units, tiles, tps, nseg, share;  // tps: tiles of a segment; share: 0 or as above
 };
 struct Unit {
   int seg, b, c0, first, last;  // tiles [first, last)
 };
+// The next tile to be copied, and of which unit
+struct Next {
+  int u, tile, end, len, issued;  // end: of its tiles, forwards
+  Unit v;
+};
+// This block's share [lo, hi) of its group's tiles, counted as they are processed
+struct Share {
+  int lo, hi;
+};
+__device__ __forceinline__ Share share_of(const Cut &cut, int B) {
+  const int lo = (int)blockIdx.x / cut.groups * cut.share;
+  return {lo, min(lo + cut.share, B * cut.tiles)};
+}
+// How a kernel goes through them: clusters over whole units (or a unit's segments),
+// the first launch that reduces the segments to their maps, blocks with shares.
+enum Mode { UNITS, MAPS, SHARES };
+
+template <Mode M>
+__device__ __forceinline__ int count_units(const Cut &cut, int B) {
+  if (M != SHARES) return cut.units;
+  const Share s = share_of(cut, B);
+  return (s.hi - 1) / cut.tiles - s.lo / cut.tiles + 1;
+}
+// BACK: the tiles are processed from the last to the first.
+template <Mode M, bool BACK>
 __device__ __forceinline__ Unit unit_of(const Cut &cut, int B, int u, int cw) {
   Unit v;
+  if (M == SHARES) {
+    const Share s = share_of(cut, B);
+    v.seg = 0;
+    v.b = (s.hi - 1) / cut.tiles - u;
+    v.c0 = (int)blockIdx.x % cut.groups * cw;
+    const int from = max(s.lo - v.b * cut.tiles, 0), to = min(s.hi - v.b * cut.tiles, cut.tiles);
+    v.first = BACK ? cut.tiles - to : from;
+    v.last = BACK ? cut.tiles - from : to;
+    return v;
+  }
+  if (BACK && M == MAPS) u += B * cut.groups;  // not of the first segment
   v.c0 = u % cut.groups * cw;
   const int q = u / cut.groups;
   v.b = q % B;
@@ -321,6 +363,34 @@ __device__ __forceinline__ void wait_round(uint64_t *bar, uint32_t parity, int *
     if ((spins & 255u) == 0 && give_up(deadline, err, abort)) return;
 }
 
+// ---- shares: the carry of a row that this block leaves to the next of its group.
+// mem: [blocks] counts of lanes that have, zero before the launch, then [blocks][32]
+// carries.  (Lane by lane: a warp's barrier cost the backward registers in its loop.)
+
+constexpr size_t carry_flags(int blocks) { return ((size_t)blocks * 4 + 15) / 16 * 16; }
+
+template <typename V>
+__device__ __forceinline__ V *carry_at(void *mem, int block) {
+  return reinterpret_cast<V *>(static_cast<uint8_t *>(mem) + carry_flags(gridDim.x)) + block * 32 +
+         threadIdx.x % 32;
+}
+// by one warp
+template <typename V>
+__device__ __forceinline__ void leave_carry(void *mem, V carry) {
+  *carry_at<V>(mem, blockIdx.x) = carry;
+  red_release_gpu_add(static_cast<unsigned *>(mem) + blockIdx.x, 1);
+}
+// by each warp; that block runs (a cooperative launch) and left it before all its other work
+template <typename V>
+__device__ __forceinline__ V take_carry(void *mem, int from, int *err, volatile int *abort) {
+  const unsigned *lanes = static_cast<const unsigned *>(mem) + from;
+  if (ld_acquire_gpu(lanes) != 32) {
+    const uint64_t deadline = globaltimer_ns() + WAIT_NS;
+    while (ld_acquire_gpu(lanes) != 32 && !give_up(deadline, err, abort)) __nanosleep(100);
+  }
+  return __ldcg(carry_at<V>(mem, from));
+}
+
 // ---- segments: the maps that a first launch leaves, [segment][row][group][lane]
 
 template <typename V>
@@ -402,16 +472,23 @@ Resident resident(void (*fn)(KArgs...), int threads, int max_cs, size_t smem0, s
 // block.  A larger cluster splits a sequence further, which pays where there
 // are fewer rows than blocks (or a last, thin wave of them), and costs its
 // blocks' exchange and their waiting for one another, some three tenths of a turn
-// (backward from 8 bits, T=1000 B=32 H=1024: 145 us without clusters, 159 in
-// pairs, though 16 turns each; 32 rows of 65536 steps forward: 250 us with 12
-// blocks a row, 290 with 8).
+// (backward from 8 bits, T=1000 B=32 H=1024: 145 us in whole rows, 159 in pairs,
+// though 32 turns each; 32 rows of 65536 steps forward: 250 us with 12 blocks a
+// row, 290 with 8).
+//
+// With more rows than blocks, but few for each, whole rows leave blocks idle in the
+// last wave; equal shares of the tiles cost
+// about a turn, the flags' clearing and a cooperative launch.
+// bf16 H=1024 T=1000: backward B=24 113 -> 78 us, from 8 bits B=32 144 -> 117,
+// forward B=29 65 -> 50.  (A row is never cut in three: the middle would wait for
+// the first and the last for both.)
 //
 // With few rows, clusters leave most of the GPU idle: then the sequence is cut into
-// segments that run as rows of their own, after a first launch (costing `share` of
+// segments that run as rows of their own, after a first launch (costing `map` of
 // the second) has reduced each segment to its affine map.  One row of 65536 steps x
 // 256 channels, bf16: forward 159 us in a cluster of 12, 57 us in segments;
 // backward 389 and 82.
-inline Plan plan_cut(int tiles, int B, int groups, const Resident &res, double share) {
+inline Plan plan_cut(int tiles, int B, int groups, const Resident &res, int blocks, double map) {
   Plan pl;
   const int64_t rows = (int64_t)B * groups;
   double best = 0;
@@ -424,7 +501,20 @@ inline Plan plan_cut(int tiles, int B, int groups, const Resident &res, double s
   }
   pl.cut.nseg = 1;
   const int nseg = (int)std::min<int64_t>(res.clusters[1] / rows, tiles / 4);
-  if (nseg > 1 && (1 + share) * ceil_div(tiles, nseg) + 6 < best) pl.cut.nseg = nseg, pl.cs = 1;
+  if (nseg > 1 && (1 + map) * ceil_div(tiles, nseg) + 6 < best)
+    best = (1 + map) * ceil_div(tiles, nseg) + 6, pl.cut.nseg = nseg, pl.cs = 1;
+  pl.cut.share = 0;
+  const int each = blocks / groups;  // blocks of a group
+  if (each > 0 && (int64_t)B * tiles < 1 << 30) {
+    const int cut = std::max(tiles, ceil_div(B * tiles, each)), whole = ceil_div(B, each) * tiles;
+    const int share = cut + 1 < whole ? cut : whole;
+    if (share + (share == cut) <= best || share == best) {
+      pl.cs = 1;
+      pl.cut = Cut{groups, (int)rows, tiles, tiles, 1, share};
+      pl.grid = ceil_div(B * tiles, share) * groups;
+      return pl;
+    }
+  }
   pl.cut.groups = groups;
   pl.cut.tiles = tiles;
   pl.cut.tps = ceil_div(tiles, pl.cut.nseg);
@@ -447,11 +537,17 @@ cudaError_t launch_cut(void (*fn)(KArgs...), const Plan &pl, int threads, size_t
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = pl.cs;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  const bool waits = pl.cut.share && pl.cut.share % pl.cut.tiles;
+  if (waits) {  // blocks wait for one another
+    at.id = cudaLaunchAttributeCooperative;
+    at.val.cooperative = 1;
+  } else {
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = pl.cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  }
   cfg.attrs = &at;
-  cfg.numAttrs = pl.cs > 1 ? 1 : 0;
+  cfg.numAttrs = pl.cs > 1 || waits ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 

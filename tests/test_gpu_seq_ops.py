@@ -315,6 +315,44 @@ def test_linrec_segments(ops, path, T, B, H, lengths):
     assert ops.launch_count() == 3
 
 
+@pytest.mark.parametrize("dtype,T,B,H,batch_first,act,lengths",
+                         [("bf16", 130, 500, 40, False, False, None),
+                          ("bf16", 200, 131, 300, True, False, "mixed"),
+                          ("f32", 130, 350, 64, False, True, "mixed"),
+                          ("bf16", 321, 160, 200, False, True, None),
+                          ("f32", 70, 600, 33, True, False, "mixed")])
+def test_linrec_shares(ops, path, dtype, T, B, H, batch_first, act, lengths):
+    """More rows than blocks and no multiple of them: rows that two blocks have a part of."""
+    if lengths:
+        g = torch.Generator().manual_seed(B)
+        lengths = torch.randint(0, T + 1, (B,), generator=g).tolist()
+    check_rec(ops, T, B, H, dtype, batch_first, lengths, act=act)
+
+
+def test_linrec_shares_in_a_graph(ops, path):
+    """Replays start from flags of their own, and give the same bits each time."""
+    x, r, i, lam, h0 = (t.cuda() for t in rec_inputs(130, 500, 40, "bf16", 31))
+
+    def passes():
+        y, h_n, st = ops.linrec_forward(x, r, i, lam, h0=h0, states=True)
+        return (y, h_n, *ops.linrec_backward(y, x, r, i, lam, st, dh_n=h_n))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = passes()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = passes()
+    for _ in range(3):
+        for t in held:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(held, want))
+    assert ops.status() == 0
+
+
 def test_linrec_nan_codes(ops, path):
     """A code that is not a number reaches what its value enters, and no more."""
     T, B, H = 70, 1, 64
