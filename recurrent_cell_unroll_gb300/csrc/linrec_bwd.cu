@@ -70,7 +70,7 @@ __device__ __forceinline__ uint32_t tile_raw(const uint8_t *row, int lane) {
 // alone, into `mem`, which the launch after it starts its segments from.  (With
 // SHARES, mem has their carries.)
 template <typename IT, typename T, bool TMA, Mode M>
-__global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 ? PER_SM : 1)
+__global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER_SM : 1)
     linrec_bwd_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mr,
                       const __grid_constant__ CUtensorMap mi, const __grid_constant__ CUtensorMap mdy,
                       const LinrecBwd p, const Cut cut, void *mem, float *__restrict__ partial,
