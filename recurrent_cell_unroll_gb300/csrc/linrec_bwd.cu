@@ -23,8 +23,9 @@ using namespace linrec;
 
 // Eight warps of 8 steps: the tile is what one kept state covers, and 16 steps a
 // lane would need more than the 255 registers a thread can have.  Two blocks an SM
-// (128 registers); bf16 rows that TMA cannot address take more, and one block is
-// faster there (T=15731 B=1 H=2133: 282 us, 308 with two).
+// (128 registers); bf16 rows that TMA cannot address take more, and beside a cluster's
+// exchange one block is faster there (T=15731 B=1 H=2133: 282 us, 308 with two; with
+// shares two are: T=521 B=86 H=748 199 us, 305 with one).
 constexpr int NW = 8, NT = 32 * NW, S = CHUNK / NW, STEPS = CHUNK, STAGES = 2, PER_SM = 2;
 constexpr int MAXCS = 8;  // blocks of a cluster
 constexpr int BATCH = 4;  // pairs whose gates are computed together
@@ -166,6 +167,9 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
+  // the inputs' rows lie alike
+  const bool same = !TMA && p.x.st == p.r.st && p.x.st == p.i.st && p.x.sb == p.r.sb &&
+                    p.x.sb == p.i.sb && alike(p.x.p, p.r.p) && alike(p.x.p, p.i.p);
   set(sh.sum[warp][lane], 0.f);
   int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
   bool small = false;
@@ -242,23 +246,33 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
         } else {
           copy_wait<STAGES - 1>();
           __syncwarp();
-          const int64_t b = v.b;
+          auto row_off = [&](const SeqIn &in, int size) {
+            return (uint32_t)(reinterpret_cast<uintptr_t>(in.p) +
+                              ((int64_t)tw * in.st + (int64_t)v.b * in.sb + v.c0) * size) & 15;
+          };
+          if (MAP) {
+            const uint32_t off[1] = {row_off(p.r, sizeof(IT))},
+                           more[1] = {(uint32_t)p.r.st * (int)sizeof(IT)};
+            uint32_t rr[1][S];
+            loose_rows<IT, CPT>(src + IN + warp * S * IN_ROW, 0, off, more, true, rr);
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const SeqIn &in = (&p.x)[k];
-            if (MAP && k != 1) {
+            for (int s = 0; s < S; ++s) raw[0][s] = raw[2][s] = 0u, raw[1][s] = rr[0][s];
+          } else {
+            uint32_t off[3], more[3];
 #pragma unroll
-              for (int s = 0; s < S; ++s) raw[k][s] = 0u;
-              continue;
+            for (int k = 0; k < 3; ++k) {
+              const SeqIn &in = (&p.x)[k];
+              off[k] = row_off(in, sizeof(IT));
+              more[k] = (uint32_t)in.st * (int)sizeof(IT);
             }
-            loose_rows<IT, CPT, S>(
-                src + k * IN + warp * S * IN_ROW,
-                static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
-                in.st * (int64_t)sizeof(IT), raw[k]);
+            loose_rows<IT, CPT>(src + warp * S * IN_ROW, IN, off, more, same, raw);
           }
-          loose_rows<T, CPT, S>(src + 3 * IN + warp * S * DY_ROW,
-                                static_cast<const T *>(p.dy.p) + tw * p.dy.st + b * p.dy.sb + v.c0,
-                                p.dy.st * (int64_t)sizeof(T), rawd);
+          const uint32_t off[1] = {row_off(p.dy, sizeof(T))},
+                         more[1] = {(uint32_t)p.dy.st * (int)sizeof(T)};
+          uint32_t rd[1][S];
+          loose_rows<T, CPT>(src + 3 * IN + warp * S * DY_ROW, 0, off, more, true, rd);
+#pragma unroll
+          for (int s = 0; s < S; ++s) rawd[s] = rd[0][s];
         }
         if (tw >= len) {  // a warp past the row's end has the identity
 #pragma unroll
@@ -527,7 +541,7 @@ cudaError_t linrec::launch_dlambda(const float *partial, int64_t rows, const Lin
 
 cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm, bool vec,
                               cudaStream_t s, int *launches) {
-  if (linrec::short_bwd_pays(p, PER_SM * nsm))
+  if (linrec::short_bwd_pays(p, PER_SM * nsm, vec))
     return linrec::launch_short_bwd(p, ws, err, nsm, s, launches);
   const bool q8 = p.saved == RCU_I8;
   if (p.dtype == RCU_BF16)

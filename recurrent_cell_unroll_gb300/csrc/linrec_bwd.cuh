@@ -181,8 +181,8 @@ __device__ __forceinline__ void spoil_codes(const uint32_t (&raw)[3][N], V (&em1
 // dlambda from partial sums: partial [rows][H] (linrec_bwd.cu)
 cudaError_t launch_dlambda(const float *partial, int64_t rows, const LinrecBwd &p, cudaStream_t s);
 // The kernel for short sequences of many rows (linrec_bwd_short.cu), and whether it is
-// the faster one; resident_blocks: of the tiled kernel.
-bool short_bwd_pays(const LinrecBwd &p, int resident_blocks);
+// the faster one; resident_blocks: of the tiled kernel, vec: as of launch_linrec_bwd.
+bool short_bwd_pays(const LinrecBwd &p, int resident_blocks, bool vec);
 cudaError_t launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s,
                              int *launches);
 

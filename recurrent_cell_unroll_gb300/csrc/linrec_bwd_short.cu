@@ -8,6 +8,11 @@
 // constants it keeps, from one batch row to the next.  Making the gates twice tells
 // with the length: bf16 B=250 H=2048 takes 91 us here and 118 tiled at 20 steps, 165
 // and 122 at 40; fp32 B=183 H=3312 158 and 202 at 17 steps.
+//
+// How far it pays goes by the rows: those that TMA cannot address cost the tiled kernel
+// more, and this one only where a lane's values are not a word.  B=188, here and tiled:
+// fp32 H=1921 T=48 217 and 234 us; bf16 H=1922 T=18 91 and 127, T=26 132 and 129;
+// H=1921 T=12 113 and 127, T=18 187 and 126.
 #include "linrec_bwd.cuh"
 
 namespace rcu {
@@ -16,7 +21,8 @@ namespace {
 using namespace linrec;
 
 constexpr int NW = 4, NT = 32 * NW, N = 4;  // N: steps whose reads are in flight together
-constexpr int SHORT_T = 20;
+constexpr int SHORT_T = 20, SHORT_LOOSE = 48, SHORT_SPLIT = 13;  // most steps: TMA's rows; fp32
+                                                                 // rows off it; split words
 
 // A lane's values of a step from global memory (`word`: as one access)
 template <typename IT, int CPT>
@@ -191,9 +197,25 @@ cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t 
 
 }  // namespace
 
-bool linrec::short_bwd_pays(const LinrecBwd &p, int resident_blocks) {
-  const int groups = ceil_div(p.H, p.dtype == RCU_BF16 ? Shape<bf16>::CW : Shape<float>::CW);
-  return p.T <= SHORT_T && (int64_t)p.B * groups >= resident_blocks;
+bool linrec::short_bwd_pays(const LinrecBwd &p, int resident_blocks, bool vec) {
+  const bool half = p.dtype == RCU_BF16;
+  const int groups = ceil_div(p.H, half ? Shape<bf16>::CW : Shape<float>::CW);
+  if (p.T > SHORT_LOOSE || (int64_t)p.B * groups < resident_blocks) return false;
+  // whether the inputs' rows start on multiples of `bytes` (8-bit ones of `bytes8`)
+  auto aligned = [&](int bytes, int bytes8) {
+    const SeqIn *in[4] = {&p.x, &p.r, &p.i, &p.dy};
+    for (int k = 0; k < 4; ++k) {
+      const bool q8 = k < 3 && p.saved == RCU_I8;
+      const int size = q8 ? 1 : half ? 2 : 4, to = q8 ? bytes8 : bytes;
+      if (reinterpret_cast<uintptr_t>(in[k]->p) % to || in[k]->st * size % to ||
+          in[k]->sb * size % to)
+        return false;
+    }
+    return true;
+  };
+  if (vec && aligned(16, 16)) return p.T <= SHORT_T;
+  if (!half) return true;
+  return p.T <= (aligned(4, 2) ? SHORT_T : SHORT_SPLIT);
 }
 
 cudaError_t linrec::launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm,

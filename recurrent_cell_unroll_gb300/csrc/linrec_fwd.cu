@@ -161,6 +161,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
+  // the inputs' rows lie alike
+  const bool same = !TMA && p.x.st == p.r.st && p.x.st == p.i.st && p.x.sb == p.r.sb &&
+                    p.x.sb == p.i.sb && alike(p.x.p, p.r.p) && alike(p.x.p, p.i.p);
   int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
   V k2;
   Limits lim;
@@ -214,14 +217,15 @@ __global__ void __launch_bounds__(NT, PER_SM)
         } else {
           copy_wait<STAGES - 1>();
           __syncwarp();
+          uint32_t off[3], more[3];
 #pragma unroll
           for (int k = 0; k < 3; ++k) {
             const SeqIn &in = (&p.x)[k];
-            loose_rows<T, CPT, S>(src + k * (STAGE / 3),
-                                  static_cast<const T *>(in.p) + (int64_t)tw * in.st +
-                                      (int64_t)v.b * in.sb + v.c0,
-                                  in.st * (int64_t)sizeof(T), raw[k]);
+            off[k] = (uint32_t)(reinterpret_cast<uintptr_t>(in.p) +
+                                ((int64_t)tw * in.st + (int64_t)v.b * in.sb + v.c0) * (int)sizeof(T)) & 15;
+            more[k] = (uint32_t)in.st * (int)sizeof(T);
           }
+          loose_rows<T, CPT>(src, STAGE / 3, off, more, same, raw);
         }
         if (small) gates<true>(raw, k2, lim, em1, nb);
         else gates<false>(raw, k2, lim, em1, nb);
@@ -314,6 +318,15 @@ __global__ void __launch_bounds__(NT, PER_SM)
         }
       } else {
         T *y = static_cast<T *>(p.y.p) + (int64_t)tw * p.y.st + (int64_t)v.b * p.y.sb + ch;
+        if (words && on && tw + S <= len && live == CPT) {
+#pragma unroll
+          for (int s = 0; s < S; ++s) {
+            h = step(em1[s], h, nb[s]);
+            store_word(y, neg_v(h));
+            y += p.y.st;
+          }
+          continue;
+        }
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           if (on && tw < len) h = step(em1[s], h, nb[s]);

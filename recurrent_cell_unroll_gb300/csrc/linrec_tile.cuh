@@ -185,25 +185,46 @@ __device__ __forceinline__ void copy_rows(uint8_t *dst, const void *src, int64_t
   }
 }
 
-// A lane's CPT values of S rows of such a copy, whose source rows start at `src`.
-template <typename IT, int CPT, int S>
-__device__ __forceinline__ void loose_rows(const uint8_t *tile, const void *src, int64_t pitch,
-                                           uint32_t (&raw)[S]) {
+__device__ __forceinline__ bool alike(const void *a, const void *b) {
+  return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15) == 0;
+}
+
+// A lane's CPT values of S rows of K such copies (`apart` bytes from one to the next), whose
+// rows start at off[k] of their words and move on by more[k].  Copies that agree in
+// both, as tensors of one layout do, share the arithmetic: `same`.
+template <typename IT, int CPT, int K, int S>
+__device__ __forceinline__ void loose_rows(const uint8_t *tile, int apart, const uint32_t (&off)[K],
+                                           const uint32_t (&more)[K], bool same,
+                                           uint32_t (&raw)[K][S]) {
   typedef Loose<IT, CPT> L;
   constexpr int N = CPT * (int)sizeof(IT);
   const uint32_t base = tc::smem_u32(tile) + threadIdx.x % 32 * N;
-  uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(src) & 15);
-  const uint32_t more = (uint32_t)pitch;
-#pragma unroll
-  for (int s = 0; s < S; ++s, off = (off + more) & 15) {
-    const uint32_t at = base + s * L::PITCH + off;
+  auto get = [&](int k, int s, uint32_t word, uint32_t shift) {
+    const uint32_t at = word + (s * L::PITCH + k * apart);
     uint32_t w0, w1;
     if (sizeof(IT) == 4) {
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw[s]) : "r"(at) : "memory");
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw[k][s]) : "r"(at) : "memory");
     } else {  // the two words that hold them, shifted together
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at & ~3u) : "memory");
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"((at & ~3u) + 4) : "memory");
-      raw[s] = __funnelshift_r(w0, w1, (at & 3) * 8) & (N == 4 ? ~0u : (1u << (8 * (N & 3))) - 1);
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at) : "memory");
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"(at + 4) : "memory");
+      raw[k][s] = __funnelshift_r(w0, w1, shift) & (N == 4 ? ~0u : (1u << (8 * (N & 3))) - 1);
+    }
+  };
+  auto row = [&](int k, int s, uint32_t o, int n) {
+    const uint32_t word = (base + o) & ~3u, shift = (base + o) * 8;
+#pragma unroll
+    for (int m = 0; m < n; ++m) get(k + m, s, word, shift);
+  };
+  if (same) {
+    uint32_t o = off[0];
+#pragma unroll
+    for (int s = 0; s < S; ++s, o = (o + more[0]) & 15) row(0, s, o, K);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      uint32_t o = off[k];
+#pragma unroll
+      for (int s = 0; s < S; ++s, o = (o + more[k]) & 15) row(k, s, o, 1);
     }
   }
 }

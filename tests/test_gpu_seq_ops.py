@@ -248,7 +248,8 @@ def test_linrec_lengths(ops, path, dtype, batch_first):
 @pytest.mark.parametrize("T,B,H,batch_first,act,lengths", [
     (1, 320, 33, False, False, False), (4, 170, 130, False, False, True),
     (5, 330, 64, True, True, True), (19, 160, 131, False, True, False), (20, 110, 192, True, False, True),
-    (21, 110, 192, False, False, False)])
+    (21, 110, 192, False, False, False), (13, 170, 131, False, False, True), (48, 320, 33, False, True, True),
+    (49, 310, 33, True, False, False)])
 def test_linrec_short_sequences_of_many_rows(ops, path, dtype, T, B, H, batch_first, act, lengths):
     ln = [(7 * b) % (T + 1) for b in range(B)] if lengths else None
     check_rec(ops, T, B, H, dtype, batch_first, ln, act=act)
