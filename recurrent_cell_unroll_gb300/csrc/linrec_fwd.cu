@@ -12,8 +12,8 @@
 // move: bound by memory (77 % of DRAM's peak), with the FMA pipe half busy.
 // T=65536 B=1 H=2048 242 us, 4.5 TB/s: 32 clusters of 12 blocks fill 384 of the
 // 456 places, and each round of tiles waits for its cluster's slowest block.
-// fp32 T=512 B=128 H=1024 162 us, 6.7 TB/s.  T=80 B=1 H=256 is the call's own
-// cost, 19 us, of which the kernel is 6.
+// fp32 T=512 B=128 H=1024 161 us, 6.7 TB/s.  T=80 B=1 H=256 is the call's own
+// cost, 18 us, of which the kernel is 6.
 #include "linrec_tile.cuh"
 
 namespace rcu {
