@@ -95,6 +95,9 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
   const int stride = M == SHARES ? 1 : gridDim.x / cs, u0 = M == SHARES ? 0 : blockIdx.x / cs;
   const int units = count_units<M>(cut, p.B);
 
+  // the inputs' rows lie alike
+  const bool same = !TMA && p.x.st == p.r.st && p.x.st == p.i.st && p.x.sb == p.r.sb &&
+                    p.x.sb == p.i.sb && alike(p.x.p, p.r.p) && alike(p.x.p, p.i.p);
   // Copies of the live tiles of this block, the last steps first: by TMA (thread
   // 0, the whole tile) or by each warp its own rows.
   // With TMA it is one thread that copies: what it keeps for that is in shared memory,
@@ -139,17 +142,27 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
       }
       tma_load_3d(dst + 3 * IN, &mdy, bar, v.c0, v.b, tile * STEPS);
     } else {
-      const int64_t tw = tile * STEPS + warp * S, b = v.b;
-      const int width = min(CW, p.H - v.c0), rows = (int)min(next.len - tw, (int64_t)S);
+      const int tw = tile * STEPS + warp * S, rows = min(next.len - tw, S);
+      const int width = min(CW, p.H - v.c0);
+      auto pos = [&](const SeqIn &in, int size) {
+        return ((int64_t)tw * in.st + (int64_t)v.b * in.sb + v.c0) * size;
+      };
+      uint8_t *to = dst + warp * S * IN_ROW;
+      if (!MAP && same) {
+        const void *const base[3] = {p.x.p, p.r.p, p.i.p};
+        copy_rows<IT, CPT>(to, IN, base, pos(p.x, sizeof(IT)), p.x.st * (int64_t)sizeof(IT), rows,
+                           width * (int)sizeof(IT));
+      } else {
 #pragma unroll 1
-      for (int k = MAP ? 1 : 0; k < (MAP ? 2 : 3); ++k) {
-        const SeqIn &in = (&p.x)[k];
-        copy_rows<IT, CPT>(dst + k * IN + warp * S * IN_ROW,
-                           static_cast<const IT *>(in.p) + tw * in.st + b * in.sb + v.c0,
-                           in.st * (int64_t)sizeof(IT), rows, width * (int)sizeof(IT));
+        for (int k = MAP ? 1 : 0; k < (MAP ? 2 : 3); ++k) {
+          const SeqIn &in = (&p.x)[k];
+          const void *const base[1] = {in.p};
+          copy_rows<IT, CPT>(to + k * IN, 0, base, pos(in, sizeof(IT)),
+                             in.st * (int64_t)sizeof(IT), rows, width * (int)sizeof(IT));
+        }
       }
-      copy_rows<T, CPT>(dst + 3 * IN + warp * S * DY_ROW,
-                        static_cast<const T *>(p.dy.p) + tw * p.dy.st + b * p.dy.sb + v.c0,
+      const void *const base[1] = {p.dy.p};
+      copy_rows<T, CPT>(dst + 3 * IN + warp * S * DY_ROW, 0, base, pos(p.dy, sizeof(T)),
                         p.dy.st * (int64_t)sizeof(T), rows, width * (int)sizeof(T));
     }
     if (!TMA) copy_commit();
@@ -167,9 +180,6 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
-  // the inputs' rows lie alike
-  const bool same = !TMA && p.x.st == p.r.st && p.x.st == p.i.st && p.x.sb == p.r.sb &&
-                    p.x.sb == p.i.sb && alike(p.x.p, p.r.p) && alike(p.x.p, p.i.p);
   set(sh.sum[warp][lane], 0.f);
   int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
   bool small = false;

@@ -5,8 +5,7 @@
 // gates stay in registers between the reduction to affine maps and the second
 // run over the steps.  A long sequence of few channels is split over the blocks
 // of a cluster, which exchange their tiles' maps through distributed shared
-// memory: no second read, no flags in global memory, and the order of every
-// sum is fixed.
+// memory: no second read, and the order of every sum is fixed.
 //
 // Measured, bf16: T=512 B=256 H=1024 174 us, 6.2 TB/s of the 1084 MB it must
 // move: bound by memory (77 % of DRAM's peak), with the FMA pipe half busy.
@@ -107,6 +106,9 @@ __global__ void __launch_bounds__(NT, PER_SM)
   const int stride = M == SHARES ? 1 : gridDim.x / cs, u0 = M == SHARES ? 0 : blockIdx.x / cs;
   const int units = count_units<M>(cut, p.B);
 
+  // the inputs' rows lie alike
+  const bool same = !TMA && p.x.st == p.r.st && p.x.st == p.i.st && p.x.sb == p.r.sb &&
+                    p.x.sb == p.i.sb && alike(p.x.p, p.r.p) && alike(p.x.p, p.i.p);
   // Copies of the live tiles of this block, in the order they are used: by TMA
   // (thread 0, the whole tile) or by each warp its own rows.
   Next next;
@@ -135,15 +137,23 @@ __global__ void __launch_bounds__(NT, PER_SM)
       tma_load_3d(dst + STAGE / 3, &mr, bar, v.c0, v.b, tile * STEPS);
       tma_load_3d(dst + 2 * STAGE / 3, &mi, bar, v.c0, v.b, tile * STEPS);
     } else {
-      const int64_t tw = tile * STEPS + warp * S;
+      const int tw = tile * STEPS + warp * S, rows = min(next.len - tw, S);
       const int bytes = min(CW, p.H - v.c0) * (int)sizeof(T);
+      uint8_t *to = dst + warp * (STAGE / 3 / NW);
+      auto pos = [&](const SeqIn &in) {
+        return ((int64_t)tw * in.st + (int64_t)v.b * in.sb + v.c0) * (int)sizeof(T);
+      };
+      if (same) {
+        const void *const base[3] = {p.x.p, p.r.p, p.i.p};
+        copy_rows<T, CPT>(to, STAGE / 3, base, pos(p.x), p.x.st * (int64_t)sizeof(T), rows, bytes);
+      } else {
 #pragma unroll 1
-      for (int k = 0; k < 3; ++k) {
-        const SeqIn &in = (&p.x)[k];
-        copy_rows<T, CPT>(
-            dst + k * (STAGE / 3) + warp * (STAGE / 3 / NW),
-            static_cast<const T *>(in.p) + tw * in.st + (int64_t)v.b * in.sb + v.c0,
-            in.st * (int64_t)sizeof(T), (int)min(next.len - tw, (int64_t)S), bytes);
+        for (int k = 0; k < 3; ++k) {
+          const SeqIn &in = (&p.x)[k];
+          const void *const base[1] = {in.p};
+          copy_rows<T, CPT>(to + k * (STAGE / 3), 0, base, pos(in), in.st * (int64_t)sizeof(T), rows,
+                            bytes);
+        }
       }
     }
     if (!TMA) copy_commit();
@@ -161,9 +171,6 @@ __global__ void __launch_bounds__(NT, PER_SM)
   __syncthreads();
   if (cs > 1) tc::cluster_sync();  // every block of the cluster runs before its memory is written
 
-  // the inputs' rows lie alike
-  const bool same = !TMA && p.x.st == p.r.st && p.x.st == p.i.st && p.x.sb == p.r.sb &&
-                    p.x.sb == p.i.sb && alike(p.x.p, p.r.p) && alike(p.x.p, p.i.p);
   int used = 0, parity = 0, round = 0, held = -1;  // held: the channels k2 and so on are of
   V k2;
   Limits lim;

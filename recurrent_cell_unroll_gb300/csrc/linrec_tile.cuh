@@ -164,24 +164,31 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// `rows` rows from `src` (`pitch` bytes apart), `bytes` of each.  The loops stay
-// loops: unrolled, the kernel outgrew the instruction cache.
-template <typename IT, int CPT>
-__device__ __forceinline__ void copy_rows(uint8_t *dst, const void *src, int64_t pitch, int rows,
-                                          int bytes) {
+// `rows` rows of K tensors that lie alike, from `pos` bytes behind each `base` and
+// `pitch` bytes apart, `bytes` of each; to `dst`, a tensor `apart` from the one before.
+// The loop stays a loop: unrolled, the kernel outgrew the instruction cache.
+template <typename IT, int CPT, int K>
+__device__ __forceinline__ void copy_rows(uint8_t *dst, int apart, const void *const (&base)[K],
+                                          int64_t pos, int64_t pitch, int rows, int bytes) {
   typedef Loose<IT, CPT> L;
   constexpr int WORDS = L::PITCH / 16, TOGETHER = 32 / WORDS;  // of a row; rows at once
   const int lane = threadIdx.x % 32, at = lane % WORDS * 16;
   const int first = lane / WORDS < TOGETHER ? lane / WORDS : rows;
-  const uint8_t *p = static_cast<const uint8_t *>(src) + first * pitch;
+  const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(base[0]);
   uint32_t to = tc::smem_u32(dst) + first * L::PITCH + at;
+  pos += first * pitch;
 #pragma unroll 1
-  for (int s = first; s < rows; s += TOGETHER, p += TOGETHER * pitch, to += TOGETHER * L::PITCH) {
-    const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15), left = off + bytes - at;
-    if (left > 0)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(p - off + at),
-                   "r"(min(left, 16))
-                   : "memory");
+  for (int s = first; s < rows; s += TOGETHER, pos += TOGETHER * pitch, to += TOGETHER * L::PITCH) {
+    const int off = (int)((low + (uint32_t)pos) & 15), left = off + bytes - at;
+    if (left > 0) {
+      const int64_t from = pos + (at - off);
+      const int size = min(left, 16);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + k * apart),
+                     "l"(static_cast<const uint8_t *>(base[k]) + from), "r"(size)
+                     : "memory");
+    }
   }
 }
 

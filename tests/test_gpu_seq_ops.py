@@ -280,6 +280,26 @@ def test_linrec_slices_of_wider_tensors(ops, path, dtype):
     check_rec(ops, 70, 2, 40, dtype, wide=True, batch_first=True)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,H", [(130, 3, 77), (65, 400, 75)])
+def test_linrec_inputs_that_lie_differently(ops, path, dtype, T, B, H):
+    """Rows at other offsets and strides than their neighbours': the same bits."""
+    x, r, i, lam, h0 = (t.cuda() for t in rec_inputs(T, B, H, dtype, 9))
+
+    def moved(t, width, at):
+        big = torch.zeros(*t.shape[:2], width, dtype=t.dtype, device="cuda")
+        big[..., at:at + H] = t
+        return big[..., at:at + H]
+
+    def passes(x, r, i, dy):
+        y, h_n, st = ops.linrec_forward(x, r, i, lam, h0=h0, states=True)
+        return (y, h_n, *ops.linrec_backward(dy, x, r, i, lam, st, dh_n=h_n))
+    want = passes(x, r, i, x)
+    got = passes(x, moved(r, H + 4, 3), moved(i, 2 * H, 1), moved(x, H + 1, 1))
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+
+
 def test_linrec_without_h0(ops, path):
     check_rec(ops, 90, 2, 64, "f32", use_h0=False)
 
