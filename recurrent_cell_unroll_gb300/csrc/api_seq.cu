@@ -220,7 +220,7 @@ extern "C" int rcu_linrec_forward(rcu_seq *h, int dtype, int layout, int T, int 
                     seq_in(layout, T, B, i, ldi), lambda, (float)c, lengths, h0,
                     seq_out(layout, T, B, y, ldy), h_n, states};
   begin(h, "linrec_forward", s);
-  CU(launch_linrec_fwd(p, *h, (int *)h->ctl.p, !h->force_path, s, &h->launches));
+  CU(launch_linrec_fwd(p, *h, (int *)h->ctl.p, h->nsm, !h->force_path, s, &h->launches));
   h->prof_end(s);
   return RCU_OK;
 }

@@ -24,8 +24,8 @@ using namespace linrec;
 // Eight warps of 8 steps: the tile is what one kept state covers, and 16 steps a
 // lane would need more than the 255 registers a thread can have.  Two blocks an SM
 // (128 registers); bf16 rows that TMA cannot address take more, and beside a cluster's
-// exchange one block is faster there (T=15731 B=1 H=2133: 282 us, 308 with two; with
-// shares two are: T=521 B=86 H=748 199 us, 305 with one).
+// exchange one block is faster there (T=15731 B=1 H=2133: 258 us, 280 with two; with
+// shares two are: T=521 B=86 H=748 178 us, 280 with one).
 constexpr int NW = 8, NT = 32 * NW, S = CHUNK / NW, STEPS = CHUNK, STAGES = 2, PER_SM = 2;
 constexpr int MAXCS = 8;  // blocks of a cluster
 constexpr int BATCH = 4;  // pairs whose gates are computed together

@@ -11,8 +11,9 @@
 //
 // How far it pays goes by the rows: those that TMA cannot address cost the tiled kernel
 // more, and this one only where a lane's values are not a word.  B=188, here and tiled:
-// fp32 H=1921 T=48 217 and 234 us; bf16 H=1922 T=18 91 and 127, T=26 132 and 129;
-// H=1921 T=12 113 and 127, T=18 187 and 126.
+// bf16 H=1920 T=20 70 and 73 us, H=1922 T=20 94 and 118, H=1921 T=11 107 and 115,
+// T=13 129 and 114; from 8 bits H=1920 T=14 82 and 95, T=18 109 and 91; fp32 H=1920
+// T=17 102 and 102, H=1921 T=44 199 and 207.
 #include "linrec_bwd.cuh"
 
 namespace rcu {
@@ -21,29 +22,8 @@ namespace {
 using namespace linrec;
 
 constexpr int NW = 4, NT = 32 * NW, N = 4;  // N: steps whose reads are in flight together
-constexpr int SHORT_T = 20, SHORT_LOOSE = 48, SHORT_SPLIT = 13;  // most steps: TMA's rows; fp32
-                                                                 // rows off it; split words
-
-// A lane's values of a step from global memory (`word`: as one access)
-template <typename IT, int CPT>
-__device__ __forceinline__ uint32_t global_raw(const IT *p, int live, bool word) {
-  constexpr int B = CPT * (int)sizeof(IT);
-  if (B == 4 && word && live == CPT) return __ldg(reinterpret_cast<const uint32_t *>(p));
-  if (B == 2 && word && live == CPT) return __ldg(reinterpret_cast<const unsigned short *>(p));
-  uint32_t v = 0;
-  if (sizeof(IT) == 4) {
-    if (live > 0) v = __ldg(reinterpret_cast<const uint32_t *>(p));
-  } else if (sizeof(IT) == 2) {
-    const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
-    if (live > 0) v = __ldg(q);
-    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 16;
-  } else {
-    const unsigned char *q = reinterpret_cast<const unsigned char *>(p);
-    if (live > 0) v = __ldg(q);
-    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 8;
-  }
-  return v;
-}
+// the most steps: at all; of pairs from 8 bits; of fp32 rows off TMA; of split words
+constexpr int SHORT_T = 20, SHORT_Q8 = 16, SHORT_LOOSE = 44, SHORT_SPLIT = 12;
 
 template <typename IT, typename T>
 __global__ void __launch_bounds__(NT, 3)
@@ -213,9 +193,9 @@ bool linrec::short_bwd_pays(const LinrecBwd &p, int resident_blocks, bool vec) {
     }
     return true;
   };
-  if (vec && aligned(16, 16)) return p.T <= SHORT_T;
-  if (!half) return true;
-  return p.T <= (aligned(4, 2) ? SHORT_T : SHORT_SPLIT);
+  if (!half) return p.T <= (vec && aligned(16, 16) ? SHORT_T : SHORT_LOOSE);
+  if (!aligned(4, 2)) return p.T <= SHORT_SPLIT;
+  return p.T <= (p.saved == RCU_I8 ? SHORT_Q8 : SHORT_T);
 }
 
 cudaError_t linrec::launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm,

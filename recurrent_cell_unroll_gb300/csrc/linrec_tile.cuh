@@ -236,6 +236,29 @@ __device__ __forceinline__ void loose_rows(const uint8_t *tile, int apart, const
   }
 }
 
+// ---- one lane's values of a step, without a tile
+
+// A lane's values of a step from global memory (`word`: as one access)
+template <typename IT, int CPT>
+__device__ __forceinline__ uint32_t global_raw(const IT *p, int live, bool word) {
+  constexpr int B = CPT * (int)sizeof(IT);
+  if (B == 4 && word && live == CPT) return __ldg(reinterpret_cast<const uint32_t *>(p));
+  if (B == 2 && word && live == CPT) return __ldg(reinterpret_cast<const unsigned short *>(p));
+  uint32_t v = 0;
+  if (sizeof(IT) == 4) {
+    if (live > 0) v = __ldg(reinterpret_cast<const uint32_t *>(p));
+  } else if (sizeof(IT) == 2) {
+    const unsigned short *q = reinterpret_cast<const unsigned short *>(p);
+    if (live > 0) v = __ldg(q);
+    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 16;
+  } else {
+    const unsigned char *q = reinterpret_cast<const unsigned char *>(p);
+    if (live > 0) v = __ldg(q);
+    if (CPT > 1 && live > 1) v |= (uint32_t)__ldg(q + 1) << 8;
+  }
+  return v;
+}
+
 // ---- one lane's values of a step, as they go out
 
 __device__ __forceinline__ void store_raw(float *p, float v, int live, bool) {
@@ -578,6 +601,11 @@ cudaError_t launch_cut(void (*fn)(KArgs...), const Plan &pl, int threads, size_t
   cfg.numAttrs = pl.cs > 1 || waits ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
+
+// The forward kernel for short sequences of many rows (linrec_fwd_short.cu), and whether
+// it is the faster one; resident_blocks: of the tiled kernel, vec: as of launch_linrec_fwd.
+bool short_fwd_pays(const LinrecFwd &p, int resident_blocks, bool vec);
+cudaError_t launch_short_fwd(const LinrecFwd &p, int *err, int nsm, cudaStream_t s, int *launches);
 
 }  // namespace linrec
 }  // namespace rcu

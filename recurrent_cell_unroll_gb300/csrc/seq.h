@@ -82,8 +82,8 @@ __device__ __forceinline__ void wait_for_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-cudaError_t launch_linrec_fwd(const LinrecFwd &p, DevMem &ws, int *err, bool vec, cudaStream_t s,
-                              int *launches);
+cudaError_t launch_linrec_fwd(const LinrecFwd &p, DevMem &ws, int *err, int nsm, bool vec,
+                              cudaStream_t s, int *launches);
 cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm, bool vec,
                               cudaStream_t s, int *launches);
 cudaError_t launch_linrec_step(int dtype, int B, int H, const void *x, int64_t ldx, const void *r,

@@ -281,6 +281,19 @@ def test_linrec_slices_of_wider_tensors(ops, path, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,H,batch_first,lengths", [
+    (1, 500, 33, False, False), (3, 240, 130, True, True), (8, 470, 64, False, True),
+    (9, 240, 67, True, False), (31, 160, 200, False, True), (32, 480, 30, True, True),
+    (33, 480, 30, False, False), (64, 460, 31, True, True), (20, 240, 67, False, False),
+    (21, 240, 67, False, True), (32, 500, 64, False, False)])
+def test_linrec_forward_of_short_sequences(ops, path, dtype, T, B, H, batch_first, lengths):
+    ln = [(5 * b) % (T + 1) for b in range(B)] if lengths else None
+    check_rec(ops, T, B, H, dtype, batch_first, ln)
+    if T == 9:
+        check_rec(ops, T, B, H, dtype, use_h0=False, wide=True)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("T,B,H", [(130, 3, 77), (65, 400, 75)])
 def test_linrec_inputs_that_lie_differently(ops, path, dtype, T, B, H):
     """Rows at other offsets and strides than their neighbours': the same bits."""
