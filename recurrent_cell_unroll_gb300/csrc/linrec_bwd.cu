@@ -102,8 +102,9 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
   // 0, the whole tile) or by each warp its own rows.
   // With TMA it is one thread that copies: what it keeps for that is in shared memory,
   // as its registers would be every thread's (bf16 T=512 B=256 H=1024: 345 us, 353 with
-  // registers).  Clusters, with more to do between two tiles, lose by it (238, 249).
-  constexpr bool ONE = TMA && M != UNITS;
+  // registers).  Clusters, with more to do between two tiles, lose by it (238, 249) but
+  // for pairs from 8 bits (T=8192 B=4 H=2048 291, 298).
+  constexpr bool ONE = TMA && (M != UNITS || (Q8 && CPT == 2));
   Next own;
   Next &next = ONE ? sh.next : own;
   if (!ONE || threadIdx.x == 0) {
@@ -212,10 +213,10 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
     sum = zero;
     // 8 bits: lane 8 k + s has the exponent of tensor k at the warp's step s, read a
     // tile ahead
-    int ex = 0;
+    int ex = FREE_EXP;
     auto read_exponent = [&](int tile) {
       const int t = tile * STEPS + warp * S + lane % S, k = lane / S;
-      ex = 0;
+      ex = FREE_EXP;
       if (k < 3 && tile >= v.first && t < len)
         ex = (int)__ldg((k == 0 ? p.x.e : k == 1 ? p.r.e : p.i.e) +
                         ((int64_t)t * p.et + v.b * p.eb) * ceil_div(p.H, BLOCK8) + v.c0 / BLOCK8);
@@ -230,7 +231,9 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
         if (!MAP && !(TMA && bulk_states))
           load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
         float scale[3][S];
+        bool bounded = true;  // the gates' logits, by their blocks' exponents
         if (Q8) {
+          bounded = !__any_sync(0xffffffffu, lane >= S && ex > FREE_EXP);
           const float f = power2(ex) * (lane < S ? 1.f : -LOG2E);
           read_exponent(tile - cs);
 #pragma unroll
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
         if (tw >= len) {  // a warp past the row's end has the identity
 #pragma unroll
           for (int s = 0; s < S; ++s) em1[s] = nb[s] = ns[s] = ng[s] = 0;
-        } else if (small) {
+        } else if (small && bounded) {
           gates<IT, true, BATCH>(raw, scale, k2, lim, em1, nb, ns, ng);
         } else {
           gates<IT, false, BATCH>(raw, scale, k2, lim, em1, nb, ns, ng);

@@ -49,7 +49,9 @@ __global__ void __launch_bounds__(NT, 3)
 
   uint32_t raw[3][N], rawd[N];
   float scale[3][N];
+  int top = FREE_EXP;  // the largest of the gates' exponents
   auto load = [&](int64_t b, int t0, int len, bool with_dy) {
+    top = FREE_EXP;
 #pragma unroll
     for (int s = 0; s < N; ++s) {
       const int64_t t = t0 + s;
@@ -59,9 +61,11 @@ __global__ void __launch_bounds__(NT, 3)
         const SeqIn &in = (&p.x)[k];
         raw[k][s] = global_raw<IT, CPT>(static_cast<const IT *>(in.p) + t * in.st + b * in.sb + ch,
                                         on, words >> k & 1);
-        if (Q8)
-          scale[k][s] = power2(on ? __ldg(in.e + (t * p.et + b * p.eb) * nb8 + c0 / BLOCK8) : 0) *
-                        (k ? -LOG2E : 1.f);
+        if (Q8) {
+          const int e = on ? (int)__ldg(in.e + (t * p.et + b * p.eb) * nb8 + c0 / BLOCK8) : FREE_EXP;
+          if (k) top = max(top, e);
+          scale[k][s] = power2(e) * (k ? -LOG2E : 1.f);
+        }
       }
       if (with_dy)
         rawd[s] = global_raw<T, CPT>(static_cast<const T *>(p.dy.p) + t * p.dy.st + b * p.dy.sb + ch,
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(NT, 3)
   };
   V em1[N], nb[N], ns[N], ng[N];
   auto make_gates = [&](int t0, int len) {
-    if (small) gates<IT, true, 2>(raw, scale, k2, lim, em1, nb, ns, ng);
+    if (small && top <= FREE_EXP) gates<IT, true, 2>(raw, scale, k2, lim, em1, nb, ns, ng);
     else gates<IT, false, 2>(raw, scale, k2, lim, em1, nb, ns, ng);
     if (Q8) spoil_codes<CPT>(raw, em1, nb, ns, ng);
     if (t0 + N > len) {

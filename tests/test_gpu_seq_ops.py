@@ -440,6 +440,16 @@ def test_linrec_extreme_gates(ops, path):
         assert bool(torch.isfinite(t).all())
 
 
+@pytest.mark.parametrize("dtype,T,B,H", [("f32", 96, 2, 128), ("bf16", 96, 2, 128), ("bf16", 14, 300, 131),
+                                         ("f32", 14, 310, 33), ("bf16", 9000, 1, 64)])
+def test_linrec_wide_gates_from_8_bits(ops, path, dtype, T, B, H):
+    """Steps whose blocks hold logits beyond the gates' limits between steps without."""
+    x, r, i, lam, h0 = rec_inputs(T, B, H, dtype, 10)
+    r[::3] *= 60
+    i[1::4] *= 60
+    check_rec(ops, T, B, H, dtype, inputs=(x, r, i, lam, h0), act=True)
+
+
 def test_linrec_nan_stays_in_its_row_and_channel(ops, path):
     T, B, H = 150, 2, 64
     x, r, i, lam, h0 = (t.cuda() for t in rec_inputs(T, B, H, "f32", 5))
