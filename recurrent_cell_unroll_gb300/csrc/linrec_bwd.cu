@@ -12,8 +12,8 @@
 // which is what 16 warps an SM reach at 128 registers a thread: DRAM is half busy.
 // Measured: bf16 T=512 B=256 H=1024 344 us, T=8192 B=4 H=2048 236 us (944 MB,
 // 4.0 TB/s); fp32 T=500 B=64 H=512 with mixed lengths 71 us (348 MB, 4.9 TB/s).
-// From 8 bits it issues 79 an element, the codes' scaling among them: T=1000 B=32
-// H=1024 115 us for 364 MB.
+// From 8 bits it issues nearly 80, the codes' scaling among them: T=1000 B=32
+// H=1024 114 us for 364 MB.
 #include "linrec_bwd.cuh"
 
 namespace rcu {
