@@ -87,6 +87,7 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][N], const float (
                                       const Limits &lim, F2 (&em1)[N], F2 (&nb)[N], F2 (&ns)[N],
                                       F2 (&ng)[N]) {
   typedef Decode<IT, F2> D;
+  static_assert(N % BATCH == 0, "the steps are whole batches");
 #pragma unroll
   for (int s = 0; s < N; s += BATCH) {
     F2 x[BATCH], r[BATCH], i[BATCH];
@@ -106,6 +107,7 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][N], const float (
                                       float k2, const Limits &lim, float (&em1)[N], float (&nb)[N],
                                       float (&ns)[N], float (&ng)[N]) {
   typedef Decode<IT, float> D;
+  static_assert(N % (2 * BATCH) == 0, "the steps are whole batches");
 #pragma unroll
   for (int s = 0; s < N; s += 2 * BATCH) {
     F2 x[BATCH], r[BATCH], i[BATCH], m[BATCH], b[BATCH], vs[BATCH], vg[BATCH];

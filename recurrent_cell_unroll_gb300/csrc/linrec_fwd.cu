@@ -26,6 +26,7 @@ using namespace linrec;
 constexpr int NW = 4, NT = 32 * NW, S = 16, STEPS = NW * S, STAGES = 2, PER_SM = 3;
 constexpr int MAXCS = 12;  // blocks of a cluster: with more, their maps leave room for two on an SM
 constexpr int BATCH = 4;   // pairs whose gates are computed together
+static_assert(S % (2 * BATCH) == 0, "the steps are whole batches, of pairs of steps too");
 constexpr int TILE_BYTES = STEPS * 128;
 static_assert(STEPS == CHUNK, "a tile starts from one of the kept states");
 

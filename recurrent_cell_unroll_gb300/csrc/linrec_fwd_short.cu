@@ -28,6 +28,7 @@ template <typename T>
 __global__ void __launch_bounds__(NT, PER_SM)
     linrec_fwd_short_kernel(const LinrecFwd p, const int groups, const int words, int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
+  constexpr int BATCH = CPT == 2 ? N : N / 2;  // the N steps at once: pairs of channels, or of steps
   typedef typename Lane<T>::V V;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int w = blockIdx.x * NW + warp, c0 = w % groups * CW, stride = gridDim.x * NW / groups;
@@ -64,8 +65,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
     T *y = static_cast<T *>(p.y.p) + b * p.y.sb + ch;
     for (int t0 = 0; t0 < p.T; t0 += N) {
       V em1[N], nb[N], ns[N], ng[N];
-      if (small) gates<T, true, 4>(raw, scale, k2, lim, em1, nb, ns, ng);
-      else gates<T, false, 4>(raw, scale, k2, lim, em1, nb, ns, ng);
+      if (small) gates<T, true, BATCH>(raw, scale, k2, lim, em1, nb, ns, ng);
+      else gates<T, false, BATCH>(raw, scale, k2, lim, em1, nb, ns, ng);
       if (t0 + N < len) load(b, t0 + N, len);
 #pragma unroll
       for (int s = 0; s < N; ++s) {
