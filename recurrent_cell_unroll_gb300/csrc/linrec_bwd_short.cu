@@ -25,6 +25,16 @@ constexpr int NW = 4, NT = 32 * NW, N = 4;  // N: steps whose reads are in fligh
 // the most steps: at all; of pairs from 8 bits; of fp32 rows off TMA; of split words
 constexpr int SHORT_T = 20, SHORT_Q8 = 16, SHORT_LOOSE = 44, SHORT_SPLIT = 12;
 
+// Of a block's states.  Below what a launch may have without asking: what a kernel is
+// allowed beyond that is one setting for all the process's threads.
+template <typename T>
+constexpr size_t state_bytes(int steps) {
+  return (size_t)NW * steps * 32 * sizeof(typename Lane<T>::V);
+}
+static_assert(state_bytes<float>(std::max(SHORT_T, SHORT_LOOSE)) <= 48 << 10 &&
+                  state_bytes<bf16>(std::max({SHORT_T, SHORT_Q8, SHORT_SPLIT})) <= 48 << 10,
+              "a block's states fit the default limit");
+
 template <typename IT, typename T>
 __global__ void __launch_bounds__(NT, 3)
     linrec_bwd_short_kernel(const LinrecBwd p, const int groups, float *__restrict__ partial,
@@ -142,11 +152,8 @@ __global__ void __launch_bounds__(NT, 3)
 template <typename IT, typename T>
 cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s, int *launches) {
   const int groups = ceil_div(p.H, Shape<T>::CW);
-  const size_t smem = (size_t)NW * p.T * 32 * sizeof(typename Lane<T>::V);
+  const size_t smem = state_bytes<T>(p.T);
   auto fn = linrec_bwd_short_kernel<IT, T>;
-  cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
-  if (e != cudaSuccess) return e;
   // a whole number of warps a group: each warp stays with its channels
   const int64_t most = (int64_t)3 * nsm * NW;
   const int64_t each = std::max<int64_t>(1, std::min<int64_t>(p.B, most / groups));
@@ -168,12 +175,12 @@ cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t 
     words |= whole(out[k]->p, out[k]->st, out[k]->sb, sizeof(T)) << (4 + k);
   float *partial = nullptr;
   if (p.dlambda) {
-    e = ws.get((size_t)p.B * p.H * 4, &partial);
+    const cudaError_t e = ws.get((size_t)p.B * p.H * 4, &partial);
     if (e != cudaSuccess) return e;
   }
   fn<<<(unsigned)blocks, NT, smem, s>>>(p, groups, partial, words, err);
   ++*launches;
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.dlambda) return e;
   ++*launches;
   return launch_dlambda(partial, p.B, p, s);
