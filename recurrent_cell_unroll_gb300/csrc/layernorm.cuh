@@ -6,6 +6,7 @@
 #include "act8.cuh"
 #include "common.cuh"
 #include "linrec_math.cuh"
+#include "per_device.h"
 #include "rcu.h"
 #include "seq.h"
 

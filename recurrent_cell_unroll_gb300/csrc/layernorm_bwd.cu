@@ -226,11 +226,10 @@ template <typename IT, typename T, int VEC, int N, int W>
 cudaError_t run(const LnBwd &p, DevMem &ws, int nsm, cudaStream_t s, int *launches) {
   constexpr int R = W >= 4 ? 1 : 4 / W, NT = 32 * W * R;
   constexpr size_t SMEM = R > 1 ? (size_t)R * 2 * N * 32 * W * VEC * 4 : 0;
-  static const int blocks = [&] {
-    cudaFuncSetAttribute((const void *)ln_bwd_kernel<IT, T, VEC, N, W, R>,
-                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
-    return resident_blocks(ln_bwd_kernel<IT, T, VEC, N, W, R>, NT, SMEM, nsm);
-  }();
+  static_assert(SMEM <= 40 << 10, "within the default limit, with what the kernel has besides");
+  static PerDevice<int> room;
+  const int blocks = room.here(
+      [&] { return resident_blocks(ln_bwd_kernel<IT, T, VEC, N, W, R>, NT, SMEM, nsm); });
   const int grid = (int)std::min<int64_t>((p.rows + R - 1) / R, blocks);
   float *part = nullptr;
   const bool columns = p.dweight || p.dbias;

@@ -163,7 +163,9 @@ __global__ void __launch_bounds__(LONG_NT) ln_fwd_long_kernel(const LnFwd p) {
 template <typename T, int VEC, int N, int W, bool RES>
 void run(const LnFwd &p, int nsm, cudaStream_t s) {
   constexpr int R = W >= 4 ? 1 : 4 / W;
-  static const int blocks = resident_blocks(ln_fwd_kernel<T, VEC, N, W, R, RES>, 32 * W * R, 0, nsm);
+  static PerDevice<int> room;
+  const int blocks = room.here(
+      [&] { return resident_blocks(ln_fwd_kernel<T, VEC, N, W, R, RES>, 32 * W * R, 0, nsm); });
   const int grid = (int)std::min<int64_t>((p.rows + R - 1) / R, blocks);
   ln_fwd_kernel<T, VEC, N, W, R, RES><<<grid, 32 * W * R, 0, s>>>(p);
 }

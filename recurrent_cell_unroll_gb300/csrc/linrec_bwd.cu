@@ -499,11 +499,14 @@ cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStr
   constexpr size_t SMEM =
       sizeof(Smem<typename Lane<T>::V>) + STAGES * stage_bytes<IT, T, TMA>();
   typedef typename Lane<T>::V V;
-  static const Resident res = resident(linrec_bwd_kernel<IT, T, TMA, UNITS>, NT, MAXCS, SMEM, 0);
-  static const Resident res_map = resident(linrec_bwd_kernel<IT, T, TMA, MAPS>, NT, 1, SMEM, 0);
-  static const int blocks =
-      resident(linrec_bwd_kernel<IT, T, TMA, SHARES>, NT, 1, SMEM, 0).clusters[1];
-  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, blocks, 0.5);
+  static PerDevice<Room> rooms;
+  const Room room = rooms.here([] {
+    return Room{resident(linrec_bwd_kernel<IT, T, TMA, UNITS>, NT, MAXCS, SMEM, 0),
+                resident(linrec_bwd_kernel<IT, T, TMA, MAPS>, NT, 1, SMEM, 0),
+                resident(linrec_bwd_kernel<IT, T, TMA, SHARES>, NT, 1, SMEM, 0).clusters[1]};
+  });
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), room.units,
+                           room.shares, 0.5);
   const int64_t rows = pl.cut.share ? pl.grid / pl.cut.groups : (int64_t)p.B * pl.cut.nseg * pl.cs;
   // the workspace: the segments' maps or the shares' carries, then dlambda's partial sums
   const size_t flags = pl.cut.share % pl.cut.tiles ? carry_flags(pl.grid) : 0;
@@ -521,7 +524,7 @@ cudaError_t run(const LinrecBwd &p, const Maps &v, DevMem &ws, int *err, cudaStr
   if (pl.cut.nseg > 1) {
     Plan first = pl;
     first.cut.units = pl.cut.units / pl.cut.nseg * (pl.cut.nseg - 1);
-    first.grid = std::min(first.cut.units, res_map.clusters[1]);
+    first.grid = std::min(first.cut.units, room.maps.clusters[1]);
     e = launch_cut(linrec_bwd_kernel<IT, T, TMA, MAPS>, first, NT, SMEM, s, v.m[0], v.m[1], v.m[2],
                    v.m[3], p, first.cut, (void *)mem, partial, v.words, v.states, err);
     if (e != cudaSuccess) return e;

@@ -365,13 +365,15 @@ cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], DevMem &ws, int *
   constexpr size_t SMEM0 =
       sizeof(Smem<V>) + STAGES * stage_bytes<T, TMA>() + (TMA ? TILE_BYTES : 0);
   constexpr size_t SMEM_PER_CS = 2 * 32 * sizeof(Aff<V>);
-  static const Resident res =
-      resident(linrec_fwd_kernel<T, TMA, UNITS>, NT, MAXCS, SMEM0, SMEM_PER_CS);
-  static const Resident res_map =
-      resident(linrec_fwd_kernel<T, TMA, MAPS>, NT, 1, SMEM0, SMEM_PER_CS);
-  static const int blocks =
-      resident(linrec_fwd_kernel<T, TMA, SHARES>, NT, 1, SMEM0, SMEM_PER_CS).clusters[1];
-  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), res, blocks, 0.8);
+  static PerDevice<Room> rooms;
+  const Room room = rooms.here([] {
+    return Room{
+        resident(linrec_fwd_kernel<T, TMA, UNITS>, NT, MAXCS, SMEM0, SMEM_PER_CS),
+        resident(linrec_fwd_kernel<T, TMA, MAPS>, NT, 1, SMEM0, SMEM_PER_CS),
+        resident(linrec_fwd_kernel<T, TMA, SHARES>, NT, 1, SMEM0, SMEM_PER_CS).clusters[1]};
+  });
+  const Plan pl = plan_cut(ceil_div(p.T, STEPS), p.B, ceil_div(p.H, Shape<T>::CW), room.units,
+                           room.shares, 0.8);
   const size_t smem = SMEM0 + pl.cs * SMEM_PER_CS;
   const bool words = word_aligned(p.y.p, p.y.st, p.y.sb, sizeof(T));
   void *mem = nullptr;
@@ -383,7 +385,7 @@ cudaError_t run(const LinrecFwd &p, const CUtensorMap (&m)[4], DevMem &ws, int *
   } else if (pl.cut.nseg > 1) {
     Plan first = pl;
     first.cut.units = pl.cut.units / pl.cut.nseg * (pl.cut.nseg - 1);
-    first.grid = std::min(first.cut.units, res_map.clusters[1]);
+    first.grid = std::min(first.cut.units, room.maps.clusters[1]);
     e = ws.get((size_t)first.cut.units * 32 * sizeof(Aff<V>), &mem);
     if (e == cudaSuccess)
       e = launch_cut(linrec_fwd_kernel<T, TMA, MAPS>, first, NT, smem, s, m[0], m[1], m[2], m[3], p,

@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "linrec_math.cuh"
+#include "per_device.h"
 #include "rcu.h"
 #include "seq.h"
 #include "tc.h"
@@ -483,7 +484,8 @@ struct Plan {
   int cs, grid;
 };
 
-// How many clusters of each size a kernel can have resident (size 1: blocks).
+// How many clusters of each size a kernel can have resident (size 1: blocks), on the
+// current device; resident() sets the kernel's limits there too.
 struct Resident {
   static constexpr int MAX = 16;
   int clusters[MAX + 1] = {};
@@ -517,6 +519,12 @@ Resident resident(void (*fn)(KArgs...), int threads, int max_cs, size_t smem0, s
   cudaGetLastError();  // a size the GPU has no room for is no error of the call
   return r;
 }
+
+// Of a pass's kernels: over whole units, the first launch of segments, with shares.
+struct Room {
+  Resident units, maps;
+  int shares;
+};
 
 // How the recurrence over `tiles` tiles of B rows x `groups` channel groups is
 // cut: the cluster size that needs the fewest turns, a turn being one tile a
