@@ -21,6 +21,7 @@ import argparse
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding
 
@@ -38,6 +39,7 @@ class _Norm(torch.autograd.Function):
         return y, u
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dsum):
         *u, mean, rstd, weight = ctx.saved_tensors
         du, dw, db = ctx.ops.layernorm_backward(dy, tuple(u) if ctx.act8 else u[0], mean, rstd,
@@ -58,6 +60,7 @@ class _Recurrence(torch.autograd.Function):
         return y, h_n
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh_n):
         lam, states, *kept = ctx.saved_tensors
         parts = [tuple(kept[k:k + 2]) for k in (0, 2, 4)] if ctx.act8 else kept[0].chunk(3, -1)
