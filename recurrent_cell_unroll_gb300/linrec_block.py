@@ -54,18 +54,18 @@ class _Recurrence(torch.autograd.Function):
     def forward(ctx, ops, act8, z, lam, h0, lengths):
         parts = z.chunk(3, -1)
         y, h_n, states = ops.linrec_forward(*parts, lam, c=C, lengths=lengths, h0=h0, states=True)
-        ctx.ops, ctx.act8, ctx.lengths = ops, act8, lengths
+        ctx.ops, ctx.act8 = ops, act8
         kept = [t for p in parts for t in ops.act8_pack(p)] if act8 else [z]
-        ctx.save_for_backward(lam, states, *kept)
+        ctx.save_for_backward(lam, states, lengths, *kept)
         return y, h_n
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh_n):
-        lam, states, *kept = ctx.saved_tensors
+        lam, states, lengths, *kept = ctx.saved_tensors
         parts = [tuple(kept[k:k + 2]) for k in (0, 2, 4)] if ctx.act8 else kept[0].chunk(3, -1)
         dz = torch.empty((*dy.shape[:2], 3 * dy.shape[2]), dtype=dy.dtype, device=dy.device)
-        *_, dlam, dh0 = ctx.ops.linrec_backward(dy, *parts, lam, states, c=C, lengths=ctx.lengths,
+        *_, dlam, dh0 = ctx.ops.linrec_backward(dy, *parts, lam, states, c=C, lengths=lengths,
                                                 dh_n=dh_n, out=dz)
         return None, None, dz, dlam, dh0, None
 

@@ -66,3 +66,15 @@ def test_second_derivatives_are_refused():
         first, = torch.autograd.grad((out * out).sum(), wrt, create_graph=True)
         with pytest.raises(RuntimeError, match="once_differentiable"):
             (first.square().sum() + wrt.pow(3).sum()).backward()
+
+
+def test_lengths_changed_before_the_backward_are_noticed():
+    """A buffer of lengths that the next batch has been written to: autograd's error for
+    saved tensors, not the gradients of other lengths."""
+    ops = PlainOps()
+    z, lam, h0 = leaves((5, 2, 9), (3,), (2, 3))
+    lengths = torch.tensor([5, 2])
+    y, h = _Recurrence.apply(ops, False, z, lam, h0, lengths)
+    lengths.copy_(torch.tensor([1, 5]))
+    with pytest.raises(RuntimeError, match="inplace"):
+        (y.sum() + h.sum()).backward()
