@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
         uint32_t raw[3][S], rawd[S];
         const uint8_t *src = ring + used % STAGES * STAGE;
         if (TMA) {
-          tc::mbar_wait(&sh.full[used % STAGES], (used / STAGES) & 1, err, &sh.abort, WAIT_NS);
+          wait_copy(&sh.full[used % STAGES], (used / STAGES) & 1, err, &sh.abort);
 #pragma unroll
           for (int k = 0; k < 3; ++k)
 #pragma unroll

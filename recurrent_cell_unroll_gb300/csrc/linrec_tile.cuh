@@ -104,14 +104,37 @@ __device__ __forceinline__ Unit unit_of(const Cut &cut, int B, int u, int cw) {
   return v;
 }
 
+// A wait has run out, and results with it.  It is reported in place of a length or slot
+// that was out of range, which they would have outlived.
+__device__ __forceinline__ void report_timeout(int *err) {
+  atomicExch(err, (int)DEV_TIMEOUT);
+}
 // Whether a wait is to end unfinished: past its limit, or as another one ran out.
 __device__ __forceinline__ bool give_up(uint64_t deadline, int *err, volatile int *abort) {
   if (!*abort && ld_volatile_int(err) != (int)DEV_TIMEOUT) {
     if (globaltimer_ns() <= deadline) return false;
-    atomicCAS(err, (int)DEV_OK, (int)DEV_TIMEOUT);
+    report_timeout(err);
   }
   *abort = 1;
   return true;
+}
+// Until a tile's copies have landed (whatever has been reported elsewhere: they are this
+// block's own).
+__device__ __forceinline__ void wait_copy(uint64_t *bar, uint32_t parity, int *err,
+                                          volatile int *abort) {
+  if (tc::mbar_try_wait(bar, parity)) return;
+  const uint64_t deadline = globaltimer_ns() + WAIT_NS;
+  uint32_t spins = 0;
+  while (!tc::mbar_try_wait(bar, parity)) {
+    if ((++spins & 255u) == 0) {
+      if (*abort) return;
+      if (globaltimer_ns() > deadline) {
+        report_timeout(err);
+        *abort = 1;
+        return;
+      }
+    }
+  }
 }
 
 __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
