@@ -556,7 +556,9 @@ RCU_API int rssm_destroy(rcu_rssm_t h);
  * width; rows are dense), so that a slice of a wider matrix, for example one
  * gate of a fused projection's output, is passed as it is.  dtype is RCU_F32
  * or RCU_BF16; sums, statistics and states are fp32 throughout.  Any alignment
- * that the type itself has is taken; 16-byte aligned rows run fastest.
+ * that the type itself has is taken; 16-byte aligned rows run fastest.  A row has
+ * at most 2^31 - 8192 values, a sequence 2^30 steps and B * H / 32 is at most 2^30;
+ * more is RCU_ERR_UNSUPPORTED.
  */
 typedef struct rcu_seq_s rcu_seq;
 

@@ -48,6 +48,10 @@ void begin(rcu_seq *h, const char *name, cudaStream_t s) {
   h->prof_begin(name, s);
 }
 
+// A row's columns are counted in 32 bits, and blocks of them end past its own end (by
+// 4096 at most: layer norm of long rows).
+constexpr int WIDEST = INT32_MAX - 8191;
+
 bool dtype_ok(int dtype) { return dtype == RCU_F32 || dtype == RCU_BF16; }
 
 // The handle, and that its device is the current one.
@@ -102,6 +106,7 @@ int check_linrec(const char *fn, rcu_seq *h, int dtype, int layout, int T, int B
     return fail(RCU_ERR_INVALID, "%s: unknown layout %d", fn, layout);
   if (T < 0 || B < 0 || H < 1)
     return fail(RCU_ERR_INVALID, "%s: T, B must be >= 0 and H >= 1 (got %d, %d, %d)", fn, T, B, H);
+  if (H > WIDEST) return fail(RCU_ERR_UNSUPPORTED, "%s: H above 2^31 - 8192", fn);
   // tiles and rows are counted in 32 bits
   if (T > (1 << 30) || (int64_t)B * ((H + 31) / 32) > (1 << 30))
     return fail(RCU_ERR_UNSUPPORTED, "%s: T or B * H / 32 above 2^30", fn);
@@ -119,6 +124,7 @@ int check_rows(const char *fn, rcu_seq *h, int dtype, int64_t rows, int n) {
   if (rows < 0 || n < 1)
     return fail(RCU_ERR_INVALID, "%s: rows must be >= 0 and n >= 1 (got %lld, %d)", fn,
                 (long long)rows, n);
+  if (n > WIDEST) return fail(RCU_ERR_UNSUPPORTED, "%s: n above 2^31 - 8192", fn);
   return RCU_OK;
 }
 
