@@ -131,7 +131,8 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
     uint8_t *dst = ring + issued % STAGES * STAGE;
     if (TMA) {
       uint64_t *bar = &sh.full[issued % STAGES];
-      const int states = bulk_states && !MAP ? min(CW, p.H - v.c0) * 4 : 0;
+      const bool kept = bulk_states && !MAP && RCU_DCHECK(tile >= 0 && tile * STEPS < p.T, err);
+      const int states = kept ? min(CW, p.H - v.c0) * 4 : 0;
       tc::mbar_arrive_expect_tx(bar, (MAP ? TENSORS - 2 * IN : TENSORS) + states);
       if (states)
         tc::bulk_load(dst + TENSORS, p.states + ((int64_t)tile * p.B + v.b) * p.H + v.c0, states,
@@ -143,7 +144,10 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
       }
       tma_load_3d(dst + 3 * IN, &mdy, bar, v.c0, v.b, tile * STEPS);
     } else {
-      const int tw = tile * STEPS + warp * S, rows = min(next.len - tw, S);
+      const int tw = tile * STEPS + warp * S;
+      const int rows = RCU_DCHECK(tile >= 0 && v.b < p.B && v.c0 < p.H && next.len <= p.T, err)
+                           ? min(next.len - tw, S)
+                           : 0;
       const int width = min(CW, p.H - v.c0);
       auto pos = [&](const SeqIn &in, int size) {
         return ((int64_t)tw * in.st + (int64_t)v.b * in.sb + v.c0) * size;
@@ -205,7 +209,8 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
     if (p.dh_n) load_v(p.dh_n + row, live, nc);
     nc = neg_v(nc);  // the carry, negated: -dL/dh after the steps so far
     if (!MAP && v.seg < cut.nseg - 1)
-      nc = apply(chain_segments<V, NW>(mem, cut, p.B, v, CW, cut.nseg - 1, v.seg, -1, sh.part[0]),
+      nc = apply(chain_segments<V, NW>(mem, cut, p.B, v, CW, cut.nseg - 1, v.seg, -1, sh.part[0],
+                                        err),
                  nc);
     if (M == SHARES && v.last < cut.tiles)
       nc = take_carry<V>(mem, blockIdx.x - cut.groups, err, &sh.abort);
@@ -228,7 +233,7 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
       V em1[S], nb[S], ns[S], ng[S], dy[S], h = zero, fe = zero;
       Aff<V> mine = identity<V>();
       if (on) {
-        if (!MAP && !(TMA && bulk_states))
+        if (!MAP && !(TMA && bulk_states) && RCU_DCHECK(v.b < p.B, err))
           load_v(p.states + (int64_t)tile * p.B * p.H + row, live, h);
         float scale[3][S];
         bool bounded = true;  // the gates' logits, by their blocks' exponents
@@ -418,7 +423,8 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
       }
     }
     if (MAP) {
-      if (warp == 0) put(segment_map<V>(mem, cut, p.B, v.seg, v, CW), all_map);
+      if (warp == 0 && RCU_DCHECK(v.seg > 0 && v.seg < cut.nseg && v.b < p.B, err))
+        put(segment_map<V>(mem, cut, p.B, v.seg, v, CW), all_map);
       continue;
     }
     if (rank == 0 && warp == 0) {
@@ -437,7 +443,8 @@ __global__ void __launch_bounds__(NT, TMA || sizeof(T) == 4 || M == SHARES ? PER
         for (int w = 0; w < NW; ++w) sum = add_v(sum, sh.sum[w][lane]);
         const int64_t at = M == SHARES ? blockIdx.x / cut.groups
                                   : (int64_t)(v.seg * p.B + v.b) * cs + rank;
-        store_v(partial + at * p.H + ch, sum, live);
+        const int64_t rows = M == SHARES ? gridDim.x / cut.groups : (int64_t)cut.nseg * p.B * cs;
+        if (RCU_DCHECK(at < rows, err)) store_v(partial + at * p.H + ch, sum, live);
       }
       __syncthreads();
       sh.sum[warp][lane] = zero;

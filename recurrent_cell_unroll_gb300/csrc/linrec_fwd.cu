@@ -138,7 +138,10 @@ __global__ void __launch_bounds__(NT, PER_SM)
       tma_load_3d(dst + STAGE / 3, &mr, bar, v.c0, v.b, tile * STEPS);
       tma_load_3d(dst + 2 * STAGE / 3, &mi, bar, v.c0, v.b, tile * STEPS);
     } else {
-      const int tw = tile * STEPS + warp * S, rows = min(next.len - tw, S);
+      const int tw = tile * STEPS + warp * S;
+      const int rows = RCU_DCHECK(tile >= 0 && v.b < p.B && v.c0 < p.H && next.len <= p.T, err)
+                           ? min(next.len - tw, S)
+                           : 0;
       const int bytes = min(CW, p.H - v.c0) * (int)sizeof(T);
       uint8_t *to = dst + warp * (STAGE / 3 / NW);
       auto pos = [&](const SeqIn &in) {
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
       carry = take_carry<V>(mem, blockIdx.x - cut.groups, err, &sh.abort);
     Aff<V> whole = identity<V>();
     if (!MAP && v.seg > 0)
-      carry = apply(chain_segments<V, NW>(mem, cut, p.B, v, CW, 0, v.seg, 1, sh.part[0]), carry);
+      carry = apply(chain_segments<V, NW>(mem, cut, p.B, v, CW, 0, v.seg, 1, sh.part[0], err), carry);
     for (int base = v.first; base < v.last; base += cs) {
       const int tile = base + rank, tw = tile * STEPS + warp * S;
       const bool on = tile < v.last && tile * STEPS < len;  // the same for the whole block
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
         parity ^= 1;
       }
       if (MAP || tile >= v.last) continue;
-      if (warp == 0 && p.states)
+      if (warp == 0 && p.states && RCU_DCHECK(tile * STEPS < p.T && v.b < p.B, err))
         store_v(p.states + (int64_t)tile * p.B * p.H + row, neg_v(h), live);
       if (TMA) {
         uint32_t *to = reinterpret_cast<uint32_t *>(out + warp * S * 128) + lane;
@@ -345,7 +348,8 @@ __global__ void __launch_bounds__(NT, PER_SM)
       }
     }
     if (MAP) {
-      if (warp == 0) put(segment_map<V>(mem, cut, p.B, v.seg, v, CW), whole);
+      if (warp == 0 && RCU_DCHECK(v.seg < cut.nseg - 1 && v.b < p.B, err))
+        put(segment_map<V>(mem, cut, p.B, v.seg, v, CW), whole);
     } else if (rank == 0 && warp == 0) {
       if (v.last == cut.tiles) {
         if (p.h_n) store_v(p.h_n + row, neg_v(carry), live);

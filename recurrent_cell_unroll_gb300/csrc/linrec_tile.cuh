@@ -458,6 +458,7 @@ __device__ __forceinline__ void leave_carry(void *mem, V carry) {
 // by each warp; that block runs (a cooperative launch) and left it before all its other work
 template <typename V>
 __device__ __forceinline__ V take_carry(void *mem, int from, int *err, volatile int *abort) {
+  if (!RCU_DCHECK(from >= 0 && from < (int)blockIdx.x, err)) return V{};
   const unsigned *lanes = static_cast<const unsigned *>(mem) + from;
   if (ld_acquire_gpu(lanes) != 32) {
     const uint64_t deadline = globaltimer_ns() + WAIT_NS;
@@ -479,13 +480,14 @@ __device__ __forceinline__ typename Slot<V>::type *segment_map(void *maps, const
 template <typename V, int NWARP>
 __device__ __forceinline__ Aff<V> chain_segments(void *maps, const Cut &cut, int B, const Unit &v,
                                                  int cw, int from, int to, int by,
-                                                 typename Slot<V>::type (*part)[32]) {
+                                                 typename Slot<V>::type (*part)[32], int *err) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n = (to - from) * by, each = ceil_div(n, NWARP);
   Aff<V> a = identity<V>();
 #pragma unroll 8
   for (int q = warp * each; q < min(n, (warp + 1) * each); ++q)
-    a = then(a, get(segment_map<V>(maps, cut, B, from + q * by, v, cw)));
+    if (RCU_DCHECK(from + q * by >= 0 && from + q * by < cut.nseg && v.b < B, err))
+      a = then(a, get(segment_map<V>(maps, cut, B, from + q * by, v, cw)));
   __syncthreads();
   put(&part[warp][lane], a);
   __syncthreads();
