@@ -565,7 +565,7 @@ cudaError_t linrec::launch_dlambda(const float *partial, int64_t rows, const Lin
 cudaError_t launch_linrec_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm, bool vec,
                               cudaStream_t s, int *launches) {
   if (linrec::short_bwd_pays(p, PER_SM * nsm, vec))
-    return linrec::launch_short_bwd(p, ws, err, nsm, s, launches);
+    return linrec::launch_short_bwd(p, ws, err, s, launches);
   const bool q8 = p.saved == RCU_I8;
   if (p.dtype == RCU_BF16)
     return q8 ? bwd<int8_t, bf16>(p, ws, err, vec, s, launches)

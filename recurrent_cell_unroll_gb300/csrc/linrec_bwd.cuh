@@ -194,7 +194,7 @@ cudaError_t launch_dlambda(const float *partial, int64_t rows, const LinrecBwd &
 // The kernel for short sequences of many rows (linrec_bwd_short.cu), and whether it is
 // the faster one; resident_blocks: of the tiled kernel, vec: as of launch_linrec_bwd.
 bool short_bwd_pays(const LinrecBwd &p, int resident_blocks, bool vec);
-cudaError_t launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s,
+cudaError_t launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, cudaStream_t s,
                              int *launches);
 
 }  // namespace linrec

@@ -31,21 +31,26 @@ template <typename T>
 constexpr size_t state_bytes(int steps) {
   return (size_t)NW * steps * 32 * sizeof(typename Lane<T>::V);
 }
-static_assert(state_bytes<float>(std::max(SHORT_T, SHORT_LOOSE)) <= 48 << 10 &&
-                  state_bytes<bf16>(std::max({SHORT_T, SHORT_Q8, SHORT_SPLIT})) <= 48 << 10,
+template <typename T>
+constexpr int most_steps() {
+  return sizeof(T) == 4 ? std::max(SHORT_T, SHORT_LOOSE) : std::max({SHORT_T, SHORT_Q8, SHORT_SPLIT});
+}
+static_assert(std::max(state_bytes<float>(most_steps<float>()), state_bytes<bf16>(most_steps<bf16>())) <=
+                  48 << 10,
               "a block's states fit the default limit");
 
 template <typename IT, typename T>
 __global__ void __launch_bounds__(NT, 3)
-    linrec_bwd_short_kernel(const LinrecBwd p, const int groups, float *__restrict__ partial,
-                            const int words, int *err) {
+    linrec_bwd_short_kernel(const LinrecBwd p, const int groups, const int each,
+                            float *__restrict__ partial, const int words, int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   constexpr bool Q8 = sizeof(IT) == 1;
   typedef typename Lane<T>::V V;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   V *before = reinterpret_cast<V *>(smem) + (size_t)warp * p.T * 32 + lane;  // the state before t
-  const int w = blockIdx.x * NW + warp, c0 = w % groups * CW, stride = gridDim.x * NW / groups;
+  const int w = blockIdx.x * NW + warp, c0 = w % groups * CW;
+  if (w >= each * groups) return;
   const int ch = c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
   const int nb8 = ceil_div(p.H, BLOCK8);
   V k2, nk, zero, minus;
@@ -93,7 +98,7 @@ __global__ void __launch_bounds__(NT, 3)
         if (t0 + s >= len) em1[s] = nb[s] = ns[s] = ng[s] = 0;
     }
   };
-  for (int64_t b = w / groups; b < p.B; b += stride) {
+  for (int64_t b = w / groups; b < p.B; b += each) {
     const int64_t row = b * p.H + ch;
     const int len = row_length(p.lengths, (int)b, p.T, err);
     V h, nc = zero, sum = zero;
@@ -150,17 +155,14 @@ __global__ void __launch_bounds__(NT, 3)
 }
 
 template <typename IT, typename T>
-cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s, int *launches) {
+cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, cudaStream_t s, int *launches) {
   const int groups = ceil_div(p.H, Shape<T>::CW);
   const size_t smem = state_bytes<T>(p.T);
   auto fn = linrec_bwd_short_kernel<IT, T>;
-  // a whole number of warps a group: each warp stays with its channels
-  const int64_t most = (int64_t)3 * nsm * NW;
-  const int64_t each = std::max<int64_t>(1, std::min<int64_t>(p.B, most / groups));
-  const int64_t warps = each * groups;
-  // blocks of NW warps: a multiple of the groups in all
-  int64_t blocks = (warps + NW - 1) / NW;
-  while (blocks * NW % groups) ++blocks;
+  static PerDevice<int> rooms;
+  const int room =
+      rooms.here([=] { return resident_blocks(fn, NT, state_bytes<T>(most_steps<T>())); });
+  const Warps w = warps_of(p.B, groups, room, NW);
   const SeqIn *in[4] = {&p.x, &p.r, &p.i, &p.dy};
   const SeqOut *out[3] = {&p.dx, &p.dr, &p.di};
   auto whole = [](const void *q, int64_t st, int64_t sb, int size) {
@@ -178,7 +180,7 @@ cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t 
     const cudaError_t e = ws.get((size_t)p.B * p.H * 4, &partial);
     if (e != cudaSuccess) return e;
   }
-  fn<<<(unsigned)blocks, NT, smem, s>>>(p, groups, partial, words, err);
+  fn<<<w.blocks, NT, smem, s>>>(p, groups, w.each, partial, words, err);
   ++*launches;
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !p.dlambda) return e;
@@ -209,14 +211,14 @@ bool linrec::short_bwd_pays(const LinrecBwd &p, int resident_blocks, bool vec) {
   return p.T <= (p.saved == RCU_I8 ? SHORT_Q8 : SHORT_T);
 }
 
-cudaError_t linrec::launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, int nsm,
-                                     cudaStream_t s, int *launches) {
+cudaError_t linrec::launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, cudaStream_t s,
+                                     int *launches) {
   const bool q8 = p.saved == RCU_I8;
   if (p.dtype == RCU_BF16)
-    return q8 ? run<int8_t, bf16>(p, ws, err, nsm, s, launches)
-              : run<bf16, bf16>(p, ws, err, nsm, s, launches);
-  return q8 ? run<int8_t, float>(p, ws, err, nsm, s, launches)
-            : run<float, float>(p, ws, err, nsm, s, launches);
+    return q8 ? run<int8_t, bf16>(p, ws, err, s, launches)
+              : run<bf16, bf16>(p, ws, err, s, launches);
+  return q8 ? run<int8_t, float>(p, ws, err, s, launches)
+            : run<float, float>(p, ws, err, s, launches);
 }
 
 }  // namespace rcu

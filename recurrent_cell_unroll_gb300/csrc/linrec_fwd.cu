@@ -418,7 +418,7 @@ cudaError_t fwd(const LinrecFwd &p, DevMem &ws, int *err, bool vec, cudaStream_t
 cudaError_t launch_linrec_fwd(const LinrecFwd &p, DevMem &ws, int *err, int nsm, bool vec,
                               cudaStream_t s, int *launches) {
   if (linrec::short_fwd_pays(p, PER_SM * nsm, vec))
-    return linrec::launch_short_fwd(p, err, nsm, s, launches);
+    return linrec::launch_short_fwd(p, err, s, launches);
   return p.dtype == RCU_BF16 ? fwd<bf16>(p, ws, err, vec, s, launches)
                              : fwd<float>(p, ws, err, vec, s, launches);
 }

@@ -23,15 +23,17 @@ constexpr int NW = 4, NT = 32 * NW, N = 4, PER_SM = 6;  // N: steps whose reads 
 // the most steps: of TMA's rows; of others; of split words
 constexpr int SHORT_T = 32, SHORT_LOOSE = CHUNK, SHORT_SPLIT = 20;
 
-// words: bit k: input k's (x, r, i) values of a lane are one word; bit 3: the output's
+// each: warps that share a group's rows; words: bit k: input k's (x, r, i) values of a lane are one word; bit 3: the output's
 template <typename T>
 __global__ void __launch_bounds__(NT, PER_SM)
-    linrec_fwd_short_kernel(const LinrecFwd p, const int groups, const int words, int *err) {
+    linrec_fwd_short_kernel(const LinrecFwd p, const int groups, const int each, const int words,
+                            int *err) {
   constexpr int CPT = Shape<T>::CPT, CW = Shape<T>::CW;
   constexpr int BATCH = CPT == 2 ? N : N / 2;  // the N steps at once: pairs of channels, or of steps
   typedef typename Lane<T>::V V;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int w = blockIdx.x * NW + warp, c0 = w % groups * CW, stride = gridDim.x * NW / groups;
+  const int w = blockIdx.x * NW + warp, c0 = w % groups * CW;
+  if (w >= each * groups) return;
   const int ch = c0 + lane * CPT, live = min(max(p.H - ch, 0), CPT);
   V k2, zero, minus;
   set(zero, 0.f);
@@ -55,7 +57,7 @@ __global__ void __launch_bounds__(NT, PER_SM)
       }
     }
   };
-  for (int64_t b = w / groups; b < p.B; b += stride) {
+  for (int64_t b = w / groups; b < p.B; b += each) {
     const int64_t row = b * p.H + ch;
     const int len = row_length(p.lengths, (int)b, p.T, err);
     load(b, 0, len);
@@ -80,13 +82,11 @@ __global__ void __launch_bounds__(NT, PER_SM)
 }
 
 template <typename T>
-cudaError_t run(const LinrecFwd &p, int *err, int nsm, cudaStream_t s, int *launches) {
+cudaError_t run(const LinrecFwd &p, int *err, cudaStream_t s, int *launches) {
   const int groups = ceil_div(p.H, Shape<T>::CW);
-  // a whole number of warps a group: each warp stays with its channels
-  const int64_t most = (int64_t)PER_SM * nsm * NW;
-  const int64_t each = std::max<int64_t>(1, std::min<int64_t>(p.B, most / groups));
-  int64_t blocks = (each * groups + NW - 1) / NW;
-  while (blocks * NW % groups) ++blocks;
+  static PerDevice<int> rooms;
+  const int room = rooms.here([] { return resident_blocks(linrec_fwd_short_kernel<T>, NT, 0); });
+  const Warps w = warps_of(p.B, groups, room, NW);
   auto whole = [](const void *q, int64_t st, int64_t sb) {
     constexpr int bytes = Shape<T>::CPT * (int)sizeof(T);
     return reinterpret_cast<uintptr_t>(q) % bytes == 0 && st * (int)sizeof(T) % bytes == 0 &&
@@ -94,7 +94,7 @@ cudaError_t run(const LinrecFwd &p, int *err, int nsm, cudaStream_t s, int *laun
   };
   const int words = whole(p.x.p, p.x.st, p.x.sb) | whole(p.r.p, p.r.st, p.r.sb) << 1 |
                     whole(p.i.p, p.i.st, p.i.sb) << 2 | whole(p.y.p, p.y.st, p.y.sb) << 3;
-  linrec_fwd_short_kernel<T><<<(unsigned)blocks, NT, 0, s>>>(p, groups, words, err);
+  linrec_fwd_short_kernel<T><<<w.blocks, NT, 0, s>>>(p, groups, w.each, words, err);
   ++*launches;
   return cudaGetLastError();
 }
@@ -118,10 +118,8 @@ bool linrec::short_fwd_pays(const LinrecFwd &p, int resident_blocks, bool vec) {
   return aligned(4) || p.T <= SHORT_SPLIT;
 }
 
-cudaError_t linrec::launch_short_fwd(const LinrecFwd &p, int *err, int nsm, cudaStream_t s,
-                                     int *launches) {
-  return p.dtype == RCU_BF16 ? run<bf16>(p, err, nsm, s, launches)
-                             : run<float>(p, err, nsm, s, launches);
+cudaError_t linrec::launch_short_fwd(const LinrecFwd &p, int *err, cudaStream_t s, int *launches) {
+  return p.dtype == RCU_BF16 ? run<bf16>(p, err, s, launches) : run<float>(p, err, s, launches);
 }
 
 }  // namespace rcu

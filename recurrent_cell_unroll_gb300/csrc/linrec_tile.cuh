@@ -516,17 +516,21 @@ struct Resident {
   int clusters[MAX + 1] = {};
 };
 template <typename... KArgs>
-Resident resident(void (*fn)(KArgs...), int threads, int max_cs, size_t smem0, size_t smem_per_cs) {
-  Resident r;
+int resident_blocks(void (*fn)(KArgs...), int threads, size_t smem) {
   int dev = 0, nsm = 0, blocks = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, fn, threads, smem);
+  return std::max(1, blocks * nsm);
+}
+template <typename... KArgs>
+Resident resident(void (*fn)(KArgs...), int threads, int max_cs, size_t smem0, size_t smem_per_cs) {
+  Resident r;
   const size_t most = smem0 + max_cs * smem_per_cs;
   cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
   if (max_cs > 8)
     cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, fn, threads, smem0 + smem_per_cs);
-  r.clusters[1] = std::max(1, blocks * nsm);
+  r.clusters[1] = resident_blocks(fn, threads, smem0 + smem_per_cs);
   for (int cs = 2; cs <= max_cs; ++cs) {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute at;
@@ -635,10 +639,21 @@ cudaError_t launch_cut(void (*fn)(KArgs...), const Plan &pl, int threads, size_t
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// The short kernels' warps: `each` a group of channels, which they stay with from row to
+// row; no more in all than the GPU has room for, as one block too many takes a wave of
+// its own (bf16 T=11 B=188 H=1921, 31 groups: backward 176 us in 465 blocks, 128 in
+// 450).  The last block's warps past each * groups have nothing to do.
+struct Warps {
+  int each, blocks;
+};
+inline Warps warps_of(int B, int groups, int room, int per_block) {
+  const int each = std::max(1, std::min(B, room * per_block / groups));
+  return {each, ceil_div(each * groups, per_block)};
+}
 // The forward kernel for short sequences of many rows (linrec_fwd_short.cu), and whether
 // it is the faster one; resident_blocks: of the tiled kernel, vec: as of launch_linrec_fwd.
 bool short_fwd_pays(const LinrecFwd &p, int resident_blocks, bool vec);
-cudaError_t launch_short_fwd(const LinrecFwd &p, int *err, int nsm, cudaStream_t s, int *launches);
+cudaError_t launch_short_fwd(const LinrecFwd &p, int *err, cudaStream_t s, int *launches);
 
 }  // namespace linrec
 }  // namespace rcu
