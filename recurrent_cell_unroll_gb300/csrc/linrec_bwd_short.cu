@@ -6,14 +6,18 @@
 // steps, first forwards, keeping the states in shared memory, then backwards with
 // the gates made again; nothing is exchanged.  It stays with its channels, whose
 // constants it keeps, from one batch row to the next.  Making the gates twice tells
-// with the length: bf16 B=250 H=2048 takes 91 us here and 118 tiled at 20 steps, 165
-// and 122 at 40; fp32 B=183 H=3312 158 and 202 at 17 steps.
+// with the length: bf16 B=250 H=2048 takes 90 us here and 120 tiled at 20 steps, 164
+// and 124 at 40.
 //
 // How far it pays goes by the rows: those that TMA cannot address cost the tiled kernel
-// more, and this one only where a lane's values are not a word.  B=188, here and tiled:
-// bf16 H=1920 T=20 70 and 73 us, H=1922 T=20 94 and 118, H=1921 T=11 107 and 115,
-// T=13 129 and 114; from 8 bits H=1920 T=14 82 and 95, T=18 109 and 91; fp32 H=1920
-// T=17 102 and 102, H=1921 T=44 199 and 207.
+// more, and this one only where a lane's values are not a word.  In us, here and tiled:
+//   bf16   T=20: B=188 H=1920 72 and 73, H=1922 75 and 115; B=80 H=1984 38 and 38;
+//          split words: B=188 H=1921 T=9 108 and 113, T=10 118 and 113; B=700 H=1023
+//          T=8 160 and 183; B=80 H=1985 T=8 34 and 51
+//          from 8 bits: B=188 H=1920 T=9 77 and 86, T=10 88 and 87; B=700 H=1024 T=8
+//          125 and 163, T=11 170 and 165; B=80 H=1984 T=14 43 and 47
+//   fp32   T=20: B=188 H=1920 86 and 100, B=60 H=1984 36 and 52; B=700 H=1024 T=17 149
+//          and 246; T=44, off TMA: B=188 H=1921 172 and 204, B=60 H=1985 70 and 70
 #include "linrec_bwd.cuh"
 
 namespace rcu {
@@ -22,8 +26,9 @@ namespace {
 using namespace linrec;
 
 constexpr int NW = 4, NT = 32 * NW, N = 4;  // N: steps whose reads are in flight together
-// the most steps: at all; of pairs from 8 bits; of fp32 rows off TMA; of split words
-constexpr int SHORT_T = 20, SHORT_Q8 = 16, SHORT_LOOSE = 44, SHORT_SPLIT = 12;
+// the most steps: at all; of pairs from 8 bits; of fp32 rows off TMA; of split words; and
+// of pairs from 8 bits or split words by steps_within(), where warps have many rows each
+constexpr int SHORT_T = 20, SHORT_Q8 = 16, SHORT_LOOSE = 44, SHORT_SPLIT = 12, SHORT_MANY = 12;
 
 // Of a block's states.  Below what a launch may have without asking: what a kernel is
 // allowed beyond that is one setting for all the process's threads.
@@ -155,14 +160,20 @@ __global__ void __launch_bounds__(NT, 3)
 }
 
 template <typename IT, typename T>
+Warps warps(const LinrecBwd &p) {
+  static PerDevice<int> rooms;
+  const int room = rooms.here([] {
+    return resident_blocks(linrec_bwd_short_kernel<IT, T>, NT, state_bytes<T>(most_steps<T>()));
+  });
+  return warps_of(p.B, ceil_div(p.H, Shape<T>::CW), room, NW);
+}
+
+template <typename IT, typename T>
 cudaError_t run(const LinrecBwd &p, DevMem &ws, int *err, cudaStream_t s, int *launches) {
   const int groups = ceil_div(p.H, Shape<T>::CW);
   const size_t smem = state_bytes<T>(p.T);
   auto fn = linrec_bwd_short_kernel<IT, T>;
-  static PerDevice<int> rooms;
-  const int room =
-      rooms.here([=] { return resident_blocks(fn, NT, state_bytes<T>(most_steps<T>())); });
-  const Warps w = warps_of(p.B, groups, room, NW);
+  const Warps w = warps<IT, T>(p);
   const SeqIn *in[4] = {&p.x, &p.r, &p.i, &p.dy};
   const SeqOut *out[3] = {&p.dx, &p.dr, &p.di};
   auto whole = [](const void *q, int64_t st, int64_t sb, int size) {
@@ -207,8 +218,12 @@ bool linrec::short_bwd_pays(const LinrecBwd &p, int resident_blocks, bool vec) {
     return true;
   };
   if (!half) return p.T <= (vec && aligned(16, 16) ? SHORT_T : SHORT_LOOSE);
-  if (!aligned(4, 2)) return p.T <= SHORT_SPLIT;
-  return p.T <= (p.saved == RCU_I8 ? SHORT_Q8 : SHORT_T);
+  const bool q8 = p.saved == RCU_I8;
+  const bool whole = aligned(4, 2);
+  if (!q8 && whole) return p.T <= SHORT_T;
+  if (p.T > (whole ? SHORT_Q8 : SHORT_SPLIT)) return false;
+  const Warps w = q8 ? warps<int8_t, bf16>(p) : warps<bf16, bf16>(p);
+  return p.B <= 2 * w.each || steps_within(p.T, p.B, w, SHORT_MANY);
 }
 
 cudaError_t linrec::launch_short_bwd(const LinrecBwd &p, DevMem &ws, int *err, cudaStream_t s,

@@ -6,12 +6,15 @@
 // after another; nothing is exchanged, and N steps' reads are in flight together.
 // It stays with its channels, whose constants it keeps, from one batch row to the
 // next.  Bound by the reads' latency: 24 warps an SM with 12 words each in flight (8
-// steps at once and 16 warps took 32 us where this takes 25, bf16 T=20 B=250 H=2048).
+// steps at once and 16 warps took 32 us where this took 25, bf16 T=20 B=250 H=2048).
 //
-// How far it pays goes by the rows, as for the backward.  B=250, here and tiled: bf16
-// H=2048 T=4 21 and 42 us, T=20 25 and 45, T=40 51 and 54; H=2046 T=40 52 and 89;
-// H=2047, whose pairs are not words, T=12 34 and 71, T=24 89 and 80; fp32 H=2048 T=20 42
-// and 65, T=32 62 and 63; H=2047 T=64 115 and 118.
+// How far it pays goes by the rows, as for the backward.  In us, here and tiled:
+//   bf16   B=250 H=2048 T=4 20 and 40, T=20 29 and 45, T=32 41 and 43; B=900 H=1024 T=32
+//          65 and 86; off TMA, T=64: B=250 H=2046 77 and 92, B=100 H=1922 35 and 41;
+//          split words: B=250 H=2047 T=12 66 and 70, T=16 87 and 74; B=900 H=1023 T=16
+//          117 and 133; B=100 H=1921 T=20 24 and 35
+//   fp32   B=250 H=2048 T=20 39 and 64, T=32 57 and 62; off TMA, T=64: B=250 H=2047 105
+//          and 116, B=60 H=1985 31 and 33
 #include "linrec_bwd.cuh"
 
 namespace rcu {
@@ -20,7 +23,7 @@ namespace {
 using namespace linrec;
 
 constexpr int NW = 4, NT = 32 * NW, N = 4, PER_SM = 6;  // N: steps whose reads are in flight together
-// the most steps: of TMA's rows; of others; of split words
+// the most steps: of TMA's rows; of others; of split words, by steps_within()
 constexpr int SHORT_T = 32, SHORT_LOOSE = CHUNK, SHORT_SPLIT = 20;
 
 // each: warps that share a group's rows; words: bit k: input k's (x, r, i) values of a lane are one word; bit 3: the output's
@@ -82,11 +85,16 @@ __global__ void __launch_bounds__(NT, PER_SM)
 }
 
 template <typename T>
-cudaError_t run(const LinrecFwd &p, int *err, cudaStream_t s, int *launches) {
-  const int groups = ceil_div(p.H, Shape<T>::CW);
+Warps warps(const LinrecFwd &p) {
   static PerDevice<int> rooms;
   const int room = rooms.here([] { return resident_blocks(linrec_fwd_short_kernel<T>, NT, 0); });
-  const Warps w = warps_of(p.B, groups, room, NW);
+  return warps_of(p.B, ceil_div(p.H, Shape<T>::CW), room, NW);
+}
+
+template <typename T>
+cudaError_t run(const LinrecFwd &p, int *err, cudaStream_t s, int *launches) {
+  const int groups = ceil_div(p.H, Shape<T>::CW);
+  const Warps w = warps<T>(p);
   auto whole = [](const void *q, int64_t st, int64_t sb) {
     constexpr int bytes = Shape<T>::CPT * (int)sizeof(T);
     return reinterpret_cast<uintptr_t>(q) % bytes == 0 && st * (int)sizeof(T) % bytes == 0 &&
@@ -115,7 +123,7 @@ bool linrec::short_fwd_pays(const LinrecFwd &p, int resident_blocks, bool vec) {
     return true;
   };
   if (vec && aligned(16)) return p.T <= SHORT_T;
-  return aligned(4) || p.T <= SHORT_SPLIT;
+  return aligned(4) || steps_within(p.T, p.B, warps<bf16>(p), SHORT_SPLIT);
 }
 
 cudaError_t linrec::launch_short_fwd(const LinrecFwd &p, int *err, cudaStream_t s, int *launches) {

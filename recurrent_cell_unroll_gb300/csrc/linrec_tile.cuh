@@ -650,6 +650,11 @@ inline Warps warps_of(int B, int groups, int room, int per_block) {
   const int each = std::max(1, std::min(B, room * per_block / groups));
   return {each, ceil_div(each * groups, per_block)};
 }
+// Whether they take at most `limit` steps a row of B rows of T steps, counting what warps
+// without a row in the last turn could have taken.
+inline bool steps_within(int T, int B, const Warps &w, int limit) {
+  return (int64_t)T * ceil_div(B, w.each) * w.each <= (int64_t)limit * B;
+}
 // The forward kernel for short sequences of many rows (linrec_fwd_short.cu), and whether
 // it is the faster one; resident_blocks: of the tiled kernel, vec: as of launch_linrec_fwd.
 bool short_fwd_pays(const LinrecFwd &p, int resident_blocks, bool vec);
