@@ -63,7 +63,7 @@ struct Decode<float, float> {
     return limit_r(__uint_as_float(v), l) * -LOG2E;
   }
   __device__ __forceinline__ static float i(uint32_t v, float) {
-    return floor_logit(__uint_as_float(v)) * -LOG2E;
+    return __uint_as_float(v) * -LOG2E;
   }
   __device__ __forceinline__ static float bounded(uint32_t v, float s) { return i(v, s); }
 };
@@ -73,11 +73,9 @@ struct Decode<int8_t, float> {
     return (code_bits(v ^ 0x80u, 0) - 8388736.f) * scale;
   }
   __device__ __forceinline__ static float r(uint32_t v, float scale, const Limits &l) {
-    return fmaxf(i(v, scale), l.top * -LOG2E);
+    return fmaxf(x(v, scale), l.top * -LOG2E);
   }
-  __device__ __forceinline__ static float i(uint32_t v, float scale) {
-    return fminf(x(v, scale), EXP_TOP);
-  }
+  __device__ __forceinline__ static float i(uint32_t v, float scale) { return x(v, scale); }
   __device__ __forceinline__ static float bounded(uint32_t v, float s) { return x(v, s); }
 };
 
@@ -98,7 +96,7 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][N], const float (
       r[n] = SMALL ? D::bounded(raw[1][q], scale[1][q]) : D::r(raw[1][q], scale[1][q], lim);
       i[n] = SMALL ? D::bounded(raw[2][q], scale[2][q]) : D::i(raw[2][q], scale[2][q]);
     }
-    gates_n<SMALL, BATCH>(x, r, i, k2, em1 + s, nb + s, ns + s, ng + s);
+    gates_n<SMALL, true, BATCH>(x, r, i, k2, em1 + s, nb + s, ns + s, ng + s);
   }
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
@@ -120,7 +118,7 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][N], const float (
       i[n] = SMALL ? f2(D::bounded(raw[2][q], scale[2][q]), D::bounded(raw[2][q + 1], scale[2][q + 1]))
                    : f2(D::i(raw[2][q], scale[2][q]), D::i(raw[2][q + 1], scale[2][q + 1]));
     }
-    gates_n<SMALL, BATCH>(x, r, i, f2(k2), m, b, vs, vg);
+    gates_n<SMALL, false, BATCH>(x, r, i, f2(k2), m, b, vs, vg);
 #pragma unroll
     for (int n = 0; n < BATCH; ++n) {
       const int q = s + 2 * n;

@@ -57,7 +57,7 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], F2 k2, const 
           bf16_pair(SMALL ? floor_logit(raw[1][s + n]) : limit_r(raw[1][s + n], lim)));
       i[n] = exponent_of(bf16_pair(floor_logit(raw[2][s + n])));
     }
-    gates_n<SMALL, BATCH>(x, r, i, k2, em1 + s, nb + s, ns, ng);
+    gates_n<SMALL, true, BATCH>(x, r, i, k2, em1 + s, nb + s, ns, ng);
   }
 }
 // fp32 has one channel a lane: there the arithmetic pairs two steps
@@ -73,9 +73,9 @@ __device__ __forceinline__ void gates(const uint32_t (&raw)[3][S], float k2, con
       const int q = s + 2 * n;
       x[n] = f2(at(0, q), at(0, q + 1));
       r[n] = exponent_of(f2(limit_r(at(1, q), lim), limit_r(at(1, q + 1), lim)));
-      i[n] = exponent_of(f2(floor_logit(at(2, q)), floor_logit(at(2, q + 1))));
+      i[n] = exponent_of(f2(at(2, q), at(2, q + 1)));
     }
-    gates_n<SMALL, BATCH>(x, r, i, f2(k2), m, b, ns, ng);
+    gates_n<SMALL, false, BATCH>(x, r, i, f2(k2), m, b, ns, ng);
 #pragma unroll
     for (int n = 0; n < BATCH; ++n) {
       em1[s + 2 * n] = lo(m[n]), em1[s + 2 * n + 1] = hi(m[n]);

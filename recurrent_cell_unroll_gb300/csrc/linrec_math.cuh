@@ -45,15 +45,10 @@ __device__ __forceinline__ float rsq(float v) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-// minimum / maximum that keep a NaN
+// the minimum, which keeps a NaN
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
@@ -133,9 +128,12 @@ __device__ __forceinline__ bool small_rate(F2 k2) {
   return lo(k2) <= SMALL_RATE && hi(k2) <= SMALL_RATE;
 }
 
-// The two sigmoids share one reciprocal, of the product of their denominators:
+// bf16: the two sigmoids share one reciprocal, of the product of their denominators:
 // logits stop at -42, where e^42 = 2^60.6 keeps that product a normal number and
-// a sigmoid is 6e-19.  r above r_ceiling of its channel's rate, where a is 2^-90, is
+// a sigmoid is 6e-19, and a NaN in one gate reaches the other.  fp32, and the single
+// step, have a reciprocal for each, where e^inf = inf makes an infinite logit exact:
+// there it costs nothing (bf16 T=512 B=256 H=1024 forward 181 us with it, 174 without;
+// fp32 T=253 B=134 H=989 113 and 115).  r above r_ceiling of its channel's rate, where a is 2^-90, is
 // taken as that: what the state would still pass on is below any rounding, and
 // ex2m1 keeps its range (SMALL_RATE needs no ceiling).  A NaN stays one.  bf16
 // logits are limited as packed pairs, two at a time; a ceiling rounded to bf16 moves
@@ -145,7 +143,6 @@ __device__ __forceinline__ float r_ceiling(float k2) {
   const float s = 90.f / k2;  // sigmoid(r) at the limit
   return s < 1.f ? fmaxf(logf(s / (1.f - s)), LOGIT_FLOOR) : __int_as_float(0x7f800000);
 }
-__device__ __forceinline__ float floor_logit(float v) { return max_nan(v, LOGIT_FLOOR); }
 __device__ __forceinline__ uint32_t floor_logit(uint32_t v) {  // bf16 -42 = 0xc228
   uint32_t r;
   asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0xc228c228u));
@@ -155,7 +152,7 @@ struct Limits {
   float top;       // fp32: of the lane's channel
   uint32_t top2;   // bf16: of its two channels
 };
-__device__ __forceinline__ float limit_r(float v, const Limits &l) { return min_nan(floor_logit(v), l.top); }
+__device__ __forceinline__ float limit_r(float v, const Limits &l) { return min_nan(v, l.top); }
 __device__ __forceinline__ uint32_t limit_r(uint32_t v, const Limits &l) {
   uint32_t r;
   asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(floor_logit(v)), "r"(l.top2));
@@ -182,11 +179,12 @@ __device__ __forceinline__ float inv_beta(float w) { return rsq(w); }
 
 // Of N pairs of elements: em1 = a - 1, nb = -beta g x, and the sigmoids negated
 // (ns makes the decay's exponent k2 ns; the other signs cancel in products).  The
-// gates come as exponents, tr = -r log2(e) and ti likewise, of limited logits.
+// gates come as exponents, tr = -r log2(e) and ti likewise, of limited logits.  SMALL:
+// of rates up to SMALL_RATE; SHARED: with one reciprocal for both sigmoids.
 // Written stage by stage over the N pairs: each stage's operations are
 // independent, and a warp has few others to hide the latency of a chain of
 // twenty dependent ones behind.
-template <bool SMALL, int N>
+template <bool SMALL, bool SHARED, int N>
 __device__ __forceinline__ void gates_n(const F2 (&x)[N], const F2 (&tr)[N], const F2 (&ti)[N],
                                         F2 k2, F2 *em1, F2 *nb, F2 *ns, F2 *ng) {
   F2 pr[N], pi[N], t[N];
@@ -199,14 +197,16 @@ __device__ __forceinline__ void gates_n(const F2 (&x)[N], const F2 (&tr)[N], con
   for (int n = 0; n < N; ++n) {
     pr[n] = add2(pr[n], f2(1.f));
     pi[n] = add2(pi[n], f2(1.f));
-    t[n] = mul2(pr[n], pi[n]);
+    if (SHARED) t[n] = mul2(pr[n], pi[n]);
+  }
+  if (SHARED) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) t[n] = f2(rcp(-lo(t[n])), rcp(-hi(t[n])));
   }
 #pragma unroll
-  for (int n = 0; n < N; ++n) t[n] = f2(rcp(-lo(t[n])), rcp(-hi(t[n])));
-#pragma unroll
   for (int n = 0; n < N; ++n) {
-    ns[n] = mul2(t[n], pi[n]);
-    ng[n] = mul2(t[n], pr[n]);
+    ns[n] = SHARED ? mul2(t[n], pi[n]) : f2(rcp(-lo(pr[n])), rcp(-hi(pr[n])));
+    ng[n] = SHARED ? mul2(t[n], pr[n]) : f2(rcp(-lo(pi[n])), rcp(-hi(pi[n])));
     t[n] = mul2(k2, ns[n]);
   }
   if (SMALL) {

@@ -82,12 +82,12 @@ __global__ void __launch_bounds__(NT) linrec_step_kernel(const StepArgs a, int *
 #pragma unroll
         for (int j = 0; j < PAIRS; ++j) {
           vx[j] = f2(at(x[q], 2 * j), at(x[q], 2 * j + 1));
-          vr[j] = exponent_of(f2(min_nan(floor_logit(at(r[q], 2 * j)), top[2 * j]),
-                                 min_nan(floor_logit(at(r[q], 2 * j + 1)), top[2 * j + 1])));
-          vi[j] = exponent_of(f2(floor_logit(at(i[q], 2 * j)), floor_logit(at(i[q], 2 * j + 1))));
+          vr[j] = exponent_of(
+              f2(min_nan(at(r[q], 2 * j), top[2 * j]), min_nan(at(r[q], 2 * j + 1), top[2 * j + 1])));
+          vi[j] = exponent_of(f2(at(i[q], 2 * j), at(i[q], 2 * j + 1)));
           const F2 one_x[1] = {vx[j]}, one_r[1] = {vr[j]}, one_i[1] = {vi[j]};
-          gates_n<false, 1>(one_x, one_r, one_i, f2(k2[2 * j], k2[2 * j + 1]), em1 + j, nb + j,
-                            ns + j, ng + j);
+          gates_n<false, false, 1>(one_x, one_r, one_i, f2(k2[2 * j], k2[2 * j + 1]), em1 + j,
+                                   nb + j, ns + j, ng + j);
         }
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
