@@ -608,9 +608,21 @@ RCU_API int rcu_seq_last_launch_count(rcu_seq *h);
  *            steps 0, 64, 128, ..., which rcu_linrec_backward needs (of a
  *            chunk past a row's end: its last state).
  * T or B may be 0.  Long sequences of few channels are split over time;
- * results do not depend on anything but the inputs.  The decay is applied as
- * h + (a - 1) h, which keeps slow decays exact; an infinite state is NaN one
- * step later.
+ * results do not depend on anything but the inputs.
+ * Where fp32 or the kernels' arithmetic end:
+ *  - bf16: r and i below -42 are taken as -42, a sigmoid of 6e-19.  r = -inf
+ *    does not hold a state exactly but lets in sqrt(1.2e-18 c softplus(lambda))
+ *    of g x, some 1e-9 of it, and i = -inf lets in 6e-19 of x (an infinite x is
+ *    then infinite, not NaN).  In fp32, and in rcu_linrec_step, infinite logits
+ *    are exact.  A row's steps that are not to count are left out exactly by
+ *    its length, in either type (in rcu_linrec_step by slot -1).
+ *  - decays a below 1e-27 are taken as some 1e-27, and c softplus(lambda) above
+ *    6e19 as that.
+ *  - a - 1 is kept, not a, and the decay of a step is h + (a - 1) h; but across
+ *    groups of steps it is the fp32 product of their decays.  A decay within
+ *    some 3e-8 of 1 is lost there, as it is in one multiplication and addition
+ *    a step: after 9000 steps of a = 1 - 1.3e-8 a state is off by 1e-4.
+ *  - an infinite state is NaN one step later.
  */
 RCU_API int rcu_linrec_forward(rcu_seq *h, int dtype, int layout, int T, int B, int H,
                                const void *x, int64_t ldx, const void *r, int64_t ldr,
@@ -629,6 +641,9 @@ RCU_API int rcu_linrec_forward(rcu_seq *h, int dtype, int layout, int T, int B, 
  *   dx, dr, di  [T, B, H] of type dtype, each may be NULL; 0 past a row's end.
  *   dlambda  [H] fp32 or NULL: summed over steps and rows, in a fixed order.
  *   dh0      [B, H] fp32 or NULL.
+ * A NaN in r makes its channel's gradients of the row NaN at that step and at
+ * all before it, as by the formulas; in bf16 one in i does too (by the formulas
+ * it leaves the steps before it, as it does in fp32 and from 8 bits).
  */
 RCU_API int rcu_linrec_backward(rcu_seq *h, int dtype, int saved, int layout, int T, int B, int H,
                                 const void *x, int64_t ldx, const void *r, int64_t ldr,

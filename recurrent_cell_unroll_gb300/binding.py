@@ -699,7 +699,10 @@ class SeqOps:
     of any other layout as a contiguous copy.  Parameters, states and
     statistics are float32.  With ``stream`` the outputs are allocated for
     that stream, and work on it follows what it held before: a caller that
-    made an input on another stream orders the two.
+    made an input on another stream orders the two, and keeps the input until
+    the work is done (``Tensor.record_stream``).  One stream at a time uses a
+    SeqOps: its calls share a workspace, so calls that overlap on the GPU, on
+    two streams or in a replayed graph beside them, need one each.
     """
 
     _DTYPES = {torch.float32: RCU_F32, torch.bfloat16: RCU_BF16}

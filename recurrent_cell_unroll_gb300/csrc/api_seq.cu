@@ -1,6 +1,6 @@
 // Host side of the C ABI's sequence operators (include/rcu.h): the handle,
-// argument checks and the launches of the gated linear recurrence (linrec.cu),
-// layer norm (layernorm.cu) and 8-bit activation checkpoints (act8.cu).
+// argument checks and the launches of the gated linear recurrence (linrec_*.cu),
+// layer norm (layernorm_*.cu) and 8-bit activation checkpoints (act8.cu).
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

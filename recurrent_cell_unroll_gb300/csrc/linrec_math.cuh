@@ -9,7 +9,9 @@
 //   a h + b  =  h + (em1 h + b)        the decay keeps its relative precision
 //   w = 1 - a^2 = -em1 (2 + em1)       and so does the input's scale
 // An a rounded to fp32 has a step of 6e-8; times 2000 steps of memory that was
-// measured as an error of 7e-6 in dh0, against 1e-6 in this form.
+// measured as an error of 7e-6 in dh0, against 1e-6 in this form.  (The products of
+// several steps' decays are plain fp32: what is lost there shows where a state
+// remembers for millions of steps.)
 //
 // The forward in bf16 moves 8 bytes an element, which leaves an SM about 0.34
 // cycles for it, or 43 issue slots: every operation counts.  So arithmetic runs

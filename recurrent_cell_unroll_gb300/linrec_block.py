@@ -72,7 +72,9 @@ class _Recurrence(torch.autograd.Function):
 
 class LinRecStack:
     """`layers` blocks of width `dim`, the recurrence `hidden` wide, over [T, B,
-    dim] sequences; parameters as torch leaves (float32; products in `dtype`)."""
+    dim] sequences; parameters as torch leaves (float32; products in `dtype`).
+    One stream at a time uses a stack: its calls share the workspace of its SeqOps.
+    Its gradients can be differentiated once."""
 
     def __init__(self, layers: int, dim: int, hidden: int, dtype=torch.bfloat16, seed: int = 0,
                  device="cuda"):
