@@ -722,6 +722,186 @@ RCU_API int rcu_act8_pack(rcu_seq *h, int dtype, int64_t rows, int n, const void
 RCU_API int rcu_act8_unpack(rcu_seq *h, int dtype, int64_t rows, int n, const int8_t *codes,
                             int64_t ldc, const int8_t *exps, void *y, int64_t ldy, void *stream);
 
+/* ------------------------------------------------------------------------ */
+/* Selective state space blocks: short causal convolution and selective scan  */
+/* ------------------------------------------------------------------------ */
+
+/* Taps of a short convolution and states of a scan's channel, at most. */
+#define RCU_CONV_MAX_TAPS 8
+#define RCU_SELSCAN_MAX_STATES 64
+
+/*
+ * Short causal convolution along time, a channel by itself, for t < lengths[b]:
+ *   v_t = bias + sum over k < W of weight[k] * x_{t - W + 1 + k},  y = v, or
+ *   silu(v) = v sigmoid(v) if `silu` is not 0.
+ *   x, y     [T, B, H] in `layout`, of type dtype.
+ *   weight   [H, W] fp32, 1 <= W <= RCU_CONV_MAX_TAPS; the last tap meets the
+ *            current input.  bias [H] fp32 or NULL (0).
+ *   lengths  as for rcu_linrec_forward: y is 0 at t >= lengths[b], the inputs
+ *            there are not used.
+ *   state    [B, W - 1, H] of type dtype or NULL (zeros): the inputs before x,
+ *            oldest first.
+ *   state_n  [B, W - 1, H] of type dtype or NULL: the last W - 1 inputs of each
+ *            row, those of `state` among them where the row is shorter.  May be
+ *            `state` itself.
+ * T or B may be 0.  Sums are fp32.  Of these operators and the scans, B * H and T * B are at most 2^29;
+ * more is RCU_ERR_UNSUPPORTED.
+ */
+RCU_API int rcu_conv_forward(rcu_seq *h, int dtype, int layout, int T, int B, int H, int W,
+                             const void *x, int64_t ldx, const float *weight, const float *bias,
+                             int silu, const int32_t *lengths, const void *state, void *y,
+                             int64_t ldy, void *state_n, void *stream);
+
+/*
+ * Backward pass of rcu_conv_forward, from its inputs.
+ *   dy, dx    [T, B, H] of type dtype; dx is 0 past a row's end.
+ *   dstate_n  [B, W - 1, H] of type dtype or NULL (0): the gradient reaching
+ *             state_n.  dstate [B, W - 1, H] of type dtype or NULL, another tensor.
+ *   dweight [H, W], dbias [H] fp32, each may be NULL; summed in a fixed order.
+ */
+RCU_API int rcu_conv_backward(rcu_seq *h, int dtype, int layout, int T, int B, int H, int W,
+                              const void *x, int64_t ldx, const float *weight, const float *bias,
+                              int silu, const int32_t *lengths, const void *state, const void *dy,
+                              int64_t lddy, const void *dstate_n, void *dx, int64_t lddx,
+                              float *dweight, float *dbias, void *dstate, void *stream);
+
+/*
+ * One step of the convolution for B requests: x, y [B, H]; state [slots, W - 1, H]
+ * of type dtype is shifted by x in place.  slot as for rcu_linrec_step.
+ */
+RCU_API int rcu_conv_step(rcu_seq *h, int dtype, int B, int H, int W, const void *x, int64_t ldx,
+                          const float *weight, const float *bias, int silu, void *state, int slots,
+                          const int32_t *slot, void *y, int64_t ldy, void *stream);
+
+/* Steps between the states rcu_selscan_forward keeps for the backward pass. */
+#define RCU_SELSCAN_CHUNK 32
+
+/*
+ * Selective scan: a linear recurrence of N states a channel whose step size,
+ * input and output weights are inputs of every step.  For t < lengths[b]:
+ *   delta = softplus(dt_t + dt_bias),  A = -exp(a_log)
+ *   h_t[n] = exp(delta A[n]) h_{t-1}[n] + delta x_t b_t[n]
+ *   s_t = sum over n of c_t[n] h_t[n] + d x_t,   y_t = s_t, or s_t silu(z_t)
+ *   x, dt, z, y  [T, B, H] in `layout`, of type dtype; z may be NULL (no gate).
+ *   b, c     [T, B, N] in `layout`, of type dtype, the same for all channels;
+ *            1 <= N <= RCU_SELSCAN_MAX_STATES.
+ *   a_log    [H, N] fp32; d, dt_bias [H] fp32, each may be NULL (0).
+ *   lengths  as for rcu_linrec_forward: y is 0 at t >= lengths[b], the inputs
+ *            there are not used and the states stay.
+ *   h0       [B, H, N] fp32 or NULL (zeros); h_n [B, H, N] fp32 or NULL: the
+ *            states after each row's last step.
+ *   states   [ceil(T / RCU_SELSCAN_CHUNK), B, H, N] fp32 or NULL: the states
+ *            before steps 0, 32, 64, ..., which rcu_selscan_backward needs (of
+ *            a chunk past a row's end: its last states).
+ * T or B may be 0.  Long sequences of few channels are split over time; results
+ * do not depend on anything but the inputs.  States and sums are fp32; an
+ * exponential of base 2 is the hardware's (2 units in the last place).
+ * An infinite x (or b) makes its channel's states infinite, and NaN where a
+ * product with 0 meets them.
+ */
+RCU_API int rcu_selscan_forward(rcu_seq *h, int dtype, int layout, int T, int B, int H, int N,
+                                const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                                const float *a_log, const void *b, int64_t ldb, const void *c,
+                                int64_t ldc, const float *d, const float *dt_bias, const void *z,
+                                int64_t ldz, const int32_t *lengths, const float *h0, void *y,
+                                int64_t ldy, float *h_n, float *states, void *stream);
+
+/*
+ * Backward pass of rcu_selscan_forward, from its inputs and its states.
+ *   dy [T, B, H] of type dtype; dh_n [B, H, N] fp32 or NULL (0).
+ *   dx, ddt, dz [T, B, H], db, dc [T, B, N] of type dtype, each may be NULL; 0
+ *   past a row's end (dz only with a z).  da_log [H, N], dd (only with a d),
+ *   ddt_bias [H], dh0 [B, H, N] fp32, each may be NULL.  Sums over steps, rows and channels are fp32 in a fixed order.
+ */
+RCU_API int rcu_selscan_backward(rcu_seq *h, int dtype, int layout, int T, int B, int H, int N,
+                                 const void *x, int64_t ldx, const void *dt, int64_t lddt,
+                                 const float *a_log, const void *b, int64_t ldb, const void *c,
+                                 int64_t ldc, const float *d, const float *dt_bias, const void *z,
+                                 int64_t ldz, const int32_t *lengths, const float *states,
+                                 const void *dy, int64_t lddy, const float *dh_n, void *dx,
+                                 int64_t lddx, void *ddt, int64_t ldddt, float *da_log, void *db,
+                                 int64_t lddb, void *dc, int64_t lddc, float *dd, float *ddt_bias,
+                                 void *dz, int64_t lddz, float *dh0, void *stream);
+
+/*
+ * One step of the scan for B requests: x, dt, z, y [B, H]; b, c [B, N]; state
+ * [slots, H, N] fp32 is updated in place.  slot as for rcu_linrec_step.
+ */
+RCU_API int rcu_selscan_step(rcu_seq *h, int dtype, int B, int H, int N, const void *x,
+                             int64_t ldx, const void *dt, int64_t lddt, const float *a_log,
+                             const void *b, int64_t ldb, const void *c, int64_t ldc, const float *d,
+                             const float *dt_bias, const void *z, int64_t ldz, float *state,
+                             int slots, const int32_t *slot, void *y, int64_t ldy, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* AdamW over many tensors                                                    */
+/* ------------------------------------------------------------------------ */
+
+/* Values of an 8-bit optimizer state that share an exponent. */
+#define RCU_STATE8_BLOCK 64
+
+/*
+ * One tensor of a step: n values of parameter p (type p_type) with gradient g
+ * (type g_type), RCU_F32 or RCU_BF16 each, and its two states, either fp32 m and v
+ * [n] (m_exp, v_exp NULL) or 8-bit ones: int8 codes m and v [n] with exponents
+ * m_exp, v_exp int8 [ceil(n / 64)].  copy: NULL, or bf16 [n] that receives the
+ * new parameter rounded (for fp32 p).  All are dense.  An n of 0 is left out.
+ */
+typedef struct rcu_adamw_tensor {
+  void *p;
+  const void *g;
+  void *m, *v;
+  int8_t *m_exp, *v_exp;
+  void *copy;
+  int64_t n;
+  int32_t p_type, g_type;
+} rcu_adamw_tensor;
+
+/*
+ * One AdamW step (decoupled weight decay, bias correction) of `count` tensors;
+ * `tensors` is host memory, read before the call returns.  In fp32, each
+ * product, sum and quotient of m and v rounded by itself:
+ *   g' = g * scale
+ *   m = m * beta1 + g' * (1 - beta1),   v = v * beta2 + (g' * (1 - beta2)) * g'
+ *   p = p * (1 - lr weight_decay)
+ *       - m / (sqrt(v) / sqrt(1 - beta2^step) + eps) * (lr / (1 - beta1^step))
+ * The new p is rounded to the nearest of its type.  p, m and v are updated in place.
+ *   scale     NULL (1) or a device fp32 number, of gradient clipping or loss scaling.
+ *   step      >= 1, or, with step_dev, a device int32 that is read instead; lr_dev:
+ *             a device fp32 number that is read in lr's place (NULL: lr).  With these
+ *             a captured step follows both.
+ *   seed      its low 32 bits: of the rounding of 8-bit states.
+ *   0 <= beta1, beta2 < 1; eps >= 0.
+ *
+ * 8-bit states: a block of 64 values has the exponent e, that of its largest
+ * finite magnitude, held in [-126, 126].  With f = |value| 2^-e and an offset o,
+ * 2^-14 for m and 2^-30 for v, f + o is rounded to three bits behind its leading
+ * one, and the code counts such steps above o: steps of a 16th to an 8th of f
+ * where f is far above o, of o / 8 below.  m's code is an int8 with the value's
+ * sign (127 at most); v's is the count less 128, 254 - 128 at most, and a v above 0
+ * is never held as 0.  m's code -128 and v's 127 stand for what is not finite and
+ * come back as NaN.  Rounding is up or down at random, so that changes smaller than a
+ * step are kept on average: 16 bits behind the cut are compared with those of
+ *   mix(mix(mix(seed + 0x9e3779b9 step) + tensor's place in the list) ^ index),
+ * the low half of the word for m, the high half for v, where mix is x ^= x >> 16,
+ * x *= 0x7feb352d, x ^= x >> 15, x *= 0x846ca68b, x ^= x >> 16 on 32 bits.  A tensor
+ * has at most 2^32 values with 8-bit states and 2^40 else; `count` is at most 2^24.
+ */
+RCU_API int rcu_adamw_step(rcu_seq *h, int64_t count, const rcu_adamw_tensor *tensors, double lr,
+                           double beta1, double beta2, double eps, double weight_decay,
+                           int64_t step, int64_t seed, const float *scale,
+                           const int32_t *step_dev, const float *lr_dev, void *stream);
+
+/*
+ * 8-bit optimizer states on their own, codes [n] and exps [ceil(n / 64)]: packing
+ * rounds to the nearest code (the upper one of two as near); `is_signed` 0: the format of v,
+ * whose negative values are taken as 0.
+ */
+RCU_API int rcu_state8_pack(rcu_seq *h, int is_signed, int64_t n, const float *x, int8_t *codes,
+                            int8_t *exps, void *stream);
+RCU_API int rcu_state8_unpack(rcu_seq *h, int is_signed, int64_t n, const int8_t *codes,
+                              const int8_t *exps, float *y, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

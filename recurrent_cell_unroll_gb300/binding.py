@@ -33,6 +33,7 @@ RCU_CLIP_CELL, RCU_CLIP_PROJ = 0, 1
 RCU_ATTR_HOST_CHUNKS, RCU_MAX_HOST_CHUNKS = 8, 16
 RCU_TIME_FIRST, RCU_BATCH_FIRST = 0, 1
 RCU_LINREC_CHUNK, RCU_ACT8_BLOCK = 64, 64
+RCU_CONV_MAX_TAPS, RCU_SELSCAN_MAX_STATES, RCU_SELSCAN_CHUNK, RCU_STATE8_BLOCK = 8, 64, 32, 64
 
 EXPORTED = (
     "rcu_last_error", "rcu_version", "rnn_create", "rnn_set_weights", "rnn_forward",
@@ -49,6 +50,9 @@ EXPORTED = (
     "rcu_seq_profile_entry", "rcu_seq_profile_reset", "rcu_seq_last_launch_count",
     "rcu_linrec_forward", "rcu_linrec_backward", "rcu_linrec_step", "rcu_layernorm_forward",
     "rcu_layernorm_backward", "rcu_act8_pack", "rcu_act8_unpack",
+    "rcu_conv_forward", "rcu_conv_backward", "rcu_conv_step", "rcu_selscan_forward",
+    "rcu_selscan_backward", "rcu_selscan_step", "rcu_adamw_step", "rcu_state8_pack",
+    "rcu_state8_unpack",
 )
 
 _lib = None
@@ -127,6 +131,20 @@ def signatures() -> dict:
                                        P, P, P]),
         "rcu_act8_pack": (I, [P, I, I64, I, P, I64, P, I64, P, P]),
         "rcu_act8_unpack": (I, [P, I, I64, I, P, I64, P, P, I64, P]),
+        "rcu_conv_forward": (I, [P, I, I, I, I, I, I, P, I64, P, P, I, P, P, P, I64, P, P]),
+        "rcu_conv_backward": (I, [P, I, I, I, I, I, I, P, I64, P, P, I, P, P, P, I64, P, P, I64, P,
+                                  P, P, P]),
+        "rcu_conv_step": (I, [P, I, I, I, I, P, I64, P, P, I, P, I, P, P, I64, P]),
+        "rcu_selscan_forward": (I, [P, I, I, I, I, I, I] + [P, I64] * 2 + [P] + [P, I64] * 2
+                                + [P, P, P, I64, P, P, P, I64, P, P, P]),
+        "rcu_selscan_backward": (I, [P, I, I, I, I, I, I] + [P, I64] * 2 + [P] + [P, I64] * 2
+                                 + [P, P, P, I64, P, P, P, I64, P, P, I64, P, I64, P, P, I64, P,
+                                    I64, P, P, P, I64, P, P]),
+        "rcu_selscan_step": (I, [P, I, I, I, I] + [P, I64] * 2 + [P] + [P, I64] * 2
+                             + [P, P, P, I64, P, I, P, P, I64, P]),
+        "rcu_adamw_step": (I, [P, I64, P, D, D, D, D, D, I64, I64, P, P, P, P]),
+        "rcu_state8_pack": (I, [P, I, I64, P, P, P, P]),
+        "rcu_state8_unpack": (I, [P, I, I64, P, P, P, P]),
     }
 
 
@@ -975,6 +993,287 @@ class SeqOps:
         y = torch.empty(shape, dtype=dtype, device=codes.device)
         _check(self.lib.rcu_act8_unpack(self.h, dt, rows, n, cp, cl, ep, y.data_ptr(), n,
                                         self._raw_stream()))
+        return y
+
+    # ---- short causal convolution
+
+    def conv_forward(self, x, weight, bias=None, silu=True, lengths=None, state=None,
+                     batch_first=False, stream=None):
+        """(y, state_n) of x [T, B, H] (batch_first: [B, T, H]) with weight
+        [H, W] and bias [H]; state, state_n [B, W - 1, H] of x's type: the
+        inputs before x, and the last ones of each row."""
+        if stream is not None:
+            return self._on_stream(stream, self.conv_forward, x, weight, bias, silu, lengths, state,
+                                   batch_first)
+        dtype, dt, shape = self._type(x, "x", 3)
+        T, B, H = shape
+        if batch_first:
+            T, B = B, T
+        W, wide = self._taps(weight, B, H)
+        keep, f32, dev = [], torch.float32, x.device
+        xp, xl = self._rows(x, "x", dtype, shape, keep)
+        wp = self._dense(weight, "weight", f32, (H, W), keep)
+        bp = self._dense(bias, "bias", f32, (H,), keep)
+        np_ = self._dense(lengths, "lengths", torch.int32, (B,), keep)
+        sp = self._dense(state, "state", dtype, wide, keep)
+        y = torch.empty(shape, dtype=dtype, device=dev)
+        state_n = torch.empty(wide, dtype=dtype, device=dev)
+        _check(self.lib.rcu_conv_forward(
+            self.h, dt, 1 if batch_first else 0, T, B, H, W, xp, xl, wp, bp, 1 if silu else 0, np_,
+            sp, y.data_ptr(), H, state_n.data_ptr(), self._raw_stream()))
+        return y, state_n
+
+    def conv_backward(self, dy, x, weight, bias=None, silu=True, lengths=None, state=None,
+                      dstate_n=None, batch_first=False, stream=None):
+        """(dx, dweight, dbias, dstate), from the forward's inputs; dstate_n:
+        the gradient reaching its state_n."""
+        if stream is not None:
+            return self._on_stream(stream, self.conv_backward, dy, x, weight, bias, silu, lengths,
+                                   state, dstate_n, batch_first)
+        dtype, dt, shape = self._type(x, "x", 3)
+        T, B, H = shape
+        if batch_first:
+            T, B = B, T
+        W, wide = self._taps(weight, B, H)
+        keep, f32, dev = [], torch.float32, x.device
+        xp, xl = self._rows(x, "x", dtype, shape, keep)
+        yp, yl = self._rows(dy, "dy", dtype, shape, keep)
+        wp = self._dense(weight, "weight", f32, (H, W), keep)
+        bp = self._dense(bias, "bias", f32, (H,), keep)
+        np_ = self._dense(lengths, "lengths", torch.int32, (B,), keep)
+        sp = self._dense(state, "state", dtype, wide, keep)
+        dp = self._dense(dstate_n, "dstate_n", dtype, wide, keep)
+        dx = torch.empty(shape, dtype=dtype, device=dev)
+        dw = torch.empty((H, W), dtype=f32, device=dev)
+        db = torch.empty((H,), dtype=f32, device=dev)
+        ds = torch.empty(wide, dtype=dtype, device=dev)
+        _check(self.lib.rcu_conv_backward(
+            self.h, dt, 1 if batch_first else 0, T, B, H, W, xp, xl, wp, bp, 1 if silu else 0, np_,
+            sp, yp, yl, dp, dx.data_ptr(), H, dw.data_ptr(), db.data_ptr(), ds.data_ptr(),
+            self._raw_stream()))
+        return dx, dw, db, ds
+
+    def conv_step(self, x, weight, state, bias=None, silu=True, slot=None, stream=None):
+        """y [B, H] of one step of B requests; state [slots, W - 1, H] of x's
+        type is shifted in place, at slot[b] (int32 [B], -1: takes no part;
+        None: row b)."""
+        if stream is not None:
+            return self._on_stream(stream, self.conv_step, x, weight, state, bias, silu, slot)
+        dtype, dt, shape = self._type(x, "x", 2)
+        B, H = shape
+        keep, f32 = [], torch.float32
+        slots = self._table(state, "state", 3)
+        W, wide = self._taps(weight, slots, H)
+        xp, xl = self._rows(x, "x", dtype, shape, keep)
+        wp = self._dense(weight, "weight", f32, (H, W), keep)
+        bp = self._dense(bias, "bias", f32, (H,), keep)
+        sp = self._dense(state, "state", dtype, wide, keep)
+        tp = self._dense(slot, "slot", torch.int32, (B,), keep)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+        # (a table of W - 1 = 0 rows has no address)
+        _check(self.lib.rcu_conv_step(self.h, dt, B, H, W, xp, xl, wp, bp, 1 if silu else 0,
+                                      sp or wp, slots, tp, y.data_ptr(), H, self._raw_stream()))
+        return y
+
+    def _taps(self, weight, rows, H):
+        """(W, the shape of `rows` states) of a convolution's weight."""
+        if not isinstance(weight, torch.Tensor) or weight.dim() != 2 or weight.shape[1] < 1:
+            raise ValueError("weight must be an [H, W] tensor, W >= 1")
+        W = weight.shape[1]
+        return W, (rows, W - 1, H)
+
+    def _table(self, state, name, dims):
+        """Slots of a table of states that a call updates in place."""
+        if not isinstance(state, torch.Tensor) or state.dim() != dims or not state.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of {dims} dimensions")
+        return state.shape[0]
+
+    # ---- selective scan
+
+    def _scan_args(self, x, dt, a_log, b, c, d, dt_bias, z, lengths, T, B, dtype, shape, keep):
+        """(N, the pointers and strides that both passes take up to the lengths)."""
+        f32, H = torch.float32, shape[-1]
+        if not isinstance(a_log, torch.Tensor) or a_log.dim() != 2 or a_log.shape[1] < 1:
+            raise ValueError("a_log must be an [H, N] tensor, N >= 1")
+        N = a_log.shape[1]
+        narrow = (*shape[:-1], N)
+        zp, zl = self._rows(z, "z", dtype, shape, keep) if z is not None else (None, 0)
+        return N, (*self._rows(x, "x", dtype, shape, keep), *self._rows(dt, "dt", dtype, shape, keep),
+                   self._dense(a_log, "a_log", f32, (H, N), keep),
+                   *self._rows(b, "b", dtype, narrow, keep), *self._rows(c, "c", dtype, narrow, keep),
+                   self._dense(d, "d", f32, (H,), keep), self._dense(dt_bias, "dt_bias", f32, (H,), keep),
+                   zp, zl, self._dense(lengths, "lengths", torch.int32, (B,), keep))
+
+    def selscan_forward(self, x, dt, a_log, b, c, d=None, dt_bias=None, z=None, lengths=None,
+                        h0=None, batch_first=False, states=False, stream=None):
+        """y, h_n [B, H, N] and, with states=True, what selscan_backward needs
+        (else None).  x, dt, z: [T, B, H] (batch_first: [B, T, H]); b, c: the
+        same with N in the place of H; a_log [H, N]; d, dt_bias [H]; lengths
+        int32 [B]; h0 [B, H, N]."""
+        if stream is not None:
+            return self._on_stream(stream, self.selscan_forward, x, dt, a_log, b, c, d, dt_bias, z,
+                                   lengths, h0, batch_first, states)
+        dtype, ty, shape = self._type(x, "x", 3)
+        T, B, H = shape
+        if batch_first:
+            T, B = B, T
+        keep, f32, dev = [], torch.float32, x.device
+        N, args = self._scan_args(x, dt, a_log, b, c, d, dt_bias, z, lengths, T, B, dtype, shape, keep)
+        hp = self._dense(h0, "h0", f32, (B, H, N), keep)
+        y = torch.empty(shape, dtype=dtype, device=dev)
+        h_n = torch.empty((B, H, N), dtype=f32, device=dev)
+        st = torch.empty((-(-T // RCU_SELSCAN_CHUNK), B, H, N), dtype=f32, device=dev) if states \
+            else None
+        _check(self.lib.rcu_selscan_forward(
+            self.h, ty, 1 if batch_first else 0, T, B, H, N, *args, hp, y.data_ptr(), H,
+            h_n.data_ptr(), st.data_ptr() if states else None, self._raw_stream()))
+        return y, h_n, st
+
+    def selscan_backward(self, dy, x, dt, a_log, b, c, states, d=None, dt_bias=None, z=None,
+                         lengths=None, dh_n=None, batch_first=False, stream=None):
+        """A dict of the gradients: dx, ddt, db, dc, dz (of dy's type), da_log,
+        dd, ddt_bias and dh0 (float32); None where there is no such input
+        (d, dt_bias, z).  Takes the forward's inputs and states."""
+        if stream is not None:
+            return self._on_stream(stream, self.selscan_backward, dy, x, dt, a_log, b, c, states, d,
+                                   dt_bias, z, lengths, dh_n, batch_first)
+        dtype, ty, shape = self._type(dy, "dy", 3)
+        T, B, H = shape
+        if batch_first:
+            T, B = B, T
+        keep, f32, dev = [], torch.float32, dy.device
+        N, args = self._scan_args(x, dt, a_log, b, c, d, dt_bias, z, lengths, T, B, dtype, shape, keep)
+        sp = self._dense(states, "states", f32, (-(-T // RCU_SELSCAN_CHUNK), B, H, N), keep)
+        yp, yl = self._rows(dy, "dy", dtype, shape, keep)
+        hp = self._dense(dh_n, "dh_n", f32, (B, H, N), keep)
+
+        def make(there, *size, dtype=dtype):
+            return torch.empty(size, dtype=dtype, device=dev) if there else None
+        g = {"dx": make(True, *shape), "ddt": make(True, *shape), "db": make(True, *shape[:-1], N),
+             "dc": make(True, *shape[:-1], N), "dz": make(z is not None, *shape),
+             "da_log": make(True, H, N, dtype=f32), "dd": make(d is not None, H, dtype=f32),
+             "ddt_bias": make(dt_bias is not None, H, dtype=f32), "dh0": make(True, B, H, N, dtype=f32)}
+        at = {k: t.data_ptr() if t is not None else None for k, t in g.items()}
+        _check(self.lib.rcu_selscan_backward(
+            self.h, ty, 1 if batch_first else 0, T, B, H, N, *args, sp, yp, yl, hp, at["dx"], H,
+            at["ddt"], H, at["da_log"], at["db"], N, at["dc"], N, at["dd"], at["ddt_bias"], at["dz"],
+            H, at["dh0"], self._raw_stream()))
+        return g
+
+    def selscan_step(self, x, dt, a_log, b, c, state, d=None, dt_bias=None, z=None, slot=None,
+                     stream=None):
+        """y [B, H] of one step of B requests (x, dt, z [B, H]; b, c [B, N]);
+        state [slots, H, N] is updated in place, slots as in conv_step."""
+        if stream is not None:
+            return self._on_stream(stream, self.selscan_step, x, dt, a_log, b, c, state, d, dt_bias,
+                                   z, slot)
+        dtype, ty, shape = self._type(x, "x", 2)
+        B, H = shape
+        keep = []
+        slots = self._table(state, "state", 3)
+        N, args = self._scan_args(x, dt, a_log, b, c, d, dt_bias, z, None, 1, B, dtype, shape, keep)
+        sp = self._dense(state, "state", torch.float32, (slots, H, N), keep)
+        tp = self._dense(slot, "slot", torch.int32, (B,), keep)
+        y = torch.empty(shape, dtype=dtype, device=x.device)
+        _check(self.lib.rcu_selscan_step(self.h, ty, B, H, N, *args[:-1], sp, slots, tp,
+                                         y.data_ptr(), H, self._raw_stream()))
+        return y
+
+    # ---- AdamW
+
+    def adamw_step(self, params, grads, m, v, step, lr=1e-3, betas=(0.9, 0.999), eps=1e-8,
+                   weight_decay=0.01, scale=None, seed=0, copies=None, stream=None):
+        """One step of lists of tensors, in place.  params, grads: float32 or
+        bfloat16 (a grad of None leaves its tensor out); m, v: float32 tensors
+        like the parameters, or 8-bit states (codes int8 like the parameter,
+        exponents int8 [ceil(n / 64)]), of both alike.  step (from 1) and lr
+        are numbers, or tensors of one int32 and one float32 on the device,
+        which a captured step then follows; scale: a float32 on the device that
+        gradients are multiplied by; seed: of the 8-bit states' rounding.
+        copies: bfloat16 tensors (or None) that receive the new parameters.
+        All tensors are contiguous."""
+        if stream is not None:
+            return self._on_stream(stream, self.adamw_step, params, grads, m, v, step, lr, betas, eps,
+                                   weight_decay, scale, seed, copies)
+        count = len(params)
+        if not (len(grads) == len(m) == len(v) == count) or (copies is not None
+                                                            and len(copies) != count):
+            raise ValueError("params, grads, m, v and copies must be lists of one length")
+        f32, bf16, types, device, keep = torch.float32, torch.bfloat16, self._DTYPES, self.device, []
+
+        def dense(t, name, k, like, dtype=None):
+            if (isinstance(t, torch.Tensor) and t.get_device() == device and t.is_contiguous()
+                    and t.shape == like.shape and (t.dtype in types if dtype is None
+                                                   else t.dtype is dtype)):
+                return t.data_ptr()
+            raise ValueError(f"{name}[{k}] must be a contiguous tensor on cuda:{device} of shape "
+                             f"{list(like.shape)} and type {dtype or 'float32 or bfloat16'}")
+
+        rows = []
+        for k, (p, g, mk, vk) in enumerate(zip(params, grads, m, v)):
+            if not isinstance(p, torch.Tensor):
+                raise ValueError(f"params[{k}] must be a tensor")
+            if g is None:
+                rows += (None, None, None, None, None, None, None, 0, 0)
+                continue
+            me = ve = None
+            at_p, at_g, n = dense(p, "params", k, p), dense(g, "grads", k, p), p.numel()
+            if isinstance(mk, torch.Tensor) and isinstance(vk, torch.Tensor):
+                at_m, at_v = dense(mk, "m", k, p, f32), dense(vk, "v", k, p, f32)
+            else:
+                if isinstance(mk, torch.Tensor) or isinstance(vk, torch.Tensor):
+                    raise ValueError(f"m[{k}] and v[{k}] must be held alike")
+                (mk, me), (vk, ve) = mk, vk
+                at_m, at_v = dense(mk, "m", k, p, torch.int8), dense(vk, "v", k, p, torch.int8)
+                exps = (-(-n // RCU_STATE8_BLOCK),)
+                for t in (me, ve):
+                    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int8 and t.shape == exps
+                            and t.get_device() == device and t.is_contiguous()):
+                        raise ValueError(f"exponents of m[{k}] and v[{k}] must be contiguous int8 "
+                                         f"{list(exps)} on cuda:{device}")
+                me, ve = me.data_ptr(), ve.data_ptr()
+            low = copies[k] if copies is not None else None
+            low = dense(low, "copies", k, p, bf16) if low is not None else None
+            rows += (at_p, at_g, at_m, at_v, me, ve, low, n, types[p.dtype] | types[g.dtype] << 32)
+        table = (ctypes.c_int64 * len(rows))(*[r or 0 for r in rows])
+        on_dev = [None, None, None]
+        for q, (t, dtype, name) in enumerate(((scale, f32, "scale"), (step, torch.int32, "step"),
+                                              (lr, f32, "lr"))):
+            if isinstance(t, torch.Tensor):
+                on_dev[q] = self._dense(t.reshape(-1) if t.dim() != 1 else t, name, dtype, (1,), keep)
+            elif q == 0 and t is not None:
+                raise ValueError("scale must be a tensor on a CUDA device")
+        _check(self.lib.rcu_adamw_step(
+            self.h, count, ctypes.addressof(table), 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
+            weight_decay, 1 if on_dev[1] else step, seed & 0xffffffff, *on_dev, self._raw_stream()))
+
+    def state8_pack(self, x, signed, stream=None):
+        """(codes like x, exponents [ceil(n / 64)]) of an 8-bit optimizer state:
+        signed for m, not for v; to the nearest code."""
+        if stream is not None:
+            return self._on_stream(stream, self.state8_pack, x, signed)
+        if not isinstance(x, torch.Tensor):
+            raise ValueError("x must be a tensor on a CUDA device")
+        keep, n = [], x.numel()
+        xp = self._dense(x, "x", torch.float32, x.shape, keep)
+        codes = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        exps = torch.empty((-(-n // RCU_STATE8_BLOCK),), dtype=torch.int8, device=x.device)
+        _check(self.lib.rcu_state8_pack(self.h, 1 if signed else 0, n, xp, codes.data_ptr(),
+                                        exps.data_ptr(), self._raw_stream()))
+        return codes, exps
+
+    def state8_unpack(self, codes, exps, signed, stream=None):
+        """The values that an 8-bit optimizer state stands for, float32."""
+        if stream is not None:
+            return self._on_stream(stream, self.state8_unpack, codes, exps, signed)
+        if not isinstance(codes, torch.Tensor):
+            raise ValueError("codes must be a tensor on a CUDA device")
+        keep, n = [], codes.numel()
+        cp = self._dense(codes, "codes", torch.int8, codes.shape, keep)
+        ep = self._dense(exps, "exps", torch.int8, (-(-n // RCU_STATE8_BLOCK),), keep)
+        y = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
+        _check(self.lib.rcu_state8_unpack(self.h, 1 if signed else 0, n, cp, ep, y.data_ptr(),
+                                          self._raw_stream()))
         return y
 
     # ---- handle
