@@ -4,12 +4,12 @@
 //   h_t[n] = 2^(delta A2[n]) h_{t-1}[n] + (delta x_t) b_t[n]
 //
 // The work is N exponentials and some 4 N products a step and channel against 8
-// bytes moved in bf16, so the arithmetic units bound it, not the memory.  A thread
-// keeps 8 states of a channel in registers, and LANES = N / 8 threads that stand
-// side by side in a warp make up the channel; what does not depend on the state
-// (softplus, gates) is computed once for a tile of TILE steps and put into shared
-// memory, as are the tile's rows of b and c, which all channels read.  States are
-// computed as packed pairs.
+// bytes moved in bf16, so the arithmetic units bound it, not the memory: the special
+// function unit (32 exponentials a cycle and SM) and the issue of instructions.  So
+// states are worked on as packed pairs, of two neighbouring channels: the pair's
+// steps and inputs then lie beside one another, and what all channels share (b, c) is
+// laid out twice.  What does not depend on the state (softplus, gates) is computed
+// once for a tile of steps, in shared memory.
 //
 // Long sequences of few channels are split over time into segments: a first
 // kernel finds each segment's last states from states of 0 and its sum of delta
@@ -28,16 +28,30 @@ namespace selscan {
 
 using namespace ssm;
 
-constexpr int S = 8;                       // states of a thread
-constexpr int TILE = RCU_SELSCAN_CHUNK;    // steps of a tile
+constexpr int CHUNK = RCU_SELSCAN_CHUNK;  // steps between kept states
 
-// ln(1 + e) for 0 <= e <= 1 with its relative precision.
-__device__ __forceinline__ float log1p_small(float e) { return log1pf(e); }
-// softplus(v) = max(v, 0) + ln(1 + e^-|v|)
-__device__ __forceinline__ float softplus(float v) {
-  float top;  // not fmaxf, which drops a NaN
-  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(top) : "f"(v));
-  return top + log1p_small(ex2(-LOG2E * fabsf(v)));
+__device__ __forceinline__ float max0(float v) {  // not fmaxf, which drops a NaN
+  float r;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+  return r;
+}
+// softplus(v) = max(v, 0) + ln(1 + e), e = e^-|v|, with the relative precision of
+// its small values: ln(1 + e) = s p(s^2), s = e / (2 + e), p a polynomial fitted to
+// 2 artanh(s) / s over 0 <= s <= 1/3 with the least relative error (4e-9; 2e-7 as
+// rounded).
+__device__ __forceinline__ F2 softplus(F2 v) {
+  const F2 e = f2(ex2(-LOG2E * fabsf(lo(v))), ex2(-LOG2E * fabsf(hi(v))));
+  const F2 d = add2(e, f2(2.f)), s = mul2(e, f2(rcp(lo(d)), rcp(hi(d)))), q = mul2(s, s);
+  F2 p = f2(0.2817833423614502f);
+  p = fma2(p, q, f2(0.27960601449012756f));
+  p = fma2(p, q, f2(0.40024909377098083f));
+  p = fma2(p, q, f2(0.6666631698608398f));
+  p = fma2(p, q, f2(2.f));
+  return fma2(s, p, f2(max0(lo(v)), max0(hi(v))));
+}
+__device__ __forceinline__ float softplus(float v) { return lo(softplus(f2(v, v))); }
+__device__ __forceinline__ F2 silu(F2 v) {
+  return mul2(v, f2(sigmoid(lo(v)), sigmoid(hi(v))));
 }
 
 // -exp(a_log) log2(e), finite, so that a step of delta 0 leaves any state alone.
@@ -46,61 +60,149 @@ __device__ __forceinline__ float rate2(float a_log) {
   return r < -3e38f ? -3e38f : r;
 }
 
-// A tile's tensor [TILE][CC] of a block's channels, read a tile ahead into
-// registers: EV words of VE values a thread (VE = 1: rows that are not aligned).
-template <typename T, int NT, int CC, int VE>
-struct Ahead {
-  static constexpr int EV = TILE * CC / (NT * VE);
-  static constexpr int PER_ROW = CC / VE;
-  Word<T, VE> w[EV];
-  __device__ __forceinline__ static int row(int k) { return (k * NT + (int)threadIdx.x) / PER_ROW; }
-  __device__ __forceinline__ static int col(int k) { return (k * NT + (int)threadIdx.x) % PER_ROW * VE; }
-  // rows t0 .. t0 + TILE that are before `end`, channels before `width`
-  __device__ __forceinline__ void read(const T *p, int64_t st, int t0, int end, int h0, int width) {
+// A tile [TILE][CC] of a tensor's rows t0 .. and channels h0 .. on its way to shared
+// memory: 16 bytes at a time and asynchronous where rows are aligned.  What is past
+// the row's end or the last channel keeps what was there.  Made once for a block.
+template <typename T, int NT, int TILE, int CC, bool ALIGNED>
+struct Fetch {
+  static constexpr int V = ALIGNED ? 16 / sizeof(T) : 1, ROW = CC / V;  // pieces of a row
+  static constexpr int PASS = NT / ROW > 0 ? NT / ROW : 1;              // rows of a pass
+  static constexpr int ACROSS = ROW > NT ? ROW / NT : 1;                // passes of a row
+  static_assert(PASS * ROW == NT * ACROSS, "whole rows");
+  const T *from;   // at the thread's row and channel of step 0
+  int64_t st;
+  int row, col, left;  // left: channels from the thread's on
+  __device__ __forceinline__ Fetch(const T *p, int64_t st_, int h0, int width) : st(st_) {
+    row = threadIdx.x / ROW, col = threadIdx.x % ROW * V;
+    if (ROW > NT) row = 0, col = threadIdx.x * V;
+    from = p + row * st + h0 + col;
+    left = width - h0 - col;
+  }
+  __device__ __forceinline__ void start(T (*to)[CC], int t0, int end) const {
+    const T *p = from + t0 * st;
+    const int rows = end - t0 - row;  // of the thread's, that exist
+#pragma unroll
+    for (int k = 0; k < (TILE + PASS - 1) / PASS; ++k, p += PASS * st) {
+      if (k * PASS >= rows || (TILE % PASS && k * PASS + row >= TILE)) break;
+#pragma unroll
+      for (int q = 0; q < ACROSS; ++q) {
+        if (q * NT * V >= left) break;
+        T *s = &to[k * PASS + row][col + q * NT * V];
+        const T *g = p + q * NT * V;
+        if (ALIGNED)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(s)),
+                       "l"(g) : "memory");
+        else
+          *s = *g;
+      }
+    }
+  }
+};
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A tile's rows of b or c [TILE][N], read a tile ahead into registers, four neighbouring
+// values at a time (`words`: as words), in fp32 in shared memory.
+template <typename T, int NT, int TILE, int NP>
+struct Weights {
+  static constexpr int ROW = NP / 4, PASS = NT / ROW, EV = (TILE + PASS - 1) / PASS;
+  static_assert(NT % ROW == 0, "whole rows");
+  const T *from;
+  int64_t st;
+  int row, rows, left;  // rows: of the tile in v, from the thread's on, that exist
+  bool words;
+  Word<T, 4> v[EV];
+  __device__ __forceinline__ Weights(const T *p, int64_t st_, int N, bool words_)
+      : st(st_), rows(0), words(words_) {
+    row = threadIdx.x / ROW;
+    from = p + row * st + threadIdx.x % ROW * 4;
+    left = N - (int)threadIdx.x % ROW * 4;
+  }
+  __device__ __forceinline__ void read(int t0, int end) {
+    const T *p = from + t0 * st;
+    rows = left > 0 ? end - t0 - row : 0;
+#pragma unroll
+    for (int k = 0; k < EV; ++k, p += PASS * st) {
+      if (k * PASS >= rows) break;
+      if (words) {
+        v[k] = *reinterpret_cast<const Word<T, 4> *>(p);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < left) v[k].v[j] = p[j];
+      }
+    }
+  }
+  __device__ __forceinline__ void put(float (*out)[NP]) const {
 #pragma unroll
     for (int k = 0; k < EV; ++k) {
-      const int t = t0 + row(k), h = h0 + col(k);
-      if (t < end && h < width) w[k] = *reinterpret_cast<const Word<T, VE> *>(p + t * st + h);
+      if (TILE % PASS && k * PASS + row >= TILE) break;
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = k * PASS < rows && j < left ? to_f(v[k].v[j]) : 0.f;
+      *reinterpret_cast<float4 *>(&out[k * PASS + row][threadIdx.x % ROW * 4]) =
+          make_float4(w[0], w[1], w[2], w[3]);
     }
   }
 };
 
-// The same of b or c [TILE][N], single values.
-template <typename T, int NT, int NP>
-struct AheadRows {
-  static constexpr int EV = (TILE * NP + NT - 1) / NT;
-  T v[EV];
-  __device__ __forceinline__ void read(const T *p, int64_t st, int t0, int end, int N) {
-#pragma unroll
-    for (int k = 0; k < EV; ++k) {
-      const int at = k * NT + threadIdx.x, t = at / NP, n = at % NP;
-      if (t < TILE && t0 + t < end && n < N) v[k] = p[(t0 + t) * st + n];
-    }
-  }
-  __device__ __forceinline__ void put(float (*out)[NP], int t0, int end, int N) const {
-#pragma unroll
-    for (int k = 0; k < EV; ++k) {
-      const int at = k * NT + threadIdx.x, t = at / NP, n = at % NP;
-      if (t < TILE) out[t][n] = t0 + t < end && n < N ? to_f(v[k]) : 0.f;
-    }
-  }
+// Two pairs: four neighbouring values of T.
+struct Four {
+  F2 a, b;
 };
+__device__ __forceinline__ Four four(const float *p) {
+  const float4 v = *reinterpret_cast<const float4 *>(p);
+  return {f2(v.x, v.y), f2(v.z, v.w)};
+}
+__device__ __forceinline__ Four four(const bf16 *p) {
+  const Word<bf16, 4> v = *reinterpret_cast<const Word<bf16, 4> *>(p);
+  return {f2(to_f(v.v[0]), to_f(v.v[1])), f2(to_f(v.v[2]), to_f(v.v[3]))};
+}
+__device__ __forceinline__ void put_four(float *p, const Four &v) {
+  *reinterpret_cast<float4 *>(p) = make_float4(lo(v.a), hi(v.a), lo(v.b), hi(v.b));
+}
+__device__ __forceinline__ void put_four(bf16 *p, const Four &v) {
+  Word<bf16, 4> w;
+  w.v[0] = from_f<bf16>(lo(v.a)), w.v[1] = from_f<bf16>(hi(v.a));
+  w.v[2] = from_f<bf16>(lo(v.b)), w.v[3] = from_f<bf16>(hi(v.b));
+  *reinterpret_cast<Word<bf16, 4> *>(p) = w;
+}
+// Four channels' constants [H], 0 where there are none.
+__device__ __forceinline__ Four constants(const float *p, int h, int width) {
+  float v[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = p && h + k < width ? p[h + k] : 0.f;
+  return {f2(v[0], v[1]), f2(v[2], v[3])};
+}
 
-// 8 states of [.., N] fp32 at p, `n` of them there.
+// S states of [.., N] fp32 at p, `n` of them there.
+template <int S>
 __device__ __forceinline__ void load_states(const float *p, int n, bool wide, float (&v)[S]) {
+  if (S == 2 && wide && n == S) {
+    const float2 a = *reinterpret_cast<const float2 *>(p);
+    v[0] = a.x, v[1] = a.y;
+    return;
+  }
   if (wide && n == S) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+    for (int k = 0; k + 3 < S; k += 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(p + k);
+      v[k] = a.x, v[k + 1] = a.y, v[k + 2] = a.z, v[k + 3] = a.w;
+    }
     return;
   }
 #pragma unroll
   for (int k = 0; k < S; ++k) v[k] = k < n ? p[k] : 0.f;
 }
+template <int S>
 __device__ __forceinline__ void store_states(float *p, int n, bool wide, const float (&v)[S]) {
+  if (S == 2 && wide && n == S) {
+    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
+    return;
+  }
   if (wide && n == S) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int k = 0; k + 3 < S; k += 4)
+      *reinterpret_cast<float4 *>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
     return;
   }
 #pragma unroll
@@ -108,39 +210,38 @@ __device__ __forceinline__ void store_states(float *p, int n, bool wide, const f
     if (k < n) p[k] = v[k];
 }
 
-// Two neighbouring values of shared memory as a pair.
-__device__ __forceinline__ void load_pairs(const float *p, F2 (&v)[S / 2]) {
-  const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p);
-  const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+// N neighbouring pairs of shared memory.
+template <int N>
+__device__ __forceinline__ void load_pairs(const float *p, F2 (&v)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p + 2 * k);
+    v[k] = a.x, v[k + 1] = a.y;
+  }
+}
+__device__ __forceinline__ void load_row(const float *p, float (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4 *>(p);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
 }
 __device__ __forceinline__ F2 ex2_2(F2 v) { return f2(ex2(lo(v)), ex2(hi(v))); }
 
-// v[t] of LANES steps summed over the channel's LANES lanes; lane l gets step l's.
-template <int LANES>
-__device__ __forceinline__ float sum_over_lanes(float (&v)[LANES], int lane) {
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o /= 2)
-#pragma unroll
-    for (int j = 0; j < o; ++j) {
-      const float keep = lane & o ? v[j + o] : v[j], give = lane & o ? v[j] : v[j + o];
-      v[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-    }
-  return v[0];
-}
-
-// How a sequence is split: segments of `len` steps (whole tiles).
+// How a sequence is split: segments of `len` steps (whole chunks).
 struct Segments {
   int n, len;
 };
 
-// Segments so that `blocks` blocks a segment make `want` in all, of 4 tiles at
-// least.  A split costs the first kernel, some 0.6 of the main one's work.
-inline Segments segments_of(int T, int64_t blocks, int64_t want) {
-  const int tiles = ceil_div(T, TILE);
+// Segments of a sequence whose kernel takes `blocks` blocks a segment: some `per_sm`
+// blocks an SM, of two chunks or more.  A split costs the first kernel, 0.6 of the
+// main one's work on all segments but one, and two launches, so there is one only
+// where an SM would have two blocks or fewer, of eight chunks or more (forward bf16
+// N=16: T=2048 B=8 H=2048, 256 blocks, 357 -> 303 us; T=300 B=32 H=1024, 512 blocks,
+// 77 us, 98 with one; T=512 B=4 H=1024 92 -> 40; T=100 B=4 H=1024 25, 31 with one).
+inline Segments segments_of(int T, int64_t blocks, int nsm, int per_sm) {
+  const int chunks = ceil_div(T, CHUNK);
   int n = 1;
-  if (blocks * 2 <= want) n = (int)std::min<int64_t>(want / blocks, std::max(tiles / 4, 1));
-  const int len = ceil_div(tiles, n) * TILE;
+  if (blocks <= 2 * nsm && chunks >= 8)
+    n = (int)std::max<int64_t>(std::min<int64_t>((int64_t)per_sm * nsm / blocks, chunks / 2), 1);
+  const int len = ceil_div(chunks, n) * CHUNK;
   return {ceil_div(T, len), len};
 }
 
@@ -155,18 +256,6 @@ struct Meeting {
 // chain gradients of the states, with `dy` and c in the place of delta x and b.
 cudaError_t launch_local(const ScanIn &p, bool backwards, const SeqIn &dy, const float *first,
                          const Meeting &m, int *err, bool vec, cudaStream_t s, int *launches);
-
-inline int lanes_of(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
-
-template <typename F>
-cudaError_t by_lanes(int N, F f) {
-  switch (lanes_of(N)) {
-    case 1: return f(std::integral_constant<int, 1>());
-    case 2: return f(std::integral_constant<int, 2>());
-    case 4: return f(std::integral_constant<int, 4>());
-    default: return f(std::integral_constant<int, 8>());
-  }
-}
 
 }  // namespace selscan
 }  // namespace rcu

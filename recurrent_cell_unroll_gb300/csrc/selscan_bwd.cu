@@ -20,8 +20,9 @@ namespace {
 
 using namespace selscan;
 
+constexpr int TILE = CHUNK;                // steps of a tile: those between two kept states
 constexpr int SUB = 4, SUBS = TILE / SUB;  // steps in registers, and groups of them in a chunk
-constexpr int K = 2;                       // channels of a thread
+constexpr int S = 8, K = 2;                // states and channels of a thread
 constexpr int SLOT = 32 * K * S;           // floats of a warp's checkpoint
 
 struct Args {
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const Args a, int *err
   T *ddt = p.ddt.p ? static_cast<T *>(p.ddt.p) + b * p.ddt.sb + ch0 : nullptr;
   T *dz = p.dz.p && z ? static_cast<T *>(p.dz.p) + b * p.dz.sb + ch0 : nullptr;
 
-  auto load_pairs_of = [&](const float *row, F2 (&v)[S / 2]) { load_pairs(row + n0, v); };
+  auto load_pairs_of = [&](const float *row, F2 (&v)[S / 2]) { load_pairs<S / 2>(row + n0, v); };
   // h after a step, from the state before it; the decay where it is wanted
   auto step = [&](int t, const F2 (&w)[S / 2], F2 (&h)[K][S / 2], F2 (*decay)[S / 2]) {
     const float2 d = *reinterpret_cast<const float2 *>(s_delta + t * CC + own);
@@ -353,6 +354,17 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const Args a, int *err
   }
 }
 
+int lanes_of(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
+template <typename F>
+cudaError_t by_lanes(int N, F f) {
+  switch (lanes_of(N)) {
+    case 1: return f(std::integral_constant<int, 1>());
+    case 2: return f(std::integral_constant<int, 2>());
+    case 4: return f(std::integral_constant<int, 4>());
+    default: return f(std::integral_constant<int, 8>());
+  }
+}
+
 // db and dc from the blocks' sums, [groups][T][B][2][N]: a thread a value.
 template <typename T>
 __global__ void __launch_bounds__(256) sum_bc_kernel(const float *part, int groups, int T_, int B, int N,
@@ -400,7 +412,7 @@ cudaError_t launch_scan_bwd(const ScanBwd &p, DevMem &ws, int *err, int nsm, boo
   const int wc = 64 / lanes_of(in.N);
   a.warps = std::min(ceil_div(in.H, wc), lanes_of(in.N) == 1 ? 2 : 4);
   a.groups = ceil_div(in.H, wc * a.warps);
-  a.seg = segments_of(in.T, (int64_t)a.groups * in.B, 2 * (int64_t)nsm);
+  a.seg = segments_of(in.T, (int64_t)a.groups * in.B, nsm, 3);
   const bool bc = p.db.p || p.dc.p, sums = p.da_log || p.dd || p.ddt_bias;
   const int64_t n_bc = bc ? (int64_t)a.groups * in.T * in.B * 2 * in.N : 0;
   const int64_t n_part = sums ? (int64_t)a.seg.n * in.B * in.H * (in.N + 2) : 0;

@@ -22,161 +22,263 @@ struct Args {
   float *h_n, *states;
   Meeting m;
   int groups;
-  bool wide_states;
+  bool wide_states, wide_bc;
 };
 
-// Warps of a block: channels of a block are 32 / LANES of each.
-template <int LANES>
-constexpr int warps() { return LANES == 1 ? 2 : LANES == 2 ? 4 : 8; }
+// A thread has S states of K neighbouring channels, as pairs of channels; the LANES
+// threads that hold a channel's N stand side by side in a warp.  Tiles are of half a
+// chunk: a block's shared memory then leaves room for seven others.
+constexpr int K = 4, P = K / 2, TILE = CHUNK / 2;
+template <int S, int LANES>
+struct Shape {
+  static constexpr int WARPS = LANES <= 2 ? 1 : LANES / 2;   // of a block
+  static constexpr int NT = 32 * WARPS, CC = NT / LANES * K, NP = S * LANES;
+  // sums over a channel's states come in PARTS, added as they are read; the first two
+  // are where the steps' delta and input stood
+  static constexpr int PARTS = LANES < 4 ? LANES : 4;
+  static constexpr int BUF = TILE * CC + 8;              // floats: parts 8 banks apart
+  static constexpr int BUFS = PARTS < 2 ? 2 : PARTS;
+};
+template <typename T, int S, int LANES, Mode MODE>
+constexpr int shared_bytes() {
+  typedef Shape<S, LANES> Sh;
+  return (MODE == MAIN ? Sh::BUFS : 2) * Sh::BUF * 4 + (MODE == MAIN ? 2 : 1) * TILE * Sh::NP * 4 +
+         2 * (MODE == ENDS ? 2 : 3) * TILE * Sh::CC * (int)sizeof(T);
+}
 
-template <typename T, int LANES, int VE, Mode MODE>
-__global__ void __launch_bounds__(32 * warps<LANES>()) scan_kernel(const Args a, int *err) {
-  constexpr int NT = 32 * warps<LANES>(), CC = NT / LANES, NP = S * LANES;
-  __shared__ float2 step_in[TILE][CC];                      // delta, delta x (or gy)
-  __shared__ float2 gate[MODE == MAIN ? TILE : 1][CC];      // silu(z), d x silu(z)
-  __shared__ alignas(16) float in_w[TILE][NP];              // b (GRADS: c)
-  __shared__ alignas(16) float out_w[MODE == MAIN ? TILE : 1][NP];  // c
+template <typename T, int S, int LANES, bool ALIGNED, Mode MODE>
+__global__ void __launch_bounds__(Shape<S, LANES>::NT) scan_kernel(const Args a, int *err) {
+  typedef Shape<S, LANES> Sh;
+  constexpr int NT = Sh::NT, CC = Sh::CC, NP = Sh::NP, BUF = Sh::BUF, PARTS = Sh::PARTS;
+  constexpr int U = 2;                 // steps worked on together
+  constexpr int RAW = MODE == ENDS ? 2 : 3;
+  constexpr int ROW = CC / 4, EV = (TILE * ROW + NT - 1) / NT;  // words of four of a thread, of the same channels
+  constexpr bool IDLE = TILE * ROW < NT;  // some threads have none
+  extern __shared__ float4 shared4[];
+  float *buf = reinterpret_cast<float *>(shared4);                     // [BUFS][BUF]: delta, input
+  float(*in_w)[NP] = reinterpret_cast<float(*)[NP]>(buf + (MODE == MAIN ? Sh::BUFS : 2) * BUF);  // b (GRADS: c)
+  float(*out_w)[NP] = in_w + TILE;                                    // MAIN: c
+  T(*raw)[TILE][CC] = reinterpret_cast<T(*)[TILE][CC]>(MODE == MAIN ? out_w + TILE : in_w + TILE);
   const ScanIn &p = a.in;
   const int group = blockIdx.x % a.groups;
-  const int b = (int)(blockIdx.x / a.groups % p.B), seg = (int)(blockIdx.x / a.groups / p.B);
-  const int tid = threadIdx.x, l = tid % LANES, cl = tid / LANES;
-  const int ch0 = group * CC, ch = ch0 + cl, n0 = l * S;
-  const bool live = ch < p.H;
-  const int here = live ? min(max(p.N - n0, 0), S) : 0;  // states that exist
-  const int64_t row = (int64_t)b * p.H + ch;             // of [B][H]
-  const int64_t at = row * p.N + n0;                     // of [B][H][N]
+  // GRADS: of all segments but the first; ENDS: but the last (by the grid)
+  const int b = (int)(blockIdx.x / a.groups % p.B), seg = (int)(blockIdx.x / a.groups / p.B) + (MODE == GRADS);
+  const int tid = threadIdx.x, l = tid % LANES, own = tid / LANES * K;  // own: of the block's channels
+  const int ch0 = group * CC, n0 = l * S;
   const int64_t table = (int64_t)p.B * p.H * p.N;
   const int n = row_length(p.lengths, b, p.T, err);
   const int t0 = seg * a.m.seg.len, t1 = min(t0 + a.m.seg.len, p.T), end = min(t1, n);
 
-  F2 A2[S / 2], h[S / 2];
-  {
-    float v[S];
-    load_states(p.a_log + (int64_t)ch * p.N + n0, here, a.wide_states && live, v);
-#pragma unroll
-    for (int k = 0; k < S; ++k) v[k] = k < here ? rate2(v[k]) : 0.f;
-#pragma unroll
-    for (int k = 0; k < S / 2; ++k) A2[k] = f2(v[2 * k], v[2 * k + 1]);
-#pragma unroll
-    for (int k = 0; k < S; ++k) v[k] = 0.f;
-    if (MODE == MAIN && a.h0 && live)
-      load_states(a.h0 + (a.m.seg.n > 1 ? seg * table : 0) + at, here, a.wide_states, v);
-#pragma unroll
-    for (int k = 0; k < S / 2; ++k) h[k] = f2(v[2 * k], v[2 * k + 1]);
-  }
-  auto keep = [&](float *to) {
-    float v[S];
-#pragma unroll
-    for (int k = 0; k < S / 2; ++k) v[2 * k] = lo(h[k]), v[2 * k + 1] = hi(h[k]);
-    if (live) store_states(to + at, here, a.wide_states, v);
-  };
-
-  const T *x = static_cast<const T *>(p.x.p) + b * p.x.sb;
-  const T *dt = static_cast<const T *>(p.dt.p) + b * p.dt.sb;
-  const T *z = p.z.p ? static_cast<const T *>(p.z.p) + b * p.z.sb : nullptr;
-  const T *dy = MODE == GRADS ? static_cast<const T *>(a.dy.p) + b * a.dy.sb : nullptr;
-  const SeqIn &wi = MODE == GRADS ? p.c : p.b;
-  const T *w1 = static_cast<const T *>(wi.p) + b * wi.sb;
-  const T *w2 = static_cast<const T *>(p.c.p) + b * p.c.sb;
+  const SeqIn &sx = MODE == GRADS ? a.dy : p.x, &sw = MODE == GRADS ? p.c : p.b;
+  typedef Fetch<T, NT, TILE, CC, ALIGNED> F;
+  const F fdt(static_cast<const T *>(p.dt.p) + b * p.dt.sb, p.dt.st, ch0, p.H);
+  const F fx(static_cast<const T *>(sx.p) + b * sx.sb, sx.st, ch0, p.H);
+  const bool use_z = p.z.p && MODE != ENDS;
+  const F fz(static_cast<const T *>(p.z.p) + (use_z ? b * p.z.sb : 0), p.z.st, ch0, p.H);
+  Weights<T, NT, TILE, NP> r1(static_cast<const T *>(sw.p) + b * sw.sb, sw.st, p.N, a.wide_bc);
+  Weights<T, NT, TILE, NP> r2(static_cast<const T *>(p.c.p) + b * p.c.sb, p.c.st, p.N, a.wide_bc);
   T *y = MODE == MAIN ? static_cast<T *>(a.y.p) + b * a.y.sb : nullptr;
 
-  const bool use_z = z && MODE != ENDS;
-  Ahead<T, NT, CC, VE> rx, rdt, rz;
-  AheadRows<T, NT, NP> r1, r2;
-  auto read = [&](int t) {
-    rdt.read(dt, p.dt.st, t, end, ch0, p.H);
-    if (MODE == GRADS) rx.read(dy, a.dy.st, t, end, ch0, p.H);
-    else rx.read(x, p.x.st, t, end, ch0, p.H);
-    if (use_z) rz.read(z, p.z.st, t, end, ch0, p.H);
-    r1.read(w1, wi.st, t, end, p.N);
-    if (MODE == MAIN) r2.read(w2, p.c.st, t, end, p.N);
-  };
-  float total = 0.f;  // of delta
   const int tiles = t0 < end ? ceil_div(end - t0, TILE) : 0;
   auto tile_at = [&](int k) { return t0 + (MODE == GRADS ? tiles - 1 - k : k) * TILE; };
-  if (tiles) read(tile_at(0));
+  // tile k's rows, into the buffers of its parity
+  auto start = [&](int k) {
+    T(*to)[TILE][CC] = raw + k % 2 * RAW;
+    const int t = tile_at(k);
+    fdt.start(to[0], t, end);
+    fx.start(to[1], t, end);
+    if (use_z) fz.start(to[RAW - 1], t, end);
+    r1.read(t, end);
+    if (MODE == MAIN) r2.read(t, end);
+  };
+  if (tiles) start(0);
+
+  int here[K];          // states that exist
+  F2 A2[P][S], h[P][S]; // of pairs of channels
+#pragma unroll
+  for (int c = 0; c < K; c += 2) {
+    float r[2][S], v[2][S];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int ch = ch0 + own + c + j;
+      here[c + j] = ch < p.H ? min(max(p.N - n0, 0), S) : 0;
+      load_states(p.a_log + (int64_t)ch * p.N + n0, here[c + j], a.wide_states, r[j]);
+#pragma unroll
+      for (int k = 0; k < S; ++k) {
+        r[j][k] = k < here[c + j] ? rate2(r[j][k]) : 0.f;
+        v[j][k] = 0.f;
+      }
+      if (MODE == MAIN && a.h0)
+        load_states(a.h0 + (a.m.seg.n > 1 ? seg * table : 0) + ((int64_t)b * p.H + ch) * p.N + n0, here[c + j],
+                    a.wide_states, v[j]);
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k) A2[c / 2][k] = f2(r[0][k], r[1][k]), h[c / 2][k] = f2(v[0][k], v[1][k]);
+  }
+  auto keep = [&](float *to) {
+    to += ((int64_t)b * p.H + ch0 + own) * p.N + n0;
+#pragma unroll
+    for (int c = 0; c < K; ++c) {
+      float v[S];
+#pragma unroll
+      for (int k = 0; k < S; ++k) v[k] = c % 2 ? hi(h[c / 2][k]) : lo(h[c / 2][k]);
+      store_states(to + (int64_t)c * p.N, here[c], a.wide_states, v);
+    }
+  };
+  const int col = tid % ROW * 4, row0 = tid / ROW;  // of the thread's words: rows NT / ROW apart
+  const Four bias = constants(p.dt_bias, ch0 + col, p.H);
+  const Four skip = constants(MODE == MAIN ? p.d : nullptr, ch0 + col, p.H);
+  F2 total[P] = {};  // of delta
+
   for (int k = 0; k < tiles; ++k) {
-    const int base = tile_at(k);
-    __syncthreads();  // the tile before is done with
+    const int base = tile_at(k), steps = min(TILE, end - base);
+    T(*now)[TILE][CC] = raw + k % 2 * RAW;
+    if (k == 0) {
+      fetched();
+      __syncthreads();
+    }
 #pragma unroll
-    for (int q = 0; q < Ahead<T, NT, CC, VE>::EV; ++q) {
-      const int t = rx.row(q), c = rx.col(q);
+    for (int q = 0; q < EV; ++q) {
+      const int r = row0 + q * (NT / ROW);
+      if (IDLE && r >= TILE) break;
+      Four v = four(&now[0][r][col]), u = four(&now[1][r][col]);
+      v.a = softplus(add2(v.a, bias.a)), v.b = softplus(add2(v.b, bias.b));
+      if (MODE != GRADS) {
+        u.a = mul2(v.a, u.a), u.b = mul2(v.b, u.b);
+      } else if (use_z) {
+        const Four g = four(&now[RAW - 1][r][col]);
+        u.a = mul2(u.a, silu(g.a)), u.b = mul2(u.b, silu(g.b));
+      }
+      // steps past the end have delta and input 0, and so leave the states alone
+      if (steps < TILE && r >= steps) v = u = {f2(0.f), f2(0.f)};
+      put_four(buf + r * CC + col, v);
+      put_four(buf + BUF + r * CC + col, u);
+    }
+    r1.put(in_w);
+    if (MODE == MAIN) r2.put(out_w);
+    __syncthreads();
+    if (k + 1 < tiles) start(k + 1);
+    if (MODE == MAIN && a.states && base % CHUNK == 0) keep(a.states + (base / CHUNK) * table);
+
+    const int groups = ceil_div(steps, U);
+    for (int g = 0; g < groups; ++g) {
+      F2 decay[U][P][S], add[U][P][S];
+      const int first = MODE == GRADS ? (groups - 1 - g) * U : g * U;
 #pragma unroll
-      for (int j = 0; j < VE; ++j) {
-        float2 in = make_float2(0.f, 0.f), g = make_float2(0.f, 0.f);
-        if (base + t < end && ch0 + c + j < p.H) {
-          const float v = to_f(rx.w[q].v[j]);
-          const float delta =
-              softplus(to_f(rdt.w[q].v[j]) + (p.dt_bias ? p.dt_bias[ch0 + c + j] : 0.f));
-          float silu = 1.f;
-          if (use_z) {
-            const float zv = to_f(rz.w[q].v[j]);
-            silu = zv * sigmoid(zv);
+      for (int j = 0; j < U; ++j) {
+        F2 d[P], in[P];
+        float w[S];
+        load_pairs<P>(buf + (first + j) * CC + own, d);
+        load_pairs<P>(buf + BUF + (first + j) * CC + own, in);
+        load_row(in_w[first + j] + n0, w);
+#pragma unroll
+        for (int c = 0; c < P; ++c) {
+          if (MODE != MAIN) total[c] = add2(total[c], d[c]);
+#pragma unroll
+          for (int q = 0; q < S; ++q) {
+            decay[j][c][q] = ex2_2(mul2(d[c], A2[c][q]));
+            add[j][c][q] = mul2(in[c], f2(w[q]));
           }
-          in = make_float2(delta, MODE == GRADS ? v * silu : delta * v);
-          if (MODE == MAIN) g = make_float2(silu, p.d ? p.d[ch0 + c + j] * v * silu : 0.f);
         }
-        step_in[t][c + j] = in;
-        if (MODE == MAIN) gate[t][c + j] = g;
+      }
+      F2 v[U][P];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int j = MODE == GRADS ? U - 1 - i : i;
+        float w[S];
+        if (MODE == MAIN) load_row(out_w[first + j] + n0, w);
+#pragma unroll
+        for (int c = 0; c < P; ++c)
+#pragma unroll
+          for (int q = 0; q < S; ++q) {
+            F2 &s = h[c][q];
+            if (MODE == GRADS) s = mul2(decay[j][c][q], add2(add[j][c][q], s));
+            else s = fma2(decay[j][c][q], s, add[j][c][q]);
+            if (MODE == MAIN) v[j][c] = q ? fma2(s, f2(w[q]), v[j][c]) : mul2(s, f2(w[q]));
+          }
+      }
+      if (MODE == MAIN) {
+        // down to PARTS lanes: of 8, every half of them takes one of the steps, of 16, a
+        // half of its channels
+        int at = 0, count = U * P;
+        F2 *sum = &v[0][0];
+#pragma unroll
+        for (int o = LANES / 2; o >= PARTS && o > 0; o /= 2) {
+          count /= 2;
+          const bool upper = l & o;
+          at += upper ? count : 0;
+#pragma unroll
+          for (int j = 0; j < U * P / 2; ++j)
+            if (j < count) {
+              const F2 mine = upper ? sum[j + count] : sum[j], other = upper ? sum[j] : sum[j + count];
+              sum[j] = add2(mine, __shfl_xor_sync(0xffffffffu, other, o));
+            }
+        }
+        __syncwarp();  // the parts stand where the warp's other lanes have read from
+        float *to = buf + l % PARTS * BUF + (first + at / P) * CC + own;
+        if (count >= P) {
+#pragma unroll
+          for (int j = 0; j < U; ++j)
+            if (j * P < count)
+              *reinterpret_cast<float4 *>(to + j * CC) = make_float4(lo(v[j][0]), hi(v[j][0]), lo(v[j][1]), hi(v[j][1]));
+        } else {
+          *reinterpret_cast<F2 *>(to + at % P * 2) = sum[0];
+        }
       }
     }
-    r1.put(in_w, base, end, p.N);
-    if (MODE == MAIN) r2.put(out_w, base, end, p.N);
-    if (k + 1 < tiles) read(tile_at(k + 1));
+    fetched();
     __syncthreads();
-    if (MODE == MAIN && a.states) keep(a.states + (base / TILE) * table);
-    const int steps = min(TILE, end - base);
     if (MODE == MAIN) {
-      for (int t = 0; t < steps; t += LANES) {  // steps past the end have delta 0
-        float v[LANES];
+      // y = (sum + d x) silu(z)
 #pragma unroll
-        for (int j = 0; j < LANES; ++j) {
-          const float2 in = step_in[t + j][cl];
-          F2 bw[S / 2], cw[S / 2], sum;
-          load_pairs(&in_w[t + j][n0], bw);
-          load_pairs(&out_w[t + j][n0], cw);
-          const F2 d2 = f2(in.x), u2 = f2(in.y);
+      for (int q = 0; q < EV; ++q) {
+        const int r = row0 + q * (NT / ROW);
+        if (r >= steps) break;
+        Four v = four(buf + r * CC + col);
 #pragma unroll
-          for (int q = 0; q < S / 2; ++q) {
-            h[q] = fma2(ex2_2(mul2(d2, A2[q])), h[q], mul2(u2, bw[q]));
-            sum = q ? fma2(h[q], cw[q], sum) : mul2(h[q], cw[q]);
-          }
-          v[j] = lo(sum) + hi(sum);
+        for (int k2 = 1; k2 < PARTS; ++k2) {
+          const Four more = four(buf + k2 * BUF + r * CC + col);
+          v.a = add2(v.a, more.a), v.b = add2(v.b, more.b);
         }
-        const float s = sum_over_lanes<LANES>(v, l);
-        if (t + l < steps && live) {
-          const float2 g = gate[t + l][cl];
-          y[(base + t + l) * a.y.st + ch] = from_f<T>(fmaf(s, g.x, g.y));
+        if (p.d) {
+          const Four xs = four(&now[1][r][col]);
+          v.a = fma2(skip.a, xs.a, v.a), v.b = fma2(skip.b, xs.b, v.b);
         }
-      }
-    } else {
-#pragma unroll 4
-      for (int j = 0; j < steps; ++j) {
-        const int t = MODE == GRADS ? steps - 1 - j : j;
-        const float2 in = step_in[t][cl];
-        F2 w[S / 2];
-        load_pairs(&in_w[t][n0], w);
-        const F2 d2 = f2(in.x), u2 = f2(in.y);
-        total += in.x;
+        if (use_z) {
+          const Four g = four(&now[RAW - 1][r][col]);
+          v.a = mul2(v.a, silu(g.a)), v.b = mul2(v.b, silu(g.b));
+        }
+        T *to = y + (base + r) * a.y.st + ch0 + col;
+        if (ALIGNED) {
+          if (ch0 + col < p.H) put_four(to, v);
+        } else {
+          const float out[4] = {lo(v.a), hi(v.a), lo(v.b), hi(v.b)};
 #pragma unroll
-        for (int q = 0; q < S / 2; ++q) {
-          const F2 decay = ex2_2(mul2(d2, A2[q]));
-          h[q] = MODE == GRADS ? mul2(decay, fma2(u2, w[q], h[q])) : fma2(decay, h[q], mul2(u2, w[q]));
+          for (int j = 0; j < 4; ++j)
+            if (ch0 + col + j < p.H) to[j] = from_f<T>(out[j]);
         }
       }
     }
   }
   if (MODE != MAIN) {
     keep(a.m.end + seg * table);
-    if (live && l == 0) a.m.sums[(int64_t)seg * p.B * p.H + row] = total;
+    if (l == 0) {
+      float *to = a.m.sums + ((int64_t)seg * p.B + b) * p.H + ch0 + own;
+#pragma unroll
+      for (int c = 0; c < K; ++c)
+        if (here[c]) to[c] = c % 2 ? hi(total[c / 2]) : lo(total[c / 2]);
+    }
     return;
   }
   // what lies past the row's end
   if (a.states)
-    for (int t = t0 + tiles * TILE; t < t1; t += TILE) keep(a.states + (t / TILE) * table);
+    for (int t = t0 + round_up(tiles * TILE, CHUNK); t < t1; t += CHUNK) keep(a.states + (t / CHUNK) * table);
   if (a.h_n && seg == a.m.seg.n - 1) keep(a.h_n);
-  if (live)
-    for (int t = max(t0, end) + l; t < t1; t += LANES) y[t * a.y.st + ch] = from_f<T>(0.f);
+  const int past = max(t0, end);
+  for (int64_t i = tid; i < (int64_t)(t1 - past) * CC; i += NT) {
+    const int c = ch0 + (int)(i % CC);
+    if (c < p.H) y[(past + i / CC) * a.y.st + c] = from_f<T>(0.f);
+  }
 }
 
 // The states that enter each segment, in the place of those that it ended with
@@ -192,38 +294,61 @@ __global__ void __launch_bounds__(128) chain_kernel(const float *a_log, const fl
   float h = first ? first[i] : 0.f;
   for (int k = 0; k < m.seg.n; ++k) {
     const int s = BACKWARDS ? m.seg.n - 1 - k : k;
+    if (k == m.seg.n - 1) {  // nothing follows it
+      m.end[s * table + i] = h;
+      break;
+    }
     const float own = m.end[s * table + i], decay = ex2(A2 * m.sums[s * rows + row]);
     m.end[s * table + i] = h;
     h = fmaf(decay, h, own);
   }
 }
 
-template <typename T, int LANES, int VE, Mode MODE>
+template <typename T, int S, int LANES, bool ALIGNED, Mode MODE>
 cudaError_t run(Args a, int *err, cudaStream_t s, int *launches) {
-  constexpr int NT = 32 * warps<LANES>();
-  a.groups = ceil_div(a.in.H, NT / LANES);
+  typedef Shape<S, LANES> Sh;
+  constexpr int bytes = shared_bytes<T, S, LANES, MODE>();
+  auto fn = scan_kernel<T, S, LANES, ALIGNED, MODE>;
+  static PerDevice<cudaError_t> ready;
+  const cudaError_t set =
+      ready.here([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+  if (set != cudaSuccess) return set;
+  a.groups = ceil_div(a.in.H, Sh::CC);
   ++*launches;
-  const int64_t blocks = (int64_t)a.groups * a.in.B * a.m.seg.n;
-  scan_kernel<T, LANES, VE, MODE><<<(unsigned)blocks, NT, 0, s>>>(a, err);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((int64_t)a.groups * a.in.B * (a.m.seg.n - (MODE != MAIN))));
+  cfg.blockDim = dim3(Sh::NT);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, fn, a, err);
 }
 
+template <typename T, Mode MODE, int S, int LANES>
+cudaError_t of_lanes(const Args &a, bool aligned, int *err, cudaStream_t s, int *launches) {
+  return aligned ? run<T, S, LANES, true, MODE>(a, err, s, launches) : run<T, S, LANES, false, MODE>(a, err, s, launches);
+}
+template <typename T, Mode MODE>
+cudaError_t of_type(const Args &a, bool aligned, int *err, cudaStream_t s, int *launches) {
+  const int N = a.in.N;
+  if (N <= 4) return of_lanes<T, MODE, 4, 1>(a, aligned, err, s, launches);
+  if (N <= 8) return of_lanes<T, MODE, 4, 2>(a, aligned, err, s, launches);
+  if (N <= 16) return of_lanes<T, MODE, 4, 4>(a, aligned, err, s, launches);
+  if (N <= 32) return of_lanes<T, MODE, 4, 8>(a, aligned, err, s, launches);
+  return of_lanes<T, MODE, 4, 16>(a, aligned, err, s, launches);
+}
 template <Mode MODE>
-cudaError_t dispatch(const Args &a, bool vec, int *err, cudaStream_t s, int *launches) {
+cudaError_t dispatch(Args a, bool vec, int *err, cudaStream_t s, int *launches) {
   const ScanIn &p = a.in;
-  const int size = p.dtype == RCU_BF16 ? 2 : 4;
-  const bool wide = vec && p.H % 4 == 0 && aligned(p.x, size, 4) && aligned(p.dt, size, 4) &&
-                    (!p.z.p || aligned(p.z, size, 4)) && (MODE != GRADS || aligned(a.dy, size, 4));
-  return by_lanes(p.N, [&](auto lanes) {
-    constexpr int L = decltype(lanes)::value;
-    if (p.dtype == RCU_BF16)
-      return wide ? run<bf16, L, 4, MODE>(a, err, s, launches) : run<bf16, L, 1, MODE>(a, err, s, launches);
-    return wide ? run<float, L, 4, MODE>(a, err, s, launches) : run<float, L, 1, MODE>(a, err, s, launches);
-  });
+  const int size = p.dtype == RCU_BF16 ? 2 : 4, n = 16 / size;
+  const bool wide = vec && p.H % n == 0 && aligned(p.x, size, n) && aligned(p.dt, size, n) &&
+                    (!p.z.p || aligned(p.z, size, n)) && (MODE != GRADS || aligned(a.dy, size, n)) &&
+                    (MODE != MAIN || aligned(a.y, size, n));
+  return p.dtype == RCU_BF16 ? of_type<bf16, MODE>(a, wide, err, s, launches)
+                             : of_type<float, MODE>(a, wide, err, s, launches);
 }
 
 bool wide_states(const ScanIn &p, bool vec, std::initializer_list<const void *> tables) {
-  if (!vec || p.N % S) return false;
+  if (!vec || p.N % 4) return false;
   for (const void *t : tables)
     if (t && !aligned(t, 4, 4, 4)) return false;
   return true;
@@ -261,9 +386,8 @@ cudaError_t launch_scan_fwd(const ScanFwd &p, DevMem &ws, int *err, int nsm, boo
   a.y = p.y;
   a.h_n = p.h_n;
   a.states = p.states;
-  // a block holds 64 channels (32 of those with more than 32 states)
-  const int64_t blocks = (int64_t)ceil_div(in.H, in.N > 32 ? 32 : 64) * in.B;
-  a.m.seg = segments_of(in.T, blocks, 4 * (int64_t)nsm);
+  const int64_t blocks = (int64_t)ceil_div(in.H, in.N > 4 ? 64 : 128) * in.B;
+  a.m.seg = segments_of(in.T, blocks, nsm, 8);
   if (a.m.seg.n > 1) {
     const cudaError_t e = ws.get((size_t)a.m.seg.n * (table + (int64_t)in.B * in.H) * 4, &a.m.end);
     if (e != cudaSuccess) return e;
