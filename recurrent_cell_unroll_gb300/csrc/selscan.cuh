@@ -213,8 +213,9 @@ __device__ __forceinline__ void store_states(float *p, int n, bool wide, const f
 // N neighbouring pairs of shared memory.
 template <int N>
 __device__ __forceinline__ void load_pairs(const float *p, F2 (&v)[N]) {
+  if (N == 1) v[0] = *reinterpret_cast<const F2 *>(p);
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
+  for (int k = 0; k + 1 < N; k += 2) {
     const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(p + 2 * k);
     v[k] = a.x, v[k + 1] = a.y;
   }

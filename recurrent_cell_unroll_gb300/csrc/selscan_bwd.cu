@@ -8,11 +8,14 @@
 // A block takes the chunks of 32 steps from the last to the first.  In a chunk it
 // runs the states forward from the kept ones, leaving those before every fourth
 // step in shared memory, then takes four steps at a time backwards: their states
-// and decays once more, in registers, and the gradients against them.
+// once more, in registers, and the gradients against them.
 //
-// The sums over channels (db, dc) are what costs beside that: a thread has two
-// channels, whose products it adds first, and the warp's lanes exchange theirs
-// through the checkpoint of the four steps, which has been read by then.
+// A thread has S states of K neighbouring channels, a warp all states of its own
+// channels, so only the sums over channels (db, dc) leave a warp.  They are what
+// costs beside the exponentials: a thread adds its four channels' first, the lanes
+// exchange theirs in shared memory, and the warps' sums stand where the checkpoint
+// of the four steps was.  Sums over states are left in parts by the lanes, and added
+// by the threads that compute the outputs, as words of four channels.
 #include "selscan.cuh"
 
 namespace rcu {
@@ -22,42 +25,118 @@ using namespace selscan;
 
 constexpr int TILE = CHUNK;                // steps of a tile: those between two kept states
 constexpr int SUB = 4, SUBS = TILE / SUB;  // steps in registers, and groups of them in a chunk
-constexpr int S = 8, K = 2;                // states and channels of a thread
+constexpr int S = 4, K = 2;                // states and channels (a pair) of a thread
 constexpr int SLOT = 32 * K * S;           // floats of a warp's checkpoint
 
 struct Args {
   ScanBwd p;
-  int groups, warps;     // blocks of channels; warps of a block
+  int groups;            // blocks of channels
   Segments seg;
   const float *enter;    // [seg][B][H][N]: gradients that enter each segment, or dh_n
   float *part_bc;        // [groups][T][B][2][N], or NULL
   float *part;           // [B * seg][H N | H | H], or NULL
-  bool wide_states;
+  bool wide_states, wide_bc;
 };
 
 template <int LANES>
-constexpr int slots() { return LANES == 8 ? SUBS : SUBS - 1; }
-template <int LANES>
-constexpr int channels() { return 32 / LANES * K; }  // of a warp
-template <int LANES>
-size_t shared_bytes(int warps) {
-  const size_t cc = (size_t)channels<LANES>() * warps;
-  return (size_t)warps * slots<LANES>() * SLOT * 4 + 3 * TILE * cc * 4 + 2 * TILE * LANES * S * 4;
+struct Shape {
+  static constexpr int NP = S * LANES;
+  static constexpr int WC = 32 / LANES * K;                    // channels of a warp
+  static constexpr int WARPS = WC >= 64 ? 1 : WC == 32 ? 2 : 4;  // of a block
+  static constexpr int NT = 32 * WARPS, CC = WC * WARPS;
+  // Checkpoints of a chunk, one of the first steps only where the sums over channels
+  // of two groups of steps do not fit into one.
+  static constexpr int SLOTS = NP > 16 ? SUBS : SUBS - 1;
+  static constexpr int SUMS = NP > 32 ? TILE * 2 * NP : 0;     // floats of such sums elsewhere
+  static constexpr int PARTS = LANES < 4 ? LANES : 4;
+  static constexpr int WORDS = SUB * WC / K;                   // pairs of a warp's four steps
+  static constexpr int MINE = (WORDS + 31) / 32;               // of them, of a lane
+  static constexpr int PART = SUB * WC + 8;                    // floats: parts 8 banks apart
+  // floats of a warp: checkpoints, parts of three sums, the lanes' exchange
+  static constexpr int WARP = SLOTS * SLOT + SUMS + 3 * PARTS * PART + 256;
+  static constexpr int SHARED = 4 * (WARPS * WARP + 3 * TILE * CC + 2 * TILE * NP + 2 * CC);
+};
+
+// Four channels' values of a row, by a word where rows are aligned.
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ Word<T, 4> load_four(const T *p, int left) {
+  Word<T, 4> w;
+  if constexpr (ALIGNED) {
+    w = *reinterpret_cast<const Word<T, 4> *>(p);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w.v[j] = j < left ? p[j] : from_f<T>(0.f);
+  }
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ Four pairs_of(const Word<T, 4> &w) {
+  return {f2(to_f(w.v[0]), to_f(w.v[1])), f2(to_f(w.v[2]), to_f(w.v[3]))};
+}
+__device__ __forceinline__ Four operator*(const Four &x, const Four &y) {
+  return {mul2(x.a, y.a), mul2(x.b, y.b)};
+}
+__device__ __forceinline__ Four operator+(const Four &x, const Four &y) {
+  return {add2(x.a, y.a), add2(x.b, y.b)};
+}
+__device__ __forceinline__ Four sigmoid(const Four &v) {
+  return {f2(ssm::sigmoid(lo(v.a)), ssm::sigmoid(hi(v.a))), f2(ssm::sigmoid(lo(v.b)), ssm::sigmoid(hi(v.b)))};
 }
 
-template <typename T, int LANES>
-__global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const Args a, int *err) {
-  constexpr int NP = S * LANES, WC = channels<LANES>(), SLOTS = slots<LANES>();
+// Two channels' values of a row.
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ Word<T, 2> load_two(const T *p, int left) {
+  Word<T, 2> w;
+  if (ALIGNED) return *reinterpret_cast<const Word<T, 2> *>(p);
+  w.v[0] = p[0];
+  w.v[1] = left > 1 ? p[1] : from_f<T>(0.f);
+  return w;
+}
+template <typename T>
+__device__ __forceinline__ F2 pair_of(const Word<T, 2> &w) { return f2(to_f(w.v[0]), to_f(w.v[1])); }
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ void store_two(T *p, int left, F2 v) {
+  Word<T, 2> w;
+  w.v[0] = from_f<T>(lo(v)), w.v[1] = from_f<T>(hi(v));
+  if (ALIGNED) {
+    *reinterpret_cast<Word<T, 2> *>(p) = w;
+    return;
+  }
+  p[0] = w.v[0];
+  if (left > 1) p[1] = w.v[1];
+}
+__device__ __forceinline__ F2 sigmoid2(F2 v) { return f2(ssm::sigmoid(lo(v)), ssm::sigmoid(hi(v))); }
+__device__ __forceinline__ F2 pair_at(const float *p) { return *reinterpret_cast<const F2 *>(p); }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void prefetch(const void *p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
+
+template <typename T, int LANES, bool ALIGNED>
+__global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a, int *err) {
+  typedef Shape<LANES> Sh;
+  constexpr int NP = Sh::NP, WC = Sh::WC, NT = Sh::NT, CC = Sh::CC, SLOTS = Sh::SLOTS, PARTS = Sh::PARTS;
+  constexpr int PART = Sh::PART, ROW = CC / 4;
+  // What the outputs need of the inputs, and the first states a second time, come by
+  // asynchronous copies into checkpoints that have been read: a plain read would be
+  // waited for, some 1700 cycles, by six warps an SM.  Of 16 states a channel, which
+  // leave the upper halves of the checkpoints free.
+  constexpr bool AHEAD = LANES == 4 && ALIGNED;
   const ScanBwd &p = a.p;
   const ScanIn &in = p.in;
-  const int NT = a.warps * 32, CC = WC * a.warps;
   extern __shared__ float4 shared4[];
-  float *check = reinterpret_cast<float *>(shared4);    // [warps][SLOTS][SLOT]
-  float *s_delta = check + a.warps * SLOTS * SLOT;      // [TILE][CC]
-  float *s_u = s_delta + TILE * CC;                     // delta x
+  float *shared = reinterpret_cast<float *>(shared4);
+  float *s_delta = shared + Sh::WARPS * Sh::WARP;  // [TILE][CC]
+  float *s_u = s_delta + TILE * CC;
   float *s_gy = s_u + TILE * CC;
-  float *s_b = s_gy + TILE * CC;                        // [TILE][NP]
-  float *s_c = s_b + TILE * NP;
+  float(*s_b)[NP] = reinterpret_cast<float(*)[NP]>(s_gy + TILE * CC);
+  float(*s_c)[NP] = s_b + TILE;
+  float *s_bias = &s_c[TILE][0], *s_skip = s_bias + CC;  // dt_bias, d
 
   const int group = blockIdx.x % a.groups;
   const int b = (int)(blockIdx.x / a.groups % in.B), seg = (int)(blockIdx.x / a.groups / in.B);
@@ -65,303 +144,408 @@ __global__ void __launch_bounds__(128, 2) scan_bwd_kernel(const Args a, int *err
   const int ch0 = group * CC, own = warp * WC + cl * K;  // the thread's channels in the block
   const int n0 = l * S;
   const int64_t table = (int64_t)in.B * in.H * in.N;
+  const int64_t at0 = ((int64_t)b * in.H + ch0 + own) * in.N + n0;  // of [B][H][N]
   const int n = row_length(in.lengths, b, in.T, err);
   const int t0 = seg * a.seg.len, t1 = min(t0 + a.seg.len, in.T), end = min(t1, n);
-  float *mine = check + warp * SLOTS * SLOT;
+  float *check = shared + warp * Sh::WARP;    // [SLOTS][SLOT]
+  float *parts = check + SLOTS * SLOT + Sh::SUMS;  // [3][PARTS][PART]
+  float *swap = parts + 3 * PARTS * PART;     // [256]
 
-  int here[K];  // states that exist
-  int64_t at[K];
-  F2 A2[K][S / 2], e[K][S / 2], dA[K][S / 2];
+  auto here = [&](int c) { return ch0 + own + c < in.H ? min(max(in.N - n0, 0), S) : 0; };
+  auto load_all = [&](const float *from, F2 (&v)[S]) {
+    float x[S], y[S];
+    load_states(from, here(0), a.wide_states, x);
+    load_states(from + in.N, here(1), a.wide_states, y);
 #pragma unroll
-  for (int c = 0; c < K; ++c) {
-    const int ch = ch0 + own + c;
-    here[c] = ch < in.H ? min(max(in.N - n0, 0), S) : 0;
-    at[c] = ((int64_t)b * in.H + ch) * in.N + n0;
-    float v[S];
-    load_states(in.a_log + (int64_t)ch * in.N + n0, here[c], a.wide_states, v);
+    for (int k = 0; k < S; ++k) v[k] = f2(x[k], y[k]);
+  };
+  auto store_all = [&](float *to, const F2 (&v)[S]) {
 #pragma unroll
-    for (int k = 0; k < S; ++k) v[k] = k < here[c] ? rate2(v[k]) : 0.f;
+    for (int c = 0; c < K; ++c) {
+      float x[S];
 #pragma unroll
-    for (int k = 0; k < S / 2; ++k) A2[c][k] = f2(v[2 * k], v[2 * k + 1]);
-#pragma unroll
-    for (int k = 0; k < S; ++k) v[k] = 0.f;
-    if (a.enter) load_states(a.enter + (a.seg.n > 1 ? seg * table : 0) + at[c], here[c], a.wide_states, v);
-#pragma unroll
-    for (int k = 0; k < S / 2; ++k) {
-      e[c][k] = f2(v[2 * k], v[2 * k + 1]);
-      dA[c][k] = f2(0.f);
+      for (int k = 0; k < S; ++k) x[k] = c ? hi(v[k]) : lo(v[k]);
+      store_states(to + (int64_t)c * in.N, here(c), a.wide_states, x);
     }
+  };
+
+  F2 A2[S], e[S], dA[S];
+  load_all(in.a_log + (int64_t)(ch0 + own) * in.N + n0, A2);
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    A2[k] = f2(k < here(0) ? rate2(lo(A2[k])) : 0.f, k < here(1) ? rate2(hi(A2[k])) : 0.f);
+    e[k] = dA[k] = f2(0.f);
   }
-  // the channel whose sums over states this lane ends up with, if it is one of the
-  // first two lanes of its channels (with one lane: both)
-  constexpr int OWN = LANES == 1 ? K : 1;
-  float dd[OWN] = {}, ddtb[OWN] = {};
+  if (a.enter) load_all(a.enter + (a.seg.n > 1 ? seg * table : 0) + at0, e);
 
-  const T *x = static_cast<const T *>(in.x.p) + b * in.x.sb + ch0;
-  const T *dt = static_cast<const T *>(in.dt.p) + b * in.dt.sb + ch0;
-  const T *z = in.z.p ? static_cast<const T *>(in.z.p) + b * in.z.sb + ch0 : nullptr;
-  const T *dy = static_cast<const T *>(p.dy.p) + b * p.dy.sb + ch0;
-  const T *bw = static_cast<const T *>(in.b.p) + b * in.b.sb;
-  const T *cw = static_cast<const T *>(in.c.p) + b * in.c.sb;
-  T *dx = p.dx.p ? static_cast<T *>(p.dx.p) + b * p.dx.sb + ch0 : nullptr;
-  T *ddt = p.ddt.p ? static_cast<T *>(p.ddt.p) + b * p.ddt.sb + ch0 : nullptr;
-  T *dz = p.dz.p && z ? static_cast<T *>(p.dz.p) + b * p.dz.sb + ch0 : nullptr;
+  const T *x = static_cast<const T *>(in.x.p) + b * in.x.sb;
+  const T *dt = static_cast<const T *>(in.dt.p) + b * in.dt.sb;
+  const T *z = in.z.p ? static_cast<const T *>(in.z.p) + b * in.z.sb : nullptr;
+  const T *dy = static_cast<const T *>(p.dy.p) + b * p.dy.sb;
+  T *dx = p.dx.p ? static_cast<T *>(p.dx.p) + b * p.dx.sb : nullptr;
+  T *ddt = p.ddt.p ? static_cast<T *>(p.ddt.p) + b * p.ddt.sb : nullptr;
+  T *dz = p.dz.p ? static_cast<T *>(p.dz.p) + b * p.dz.sb : nullptr;
+  Weights<T, NT, TILE, NP> rb(static_cast<const T *>(in.b.p) + b * in.b.sb, in.b.st, in.N, a.wide_bc);
+  Weights<T, NT, TILE, NP> rc(static_cast<const T *>(in.c.p) + b * in.c.sb, in.c.st, in.N, a.wide_bc);
 
-  auto load_pairs_of = [&](const float *row, F2 (&v)[S / 2]) { load_pairs<S / 2>(row + n0, v); };
-  // h after a step, from the state before it; the decay where it is wanted
-  auto step = [&](int t, const F2 (&w)[S / 2], F2 (&h)[K][S / 2], F2 (*decay)[S / 2]) {
-    const float2 d = *reinterpret_cast<const float2 *>(s_delta + t * CC + own);
-    const float2 u = *reinterpret_cast<const float2 *>(s_u + t * CC + own);
+  // words of four channels of the tile's inputs (rows NT / ROW apart), and of two of the
+  // warp's outputs (a lane's are of the same channels)
+  const int in_col = tid % ROW * 4, in_row = tid / ROW, in_left = in.H - ch0 - in_col;
+  constexpr int OUT = WC / K;  // words of an output row
+  const int out_col = warp * WC + lane % OUT * K, out_row = lane / OUT, out_left = in.H - ch0 - out_col;
+  for (int c = tid; c < CC; c += NT) {
+    s_bias[c] = in.dt_bias && ch0 + c < in.H ? in.dt_bias[ch0 + c] : 0.f;
+    s_skip[c] = in.d && ch0 + c < in.H ? in.d[ch0 + c] : 0.f;
+  }
+  __syncthreads();
+  F2 dd = f2(0.f), ddtb = f2(0.f);  // of the lane's outputs
+
+  // h after step t of the tile, from the state before it
+  auto step = [&](int t, F2 (&h)[S]) {
+    const F2 d = pair_at(s_delta + t * CC + own), u = pair_at(s_u + t * CC + own);
+    float w[S];
+    load_row(s_b[t] + n0, w);
 #pragma unroll
-    for (int c = 0; c < K; ++c) {
-      const F2 d2 = f2(c ? d.y : d.x), u2 = f2(c ? u.y : u.x);
-#pragma unroll
-      for (int q = 0; q < S / 2; ++q) {
-        const F2 r = ex2_2(mul2(d2, A2[c][q]));
-        if (decay) decay[c][q] = r;
-        h[c][q] = fma2(r, h[c][q], mul2(u2, w[q]));
-      }
-    }
+    for (int q = 0; q < S; ++q) h[q] = fma2(ex2_2(mul2(d, A2[q])), h[q], mul2(u, f2(w[q])));
   };
-  auto save = [&](int slot, const F2 (&h)[K][S / 2]) {
-    ulonglong2 *to = reinterpret_cast<ulonglong2 *>(mine + slot * SLOT) + lane;
+  auto save = [&](int slot, const F2 (&h)[S]) {
+    ulonglong2 *to = reinterpret_cast<ulonglong2 *>(check + slot * SLOT) + lane;
 #pragma unroll
-    for (int q = 0; q < K * S / 4; ++q)
-      to[q * 32] = make_ulonglong2(h[q / 2][q % 2 * 2], h[q / 2][q % 2 * 2 + 1]);
+    for (int q = 0; q < S / 2; ++q) to[q * 32] = make_ulonglong2(h[2 * q], h[2 * q + 1]);
   };
-  auto restore = [&](int slot, F2 (&h)[K][S / 2]) {
-    const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(mine + slot * SLOT) + lane;
+  auto restore = [&](int slot, F2 (&h)[S]) {
+    const ulonglong2 *from = reinterpret_cast<const ulonglong2 *>(check + slot * SLOT) + lane;
 #pragma unroll
-    for (int q = 0; q < K * S / 4; ++q) {
+    for (int q = 0; q < S / 2; ++q) {
       const ulonglong2 v = from[q * 32];
-      h[q / 2][q % 2 * 2] = v.x;
-      h[q / 2][q % 2 * 2 + 1] = v.y;
+      h[2 * q] = v.x, h[2 * q + 1] = v.y;
     }
   };
-  auto first_states = [&](int base, F2 (&h)[K][S / 2]) {
+  auto copy = [](const F2 (&from)[S], F2 (&to)[S]) {
 #pragma unroll
-    for (int c = 0; c < K; ++c) {
-      float v[S];
-      load_states(p.states + (base / TILE) * table + at[c], here[c], a.wide_states, v);
-#pragma unroll
-      for (int k = 0; k < S / 2; ++k) h[c][k] = f2(v[2 * k], v[2 * k + 1]);
-    }
+    for (int q = 0; q < S; ++q) to[q] = from[q];
+  };
+  // where the warp's db and dc of a group of four steps are: in the place of its
+  // checkpoint; of the first group, which has none, behind those of the second
+  auto sums_of = [&](float *from, int sub) {
+    const int slot = sub + SLOTS - SUBS;
+    if (Sh::SUMS) return from + SLOTS * SLOT + sub * SUB * 2 * NP;
+    return from + (slot < 0 ? SUB * 2 * NP : slot * SLOT);
   };
 
   const int tiles = t0 < end ? ceil_div(end - t0, TILE) : 0;
   for (int k = tiles - 1; k >= 0; --k) {
-    const int base = t0 + k * TILE;
-    for (int i = tid; i < TILE * CC; i += NT) {
-      const int t = i / CC, c = i % CC;
-      float delta = 0.f, u = 0.f, gy = 0.f;
-      if (base + t < end && ch0 + c < in.H) {
-        const int64_t s = base + t;
-        delta = softplus(to_f(dt[s * in.dt.st + c]) + (in.dt_bias ? in.dt_bias[ch0 + c] : 0.f));
-        u = delta * to_f(x[s * in.x.st + c]);
-        gy = to_f(dy[s * p.dy.st + c]);
-        if (z) {
-          const float v = to_f(z[s * in.z.st + c]);
-          gy *= v * sigmoid(v);
-        }
+    const int base = t0 + k * TILE, steps = min(TILE, end - base), subs = ceil_div(steps, SUB);
+    rb.read(base, end);
+    rc.read(base, end);
+    const float *first = p.states + (base / TILE) * table + at0;  // the states before the tile
+    F2 h[S];
+    load_all(first, h);
+    constexpr int PASS = NT / ROW, MOST = 4;
+    constexpr int BATCH = TILE / PASS < MOST ? TILE / PASS : MOST;  // words in flight, of rows PASS apart
+#pragma unroll 1
+    for (int r0 = in_row; r0 < TILE; r0 += BATCH * PASS) {
+      Word<T, 4> wx[BATCH], wt[BATCH], wy[BATCH], wz[BATCH];
+#pragma unroll
+      for (int q = 0; q < BATCH; ++q) {
+        const int64_t t = base + r0 + q * PASS;
+        if (r0 + q * PASS >= steps || in_left <= 0) break;
+        wx[q] = load_four<ALIGNED>(x + t * in.x.st + ch0 + in_col, in_left);
+        wt[q] = load_four<ALIGNED>(dt + t * in.dt.st + ch0 + in_col, in_left);
+        wy[q] = load_four<ALIGNED>(dy + t * p.dy.st + ch0 + in_col, in_left);
+        if (z) wz[q] = load_four<ALIGNED>(z + t * in.z.st + ch0 + in_col, in_left);
       }
-      s_delta[i] = delta;
-      s_u[i] = u;
-      s_gy[i] = gy;
+#pragma unroll
+      for (int q = 0; q < BATCH; ++q) {
+        const int r = r0 + q * PASS;
+        Four v{}, u{}, g{};  // 0 past the row's end
+        if (r < steps && in_left > 0) {
+          v = pairs_of(wt[q]) + four(s_bias + in_col);
+          v = {softplus(v.a), softplus(v.b)};
+          u = v * pairs_of(wx[q]);
+          g = pairs_of(wy[q]);
+          if (z) {
+            const Four zs = pairs_of(wz[q]);
+            g = g * zs * sigmoid(zs);
+          }
+        }
+        put_four(s_delta + r * CC + in_col, v);
+        put_four(s_u + r * CC + in_col, u);
+        put_four(s_gy + r * CC + in_col, g);
+      }
     }
-    for (int i = tid; i < TILE * NP; i += NT) {
-      const int t = i / NP, m = i % NP;
-      const bool there = base + t < end && m < in.N;
-      s_b[i] = there ? to_f(bw[(base + t) * in.b.st + m]) : 0.f;
-      s_c[i] = there ? to_f(cw[(base + t) * in.c.st + m]) : 0.f;
-    }
-    F2 h[K][S / 2];
-    first_states(base, h);
+    rb.put(s_b);
+    rc.put(s_c);
     __syncthreads();
-    const int steps = min(TILE, end - base), subs = ceil_div(steps, SUB);
+    if (k > 0) {  // the tile before, into the second-level cache
+      constexpr int LINE = 128 / sizeof(T);  // values
+      for (int i = tid; i < TILE * ((CC + LINE - 1) / LINE); i += NT) {
+        const int64_t t = base - TILE + i % TILE;
+        const int c = ch0 + i / TILE * LINE;
+        if (c >= in.H) break;
+        prefetch(x + t * in.x.st + c);
+        prefetch(dt + t * in.dt.st + c);
+        prefetch(dy + t * p.dy.st + c);
+        if (z) prefetch(z + t * in.z.st + c);
+      }
+      const float *before = p.states + (base / TILE - 1) * table + ((int64_t)b * in.H + ch0) * in.N;
+      for (int i = tid * 32; i < min(CC, in.H - ch0) * in.N; i += NT * 32) prefetch(before + i);
+    }
     if (SLOTS == SUBS) save(0, h);
     for (int t = 0; t < (subs - 1) * SUB; ++t) {
-      F2 w[S / 2];
-      load_pairs_of(s_b + t * NP, w);
-      step(t, w, h, nullptr);
+      step(t, h);
       if (t % SUB == SUB - 1) save(t / SUB + SLOTS - (SUBS - 1), h);
     }
+#pragma unroll 1
     for (int sub = subs - 1; sub >= 0; --sub) {
-      const int slot = sub + SLOTS - SUBS;  // where its checkpoint is; before the first: none
-      F2 before[SUB][K][S / 2], decay[SUB][K][S / 2];
-      if (slot >= 0) {
-        if (sub < subs - 1) restore(slot, h);  // the last one's is at hand
-      } else if (subs > 1) {
-        first_states(base, h);
+      const int slot = sub + SLOTS - SUBS;
+      // AHEAD: the upper half of a slot, 16 bytes a lane; the first states are in those of
+      // slots 2 and 3
+      auto upper = [&](int of) { return check + of * SLOT + SLOT / 2; };
+      auto first_at = [&](int c) { return upper(2 + c) + lane * 4; };
+      if (AHEAD && a.wide_states && sub == 1) {
+#pragma unroll
+        for (int c = 0; c < K; ++c)
+          if (here(c) == S) copy_async<16>(first_at(c), first + (int64_t)c * in.N);
+          else *reinterpret_cast<float4 *>(first_at(c)) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      Word<T, 2> wx, wt, wy, wz;
+      auto read = [&](int r) {  // the words of the outputs at row r of the tile
+        const int64_t t = base + r;
+        if (r >= steps || out_left <= 0 || (Sh::WORDS < 32 && out_row >= SUB)) return;
+        wx = load_two<ALIGNED>(x + t * in.x.st + ch0 + out_col, out_left);
+        wt = load_two<ALIGNED>(dt + t * in.dt.st + ch0 + out_col, out_left);
+        if (z) {
+          wy = load_two<ALIGNED>(dy + t * p.dy.st + ch0 + out_col, out_left);
+          wz = load_two<ALIGNED>(z + t * in.z.st + ch0 + out_col, out_left);
+        }
+      };
+      // AHEAD: where the i-th of them waits, of fp32 the third and fourth in the next slot
+      // (the first steps, whose sums are in the upper half of slot 0, take slot 1)
+      const bool two_slots = sizeof(T) == 4, rest = !two_slots || slot + 1 < SLOTS;
+      auto word_at = [&](int i) {
+        const int of = slot < 0 ? 1 : slot;
+        float *to = two_slots ? upper(of + i / 2) + i % 2 * 64 + lane * 2 : upper(of) + i * 32 + lane;
+        return reinterpret_cast<Word<T, 2> *>(to);
+      };
+      auto read_ahead = [&]() {
+        const int r = sub * SUB + out_row;
+        const int64_t t = base + r;
+        if (r >= steps || out_left <= 0) return;
+        copy_async<sizeof(wx)>(word_at(0), x + t * in.x.st + ch0 + out_col);
+        copy_async<sizeof(wx)>(word_at(1), dt + t * in.dt.st + ch0 + out_col);
+        if (z && rest) {
+          copy_async<sizeof(wx)>(word_at(2), dy + t * p.dy.st + ch0 + out_col);
+          copy_async<sizeof(wx)>(word_at(3), z + t * in.z.st + ch0 + out_col);
+        }
+      };
+      auto start = [&](F2 (&h)[S]) {  // the states before the four steps
+        if (slot >= 0) {
+          restore(slot, h);
+        } else if (AHEAD && a.wide_states && subs > 1) {
+          float v[K][S];
+          load_row(first_at(0), v[0]);
+          load_row(first_at(1), v[1]);
+#pragma unroll
+          for (int q = 0; q < S; ++q) h[q] = f2(v[0][q], v[1][q]);
+        } else {
+          load_all(first, h);
+        }
+      };
+      constexpr int OUTS = LANES > 4 ? LANES / 4 : 1;  // sums over channels of a lane, at a step
+      float bc[SUB][OUTS];
+      F2 before[SUB][S];
+      auto back = [&](int j) {  // step j backwards; h after it
+        const int t = sub * SUB + j;
+        const F2 d = pair_at(s_delta + t * CC + own), u = pair_at(s_u + t * CC + own);
+        const F2 g = pair_at(s_gy + t * CC + own);
+        float w[S], v[S], db[S], dc[S];
+        load_row(s_b[t] + n0, w);
+        load_row(s_c[t] + n0, v);
+        F2 so, sd, sl;
+#pragma unroll
+        for (int q = 0; q < S; ++q) {
+          e[q] = fma2(g, f2(v[q]), e[q]);
+          so = q ? fma2(h[q], f2(v[q]), so) : mul2(h[q], f2(v[q]));
+          sd = q ? fma2(e[q], f2(w[q]), sd) : mul2(e[q], f2(w[q]));
+          db[q] = fmaf(hi(e[q]), hi(u), lo(e[q]) * lo(u));
+          dc[q] = fmaf(hi(h[q]), hi(g), lo(h[q]) * lo(g));
+          e[q] = mul2(e[q], ex2_2(mul2(d, A2[q])));
+          const F2 r = mul2(e[q], before[j][q]);
+          sl = q ? fma2(r, A2[q], sl) : mul2(r, A2[q]);
+          dA[q] = fma2(r, d, dA[q]);
+          h[q] = before[j][q];
+        }
+        // sums over the states, down to PARTS lanes
+#pragma unroll
+        for (int o = LANES / 2; o >= PARTS && o > 0; o /= 2) {
+          so = add2(so, __shfl_xor_sync(0xffffffffu, so, o));
+          sd = add2(sd, __shfl_xor_sync(0xffffffffu, sd, o));
+          sl = add2(sl, __shfl_xor_sync(0xffffffffu, sl, o));
+        }
+        float *to = parts + l % PARTS * PART + j * WC + cl * K;
+        if (LANES <= 4 || l < 4) {
+          *reinterpret_cast<F2 *>(to) = so;
+          *reinterpret_cast<F2 *>(to + PARTS * PART) = sd;
+          *reinterpret_cast<F2 *>(to + 2 * PARTS * PART) = sl;
+        }
+        // sums over the warp's channels: lane (cl, l) leaves 8 values, of b and c; the
+        // two halves of every other four lanes change places, to hit different banks
+        {
+          __syncwarp();
+          float4 *put = reinterpret_cast<float4 *>(swap) + lane * 2;
+          const int turn = lane >> 2 & 1;
+          put[turn] = make_float4(db[0], db[1], db[2], db[3]);
+          put[turn ^ 1] = make_float4(dc[0], dc[1], dc[2], dc[3]);
+          __syncwarp();
+          auto value = [&](int s, int i) { return swap[s * 8 + ((i >> 2) ^ (s >> 2 & 1)) * 4 + (i & 3)]; };
+          if (LANES <= 4) {
+            // output (l, i) by lanes of 8 sources each
+            const int i = lane / LANES % 8, from = lane / LANES / 8 * 8;
+            float s = 0.f;
+#pragma unroll
+            for (int m = 0; m < 8; ++m) s += value((from + m) * LANES + l, i);
+#pragma unroll
+            for (int o = 8 * LANES; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+            bc[j][0] = s;
+          } else {
+            // OUTS outputs of a lane: l, i = (lane / LANES) + 32 / LANES m
+#pragma unroll
+            for (int m = 0; m < OUTS; ++m) {
+              float s = 0.f;
+#pragma unroll
+              for (int f = 0; f < 32 / LANES; ++f) s += value(f * LANES + l, cl + 32 / LANES * m);
+              bc[j][m] = s;
+            }
+          }
+        }
+      };
+      if (AHEAD && sub == 0) fetched();
+      if (sub < subs - 1) start(h);  // the last ones are at hand
+      if (AHEAD) {
+        __syncwarp();  // all lanes have what was there
+        read_ahead();
       }
 #pragma unroll
       for (int j = 0; j < SUB; ++j) {
-#pragma unroll
-        for (int c = 0; c < K; ++c)
-#pragma unroll
-          for (int q = 0; q < S / 2; ++q) before[j][c][q] = h[c][q];
-        F2 w[S / 2];
-        load_pairs_of(s_b + (sub * SUB + j) * NP, w);
-        step(sub * SUB + j, w, h, decay[j]);
+        copy(h, before[j]);
+        step(sub * SUB + j, h);
       }
-      // the lanes' exchange is where the checkpoint was, or, of the first steps, the
-      // next one's, whose db and dc have been added by then
-      float *room = mine + max(slot, 0) * SLOT;
-      (void)room;
+#pragma unroll
+      for (int j = SUB - 1; j >= 0; --j) back(j);
+      if (a.part_bc) {
+        float *to = sums_of(check, sub);
+#pragma unroll
+        for (int j = 0; j < SUB; ++j)
+#pragma unroll
+          for (int m = 0; m < OUTS; ++m) {
+            const int i = LANES <= 4 ? lane / LANES % 8 : cl + 32 / LANES * m;
+            if (LANES > 4 || lane / LANES < 8) to[j * 2 * NP + (i >> 2) * NP + n0 + (i & 3)] = bc[j][m];
+          }
+      }
       __syncwarp();
+      // the outputs: dx = delta sd + gy d, ddt = (sl A + sd x) sigmoid(dt), dz = dy (so + d x) silu'(z)
 #pragma unroll
-      for (int j = SUB - 1; j >= 0; --j) {
-        const int t = sub * SUB + j;
-        F2 w[S / 2], v[S / 2], db[S / 2], dc[S / 2];
-        load_pairs_of(s_b + t * NP, w);
-        load_pairs_of(s_c + t * NP, v);
-        const float2 d = *reinterpret_cast<const float2 *>(s_delta + t * CC + own);
-        const float2 u = *reinterpret_cast<const float2 *>(s_u + t * CC + own);
-        const float2 g = *reinterpret_cast<const float2 *>(s_gy + t * CC + own);
-        float out[K], du[K], dlog[K];
-#pragma unroll
-        for (int c = 0; c < K; ++c) {
-          const F2 d2 = f2(c ? d.y : d.x), u2 = f2(c ? u.y : u.x), g2 = f2(c ? g.y : g.x);
-          F2 so, sd, sl;
-#pragma unroll
-          for (int q = 0; q < S / 2; ++q) {
-            e[c][q] = fma2(g2, v[q], e[c][q]);
-            so = q ? fma2(h[c][q], v[q], so) : mul2(h[c][q], v[q]);
-            sd = q ? fma2(e[c][q], w[q], sd) : mul2(e[c][q], w[q]);
-            db[q] = c ? fma2(e[c][q], u2, db[q]) : mul2(e[c][q], u2);
-            dc[q] = c ? fma2(h[c][q], g2, dc[q]) : mul2(h[c][q], g2);
-            e[c][q] = mul2(e[c][q], decay[j][c][q]);
-            const F2 r = mul2(e[c][q], before[j][c][q]);
-            sl = q ? fma2(r, A2[c][q], sl) : mul2(r, A2[c][q]);
-            dA[c][q] = fma2(r, d2, dA[c][q]);
-            h[c][q] = before[j][c][q];
-          }
-          out[c] = lo(so) + hi(so);
-          du[c] = lo(sd) + hi(sd);
-          dlog[c] = lo(sl) + hi(sl);
+      for (int i = 0; i < Sh::MINE; ++i) {
+        const int j = out_row + i * (32 / OUT), r = sub * SUB + j;
+        const int64_t t = base + r;
+        if (AHEAD) {
+          fetched();
+          wx = *word_at(0), wt = *word_at(1);
+          if (z && rest) wy = *word_at(2), wz = *word_at(3);
         }
-        // sums over the states: lane 0 of a channel pair gets the first one's, lane 1
-        // the second's
-        if (LANES > 1) {
-          float *const sums[3] = {out, du, dlog};
-#pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            const float keep = l & 1 ? sums[q][1] : sums[q][0], give = l & 1 ? sums[q][0] : sums[q][1];
-            float s = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-#pragma unroll
-            for (int o = 2; o < LANES; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-            sums[q][0] = s;
-          }
+        if (r >= steps || out_left <= 0 || (Sh::WORDS < 32 && j >= SUB)) continue;
+        if (!AHEAD) {
+          read(r);
+        } else if (z && !rest) {
+          wy = load_two<ALIGNED>(dy + t * p.dy.st + ch0 + out_col, out_left);
+          wz = load_two<ALIGNED>(z + t * in.z.st + ch0 + out_col, out_left);
         }
-        if (l < K && t < steps) {
+        const float *from = parts + j * WC + out_col - warp * WC;
+        F2 so = pair_at(from), sd = pair_at(from + PARTS * PART), sl = pair_at(from + 2 * PARTS * PART);
 #pragma unroll
-          for (int c = 0; c < OWN; ++c) {
-            const int ch = own + (LANES == 1 ? c : l);
-            if (ch0 + ch < in.H) {
-              const int64_t s = base + t;
-              const float xv = to_f(x[s * in.x.st + ch]);
-              const float delta = s_delta[t * CC + ch], gy = s_gy[t * CC + ch];
-              const float skip = p.in.d ? in.d[ch0 + ch] : 0.f;
-              if (dx) dx[s * p.dx.st + ch] = from_f<T>(fmaf(du[c], delta, gy * skip));
-              const float logit = to_f(dt[s * in.dt.st + ch]) + (in.dt_bias ? in.dt_bias[ch0 + ch] : 0.f);
-              // A2 is in units of log2(e)
-              const float gdt = fmaf(dlog[c], 1.f / LOG2E, du[c] * xv) * sigmoid(logit);
-              if (ddt) ddt[s * p.ddt.st + ch] = from_f<T>(gdt);
-              if (dz) {
-                const float zv = to_f(z[s * in.z.st + ch]), sg = sigmoid(zv);
-                const float total = p.in.d ? fmaf(skip, xv, out[c]) : out[c];
-                dz[s * p.dz.st + ch] =
-                    from_f<T>(to_f(dy[s * p.dy.st + ch]) * total * sg * fmaf(zv, 1.f - sg, 1.f));
-              }
-              ddtb[c] += gdt;
-              dd[c] = fmaf(gy, xv, dd[c]);
-            }
-          }
+        for (int m = 1; m < PARTS; ++m) {
+          so = add2(so, pair_at(from + m * PART));
+          sd = add2(sd, pair_at(from + (PARTS + m) * PART));
+          sl = add2(sl, pair_at(from + (2 * PARTS + m) * PART));
         }
-        if (a.part_bc) {
-          // sums over the warp's channels, then over the warps below
-          float val[2 * S];
-#pragma unroll
-          for (int q = 0; q < S / 2; ++q) {
-            val[2 * q] = lo(db[q]), val[2 * q + 1] = hi(db[q]);
-            val[S + 2 * q] = lo(dc[q]), val[S + 2 * q + 1] = hi(dc[q]);
-          }
-#pragma unroll
-          for (int q = 0; q < 2 * S; ++q)
-#pragma unroll
-            for (int o = LANES; o < 32; o *= 2) val[q] += __shfl_xor_sync(0xffffffffu, val[q], o);
-          // a group of four steps needs 4 * 2 * NP floats of its slot
-          float *to = mine + max(slot, 0) * SLOT + (slot < 0 ? SUB * 2 * NP : 0) + j * 2 * NP;
-          if (cl == 0) {
-#pragma unroll
-            for (int q = 0; q < S; ++q) {
-              to[n0 + q] = val[q];
-              to[NP + n0 + q] = val[S + q];
-            }
-          }
+        const F2 delta = pair_at(s_delta + r * CC + out_col), gy = pair_at(s_gy + r * CC + out_col);
+        const F2 skip = pair_at(s_skip + out_col), xv = pair_of(wx);
+        if (dx) {
+          F2 v = mul2(sd, delta);
+          if (in.d) v = fma2(gy, skip, v);
+          store_two<ALIGNED>(dx + t * p.dx.st + ch0 + out_col, out_left, v);
         }
+        // A2 is in units of log2(e)
+        const F2 gdt = mul2(fma2(sl, f2(1.f / LOG2E), mul2(sd, xv)),
+                            sigmoid2(add2(pair_of(wt), pair_at(s_bias + out_col))));
+        if (ddt) store_two<ALIGNED>(ddt + t * p.ddt.st + ch0 + out_col, out_left, gdt);
+        if (dz) {
+          const F2 zs = pair_of(wz), sg = sigmoid2(zs);
+          if (in.d) so = fma2(skip, xv, so);
+          const F2 slope = mul2(sg, fma2(zs, fma2(sg, f2(-1.f), f2(1.f)), f2(1.f)));
+          store_two<ALIGNED>(dz + t * p.dz.st + ch0 + out_col, out_left, mul2(mul2(pair_of(wy), so), slope));
+        }
+        ddtb = add2(ddtb, gdt);
+        dd = fma2(gy, xv, dd);
       }
+      __syncwarp();  // before the next steps' parts
     }
     __syncthreads();
     if (a.part_bc) {
-      float *to = a.part_bc + (int64_t)group * in.T * in.B * 2 * in.N;
-      for (int i = tid; i < steps * 2 * NP; i += NT) {
-        const int t = i / (2 * NP), m = i % (2 * NP), sub = t / SUB, slot = sub + SLOTS - SUBS;
-        const float *from = check + max(slot, 0) * SLOT + (slot < 0 ? SUB * 2 * NP : 0) + t % SUB * 2 * NP + m;
-        float s = 0.f;
-        for (int w = 0; w < a.warps; ++w) s += from[w * SLOTS * SLOT];
-        if (m % NP < in.N)
-          to[((int64_t)(base + t) * in.B + b) * 2 * in.N + (m / NP) * in.N + m % NP] = s;
+      // four neighbouring sums of a step at a time: [steps][2][N]
+      float *to = a.part_bc + (((int64_t)group * in.T + base) * in.B + b) * 2 * in.N;
+      const int64_t row = (int64_t)in.B * 2 * in.N;
+      constexpr int QUADS = 2 * NP / 4;
+      for (int i = tid; i < steps * QUADS; i += NT) {
+        const int t = i / QUADS, m = i % QUADS * 4, q = m % NP;
+        const float *from = sums_of(shared, t / SUB) + t % SUB * 2 * NP + m;
+        Four v = four(from);
+#pragma unroll
+        for (int w = 1; w < Sh::WARPS; ++w) v = v + four(from + w * Sh::WARP);
+        float *at = to + t * row + (m / NP) * in.N + q;
+        const float out[4] = {lo(v.a), hi(v.a), lo(v.b), hi(v.b)};
+        if (in.N % 4 == 0) {
+          if (q < in.N) *reinterpret_cast<float4 *>(at) = make_float4(out[0], out[1], out[2], out[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (q + j < in.N) at[j] = out[j];
+        }
       }
       __syncthreads();
     }
   }
   // past the row's end
-  for (int64_t i = tid; i < (int64_t)(t1 - max(t0, end)) * CC; i += NT) {
-    const int64_t t = max(t0, end) + i / CC;
-    const int c = (int)(i % CC);
-    if (ch0 + c >= in.H) continue;
+  const int past = max(t0, end);
+  for (int64_t i = tid; i < (int64_t)(t1 - past) * CC; i += NT) {
+    const int64_t t = past + i / CC;
+    const int c = ch0 + (int)(i % CC);
+    if (c >= in.H) continue;
     if (dx) dx[t * p.dx.st + c] = from_f<T>(0.f);
     if (ddt) ddt[t * p.ddt.st + c] = from_f<T>(0.f);
     if (dz) dz[t * p.dz.st + c] = from_f<T>(0.f);
   }
-  auto put = [&](float *to, const F2 (&v)[S / 2], int k, float scale2, const F2 *scale) {
-    float out[S];
+  if (seg == 0 && p.dh0) store_all(p.dh0 + at0, e);
+  if (!a.part) return;
+  float *to = a.part + ((int64_t)seg * in.B + b) * in.H * (in.N + 2);
 #pragma unroll
-    for (int q = 0; q < S / 2; ++q) {
-      out[2 * q] = lo(v[q]) * (scale ? lo(scale[q]) * scale2 : 1.f);
-      out[2 * q + 1] = hi(v[q]) * (scale ? hi(scale[q]) * scale2 : 1.f);
-    }
-    store_states(to, k, false, out);
-  };
-#pragma unroll
-  for (int c = 0; c < K; ++c) {
-    if (seg == 0 && p.dh0) put(p.dh0 + at[c], e[c], here[c], 1.f, nullptr);
-    if (a.part) {
-      float *to = a.part + ((int64_t)seg * in.B + b) * in.H * (in.N + 2);
-      put(to + (int64_t)(ch0 + own + c) * in.N + n0, dA[c], here[c], 1.f / LOG2E, A2[c]);
-    }
+  for (int q = 0; q < S; ++q) {
+    const F2 v = mul2(dA[q], mul2(A2[q], f2(1.f / LOG2E)));
+    float *at = to + (int64_t)(ch0 + own) * in.N + n0 + q;
+    if (q < here(0)) at[0] = lo(v);
+    if (q < here(1)) at[in.N] = hi(v);
   }
-  if (a.part && l < K) {
+  // lanes with the same channels of the outputs
 #pragma unroll
-    for (int c = 0; c < OWN; ++c) {
-      const int ch = ch0 + own + (LANES == 1 ? c : l);
-      if (ch < in.H) {
-        float *to = a.part + ((int64_t)seg * in.B + b) * in.H * (in.N + 2) + (int64_t)in.H * in.N;
-        to[ch] = dd[c];
-        to[in.H + ch] = ddtb[c];
-      }
-    }
+  for (int o = OUT; o < 32; o *= 2) {
+    dd = add2(dd, __shfl_xor_sync(0xffffffffu, dd, o));
+    ddtb = add2(ddtb, __shfl_xor_sync(0xffffffffu, ddtb, o));
   }
-}
-
-int lanes_of(int N) { return N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8; }
-template <typename F>
-cudaError_t by_lanes(int N, F f) {
-  switch (lanes_of(N)) {
-    case 1: return f(std::integral_constant<int, 1>());
-    case 2: return f(std::integral_constant<int, 2>());
-    case 4: return f(std::integral_constant<int, 4>());
-    default: return f(std::integral_constant<int, 8>());
+  if (out_row == 0) {
+    to += (int64_t)in.H * in.N + ch0 + out_col;
+    if (out_left > 0) to[0] = lo(dd), to[in.H] = lo(ddtb);
+    if (out_left > 1) to[1] = hi(dd), to[in.H + 1] = hi(ddtb);
   }
 }
 
@@ -382,23 +566,30 @@ __global__ void __launch_bounds__(256) sum_bc_kernel(const float *part, int grou
   static_cast<T *>(to.p)[t * to.st + b * to.sb + m % N] = from_f<T>(s);
 }
 
-template <typename T, int LANES>
+template <typename T, int LANES, bool ALIGNED>
 cudaError_t run(Args a, int *err, cudaStream_t s, int *launches) {
-  const size_t bytes = shared_bytes<LANES>(a.warps);
+  typedef Shape<LANES> Sh;
+  auto fn = scan_bwd_kernel<T, LANES, ALIGNED>;
   static PerDevice<cudaError_t> ready;
-  const cudaError_t set = ready.here([] {
-    return cudaFuncSetAttribute(scan_bwd_kernel<T, LANES>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)shared_bytes<LANES>(4));
-  });
+  const cudaError_t set = ready.here(
+      [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SHARED); });
   if (set != cudaSuccess) return set;
   ++*launches;
-  const int64_t blocks = (int64_t)a.groups * a.p.in.B * a.seg.n;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3(32 * a.warps);
-  cfg.dynamicSmemBytes = bytes;
+  cfg.gridDim = dim3((unsigned)((int64_t)a.groups * a.p.in.B * a.seg.n));
+  cfg.blockDim = dim3(Sh::NT);
+  cfg.dynamicSmemBytes = Sh::SHARED;
   cfg.stream = s;
-  return cudaLaunchKernelEx(&cfg, scan_bwd_kernel<T, LANES>, a, err);
+  return cudaLaunchKernelEx(&cfg, fn, a, err);
+}
+
+template <typename F>
+cudaError_t by_lanes(int N, F f) {
+  if (N <= 4) return f(std::integral_constant<int, 1>());
+  if (N <= 8) return f(std::integral_constant<int, 2>());
+  if (N <= 16) return f(std::integral_constant<int, 4>());
+  if (N <= 32) return f(std::integral_constant<int, 8>());
+  return f(std::integral_constant<int, 16>());
 }
 
 }  // namespace
@@ -409,10 +600,11 @@ cudaError_t launch_scan_bwd(const ScanBwd &p, DevMem &ws, int *err, int nsm, boo
   const int64_t table = (int64_t)in.B * in.H * in.N, rows = (int64_t)in.B * in.H;
   Args a{};
   a.p = p;
-  const int wc = 64 / lanes_of(in.N);
-  a.warps = std::min(ceil_div(in.H, wc), lanes_of(in.N) == 1 ? 2 : 4);
-  a.groups = ceil_div(in.H, wc * a.warps);
-  a.seg = segments_of(in.T, (int64_t)a.groups * in.B, nsm, 3);
+  by_lanes(in.N, [&](auto lanes) {
+    a.groups = ceil_div(in.H, Shape<decltype(lanes)::value>::CC);
+    return cudaSuccess;
+  });
+  a.seg = segments_of(in.T, (int64_t)a.groups * in.B, nsm, 4);
   const bool bc = p.db.p || p.dc.p, sums = p.da_log || p.dd || p.ddt_bias;
   const int64_t n_bc = bc ? (int64_t)a.groups * in.T * in.B * 2 * in.N : 0;
   const int64_t n_part = sums ? (int64_t)a.seg.n * in.B * in.H * (in.N + 2) : 0;
@@ -434,10 +626,17 @@ cudaError_t launch_scan_bwd(const ScanBwd &p, DevMem &ws, int *err, int nsm, boo
     a.enter = m.end;
   }
   a.wide_states = vec && in.N % S == 0 && aligned(in.a_log, 4, 4, 4) && aligned(p.states, 4, 4, 4) &&
-                  (!a.enter || aligned(a.enter, 4, 4, 4));
+                  (!a.enter || aligned(a.enter, 4, 4, 4)) && (!p.dh0 || aligned(p.dh0, 4, 4, 4));
+  const int size = in.dtype == RCU_BF16 ? 2 : 4;
+  a.wide_bc = vec && in.N % 4 == 0 && aligned(in.b, size, 4) && aligned(in.c, size, 4);
+  auto fits = [&](const auto &t) { return !t.p || aligned(t, size, 4); };
+  const bool wide = vec && in.H % 4 == 0 && fits(in.x) && fits(in.dt) && fits(in.z) && fits(p.dy) &&
+                    fits(p.dx) && fits(p.ddt) && fits(p.dz);
   cudaError_t e = by_lanes(in.N, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    return in.dtype == RCU_BF16 ? run<bf16, L>(a, err, s, launches) : run<float, L>(a, err, s, launches);
+    if (in.dtype == RCU_BF16)
+      return wide ? run<bf16, L, true>(a, err, s, launches) : run<bf16, L, false>(a, err, s, launches);
+    return wide ? run<float, L, true>(a, err, s, launches) : run<float, L, false>(a, err, s, launches);
   });
   if (e != cudaSuccess) return e;
   if (sums) {

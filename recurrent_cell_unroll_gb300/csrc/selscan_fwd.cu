@@ -292,15 +292,20 @@ __global__ void __launch_bounds__(128) chain_kernel(const float *a_log, const fl
   const int64_t row = i / N, rows = (int64_t)B * H;
   const float A2 = rate2(a_log[i % ((int64_t)H * N)]);
   float h = first ? first[i] : 0.f;
-  for (int k = 0; k < m.seg.n; ++k) {
-    const int s = BACKWARDS ? m.seg.n - 1 - k : k;
-    if (k == m.seg.n - 1) {  // nothing follows it
-      m.end[s * table + i] = h;
-      break;
+  constexpr int READ = 8;  // segments in flight
+  for (int k0 = 0; k0 < m.seg.n; k0 += READ) {
+    float own[READ], sum[READ];
+#pragma unroll
+    for (int k = 0; k < READ; ++k) {
+      const int s = BACKWARDS ? m.seg.n - 1 - k0 - k : k0 + k;
+      if (k0 + k < m.seg.n - 1) own[k] = m.end[s * table + i], sum[k] = m.sums[s * rows + row];
     }
-    const float own = m.end[s * table + i], decay = ex2(A2 * m.sums[s * rows + row]);
-    m.end[s * table + i] = h;
-    h = fmaf(decay, h, own);
+#pragma unroll
+    for (int k = 0; k < READ; ++k) {
+      if (k0 + k >= m.seg.n) break;
+      m.end[(BACKWARDS ? m.seg.n - 1 - k0 - k : k0 + k) * table + i] = h;
+      if (k0 + k < m.seg.n - 1) h = fmaf(ex2(A2 * sum[k]), h, own[k]);  // nothing follows the last
+    }
   }
 }
 
