@@ -13,6 +13,7 @@ cuDNN flat-storage clones + thread-local recurrent mode", pytorch/rl PR 3754).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -1199,43 +1200,45 @@ class SeqOps:
         if not (len(grads) == len(m) == len(v) == count) or (copies is not None
                                                             and len(copies) != count):
             raise ValueError("params, grads, m, v and copies must be lists of one length")
-        f32, bf16, types, device, keep = torch.float32, torch.bfloat16, self._DTYPES, self.device, []
-
-        def dense(t, name, k, like, dtype=None):
-            if (isinstance(t, torch.Tensor) and t.get_device() == device and t.is_contiguous()
-                    and t.shape == like.shape and (t.dtype in types if dtype is None
-                                                   else t.dtype is dtype)):
-                return t.data_ptr()
-            raise ValueError(f"{name}[{k}] must be a contiguous tensor on cuda:{device} of shape "
-                             f"{list(like.shape)} and type {dtype or 'float32 or bfloat16'}")
-
-        rows = []
-        for k, (p, g, mk, vk) in enumerate(zip(params, grads, m, v)):
-            if not isinstance(p, torch.Tensor):
-                raise ValueError(f"params[{k}] must be a tensor")
+        # A step of many small tensors is bound by this loop, so each tensor takes one
+        # pass of cheap checks.
+        f32, int8, types, device, keep = torch.float32, torch.int8, self._DTYPES, self.device, []
+        rows = array.array("q")
+        for k in range(count):
+            p, g, mk, vk = params[k], grads[k], m[k], v[k]
             if g is None:
-                rows += (None, None, None, None, None, None, None, 0, 0)
+                rows.extend((0,) * 9)
                 continue
-            me = ve = None
-            at_p, at_g, n = dense(p, "params", k, p), dense(g, "grads", k, p), p.numel()
-            if isinstance(mk, torch.Tensor) and isinstance(vk, torch.Tensor):
-                at_m, at_v = dense(mk, "m", k, p, f32), dense(vk, "v", k, p, f32)
-            else:
-                if isinstance(mk, torch.Tensor) or isinstance(vk, torch.Tensor):
-                    raise ValueError(f"m[{k}] and v[{k}] must be held alike")
-                (mk, me), (vk, ve) = mk, vk
-                at_m, at_v = dense(mk, "m", k, p, torch.int8), dense(vk, "v", k, p, torch.int8)
-                exps = (-(-n // RCU_STATE8_BLOCK),)
-                for t in (me, ve):
-                    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int8 and t.shape == exps
-                            and t.get_device() == device and t.is_contiguous()):
-                        raise ValueError(f"exponents of m[{k}] and v[{k}] must be contiguous int8 "
-                                         f"{list(exps)} on cuda:{device}")
-                me, ve = me.data_ptr(), ve.data_ptr()
             low = copies[k] if copies is not None else None
-            low = dense(low, "copies", k, p, bf16) if low is not None else None
-            rows += (at_p, at_g, at_m, at_v, me, ve, low, n, types[p.dtype] | types[g.dtype] << 32)
-        table = (ctypes.c_int64 * len(rows))(*[r or 0 for r in rows])
+            try:
+                n, me, ve = p.numel(), 0, 0
+                ok = (p.get_device() == device and g.get_device() == device and p.is_contiguous()
+                      and g.is_contiguous() and g.shape == p.shape)
+                kinds = types[p.dtype] | types[g.dtype] << 32
+                held = f32
+                if type(mk) is tuple:
+                    (mk, me), (vk, ve) = mk, vk
+                    held, blocks = int8, -(-n // RCU_STATE8_BLOCK)
+                    for e in (me, ve):
+                        ok = (ok and e.dtype is int8 and e.numel() == blocks and e.is_contiguous()
+                              and e.get_device() == device)
+                    me, ve = me.data_ptr(), ve.data_ptr()
+                ok = (ok and mk.dtype is held and vk.dtype is held and mk.numel() == n
+                      and vk.numel() == n and mk.is_contiguous() and vk.is_contiguous()
+                      and mk.get_device() == device and vk.get_device() == device)
+                if low is not None:
+                    ok = (ok and low.dtype is torch.bfloat16 and low.numel() == n
+                          and low.is_contiguous() and low.get_device() == device)
+                    low = low.data_ptr()
+            except (AttributeError, KeyError, TypeError, ValueError):
+                ok = False
+            if not ok:
+                raise ValueError(
+                    f"tensor {k}: params, grads (float32 or bfloat16), m, v (float32, or int8 codes "
+                    f"with exponents [ceil(n / {RCU_STATE8_BLOCK})], of both) and copies (bfloat16) "
+                    f"must be contiguous tensors of one shape on cuda:{device}")
+            rows.extend((p.data_ptr(), g.data_ptr(), mk.data_ptr(), vk.data_ptr(), me, ve, low or 0, n,
+                         kinds))
         on_dev = [None, None, None]
         for q, (t, dtype, name) in enumerate(((scale, f32, "scale"), (step, torch.int32, "step"),
                                               (lr, f32, "lr"))):
@@ -1244,7 +1247,7 @@ class SeqOps:
             elif q == 0 and t is not None:
                 raise ValueError("scale must be a tensor on a CUDA device")
         _check(self.lib.rcu_adamw_step(
-            self.h, count, ctypes.addressof(table), 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
+            self.h, count, rows.buffer_info()[0], 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
             weight_decay, 1 if on_dev[1] else step, seed & 0xffffffff, *on_dev, self._raw_stream()))
 
     def state8_pack(self, x, signed, stream=None):

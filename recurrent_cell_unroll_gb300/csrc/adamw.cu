@@ -1,7 +1,9 @@
 // AdamW over many tensors in few launches, states in 32 bits or in 8.
 //
-// Bound by memory: a parameter in fp32 moves 28 bytes with fp32 states, some 16
-// with 8-bit ones, for a dozen operations (and some sixty more for the codes).
+// Bound by memory with fp32 states: a parameter in fp32 moves 28 bytes for a dozen
+// operations.  With 8-bit ones it moves some 16, and the codes take fifty operations
+// more, which bound it as much: so what is rare (values that are not finite, codes
+// that stand for them, the ends of a tensor) leaves a warp's usual path.
 // The tensors' table comes as the kernel's parameter, so a captured launch keeps it
 // and nothing is copied or kept on the device; a block finds the tensor of its
 // piece of PIECE values by halving.
@@ -20,7 +22,8 @@ namespace {
 using namespace ssm;
 
 constexpr int NT = 256, V = 8;
-constexpr int PIECE = NT * V;  // values of a block: 32 blocks of 64
+constexpr int TURNS = 4;
+constexpr int PIECE = NT * V * TURNS;  // values of a block; a turn's are 32 blocks of 64
 
 struct Tensor {
   void *p;
@@ -177,6 +180,72 @@ __device__ __forceinline__ void encode(const float (&v)[V], const uint32_t (&bit
   if (threadIdx.x % 8 == 0 && n > 0) *exps = (int8_t)e;
 }
 
+// The same of whole words of a warp whose codes and values are all finite; false where
+// they are not (and then nothing is done).
+template <bool SIGNED>
+__device__ __forceinline__ bool decode_words(const uint2 &w, int e, float (&v)[V]) {
+  // a byte of 0 where a code stands for what is not finite
+  auto none = [](uint32_t t) { return ((t - 0x01010101u) & ~t & 0x80808080u) == 0; };
+  const uint32_t nan = SIGNED ? 0x80808080u : 0x7f7f7f7fu;
+  if (!__all_sync(0xffffffffu, none(w.x ^ nan) && none(w.y ^ nan))) return false;
+  const float scale = power(e);
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const uint32_t word = k < 4 ? w.x : w.y;
+    if (SIGNED) {
+      const int q = (int)(word << (24 - k % 4 * 8)) >> 24;
+      const float f = __fadd_rn(__int_as_float((abs(q) << 20) + (State8<true>::BASE << 20)), -State8<true>::offset());
+      v[k] = __fmul_rn(f, __int_as_float(__float_as_int(scale) | (q & 0x80000000)));
+    } else {
+      const int q = (word ^ 0x80808080u) >> (k % 4 * 8) & 255;
+      v[k] = __fmul_rn(__fadd_rn(__int_as_float((q << 20) + (State8<false>::BASE << 20)), -State8<false>::offset()),
+                       scale);
+    }
+  }
+  return true;
+}
+// `random`: a word an element, of which this state takes its half
+template <bool SIGNED>
+__device__ __forceinline__ bool encode_words(const float (&v)[V], const uint32_t (&random)[V], int8_t *codes,
+                                             int8_t *exps) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < V; ++k) top = max(top, __float_as_uint(v[k]) & (SIGNED ? 0x7fffffffu : 0xffffffffu));
+#pragma unroll
+  for (int o = 1; o < 8; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  // finite, and small enough that no code passes the last one
+  if (!__all_sync(0xffffffffu, top < 0x7f000000u)) return false;
+  const int e = max((int)(top >> 23) - 127, -126);
+  const float scale = power(-e);
+  constexpr uint32_t BASE = (uint32_t)State8<SIGNED>::BASE << 20;
+  uint32_t q[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const float f = __fadd_rn(__fmul_rn(fabsf(v[k]), scale), State8<SIGNED>::offset());
+    const uint32_t bits = (SIGNED ? random[k] << 4 : random[k] >> 12) & 0xffff0u;
+    const uint32_t n = (__float_as_uint(f) + bits + (8u - BASE)) >> 20;
+    if (SIGNED) {
+      const uint32_t s = (int)__float_as_uint(v[k]) >> 31;
+      q[k] = (n ^ s) - s;
+    } else {
+      q[k] = max(n, min(__float_as_uint(v[k]), 1u));
+    }
+  }
+  uint2 w;
+  w.x = __byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410);
+  w.y = __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410);
+  if (!SIGNED) w.x ^= 0x80808080u, w.y ^= 0x80808080u;
+  *reinterpret_cast<uint2 *>(codes) = w;
+  if (threadIdx.x % 8 == 0) *exps = (int8_t)e;
+  return true;
+}
+
+__device__ __forceinline__ float root(float v) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 template <int COUNT>
 struct Table {
   int count;
@@ -184,7 +253,7 @@ struct Table {
 };
 
 template <int COUNT>
-__global__ void __launch_bounds__(NT) adamw_kernel(const __grid_constant__ Table<COUNT> table,
+__global__ void __launch_bounds__(NT, 4) adamw_kernel(const __grid_constant__ Table<COUNT> table,
                                                    const __grid_constant__ Given given) {
   __shared__ Constants shared;
   if (given.s.step_dev || given.s.lr_dev) {
@@ -203,49 +272,69 @@ __global__ void __launch_bounds__(NT) adamw_kernel(const __grid_constant__ Table
     else hi = mid;
   }
   const Tensor &t = table.t[lo];
-  const int64_t i = (blockIdx.x - t.first) * PIECE + threadIdx.x * V;
-  const int64_t n = max((int64_t)0, t.n - i);  // all of a block's threads stay for the exchanges
-  const bool words = t.flags & WORDS;
-  float p[V], g[V], m[V], v[V];
-  if (t.flags & P16) load(static_cast<const bf16 *>(t.p) + i, n, words, p);
-  else load(static_cast<const float *>(t.p) + i, n, words, p);
-  if (t.flags & G16) load(static_cast<const bf16 *>(t.g) + i, n, words, g);
-  else load(static_cast<const float *>(t.g) + i, n, words, g);
-  int8_t *me = t.me + i / 64, *ve = t.ve + i / 64;
-  if (t.flags & STATES8) {
-    decode<true>(static_cast<const int8_t *>(t.m) + i, n > 0 ? *me : 0, n, words, m);
-    decode<false>(static_cast<const int8_t *>(t.v) + i, n > 0 ? *ve : 0, n, words, v);
-  } else {
-    load(static_cast<const float *>(t.m) + i, n, words, m);
-    load(static_cast<const float *>(t.v) + i, n, words, v);
-  }
+  const bool words = t.flags & WORDS, held8 = t.flags & STATES8;
   const float scale = given.s.scale ? *given.s.scale : 1.f;
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    if (given.s.scale) g[k] = __fmul_rn(g[k], scale);
-    // each product rounded by itself: a code's rounding is then the same everywhere
-    m[k] = __fadd_rn(__fmul_rn(m[k], c.beta1), __fmul_rn(g[k], c.one_beta1));
-    v[k] = __fadd_rn(__fmul_rn(v[k], c.beta2), __fmul_rn(__fmul_rn(g[k], c.one_beta2), g[k]));
-    const float step = __fdividef(m[k], fmaf(sqrtf(v[k]), c.root, c.eps));
-    p[k] = fmaf(-c.size, step, p[k] * c.kept);
-  }
-  if (t.flags & P16) store(static_cast<bf16 *>(t.p) + i, n, words, p);
-  else store(static_cast<float *>(t.p) + i, n, words, p);
-  if (t.copy) store(static_cast<bf16 *>(t.copy) + i, n, words, p);
-  if (t.flags & STATES8) {
-    const uint32_t key = mix(c.random + t.key);
-    uint32_t bm[V], bv[V];
+  const uint32_t key = mix(c.random + t.key);
+  const int64_t start = (blockIdx.x - t.first) * PIECE;
+#pragma unroll 1
+  for (int64_t at = start; at < min(start + PIECE, t.n); at += NT * V) {
+    const int64_t i = at + threadIdx.x * V;
+    const int64_t n = max((int64_t)0, t.n - i);  // all of a block's threads stay for the exchanges
+    float p[V], g[V], m[V], v[V];
+    if (t.flags & P16) load(static_cast<const bf16 *>(t.p) + i, n, words, p);
+    else load(static_cast<const float *>(t.p) + i, n, words, p);
+    if (t.flags & G16) load(static_cast<const bf16 *>(t.g) + i, n, words, g);
+    else load(static_cast<const float *>(t.g) + i, n, words, g);
+    int8_t *me = t.me + i / 64, *ve = t.ve + i / 64, *mc = static_cast<int8_t *>(t.m) + i;
+    int8_t *vc = static_cast<int8_t *>(t.v) + i;
+    const bool whole = held8 && words && __all_sync(0xffffffffu, n >= V);  // of the warp
+    if (held8) {
+      const int em = n > 0 ? *me : 0, ev = n > 0 ? *ve : 0;
+      if (whole) {
+        const uint2 wm = *reinterpret_cast<const uint2 *>(mc), wv = *reinterpret_cast<const uint2 *>(vc);
+        if (!decode_words<true>(wm, em, m)) decode<true>(mc, em, n, true, m);
+        if (!decode_words<false>(wv, ev, v)) decode<false>(vc, ev, n, true, v);
+      } else {
+        decode<true>(mc, em, n, words, m);
+        decode<false>(vc, ev, n, words, v);
+      }
+    } else {
+      load(static_cast<const float *>(t.m) + i, n, words, m);
+      load(static_cast<const float *>(t.v) + i, n, words, v);
+    }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const uint32_t r = mix((uint32_t)(i + k) ^ key);
-      bm[k] = (r & 0xffffu) << 4 | 8;
-      bv[k] = (r >> 16) << 4 | 8;
+      if (given.s.scale) g[k] = __fmul_rn(g[k], scale);
+      // each product rounded by itself: a code's rounding is then the same everywhere
+      m[k] = __fadd_rn(__fmul_rn(m[k], c.beta1), __fmul_rn(g[k], c.one_beta1));
+      v[k] = __fadd_rn(__fmul_rn(v[k], c.beta2), __fmul_rn(__fmul_rn(g[k], c.one_beta2), g[k]));
+      // the root keeps small v (an eps of 0 divides by it), the quotient is good to 2 units
+      p[k] = fmaf(-c.size, m[k] * rcp(fmaf(root(v[k]), c.root, c.eps)), p[k] * c.kept);
     }
-    encode<true>(m, bm, static_cast<int8_t *>(t.m) + i, me, n, words);
-    encode<false>(v, bv, static_cast<int8_t *>(t.v) + i, ve, n, words);
-  } else {
-    store(static_cast<float *>(t.m) + i, n, words, m);
-    store(static_cast<float *>(t.v) + i, n, words, v);
+    if (t.flags & P16) store(static_cast<bf16 *>(t.p) + i, n, words, p);
+    else store(static_cast<float *>(t.p) + i, n, words, p);
+    if (t.copy) store(static_cast<bf16 *>(t.copy) + i, n, words, p);
+    if (held8) {
+      uint32_t random[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) random[k] = mix(((uint32_t)i + k) ^ key);
+      const bool m_done = whole && encode_words<true>(m, random, mc, me);
+      const bool v_done = whole && encode_words<false>(v, random, vc, ve);
+      uint32_t bits[V];
+      if (!m_done) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) bits[k] = (random[k] & 0xffffu) << 4 | 8;
+        encode<true>(m, bits, mc, me, n, words);
+      }
+      if (!v_done) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) bits[k] = (random[k] >> 16) << 4 | 8;
+        encode<false>(v, bits, vc, ve, n, words);
+      }
+    } else {
+      store(static_cast<float *>(t.m) + i, n, words, m);
+      store(static_cast<float *>(t.v) + i, n, words, v);
+    }
   }
 }
 
@@ -270,7 +359,11 @@ __global__ void __launch_bounds__(NT) unpack_kernel(int64_t all, const int8_t *c
   const int64_t i = ((int64_t)blockIdx.x * NT + threadIdx.x) * V, n = all - i;
   if (n <= 0) return;
   float v[V];
-  decode<SIGNED>(codes + i, exps[i / 64], n, words, v);
+  const int e = exps[i / 64];
+  // (the last block's threads decide by themselves)
+  if (!(words && (int64_t)(blockIdx.x + 1) * NT * V <= all &&
+        decode_words<SIGNED>(*reinterpret_cast<const uint2 *>(codes + i), e, v)))
+    decode<SIGNED>(codes + i, e, n, words, v);
   store(y + i, n, words, v);
 }
 
@@ -334,7 +427,7 @@ cudaError_t launch_state8_pack(int is_signed, int64_t n, const float *x, int8_t 
                                int nsm, bool vec, cudaStream_t s, int *launches) {
   (void)nsm;
   ++*launches;
-  const unsigned blocks = (unsigned)((n + PIECE - 1) / PIECE);
+  const unsigned blocks = (unsigned)((n + NT * V - 1) / (NT * V));
   const bool words = vec && whole(x, 4) && whole(codes, 1);
   if (is_signed) pack_kernel<true><<<blocks, NT, 0, s>>>(n, x, codes, exps, words);
   else pack_kernel<false><<<blocks, NT, 0, s>>>(n, x, codes, exps, words);
@@ -345,7 +438,7 @@ cudaError_t launch_state8_unpack(int is_signed, int64_t n, const int8_t *codes, 
                                  float *y, int nsm, bool vec, cudaStream_t s, int *launches) {
   (void)nsm;
   ++*launches;
-  const unsigned blocks = (unsigned)((n + PIECE - 1) / PIECE);
+  const unsigned blocks = (unsigned)((n + NT * V - 1) / (NT * V));
   const bool words = vec && whole(y, 4) && whole(codes, 1);
   if (is_signed) unpack_kernel<true><<<blocks, NT, 0, s>>>(n, codes, exps, y, words);
   else unpack_kernel<false><<<blocks, NT, 0, s>>>(n, codes, exps, y, words);

@@ -8,7 +8,9 @@
 // and 6 W + 10 operations.  A thread keeps VEC channels and walks a stretch of
 // steps with the last W inputs (and, backwards, W gradients) in registers, so
 // that an input is read once but for the W - 1 that a stretch shares with the
-// one before it.
+// one before it.  Reads run 8 steps ahead by asynchronous copies into a ring of the
+// thread's own in shared memory (in registers they would cost half of the threads),
+// and channels are worked on as packed pairs.
 #include <type_traits>
 
 #include "per_device.h"
@@ -20,7 +22,7 @@ namespace {
 using namespace ssm;
 
 constexpr int NT = 128;
-constexpr int AHEAD = 8;      // steps whose reads are in flight together
+constexpr int AHEAD = 4, BATCHES = 4;  // steps that are read together, and how often in the ring
 constexpr int SHORTEST = 16;  // steps of a stretch, at least
 
 // Threads are numbered over groups of VEC channels, then rows (or runs of `per`
@@ -44,19 +46,27 @@ Split split_of(int T, int B, int H, int vec, int64_t room) {
   return s;
 }
 
+// VEC neighbouring values as pairs (of a single one: with a 0).
+template <int VEC>
+constexpr int pairs() { return (VEC + 1) / 2; }
 template <typename T, int VEC>
-__device__ __forceinline__ void load(const T *p, float (&v)[VEC]) {
-  const Word<T, VEC> w = *reinterpret_cast<const Word<T, VEC> *>(p);
+__device__ __forceinline__ void widen(const Word<T, VEC> &w, F2 (&v)[pairs<VEC>()]) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) v[j] = to_f(w.v[j]);
+  for (int j = 0; j < pairs<VEC>(); ++j)
+    v[j] = f2(to_f(w.v[2 * j]), VEC > 1 ? to_f(w.v[VEC > 1 ? 2 * j + 1 : 0]) : 0.f);
 }
 template <typename T, int VEC>
-__device__ __forceinline__ void store(T *p, const float (&v)[VEC]) {
+__device__ __forceinline__ Word<T, VEC> word(const T *p) {
+  return *reinterpret_cast<const Word<T, VEC> *>(p);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store(T *p, const F2 (&v)[pairs<VEC>()]) {
   Word<T, VEC> w;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) w.v[j] = from_f<T>(v[j]);
+  for (int j = 0; j < VEC; ++j) w.v[j] = from_f<T>(j % 2 ? hi(v[j / 2]) : lo(v[j / 2]));
   *reinterpret_cast<Word<T, VEC> *>(p) = w;
 }
+__device__ __forceinline__ F2 sigmoid2(F2 v) { return f2(sigmoid(lo(v)), sigmoid(hi(v))); }
 
 // Taps in registers: W, or, for W = 0, room for all the numbers of taps that a
 // call may have; the call's w_n are the last ones.
@@ -65,14 +75,16 @@ constexpr int taps() { return W ? W : RCU_CONV_MAX_TAPS; }
 
 template <int W, int VEC>
 __device__ __forceinline__ void load_taps(const float *weight, const float *bias, int h, int w_n,
-                                          float (&w)[taps<W>()][VEC], float (&add)[VEC]) {
+                                          F2 (&w)[taps<W>()][pairs<VEC>()], F2 (&add)[pairs<VEC>()]) {
   constexpr int MW = taps<W>();
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    add[j] = bias ? bias[h + j] : 0.f;
+  for (int j = 0; j < pairs<VEC>(); ++j) {
+    const int64_t a = h + 2 * j, b = VEC > 1 ? a + 1 : a;
+    add[j] = bias ? f2(bias[a], bias[b]) : f2(0.f);
 #pragma unroll
     for (int k = 0; k < MW; ++k)
-      w[k][j] = k >= MW - w_n ? weight[(int64_t)(h + j) * w_n + k - (MW - w_n)] : 0.f;
+      w[k][j] = k >= MW - w_n ? f2(weight[a * w_n + k - (MW - w_n)], weight[b * w_n + k - (MW - w_n)])
+                              : f2(0.f);
   }
 }
 
@@ -82,23 +94,23 @@ struct Row {
   const T *x, *state;  // at channel h; state rows are `wide` apart
   int64_t st;
   int w_n, wide;
-  __device__ __forceinline__ void at(int t, float (&v)[VEC]) const {
+  __device__ __forceinline__ void at(int t, F2 (&v)[pairs<VEC>()]) const {
     if (t >= 0) {
-      load<T, VEC>(x + t * st, v);
+      widen<T, VEC>(word<T, VEC>(x + t * st), v);
     } else if (state) {
-      load<T, VEC>(state + (int64_t)(t + w_n - 1) * wide, v);
+      widen<T, VEC>(word<T, VEC>(state + (int64_t)(t + w_n - 1) * wide), v);
     } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] = 0.f;
+      for (int j = 0; j < pairs<VEC>(); ++j) v[j] = f2(0.f);
     }
   }
   // the w_n - 1 inputs before step t, behind one another at the end of v
   template <int MW>
-  __device__ __forceinline__ void before(int t, float (&v)[MW][VEC]) const {
+  __device__ __forceinline__ void before(int t, F2 (&v)[MW][pairs<VEC>()]) const {
 #pragma unroll
     for (int k = 1; k < MW; ++k) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[k - 1][j] = 0.f;
+      for (int j = 0; j < pairs<VEC>(); ++j) v[k - 1][j] = f2(0.f);
       if (k > MW - w_n) at(t - (MW - k), v[k - 1]);
     }
   }
@@ -110,16 +122,97 @@ __device__ __forceinline__ Row<T, VEC> row_of(const SeqIn &x, const void *state,
           state ? static_cast<const T *>(state) + (int64_t)b * (w_n - 1) * H + h : nullptr, x.st,
           w_n, H};
 }
+// A thread's steps of a row from t0 to end, AHEAD at a time and BATCHES - 1 such
+// batches ahead: words of 4 bytes or more by asynchronous copies, single bf16 values by
+// plain reads one batch ahead.
+template <typename T, int VEC>
+struct Steps {
+  static constexpr bool ASYNC = sizeof(T) * VEC >= 4;
+  static constexpr int BYTES = ASYNC ? BATCHES * AHEAD * NT * VEC * sizeof(T) : 0;  // of a block
+  const T *p;
+  int64_t st;
+  Word<T, VEC> *ring;
+  int end, batch;
+  Word<T, VEC> next[ASYNC ? 1 : AHEAD];
+  __device__ __forceinline__ Steps(const Row<T, VEC> &row, void *room, int end_)
+      : p(row.x), st(row.st), ring(static_cast<Word<T, VEC> *>(room) + threadIdx.x), end(end_), batch(0) {}
+  __device__ __forceinline__ void fetch(int t, int k) {
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) {
+      if (t + q >= end) break;
+      const T *from = p + (t + q) * st;
+      if constexpr (ASYNC)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                         (uint32_t)__cvta_generic_to_shared(ring + (k * AHEAD + q) * NT)),
+                     "l"(from), "n"((int)sizeof(Word<T, VEC>)) : "memory");
+      else
+        next[q] = word<T, VEC>(from);
+    }
+  }
+  // the batch at t, once it has arrived
+  __device__ __forceinline__ void take(int t, Word<T, VEC> (&w)[AHEAD]) {
+    if constexpr (ASYNC) {
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) w[q] = ring[(batch * AHEAD + q) * NT];
+      batch = batch == BATCHES - 1 ? 0 : batch + 1;
+    } else {
+#pragma unroll
+      for (int q = 0; q < AHEAD; ++q) w[q] = next[q];
+      fetch(t + AHEAD, 0);
+    }
+  }
+};
+// The first batches of all of a thread's rows; then, before a batch is taken, the one
+// BATCHES - 1 behind it (a group of copies each), and the wait for the batch itself.
+template <typename... Rows>
+__device__ __forceinline__ void begin(int t0, Rows &...rows) {
+  constexpr bool ASYNC = (Rows::ASYNC && ...);
+#pragma unroll
+  for (int k = 0; k < (ASYNC ? BATCHES - 1 : 1); ++k) {
+    (rows.fetch(t0 + k * AHEAD, k), ...);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+}
+template <typename... Rows>
+__device__ __forceinline__ void ahead(int t, Rows &...rows) {
+  if constexpr ((Rows::ASYNC && ...)) {
+    (rows.fetch(t + (BATCHES - 1) * AHEAD, rows.batch == 0 ? BATCHES - 1 : rows.batch - 1), ...);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(BATCHES - 1) : "memory");
+  }
+}
+
+template <int N, int P>
+__device__ __forceinline__ void shift(F2 (&v)[N][P]) {
+#pragma unroll
+  for (int k = 0; k + 1 < N; ++k)
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[k][j] = v[k + 1][j];
+}
+// v = bias + taps times window
+template <int W, int VEC>
+__device__ __forceinline__ void filter(const F2 (&w)[taps<W>()][pairs<VEC>()], int w_n, const F2 (&bias)[pairs<VEC>()],
+                                       const F2 (&win)[taps<W>()][pairs<VEC>()], F2 (&v)[pairs<VEC>()]) {
+#pragma unroll
+  for (int j = 0; j < pairs<VEC>(); ++j) v[j] = bias[j];
+#pragma unroll
+  for (int k = 0; k < taps<W>(); ++k)
+    if (W || k >= taps<W>() - w_n) {
+#pragma unroll
+      for (int j = 0; j < pairs<VEC>(); ++j) v[j] = fma2(w[k][j], win[k][j], v[j]);
+    }
+}
 
 template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Split sp, int *err) {
-  constexpr int MW = taps<W>();
+  constexpr int MW = taps<W>(), P = pairs<VEC>();
   const int w_n = W ? W : a.W;
   const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
   if (id >= sp.threads()) return;
   const int h = (int)(id % sp.groups) * VEC, run = (int)(id / sp.groups % sp.runs);
   const int seg = (int)(id / sp.groups / sp.runs);
-  float w[MW][VEC], bias[VEC];
+  extern __shared__ float4 ring[];
+  F2 w[MW][P], bias[P];
   load_taps<W, VEC>(a.weight, a.bias, h, w_n, w, bias);
   const int t0 = seg * sp.len, t1 = min(t0 + sp.len, a.T);
   const int last_b = min((run + 1) * sp.per, a.B);
@@ -127,10 +220,12 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Spl
     const int n = row_length(a.lengths, b, a.T, err), end = min(t1, n);
     const Row<T, VEC> row = row_of<T, VEC>(a.x, a.state, b, h, w_n, a.H);
     T *y = static_cast<T *>(a.y.p) + b * a.y.sb + h;
-    float win[MW][VEC];  // the inputs of a step, the newest last
+    Steps<T, VEC> in(row, ring, end);
+    begin(t0, in);
+    F2 win[MW][P];  // the inputs of a step, the newest last
     if (t0 < end) row.before(t0, win);
     if (seg == 0 && a.state_n) {  // after the window: state_n may be the state itself
-      float last[MW][VEC];
+      F2 last[MW][P];
       row.before(n, last);
       T *out = static_cast<T *>(a.state_n) + (int64_t)b * (w_n - 1) * a.H + h;
 #pragma unroll
@@ -139,37 +234,26 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Spl
     }
     int t = t0;
     for (; t < end; t += AHEAD) {
-      Word<T, VEC> raw[AHEAD];
-#pragma unroll
-      for (int q = 0; q < AHEAD; ++q)
-        if (t + q < end) raw[q] = *reinterpret_cast<const Word<T, VEC> *>(row.x + (t + q) * row.st);
+      Word<T, VEC> now[AHEAD];
+      ahead(t, in);
+      in.take(t, now);
 #pragma unroll
       for (int q = 0; q < AHEAD; ++q) {
         if (t + q >= end) break;
-        float v[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          win[MW - 1][j] = to_f(raw[q].v[j]);
-          v[j] = bias[j];
-        }
-#pragma unroll
-        for (int k = 0; k < MW; ++k)
-          if (W || k >= MW - w_n) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) v[j] = fmaf(w[k][j], win[k][j], v[j]);
-          }
+        F2 v[P];
+        widen<T, VEC>(now[q], win[MW - 1]);
+        filter<W, VEC>(w, w_n, bias, win, v);
         if (a.silu) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) v[j] *= sigmoid(v[j]);
+          for (int j = 0; j < P; ++j) v[j] = mul2(v[j], sigmoid2(v[j]));
         }
         store<T, VEC>(y + (t + q) * a.y.st, v);
-#pragma unroll
-        for (int k = 0; k + 1 < MW; ++k)
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) win[k][j] = win[k + 1][j];
+        shift(win);
       }
     }
-    const float zero[VEC] = {};
+    F2 zero[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) zero[j] = f2(0.f);
     for (t = max(t0, end); t < t1; ++t) store<T, VEC>(y + t * a.y.st, zero);
   }
 }
@@ -180,114 +264,124 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Spl
 template <typename T, int W, int VEC>
 __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Split sp, float *part,
                                                       int *err) {
-  constexpr int MW = taps<W>(), READ = 4;
+  constexpr int MW = taps<W>(), P = pairs<VEC>();
   const int w_n = W ? W : a.W;
   const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
   if (id >= sp.threads()) return;
   const int h = (int)(id % sp.groups) * VEC, run = (int)(id / sp.groups % sp.runs);
   const int seg = (int)(id / sp.groups / sp.runs);
-  float w[MW][VEC], bias[VEC], dw[MW][VEC] = {}, db[VEC] = {};
+  extern __shared__ float4 ring[];
+  F2 w[MW][P], bias[P], dw[MW][P], db[P], zero[P];
   load_taps<W, VEC>(a.weight, a.bias, h, w_n, w, bias);
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    zero[j] = db[j] = f2(0.f);
+#pragma unroll
+    for (int k = 0; k < MW; ++k) dw[k][j] = f2(0.f);
+  }
   const int t0 = seg * sp.len, t1 = min(t0 + sp.len, a.T);
   const int last_b = min((run + 1) * sp.per, a.B);
   for (int b = run * sp.per; b < last_b; ++b) {
     const int n = row_length(a.lengths, b, a.T, err), end = min(t1, n);
     const Row<T, VEC> row = row_of<T, VEC>(a.x, a.state, b, h, w_n, a.H);
-    const T *dy = static_cast<const T *>(a.dy.p) + b * a.dy.sb + h;
+    const Row<T, VEC> row_dy = row_of<T, VEC>(a.dy, nullptr, b, h, w_n, a.H);
     T *dx = a.dx.p ? static_cast<T *>(a.dx.p) + b * a.dx.sb + h : nullptr;
     const T *dlast = a.dstate_n ? static_cast<const T *>(a.dstate_n) + (int64_t)b * (w_n - 1) * a.H + h
                                 : nullptr;
     T *dstate = a.dstate ? static_cast<T *>(a.dstate) + (int64_t)b * (w_n - 1) * a.H + h : nullptr;
     // steps whose dv is wanted: the stretch and the W - 1 after it; the ones past
     // the row's end have none, and only bring out what is still on its way
-    const int stop = t0 < end || seg == 0 ? end + w_n - 1 : t0;
-    float win[MW][VEC], grad[MW][VEC] = {};  // x and dv, the newest last
-    if (stop > t0 && t0 < n) row.before(t0, win);
-    for (int t = t0; t < stop; t += READ) {
-      Word<T, VEC> rx[READ], ry[READ];
+    const int stop = t0 < end || seg == 0 ? end + w_n - 1 : t0, live = min(stop, n);
+    F2 win[MW][P], grad[MW][P];  // x and dv, the newest last
 #pragma unroll
-      for (int q = 0; q < READ; ++q)
-        if (t + q < stop && t + q < n) {
-          rx[q] = *reinterpret_cast<const Word<T, VEC> *>(row.x + (t + q) * row.st);
-          ry[q] = *reinterpret_cast<const Word<T, VEC> *>(dy + (t + q) * a.dy.st);
-        }
+    for (int k = 0; k < MW; ++k)
 #pragma unroll
-      for (int q = 0; q < READ; ++q) {
-        if (t + q >= stop) break;
+      for (int j = 0; j < P; ++j) grad[k][j] = f2(0.f);
+    Steps<T, VEC> in_x(row, ring, live);
+    Steps<T, VEC> in_y(row_dy, reinterpret_cast<char *>(ring) + Steps<T, VEC>::BYTES, live);
+    begin(t0, in_x, in_y);
+    if (t0 < live) row.before(t0, win);
+    // Step t with its words; INNER: all that it touches is the row's and the stretch's.
+    auto step = [&](auto inner, int t, const Word<T, VEC> &wx, const Word<T, VEC> &wy) {
+      constexpr bool INNER = decltype(inner)::value;
+      if (INNER || t < n) {
+        F2 v[P];
+        widen<T, VEC>(wx, win[MW - 1]);
+        widen<T, VEC>(wy, grad[MW - 1]);
+        if (a.silu) {
+          filter<W, VEC>(w, w_n, bias, win, v);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) grad[MW - 1][j] = 0.f;
-        if (t + q < n) {
-          float v[VEC];
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            win[MW - 1][j] = to_f(rx[q].v[j]);
-            v[j] = bias[j];
-          }
-          if (a.silu) {
-#pragma unroll
-            for (int k = 0; k < MW; ++k)
-              if (W || k >= MW - w_n) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) v[j] = fmaf(w[k][j], win[k][j], v[j]);
-              }
-          }
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float s = sigmoid(v[j]);
-            const float slope = a.silu ? s * fmaf(v[j], 1.f - s, 1.f) : 1.f;
-            grad[MW - 1][j] = to_f(ry[q].v[j]) * slope;
-          }
-          if (t + q < t1) {
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) db[j] += grad[MW - 1][j];
-#pragma unroll
-            for (int k = 0; k < MW; ++k)
-              if (W || k >= MW - w_n) {
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) dw[k][j] = fmaf(grad[MW - 1][j], win[k][j], dw[k][j]);
-              }
+          for (int j = 0; j < P; ++j) {
+            const F2 s = sigmoid2(v[j]);
+            const F2 slope = mul2(s, fma2(v[j], fma2(s, f2(-1.f), f2(1.f)), f2(1.f)));
+            grad[MW - 1][j] = mul2(grad[MW - 1][j], slope);
           }
         }
-        // dx of the step w_n - 1 back: tap k met it at the gradient that stands at
-        // MW - 1 - k behind the oldest of the w_n
-        const int at = t + q - (w_n - 1);
-        if ((at >= t0 || seg == 0) && at < end) {
-          float v[VEC] = {};
-          if (dlast && at >= n - (w_n - 1)) load<T, VEC>(dlast + (int64_t)(at - n + w_n - 1) * a.H, v);
+        if (INNER || t < t1) {
+#pragma unroll
+          for (int j = 0; j < P; ++j) db[j] = add2(db[j], grad[MW - 1][j]);
 #pragma unroll
           for (int k = 0; k < MW; ++k)
             if (W || k >= MW - w_n) {
 #pragma unroll
-              for (int j = 0; j < VEC; ++j) {
-                const int newest = MW - 1 - k + (MW - w_n);  // of the gradients in grad
-                if (W) {
-                  v[j] = fmaf(w[k][j], grad[MW - 1 - k][j], v[j]);
-                } else {
-#pragma unroll
-                  for (int m = 0; m < MW; ++m)
-                    if (m == newest) v[j] = fmaf(w[k][j], grad[m][j], v[j]);
-                }
-              }
+              for (int j = 0; j < P; ++j) dw[k][j] = fma2(grad[MW - 1][j], win[k][j], dw[k][j]);
             }
-          if (at >= 0) {
-            if (dx) store<T, VEC>(dx + at * a.dx.st, v);
-          } else if (dstate) {
-            store<T, VEC>(dstate + (int64_t)(at + w_n - 1) * a.H, v);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j) grad[MW - 1][j] = f2(0.f);
+      }
+      // dx of the step w_n - 1 back, which tap k met as many steps later as it is from the
+      // last one
+      const int at = t - (w_n - 1);
+      if (INNER || ((at >= t0 || seg == 0) && at < end)) {
+        F2 v[P];
+        if (!INNER && dlast && at >= n - (w_n - 1))
+          widen<T, VEC>(word<T, VEC>(dlast + (int64_t)(at - n + w_n - 1) * a.H), v);
+        else
+#pragma unroll
+          for (int j = 0; j < P; ++j) v[j] = f2(0.f);
+#pragma unroll
+        for (int k = 0; k < MW; ++k) {
+          if (W) {
+#pragma unroll
+            for (int j = 0; j < P; ++j) v[j] = fma2(w[k][j], grad[MW - 1 - k][j], v[j]);
+          } else if (k >= MW - w_n) {
+            const int newest = MW - 1 - k + (MW - w_n);  // of the gradients in grad
+#pragma unroll
+            for (int m = 0; m < MW; ++m)
+              if (m == newest) {
+#pragma unroll
+                for (int j = 0; j < P; ++j) v[j] = fma2(w[k][j], grad[m][j], v[j]);
+              }
           }
         }
+        if (INNER || at >= 0) {
+          if (dx) store<T, VEC>(dx + at * a.dx.st, v);
+        } else if (dstate) {
+          store<T, VEC>(dstate + (int64_t)(at + w_n - 1) * a.H, v);
+        }
+      }
+      shift(win);
+      shift(grad);
+    };
+    const int from = t0 + w_n - 1;  // the step from which on dx comes out for the stretch
+    for (int t = t0; t < stop; t += AHEAD) {
+      Word<T, VEC> now_x[AHEAD], now_y[AHEAD];
+      ahead(t, in_x, in_y);
+      in_x.take(t, now_x);
+      in_y.take(t, now_y);
+      if (t >= from && t + AHEAD <= end) {
 #pragma unroll
-        for (int k = 0; k + 1 < MW; ++k)
+        for (int q = 0; q < AHEAD; ++q) step(std::true_type(), t + q, now_x[q], now_y[q]);
+      } else {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            win[k][j] = win[k + 1][j];
-            grad[k][j] = grad[k + 1][j];
-          }
+        for (int q = 0; q < AHEAD; ++q)
+          if (t + q < stop) step(std::false_type(), t + q, now_x[q], now_y[q]);
       }
     }
-    if (dx) {
-      const float zero[VEC] = {};
+    if (dx)
       for (int t = max(t0, end); t < t1; ++t) store<T, VEC>(dx + t * a.dx.st, zero);
-    }
   }
   if (!part) return;
   // [stretch, run][h, tap | bias]
@@ -296,8 +390,9 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Spl
   for (int j = 0; j < VEC; ++j) {
 #pragma unroll
     for (int k = 0; k < MW; ++k)
-      if (k >= MW - w_n) out[(int64_t)(h + j) * w_n + k - (MW - w_n)] = dw[k][j];
-    out[(int64_t)a.H * w_n + h + j] = db[j];
+      if (k >= MW - w_n)
+        out[(int64_t)(h + j) * w_n + k - (MW - w_n)] = j % 2 ? hi(dw[k][j / 2]) : lo(dw[k][j / 2]);
+    out[(int64_t)a.H * w_n + h + j] = j % 2 ? hi(db[j / 2]) : lo(db[j / 2]);
   }
 }
 
@@ -317,13 +412,11 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const ConvStep a, int *er
   float v[VEC] = {};
   if (slot >= 0) {
     T *state = static_cast<T *>(a.state) + slot * (a.W - 1) * a.H + h;
-    const Word<T, VEC> now =
-        *reinterpret_cast<const Word<T, VEC> *>(static_cast<const T *>(a.x) + b * a.ldx + h);
+    const Word<T, VEC> now = word<T, VEC>(static_cast<const T *>(a.x) + b * a.ldx + h);
     Word<T, VEC> in[RCU_CONV_MAX_TAPS];
 #pragma unroll
     for (int k = 0; k < RCU_CONV_MAX_TAPS; ++k)
-      if (k < a.W)
-        in[k] = k < a.W - 1 ? *reinterpret_cast<const Word<T, VEC> *>(state + (int64_t)k * a.H) : now;
+      if (k < a.W) in[k] = k < a.W - 1 ? word<T, VEC>(state + (int64_t)k * a.H) : now;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v[j] = a.bias ? a.bias[h + j] : 0.f;
 #pragma unroll
@@ -339,7 +432,10 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const ConvStep a, int *er
       for (int j = 0; j < VEC; ++j) v[j] *= sigmoid(v[j]);
     }
   }
-  store<T, VEC>(y, v);
+  Word<T, VEC> out;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) out.v[j] = from_f<T>(v[j]);
+  *reinterpret_cast<Word<T, VEC> *>(y) = out;
 }
 
 // Runs f with the kernel's number of taps: those of the usual widths known to the
@@ -357,38 +453,57 @@ cudaError_t by_taps(int W, F f) {
   }
 }
 
-// Threads of a kernel that fit on the GPU.
+// A kernel's launch: its shared memory allowed, and the threads that fit on the GPU.
+struct Room {
+  cudaError_t set;
+  int64_t threads;
+};
 template <typename K>
-int64_t room_of(K fn, int nsm) {
+Room room_of(K fn, int bytes, int nsm) {
+  Room r{cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), 0};
   int per = 1;
-  cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(&per, fn, NT, 0, 0);
-  return (int64_t)std::max(per, 1) * nsm * NT;
+  cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(&per, fn, NT, bytes, 0);
+  r.threads = (int64_t)std::max(per, 1) * nsm * NT;
+  return r;
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*fn)(KArgs...), const Split &sp, int bytes, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((sp.threads() + NT - 1) / NT));
+  cfg.blockDim = dim3(NT);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
 template <typename T, int VEC>
 cudaError_t fwd(const ConvFwd &p, int *err, int nsm, cudaStream_t s) {
   return by_taps<VEC>(p.W, [&](auto w) {
     auto fn = conv_fwd_kernel<T, decltype(w)::value, VEC>;
-    static PerDevice<int64_t> room;
-    const Split sp = split_of(p.T, p.B, p.H, VEC, room.here([&] { return room_of(fn, nsm); }));
-    fn<<<(unsigned)((sp.threads() + NT - 1) / NT), NT, 0, s>>>(p, sp, err);
-    return cudaGetLastError();
+    constexpr int bytes = Steps<T, VEC>::BYTES;
+    static PerDevice<Room> rooms;
+    const Room room = rooms.here([&] { return room_of(fn, bytes, nsm); });
+    if (room.set != cudaSuccess) return room.set;
+    const Split sp = split_of(p.T, p.B, p.H, VEC, room.threads);
+    return launch(fn, sp, bytes, s, p, sp, err);
   });
 }
 template <typename T, int VEC>
 cudaError_t bwd(const ConvBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s, int *launches) {
   return by_taps<VEC>(p.W, [&](auto w) {
     auto fn = conv_bwd_kernel<T, decltype(w)::value, VEC>;
-    static PerDevice<int64_t> room;
-    const Split sp = split_of(p.T, p.B, p.H, VEC, room.here([&] { return room_of(fn, nsm); }));
+    constexpr int bytes = 2 * Steps<T, VEC>::BYTES;
+    static PerDevice<Room> rooms;
+    const Room room = rooms.here([&] { return room_of(fn, bytes, nsm); });
+    if (room.set != cudaSuccess) return room.set;
+    const Split sp = split_of(p.T, p.B, p.H, VEC, room.threads);
     const int64_t rows = (int64_t)sp.runs * sp.stretches, cols = (int64_t)p.H * (p.W + 1);
     float *part = nullptr;
     if (p.dweight || p.dbias) {
       const cudaError_t e = ws.get(rows * cols * 4, &part);
       if (e != cudaSuccess) return e;
     }
-    fn<<<(unsigned)((sp.threads() + NT - 1) / NT), NT, 0, s>>>(p, sp, part, err);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch(fn, sp, bytes, s, p, sp, part, err);
     if (e != cudaSuccess || !part) return e;
     const ColumnSum sum{part, rows, cols, (int64_t)p.H * p.W, p.H, p.dweight, p.dbias, nullptr};
     return launch_column_sum(sum, s, launches);
