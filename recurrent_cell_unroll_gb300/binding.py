@@ -710,8 +710,9 @@ class RSSM:
 
 class SeqOps:
     """The sequence operators (gated linear recurrence, layer norm, 8-bit
-    activation checkpoints; see rcu.h) on torch tensors of the device that was
-    current when it was made.
+    activation checkpoints, short convolution, selective scan) and the AdamW
+    step (see rcu.h) on torch tensors of the device that was current when it
+    was made.
 
     Matrices are float32 or bfloat16.  A tensor whose rows are dense and evenly
     spaced (a slice of a wider tensor's last dimension) is used in place, one
@@ -1249,6 +1250,8 @@ class SeqOps:
         _check(self.lib.rcu_adamw_step(
             self.h, count, rows.buffer_info()[0], 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
             weight_decay, 1 if on_dev[1] else step, seed & 0xffffffff, *on_dev, self._raw_stream()))
+        # autograd is told of the change: a graph that has saved a parameter refuses to go on
+        torch.autograd.graph.increment_version([p for p, g in zip(params, grads) if g is not None])
 
     def state8_pack(self, x, signed, stream=None):
         """(codes like x, exponents [ceil(n / 64)]) of an 8-bit optimizer state:

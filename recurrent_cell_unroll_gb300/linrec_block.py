@@ -24,6 +24,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding
+from .adamw import AdamW
 
 C = 8.0  # the recurrence's constant
 
@@ -136,9 +137,10 @@ def main(argv=None):
     p.add_argument("--B", type=int, default=16)
     p.add_argument("--delay", type=int, default=4, help="steps after which the input is to be repeated")
     p.add_argument("--act8", action="store_true", help="keep activations in 8 bits")
+    p.add_argument("--opt8", action="store_true", help="keep the optimizer's states in 8 bits")
     a = p.parse_args(argv)
     net = LinRecStack(a.layers, a.dim, a.hidden)
-    opt = torch.optim.Adam(net.parameters(), lr=3e-3)
+    opt = AdamW(net.parameters(), lr=3e-3, weight_decay=0.0, state_bits=8 if a.opt8 else 32, ops=net.ops)
     g = torch.Generator(device="cuda").manual_seed(1)
     losses = []
     for _ in range(a.steps):
