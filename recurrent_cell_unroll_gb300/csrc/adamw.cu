@@ -6,7 +6,7 @@
 // that stand for them, the ends of a tensor) leaves a warp's usual path.
 // The tensors' table comes as the kernel's parameter, so a captured launch keeps it
 // and nothing is copied or kept on the device; a block finds the tensor of its
-// piece of PIECE values by halving.
+// piece by halving.
 //
 // 8-bit states (include/rcu.h has the format): 8 threads that stand side by side
 // hold a block of 64 values, 8 of them each, and find its largest magnitude by
@@ -22,8 +22,11 @@ namespace {
 using namespace ssm;
 
 constexpr int NT = 256, V = 8;
-constexpr int TURNS = 4;
-constexpr int PIECE = NT * V * TURNS;  // values of a block; a turn's are 32 blocks of 64
+constexpr int TURN = NT * V;  // values of a block at a time: 32 blocks of 64
+// A block takes as many turns as leave eight blocks an SM, 8 at most: finding its tensor
+// costs as much as a turn's arithmetic on 3 values a thread (8-bit states, 51M
+// parameters, 218 us with one turn, 180 with four, 170 with eight).
+constexpr int MOST_TURNS = 8;
 
 struct Tensor {
   void *p;
@@ -48,6 +51,7 @@ struct Constants {
 struct Given {
   AdamWStep s;
   Constants c;
+  int piece;  // values of a block
 };
 
 __host__ __device__ inline uint32_t mix(uint32_t x) {
@@ -275,9 +279,9 @@ __global__ void __launch_bounds__(NT, 4) adamw_kernel(const __grid_constant__ Ta
   const bool words = t.flags & WORDS, held8 = t.flags & STATES8;
   const float scale = given.s.scale ? *given.s.scale : 1.f;
   const uint32_t key = mix(c.random + t.key);
-  const int64_t start = (blockIdx.x - t.first) * PIECE;
+  const int64_t start = (blockIdx.x - t.first) * given.piece;
 #pragma unroll 1
-  for (int64_t at = start; at < min(start + PIECE, t.n); at += NT * V) {
+  for (int64_t at = start; at < min(start + given.piece, t.n); at += TURN) {
     const int64_t i = at + threadIdx.x * V;
     const int64_t n = max((int64_t)0, t.n - i);  // all of a block's threads stay for the exchanges
     float p[V], g[V], m[V], v[V];
@@ -386,8 +390,10 @@ cudaError_t launch(const Tensor *t, int count, int64_t pieces, const Given &give
 
 cudaError_t launch_adamw(const AdamWStep &p, int64_t count, const rcu_adamw_tensor *tensors,
                          int nsm, bool vec, cudaStream_t s, int *launches) {
-  (void)nsm;
-  Given given{p, {}};
+  int64_t turns = 0;
+  for (int64_t k = 0; k < count; ++k) turns += (tensors[k].n + TURN - 1) / TURN;
+  Given given{p, {}, 0};
+  given.piece = TURN * (int)std::min<int64_t>(std::max<int64_t>(turns / (8 * nsm), 1), MOST_TURNS);
   Constants &c = given.c;
   c.beta1 = (float)p.beta1, c.one_beta1 = (float)(1.0 - p.beta1);
   c.beta2 = (float)p.beta2, c.one_beta2 = (float)(1.0 - p.beta2);
@@ -407,7 +413,7 @@ cudaError_t launch_adamw(const AdamWStep &p, int64_t count, const rcu_adamw_tens
   for (int64_t k = 0; k < count; ++k) {
     const rcu_adamw_tensor &a = tensors[k];
     if (a.n == 0) continue;
-    const int64_t need = (a.n + PIECE - 1) / PIECE;
+    const int64_t need = (a.n + given.piece - 1) / given.piece;
     if (held == MOST || pieces + need > INT32_MAX) {
       const cudaError_t e = flush();
       if (e != cudaSuccess) return e;
@@ -427,7 +433,7 @@ cudaError_t launch_state8_pack(int is_signed, int64_t n, const float *x, int8_t 
                                int nsm, bool vec, cudaStream_t s, int *launches) {
   (void)nsm;
   ++*launches;
-  const unsigned blocks = (unsigned)((n + NT * V - 1) / (NT * V));
+  const unsigned blocks = (unsigned)((n + TURN - 1) / TURN);
   const bool words = vec && whole(x, 4) && whole(codes, 1);
   if (is_signed) pack_kernel<true><<<blocks, NT, 0, s>>>(n, x, codes, exps, words);
   else pack_kernel<false><<<blocks, NT, 0, s>>>(n, x, codes, exps, words);
@@ -438,7 +444,7 @@ cudaError_t launch_state8_unpack(int is_signed, int64_t n, const int8_t *codes, 
                                  float *y, int nsm, bool vec, cudaStream_t s, int *launches) {
   (void)nsm;
   ++*launches;
-  const unsigned blocks = (unsigned)((n + NT * V - 1) / (NT * V));
+  const unsigned blocks = (unsigned)((n + TURN - 1) / TURN);
   const bool words = vec && whole(y, 4) && whole(codes, 1);
   if (is_signed) unpack_kernel<true><<<blocks, NT, 0, s>>>(n, codes, exps, y, words);
   else unpack_kernel<false><<<blocks, NT, 0, s>>>(n, codes, exps, y, words);

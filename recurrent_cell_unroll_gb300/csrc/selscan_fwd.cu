@@ -47,10 +47,10 @@ constexpr int shared_bytes() {
 }
 
 template <typename T, int S, int LANES, bool ALIGNED, Mode MODE>
-__global__ void __launch_bounds__(Shape<S, LANES>::NT) scan_kernel(const Args a, int *err) {
+__global__ void __launch_bounds__(Shape<S, LANES>::NT, LANES == 4 ? 7 : 1) scan_kernel(const Args a, int *err) {
   typedef Shape<S, LANES> Sh;
   constexpr int NT = Sh::NT, CC = Sh::CC, NP = Sh::NP, BUF = Sh::BUF, PARTS = Sh::PARTS;
-  constexpr int U = 2;                 // steps worked on together
+  constexpr int U = 4;                 // steps worked on together
   constexpr int RAW = MODE == ENDS ? 2 : 3;
   constexpr int ROW = CC / 4, EV = (TILE * ROW + NT - 1) / NT;  // words of four of a thread, of the same channels
   constexpr bool IDLE = TILE * ROW < NT;  // some threads have none
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(Shape<S, LANES>::NT) scan_kernel(const Args a,
           }
       }
       if (MODE == MAIN) {
-        // down to PARTS lanes: of 8, every half of them takes one of the steps, of 16, a
-        // half of its channels
+        // down to PARTS lanes: of 8, every half of them takes two of the steps, of 16, a
+        // quarter one
         int at = 0, count = U * P;
         F2 *sum = &v[0][0];
 #pragma unroll
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(128) chain_kernel(const float *a_log, const fl
   const int64_t row = i / N, rows = (int64_t)B * H;
   const float A2 = rate2(a_log[i % ((int64_t)H * N)]);
   float h = first ? first[i] : 0.f;
-  constexpr int READ = 8;  // segments in flight
+  constexpr int READ = 16;  // segments in flight
   for (int k0 = 0; k0 < m.seg.n; k0 += READ) {
     float own[READ], sum[READ];
 #pragma unroll

@@ -134,7 +134,7 @@ def test_adamw_lists(lib, handle):  # noqa: F811
     assert step(lib, h, rows_of((0, 0, 0, 0, 0, 0, 0, 0, 0))) == 0 and lib.rcu_seq_last_launch_count(h) == 0
     # pieces of all tensors together beyond what one launch counts
     big = (P, P, P, P, 0, 0, 0, 1 << 40, 0)
-    assert step(lib, h, rows_of(big, *[big] * 20), 21) == 0 and lib.rcu_seq_last_launch_count(h) >= 2
+    assert step(lib, h, rows_of(*[big] * 40), 40) == 0 and lib.rcu_seq_last_launch_count(h) >= 2
     for bad, code in (((0, P, P, P, 0, 0, 0, 1, 0), INVALID), ((P, P, P, P, 0, 0, 0, -1, 0), INVALID),
                       ((P, P, P, P, P, 0, 0, 1, 0), INVALID), ((P, P, P, P, 0, 0, P, 1, bf16), INVALID),
                       ((P, P, P, P, 0, 0, 0, 1, 2), INVALID), ((P, P, P, P, P, P, 0, (1 << 32) + 1, 0), UNSUPPORTED),
