@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 import threading
 from typing import Optional
@@ -708,6 +709,11 @@ class RSSM:
             pass
 
 
+_POINTER_OF, _SIZE_OF = torch.Tensor.data_ptr, torch.Tensor.numel
+_DEVICE_OF, _CONTIGUOUS = torch.Tensor.get_device, torch.Tensor.is_contiguous
+_DTYPE_OF = operator.attrgetter("dtype")
+
+
 class SeqOps:
     """The sequence operators (gated linear recurrence, layer norm, 8-bit
     activation checkpoints, short convolution, selective scan) and the AdamW
@@ -1187,8 +1193,8 @@ class SeqOps:
                    weight_decay=0.01, scale=None, seed=0, copies=None, stream=None):
         """One step of lists of tensors, in place.  params, grads: float32 or
         bfloat16 (a grad of None leaves its tensor out); m, v: float32 tensors
-        like the parameters, or 8-bit states (codes int8 like the parameter,
-        exponents int8 [ceil(n / 64)]), of both alike.  step (from 1) and lr
+        of the parameters' sizes, or 8-bit states (tuples: codes int8 of the
+        parameter's size, exponents int8 [ceil(n / 64)]), of both alike.  step (from 1) and lr
         are numbers, or tensors of one int32 and one float32 on the device,
         which a captured step then follows; scale: a float32 on the device that
         gradients are multiplied by; seed: of the 8-bit states' rounding.
@@ -1201,45 +1207,68 @@ class SeqOps:
         if not (len(grads) == len(m) == len(v) == count) or (copies is not None
                                                             and len(copies) != count):
             raise ValueError("params, grads, m, v and copies must be lists of one length")
-        # A step of many small tensors is bound by this loop, so each tensor takes one
-        # pass of cheap checks.
-        f32, int8, types, device, keep = torch.float32, torch.int8, self._DTYPES, self.device, []
-        rows = array.array("q")
-        for k in range(count):
-            p, g, mk, vk = params[k], grads[k], m[k], v[k]
-            if g is None:
-                rows.extend((0,) * 9)
-                continue
-            low = copies[k] if copies is not None else None
+        # A step of many small tensors is bound by these checks, so a list takes one pass
+        # for each of them in C (map), and the table is filled by columns.
+        keep, f32, types = [], torch.float32, self._DTYPES
+        live = [k for k in range(count) if grads[k] is not None]
+        if len(live) < count:
+            params, grads, m, v = ([ts[k] for k in live] for ts in (params, grads, m, v))
+            copies = [copies[k] for k in live] if copies is not None else None
+        rows = array.array("q", bytes(72 * count))
+
+        def column(at, values):
+            if len(live) == count:
+                rows[at::9] = array.array("q", values)
+            else:
+                for k, value in zip(live, values):
+                    rows[9 * k + at] = value
+
+        def pointers(ts, name, sizes, dtype=None):
             try:
-                n, me, ve = p.numel(), 0, 0
-                ok = (p.get_device() == device and g.get_device() == device and p.is_contiguous()
-                      and g.is_contiguous() and g.shape == p.shape)
-                kinds = types[p.dtype] | types[g.dtype] << 32
-                held = f32
-                if type(mk) is tuple:
-                    (mk, me), (vk, ve) = mk, vk
-                    held, blocks = int8, -(-n // RCU_STATE8_BLOCK)
-                    for e in (me, ve):
-                        ok = (ok and e.dtype is int8 and e.numel() == blocks and e.is_contiguous()
-                              and e.get_device() == device)
-                    me, ve = me.data_ptr(), ve.data_ptr()
-                ok = (ok and mk.dtype is held and vk.dtype is held and mk.numel() == n
-                      and vk.numel() == n and mk.is_contiguous() and vk.is_contiguous()
-                      and mk.get_device() == device and vk.get_device() == device)
-                if low is not None:
-                    ok = (ok and low.dtype is torch.bfloat16 and low.numel() == n
-                          and low.is_contiguous() and low.get_device() == device)
-                    low = low.data_ptr()
-            except (AttributeError, KeyError, TypeError, ValueError):
+                found = set(map(_DTYPE_OF, ts))
+                ok = (all(map(_CONTIGUOUS, ts)) and set(map(_DEVICE_OF, ts)) <= {self.device}
+                      and (found <= {dtype} if dtype else found <= types.keys())
+                      and (sizes is None or list(map(_SIZE_OF, ts)) == sizes))
+            except (AttributeError, TypeError):
                 ok = False
             if not ok:
-                raise ValueError(
-                    f"tensor {k}: params, grads (float32 or bfloat16), m, v (float32, or int8 codes "
-                    f"with exponents [ceil(n / {RCU_STATE8_BLOCK})], of both) and copies (bfloat16) "
-                    f"must be contiguous tensors of one shape on cuda:{device}")
-            rows.extend((p.data_ptr(), g.data_ptr(), mk.data_ptr(), vk.data_ptr(), me, ve, low or 0, n,
-                         kinds))
+                raise ValueError(f"{name} must be contiguous tensors on cuda:{self.device} of type "
+                                 f"{dtype or 'float32 or bfloat16'} and of the parameters' sizes")
+            return list(map(_POINTER_OF, ts))
+
+        column(0, pointers(params, "params", None))
+        sizes = list(map(_SIZE_OF, params))
+        column(1, pointers(grads, "grads", sizes))
+        column(7, sizes)
+        column(8, [types[p] | types[g] << 32
+                   for p, g in zip(map(_DTYPE_OF, params), map(_DTYPE_OF, grads))])
+        for at, name, held, other in ((2, "m", m, v), (3, "v", v, m)):
+            eight = [k for k, t in enumerate(held) if type(t) is tuple]
+            if not eight:
+                column(at, pointers(held, name, sizes, f32))
+                continue
+            if any(type(other[k]) is not tuple for k in eight):
+                raise ValueError("m and v of a tensor must be held alike")
+            wide = [k for k, t in enumerate(held) if type(t) is not tuple]
+            at_codes = pointers([held[k][0] for k in eight], f"{name}'s codes", [sizes[k] for k in eight],
+                                torch.int8)
+            at_exps = pointers([held[k][1] for k in eight], f"{name}'s exponents",
+                               [-(-sizes[k] // RCU_STATE8_BLOCK) for k in eight], torch.int8)
+            values, exps = [0] * len(live), [0] * len(live)
+            for k, code, e in zip(eight, at_codes, at_exps):
+                values[k], exps[k] = code, e
+            for k, at_wide in zip(wide, pointers([held[k] for k in wide], name, [sizes[k] for k in wide],
+                                                 f32)):
+                values[k] = at_wide
+            column(at, values)
+            column(at + 2, exps)
+        if copies is not None:
+            low = [k for k, t in enumerate(copies) if t is not None]
+            values = [0] * len(live)
+            for k, at_low in zip(low, pointers([copies[k] for k in low], "copies", [sizes[k] for k in low],
+                                               torch.bfloat16)):
+                values[k] = at_low
+            column(6, values)
         on_dev = [None, None, None]
         for q, (t, dtype, name) in enumerate(((scale, f32, "scale"), (step, torch.int32, "step"),
                                               (lr, f32, "lr"))):
@@ -1251,7 +1280,7 @@ class SeqOps:
             self.h, count, rows.buffer_info()[0], 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
             weight_decay, 1 if on_dev[1] else step, seed & 0xffffffff, *on_dev, self._raw_stream()))
         # autograd is told of the change: a graph that has saved a parameter refuses to go on
-        torch.autograd.graph.increment_version([p for p, g in zip(params, grads) if g is not None])
+        torch.autograd.graph.increment_version(params)
 
     def state8_pack(self, x, signed, stream=None):
         """(codes like x, exponents [ceil(n / 64)]) of an 8-bit optimizer state:
