@@ -4,6 +4,11 @@
 // operations.  With 8-bit ones it moves some 16, and the codes take fifty operations
 // more, which bound it as much: so what is rare (values that are not finite, codes
 // that stand for them, the ends of a tensor) leaves a warp's usual path.
+//
+// Measured: fp32 states, 161M parameters, 652 us (6870 GB/s); 8-bit ones with bf16
+// gradients, 51M parameters, 178 us (717 MB, at 93 instructions a parameter), and
+// each state read out in 42 us.
+//
 // The tensors' table comes as the kernel's parameter, so a captured launch keeps it
 // and nothing is copied or kept on the device; a block finds the tensor of its
 // piece by halving.
@@ -25,7 +30,7 @@ constexpr int NT = 256, V = 8;
 constexpr int TURN = NT * V;  // values of a block at a time: 32 blocks of 64
 // A block takes as many turns as leave eight blocks an SM, 8 at most: finding its tensor
 // costs as much as a turn's arithmetic on 3 values a thread (8-bit states, 51M
-// parameters, 218 us with one turn, 180 with four, 170 with eight).
+// parameters, 218 us with one turn, 178 with four and with eight).
 constexpr int MOST_TURNS = 8;
 
 struct Tensor {

@@ -8,9 +8,14 @@
 // and 6 W + 10 operations.  A thread keeps VEC channels and walks a stretch of
 // steps with the last W inputs (and, backwards, W gradients) in registers, so
 // that an input is read once but for the W - 1 that a stretch shares with the
-// one before it.  Reads run 8 steps ahead by asynchronous copies into a ring of the
-// thread's own in shared memory (in registers they would cost half of the threads),
-// and channels are worked on as packed pairs.
+// one before it.  Reads run 12 steps ahead by asynchronous copies into a ring of the
+// thread's own in shared memory (in registers they cost half of the threads: backward
+// bf16 T=8192 B=4 H=2048 173 us, 107 so), and channels are worked on as packed pairs.
+//
+// Measured, W=4: forward bf16 T=512 B=256 H=1024 118 us (4560 GB/s), backward bf16
+// T=8192 B=4 H=2048 107 us (3770 GB/s), fp32 mixed lengths T=500 B=64 H=512 44 us: half
+// of the copy's rate, at 12 warps an SM with 160 registers (four blocks in the place of
+// three spill: 137 and 140 us) and 17 (forward) and 33 instructions a value.
 #include <type_traits>
 
 #include "per_device.h"
@@ -24,6 +29,7 @@ using namespace ssm;
 constexpr int NT = 128;
 constexpr int AHEAD = 4, BATCHES = 4;  // steps that are read together, and how often in the ring
 constexpr int SHORTEST = 16;  // steps of a stretch, at least
+constexpr int LONG = 128;     // steps of a stretch that is cut again
 
 // Threads are numbered over groups of VEC channels, then rows (or runs of `per`
 // rows), then stretches of `len` steps.
@@ -32,9 +38,13 @@ struct Split {
   __host__ __device__ int64_t threads() const { return (int64_t)groups * runs * stretches; }
 };
 
-// As many stretches as fill the GPU (`room` threads), rows joined where there
-// are more than that; a stretch of at least SHORTEST steps.
-Split split_of(int T, int B, int H, int vec, int64_t room) {
+// As many stretches as fill the GPU (`room` threads), of SHORTEST steps or more; rows are
+// joined where there are more than that.  Long stretches are cut in `waves`, so that the
+// last blocks are short ones: the W - 1 inputs that they read again are in the
+// second-level cache.  (Forward in four: bf16 T=512 B=256 H=1024, 256 blocks where 456
+// fit, 123 -> 118 us; the backward, whose blocks end with their sums, in one: bf16
+// T=8192 B=4 H=2048 107 us, 133 in four.)
+Split split_of(int T, int B, int H, int vec, int64_t room, int waves) {
   Split s;
   s.groups = ceil_div(H, vec);
   const int64_t items = (int64_t)s.groups * B;
@@ -42,6 +52,7 @@ Split split_of(int T, int B, int H, int vec, int64_t room) {
   s.runs = ceil_div(B, s.per);
   const int64_t want = std::max<int64_t>(room / ((int64_t)s.groups * s.runs), 1);
   s.len = (int)std::max<int64_t>(ceil_div(T, (int)std::min<int64_t>(want, T)), SHORTEST);
+  if (s.len >= LONG) s.len = ceil_div(s.len, waves);
   s.stretches = ceil_div(T, s.len);
   return s;
 }
@@ -396,9 +407,11 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Spl
   }
 }
 
-template <typename T, int VEC>
+// WORDS: a thread's taps, VEC * W neighbours, as words of 16 bytes.
+template <typename T, int W, int VEC, bool WORDS>
 __global__ void __launch_bounds__(NT) conv_step_kernel(const ConvStep a, int *err) {
-  const int groups = a.H / VEC;
+  constexpr int MW = taps<W>(), P = pairs<VEC>();
+  const int w_n = W ? W : a.W, groups = a.H / VEC;
   const int64_t id = (int64_t)blockIdx.x * NT + threadIdx.x;
   if (id >= (int64_t)groups * a.B) return;
   const int h = (int)(id % groups) * VEC;
@@ -409,33 +422,47 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const ConvStep a, int *er
     slot = -1;
   }
   T *y = static_cast<T *>(a.y) + b * a.ldy + h;
-  float v[VEC] = {};
+  F2 v[P];
+#pragma unroll
+  for (int j = 0; j < P; ++j) v[j] = f2(0.f);
   if (slot >= 0) {
-    T *state = static_cast<T *>(a.state) + slot * (a.W - 1) * a.H + h;
-    const Word<T, VEC> now = word<T, VEC>(static_cast<const T *>(a.x) + b * a.ldx + h);
-    Word<T, VEC> in[RCU_CONV_MAX_TAPS];
+    T *state = static_cast<T *>(a.state) + slot * (w_n - 1) * a.H + h;
+    Word<T, VEC> in[MW];  // the window, its last w_n
 #pragma unroll
-    for (int k = 0; k < RCU_CONV_MAX_TAPS; ++k)
-      if (k < a.W) in[k] = k < a.W - 1 ? word<T, VEC>(state + (int64_t)k * a.H) : now;
+    for (int k = 0; k < MW; ++k)
+      if (k >= MW - w_n)
+        in[k] = k < MW - 1 ? word<T, VEC>(state + (int64_t)(k - (MW - w_n)) * a.H)
+                           : word<T, VEC>(static_cast<const T *>(a.x) + b * a.ldx + h);
+    F2 w[MW][P], bias[P], win[MW][P];
+    if constexpr (WORDS) {
+      float f[VEC * MW];
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) v[j] = a.bias ? a.bias[h + j] : 0.f;
-#pragma unroll
-    for (int k = 0; k < RCU_CONV_MAX_TAPS; ++k)
-      if (k < a.W) {
-        if (k) *reinterpret_cast<Word<T, VEC> *>(state + (int64_t)(k - 1) * a.H) = in[k];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          v[j] = fmaf(a.weight[(int64_t)(h + j) * a.W + k], to_f(in[k].v[j]), v[j]);
+      for (int k = 0; k < VEC * MW; k += 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(a.weight + (int64_t)h * W + k);
+        f[k] = q.x, f[k + 1] = q.y, f[k + 2] = q.z, f[k + 3] = q.w;
       }
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        bias[j] = a.bias ? f2(a.bias[h + 2 * j], a.bias[h + 2 * j + 1]) : f2(0.f);
+#pragma unroll
+        for (int k = 0; k < MW; ++k) w[k][j] = f2(f[2 * j * MW + k], f[(2 * j + 1) * MW + k]);
+      }
+    } else {
+      load_taps<W, VEC>(a.weight, a.bias, h, w_n, w, bias);
+    }
+#pragma unroll
+    for (int k = 0; k < MW; ++k)
+      if (k >= MW - w_n) {
+        if (k > MW - w_n) *reinterpret_cast<Word<T, VEC> *>(state + (int64_t)(k - 1 - (MW - w_n)) * a.H) = in[k];
+        widen<T, VEC>(in[k], win[k]);
+      }
+    filter<W, VEC>(w, w_n, bias, win, v);
     if (a.silu) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[j] *= sigmoid(v[j]);
+      for (int j = 0; j < P; ++j) v[j] = mul2(v[j], sigmoid2(v[j]));
     }
   }
-  Word<T, VEC> out;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) out.v[j] = from_f<T>(v[j]);
-  *reinterpret_cast<Word<T, VEC> *>(y) = out;
+  store<T, VEC>(y, v);
 }
 
 // Runs f with the kernel's number of taps: those of the usual widths known to the
@@ -484,7 +511,7 @@ cudaError_t fwd(const ConvFwd &p, int *err, int nsm, cudaStream_t s) {
     static PerDevice<Room> rooms;
     const Room room = rooms.here([&] { return room_of(fn, bytes, nsm); });
     if (room.set != cudaSuccess) return room.set;
-    const Split sp = split_of(p.T, p.B, p.H, VEC, room.threads);
+    const Split sp = split_of(p.T, p.B, p.H, VEC, room.threads, 4);
     return launch(fn, sp, bytes, s, p, sp, err);
   });
 }
@@ -496,7 +523,7 @@ cudaError_t bwd(const ConvBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s,
     static PerDevice<Room> rooms;
     const Room room = rooms.here([&] { return room_of(fn, bytes, nsm); });
     if (room.set != cudaSuccess) return room.set;
-    const Split sp = split_of(p.T, p.B, p.H, VEC, room.threads);
+    const Split sp = split_of(p.T, p.B, p.H, VEC, room.threads, 1);
     const int64_t rows = (int64_t)sp.runs * sp.stretches, cols = (int64_t)p.H * (p.W + 1);
     float *part = nullptr;
     if (p.dweight || p.dbias) {
@@ -540,23 +567,28 @@ cudaError_t launch_conv_bwd(const ConvBwd &p, DevMem &ws, int *err, int nsm, boo
   return wide ? bwd<float, 4>(p, ws, err, nsm, s, launches) : bwd<float, 1>(p, ws, err, nsm, s, launches);
 }
 
+template <typename T, int VEC, bool WORDS>
+static cudaError_t step(const ConvStep &p, int *err, cudaStream_t s) {
+  return by_taps<VEC>(p.W, [&](auto w) {
+    const int64_t threads = (int64_t)(p.H / VEC) * p.B;
+    conv_step_kernel<T, decltype(w)::value, VEC, WORDS>
+        <<<(unsigned)((threads + NT - 1) / NT), NT, 0, s>>>(p, err);
+    return cudaGetLastError();
+  });
+}
+template <typename T>
+static cudaError_t step_of(const ConvStep &p, int *err, bool vec, cudaStream_t s) {
+  const bool wide = vec && usual(p.W) && p.H % 4 == 0 && aligned(p.x, p.ldx, sizeof(T), 4) &&
+                    aligned(p.y, p.ldy, sizeof(T), 4) && aligned(p.state, p.H, sizeof(T), 4);
+  if (!wide) return step<T, 1, false>(p, err, s);
+  return aligned(p.weight, 4, 4, 4) ? step<T, 4, true>(p, err, s) : step<T, 4, false>(p, err, s);
+}
+
 cudaError_t launch_conv_step(const ConvStep &p, int *err, int nsm, bool vec, cudaStream_t s,
                              int *launches) {
   ++*launches;
   (void)nsm;
-  const int size = p.dtype == RCU_BF16 ? 2 : 4;
-  const bool wide = vec && p.H % 4 == 0 && aligned(p.x, p.ldx, size, 4) &&
-                    aligned(p.y, p.ldy, size, 4) && aligned(p.state, p.H, size, 4);
-  const int64_t threads = (int64_t)(wide ? p.H / 4 : p.H) * p.B;
-  const unsigned blocks = (unsigned)((threads + NT - 1) / NT);
-  if (p.dtype == RCU_BF16) {
-    if (wide) conv_step_kernel<bf16, 4><<<blocks, NT, 0, s>>>(p, err);
-    else conv_step_kernel<bf16, 1><<<blocks, NT, 0, s>>>(p, err);
-  } else {
-    if (wide) conv_step_kernel<float, 4><<<blocks, NT, 0, s>>>(p, err);
-    else conv_step_kernel<float, 1><<<blocks, NT, 0, s>>>(p, err);
-  }
-  return cudaGetLastError();
+  return p.dtype == RCU_BF16 ? step_of<bf16>(p, err, vec, s) : step_of<float>(p, err, vec, s);
 }
 
 }  // namespace rcu

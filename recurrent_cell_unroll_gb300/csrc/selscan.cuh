@@ -177,14 +177,9 @@ __device__ __forceinline__ Four constants(const float *p, int h, int width) {
 // S states of [.., N] fp32 at p, `n` of them there.
 template <int S>
 __device__ __forceinline__ void load_states(const float *p, int n, bool wide, float (&v)[S]) {
-  if (S == 2 && wide && n == S) {
-    const float2 a = *reinterpret_cast<const float2 *>(p);
-    v[0] = a.x, v[1] = a.y;
-    return;
-  }
   if (wide && n == S) {
 #pragma unroll
-    for (int k = 0; k + 3 < S; k += 4) {
+    for (int k = 0; k < S; k += 4) {
       const float4 a = *reinterpret_cast<const float4 *>(p + k);
       v[k] = a.x, v[k + 1] = a.y, v[k + 2] = a.z, v[k + 3] = a.w;
     }
@@ -195,13 +190,9 @@ __device__ __forceinline__ void load_states(const float *p, int n, bool wide, fl
 }
 template <int S>
 __device__ __forceinline__ void store_states(float *p, int n, bool wide, const float (&v)[S]) {
-  if (S == 2 && wide && n == S) {
-    *reinterpret_cast<float2 *>(p) = make_float2(v[0], v[1]);
-    return;
-  }
   if (wide && n == S) {
 #pragma unroll
-    for (int k = 0; k + 3 < S; k += 4)
+    for (int k = 0; k < S; k += 4)
       *reinterpret_cast<float4 *>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
     return;
   }

@@ -12,10 +12,20 @@
 //
 // A thread has S states of K neighbouring channels, a warp all states of its own
 // channels, so only the sums over channels (db, dc) leave a warp.  They are what
-// costs beside the exponentials: a thread adds its four channels' first, the lanes
-// exchange theirs in shared memory, and the warps' sums stand where the checkpoint
-// of the four steps was.  Sums over states are left in parts by the lanes, and added
-// by the threads that compute the outputs, as words of four channels.
+// costs beside the exponentials: a thread adds its two channels' first, the lanes
+// exchange theirs in shared memory (as shuffles they took half of the time), and the
+// warps' sums stand where the checkpoint of the four steps was.  Sums over states are
+// left in parts by the lanes, and added by the lanes that compute the outputs, as words
+// of two channels.
+//
+// Two channels a thread and not four, though those read less of shared memory: 8 warps
+// an SM in the place of 6 (bf16, N=16, T=2048 B=8 H=2048 1190 -> 802 us).  Three blocks
+// an SM, at 168 registers, were no faster (the decays kept 1015 us, computed again 928,
+// two blocks 755).
+//
+// Measured, N=16: bf16 T=2048 B=8 H=2048 682 us, T=8192 B=2 H=1024 (19 segments) 500, of
+// which 100 for their ends and 32 for chaining and sums; fp32 T=500 B=32 H=512, mixed
+// lengths, 200.  Issue bound: 27 instructions a state and step at 1.9 a cycle.
 #include "selscan.cuh"
 
 namespace rcu {

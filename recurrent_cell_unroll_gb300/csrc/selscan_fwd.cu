@@ -1,7 +1,4 @@
 // Selective scan, forward (selscan.cuh has the mathematics and the layout).
-#include <type_traits>
-
-#include "per_device.h"
 #include "selscan.cuh"
 
 namespace rcu {
@@ -26,10 +23,19 @@ struct Args {
 };
 
 // A thread has S states of K neighbouring channels, as pairs of channels; the LANES
-// threads that hold a channel's N stand side by side in a warp.  Tiles are of half a
-// chunk: a block's shared memory then leaves room for seven others.
-constexpr int K = 4, P = K / 2, TILE = CHUNK / 2;
-template <int S, int LANES>
+// threads that hold a channel's N stand side by side in a warp.  With four channels a
+// thread, what it reads of shared memory (their steps and inputs, and b and c of its
+// states: a 16-byte read takes four cycles, whoever shares it) is one word a state and
+// step; with two it was 2.5, and the reads bound the kernel (T=300 B=64 H=2048 263 us,
+// 217 with four).  Tiles are of half a chunk: seven blocks then fit an SM, three with
+// whole ones (201 and 286 us).
+//
+// Measured, bf16, N=16: T=300 B=64 H=2048 201 us, 3.1e12 states a second, where the
+// special function unit would take 83 and the issue of 118 instructions a channel and
+// step 120; T=2048 B=8 H=2048 293 us, in four segments (115 of them for their ends);
+// T=65536 B=1 H=512 302.
+constexpr int S = 4, K = 4, P = K / 2, TILE = CHUNK / 2;
+template <int LANES>
 struct Shape {
   static constexpr int WARPS = LANES <= 2 ? 1 : LANES / 2;   // of a block
   static constexpr int NT = 32 * WARPS, CC = NT / LANES * K, NP = S * LANES;
@@ -39,16 +45,16 @@ struct Shape {
   static constexpr int BUF = TILE * CC + 8;              // floats: parts 8 banks apart
   static constexpr int BUFS = PARTS < 2 ? 2 : PARTS;
 };
-template <typename T, int S, int LANES, Mode MODE>
+template <typename T, int LANES, Mode MODE>
 constexpr int shared_bytes() {
-  typedef Shape<S, LANES> Sh;
+  typedef Shape<LANES> Sh;
   return (MODE == MAIN ? Sh::BUFS : 2) * Sh::BUF * 4 + (MODE == MAIN ? 2 : 1) * TILE * Sh::NP * 4 +
          2 * (MODE == ENDS ? 2 : 3) * TILE * Sh::CC * (int)sizeof(T);
 }
 
-template <typename T, int S, int LANES, bool ALIGNED, Mode MODE>
-__global__ void __launch_bounds__(Shape<S, LANES>::NT, LANES == 4 ? 7 : 1) scan_kernel(const Args a, int *err) {
-  typedef Shape<S, LANES> Sh;
+template <typename T, int LANES, bool ALIGNED, Mode MODE>
+__global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_kernel(const Args a, int *err) {
+  typedef Shape<LANES> Sh;
   constexpr int NT = Sh::NT, CC = Sh::CC, NP = Sh::NP, BUF = Sh::BUF, PARTS = Sh::PARTS;
   constexpr int U = 4;                 // steps worked on together
   constexpr int RAW = MODE == ENDS ? 2 : 3;
@@ -309,11 +315,11 @@ __global__ void __launch_bounds__(128) chain_kernel(const float *a_log, const fl
   }
 }
 
-template <typename T, int S, int LANES, bool ALIGNED, Mode MODE>
+template <typename T, int LANES, bool ALIGNED, Mode MODE>
 cudaError_t run(Args a, int *err, cudaStream_t s, int *launches) {
-  typedef Shape<S, LANES> Sh;
-  constexpr int bytes = shared_bytes<T, S, LANES, MODE>();
-  auto fn = scan_kernel<T, S, LANES, ALIGNED, MODE>;
+  typedef Shape<LANES> Sh;
+  constexpr int bytes = shared_bytes<T, LANES, MODE>();
+  auto fn = scan_kernel<T, LANES, ALIGNED, MODE>;
   static PerDevice<cudaError_t> ready;
   const cudaError_t set =
       ready.here([&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
@@ -328,18 +334,18 @@ cudaError_t run(Args a, int *err, cudaStream_t s, int *launches) {
   return cudaLaunchKernelEx(&cfg, fn, a, err);
 }
 
-template <typename T, Mode MODE, int S, int LANES>
+template <typename T, Mode MODE, int LANES>
 cudaError_t of_lanes(const Args &a, bool aligned, int *err, cudaStream_t s, int *launches) {
-  return aligned ? run<T, S, LANES, true, MODE>(a, err, s, launches) : run<T, S, LANES, false, MODE>(a, err, s, launches);
+  return aligned ? run<T, LANES, true, MODE>(a, err, s, launches) : run<T, LANES, false, MODE>(a, err, s, launches);
 }
 template <typename T, Mode MODE>
 cudaError_t of_type(const Args &a, bool aligned, int *err, cudaStream_t s, int *launches) {
   const int N = a.in.N;
-  if (N <= 4) return of_lanes<T, MODE, 4, 1>(a, aligned, err, s, launches);
-  if (N <= 8) return of_lanes<T, MODE, 4, 2>(a, aligned, err, s, launches);
-  if (N <= 16) return of_lanes<T, MODE, 4, 4>(a, aligned, err, s, launches);
-  if (N <= 32) return of_lanes<T, MODE, 4, 8>(a, aligned, err, s, launches);
-  return of_lanes<T, MODE, 4, 16>(a, aligned, err, s, launches);
+  if (N <= 4) return of_lanes<T, MODE, 1>(a, aligned, err, s, launches);
+  if (N <= 8) return of_lanes<T, MODE, 2>(a, aligned, err, s, launches);
+  if (N <= 16) return of_lanes<T, MODE, 4>(a, aligned, err, s, launches);
+  if (N <= 32) return of_lanes<T, MODE, 8>(a, aligned, err, s, launches);
+  return of_lanes<T, MODE, 16>(a, aligned, err, s, launches);
 }
 template <Mode MODE>
 cudaError_t dispatch(Args a, bool vec, int *err, cudaStream_t s, int *launches) {
