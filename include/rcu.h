@@ -3,8 +3,9 @@
  *
  * The library runs the time-unrolled forward pass of stacked LSTM, GRU and
  * LSTM-with-projection (LSTMP) networks, padded or variable-length, and the
- * RSSM prior unroll, and operators over sequences (a gated linear recurrence,
- * layer norm, 8-bit activation checkpoints), entirely in its own CUDA kernels
+ * RSSM prior unroll, operators over sequences (a gated linear recurrence,
+ * layer norm, 8-bit activation checkpoints, a short causal convolution, a
+ * selective scan) and AdamW over many tensors, entirely in its own CUDA kernels
  * (sm_103a).  The caller supplies device memory and a CUDA stream; nothing here
  * depends on PyTorch.
  *
@@ -845,7 +846,8 @@ RCU_API int rcu_selscan_step(rcu_seq *h, int dtype, int B, int H, int N, const v
  * (type g_type), RCU_F32 or RCU_BF16 each, and its two states, either fp32 m and v
  * [n] (m_exp, v_exp NULL) or 8-bit ones: int8 codes m and v [n] with exponents
  * m_exp, v_exp int8 [ceil(n / 64)].  copy: NULL, or bf16 [n] that receives the
- * new parameter rounded (for fp32 p).  All are dense.  An n of 0 is left out.
+ * new parameter rounded (for fp32 p).  All are dense; no tensor of a list overlaps
+ * another.  An n of 0 is left out.
  */
 typedef struct rcu_adamw_tensor {
   void *p;

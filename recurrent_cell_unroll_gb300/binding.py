@@ -1199,7 +1199,7 @@ class SeqOps:
         which a captured step then follows; scale: a float32 on the device that
         gradients are multiplied by; seed: of the 8-bit states' rounding.
         copies: bfloat16 tensors (or None) that receive the new parameters.
-        All tensors are contiguous."""
+        All tensors are contiguous, and none overlap."""
         if stream is not None:
             return self._on_stream(stream, self.adamw_step, params, grads, m, v, step, lr, betas, eps,
                                    weight_decay, scale, seed, copies)
@@ -1280,7 +1280,7 @@ class SeqOps:
             self.h, count, rows.buffer_info()[0], 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
             weight_decay, 1 if on_dev[1] else step, seed & 0xffffffff, *on_dev, self._raw_stream()))
         # autograd is told of the change: a graph that has saved a parameter refuses to go on
-        torch.autograd.graph.increment_version(params)
+        torch.autograd.graph.increment_version([p for p in params if not p.is_inference()])
 
     def state8_pack(self, x, signed, stream=None):
         """(codes like x, exponents [ceil(n / 64)]) of an 8-bit optimizer state:

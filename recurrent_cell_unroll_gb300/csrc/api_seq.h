@@ -34,6 +34,7 @@ struct rcu_seq_s : EventProfiler, DevMem {
       ws.n = 0;
     }
     const cudaError_t e = ws.ensure(bytes);
+    if (e != cudaSuccess) cudaGetLastError();  // reported here, not by the next launch too
     *p = ws.p;
     return e;
   }

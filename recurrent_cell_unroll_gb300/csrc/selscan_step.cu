@@ -2,9 +2,11 @@
 // in place.  Bound by memory (8 bytes a state) at serving sizes, by latency below.
 //
 // A thread keeps 4 states of a channel, neighbouring threads the channel's others,
-// and takes several requests, since a channel's rates cost more than a step; four are
-// read together (bf16 B=256 H=2048 N=16, cold: 21 us one by one, 10.3 so).  From Python
-// a call takes some 16 us, which bounds it at such sizes.
+// and takes several requests one after another, since a channel's rates cost more than
+// a step.  Reading four together is faster where the cache takes the states (10 us in
+// the place of 21, bf16 B=256 H=2048 N=16), but where memory has to, with tables taken
+// in rotation, 39 us in the place of 18 (67 MB): reads and writes then come in bursts
+// from all over the table.  From Python a call takes some 17 us.
 #include "selscan.cuh"
 
 namespace rcu {
@@ -12,7 +14,7 @@ namespace {
 
 using namespace selscan;
 
-constexpr int NT = 128, V = 4, ROWS = 4;  // states of a thread, requests read together
+constexpr int NT = 128, V = 4;  // states of a thread
 
 template <typename T, int LANES, bool WIDE>
 __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanStep a, int per, int *err) {
@@ -27,82 +29,59 @@ __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanStep a, int per
     A2[k] = n0 + k < a.N ? rate2(a.a_log[(int64_t)ch * a.N + n0 + k]) : 0.f;
   const float bias = a.dt_bias ? a.dt_bias[ch] : 0.f, skip = a.d ? a.d[ch] : 0.f;
   const bool states = n0 < a.N;  // this lane has some
-  for (int64_t first = b0; first < b1; first += ROWS) {
-    // all reads of ROWS requests before the first is worked on
-    int64_t slot[ROWS];
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      const int64_t b = first + q;
-      slot[q] = -1;
-      if (b >= b1) continue;
-      slot[q] = a.slot ? a.slot[b] : b;
-      if (slot[q] < -1 || slot[q] >= a.slots) {
-        atomicCAS(err, (int)DEV_OK, (int)DEV_SLOTS);
-        slot[q] = -1;
-      }
+  for (int64_t b = b0; b < b1; ++b) {
+    int64_t slot = a.slot ? a.slot[b] : b;
+    if (slot < -1 || slot >= a.slots) {
+      atomicCAS(err, (int)DEV_OK, (int)DEV_SLOTS);
+      slot = -1;
     }
-    T x[ROWS], dt[ROWS], z[ROWS];
-    Word<T, V> bw[ROWS], cw[ROWS];
-    float4 h[ROWS];
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      if (slot[q] < 0) continue;
-      const int64_t b = first + q;
-      x[q] = static_cast<const T *>(a.x)[b * a.ldx + ch];
-      dt[q] = static_cast<const T *>(a.dt)[b * a.lddt + ch];
-      if (a.z) z[q] = static_cast<const T *>(a.z)[b * a.ldz + ch];
-      if (!states) continue;
-      const float *state = a.state + (slot[q] * a.H + ch) * a.N + n0;
-      const T *bp = static_cast<const T *>(a.b) + b * a.ldb + n0, *cp = static_cast<const T *>(a.c) + b * a.ldc + n0;
-      if (WIDE) {
-        h[q] = *reinterpret_cast<const float4 *>(state);
-        bw[q] = *reinterpret_cast<const Word<T, V> *>(bp);
-        cw[q] = *reinterpret_cast<const Word<T, V> *>(cp);
-      } else {
-        float v[V] = {};
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          if (n0 + k < a.N) v[k] = state[k], bw[q].v[k] = bp[k], cw[q].v[k] = cp[k];
-        h[q] = make_float4(v[0], v[1], v[2], v[3]);
-      }
+    T *y = static_cast<T *>(a.y) + b * a.ldy + ch;
+    if (slot < 0) {  // the same for the warp
+      if (live && l == 0) *y = from_f<T>(0.f);
+      continue;
     }
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      const int64_t b = first + q;
-      if (b >= b1) break;
-      T *y = static_cast<T *>(a.y) + b * a.ldy + ch;
-      if (slot[q] < 0) {  // the same for the warp
-        if (live && l == 0) *y = from_f<T>(0.f);
-        continue;
+    float *state = a.state + (slot * a.H + ch) * a.N + n0;
+    const T *bp = static_cast<const T *>(a.b) + b * a.ldb + n0, *cp = static_cast<const T *>(a.c) + b * a.ldc + n0;
+    float h[V] = {}, s = 0.f;
+    Word<T, V> bw, cw;
+    if (WIDE) {
+      if (states) {
+        const float4 v = *reinterpret_cast<const float4 *>(state);
+        h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+        bw = *reinterpret_cast<const Word<T, V> *>(bp);
+        cw = *reinterpret_cast<const Word<T, V> *>(cp);
       }
-      const float xv = to_f(x[q]), delta = softplus(to_f(dt[q]) + bias), u = delta * xv;
-      float v[V] = {h[q].x, h[q].y, h[q].z, h[q].w}, s = 0.f;
+    } else {
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (WIDE ? states : n0 + k < a.N) {
-          v[k] = fmaf(ex2(delta * A2[k]), v[k], u * to_f(bw[q].v[k]));
-          s = fmaf(v[k], to_f(cw[q].v[k]), s);
-        }
-      if (live && states) {
-        float *state = a.state + (slot[q] * a.H + ch) * a.N + n0;
-        if (WIDE) {
-          *reinterpret_cast<float4 *>(state) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
+        if (n0 + k < a.N) h[k] = state[k], bw.v[k] = bp[k], cw.v[k] = cp[k];
+    }
+    const float x = to_f(static_cast<const T *>(a.x)[b * a.ldx + ch]);
+    const float delta = softplus(to_f(static_cast<const T *>(a.dt)[b * a.lddt + ch]) + bias), u = delta * x;
 #pragma unroll
-          for (int k = 0; k < V; ++k)
-            if (n0 + k < a.N) state[k] = v[k];
-        }
+    for (int k = 0; k < V; ++k)
+      if (WIDE ? states : n0 + k < a.N) {
+        h[k] = fmaf(ex2(delta * A2[k]), h[k], u * to_f(bw.v[k]));
+        s = fmaf(h[k], to_f(cw.v[k]), s);
       }
+    if (live && states) {
+      if (WIDE) {
+        *reinterpret_cast<float4 *>(state) = make_float4(h[0], h[1], h[2], h[3]);
+      } else {
 #pragma unroll
-      for (int o = LANES / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (live && l == 0) {
-        if (a.d) s = fmaf(skip, xv, s);
-        if (a.z) {
-          const float zv = to_f(z[q]);
-          s *= zv * sigmoid(zv);
-        }
-        *y = from_f<T>(s);
+        for (int k = 0; k < V; ++k)
+          if (n0 + k < a.N) state[k] = h[k];
       }
+    }
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o /= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (live && l == 0) {
+      if (a.d) s = fmaf(skip, x, s);
+      if (a.z) {
+        const float z = to_f(static_cast<const T *>(a.z)[b * a.ldz + ch]);
+        s *= z * sigmoid(z);
+      }
+      *y = from_f<T>(s);
     }
   }
 }
@@ -110,8 +89,9 @@ __global__ void __launch_bounds__(NT) scan_step_kernel(const ScanStep a, int per
 template <typename T, int LANES, bool WIDE>
 cudaError_t run(const ScanStep &a, int *err, int nsm, cudaStream_t s) {
   const int64_t across = ((int64_t)a.H * LANES + NT - 1) / NT;
-  // as many requests a thread as leave ten blocks an SM, 32 at most
-  int per = (int)std::min<int64_t>(std::max<int64_t>((int64_t)a.B * across / (10 * nsm), 1), 32);
+  // as many requests a thread as leave twelve blocks an SM, 32 at most (8 and 24 blocks
+  // take 18 and 19 us there, 4 and 48 take 28 and 21)
+  int per = (int)std::min<int64_t>(std::max<int64_t>((int64_t)a.B * across / (12 * nsm), 1), 32);
   per = std::max(per, ceil_div(a.B, 65535));
   scan_step_kernel<T, LANES, WIDE><<<dim3((unsigned)across, ceil_div(a.B, per)), NT, 0, s>>>(a, per, err);
   return cudaGetLastError();
