@@ -2,6 +2,8 @@
 
 Each .cu file is compiled to an object in parallel, then linked into
 ``recurrent_cell_unroll_gb300/_lib/librcu.so`` with the static CUDA runtime.
+``tensors.so``, the part of the Python binding that reads lists of torch tensors
+(csrc/tensors.cpp, for this Python and torch), is compiled beside it with g++.
 Objects are rebuilt only when a source or header is newer.  ``build(debug=True)``
 makes ``librcu_debug.so`` instead: the same sources with -DRCU_DEBUG, whose
 kernels check their global-memory indices and record a failed check in the
@@ -23,6 +25,7 @@ LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "librcu.so")
 LIB_DEBUG = os.path.join(LIBDIR, "librcu_debug.so")
+TENSORS = os.path.join(LIBDIR, "tensors.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -37,6 +40,18 @@ def _flags():
     return ["-O3", "-lineinfo", ARCH, "-std=c++17", "-Xcompiler", "-fPIC",
             "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
             "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
+
+
+def _tensors_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    at = os.path.dirname(torch.__file__)
+    inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    return ["g++", "-O2", "-std=c++20", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+            *(f for i in inc for f in ("-isystem", i)), os.path.join(CSRC, "tensors.cpp"), "-o", out,
+            "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
 def _newest_header():
@@ -68,10 +83,20 @@ def build(verbose: bool = False, jobs: int = 0, debug: bool = False) -> str:
             print(r.stdout, r.stderr)
         return r
 
+    tensors_tmp = TENSORS + f".tmp{os.getpid()}"
+    tensors_src = max(os.path.getmtime(os.path.join(CSRC, "tensors.cpp")),
+                      os.path.getmtime(os.path.join(INCLUDE, "rcu.h")))
+    tensors = not os.path.exists(TENSORS) or os.path.getmtime(TENSORS) < tensors_src
+    kernels = bool(cmds)
+    if tensors:
+        cmds.insert(0, _tensors_command(tensors_tmp))
+
     if cmds:
         with cf.ThreadPoolExecutor(max_workers=jobs or min(len(cmds), os.cpu_count() or 4)) as ex:
             list(ex.map(run, cmds))
-    if cmds or not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs):
+    if tensors:
+        os.replace(tensors_tmp, TENSORS)
+    if kernels or not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs):
         tmp = lib + f".tmp{os.getpid()}"
         run([nvcc(), ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-lrt", "-ldl",
              "-lpthread"])

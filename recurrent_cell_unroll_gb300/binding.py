@@ -1,4 +1,5 @@
-"""Thin ctypes binding of librcu.so (argument marshalling only).
+"""Thin binding of librcu.so (argument marshalling only, by ctypes; lists of tensors
+by csrc/tensors.cpp).
 
 Every function here has the name of the C entry point it calls (see
 include/rcu.h) and only turns torch tensors into device pointers and CUDA
@@ -13,9 +14,9 @@ cuDNN flat-storage clones + thread-local recurrent mode", pytorch/rl PR 3754).
 """
 from __future__ import annotations
 
-import array
 import ctypes
-import operator
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional
@@ -168,6 +169,24 @@ def load(path: Optional[str] = None):
             fn.argtypes = args
         _lib = lib
         return lib
+
+
+_tensors_module = None
+
+
+def _tensors():
+    """The native part that reads lists of tensors (raises if it has not been built)."""
+    global _tensors_module
+    if _tensors_module is None:
+        if not os.path.exists(_build.TENSORS):
+            raise RuntimeError(f"{_build.TENSORS} not found: build it with "
+                               "recurrent_cell_unroll_gb300._build.build()")
+        loader = importlib.machinery.ExtensionFileLoader("tensors", _build.TENSORS)
+        spec = importlib.util.spec_from_file_location("tensors", _build.TENSORS, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _tensors_module = module
+    return _tensors_module
 
 
 def _check(rc: int) -> int:
@@ -709,11 +728,6 @@ class RSSM:
             pass
 
 
-_POINTER_OF, _SIZE_OF = torch.Tensor.data_ptr, torch.Tensor.numel
-_DEVICE_OF, _CONTIGUOUS = torch.Tensor.get_device, torch.Tensor.is_contiguous
-_DTYPE_OF = operator.attrgetter("dtype")
-
-
 class SeqOps:
     """The sequence operators (gated linear recurrence, layer norm, 8-bit
     activation checkpoints, short convolution, selective scan) and the AdamW
@@ -1207,68 +1221,15 @@ class SeqOps:
         if not (len(grads) == len(m) == len(v) == count) or (copies is not None
                                                             and len(copies) != count):
             raise ValueError("params, grads, m, v and copies must be lists of one length")
-        # A step of many small tensors is bound by these checks, so a list takes one pass
-        # for each of them in C (map), and the table is filled by columns.
-        keep, f32, types = [], torch.float32, self._DTYPES
-        live = [k for k in range(count) if grads[k] is not None]
-        if len(live) < count:
-            params, grads, m, v = ([ts[k] for k in live] for ts in (params, grads, m, v))
-            copies = [copies[k] for k in live] if copies is not None else None
-        rows = array.array("q", bytes(72 * count))
-
-        def column(at, values):
-            if len(live) == count:
-                rows[at::9] = array.array("q", values)
-            else:
-                for k, value in zip(live, values):
-                    rows[9 * k + at] = value
-
-        def pointers(ts, name, sizes, dtype=None):
-            try:
-                found = set(map(_DTYPE_OF, ts))
-                ok = (all(map(_CONTIGUOUS, ts)) and set(map(_DEVICE_OF, ts)) <= {self.device}
-                      and (found <= {dtype} if dtype else found <= types.keys())
-                      and (sizes is None or list(map(_SIZE_OF, ts)) == sizes))
-            except (AttributeError, TypeError):
-                ok = False
-            if not ok:
-                raise ValueError(f"{name} must be contiguous tensors on cuda:{self.device} of type "
-                                 f"{dtype or 'float32 or bfloat16'} and of the parameters' sizes")
-            return list(map(_POINTER_OF, ts))
-
-        column(0, pointers(params, "params", None))
-        sizes = list(map(_SIZE_OF, params))
-        column(1, pointers(grads, "grads", sizes))
-        column(7, sizes)
-        column(8, [types[p] | types[g] << 32
-                   for p, g in zip(map(_DTYPE_OF, params), map(_DTYPE_OF, grads))])
-        for at, name, held, other in ((2, "m", m, v), (3, "v", v, m)):
-            eight = [k for k, t in enumerate(held) if type(t) is tuple]
-            if not eight:
-                column(at, pointers(held, name, sizes, f32))
-                continue
-            if any(type(other[k]) is not tuple for k in eight):
-                raise ValueError("m and v of a tensor must be held alike")
-            wide = [k for k, t in enumerate(held) if type(t) is not tuple]
-            at_codes = pointers([held[k][0] for k in eight], f"{name}'s codes", [sizes[k] for k in eight],
-                                torch.int8)
-            at_exps = pointers([held[k][1] for k in eight], f"{name}'s exponents",
-                               [-(-sizes[k] // RCU_STATE8_BLOCK) for k in eight], torch.int8)
-            values, exps = [0] * len(live), [0] * len(live)
-            for k, code, e in zip(eight, at_codes, at_exps):
-                values[k], exps[k] = code, e
-            for k, at_wide in zip(wide, pointers([held[k] for k in wide], name, [sizes[k] for k in wide],
-                                                 f32)):
-                values[k] = at_wide
-            column(at, values)
-            column(at + 2, exps)
-        if copies is not None:
-            low = [k for k, t in enumerate(copies) if t is not None]
-            values = [0] * len(live)
-            for k, at_low in zip(low, pointers([copies[k] for k in low], "copies", [sizes[k] for k in low],
-                                               torch.bfloat16)):
-                values[k] = at_low
-            column(6, values)
+        keep, f32 = [], torch.float32
+        rows = bytearray(72 * count)
+        bad = _tensors().adamw_rows(rows, params, grads, m, v, copies, self.device)
+        if bad >= 0:
+            raise ValueError(
+                f"tensor {bad}: params, grads (float32 or bfloat16, of one shape), m, v (float32, or int8 "
+                f"codes with exponents [ceil(n / {RCU_STATE8_BLOCK})], of both) and copies (bfloat16) "
+                f"must be contiguous tensors of one size on cuda:{self.device}")
+        table = (ctypes.c_char * len(rows)).from_buffer(rows) if count else None
         on_dev = [None, None, None]
         for q, (t, dtype, name) in enumerate(((scale, f32, "scale"), (step, torch.int32, "step"),
                                               (lr, f32, "lr"))):
@@ -1277,10 +1238,10 @@ class SeqOps:
             elif q == 0 and t is not None:
                 raise ValueError("scale must be a tensor on a CUDA device")
         _check(self.lib.rcu_adamw_step(
-            self.h, count, rows.buffer_info()[0], 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
+            self.h, count, table, 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
             weight_decay, 1 if on_dev[1] else step, seed & 0xffffffff, *on_dev, self._raw_stream()))
         # autograd is told of the change: a graph that has saved a parameter refuses to go on
-        torch.autograd.graph.increment_version([p for p in params if not p.is_inference()])
+        _tensors().changed(params, grads)
 
     def state8_pack(self, x, signed, stream=None):
         """(codes like x, exponents [ceil(n / 64)]) of an 8-bit optimizer state:
