@@ -60,12 +60,24 @@ __device__ __forceinline__ float rate2(float a_log) {
   return r < -3e38f ? -3e38f : r;
 }
 
-// A tile [TILE][CC] of a tensor's rows t0 .. and channels h0 .. on its way to shared
-// memory: 16 bytes at a time and asynchronous where rows are aligned.  What is past
-// the row's end or the last channel keeps what was there.  Made once for a block.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from), "n"(BYTES) : "memory");
+}
+
+// A tile [TILE][CC] of a tensor's rows t0 .. and channels h0 .. (a multiple of 4) on its
+// way to shared memory, all of it asynchronous: 16 bytes at a time where rows are aligned,
+// 4 where they are not (T=512 B=16 H=1001 N=16: fp32 123 us, bf16 118; as plain values 451, 287).
+// bf16 rows that start in the middle of a word are copied with the value before them, and
+// lie one value further on (`shift`); that value is the tensor's or in front of its first,
+// in the same 4 bytes.  What is past the row's end or the last channel keeps what was
+// there, or is 0.  Made once for a block.
 template <typename T, int NT, int TILE, int CC, bool ALIGNED>
 struct Fetch {
-  static constexpr int V = ALIGNED ? 16 / sizeof(T) : 1, ROW = CC / V;  // pieces of a row
+  static constexpr bool SHIFTS = !ALIGNED && sizeof(T) == 2;
+  static constexpr int RS = CC + (SHIFTS ? 4 : 0);                      // values of a row in shared memory
+  static constexpr int V = (ALIGNED ? 16 : 4) / sizeof(T), ROW = CC / V;  // pieces of a row
   static constexpr int PASS = NT / ROW > 0 ? NT / ROW : 1;              // rows of a pass
   static constexpr int ACROSS = ROW > NT ? ROW / NT : 1;                // passes of a row
   static_assert(PASS * ROW == NT * ACROSS, "whole rows");
@@ -78,7 +90,12 @@ struct Fetch {
     from = p + row * st + h0 + col;
     left = width - h0 - col;
   }
-  __device__ __forceinline__ void start(T (*to)[CC], int t0, int end) const {
+  // values that row `r` of the tile at t0 lies further on
+  __device__ __forceinline__ int shift(int t0, int r) const {
+    if constexpr (!SHIFTS) return 0;
+    return (int)(reinterpret_cast<uintptr_t>(from + (t0 + r - row) * st) / 2 & 1);
+  }
+  __device__ __forceinline__ void start(T (*to)[RS], int t0, int end) const {
     const T *p = from + t0 * st;
     const int rows = end - t0 - row;  // of the thread's, that exist
 #pragma unroll
@@ -86,16 +103,28 @@ struct Fetch {
       if (k * PASS >= rows || (TILE % PASS && k * PASS + row >= TILE)) break;
 #pragma unroll
       for (int q = 0; q < ACROSS; ++q) {
-        if (q * NT * V >= left) break;
         T *s = &to[k * PASS + row][col + q * NT * V];
         const T *g = p + q * NT * V;
-        if (ALIGNED)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(s)),
-                       "l"(g) : "memory");
-        else
-          *s = *g;
+        if constexpr (SHIFTS) {
+          const int off = reinterpret_cast<uintptr_t>(g) / 2 & 1;
+          word(s, g - off, left + off - q * NT * V);
+          if (off && col + q * NT * V == CC - V) word(s + 2, g + 1, left - 1 - q * NT * V);
+        } else {
+          if (q * NT * V >= left) break;
+          if constexpr (ALIGNED)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(s)),
+                         "l"(g) : "memory");
+          else
+            copy_async<4>(s, g);
+        }
       }
     }
+  }
+  // 4 bytes, of which the first `n` values are read
+  static __device__ __forceinline__ void word(T *s, const T *g, int n) {
+    if (n <= 0) return;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(s)),
+                 "l"(g), "r"(n > 1 ? 4 : 2) : "memory");
   }
 };
 __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -156,6 +185,19 @@ __device__ __forceinline__ Four four(const float *p) {
 __device__ __forceinline__ Four four(const bf16 *p) {
   const Word<bf16, 4> v = *reinterpret_cast<const Word<bf16, 4> *>(p);
   return {f2(to_f(v.v[0]), to_f(v.v[1])), f2(to_f(v.v[2]), to_f(v.v[3]))};
+}
+// Of a row in shared memory, its first value at `row + shift` (Fetch).
+template <bool SHIFTS, typename T>
+__device__ __forceinline__ Four four(const T *row, int col, int shift) {
+  if constexpr (SHIFTS) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(row + col);
+    const uint32_t next = *reinterpret_cast<const uint32_t *>(row + col + 4);
+    const uint32_t a = __funnelshift_r(w.x, w.y, 16 * shift), b = __funnelshift_r(w.y, next, 16 * shift);
+    return {f2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u)),
+            f2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u))};
+  } else {
+    return four(row + col);
+  }
 }
 __device__ __forceinline__ void put_four(float *p, const Four &v) {
   *reinterpret_cast<float4 *>(p) = make_float4(lo(v.a), hi(v.a), lo(v.b), hi(v.b));

@@ -118,11 +118,6 @@ __device__ __forceinline__ void store_two(T *p, int left, F2 v) {
 __device__ __forceinline__ F2 sigmoid2(F2 v) { return f2(ssm::sigmoid(lo(v)), ssm::sigmoid(hi(v))); }
 __device__ __forceinline__ F2 pair_at(const float *p) { return *reinterpret_cast<const F2 *>(p); }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *to, const void *from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
-               "l"(from), "n"(BYTES) : "memory");
-}
 __device__ __forceinline__ void prefetch(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }

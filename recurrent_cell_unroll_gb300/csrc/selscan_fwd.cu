@@ -45,11 +45,12 @@ struct Shape {
   static constexpr int BUF = TILE * CC + 8;              // floats: parts 8 banks apart
   static constexpr int BUFS = PARTS < 2 ? 2 : PARTS;
 };
-template <typename T, int LANES, Mode MODE>
+template <typename T, int LANES, bool ALIGNED, Mode MODE>
 constexpr int shared_bytes() {
   typedef Shape<LANES> Sh;
+  typedef Fetch<T, Sh::NT, TILE, Sh::CC, ALIGNED> F;
   return (MODE == MAIN ? Sh::BUFS : 2) * Sh::BUF * 4 + (MODE == MAIN ? 2 : 1) * TILE * Sh::NP * 4 +
-         2 * (MODE == ENDS ? 2 : 3) * TILE * Sh::CC * (int)sizeof(T);
+         2 * (MODE == ENDS ? 2 : 3) * TILE * F::RS * (int)sizeof(T);
 }
 
 template <typename T, int LANES, bool ALIGNED, Mode MODE>
@@ -60,11 +61,14 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
   constexpr int RAW = MODE == ENDS ? 2 : 3;
   constexpr int ROW = CC / 4, EV = (TILE * ROW + NT - 1) / NT;  // words of four of a thread, of the same channels
   constexpr bool IDLE = TILE * ROW < NT;  // some threads have none
+  typedef Fetch<T, NT, TILE, CC, ALIGNED> F;
+  constexpr int RS = F::RS;
+  constexpr bool SHIFTS = F::SHIFTS;
   extern __shared__ float4 shared4[];
   float *buf = reinterpret_cast<float *>(shared4);                     // [BUFS][BUF]: delta, input
   float(*in_w)[NP] = reinterpret_cast<float(*)[NP]>(buf + (MODE == MAIN ? Sh::BUFS : 2) * BUF);  // b (GRADS: c)
   float(*out_w)[NP] = in_w + TILE;                                    // MAIN: c
-  T(*raw)[TILE][CC] = reinterpret_cast<T(*)[TILE][CC]>(MODE == MAIN ? out_w + TILE : in_w + TILE);
+  T(*raw)[TILE][RS] = reinterpret_cast<T(*)[TILE][RS]>(MODE == MAIN ? out_w + TILE : in_w + TILE);
   const ScanIn &p = a.in;
   const int group = blockIdx.x % a.groups;
   // GRADS: of all segments but the first; ENDS: but the last (by the grid)
@@ -76,7 +80,6 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
   const int t0 = seg * a.m.seg.len, t1 = min(t0 + a.m.seg.len, p.T), end = min(t1, n);
 
   const SeqIn &sx = MODE == GRADS ? a.dy : p.x, &sw = MODE == GRADS ? p.c : p.b;
-  typedef Fetch<T, NT, TILE, CC, ALIGNED> F;
   const F fdt(static_cast<const T *>(p.dt.p) + b * p.dt.sb, p.dt.st, ch0, p.H);
   const F fx(static_cast<const T *>(sx.p) + b * sx.sb, sx.st, ch0, p.H);
   const bool use_z = p.z.p && MODE != ENDS;
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
   auto tile_at = [&](int k) { return t0 + (MODE == GRADS ? tiles - 1 - k : k) * TILE; };
   // tile k's rows, into the buffers of its parity
   auto start = [&](int k) {
-    T(*to)[TILE][CC] = raw + k % 2 * RAW;
+    T(*to)[TILE][RS] = raw + k % 2 * RAW;
     const int t = tile_at(k);
     fdt.start(to[0], t, end);
     fx.start(to[1], t, end);
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
 
   for (int k = 0; k < tiles; ++k) {
     const int base = tile_at(k), steps = min(TILE, end - base);
-    T(*now)[TILE][CC] = raw + k % 2 * RAW;
+    T(*now)[TILE][RS] = raw + k % 2 * RAW;
     if (k == 0) {
       fetched();
       __syncthreads();
@@ -147,12 +150,12 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
     for (int q = 0; q < EV; ++q) {
       const int r = row0 + q * (NT / ROW);
       if (IDLE && r >= TILE) break;
-      Four v = four(&now[0][r][col]), u = four(&now[1][r][col]);
+      Four v = four<SHIFTS>(now[0][r], col, fdt.shift(base, r)), u = four<SHIFTS>(now[1][r], col, fx.shift(base, r));
       v.a = softplus(add2(v.a, bias.a)), v.b = softplus(add2(v.b, bias.b));
       if (MODE != GRADS) {
         u.a = mul2(v.a, u.a), u.b = mul2(v.b, u.b);
       } else if (use_z) {
-        const Four g = four(&now[RAW - 1][r][col]);
+        const Four g = four<SHIFTS>(now[RAW - 1][r], col, fz.shift(base, r));
         u.a = mul2(u.a, silu(g.a)), u.b = mul2(u.b, silu(g.b));
       }
       // steps past the end have delta and input 0, and so leave the states alone
@@ -247,11 +250,11 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
           v.a = add2(v.a, more.a), v.b = add2(v.b, more.b);
         }
         if (p.d) {
-          const Four xs = four(&now[1][r][col]);
+          const Four xs = four<SHIFTS>(now[1][r], col, fx.shift(base, r));
           v.a = fma2(skip.a, xs.a, v.a), v.b = fma2(skip.b, xs.b, v.b);
         }
         if (use_z) {
-          const Four g = four(&now[RAW - 1][r][col]);
+          const Four g = four<SHIFTS>(now[RAW - 1][r], col, fz.shift(base, r));
           v.a = mul2(v.a, silu(g.a)), v.b = mul2(v.b, silu(g.b));
         }
         T *to = y + (base + r) * a.y.st + ch0 + col;
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(128) chain_kernel(const float *a_log, const fl
 template <typename T, int LANES, bool ALIGNED, Mode MODE>
 cudaError_t run(Args a, int *err, cudaStream_t s, int *launches) {
   typedef Shape<LANES> Sh;
-  constexpr int bytes = shared_bytes<T, LANES, MODE>();
+  constexpr int bytes = shared_bytes<T, LANES, ALIGNED, MODE>();
   auto fn = scan_kernel<T, LANES, ALIGNED, MODE>;
   static PerDevice<cudaError_t> ready;
   const cudaError_t set =

@@ -363,6 +363,59 @@ def test_large_strides_pass_32_bits(ops):
     assert ops.status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,H,W,N,start,gap", [
+    (37, 2, 65, 4, 16, 1, 0), (40, 3, 64, 3, 16, 1, 2), (33, 2, 128, 4, 5, 3, 1), (35, 2, 127, 2, 3, 0, 3),
+    (18, 1, 1, 4, 1, 1, 2), (20, 2, 63, 5, 33, 1, 0), (45, 2, 66, 8, 32, 2, 0), (300, 2, 61, 4, 16, 1, 5)])
+def test_rows_anywhere(ops, dtype, T, B, H, W, N, start, gap):
+    """Rows that start and end in the middle of a word, in the midst of NaN: what rows of
+    their own give, bit for bit where the rows of both are read one way."""
+    make = Make(11, dtype)
+    room = {}
+
+    def rows(t):
+        wide = t.shape[-1] + gap
+        flat = torch.full((start + T * B * wide - gap,), float("nan"), dtype=t.dtype, device="cuda")
+        v = flat.as_strided(t.shape, (B * wide, wide, 1), start)
+        v.copy_(t)
+        room[v.data_ptr()] = flat
+        return v
+
+    def around(v):  # the NaN that are left of it
+        return int(torch.isnan(room[v.data_ptr()]).sum())
+
+    (x, dt, al, b, c, d, db, z, h0), _ = scan_inputs(make, T, B, H, N)
+    w, _ = make(H, W, std=0.5, f32=True)
+    dy, _ = make(T, B, H, rows=True)
+    x, dt, b, c, z, dy = (t.contiguous() for t in (x, dt, b, c, z, dy))
+    px, pdt, pb, pc, pz, pdy = (rows(t) for t in (x, dt, b, c, z, dy))
+    how = {"d": d, "dt_bias": db, "h0": h0, "states": True}
+    want = ops.selscan_forward(x, dt, al, b, c, z=z, **how)
+    got = ops.selscan_forward(px, pdt, al, pb, pc, z=pz, **how)
+    for p, q in zip(want, got):
+        assert torch.equal(p, q)
+    how = {"d": d, "dt_bias": db}
+    want = ops.selscan_backward(dy, x, dt, al, b, c, want[2], z=z, **how)
+    got = ops.selscan_backward(pdy, px, pdt, al, pb, pc, got[2], z=pz, **how)
+    for k, t in want.items():
+        assert t is None or torch.equal(t, got[k]), k
+    want, got = ops.conv_forward(x, w, bias=d), ops.conv_forward(px, w, bias=d)
+    for p, q in zip(want, got):
+        assert torch.equal(p, q)
+    want, got = ops.conv_backward(dy, x, w, bias=d), ops.conv_backward(pdy, px, w, bias=d)
+    assert torch.equal(want[0], got[0])
+    # sums over the T B steps, in another order where other words are read: off by at most
+    # T B half steps of the sum of their terms' magnitudes, each; silu' is below 1.1
+    top = 1.1 * float(dy.abs().sum((0, 1)).max()) * max(float(x.abs().max()), 1.0)
+    for p, q in zip(want[1:3], got[1:3]):
+        assert (p is None) == (q is None)
+        if p is not None:
+            assert float((p - q).abs().max()) <= 2 * T * B * 2.0 ** -24 * top
+    for v in (px, pdt, pb, pc, pz, pdy):
+        assert around(v) == start + (T * B - 1) * gap
+    assert ops.status() == 0
+
+
 def test_lengths_and_slots_out_of_range_are_reported(ops):
     make = Make(1, "f32")
     (x, dt, al, b, c, *_), _ = scan_inputs(make, 8, 3, 10, 4)
