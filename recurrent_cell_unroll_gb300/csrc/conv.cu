@@ -66,16 +66,30 @@ __device__ __forceinline__ void widen(const Word<T, VEC> &w, F2 (&v)[pairs<VEC>(
   for (int j = 0; j < pairs<VEC>(); ++j)
     v[j] = f2(to_f(w.v[2 * j]), VEC > 1 ? to_f(w.v[VEC > 1 ? 2 * j + 1 : 0]) : 0.f);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ Word<T, VEC> word(const T *p) {
-  return *reinterpret_cast<const Word<T, VEC> *>(p);
+// LOOSE: value by value, `n` of them there.
+template <typename T, int VEC, bool LOOSE = false>
+__device__ __forceinline__ Word<T, VEC> word(const T *p, int n = VEC) {
+  Word<T, VEC> w;
+  if constexpr (LOOSE) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) w.v[j] = p[j < n ? j : 0];
+  } else {
+    w = *reinterpret_cast<const Word<T, VEC> *>(p);
+  }
+  return w;
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store(T *p, const F2 (&v)[pairs<VEC>()]) {
+template <typename T, int VEC, bool LOOSE = false>
+__device__ __forceinline__ void store(T *p, const F2 (&v)[pairs<VEC>()], int n = VEC) {
   Word<T, VEC> w;
 #pragma unroll
   for (int j = 0; j < VEC; ++j) w.v[j] = from_f<T>(j % 2 ? hi(v[j / 2]) : lo(v[j / 2]));
-  *reinterpret_cast<Word<T, VEC> *>(p) = w;
+  if constexpr (LOOSE) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (j < n) p[j] = w.v[j];
+  } else {
+    *reinterpret_cast<Word<T, VEC> *>(p) = w;
+  }
 }
 __device__ __forceinline__ F2 sigmoid2(F2 v) { return f2(sigmoid(lo(v)), sigmoid(hi(v))); }
 
@@ -86,11 +100,12 @@ constexpr int taps() { return W ? W : RCU_CONV_MAX_TAPS; }
 
 template <int W, int VEC>
 __device__ __forceinline__ void load_taps(const float *weight, const float *bias, int h, int w_n,
-                                          F2 (&w)[taps<W>()][pairs<VEC>()], F2 (&add)[pairs<VEC>()]) {
+                                          F2 (&w)[taps<W>()][pairs<VEC>()], F2 (&add)[pairs<VEC>()],
+                                          int n = VEC) {
   constexpr int MW = taps<W>();
 #pragma unroll
   for (int j = 0; j < pairs<VEC>(); ++j) {
-    const int64_t a = h + 2 * j, b = VEC > 1 ? a + 1 : a;
+    const int64_t a = h + 2 * j, b = VEC > 1 && 2 * j + 1 < n ? a + 1 : a;
     add[j] = bias ? f2(bias[a], bias[b]) : f2(0.f);
 #pragma unroll
     for (int k = 0; k < MW; ++k)
@@ -100,16 +115,19 @@ __device__ __forceinline__ void load_taps(const float *weight, const float *bias
 }
 
 // x_t of a row, out of the state for t < 0.
-template <typename T, int VEC>
+template <typename T, int VEC, bool LOOSE>
 struct Row {
   const T *x, *state;  // at channel h; state rows are `wide` apart
   int64_t st;
-  int w_n, wide;
+  int w_n, wide, left;  // left: channels from h on
+  __device__ __forceinline__ void at(const T *p, F2 (&v)[pairs<VEC>()]) const {
+    widen<T, VEC>(word<T, VEC, LOOSE>(p, left), v);
+  }
   __device__ __forceinline__ void at(int t, F2 (&v)[pairs<VEC>()]) const {
     if (t >= 0) {
-      widen<T, VEC>(word<T, VEC>(x + t * st), v);
+      at(x + t * st, v);
     } else if (state) {
-      widen<T, VEC>(word<T, VEC>(state + (int64_t)(t + w_n - 1) * wide), v);
+      at(state + (int64_t)(t + w_n - 1) * wide, v);
     } else {
 #pragma unroll
       for (int j = 0; j < pairs<VEC>(); ++j) v[j] = f2(0.f);
@@ -126,38 +144,49 @@ struct Row {
     }
   }
 };
-template <typename T, int VEC>
-__device__ __forceinline__ Row<T, VEC> row_of(const SeqIn &x, const void *state, int b, int h,
+template <typename T, int VEC, bool LOOSE>
+__device__ __forceinline__ Row<T, VEC, LOOSE> row_of(const SeqIn &x, const void *state, int b, int h,
                                               int w_n, int H) {
   return {static_cast<const T *>(x.p) + b * x.sb + h,
           state ? static_cast<const T *>(state) + (int64_t)b * (w_n - 1) * H + h : nullptr, x.st,
-          w_n, H};
+          w_n, H, H - h};
 }
 // A thread's steps of a row from t0 to end, AHEAD at a time and BATCHES - 1 such
 // batches ahead: words of 4 bytes or more by asynchronous copies, single bf16 values by
-// plain reads one batch ahead.
-template <typename T, int VEC>
+// plain reads one batch ahead (as pairs out of the one or two words that they lie in,
+// backward T=512 B=64 H=1001 167 us, 150 so).
+template <typename T, int VEC, bool LOOSE>
 struct Steps {
   static constexpr bool ASYNC = sizeof(T) * VEC >= 4;
-  static constexpr int BYTES = ASYNC ? BATCHES * AHEAD * NT * VEC * sizeof(T) : 0;  // of a block
+  static_assert(!LOOSE || sizeof(T) == 4, "values of 4 bytes");
+  static constexpr int BYTES = ASYNC ? BATCHES * AHEAD * NT * sizeof(Word<T, VEC>) : 0;  // of a block
   const T *p;
   int64_t st;
   Word<T, VEC> *ring;
-  int end, batch;
+  int end, left, batch;
   Word<T, VEC> next[ASYNC ? 1 : AHEAD];
-  __device__ __forceinline__ Steps(const Row<T, VEC> &row, void *room, int end_)
-      : p(row.x), st(row.st), ring(static_cast<Word<T, VEC> *>(room) + threadIdx.x), end(end_), batch(0) {}
+  __device__ __forceinline__ Steps(const Row<T, VEC, LOOSE> &row, void *room, int end_)
+      : p(row.x), st(row.st), ring(static_cast<Word<T, VEC> *>(room) + threadIdx.x), end(end_), left(row.left), batch(0) {}
+  template <int N>
+  static __device__ __forceinline__ void copy(void *to, const void *from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                 "l"(from), "n"(N) : "memory");
+  }
   __device__ __forceinline__ void fetch(int t, int k) {
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) {
       if (t + q >= end) break;
       const T *from = p + (t + q) * st;
-      if constexpr (ASYNC)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
-                         (uint32_t)__cvta_generic_to_shared(ring + (k * AHEAD + q) * NT)),
-                     "l"(from), "n"((int)sizeof(Word<T, VEC>)) : "memory");
-      else
+      Word<T, VEC> *to = ring + (k * AHEAD + q) * NT;
+      if constexpr (LOOSE) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (j < left) copy<4>(&to->v[j], from + j);
+      } else if constexpr (ASYNC) {
+        copy<sizeof(Word<T, VEC>)>(to, from);
+      } else {
         next[q] = word<T, VEC>(from);
+      }
     }
   }
   // the batch at t, once it has arrived
@@ -214,7 +243,7 @@ __device__ __forceinline__ void filter(const F2 (&w)[taps<W>()][pairs<VEC>()], i
     }
 }
 
-template <typename T, int W, int VEC>
+template <typename T, int W, int VEC, bool LOOSE>
 __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Split sp, int *err) {
   constexpr int MW = taps<W>(), P = pairs<VEC>();
   const int w_n = W ? W : a.W;
@@ -224,14 +253,14 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Spl
   const int seg = (int)(id / sp.groups / sp.runs);
   extern __shared__ float4 ring[];
   F2 w[MW][P], bias[P];
-  load_taps<W, VEC>(a.weight, a.bias, h, w_n, w, bias);
+  load_taps<W, VEC>(a.weight, a.bias, h, w_n, w, bias, a.H - h);
   const int t0 = seg * sp.len, t1 = min(t0 + sp.len, a.T);
   const int last_b = min((run + 1) * sp.per, a.B);
   for (int b = run * sp.per; b < last_b; ++b) {
     const int n = row_length(a.lengths, b, a.T, err), end = min(t1, n);
-    const Row<T, VEC> row = row_of<T, VEC>(a.x, a.state, b, h, w_n, a.H);
+    const Row<T, VEC, LOOSE> row = row_of<T, VEC, LOOSE>(a.x, a.state, b, h, w_n, a.H);
     T *y = static_cast<T *>(a.y.p) + b * a.y.sb + h;
-    Steps<T, VEC> in(row, ring, end);
+    Steps<T, VEC, LOOSE> in(row, ring, end);
     begin(t0, in);
     F2 win[MW][P];  // the inputs of a step, the newest last
     if (t0 < end) row.before(t0, win);
@@ -241,7 +270,7 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Spl
       T *out = static_cast<T *>(a.state_n) + (int64_t)b * (w_n - 1) * a.H + h;
 #pragma unroll
       for (int k = 1; k < MW; ++k)
-        if (k > MW - w_n) store<T, VEC>(out + (int64_t)(k - 1 - (MW - w_n)) * a.H, last[k - 1]);
+        if (k > MW - w_n) store<T, VEC, LOOSE>(out + (int64_t)(k - 1 - (MW - w_n)) * a.H, last[k - 1], a.H - h);
     }
     int t = t0;
     for (; t < end; t += AHEAD) {
@@ -258,21 +287,21 @@ __global__ void __launch_bounds__(NT) conv_fwd_kernel(const ConvFwd a, const Spl
 #pragma unroll
           for (int j = 0; j < P; ++j) v[j] = mul2(v[j], sigmoid2(v[j]));
         }
-        store<T, VEC>(y + (t + q) * a.y.st, v);
+        store<T, VEC, LOOSE>(y + (t + q) * a.y.st, v, a.H - h);
         shift(win);
       }
     }
     F2 zero[P];
 #pragma unroll
     for (int j = 0; j < P; ++j) zero[j] = f2(0.f);
-    for (t = max(t0, end); t < t1; ++t) store<T, VEC>(y + t * a.y.st, zero);
+    for (t = max(t0, end); t < t1; ++t) store<T, VEC, LOOSE>(y + t * a.y.st, zero, a.H - h);
   }
 }
 
 // A stretch [t0, t1) of dx needs dv up to W - 1 steps past it; the weights' sums
 // take the stretch's own dv.  The first stretch also gives the state's gradient:
 // dx at the steps from -(W - 1) on.
-template <typename T, int W, int VEC>
+template <typename T, int W, int VEC, bool LOOSE>
 __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Split sp, float *part,
                                                       int *err) {
   constexpr int MW = taps<W>(), P = pairs<VEC>();
@@ -283,7 +312,7 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Spl
   const int seg = (int)(id / sp.groups / sp.runs);
   extern __shared__ float4 ring[];
   F2 w[MW][P], bias[P], dw[MW][P], db[P], zero[P];
-  load_taps<W, VEC>(a.weight, a.bias, h, w_n, w, bias);
+  load_taps<W, VEC>(a.weight, a.bias, h, w_n, w, bias, a.H - h);
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     zero[j] = db[j] = f2(0.f);
@@ -294,22 +323,22 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Spl
   const int last_b = min((run + 1) * sp.per, a.B);
   for (int b = run * sp.per; b < last_b; ++b) {
     const int n = row_length(a.lengths, b, a.T, err), end = min(t1, n);
-    const Row<T, VEC> row = row_of<T, VEC>(a.x, a.state, b, h, w_n, a.H);
-    const Row<T, VEC> row_dy = row_of<T, VEC>(a.dy, nullptr, b, h, w_n, a.H);
+    const Row<T, VEC, LOOSE> row = row_of<T, VEC, LOOSE>(a.x, a.state, b, h, w_n, a.H);
+    const Row<T, VEC, LOOSE> row_dy = row_of<T, VEC, LOOSE>(a.dy, nullptr, b, h, w_n, a.H);
     T *dx = a.dx.p ? static_cast<T *>(a.dx.p) + b * a.dx.sb + h : nullptr;
     const T *dlast = a.dstate_n ? static_cast<const T *>(a.dstate_n) + (int64_t)b * (w_n - 1) * a.H + h
                                 : nullptr;
     T *dstate = a.dstate ? static_cast<T *>(a.dstate) + (int64_t)b * (w_n - 1) * a.H + h : nullptr;
-    // steps whose dv is wanted: the stretch and the W - 1 after it; the ones past
+    // steps whose dv is wanted: the stretch and the MW - 1 after it; the ones past
     // the row's end have none, and only bring out what is still on its way
-    const int stop = t0 < end || seg == 0 ? end + w_n - 1 : t0, live = min(stop, n);
+    const int stop = t0 < end || seg == 0 ? end + MW - 1 : t0, live = min(stop, n);
     F2 win[MW][P], grad[MW][P];  // x and dv, the newest last
 #pragma unroll
     for (int k = 0; k < MW; ++k)
 #pragma unroll
       for (int j = 0; j < P; ++j) grad[k][j] = f2(0.f);
-    Steps<T, VEC> in_x(row, ring, live);
-    Steps<T, VEC> in_y(row_dy, reinterpret_cast<char *>(ring) + Steps<T, VEC>::BYTES, live);
+    Steps<T, VEC, LOOSE> in_x(row, ring, live);
+    Steps<T, VEC, LOOSE> in_y(row_dy, reinterpret_cast<char *>(ring) + Steps<T, VEC, LOOSE>::BYTES, live);
     begin(t0, in_x, in_y);
     if (t0 < live) row.before(t0, win);
     // Step t with its words; INNER: all that it touches is the row's and the stretch's.
@@ -342,41 +371,33 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Spl
 #pragma unroll
         for (int j = 0; j < P; ++j) grad[MW - 1][j] = f2(0.f);
       }
-      // dx of the step w_n - 1 back, which tap k met as many steps later as it is from the
+      // dx of the step MW - 1 back, which tap k met as many steps later as it is from the
       // last one
-      const int at = t - (w_n - 1);
-      if (INNER || ((at >= t0 || seg == 0) && at < end)) {
+      const int at = t - (MW - 1);
+      if (INNER || (at >= (seg == 0 ? 1 - w_n : t0) && at < end)) {
         F2 v[P];
         if (!INNER && dlast && at >= n - (w_n - 1))
-          widen<T, VEC>(word<T, VEC>(dlast + (int64_t)(at - n + w_n - 1) * a.H), v);
+          row.at(dlast + (int64_t)(at - n + w_n - 1) * a.H, v);
         else
 #pragma unroll
           for (int j = 0; j < P; ++j) v[j] = f2(0.f);
 #pragma unroll
         for (int k = 0; k < MW; ++k) {
-          if (W) {
+          if (W || k >= MW - w_n) {
 #pragma unroll
             for (int j = 0; j < P; ++j) v[j] = fma2(w[k][j], grad[MW - 1 - k][j], v[j]);
-          } else if (k >= MW - w_n) {
-            const int newest = MW - 1 - k + (MW - w_n);  // of the gradients in grad
-#pragma unroll
-            for (int m = 0; m < MW; ++m)
-              if (m == newest) {
-#pragma unroll
-                for (int j = 0; j < P; ++j) v[j] = fma2(w[k][j], grad[m][j], v[j]);
-              }
           }
         }
         if (INNER || at >= 0) {
-          if (dx) store<T, VEC>(dx + at * a.dx.st, v);
+          if (dx) store<T, VEC, LOOSE>(dx + at * a.dx.st, v, a.H - h);
         } else if (dstate) {
-          store<T, VEC>(dstate + (int64_t)(at + w_n - 1) * a.H, v);
+          store<T, VEC, LOOSE>(dstate + (int64_t)(at + w_n - 1) * a.H, v, a.H - h);
         }
       }
       shift(win);
       shift(grad);
     };
-    const int from = t0 + w_n - 1;  // the step from which on dx comes out for the stretch
+    const int from = t0 + MW - 1;  // the step from which on dx comes out for the stretch
     for (int t = t0; t < stop; t += AHEAD) {
       Word<T, VEC> now_x[AHEAD], now_y[AHEAD];
       ahead(t, in_x, in_y);
@@ -392,13 +413,14 @@ __global__ void __launch_bounds__(NT) conv_bwd_kernel(const ConvBwd a, const Spl
       }
     }
     if (dx)
-      for (int t = max(t0, end); t < t1; ++t) store<T, VEC>(dx + t * a.dx.st, zero);
+      for (int t = max(t0, end); t < t1; ++t) store<T, VEC, LOOSE>(dx + t * a.dx.st, zero, a.H - h);
   }
   if (!part) return;
   // [stretch, run][h, tap | bias]
   float *out = part + ((int64_t)seg * sp.runs + run) * a.H * (w_n + 1);
 #pragma unroll
   for (int j = 0; j < VEC; ++j) {
+    if (LOOSE && h + j >= a.H) break;
 #pragma unroll
     for (int k = 0; k < MW; ++k)
       if (k >= MW - w_n)
@@ -466,17 +488,17 @@ __global__ void __launch_bounds__(NT) conv_step_kernel(const ConvStep a, int *er
 }
 
 // Runs f with the kernel's number of taps: those of the usual widths known to the
-// compiler, the others (of threads with one channel) not.
+// compiler, the others (of threads with one channel or two) not.
 constexpr bool usual(int W) { return W >= 2 && W <= 4; }
 template <int VEC, typename F>
 cudaError_t by_taps(int W, F f) {
+  if constexpr (VEC <= 2)
+    if (!usual(W)) return f(std::integral_constant<int, 0>());
   switch (W) {
     case 2: return f(std::integral_constant<int, 2>());
     case 3: return f(std::integral_constant<int, 3>());
     case 4: return f(std::integral_constant<int, 4>());
-    default:
-      if constexpr (VEC == 1) return f(std::integral_constant<int, 0>());
-      return cudaErrorInvalidValue;
+    default: return cudaErrorInvalidValue;
   }
 }
 
@@ -503,11 +525,11 @@ cudaError_t launch(void (*fn)(KArgs...), const Split &sp, int bytes, cudaStream_
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool LOOSE>
 cudaError_t fwd(const ConvFwd &p, int *err, int nsm, cudaStream_t s) {
   return by_taps<VEC>(p.W, [&](auto w) {
-    auto fn = conv_fwd_kernel<T, decltype(w)::value, VEC>;
-    constexpr int bytes = Steps<T, VEC>::BYTES;
+    auto fn = conv_fwd_kernel<T, decltype(w)::value, VEC, LOOSE>;
+    constexpr int bytes = Steps<T, VEC, LOOSE>::BYTES;
     static PerDevice<Room> rooms;
     const Room room = rooms.here([&] { return room_of(fn, bytes, nsm); });
     if (room.set != cudaSuccess) return room.set;
@@ -515,11 +537,11 @@ cudaError_t fwd(const ConvFwd &p, int *err, int nsm, cudaStream_t s) {
     return launch(fn, sp, bytes, s, p, sp, err);
   });
 }
-template <typename T, int VEC>
+template <typename T, int VEC, bool LOOSE>
 cudaError_t bwd(const ConvBwd &p, DevMem &ws, int *err, int nsm, cudaStream_t s, int *launches) {
   return by_taps<VEC>(p.W, [&](auto w) {
-    auto fn = conv_bwd_kernel<T, decltype(w)::value, VEC>;
-    constexpr int bytes = 2 * Steps<T, VEC>::BYTES;
+    auto fn = conv_bwd_kernel<T, decltype(w)::value, VEC, LOOSE>;
+    constexpr int bytes = 2 * Steps<T, VEC, LOOSE>::BYTES;
     static PerDevice<Room> rooms;
     const Room room = rooms.here([&] { return room_of(fn, bytes, nsm); });
     if (room.set != cudaSuccess) return room.set;
@@ -542,29 +564,49 @@ bool fits(const SeqIn &x, const void *state, const void *state_n, int H, int siz
          (!state_n || aligned(state_n, H, size, vec));
 }
 
+// The channels of a thread: as many as words of 16 (backwards 8 of bf16) bytes hold; where
+// rows are not aligned to those, or the taps so many that the registers do not hold them,
+// two, of bf16 as words of 4 bytes, of fp32 each by itself (LOOSE); of bf16 rows aligned to
+// less, one.  W=4 T=512 B=64, forward and backward us: fp32 H=1001 55 and 113 (as single
+// values 61 and 151), bf16 H=1002 47 and 75 (64 and 151); H=1024, W=5 in place of 4: 70 and
+// 179 in place of 37 and 72 (as single values 119 and 329).
+template <int VEC, bool LOOSE = false>
+struct Kind {
+  static constexpr int vec = VEC;
+  static constexpr bool loose = LOOSE;
+};
+template <typename T, int WIDE, typename Fits, typename Run>
+cudaError_t by_kind(int W, bool vec, Fits fit, Run run) {
+  if (usual(W) && vec && fit(WIDE)) return run(Kind<WIDE>());
+  if constexpr (sizeof(T) == 4) return run(Kind<2, true>());
+  else return vec && fit(2) ? run(Kind<2>()) : run(Kind<1>());
+}
+
 }  // namespace
 
 cudaError_t launch_conv_fwd(const ConvFwd &p, int *err, int nsm, bool vec, cudaStream_t s,
                             int *launches) {
   ++*launches;
-  const int size = p.dtype == RCU_BF16 ? 2 : 4, n = 16 / size;
-  const bool wide = vec && usual(p.W) && fits(p.x, p.state, p.state_n, p.H, size, n) &&
-                    aligned(p.y, size, n);
+  const int size = p.dtype == RCU_BF16 ? 2 : 4;
+  auto fit = [&](int n) { return fits(p.x, p.state, p.state_n, p.H, size, n) && aligned(p.y, size, n); };
   if (p.dtype == RCU_BF16)
-    return wide ? fwd<bf16, 8>(p, err, nsm, s) : fwd<bf16, 1>(p, err, nsm, s);
-  return wide ? fwd<float, 4>(p, err, nsm, s) : fwd<float, 1>(p, err, nsm, s);
+    return by_kind<bf16, 8>(p.W, vec, fit, [&](auto k) { return fwd<bf16, k.vec, k.loose>(p, err, nsm, s); });
+  return by_kind<float, 4>(p.W, vec, fit, [&](auto k) { return fwd<float, k.vec, k.loose>(p, err, nsm, s); });
 }
 
 cudaError_t launch_conv_bwd(const ConvBwd &p, DevMem &ws, int *err, int nsm, bool vec,
                             cudaStream_t s, int *launches) {
   ++*launches;
   const int size = p.dtype == RCU_BF16 ? 2 : 4;
-  const bool wide = vec && usual(p.W) && fits(p.x, p.state, p.dstate_n, p.H, size, 4) &&
-                    fits(p.dy, p.dstate, nullptr, p.H, size, 4) &&
-                    (!p.dx.p || aligned(p.dx, size, 4));
+  auto fit = [&](int n) {
+    return fits(p.x, p.state, p.dstate_n, p.H, size, n) && fits(p.dy, p.dstate, nullptr, p.H, size, n) &&
+           (!p.dx.p || aligned(p.dx, size, n));
+  };
   if (p.dtype == RCU_BF16)
-    return wide ? bwd<bf16, 4>(p, ws, err, nsm, s, launches) : bwd<bf16, 1>(p, ws, err, nsm, s, launches);
-  return wide ? bwd<float, 4>(p, ws, err, nsm, s, launches) : bwd<float, 1>(p, ws, err, nsm, s, launches);
+    return by_kind<bf16, 4>(p.W, vec, fit,
+                            [&](auto k) { return bwd<bf16, k.vec, k.loose>(p, ws, err, nsm, s, launches); });
+  return by_kind<float, 4>(p.W, vec, fit,
+                           [&](auto k) { return bwd<float, k.vec, k.loose>(p, ws, err, nsm, s, launches); });
 }
 
 template <typename T, int VEC, bool WORDS>

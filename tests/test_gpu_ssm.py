@@ -128,6 +128,17 @@ def test_conv(ops, path, dtype, T, B, H, W, kw):
     check_conv(ops, T, B, H, W, dtype, **kw)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,B,H,W,kw", [
+    (50, 6, 10, 4, {"lengths": [0, 1, 2, 3, 50, 49]}), (50, 6, 11, 3, {"lengths": [0, 1, 2, 3, 50, 49]}),
+    (70, 7, 22, 6, {"lengths": [0, 1, 4, 5, 6, 70, 64]}), (70, 4, 21, 7, {"lengths": [3, 70, 0, 69], "gap": 2}),
+    (41, 3, 6, 1, {"lengths": [41, 0, 7]}), (2, 900, 1001, 4, {}), (1, 700, 1002, 8, {}), (301, 2, 34, 5, {"gap": 2}),
+    (9, 2, 1, 4, {}), (9, 2, 2, 8, {"batch_first": True})])
+def test_conv_in_pairs(ops, dtype, T, B, H, W, kw):
+    """Widths of two, not of four channels, odd ones, and unusual numbers of taps."""
+    check_conv(ops, T, B, H, W, dtype, **kw)
+
+
 def test_conv_rows_beyond_the_gpu(ops):
     """More rows than threads: a thread takes several, and their sums."""
     check_conv(ops, 3, 3000, 1024, 4, "bf16", lengths=[b % 4 for b in range(3000)])
