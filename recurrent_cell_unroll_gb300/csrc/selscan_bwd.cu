@@ -12,20 +12,21 @@
 //
 // A thread has S states of K neighbouring channels, a warp all states of its own
 // channels, so only the sums over channels (db, dc) leave a warp.  They are what
-// costs beside the exponentials: a thread adds its two channels' first, the lanes
-// exchange theirs in shared memory (as shuffles they took half of the time), and the
-// warps' sums stand where the checkpoint of the four steps was.  Sums over states are
-// left in parts by the lanes, and added by the lanes that compute the outputs, as words
-// of two channels.
+// costs beside the exponentials: a thread adds its two channels' first, the lanes of the
+// same states halve theirs with one another (7 shuffles; exchanged in shared memory N=16
+// 504 us, 488 so, N=64 1060 and 979), and the warps' sums stand where the checkpoint of the
+// four steps was.  Sums over states are left in parts by the lanes, and added by the lanes
+// that compute the outputs, as words of two channels.
 //
 // Two channels a thread and not four, though those read less of shared memory: 8 warps
 // an SM in the place of 6 (bf16, N=16, T=2048 B=8 H=2048 1190 -> 802 us).  Three blocks
 // an SM, at 168 registers, were no faster (the decays kept 1015 us, computed again 928,
 // two blocks 755).
 //
-// Measured, N=16: bf16 T=2048 B=8 H=2048 682 us, T=8192 B=2 H=1024 (19 segments) 500, of
-// which 100 for their ends and 32 for chaining and sums; fp32 T=500 B=32 H=512, mixed
-// lengths, 200.  Issue bound: 27 instructions a state and step at 1.9 a cycle.
+// Measured, N=16: bf16 T=8192 B=2 H=1024 (19 segments) 488 us, of which 100 for their ends
+// and 32 for chaining and sums; fp32 T=500 B=32 H=512, mixed lengths, 212.  Bf16 T=512 B=16
+// H=1024: N=8 228, 16 282, 32 437, 64 979.  Issue bound: 27 instructions a state and step
+// at 1.9 a cycle.
 #include "selscan.cuh"
 
 namespace rcu {
@@ -57,14 +58,23 @@ struct Shape {
   // Checkpoints of a chunk, one of the first steps only where the sums over channels
   // of two groups of steps do not fit into one.
   static constexpr int SLOTS = NP > 16 ? SUBS : SUBS - 1;
-  static constexpr int SUMS = NP > 32 ? TILE * 2 * NP : 0;     // floats of such sums elsewhere
+  // Floats of a warp's sums over channels that a checkpoint does not hold: of more than
+  // 32 states, those of the last two of four steps.  (With all of them outside, 16 kB a
+  // warp, an SM had one block in the place of two: N=64 T=512 B=16 H=1024 bf16 1494 us.)
+  static constexpr int SUMS = NP > 32 ? TILE / 2 * 2 * NP : 0;
   static constexpr int PARTS = LANES < 4 ? LANES : 4;
   static constexpr int WORDS = SUB * WC / K;                   // pairs of a warp's four steps
   static constexpr int MINE = (WORDS + 31) / 32;               // of them, of a lane
   static constexpr int PART = SUB * WC + 8;                    // floats: parts 8 banks apart
-  // floats of a warp: checkpoints, parts of three sums, the lanes' exchange
-  static constexpr int WARP = SLOTS * SLOT + SUMS + 3 * PARTS * PART + 256;
-  static constexpr int SHARED = 4 * (WARPS * WARP + 3 * TILE * CC + 2 * TILE * NP + 2 * CC);
+  // floats of a warp: checkpoints, parts of three sums
+  static constexpr int WARP = SLOTS * SLOT + SUMS + 3 * PARTS * PART;
+  // What the outputs need of the tile's inputs is kept for them, x, dt, dy and z as read
+  // (read again, N=32 467 us, 450 so; fewer states leave no room, see AHEAD).
+  static constexpr bool KEPT = LANES > 4;
+  template <typename T>
+  static constexpr int shared() {
+    return 4 * (WARPS * WARP + 3 * TILE * CC + 2 * TILE * NP + 2 * CC) + (KEPT ? 4 * TILE * CC * (int)sizeof(T) : 0);
+  }
 };
 
 // Four channels' values of a row, by a word where rows are aligned.
@@ -122,8 +132,10 @@ __device__ __forceinline__ void prefetch(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
+// Blocks of eight warps an SM in all; left to itself the compiler takes 168 registers for
+// N=32 and up and spills (N=32 503 us, 445 so).
 template <typename T, int LANES, bool ALIGNED>
-__global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a, int *err) {
+__global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan_bwd_kernel(const Args a, int *err) {
   typedef Shape<LANES> Sh;
   constexpr int NP = Sh::NP, WC = Sh::WC, NT = Sh::NT, CC = Sh::CC, SLOTS = Sh::SLOTS, PARTS = Sh::PARTS;
   constexpr int PART = Sh::PART, ROW = CC / 4;
@@ -142,6 +154,8 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
   float(*s_b)[NP] = reinterpret_cast<float(*)[NP]>(s_gy + TILE * CC);
   float(*s_c)[NP] = s_b + TILE;
   float *s_bias = &s_c[TILE][0], *s_skip = s_bias + CC;  // dt_bias, d
+  constexpr bool KEPT = Sh::KEPT;
+  T(*s_in)[TILE][CC] = reinterpret_cast<T(*)[TILE][CC]>(s_skip + CC);  // KEPT
 
   const int group = blockIdx.x % a.groups;
   const int b = (int)(blockIdx.x / a.groups % in.B), seg = (int)(blockIdx.x / a.groups / in.B);
@@ -154,7 +168,6 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
   const int t0 = seg * a.seg.len, t1 = min(t0 + a.seg.len, in.T), end = min(t1, n);
   float *check = shared + warp * Sh::WARP;    // [SLOTS][SLOT]
   float *parts = check + SLOTS * SLOT + Sh::SUMS;  // [3][PARTS][PART]
-  float *swap = parts + 3 * PARTS * PART;     // [256]
 
   auto here = [&](int c) { return ch0 + own + c < in.H ? min(max(in.N - n0, 0), S) : 0; };
   auto load_all = [&](const float *from, F2 (&v)[S]) {
@@ -230,12 +243,12 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
 #pragma unroll
     for (int q = 0; q < S; ++q) to[q] = from[q];
   };
-  // where the warp's db and dc of a group of four steps are: in the place of its
-  // checkpoint; of the first group, which has none, behind those of the second
-  auto sums_of = [&](float *from, int sub) {
+  // where the warp's db and dc of step j of a group of four are: in the place of its
+  // checkpoint; of the first group, where it has none, behind those of the second
+  auto sums_of = [&](float *from, int sub, int j) {
     const int slot = sub + SLOTS - SUBS;
-    if (Sh::SUMS) return from + SLOTS * SLOT + sub * SUB * 2 * NP;
-    return from + (slot < 0 ? SUB * 2 * NP : slot * SLOT);
+    if (Sh::SUMS && j >= SUB / 2) return from + SLOTS * SLOT + (sub * SUB / 2 + j - SUB / 2) * 2 * NP;
+    return from + (slot < 0 ? SUB * 2 * NP : slot * SLOT) + j * 2 * NP;
   };
 
   const int tiles = t0 < end ? ceil_div(end - t0, TILE) : 0;
@@ -268,6 +281,11 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
           v = pairs_of(wt[q]) + four(s_bias + in_col);
           v = {softplus(v.a), softplus(v.b)};
           u = v * pairs_of(wx[q]);
+          if constexpr (KEPT) {
+            auto keep = [&](int i, const Word<T, 4> &w) { *reinterpret_cast<Word<T, 4> *>(&s_in[i][r][in_col]) = w; };
+            keep(0, wx[q]), keep(1, wt[q]);
+            if (z) keep(2, wy[q]), keep(3, wz[q]);
+          }
           g = pairs_of(wy[q]);
           if (z) {
             const Four zs = pairs_of(wz[q]);
@@ -318,6 +336,12 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
       auto read = [&](int r) {  // the words of the outputs at row r of the tile
         const int64_t t = base + r;
         if (r >= steps || out_left <= 0 || (Sh::WORDS < 32 && out_row >= SUB)) return;
+        if constexpr (KEPT) {
+          auto kept = [&](int i) { return *reinterpret_cast<const Word<T, 2> *>(&s_in[i][r][out_col]); };
+          wx = kept(0), wt = kept(1);
+          if (z) wy = kept(2), wz = kept(3);
+          return;
+        }
         wx = load_two<ALIGNED>(x + t * in.x.st + ch0 + out_col, out_left);
         wt = load_two<ALIGNED>(dt + t * in.dt.st + ch0 + out_col, out_left);
         if (z) {
@@ -394,36 +418,29 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
           *reinterpret_cast<F2 *>(to + PARTS * PART) = sd;
           *reinterpret_cast<F2 *>(to + 2 * PARTS * PART) = sl;
         }
-        // sums over the warp's channels: lane (cl, l) leaves 8 values, of b and c; the
-        // two halves of every other four lanes change places, to hit different banks
-        {
-          __syncwarp();
-          float4 *put = reinterpret_cast<float4 *>(swap) + lane * 2;
-          const int turn = lane >> 2 & 1;
-          put[turn] = make_float4(db[0], db[1], db[2], db[3]);
-          put[turn ^ 1] = make_float4(dc[0], dc[1], dc[2], dc[3]);
-          __syncwarp();
-          auto value = [&](int s, int i) { return swap[s * 8 + ((i >> 2) ^ (s >> 2 & 1)) * 4 + (i & 3)]; };
-          if (LANES <= 4) {
-            // output (l, i) by lanes of 8 sources each
-            const int i = lane / LANES % 8, from = lane / LANES / 8 * 8;
-            float s = 0.f;
+        // sums over the warp's channels: its lanes of the same states halve with one another
+        // what they hold, by b and c first
+        float v8[2 * S];
 #pragma unroll
-            for (int m = 0; m < 8; ++m) s += value((from + m) * LANES + l, i);
+        for (int q = 0; q < S; ++q) v8[q] = db[q], v8[S + q] = dc[q];
+        int count = 2 * S;
 #pragma unroll
-            for (int o = 8 * LANES; o < 32; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-            bc[j][0] = s;
-          } else {
-            // OUTS outputs of a lane: l, i = (lane / LANES) + 32 / LANES m
-#pragma unroll
-            for (int m = 0; m < OUTS; ++m) {
-              float s = 0.f;
-#pragma unroll
-              for (int f = 0; f < 32 / LANES; ++f) s += value(f * LANES + l, cl + 32 / LANES * m);
-              bc[j][m] = s;
-            }
+        for (int o = 16; o >= LANES; o /= 2) {
+          if (count == 1) {
+            v8[0] += __shfl_xor_sync(0xffffffffu, v8[0], o);
+            continue;
           }
+          count /= 2;
+          const bool upper = lane & o;
+#pragma unroll
+          for (int q = 0; q < S; ++q)
+            if (q < count) {
+              const float mine = upper ? v8[q + count] : v8[q], other = upper ? v8[q] : v8[q + count];
+              v8[q] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+            }
         }
+#pragma unroll
+        for (int m = 0; m < OUTS; ++m) bc[j][m] = v8[m];
       };
       if (AHEAD && sub == 0) fetched();
       if (sub < subs - 1) start(h);  // the last ones are at hand
@@ -439,14 +456,15 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
 #pragma unroll
       for (int j = SUB - 1; j >= 0; --j) back(j);
       if (a.part_bc) {
-        float *to = sums_of(check, sub);
 #pragma unroll
-        for (int j = 0; j < SUB; ++j)
+        for (int j = 0; j < SUB; ++j) {
+          float *to = sums_of(check, sub, j);
 #pragma unroll
           for (int m = 0; m < OUTS; ++m) {
-            const int i = LANES <= 4 ? lane / LANES % 8 : cl + 32 / LANES * m;
-            if (LANES > 4 || lane / LANES < 8) to[j * 2 * NP + (i >> 2) * NP + n0 + (i & 3)] = bc[j][m];
+            const int i = lane / (LANES < 4 ? 4 : LANES) * OUTS + m;
+            if (LANES >= 4 || lane % 4 < LANES) to[(i >> 2) * NP + n0 + (i & 3)] = bc[j][m];
           }
+        }
       }
       __syncwarp();
       // the outputs: dx = delta sd + gy d, ddt = (sl A + sd x) sigmoid(dt), dz = dy (so + d x) silu'(z)
@@ -504,7 +522,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT) scan_bwd_kernel(const Args a
       constexpr int QUADS = 2 * NP / 4;
       for (int i = tid; i < steps * QUADS; i += NT) {
         const int t = i / QUADS, m = i % QUADS * 4, q = m % NP;
-        const float *from = sums_of(shared, t / SUB) + t % SUB * 2 * NP + m;
+        const float *from = sums_of(shared, t / SUB, t % SUB) + m;
         Four v = four(from);
 #pragma unroll
         for (int w = 1; w < Sh::WARPS; ++w) v = v + four(from + w * Sh::WARP);
@@ -577,20 +595,21 @@ cudaError_t run(Args a, int *err, cudaStream_t s, int *launches) {
   auto fn = scan_bwd_kernel<T, LANES, ALIGNED>;
   static PerDevice<cudaError_t> ready;
   const cudaError_t set = ready.here(
-      [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SHARED); });
+      [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::template shared<T>()); });
   if (set != cudaSuccess) return set;
   ++*launches;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((int64_t)a.groups * a.p.in.B * a.seg.n));
   cfg.blockDim = dim3(Sh::NT);
-  cfg.dynamicSmemBytes = Sh::SHARED;
+  cfg.dynamicSmemBytes = Sh::template shared<T>();
   cfg.stream = s;
   return cudaLaunchKernelEx(&cfg, fn, a, err);
 }
 
+// Of four states or fewer a channel, half of the lanes' are idle: a kernel for those alone,
+// with one warp a block and six an SM, was slower (N=4 bf16 T=512 B=16 H=1024 315 us, 248).
 template <typename F>
 cudaError_t by_lanes(int N, F f) {
-  if (N <= 4) return f(std::integral_constant<int, 1>());
   if (N <= 8) return f(std::integral_constant<int, 2>());
   if (N <= 16) return f(std::integral_constant<int, 4>());
   if (N <= 32) return f(std::integral_constant<int, 8>());
