@@ -53,7 +53,7 @@ template <int LANES>
 struct Shape {
   static constexpr int NP = S * LANES;
   static constexpr int WC = 32 / LANES * K;                    // channels of a warp
-  static constexpr int WARPS = WC >= 64 ? 1 : WC == 32 ? 2 : 4;  // of a block
+  static constexpr int WARPS = LANES == 2 ? 2 : 4;             // of a block
   static constexpr int NT = 32 * WARPS, CC = WC * WARPS;
   // Checkpoints of a chunk, one of the first steps only where the sums over channels
   // of two groups of steps do not fit into one.
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
         }
         // sums over the states, down to PARTS lanes
 #pragma unroll
-        for (int o = LANES / 2; o >= PARTS && o > 0; o /= 2) {
+        for (int o = LANES / 2; o >= PARTS; o /= 2) {
           so = add2(so, __shfl_xor_sync(0xffffffffu, so, o));
           sd = add2(sd, __shfl_xor_sync(0xffffffffu, sd, o));
           sl = add2(sl, __shfl_xor_sync(0xffffffffu, sl, o));
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
           float *to = sums_of(check, sub, j);
 #pragma unroll
           for (int m = 0; m < OUTS; ++m) {
-            const int i = lane / (LANES < 4 ? 4 : LANES) * OUTS + m;
+            const int i = lane / (LANES < 4 ? 4 : LANES) * OUTS + m;  // of LANES 2, every other pair's
             if (LANES >= 4 || lane % 4 < LANES) to[(i >> 2) * NP + n0 + (i & 3)] = bc[j][m];
           }
         }

@@ -37,19 +37,18 @@ struct Args {
 constexpr int S = 4, K = 4, P = K / 2, TILE = CHUNK / 2;
 template <int LANES>
 struct Shape {
-  static constexpr int WARPS = LANES <= 2 ? 1 : LANES / 2;   // of a block
+  static constexpr int WARPS = LANES / 2;  // of a block
   static constexpr int NT = 32 * WARPS, CC = NT / LANES * K, NP = S * LANES;
   // sums over a channel's states come in PARTS, added as they are read; the first two
   // are where the steps' delta and input stood
   static constexpr int PARTS = LANES < 4 ? LANES : 4;
-  static constexpr int BUF = TILE * CC + 8;              // floats: parts 8 banks apart
-  static constexpr int BUFS = PARTS < 2 ? 2 : PARTS;
+  static constexpr int BUF = TILE * CC + 8;  // floats: parts 8 banks apart
 };
 template <typename T, int LANES, bool ALIGNED, Mode MODE>
 constexpr int shared_bytes() {
   typedef Shape<LANES> Sh;
   typedef Fetch<T, Sh::NT, TILE, Sh::CC, ALIGNED> F;
-  return (MODE == MAIN ? Sh::BUFS : 2) * Sh::BUF * 4 + (MODE == MAIN ? 2 : 1) * TILE * Sh::NP * 4 +
+  return (MODE == MAIN ? Sh::PARTS : 2) * Sh::BUF * 4 + (MODE == MAIN ? 2 : 1) * TILE * Sh::NP * 4 +
          2 * (MODE == ENDS ? 2 : 3) * TILE * F::RS * (int)sizeof(T);
 }
 
@@ -65,8 +64,8 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
   constexpr int RS = F::RS;
   constexpr bool SHIFTS = F::SHIFTS;
   extern __shared__ float4 shared4[];
-  float *buf = reinterpret_cast<float *>(shared4);                     // [BUFS][BUF]: delta, input
-  float(*in_w)[NP] = reinterpret_cast<float(*)[NP]>(buf + (MODE == MAIN ? Sh::BUFS : 2) * BUF);  // b (GRADS: c)
+  float *buf = reinterpret_cast<float *>(shared4);                     // [PARTS][BUF]: delta, input
+  float(*in_w)[NP] = reinterpret_cast<float(*)[NP]>(buf + (MODE == MAIN ? PARTS : 2) * BUF);  // b (GRADS: c)
   float(*out_w)[NP] = in_w + TILE;                                    // MAIN: c
   T(*raw)[TILE][RS] = reinterpret_cast<T(*)[TILE][RS]>(MODE == MAIN ? out_w + TILE : in_w + TILE);
   const ScanIn &p = a.in;
@@ -212,7 +211,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
         int at = 0, count = U * P;
         F2 *sum = &v[0][0];
 #pragma unroll
-        for (int o = LANES / 2; o >= PARTS && o > 0; o /= 2) {
+        for (int o = LANES / 2; o >= PARTS; o /= 2) {
           count /= 2;
           const bool upper = l & o;
           at += upper ? count : 0;
@@ -344,7 +343,8 @@ cudaError_t of_lanes(const Args &a, bool aligned, int *err, cudaStream_t s, int 
 template <typename T, Mode MODE>
 cudaError_t of_type(const Args &a, bool aligned, int *err, cudaStream_t s, int *launches) {
   const int N = a.in.N;
-  if (N <= 4) return of_lanes<T, MODE, 1>(a, aligned, err, s, launches);
+  // of four states or fewer, half of the lanes' are idle: a kernel for those alone was no
+  // faster (N=4 T=512 H=1024: bf16 B=16 82 us, 77 so, B=64 197 and 155)
   if (N <= 8) return of_lanes<T, MODE, 2>(a, aligned, err, s, launches);
   if (N <= 16) return of_lanes<T, MODE, 4>(a, aligned, err, s, launches);
   if (N <= 32) return of_lanes<T, MODE, 8>(a, aligned, err, s, launches);
@@ -400,7 +400,7 @@ cudaError_t launch_scan_fwd(const ScanFwd &p, DevMem &ws, int *err, int nsm, boo
   a.y = p.y;
   a.h_n = p.h_n;
   a.states = p.states;
-  const int64_t blocks = (int64_t)ceil_div(in.H, in.N > 4 ? 64 : 128) * in.B;
+  const int64_t blocks = (int64_t)ceil_div(in.H, 64) * in.B;
   a.m.seg = segments_of(in.T, blocks, nsm, 8);
   if (a.m.seg.n > 1) {
     const cudaError_t e = ws.get((size_t)a.m.seg.n * (table + (int64_t)in.B * in.H) * 4, &a.m.end);
