@@ -23,10 +23,10 @@
 // an SM, at 168 registers, were no faster (the decays kept 1015 us, computed again 928,
 // two blocks 755).
 //
-// Measured, N=16: bf16 T=8192 B=2 H=1024 (19 segments) 488 us, of which 100 for their ends
-// and 32 for chaining and sums; fp32 T=500 B=32 H=512, mixed lengths, 212.  Bf16 T=512 B=16
+// Measured, N=16: bf16 T=8192 B=2 H=1024 (19 segments) 483 us, of which 100 for their ends
+// and 32 for chaining and sums; fp32 T=500 B=32 H=512, mixed lengths, 203.  Bf16 T=512 B=16
 // H=1024: N=8 228, 16 282, 32 437, 64 979.  Issue bound: 27 instructions a state and step
-// at 1.9 a cycle.
+// at 2.0 a cycle.
 #include "selscan.cuh"
 
 namespace rcu {
