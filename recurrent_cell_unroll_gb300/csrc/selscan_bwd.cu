@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
   // waited for, some 1700 cycles, by six warps an SM.  Of 16 states a channel, which
   // leave the upper halves of the checkpoints free.
   constexpr bool AHEAD = LANES == 4 && ALIGNED;
+  constexpr bool GUARD = LANES == 16;  // the row's end, at every step (below)
   const ScanBwd &p = a.p;
   const ScanIn &in = p.in;
   extern __shared__ float4 shared4[];
@@ -319,8 +320,10 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
       step(t, h);
       if (t % SUB == SUB - 1) save(t / SUB + SLOTS - (SUBS - 1), h);
     }
-#pragma unroll 1
-    for (int sub = subs - 1; sub >= 0; --sub) {
+    // Four steps backwards.  CAREFUL: what does not exist must not get into the sums, where an
+    // infinity would make it NaN.
+    auto back_over = [&](int sub, auto care) {
+      constexpr bool CAREFUL = decltype(care)::value;
       const int slot = sub + SLOTS - SUBS;
       // AHEAD: the upper half of a slot, 16 bytes a lane; the first states are in those of
       // slots 2 and 3
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
           e[q] = mul2(e[q], ex2_2(mul2(d, A2[q])));
           const F2 r = mul2(e[q], before[j][q]);
           sl = q ? fma2(r, A2[q], sl) : mul2(r, A2[q]);
-          dA[q] = fma2(r, d, dA[q]);
+          if (!(CAREFUL || GUARD) || t < steps) dA[q] = fma2(r, d, dA[q]);
           h[q] = before[j][q];
         }
         // sums over the states, down to PARTS lanes
@@ -513,7 +516,15 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
         dd = fma2(gy, xv, dd);
       }
       __syncwarp();  // before the next steps' parts
-    }
+    };
+    // The last four steps, where the row ends in the midst of them, with care; with more than
+    // 32 states a select at every step is faster than a second body (N=64 T=512 B=16 H=1024 bf16
+    // 972 us, 997), with fewer the body is (N=16 T=300 B=64 H=2048 938 us, 981).
+    int sub = subs - 1;
+#pragma unroll 1
+    for (const int last = GUARD ? subs : steps / SUB; sub >= last; --sub) back_over(sub, std::true_type());
+#pragma unroll 1
+    for (; sub >= 0; --sub) back_over(sub, std::false_type());
     __syncthreads();
     if (a.part_bc) {
       // four neighbouring sums of a step at a time: [steps][2][N]
