@@ -132,9 +132,9 @@ __device__ __forceinline__ void prefetch(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// Blocks of eight warps an SM in all; left to itself the compiler takes 168 registers for
-// N=32 and up and spills (N=32 503 us, 445 so).
-template <typename T, int LANES, bool ALIGNED>
+// WHOLE: the lanes' states are all a channel's.  Blocks of eight warps an SM in all; left to
+// itself the compiler takes 168 registers for N=32 and up and spills (N=32 503 us, 445 so).
+template <typename T, int LANES, bool ALIGNED, bool WHOLE>
 __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan_bwd_kernel(const Args a, int *err) {
   typedef Shape<LANES> Sh;
   constexpr int NP = Sh::NP, WC = Sh::WC, NT = Sh::NT, CC = Sh::CC, SLOTS = Sh::SLOTS, PARTS = Sh::PARTS;
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
   // waited for, some 1700 cycles, by six warps an SM.  Of 16 states a channel, which
   // leave the upper halves of the checkpoints free.
   constexpr bool AHEAD = LANES == 4 && ALIGNED;
-  constexpr bool GUARD = LANES == 16;  // the row's end, at every step (below)
+  constexpr bool GUARD = WHOLE && LANES == 16;  // the row's end, at every step (below)
   const ScanBwd &p = a.p;
   const ScanIn &in = p.in;
   extern __shared__ float4 shared4[];
@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
     const float *first = p.states + (base / TILE) * table + at0;  // the states before the tile
     F2 h[S];
     load_all(first, h);
+    F2 probe = f2(0.f);  // NaN where an input of the states or of their gradients is not finite
     constexpr int PASS = NT / ROW, MOST = 4;
     constexpr int BATCH = TILE / PASS < MOST ? TILE / PASS : MOST;  // words in flight, of rows PASS apart
 #pragma unroll 1
@@ -296,11 +297,17 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
         put_four(s_delta + r * CC + in_col, v);
         put_four(s_u + r * CC + in_col, u);
         put_four(s_gy + r * CC + in_col, g);
+        if (!WHOLE) probe = fma2(u.b, f2(0.f), fma2(u.a, f2(0.f), probe));
+        if (!WHOLE) probe = fma2(g.b, f2(0.f), fma2(g.a, f2(0.f), probe));
       }
     }
     rb.put(s_b);
     rc.put(s_c);
-    __syncthreads();
+    // States that do not exist have weights of 0, and stay 0 (their gradients too) but for
+    // infinite inputs.
+    int met = 0;
+    if (WHOLE) __syncthreads();
+    else met = __syncthreads_or(isnan(lo(probe)) || isnan(hi(probe)));
     if (k > 0) {  // the tile before, into the second-level cache
       constexpr int LINE = 128 / sizeof(T);  // values
       for (int i = tid; i < TILE * ((CC + LINE - 1) / LINE); i += NT) {
@@ -324,6 +331,7 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
     // infinity would make it NaN.
     auto back_over = [&](int sub, auto care) {
       constexpr bool CAREFUL = decltype(care)::value;
+      auto keep_there = [&](int q, F2 &v) { v = f2(q < here(0) ? lo(v) : 0.f, q < here(1) ? hi(v) : 0.f); };
       const int slot = sub + SLOTS - SUBS;
       // AHEAD: the upper half of a slot, 16 bytes a lane; the first states are in those of
       // slots 2 and 3
@@ -398,11 +406,13 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
 #pragma unroll
         for (int q = 0; q < S; ++q) {
           e[q] = fma2(g, f2(v[q]), e[q]);
+          if (CAREFUL && !WHOLE) keep_there(q, e[q]), keep_there(q, h[q]), keep_there(q, before[j][q]);
           so = q ? fma2(h[q], f2(v[q]), so) : mul2(h[q], f2(v[q]));
           sd = q ? fma2(e[q], f2(w[q]), sd) : mul2(e[q], f2(w[q]));
           db[q] = fmaf(hi(e[q]), hi(u), lo(e[q]) * lo(u));
           dc[q] = fmaf(hi(h[q]), hi(g), lo(h[q]) * lo(g));
           e[q] = mul2(e[q], ex2_2(mul2(d, A2[q])));
+          if (CAREFUL && !WHOLE) keep_there(q, e[q]);
           const F2 r = mul2(e[q], before[j][q]);
           sl = q ? fma2(r, A2[q], sl) : mul2(r, A2[q]);
           if (!(CAREFUL || GUARD) || t < steps) dA[q] = fma2(r, d, dA[q]);
@@ -456,8 +466,15 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
         copy(h, before[j]);
         step(sub * SUB + j, h);
       }
+      // (rolled up where registers are full, so that the other body is not the one that spills:
+      // N=33 T=512 B=16 H=1024 fp32 833 us, 785 so)
+      if constexpr (CAREFUL && LANES == 16) {
+#pragma unroll 1
+        for (int j = SUB - 1; j >= 0; --j) back(j);
+      } else {
 #pragma unroll
-      for (int j = SUB - 1; j >= 0; --j) back(j);
+        for (int j = SUB - 1; j >= 0; --j) back(j);
+      }
       if (a.part_bc) {
 #pragma unroll
         for (int j = 0; j < SUB; ++j) {
@@ -517,12 +534,15 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
       }
       __syncwarp();  // before the next steps' parts
     };
-    // The last four steps, where the row ends in the midst of them, with care; with more than
-    // 32 states a select at every step is faster than a second body (N=64 T=512 B=16 H=1024 bf16
-    // 972 us, 997), with fewer the body is (N=16 T=300 B=64 H=2048 938 us, 981).
+    // With care: all where an infinity was met, else the last four steps, where the row ends
+    // in the midst of them.  For those, of 64 states a select at every step is faster than a
+    // second body (T=512 B=16 H=1024 bf16 972 us, 997), of fewer the body is (N=16 T=300 B=64
+    // H=2048 938 us, 981).  (The vote has the flag in a register of its own: without
+    // it N=16 T=512 B=16 H=1001 bf16 317 us, 309 so.)
+    const bool careful = !WHOLE && __any_sync(0xffffffffu, met);
     int sub = subs - 1;
 #pragma unroll 1
-    for (const int last = GUARD ? subs : steps / SUB; sub >= last; --sub) back_over(sub, std::true_type());
+    for (const int last = careful ? 0 : GUARD ? subs : steps / SUB; sub >= last; --sub) back_over(sub, std::true_type());
 #pragma unroll 1
     for (; sub >= 0; --sub) back_over(sub, std::false_type());
     __syncthreads();
@@ -600,10 +620,10 @@ __global__ void __launch_bounds__(256) sum_bc_kernel(const float *part, int grou
   static_cast<T *>(to.p)[t * to.st + b * to.sb + m % N] = from_f<T>(s);
 }
 
-template <typename T, int LANES, bool ALIGNED>
+template <typename T, int LANES, bool ALIGNED, bool WHOLE>
 cudaError_t run(Args a, int *err, cudaStream_t s, int *launches) {
   typedef Shape<LANES> Sh;
-  auto fn = scan_bwd_kernel<T, LANES, ALIGNED>;
+  auto fn = scan_bwd_kernel<T, LANES, ALIGNED, WHOLE>;
   static PerDevice<cudaError_t> ready;
   const cudaError_t set = ready.here(
       [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::template shared<T>()); });
@@ -669,9 +689,13 @@ cudaError_t launch_scan_bwd(const ScanBwd &p, DevMem &ws, int *err, int nsm, boo
                     fits(p.dx) && fits(p.ddt) && fits(p.dz);
   cudaError_t e = by_lanes(in.N, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    if (in.dtype == RCU_BF16)
-      return wide ? run<bf16, L, true>(a, err, s, launches) : run<bf16, L, false>(a, err, s, launches);
-    return wide ? run<float, L, true>(a, err, s, launches) : run<float, L, false>(a, err, s, launches);
+    const bool whole = in.N == Shape<L>::NP;
+    auto of_type = [&](auto value) {
+      typedef decltype(value) V;
+      if (whole) return wide ? run<V, L, true, true>(a, err, s, launches) : run<V, L, false, true>(a, err, s, launches);
+      return wide ? run<V, L, true, false>(a, err, s, launches) : run<V, L, false, false>(a, err, s, launches);
+    };
+    return in.dtype == RCU_BF16 ? of_type(bf16()) : of_type(float());
   });
   if (e != cudaSuccess) return e;
   if (sums) {

@@ -1,8 +1,9 @@
 """Infinite values in the selective scan: where the formulas, in 64 bits, give an infinity
 or a finite number, the kernels do too, and NaN only where the formulas have it.
 
-What a thread holds beside a call's own steps (up to a multiple of four) must stay out of
-the sums over them, since 0 times an infinity is NaN.
+What a thread holds beside a call's own steps and states (steps up to a multiple of four,
+states up to one of four or of its kind of kernel) must stay out of the sums over them,
+since 0 times an infinity is NaN.
 
 Inputs are positive, so that no infinity meets its opposite but in the gradient of dt (the
 part through the decays is negative).  Finite values: as in test_gpu_ssm.py, the gradient
@@ -127,3 +128,23 @@ def test_steps_that_are_not_there(ops, path, dtype, T, N):
         v["dh_n"][:] = 0
         _, g = check(ops, v, dtype, torch.tensor([T, T - 2]))
         assert bool(torch.isfinite(g["da_log"]).all())
+
+
+STATES = [1, 2, 4, 5, 8, 11, 12, 16, 18, 24, 32, 33, 40, 64]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", STATES)
+def test_states_that_are_not_there(ops, path, dtype, N):
+    """An infinite x, and an infinite dy, at any number of states."""
+    T, B, H = 45, 2, 8
+    y, _ = check(ops, inputs(T, B, H, N, dtype, [("x", (9, 1, 3))]), dtype)
+    assert not torch.isnan(y).any() and bool(torch.isinf(y[9:, 1, 3]).all())
+    _, g = check(ops, inputs(T, B, H, N, dtype, [("dy", (30, 0, 5))]), dtype)
+    assert bool(torch.isinf(g["dx"][:31, 0, 5]).all()) and not torch.isnan(g["dx"]).any()
+
+
+@pytest.mark.parametrize("N", [4, 30])
+@pytest.mark.parametrize("T", [1, 2, 3, 33, 47])
+def test_steps_and_states_that_are_not_there(ops, path, T, N):
+    test_steps_that_are_not_there(ops, path, "bf16", T, N)
