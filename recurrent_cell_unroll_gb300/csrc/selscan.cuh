@@ -161,16 +161,22 @@ struct Weights {
       }
     }
   }
-  __device__ __forceinline__ void put(float (*out)[NP]) const {
+  // NaN where one of them is not finite, else 0.
+  __device__ __forceinline__ float put(float (*out)[NP]) const {
+    float probe = 0.f;
 #pragma unroll
     for (int k = 0; k < EV; ++k) {
       if (TILE % PASS && k * PASS + row >= TILE) break;
       float w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = k * PASS < rows && j < left ? to_f(v[k].v[j]) : 0.f;
+      for (int j = 0; j < 4; ++j) {
+        w[j] = k * PASS < rows && j < left ? to_f(v[k].v[j]) : 0.f;
+        probe = fmaf(w[j], 0.f, probe);
+      }
       *reinterpret_cast<float4 *>(&out[k * PASS + row][threadIdx.x % ROW * 4]) =
           make_float4(w[0], w[1], w[2], w[3]);
     }
+    return probe;
   }
 };
 

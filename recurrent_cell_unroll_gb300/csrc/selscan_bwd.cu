@@ -132,7 +132,7 @@ __device__ __forceinline__ void prefetch(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
-// WHOLE: the lanes' states are all a channel's.  Blocks of eight warps an SM in all; left to
+// WHOLE: the lanes' states and channels are all there.  Blocks of eight warps an SM in all; left to
 // itself the compiler takes 168 registers for N=32 and up and spills (N=32 503 us, 445 so).
 template <typename T, int LANES, bool ALIGNED, bool WHOLE>
 __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan_bwd_kernel(const Args a, int *err) {
@@ -301,13 +301,12 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, 256 / Shape<LANES>::NT) scan
         if (!WHOLE) probe = fma2(g.b, f2(0.f), fma2(g.a, f2(0.f), probe));
       }
     }
-    rb.put(s_b);
-    rc.put(s_c);
-    // States that do not exist have weights of 0, and stay 0 (their gradients too) but for
-    // infinite inputs.
+    const float probe_bc = rb.put(s_b) + rc.put(s_c);
+    // States and channels that do not exist have weights or inputs of 0, and stay 0 (their
+    // gradients too) but for infinite inputs of those that do.
     int met = 0;
     if (WHOLE) __syncthreads();
-    else met = __syncthreads_or(isnan(lo(probe)) || isnan(hi(probe)));
+    else met = __syncthreads_or(isnan(lo(probe)) || isnan(hi(probe)) || isnan(probe_bc));
     if (k > 0) {  // the tile before, into the second-level cache
       constexpr int LINE = 128 / sizeof(T);  // values
       for (int i = tid; i < TILE * ((CC + LINE - 1) / LINE); i += NT) {
@@ -689,7 +688,7 @@ cudaError_t launch_scan_bwd(const ScanBwd &p, DevMem &ws, int *err, int nsm, boo
                     fits(p.dx) && fits(p.ddt) && fits(p.dz);
   cudaError_t e = by_lanes(in.N, [&](auto lanes) {
     constexpr int L = decltype(lanes)::value;
-    const bool whole = in.N == Shape<L>::NP;
+    const bool whole = in.N == Shape<L>::NP && in.H % Shape<L>::CC == 0;
     auto of_type = [&](auto value) {
       typedef decltype(value) V;
       if (whole) return wide ? run<V, L, true, true>(a, err, s, launches) : run<V, L, false, true>(a, err, s, launches);

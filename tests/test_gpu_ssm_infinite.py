@@ -1,9 +1,9 @@
 """Infinite values in the selective scan: where the formulas, in 64 bits, give an infinity
 or a finite number, the kernels do too, and NaN only where the formulas have it.
 
-What a thread holds beside a call's own steps and states (steps up to a multiple of four,
-states up to one of four or of its kind of kernel) must stay out of the sums over them,
-since 0 times an infinity is NaN.
+What a thread holds beside a call's own steps, states and channels (steps up to a multiple
+of four, states up to one of four or of its kind of kernel, channels up to a block's) must
+stay out of the sums over them, since 0 times an infinity is NaN.
 
 Inputs are positive, so that no infinity meets its opposite but in the gradient of dt (the
 part through the decays is negative).  Finite values: as in test_gpu_ssm.py, the gradient
@@ -148,3 +148,16 @@ def test_states_that_are_not_there(ops, path, dtype, N):
 @pytest.mark.parametrize("T", [1, 2, 3, 33, 47])
 def test_steps_and_states_that_are_not_there(ops, path, T, N):
     test_steps_that_are_not_there(ops, path, "bf16", T, N)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [1, 3, 4, 20, 63, 68])
+@pytest.mark.parametrize("N", [4, 16, 32, 64])
+def test_channels_that_are_not_there(ops, path, dtype, H, N):
+    """An infinite b or c, whose gradients are sums over channels."""
+    T, B = 45, 2
+    n = N // 2
+    _, g = check(ops, inputs(T, B, H, N, dtype, [("c", (30, 1, n))]), dtype)
+    assert bool(torch.isinf(g["db"][:31, 1, n]).all()) and not torch.isnan(g["db"]).any()
+    _, g = check(ops, inputs(T, B, H, N, dtype, [("b", (9, 0, n))]), dtype)
+    assert bool(torch.isinf(g["dc"][9:, 0, n]).all()) and not torch.isnan(g["dc"]).any()
