@@ -328,7 +328,11 @@ __global__ void __launch_bounds__(128) chain_kernel(const float *a_log, const fl
     for (int k = 0; k < READ; ++k) {
       if (k0 + k >= m.seg.n) break;
       m.end[(BACKWARDS ? m.seg.n - 1 - k0 - k : k0 + k) * table + i] = h;
-      if (k0 + k < m.seg.n - 1) h = fmaf(ex2(A2 * sum[k]), h, own[k]);  // nothing follows the last
+      if (k0 + k == m.seg.n - 1) break;  // nothing follows the last
+      float decay = A2 * sum[k];
+      // an infinite state is kept infinite by decays above 0, though their product be 0 in fp32
+      if (isinf(h) && !isinf(decay)) decay = fmaxf(decay, -100.f);
+      h = fmaf(ex2(decay), h, own[k]);
     }
   }
 }

@@ -161,3 +161,14 @@ def test_channels_that_are_not_there(ops, path, dtype, H, N):
     assert bool(torch.isinf(g["db"][:31, 1, n]).all()) and not torch.isnan(g["db"]).any()
     _, g = check(ops, inputs(T, B, H, N, dtype, [("b", (9, 0, n))]), dtype)
     assert bool(torch.isinf(g["dc"][9:, 0, n]).all()) and not torch.isnan(g["dc"]).any()
+
+
+@pytest.mark.parametrize("T", [40, 700])
+def test_an_infinite_state_outlasts_a_segment(ops, T):
+    """States that decay far below fp32's range within a segment, and are infinite: kept
+    infinite by every step's decay, so by the segment's too.  And their gradients."""
+    v = inputs(T, 1, 8, 4, "f32", [("h0", (0, 3, 1))], slow=4.0)
+    y, _ = check(ops, v, "f32")
+    assert bool(torch.isinf(y[:, 0, 3]).all())
+    _, g = check(ops, inputs(T, 1, 8, 4, "f32", [("dh_n", (0, 6, 2))], slow=4.0), "f32")
+    assert bool(torch.isinf(g["dx"][:, 0, 6]).all()) and bool(torch.isinf(g["dh0"][0, 6, 2]))
