@@ -84,8 +84,9 @@ __global__ void __launch_bounds__(Shape<LANES>::NT, LANES == 4 ? 7 : 1) scan_ker
   const F fx(static_cast<const T *>(sx.p) + b * sx.sb, sx.st, ch0, p.H);
   const bool use_z = p.z.p && MODE != ENDS;
   const F fz(static_cast<const T *>(p.z.p) + (use_z ? b * p.z.sb : 0), p.z.st, ch0, p.H);
-  Weights<T, NT, TILE, NP> r1(static_cast<const T *>(sw.p) + b * sw.sb, sw.st, p.N, a.wide_bc);
-  Weights<T, NT, TILE, NP> r2(static_cast<const T *>(p.c.p) + b * p.c.sb, p.c.st, p.N, a.wide_bc);
+  const bool words = sizeof(T) == 4 && a.wide_bc;
+  Weights<T, NT, TILE, NP> r1(static_cast<const T *>(sw.p) + b * sw.sb, sw.st, p.N, words);
+  Weights<T, NT, TILE, NP> r2(static_cast<const T *>(p.c.p) + b * p.c.sb, p.c.st, p.N, words);
   T *y = MODE == MAIN ? static_cast<T *>(a.y.p) + b * a.y.sb : nullptr;
 
   const int tiles = t0 < end ? ceil_div(end - t0, TILE) : 0;
@@ -382,6 +383,10 @@ cudaError_t dispatch(Args a, bool vec, int *err, cudaStream_t s, int *launches) 
   const bool wide = vec && p.H % n == 0 && aligned(p.x, size, n) && aligned(p.dt, size, n) &&
                     (!p.z.p || aligned(p.z, size, n)) && (MODE != GRADS || aligned(a.dy, size, n)) &&
                     (MODE != MAIN || aligned(a.y, size, n));
+  // fp32 by words (T=512 N=16 H=1024: B=16 107 -> 103 us, B=64 232 -> 226); bf16 value by value,
+  // with no other way in its kernels (T=300 B=64 H=2048 204 us, by words 226)
+  a.wide_bc = vec && p.dtype == RCU_F32 && p.N % 4 == 0 && aligned(MODE == GRADS ? p.c : p.b, 4, 4) &&
+              (MODE != MAIN || aligned(p.c, 4, 4));
   return p.dtype == RCU_BF16 ? of_type<bf16, MODE>(a, wide, err, s, launches)
                              : of_type<float, MODE>(a, wide, err, s, launches);
 }
