@@ -1240,8 +1240,9 @@ class SeqOps:
         _check(self.lib.rcu_adamw_step(
             self.h, count, table, 0.0 if on_dev[2] else lr, betas[0], betas[1], eps,
             weight_decay, 1 if on_dev[1] else step, seed & 0xffffffff, *on_dev, self._raw_stream()))
-        # autograd is told of the change: a graph that has saved a parameter refuses to go on
-        _tensors().changed(params, grads)
+        # autograd is told of the change: a graph that has saved a parameter, or its copy,
+        # refuses to go on
+        _tensors().changed(params, grads, copies)
 
     def state8_pack(self, x, signed, stream=None):
         """(codes like x, exponents [ceil(n / 64)]) of an 8-bit optimizer state:

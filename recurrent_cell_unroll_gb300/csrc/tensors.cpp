@@ -104,16 +104,22 @@ PyObject *adamw_rows(PyObject *, PyObject *args) {
   return result;
 }
 
-// changed(params, grads): tells autograd of parameters that have been changed in place.
+// changed(params, grads, copies): tells autograd of parameters and their copies (a list, or
+// None) that have been changed in place: those that have a gradient.
 PyObject *changed(PyObject *, PyObject *args) {
-  PyObject *p, *g;
-  if (!PyArg_ParseTuple(args, "OO", &p, &g)) return nullptr;
+  PyObject *p, *g, *copies;
+  if (!PyArg_ParseTuple(args, "OOO", &p, &g, &copies)) return nullptr;
   try {
-    const List ps(p), gs(g);
-    if (!ps.o || !gs.o) return nullptr;
+    const List ps(p), gs(g), cs(copies == Py_None ? p : copies);
+    if (!ps.o || !gs.o || !cs.o) return nullptr;
+    auto tell = [](PyObject *o) {
+      const at::Tensor *t = tensor_of(o);
+      if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+    };
     for (Py_ssize_t k = 0; k < ps.size() && k < gs.size(); ++k) {
-      const at::Tensor *t = tensor_of(ps[k]);
-      if (t && gs[k] != Py_None && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+      if (gs[k] == Py_None) continue;
+      tell(ps[k]);
+      if (copies != Py_None && k < cs.size()) tell(cs[k]);
     }
   } catch (const std::exception &e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());

@@ -1,0 +1,21 @@
+"""Graphs that have saved what the AdamW step changes in place."""
+import pytest
+import torch
+
+from recurrent_cell_unroll_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+
+def test_a_graph_that_saved_a_copy_refuses_to_go_on():
+    ops = binding.SeqOps()
+    p = torch.randn(8, 8, device="cuda")
+    copy = p.bfloat16()
+    x = torch.randn(8, 8, device="cuda").bfloat16().requires_grad_()
+    loss = (x @ copy).sum()
+    zeros = [torch.zeros_like(p) for _ in range(2)]
+    ops.adamw_step([p], [torch.ones_like(p)], zeros[:1], zeros[1:], 1, copies=[copy])
+    assert torch.equal(copy, p.bfloat16()) and ops.status() == 0
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    ops.close()

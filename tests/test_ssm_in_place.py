@@ -1,0 +1,40 @@
+"""What the AdamW step and the single steps change in place, autograd is told of: a graph
+that has saved such a tensor refuses to go on (no GPU needed)."""
+import pytest
+import torch
+
+from recurrent_cell_unroll_gb300 import binding
+
+
+def saved_by(weight):
+    """The loss of a graph that has saved `weight`."""
+    return (torch.ones(2, 4, requires_grad=True) @ weight).sum()
+
+
+def test_parameters_and_their_copies():
+    p, c = (torch.randn(4, 3) for _ in range(2))
+    losses = [saved_by(p), saved_by(c)]
+    binding._tensors().changed([p], [torch.ones(4, 3)], [c])
+    for loss in losses:
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+
+
+def test_tensors_that_a_step_leaves_out_have_not_changed():
+    p, c, q = (torch.randn(4, 3) for _ in range(3))
+    losses = [saved_by(p), saved_by(c), saved_by(q)]
+    binding._tensors().changed([p, q], [None, torch.ones(4, 3)], [c, None])
+    losses[0].backward()
+    losses[1].backward()
+    with pytest.raises(RuntimeError, match="inplace"):
+        losses[2].backward()
+    binding._tensors().changed([p], [torch.ones(4, 3)], None)
+    with torch.inference_mode():
+        t = torch.zeros(3)
+    binding._tensors().changed([t], [t], [t])
+
+
+def test_lists_only():
+    for args in ((1, [], None), ([], 1, None), ([], [], 1)):
+        with pytest.raises(TypeError):
+            binding._tensors().changed(*args)
