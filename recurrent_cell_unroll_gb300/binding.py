@@ -22,6 +22,7 @@ import threading
 from typing import Optional
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _build
 
@@ -927,6 +928,7 @@ class SeqOps:
         y = torch.empty(shape, dtype=dtype, device=x.device)
         _check(self.lib.rcu_linrec_step(self.h, dt, B, H, xp, xl, rp, rl, ip, il, lp, c, sp, slots,
                                         tp, y.data_ptr(), H, self._raw_stream()))
+        increment_version(state)  # a graph that has saved the table refuses to go on
         return y
 
     # ---- layer norm
@@ -1095,6 +1097,7 @@ class SeqOps:
         # (a table of W - 1 = 0 rows has no address)
         _check(self.lib.rcu_conv_step(self.h, dt, B, H, W, xp, xl, wp, bp, 1 if silu else 0,
                                       sp or wp, slots, tp, y.data_ptr(), H, self._raw_stream()))
+        increment_version(state)  # a graph that has saved the table refuses to go on
         return y
 
     def _taps(self, weight, rows, H):
@@ -1199,6 +1202,7 @@ class SeqOps:
         y = torch.empty(shape, dtype=dtype, device=x.device)
         _check(self.lib.rcu_selscan_step(self.h, ty, B, H, N, *args[:-1], sp, slots, tp,
                                          y.data_ptr(), H, self._raw_stream()))
+        increment_version(state)
         return y
 
     # ---- AdamW
