@@ -22,6 +22,8 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
         self.params = list(params)
+        if len({id(p) for p in self.params}) < len(self.params):
+            raise ValueError("a parameter is given twice: a step would update it in two places at once")
         self.lr, self.betas, self.eps, self.weight_decay = lr, tuple(betas), eps, weight_decay
         self.seed, self.steps = seed, 0
         self.ops = binding.SeqOps() if ops is None else ops
