@@ -2,8 +2,9 @@
 
 Each .cu file is compiled to an object in parallel, then linked into
 ``recurrent_cell_unroll_gb300/_lib/librcu.so`` with the static CUDA runtime.
-``tensors.so``, the part of the Python binding that reads lists of torch tensors
-(csrc/tensors.cpp, for this Python and torch), is compiled beside it with g++.
+``tensors.*.so``, the part of the Python binding that reads lists of torch tensors
+(csrc/tensors.cpp), is compiled beside it with g++; it is for one Python and one torch,
+whose versions its name has.
 Objects are rebuilt only when a source or header is newer.  ``build(debug=True)``
 makes ``librcu_debug.so`` instead: the same sources with -DRCU_DEBUG, whose
 kernels check their global-memory indices and record a failed check in the
@@ -16,6 +17,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,7 +27,6 @@ LIBDIR = os.path.join(PKG, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIB = os.path.join(LIBDIR, "librcu.so")
 LIB_DEBUG = os.path.join(LIBDIR, "librcu_debug.so")
-TENSORS = os.path.join(LIBDIR, "tensors.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -42,9 +43,13 @@ def _flags():
             "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
 
 
-def _tensors_command(out: str) -> list:
-    import sysconfig
+def tensors_path() -> str:
+    """The native part of the binding for this Python and this torch."""
+    import torch
+    return os.path.join(LIBDIR, f"tensors.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 
+
+def _tensors_command(out: str) -> list:
     import torch
     at = os.path.dirname(torch.__file__)
     inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
@@ -83,10 +88,11 @@ def build(verbose: bool = False, jobs: int = 0, debug: bool = False) -> str:
             print(r.stdout, r.stderr)
         return r
 
-    tensors_tmp = TENSORS + f".tmp{os.getpid()}"
+    tensors_so = tensors_path()
+    tensors_tmp = tensors_so + f".tmp{os.getpid()}"
     tensors_src = max(os.path.getmtime(os.path.join(CSRC, "tensors.cpp")),
                       os.path.getmtime(os.path.join(INCLUDE, "rcu.h")))
-    tensors = not os.path.exists(TENSORS) or os.path.getmtime(TENSORS) < tensors_src
+    tensors = not os.path.exists(tensors_so) or os.path.getmtime(tensors_so) < tensors_src
     kernels = bool(cmds)
     if tensors:
         cmds.insert(0, _tensors_command(tensors_tmp))
@@ -95,7 +101,7 @@ def build(verbose: bool = False, jobs: int = 0, debug: bool = False) -> str:
         with cf.ThreadPoolExecutor(max_workers=jobs or min(len(cmds), os.cpu_count() or 4)) as ex:
             list(ex.map(run, cmds))
     if tensors:
-        os.replace(tensors_tmp, TENSORS)
+        os.replace(tensors_tmp, tensors_so)
     if kernels or not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs):
         tmp = lib + f".tmp{os.getpid()}"
         run([nvcc(), ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-lrt", "-ldl",

@@ -179,11 +179,12 @@ def _tensors():
     """The native part that reads lists of tensors (raises if it has not been built)."""
     global _tensors_module
     if _tensors_module is None:
-        if not os.path.exists(_build.TENSORS):
-            raise RuntimeError(f"{_build.TENSORS} not found: build it with "
+        path = _build.tensors_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} not found: build it with "
                                "recurrent_cell_unroll_gb300._build.build()")
-        loader = importlib.machinery.ExtensionFileLoader("tensors", _build.TENSORS)
-        spec = importlib.util.spec_from_file_location("tensors", _build.TENSORS, loader=loader)
+        loader = importlib.machinery.ExtensionFileLoader("tensors", path)
+        spec = importlib.util.spec_from_file_location("tensors", path, loader=loader)
         module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         _tensors_module = module
