@@ -59,6 +59,23 @@ def _tensors_command(out: str) -> list:
             "-L", os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
+def _run(cmd, verbose):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    if verbose and (r.stdout or r.stderr):
+        print(r.stdout, r.stderr)
+
+
+def _build_tensors(verbose):
+    to = tensors_path()
+    newest = max(os.path.getmtime(f) for f in (os.path.join(CSRC, "tensors.cpp"), os.path.join(INCLUDE, "rcu.h")))
+    if not os.path.exists(to) or os.path.getmtime(to) < newest:
+        tmp = to + f".tmp{os.getpid()}"
+        _run(_tensors_command(tmp), verbose)
+        os.replace(tmp, to)
+
+
 def _newest_header():
     hs = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
@@ -80,33 +97,18 @@ def build(verbose: bool = False, jobs: int = 0, debug: bool = False) -> str:
             continue
         cmds.append([nvcc(), *_flags(), *(["-DRCU_DEBUG"] if debug else []), "-c", s, "-o", o])
 
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout, r.stderr)
-        return r
-
-    tensors_so = tensors_path()
-    tensors_tmp = tensors_so + f".tmp{os.getpid()}"
-    tensors_src = max(os.path.getmtime(os.path.join(CSRC, "tensors.cpp")),
-                      os.path.getmtime(os.path.join(INCLUDE, "rcu.h")))
-    tensors = not os.path.exists(tensors_so) or os.path.getmtime(tensors_so) < tensors_src
-    kernels = bool(cmds)
-    if tensors:
-        cmds.insert(0, _tensors_command(tensors_tmp))
-
-    if cmds:
-        with cf.ThreadPoolExecutor(max_workers=jobs or min(len(cmds), os.cpu_count() or 4)) as ex:
-            list(ex.map(run, cmds))
-    if tensors:
-        os.replace(tensors_tmp, tensors_so)
-    if kernels or not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs):
+    with cf.ThreadPoolExecutor(max_workers=jobs or min(len(cmds) + 1, os.cpu_count() or 4)) as ex:
+        tensors = ex.submit(_build_tensors, verbose)
+        list(ex.map(lambda cmd: _run(cmd, verbose), cmds))
+    if cmds or not os.path.exists(lib) or os.path.getmtime(lib) < max(os.path.getmtime(o) for o in objs):
         tmp = lib + f".tmp{os.getpid()}"
-        run([nvcc(), ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-lrt", "-ldl",
-             "-lpthread"])
+        _run([nvcc(), ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static", "-lrt", "-ldl",
+              "-lpthread"], verbose)
         os.replace(tmp, lib)
+    try:
+        tensors.result()
+    except Exception as e:  # the C library is there without it
+        raise RuntimeError(f"{lib} is built, the Python binding's native part is not: {e}") from e
     return lib
 
 

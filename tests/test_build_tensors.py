@@ -38,3 +38,15 @@ def test_it_is_built_for_each_torch(monkeypatch):
     finally:
         if os.path.exists(path):
             os.remove(path)
+
+
+@pytest.mark.parametrize("command", [["false"], ["no-such-compiler"]])
+def test_without_it_the_library_is_built(monkeypatch, tmp_path, command):
+    _build.build()
+    lib = tmp_path / "librcu.so"
+    monkeypatch.setattr(_build, "LIB", str(lib))
+    monkeypatch.setattr(_build, "tensors_path", lambda: str(tmp_path / "tensors.so"))
+    monkeypatch.setattr(_build, "_tensors_command", lambda out: command)
+    with pytest.raises(RuntimeError, match="native part"):
+        _build.build()
+    assert lib.exists()
