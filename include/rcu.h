@@ -794,11 +794,14 @@ RCU_API int rcu_conv_step(rcu_seq *h, int dtype, int B, int H, int W, const void
  *   states   [ceil(T / RCU_SELSCAN_CHUNK), B, H, N] fp32 or NULL: the states
  *            before steps 0, 32, 64, ..., which rcu_selscan_backward needs (of
  *            a chunk past a row's end: its last states).
- * T or B may be 0.  Long sequences of few channels are split over time; results
- * do not depend on anything but the inputs.  States and sums are fp32; an
+ * T or B may be 0.  Long sequences of few channels are split over time, by a rule
+ * on T, B, H, N and the number of SMs.  So results are the same from call to call
+ * for the same sizes on the same kind of device, while a row in another batch may
+ * be split elsewhere and rounded otherwise.  States and sums are fp32; an
  * exponential of base 2 is the hardware's (2 units in the last place).
  * An infinite x (or b) makes its channel's states infinite, and NaN where a
- * product with 0 meets them.
+ * product with 0 meets them; states and channels that are not infinite are as they
+ * would be without it.
  */
 RCU_API int rcu_selscan_forward(rcu_seq *h, int dtype, int layout, int T, int B, int H, int N,
                                 const void *x, int64_t ldx, const void *dt, int64_t lddt,
