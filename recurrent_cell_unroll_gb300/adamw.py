@@ -37,10 +37,17 @@ class AdamW:
     @torch.no_grad()
     def step(self, lr=None, scale=None, stream=None):
         """One step; lr in the place of the optimizer's; scale: a float32 on the
-        device that gradients are multiplied by (clipping, loss scaling)."""
+        device that gradients are multiplied by (clipping, loss scaling).  Not to be
+        captured into a graph: its number is counted here, so each replay would be the
+        same step (SeqOps.adamw_step can read it from the device)."""
+        if stream is not None:
+            return self.ops._on_stream(stream, self.step, lr, scale)
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("AdamW.step counts its steps on the host and cannot be captured; call "
+                               "SeqOps.adamw_step with step (and lr) as tensors on the device")
         self.ops.adamw_step(self.params, [p.grad for p in self.params], self.m, self.v, self.steps + 1,
                             lr=self.lr if lr is None else lr, betas=self.betas, eps=self.eps,
-                            weight_decay=self.weight_decay, scale=scale, seed=self.seed, stream=stream)
+                            weight_decay=self.weight_decay, scale=scale, seed=self.seed)
         self.steps += 1
 
     def zero_grad(self):

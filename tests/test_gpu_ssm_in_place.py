@@ -1,8 +1,8 @@
-"""Graphs that have saved what the AdamW step changes in place."""
+"""Graphs that have saved what the AdamW step changes in place, and graphs of the step itself."""
 import pytest
 import torch
 
-from recurrent_cell_unroll_gb300 import binding
+from recurrent_cell_unroll_gb300 import adamw, binding
 
 pytestmark = pytest.mark.gpu
 
@@ -19,3 +19,23 @@ def test_a_graph_that_saved_a_copy_refuses_to_go_on():
     with pytest.raises(RuntimeError, match="inplace"):
         loss.backward()
     ops.close()
+
+
+def test_the_optimizer_object_is_not_captured():
+    p = torch.randn(64, device="cuda", requires_grad=True)
+    p.grad = torch.ones_like(p)
+    opt = adamw.AdamW([p])
+    opt.step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    opt.step(stream=side)
+    torch.cuda.synchronize()
+    before = p.detach().clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = before * 2
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(kept, before * 2) and torch.equal(p.detach(), before) and opt.steps == 2
