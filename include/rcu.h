@@ -745,8 +745,8 @@ RCU_API int rcu_act8_unpack(rcu_seq *h, int dtype, int64_t rows, int n, const in
  *   state_n  [B, W - 1, H] of type dtype or NULL: the last W - 1 inputs of each
  *            row, those of `state` among them where the row is shorter.  May be
  *            `state` itself.
- * T or B may be 0.  Sums are fp32.  Of these operators and the scans, B * H and T * B are at most 2^29;
- * more is RCU_ERR_UNSUPPORTED.
+ * T or B may be 0.  Sums are fp32.  Of these operators and the scans, B * H and
+ * T * B are at most 2^29; more is RCU_ERR_UNSUPPORTED.
  */
 RCU_API int rcu_conv_forward(rcu_seq *h, int dtype, int layout, int T, int B, int H, int W,
                              const void *x, int64_t ldx, const float *weight, const float *bias,
@@ -815,7 +815,11 @@ RCU_API int rcu_selscan_forward(rcu_seq *h, int dtype, int layout, int T, int B,
  *   dy [T, B, H] of type dtype; dh_n [B, H, N] fp32 or NULL (0).
  *   dx, ddt, dz [T, B, H], db, dc [T, B, N] of type dtype, each may be NULL; 0
  *   past a row's end (dz only with a z).  da_log [H, N], dd (only with a d),
- *   ddt_bias [H], dh0 [B, H, N] fp32, each may be NULL.  Sums over steps, rows and channels are fp32 in a fixed order.
+ *   ddt_bias [H], dh0 [B, H, N] fp32, each may be NULL.  Sums over steps, rows and
+ *   channels are fp32 in a fixed order.
+ * For db and dc the workspace holds 8 T B N ceil(H / C) bytes, C = 64 channels for
+ * N <= 16, 32 for N <= 32, 16 above (8.6 GB at T B = 131072, H = 2048, N = 64); the
+ * handle keeps it.
  */
 RCU_API int rcu_selscan_backward(rcu_seq *h, int dtype, int layout, int T, int B, int H, int N,
                                  const void *x, int64_t ldx, const void *dt, int64_t lddt,
@@ -872,9 +876,9 @@ typedef struct rcu_adamw_tensor {
  *       - m / (sqrt(v) / sqrt(1 - beta2^step) + eps) * (lr / (1 - beta1^step))
  * The new p is rounded to the nearest of its type.  p, m and v are updated in place.
  *   scale     NULL (1) or a device fp32 number, of gradient clipping or loss scaling.
- *   step      >= 1, or, with step_dev, a device int32 that is read instead; lr_dev:
- *             a device fp32 number that is read in lr's place (NULL: lr).  With these
- *             a captured step follows both.
+ *   step      >= 1, or, with step_dev, a device int32 (>= 1, which is not checked) that
+ *             is read instead; lr_dev: a device fp32 number that is read in lr's place
+ *             (NULL: lr).  With these a captured step follows both.
  *   seed      its low 32 bits: of the rounding of 8-bit states.
  *   0 <= beta1, beta2 < 1; eps >= 0.
  *
@@ -889,8 +893,10 @@ typedef struct rcu_adamw_tensor {
  * step are kept on average: 16 bits behind the cut are compared with those of
  *   mix(mix(mix(seed + 0x9e3779b9 step) + tensor's place in the list) ^ index),
  * the low half of the word for m, the high half for v, where mix is x ^= x >> 16,
- * x *= 0x7feb352d, x ^= x >> 15, x *= 0x846ca68b, x ^= x >> 16 on 32 bits.  A tensor
- * has at most 2^32 values with 8-bit states and 2^40 else; `count` is at most 2^24.
+ * x *= 0x7feb352d, x ^= x >> 15, x *= 0x846ca68b, x ^= x >> 16 on 32 bits (shifts and
+ * constants as published by C. Wellons, "Prospecting for Hash Functions", 2018).  A
+ * tensor has at most 2^32 values with 8-bit states and 2^40 else; `count` is at most
+ * 2^24.
  */
 RCU_API int rcu_adamw_step(rcu_seq *h, int64_t count, const rcu_adamw_tensor *tensors, double lr,
                            double beta1, double beta2, double eps, double weight_decay,

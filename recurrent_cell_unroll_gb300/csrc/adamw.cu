@@ -59,6 +59,7 @@ struct Given {
   int piece;  // values of a block
 };
 
+// a published 32-bit mixing function (include/rcu.h)
 __host__ __device__ inline uint32_t mix(uint32_t x) {
   x ^= x >> 16;
   x *= 0x7feb352du;

@@ -12,10 +12,11 @@
 // thread's own in shared memory (in registers they cost half of the threads: backward
 // bf16 T=8192 B=4 H=2048 173 us, 107 so), and channels are worked on as packed pairs.
 //
-// Measured, W=4: forward bf16 T=512 B=256 H=1024 118 us (4560 GB/s), backward bf16
-// T=8192 B=4 H=2048 107 us (3770 GB/s), fp32 mixed lengths T=500 B=64 H=512 44 us: half
-// of the copy's rate, at 12 warps an SM with 160 registers (four blocks in the place of
-// three spill: 137 and 140 us) and 17 (forward) and 33 instructions a value.
+// Measured, W=4: forward bf16 T=512 B=256 H=1024 117 us (4590 GB/s, 68 % of the copy's
+// rate), backward bf16 T=8192 B=4 H=2048 107 us (3770 GB/s, 56 %), fp32 mixed lengths
+// T=500 B=64 H=512 44 us (46 %).  Neither the memory nor the issue of instructions is
+// full (2.1 a cycle; 17 a value forward, 33 backward): 12 warps an SM with 160 registers
+// do not hide what they wait for (four blocks in the place of three spill: 137 and 140 us).
 #include <type_traits>
 
 #include "per_device.h"

@@ -273,9 +273,19 @@ struct Segments {
 // Segments of a sequence whose kernel takes `blocks` blocks a segment: some `per_sm`
 // blocks an SM, of two chunks or more.  A split costs the first kernel, 0.6 of the
 // main one's work on all segments but one, and two launches, so there is one only
-// where an SM would have two blocks or fewer, of eight chunks or more (forward bf16
-// N=16: T=2048 B=8 H=2048, 256 blocks, 357 -> 303 us; T=300 B=32 H=1024, 512 blocks,
-// 77 us, 98 with one; T=512 B=4 H=1024 92 -> 40; T=100 B=4 H=1024 25, 31 with one).
+// where an SM would have two blocks or fewer, of eight chunks or more.
+//
+// Measured, bf16, us, one segment -> split by this rule:
+//   forward, H=1024 T=512: B=4 N=8 114 -> 36, N=16 80 -> 37, N=64 92 -> 95; B=8 N=16 80 -> 52;
+//     B=16 N=4 122 -> 74, N=8 115 -> 74, N=16 82 -> 87, N=32 99 -> 140, N=64 179 -> 292;
+//     T=2048 B=4 N=16 300 -> 91; H=2048 T=2048 B=8 N=8 440 -> 243, N=16 310 -> 288
+//   where the rule has none and two segments are forced: T=300 B=32 N=16 70, 97; T=512 B=24 111, 126
+//   backward, H=1024 T=512: B=4 N=8 233 -> 66, N=16 168 -> 86, N=64 264 -> 297; B=8 N=16 182 -> 152;
+//     B=16 N=4 287 -> 224, N=8 285 -> 227, N=16 238 -> 277, N=32 and 64 no split (436, 969);
+//     T=2048 B=4 N=16 712 -> 284; H=2048 T=2048 B=8 N=8 1093 -> 819, N=16 898 -> 1014
+// So it is right for the few warps a block of N <= 8 up to its limit, and at N=16 up to some
+// 130 blocks (forward, of long sequences, to 256); from there on, and with the more warps a
+// block of more states, a split loses: the rule counts blocks, not warps.
 inline Segments segments_of(int T, int64_t blocks, int nsm, int per_sm) {
   const int chunks = ceil_div(T, CHUNK);
   int n = 1;

@@ -19,13 +19,13 @@
 // that compute the outputs, as words of two channels.
 //
 // Two channels a thread and not four, though those read less of shared memory: 8 warps
-// an SM in the place of 6 (bf16, N=16, T=2048 B=8 H=2048 1190 -> 802 us).  Three blocks
+// an SM in the place of 6 (bf16, N=16, T=2048 B=8 H=1024 1190 -> 802 us, 544 now).  Three blocks
 // an SM, at 168 registers, were no faster (the decays kept 1015 us, computed again 928,
 // two blocks 755).
 //
-// Measured, N=16: bf16 T=8192 B=2 H=1024 (19 segments) 483 us, of which 100 for their ends
-// and 32 for chaining and sums; fp32 T=500 B=32 H=512, mixed lengths, 203.  Bf16 T=512 B=16
-// H=1024: N=8 228, 16 282, 32 437, 64 979.  Issue bound: 27 instructions a state and step
+// Measured, N=16: bf16 T=8192 B=2 H=1024 (19 segments) 480 us, of which 100 for their ends
+// and 32 for chaining and sums; fp32 T=500 B=32 H=512, mixed lengths, 194.  Bf16 T=512 B=16
+// H=1024: N=8 227, 16 277, 32 436, 64 969.  Issue bound: 27 instructions a state and step
 // at 2.0 a cycle.
 #include "selscan.cuh"
 

@@ -30,10 +30,10 @@ struct Args {
 // 217 with four).  Tiles are of half a chunk: seven blocks then fit an SM, three with
 // whole ones (201 and 286 us).
 //
-// Measured, bf16, N=16: T=300 B=64 H=2048 201 us, 3.1e12 states a second, where the
+// Measured, bf16, N=16: T=300 B=64 H=2048 203 us, 3.1e12 states a second, where the
 // special function unit would take 83 and the issue of 118 instructions a channel and
-// step 120; T=2048 B=8 H=2048 293 us, in four segments (115 of them for their ends);
-// T=65536 B=1 H=512 302.
+// step 120; T=2048 B=8 H=2048 285 us, in four segments (some 110 of them for their ends);
+// T=65536 B=1 H=512 297.
 constexpr int S = 4, K = 4, P = K / 2, TILE = CHUNK / 2;
 template <int LANES>
 struct Shape {
@@ -370,7 +370,7 @@ template <typename T, Mode MODE>
 cudaError_t of_type(const Args &a, bool aligned, int *err, cudaStream_t s, int *launches) {
   const int N = a.in.N;
   // of four states or fewer, half of the lanes' are idle: a kernel for those alone was no
-  // faster (N=4 T=512 H=1024: bf16 B=16 82 us, 77 so, B=64 197 and 155)
+  // faster (N=4 T=512 H=1024: bf16 B=16 82 us, 74 so, B=64 197 and 155)
   if (N <= 8) return of_lanes<T, MODE, 2>(a, aligned, err, s, launches);
   if (N <= 16) return of_lanes<T, MODE, 4>(a, aligned, err, s, launches);
   if (N <= 32) return of_lanes<T, MODE, 8>(a, aligned, err, s, launches);
