@@ -172,3 +172,16 @@ def test_an_infinite_state_outlasts_a_segment(ops, T):
     assert bool(torch.isinf(y[:, 0, 3]).all())
     _, g = check(ops, inputs(T, 1, 8, 4, "f32", [("dh_n", (0, 6, 2))], slow=4.0), "f32")
     assert bool(torch.isinf(g["dx"][:, 0, 6]).all()) and bool(torch.isinf(g["dh0"][0, 6, 2]))
+
+
+@pytest.mark.parametrize("N", STATES)
+def test_an_infinite_step_size(ops, path, N):
+    """It forgets every state that exists, and makes it infinite."""
+    v = inputs(45, 2, 8, N, "f32", [("dt", (9, 1, 3))])
+    y, h, *_ = formula(v)
+    on = {k: t.float().cuda() for k, t in v.items()}
+    got = ops.selscan_forward(*(on[k] for k in ("x", "dt", "a_log", "b", "c")), h0=on["h0"], d=on["d"],
+                              dt_bias=on["dt_bias"], z=on["z"])
+    assert bool(torch.isinf(y[9:, 1, 3]).all()) and not torch.isnan(y).any()
+    same(got[0], y, "y")
+    same(got[1], h, "h_n")
